@@ -64,7 +64,16 @@ typedef enum {
 /* Kernels of car_reduce_residual_rmsnorm (see car_tune_fused). */
 typedef enum { CAR_FUSED_AUTO = 0, CAR_FUSED_ROWS = 1, CAR_FUSED_PIPELINE = 2 } car_fused_kernel;
 
-typedef struct car_ctx car_ctx; /* opaque */
+/* Scales of the 8-bit output of car_reduce_residual_rmsnorm_quant. */
+typedef enum {
+  CAR_SCALE_ROW = 0,      /* fp32 [M]: one per row                                     */
+  CAR_SCALE_GROUP128 = 1, /* fp32 [M, ceil(N/128)]: one per 128 columns                */
+  CAR_SCALE_MX32 = 2,     /* e8m0 [M, ceil(N/32)] (1 byte): a power of two per 32 columns */
+  CAR_SCALE_STATIC = 3    /* fp32 [1], given by the caller                             */
+} car_scale_kind;
+
+typedef struct car_ctx car_ctx;     /* opaque */
+typedef struct car_grads car_grads; /* opaque */
 
 /* Stale-line report of the last decode-reduce on a handle.  The caller sets
  * `cap` and `entries` (a host array of cap (rank, line) pairs, may be NULL
@@ -151,6 +160,123 @@ car_status car_reduce_two_shot(car_ctx* h, const void* const* inputs, void* ar_o
 car_status car_reduce_residual_rmsnorm(car_ctx* h, const void* const* inputs, const void* residual,
                                        const void* weight, float eps, void* residual_out,
                                        void* norm_out, void* ar_out, void* stream);
+
+/* The same op with the normalised row in 8 bits (e4m3), for a product that
+ * takes its activations scaled.  With acc, h, residual_out and rms as above:
+ *   t = h * f32(weight[j]);  y = t * rms                (fp32)
+ *   s = the scale of y's group of columns (see car_scale_kind):
+ *       row, group128: max(amax / 448, 2^-126), amax = max |y| of the group
+ *       mx32: 2^k, the smallest power of two >= amax / 448, k >= -126, stored
+ *             as the byte k + 127
+ *       static: read from scales[0] (finite, > 0)
+ *   q_out[m,j] = e4m3_rne( saturate( y / s ) )           (y * (1/s) in fp32)
+ * so that q * s stands for y.  The last group of a row may be short.  amax is
+ * rms * max |t|, so a scale costs no pass of its own.  A group with a value
+ * that is not finite gets a NaN scale (byte 255 in mx32) and NaN codes; under
+ * a static scale infinities saturate and NaN stays NaN.  y is not rounded to
+ * the handle's type on the way to q_out.
+ *   q_out    : dev [M, N] bytes, e4m3 (no infinities, largest value 448).
+ *   scales   : dev, car_quant_scale_bytes(h, kind) bytes, row-major, 4-byte
+ *              aligned (any alignment for mx32); written, or read for static.
+ *   norm_out : dev [M, N] or NULL; rne_T(y), within the same bound as above
+ *              (the products associate differently: its bits may differ).
+ *   the others as above; residual_out may equal residual, ar_out one input.
+ * The kernel and launch shape are chosen automatically (car_tune_fused does
+ * not apply).
+ * Errors: as car_reduce_residual_rmsnorm; CAR_ERR_ARG also for an unknown
+ * kind. */
+car_status car_reduce_residual_rmsnorm_quant(car_ctx* h, const void* const* inputs, const void* residual,
+                                             const void* weight, float eps, car_scale_kind kind, void* residual_out,
+                                             void* q_out, void* scales, void* norm_out, void* ar_out, void* stream);
+
+/* Bytes of `scales` above; 0 for an invalid handle or kind. */
+size_t car_quant_scale_bytes(car_ctx* h, car_scale_kind kind);
+
+/* Backward of the fused op (either output form; the 8-bit one as if its
+ * rounding were not there).  Each rank brings its contribution to the
+ * gradient of norm_out, summed here like the forward's inputs.  Per row:
+ *   g  = fp32 rank sum of dnorm_r (as in car_reduce, unrounded)
+ *   h  = f32(residual_out), as the forward stored it;  rms as above
+ *   u  = h * rms;  m = mean_j( g * weight * u )
+ *   dx = rne_T( rms * (g * weight - u * m) + dresidual_out )
+ *   dweight[j] = sum over rows of g * u                   (fp32)
+ * dx is the gradient of residual and of every rank's x_r alike.
+ *   dnorm         : host array of W dev pointers, each [M, N].
+ *   residual_out  : dev [M, N].       weight : dev [N].
+ *   dresidual_out : dev [M, N], the gradient that arrives at residual_out on
+ *                   the skip path, or NULL for none.
+ *   dx            : dev [M, N]; may equal one dnorm[k], residual_out or
+ *                   dresidual_out.
+ *   dweight       : dev [N] fp32 (whatever the handle's type), overwritten,
+ *                   or NULL when the weight needs no gradient.
+ *   workspace     : dev, car_backward_workspace_bytes(h) bytes, 16-byte
+ *                   aligned; its contents do not matter before or after.  Calls
+ *                   that may overlap on the GPU need one each.  May be NULL when
+ *                   that is 0 or dweight is NULL.
+ * The same call on the same data gives the same bits (no float atomics).
+ * Errors: CAR_ERR_HANDLE, CAR_ERR_ARG (NULL, eps not finite or < 0),
+ * CAR_ERR_ALIGN, CAR_ERR_SIZE (N*s > CAR_MAX_ROW_BYTES), CAR_ERR_CUDA; a
+ * bounded wait that ran out is reported by car_sync (the row's dx is then
+ * NaN). */
+car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const void* residual_out,
+                                                const void* weight, float eps, const void* dresidual_out, void* dx,
+                                                void* dweight, void* workspace, void* stream);
+
+/* Bytes of `workspace` above; 0 when none is needed or for an invalid handle. */
+size_t car_backward_workspace_bytes(car_ctx* h);
+
+/* ---------------------------------------------------------------------- */
+/* Gradients of many tensors: rank sum, global norm, clipping              */
+/* ---------------------------------------------------------------------- */
+
+/* A gradient handle binds the buffers of one data-parallel step: n tensors,
+ * tensor t with numel[t] elements of dtypes[t] (mixed types allowed, 0
+ * elements allowed), W rank buffers each, and one output each.
+ *   inputs : host array of W * n dev pointers, inputs[r * n + t].
+ *   outs   : host array of n dev pointers; outs[t] may equal inputs[r * n + t]
+ *            (in place); other overlaps among outs or between outs and inputs
+ *            are refused.
+ * Pointers need element alignment only.  A tensor whose W + 1 pointers have
+ * the same address modulo 16 moves in 16-byte vectors, others element by
+ * element.  The pointers are kept: the buffers must stay where they are until
+ * the handle is destroyed.  The handle owns its plan and scratch on the
+ * current device (about 16 bytes per 32 KB of a tensor, 144 per tensor); it
+ * allocates and copies, so create it outside stream capture.  Its calls must
+ * not overlap on the GPU (one scratch; the outputs are the same anyway), and
+ * one handle must not be used by two threads at once.
+ * Errors: CAR_ERR_ARG (NULL, W not in 1..16, n < 1, numel < 0, unknown type,
+ * overlap; a NULL pointer is allowed for a tensor of 0 elements),
+ * CAR_ERR_ALIGN, CAR_ERR_SIZE (too many elements), CAR_ERR_CUDA.  *out is set
+ * to NULL on error. */
+car_status car_grads_create(int W, int64_t n, const int64_t* numel, const car_dtype* dtypes, const void* const* inputs,
+                            void* const* outs, car_grads** out);
+
+/* Free the handle's own memory.  Waits for nothing, like car_destroy. */
+car_status car_grads_destroy(car_grads* g);
+
+/* First half: with G = scale * (fp32 rank sum, as in car_reduce),
+ *   outs[t] = rne_T(G_t);   *sumsq = sum over all tensors of G^2
+ * from the unrounded G (squares in fp32, sums in 64 bits beyond a few hundred
+ * terms; the same call on the same data gives the same bits).  Where the
+ * model is split over several handles or devices, add their sumsq and pass
+ * the total to car_grads_clip.
+ *   scale : finite, e.g. 1 / W for the mean.
+ *   sumsq : dev, one double. */
+car_status car_grads_reduce(car_grads* g, float scale, double* sumsq, void* stream);
+
+/* Second half: norm = sqrt(*sumsq); every outs value v becomes
+ * rne_T(v * min(1, max_norm / (norm + 1e-6))).  A norm within the limit leaves
+ * outs untouched; a NaN norm makes every value NaN, an infinite one 0 (NaN
+ * where v is not finite).
+ *   max_norm : >= 0; infinity never clips.
+ *   norm_out : dev, one float (the norm before clipping), or NULL. */
+car_status car_grads_clip(car_grads* g, const double* sumsq, float max_norm, float* norm_out, void* stream);
+
+/* Both halves for a step whose gradients are all in this handle.
+ * Errors of the three calls: CAR_ERR_HANDLE, CAR_ERR_ARG (NULL sumsq, scale
+ * not finite, max_norm < 0 or NaN, another current device), CAR_ERR_ALIGN,
+ * CAR_ERR_CUDA. */
+car_status car_grads_reduce_clip(car_grads* g, float scale, float max_norm, float* norm_out, void* stream);
 
 /* ---------------------------------------------------------------------- */
 /* LL128 (P2 "LL128 的 128-byte line", "LL128 的 warp-level ready 检查")    */

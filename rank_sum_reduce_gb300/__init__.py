@@ -21,6 +21,8 @@ CAR_BF16, CAR_FP16, CAR_FP32 = 0, 1, 2
 CAR_OK, CAR_ERR_ARG, CAR_ERR_ALIGN, CAR_ERR_SIZE, CAR_ERR_CUDA, CAR_ERR_STALE_FLAG, CAR_ERR_HANDLE, CAR_ERR_TIMEOUT = \
     range(8)
 CAR_FUSED_AUTO, CAR_FUSED_ROWS, CAR_FUSED_PIPELINE = 0, 1, 2
+CAR_SCALE_ROW, CAR_SCALE_GROUP128, CAR_SCALE_MX32, CAR_SCALE_STATIC = 0, 1, 2, 3
+SCALE_CODE = {"row": CAR_SCALE_ROW, "group128": CAR_SCALE_GROUP128, "mx32": CAR_SCALE_MX32, "static": CAR_SCALE_STATIC}
 CAR_STALE_LIST_MAX = 65536
 CAR_MAX_ROW_BYTES = 64 * 1024
 DTYPE_CODE = {"bf16": CAR_BF16, "fp16": CAR_FP16, "fp32": CAR_FP32}
@@ -51,6 +53,18 @@ _SIGS = {
     "car_reduce": (ctypes.c_int, [_vp, _pvp, _vp, _vp]),
     "car_reduce_two_shot": (ctypes.c_int, [_vp, _pvp, _vp, _vp]),
     "car_reduce_residual_rmsnorm": (ctypes.c_int, [_vp, _pvp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "car_reduce_residual_rmsnorm_quant": (ctypes.c_int, [_vp, _pvp, _vp, _vp, ctypes.c_float, ctypes.c_int, _vp, _vp,
+                                                         _vp, _vp, _vp, _vp]),
+    "car_quant_scale_bytes": (ctypes.c_size_t, [_vp, ctypes.c_int]),
+    "car_reduce_residual_rmsnorm_backward": (ctypes.c_int, [_vp, _pvp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                                            _vp]),
+    "car_backward_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "car_grads_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64),
+                                        ctypes.POINTER(ctypes.c_int), _pvp, _pvp, _ctx_pp]),
+    "car_grads_destroy": (ctypes.c_int, [_vp]),
+    "car_grads_reduce": (ctypes.c_int, [_vp, ctypes.c_float, _vp, _vp]),
+    "car_grads_clip": (ctypes.c_int, [_vp, _vp, ctypes.c_float, _vp, _vp]),
+    "car_grads_reduce_clip": (ctypes.c_int, [_vp, ctypes.c_float, ctypes.c_float, _vp, _vp]),
     "car_ll128_wire_bytes": (ctypes.c_size_t, [_vp]),
     "car_ll128_encode": (ctypes.c_int, [_vp, _vp, ctypes.c_uint64, _vp, _vp]),
     "car_ll128_decode_reduce": (ctypes.c_int, [_vp, _pvp, ctypes.c_uint64, ctypes.c_int, _vp, _vp]),
@@ -117,6 +131,54 @@ def car_reduce_residual_rmsnorm(h, inputs, residual: int, weight: int, eps: floa
                                 norm_out: int, ar_out: int | None, stream: int = 0) -> int:
     return _lib.car_reduce_residual_rmsnorm(h, _table(inputs) if inputs is not None else None, residual, weight,
                                             eps, residual_out, norm_out, ar_out, stream)
+
+
+def car_reduce_residual_rmsnorm_quant(h, inputs, residual: int, weight: int, eps: float, kind: int, residual_out: int,
+                                      q_out: int, scales: int, norm_out: int | None, ar_out: int | None,
+                                      stream: int = 0) -> int:
+    return _lib.car_reduce_residual_rmsnorm_quant(h, _table(inputs) if inputs is not None else None, residual, weight,
+                                                  eps, kind, residual_out, q_out, scales, norm_out, ar_out, stream)
+
+
+def car_quant_scale_bytes(h, kind: int) -> int:
+    return int(_lib.car_quant_scale_bytes(h, kind))
+
+
+def car_reduce_residual_rmsnorm_backward(h, dnorm, residual_out: int, weight: int, eps: float,
+                                         dresidual_out: int | None, dx: int, dweight: int | None,
+                                         workspace: int | None, stream: int = 0) -> int:
+    return _lib.car_reduce_residual_rmsnorm_backward(h, _table(dnorm) if dnorm is not None else None, residual_out,
+                                                     weight, eps, dresidual_out, dx, dweight, workspace, stream)
+
+
+def car_backward_workspace_bytes(h) -> int:
+    return int(_lib.car_backward_workspace_bytes(h))
+
+
+def car_grads_create(W: int, numel, dtypes, inputs, outs):
+    """inputs: W * n device addresses, rank-major; outs: n.  Returns (status, handle)."""
+    n = len(numel)
+    out = ctypes.c_void_p()
+    st = _lib.car_grads_create(W, n, (ctypes.c_int64 * n)(*numel), (ctypes.c_int * n)(*dtypes),
+                               _table(inputs) if inputs is not None else None,
+                               _table(outs) if outs is not None else None, ctypes.byref(out))
+    return st, out.value
+
+
+def car_grads_destroy(g) -> int:
+    return _lib.car_grads_destroy(g)
+
+
+def car_grads_reduce(g, scale: float, sumsq: int, stream: int = 0) -> int:
+    return _lib.car_grads_reduce(g, scale, sumsq, stream)
+
+
+def car_grads_clip(g, sumsq: int, max_norm: float, norm_out: int | None, stream: int = 0) -> int:
+    return _lib.car_grads_clip(g, sumsq, max_norm, norm_out, stream)
+
+
+def car_grads_reduce_clip(g, scale: float, max_norm: float, norm_out: int | None, stream: int = 0) -> int:
+    return _lib.car_grads_reduce_clip(g, scale, max_norm, norm_out, stream)
 
 
 def car_ll128_wire_bytes(h) -> int:
@@ -316,6 +378,51 @@ class Car:
                                           self._p(ar_out, D, "ar_out") if ar_out is not None else None,
                                           _stream(stream)), "car_reduce_residual_rmsnorm")
 
+    def quant_scales_shape(self, kind: str) -> tuple:
+        """Shape of the scales of the 8-bit output: fp32, or one byte each for "mx32"."""
+        groups = {"row": 1, "group128": -(-self.N // 128), "mx32": -(-self.N // 32)}
+        return (1,) if kind == "static" else (self.M, groups[kind])
+
+    def reduce_residual_rmsnorm_quant(self, xs, residual, weight, eps, kind, residual_out, q_out, scales,
+                                      norm_out=None, ar_out=None, stream=None):
+        """kind: "row", "group128", "mx32" or "static" (see car_scale_kind).  q_out: M * N bytes (float8_e4m3fn or
+        uint8); scales: quant_scales_shape(kind), written, or read for "static"."""
+        if kind not in SCALE_CODE:
+            raise ValueError(f"kind: {kind!r} is none of {', '.join(SCALE_CODE)}")
+        D, code = self.D, SCALE_CODE[kind]
+        check(car_reduce_residual_rmsnorm_quant(
+            self.h, self._ranks(xs, D, "inputs"), self._p(residual, D, "residual"), self._p(weight, D // self.M, "weight"),
+            eps, code, self._p(residual_out, D, "residual_out"), self._p(q_out, self.M * self.N, "q_out"),
+            self._p(scales, car_quant_scale_bytes(self.h, code), "scales"),
+            self._p(norm_out, D, "norm_out") if norm_out is not None else None,
+            self._p(ar_out, D, "ar_out") if ar_out is not None else None, _stream(stream)),
+            "car_reduce_residual_rmsnorm_quant")
+
+    @property
+    def backward_workspace_bytes(self) -> int:
+        return car_backward_workspace_bytes(self.h)
+
+    def reduce_residual_rmsnorm_backward(self, dnorm, residual_out, weight, eps, dresidual_out, dx, dweight=None,
+                                         workspace=None, stream=None):
+        """dresidual_out and dweight may be None; dweight is fp32.  With a dweight, workspace (backward_workspace_bytes
+        bytes) is taken from torch's allocator on the current stream when none is given."""
+        D, ws = self.D, None
+        if dweight is not None:
+            need = self.backward_workspace_bytes
+            if workspace is None and need:
+                import torch
+
+                if stream is not None and _stream(stream) != torch.cuda.current_stream().cuda_stream:
+                    raise ValueError("workspace: give one for a call on another stream than the current one")
+                workspace = torch.empty(need, dtype=torch.uint8, device=dx.device)
+            ws = self._p(workspace, need, "workspace") if need else None
+        check(car_reduce_residual_rmsnorm_backward(
+            self.h, self._ranks(dnorm, D, "dnorm"), self._p(residual_out, D, "residual_out"),
+            self._p(weight, D // self.M, "weight"), eps,
+            self._p(dresidual_out, D, "dresidual_out") if dresidual_out is not None else None, self._p(dx, D, "dx"),
+            self._p(dweight, 4 * self.N, "dweight") if dweight is not None else None, ws, _stream(stream)),
+            "car_reduce_residual_rmsnorm_backward")
+
     def ll128_encode(self, data, flag, wire, stream=None):
         check(car_ll128_encode(self.h, self._p(data, self.D, "data"), flag, self._p(wire, self.ll128_wire_bytes, "wire"),
                                _stream(stream)), "car_ll128_encode")
@@ -379,3 +486,79 @@ class Car:
 
     def sync(self, stream=None):
         check(car_sync(self.h, _stream(stream)), "car_sync")
+
+
+class Grads:
+    """The gradients of one data-parallel step: rank sum, global norm, clipping.
+
+    inputs: W sequences of n tensors (one per rank); outs: n tensors.  Tensor
+    t of every rank and of outs has the same number of elements and the same
+    type (bf16, fp16 or fp32); all are contiguous on one CUDA device.  outs[t]
+    may be inputs[r][t] itself.  The object keeps the tensors."""
+
+    def __init__(self, inputs, outs):
+        import torch
+
+        code = {torch.bfloat16: CAR_BF16, torch.float16: CAR_FP16, torch.float32: CAR_FP32}
+        self.inputs, self.outs, self.h = [list(ts) for ts in inputs], list(outs), None
+        if not self.inputs or not self.outs:
+            raise ValueError("inputs, outs: need at least one rank and one tensor")
+        self.device = self.outs[0].device.index
+        for t, o in enumerate(self.outs):
+            if o.dtype not in code:
+                raise ValueError(f"outs[{t}]: {o.dtype} is not bf16, fp16 or fp32")
+        n, flat = len(self.outs), []
+        for r, ts in enumerate(self.inputs):
+            if len(ts) != n:
+                raise ValueError(f"inputs[{r}]: {len(ts)} tensors for {n} outputs")
+            for t, (x, o) in enumerate(zip(ts, self.outs)):
+                if x.dtype != o.dtype or x.numel() != o.numel():
+                    raise ValueError(f"inputs[{r}][{t}]: {x.numel()} x {x.dtype}, outs[{t}] is {o.numel()} x {o.dtype}")
+                flat.append(_ptr(x, 0, f"inputs[{r}][{t}]", self.device))
+        to = [_ptr(o, 0, f"outs[{t}]", self.device) for t, o in enumerate(self.outs)]
+        with torch.cuda.device(self.device):
+            st, h = car_grads_create(len(self.inputs), [o.numel() for o in self.outs], [code[o.dtype] for o in self.outs],
+                                     flat, to)
+        if st == CAR_ERR_ARG and car_last_error():
+            raise ValueError(car_last_error())
+        check(st, "car_grads_create")
+        self.h = h
+
+    def close(self):
+        if self.h is not None:
+            check(car_grads_destroy(self.h), "car_grads_destroy")
+            self.h = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _scalar(self, t, nbytes: int, what: str, dtype: str) -> int:
+        if str(t.dtype) != "torch." + dtype:
+            raise ValueError(f"{what}: {t.dtype}, the call needs {dtype}")
+        return _ptr(t, nbytes, what, self.device)
+
+    def reduce(self, scale, sumsq, stream=None):
+        """outs = scale * rank sums; sumsq (float64, one element) = the sum of their squares."""
+        check(car_grads_reduce(self.h, scale, self._scalar(sumsq, 8, "sumsq", "float64"), _stream(stream)),
+              "car_grads_reduce")
+
+    def clip(self, sumsq, max_norm, norm_out=None, stream=None):
+        """outs *= min(1, max_norm / (sqrt(sumsq) + 1e-6)); norm_out (float32, one element) = sqrt(sumsq)."""
+        check(car_grads_clip(self.h, self._scalar(sumsq, 8, "sumsq", "float64"), max_norm,
+                             self._scalar(norm_out, 4, "norm_out", "float32") if norm_out is not None else None,
+                             _stream(stream)), "car_grads_clip")
+
+    def reduce_clip(self, scale, max_norm, norm_out=None, stream=None):
+        """Both, for gradients that are all in this object."""
+        check(car_grads_reduce_clip(self.h, scale, max_norm,
+                                    self._scalar(norm_out, 4, "norm_out", "float32") if norm_out is not None else None,
+                                    _stream(stream)), "car_grads_reduce_clip")

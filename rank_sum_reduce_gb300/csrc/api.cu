@@ -25,8 +25,12 @@
 #include "../../include/car.h"
 #include "car_device.cuh"
 #include "car_launch.h"
+#include "quant.cuh"
 
 static_assert(car::kStaleCap == CAR_STALE_LIST_MAX, "stale list capacity mismatch");
+static_assert((int)car::kScaleRow == CAR_SCALE_ROW && (int)car::kScaleGroup128 == CAR_SCALE_GROUP128 &&
+                  (int)car::kScaleMx32 == CAR_SCALE_MX32 && (int)car::kScaleStatic == CAR_SCALE_STATIC,
+              "scale kinds mismatch");
 
 struct car_ctx {
   int W;
@@ -46,6 +50,8 @@ struct car_ctx {
   bool tma_ok;          // row fits the shared-memory ring of the pipelined kernel
   car::FusedTmaShape tma_auto;
   car::FusedTmaShape tma;
+  car::FusedShape quant;     // row kernel with an 8-bit output: the automatic shape, its own resident count
+  car::FusedShape backward;  // backward of the fused op
   int fused_kernel_auto;  // CAR_FUSED_ROWS or CAR_FUSED_PIPELINE
   int fused_kernel;
   unsigned int* d_err;  // bounded-wait failures reported by kernels (device)
@@ -380,6 +386,18 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
     h->fused_auto = h->fused;
   }
 
+  if (h->fused_ok) {
+    int groups = 0;
+    h->quant = auto_fused_shape(W, M, h->vec_per_row, h->num_sms);
+    if ((e = car::fused_quant_resident_groups(h->dtype, W, h->quant, h->num_sms, &groups)) != cudaSuccess)
+      return fail(e, "8-bit output occupancy");
+    h->quant.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
+    h->backward = row_split_shape(W, M, h->vec_per_row, h->num_sms, car::backward_has_variant, car::backward_max_threads, false);
+    if ((e = car::backward_resident_groups(h->dtype, W, h->backward, h->num_sms, &groups)) != cudaSuccess)
+      return fail(e, "backward occupancy");
+    h->backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
+  }
+
   h->lamport_ok = h->fused_ok && dtype == CAR_BF16;
   if (h->lamport_ok) {
     car::FusedShape sh = auto_lamport_shape(W, M, h->vec_per_row, h->num_sms);
@@ -531,6 +549,74 @@ car_status car_reduce_residual_rmsnorm(car_ctx* h, const void* const* inputs, co
     e = car::launch_fused(h->dtype, h->W, tbl, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err,
                           h->M, h->N, h->vec_per_row, h->fused, h->hook, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_residual_rmsnorm launch");
+}
+
+static int scale_groups(const car_ctx* h, int kind) {
+  return kind == CAR_SCALE_GROUP128 ? (int)((h->N + 127) / 128) : kind == CAR_SCALE_MX32 ? (int)((h->N + 31) / 32) : 1;
+}
+
+size_t car_quant_scale_bytes(car_ctx* h, car_scale_kind kind) {
+  if (!live(h)) return 0;
+  switch (kind) {
+    case CAR_SCALE_ROW:
+    case CAR_SCALE_GROUP128: return (size_t)h->M * (size_t)scale_groups(h, kind) * 4;
+    case CAR_SCALE_MX32: return (size_t)h->M * (size_t)scale_groups(h, kind);
+    case CAR_SCALE_STATIC: return 4;
+  }
+  return 0;
+}
+
+car_status car_reduce_residual_rmsnorm_quant(car_ctx* h, const void* const* inputs, const void* residual,
+                                             const void* weight, float eps, car_scale_kind kind, void* residual_out,
+                                             void* q_out, void* scales, void* norm_out, void* ar_out, void* stream) {
+  car_status st = check_handle(h);
+  if (st != CAR_OK) return st;
+  if (!std::isfinite(eps) || eps < 0.f) return CAR_ERR_ARG;
+  if (kind != CAR_SCALE_ROW && kind != CAR_SCALE_GROUP128 && kind != CAR_SCALE_MX32 && kind != CAR_SCALE_STATIC)
+    return CAR_ERR_ARG;
+  car::RankPtrs tbl;
+  if ((st = check_table(h, inputs, &tbl)) != CAR_OK) return st;
+  if ((st = check_dev(residual)) != CAR_OK) return st;
+  if ((st = check_dev(weight)) != CAR_OK) return st;
+  if ((st = check_dev(residual_out)) != CAR_OK) return st;
+  if ((st = check_dev(q_out)) != CAR_OK) return st;
+  if ((st = check_dev_elem(scales, kind == CAR_SCALE_MX32 ? 1 : 4)) != CAR_OK) return st;
+  if ((norm_out && !aligned16(norm_out)) || (ar_out && !aligned16(ar_out))) return CAR_ERR_ALIGN;
+  if (!h->fused_ok) return CAR_ERR_SIZE;
+  car::QuantOut out;
+  out.q = static_cast<uint8_t*>(q_out);
+  out.scales = scales;
+  out.kind = (int)kind;
+  out.groups = scale_groups(h, kind);
+  cudaError_t e = car::launch_fused_quant(h->dtype, h->W, tbl, residual, weight, eps, residual_out, out, norm_out, ar_out,
+                                          h->d_err, h->M, h->N, h->vec_per_row, h->quant, h->hook,
+                                          static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_residual_rmsnorm_quant launch");
+}
+
+size_t car_backward_workspace_bytes(car_ctx* h) {
+  if (!live(h) || !h->fused_ok || h->backward.groups == 1) return 0;
+  return (size_t)h->backward.groups * (size_t)h->N * sizeof(float);
+}
+
+car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const void* residual_out,
+                                                const void* weight, float eps, const void* dresidual_out, void* dx,
+                                                void* dweight, void* workspace, void* stream) {
+  car_status st = check_handle(h);
+  if (st != CAR_OK) return st;
+  if (!std::isfinite(eps) || eps < 0.f) return CAR_ERR_ARG;
+  car::RankPtrs tbl;
+  if ((st = check_table(h, dnorm, &tbl)) != CAR_OK) return st;
+  if ((st = check_dev(residual_out)) != CAR_OK) return st;
+  if ((st = check_dev(weight)) != CAR_OK) return st;
+  if ((st = check_dev(dx)) != CAR_OK) return st;
+  if ((dresidual_out && !aligned16(dresidual_out)) || (dweight && !aligned16(dweight))) return CAR_ERR_ALIGN;
+  if (!h->fused_ok) return CAR_ERR_SIZE;
+  if (dweight && h->backward.groups > 1 && (st = check_dev(workspace)) != CAR_OK) return st;
+  cudaError_t e = car::launch_backward(h->dtype, h->W, tbl, residual_out, weight, eps, dresidual_out, dx,
+                                       static_cast<float*>(dweight), static_cast<float*>(workspace), h->d_err, h->M, h->N,
+                                       h->vec_per_row, h->backward, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_residual_rmsnorm_backward launch");
 }
 
 size_t car_ll128_wire_bytes(car_ctx* h) { return live(h) ? (size_t)(128 * h->ll128_lines) : 0; }

@@ -214,6 +214,11 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
                "r"(bar)
                : "memory");
 }
+__device__ __forceinline__ void st_async_u32(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
+               "r"(bar)
+               : "memory");
+}
 // The same for two 32-bit words (8 bytes, `addr` 8-byte aligned).
 __device__ __forceinline__ void st_async_v2_b32(uint32_t addr, uint32_t x, uint32_t y, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),

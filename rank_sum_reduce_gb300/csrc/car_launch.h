@@ -10,6 +10,7 @@ namespace car {
 
 struct RankPtrs;
 struct StaleLog;
+struct QuantOut;
 
 // ---- plain one-shot rank sum (reduce.cu) ----
 // nvec = number of 16-byte vectors per rank.  grid = CTAs of kReduceThreads.
@@ -49,6 +50,13 @@ cudaError_t launch_fused(int dtype, int W, const RankPtrs& in, const void* resid
                          void* ar_out, unsigned int* err, int64_t rows, int64_t cols, int vec_per_row,
                          const FusedShape& sh, const WaitHook& hook, cudaStream_t s);
 
+// The same with an 8-bit output and scales (fused_quant.cu).
+cudaError_t fused_quant_resident_groups(int dtype, int W, const FusedShape& sh, int num_sms, int* groups);
+cudaError_t launch_fused_quant(int dtype, int W, const RankPtrs& in, const void* residual, const void* weight,
+                               float eps, void* residual_out, const QuantOut& out, void* norm_out, void* ar_out,
+                               unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh,
+                               const WaitHook& hook, cudaStream_t s);
+
 // ---- fused, many rows: TMA bulk copies into a shared-memory ring (fused_tma.cu) ----
 struct FusedTmaShape {
   int cluster;    // CTAs sharing each row (1 or 2)
@@ -67,6 +75,44 @@ cudaError_t launch_fused_tma(int dtype, int W, const RankPtrs& in, const void* r
                              float eps, void* residual_out, void* norm_out, void* ar_out, unsigned int* err,
                              int64_t rows, int64_t cols, int vec_per_row, const FusedTmaShape& sh,
                              cudaStream_t s);
+
+// ---- backward of the fused op (norm_backward.cu) ----
+constexpr int kBackwardThreads = 512;
+bool backward_has_variant(int W, int vpt);
+int backward_max_threads(int W, int vpt);
+cudaError_t backward_resident_groups(int dtype, int W, const FusedShape& sh, int num_sms, int* groups);
+// workspace: groups * cols floats when groups > 1 and dweight is wanted.
+cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
+                            const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
+                            int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh, cudaStream_t s);
+
+// ---- gradients of many tensors: rank sum, global norm, clipping (grads.cu) ----
+constexpr int kGradThreads = 256;
+constexpr int kGradChunkVecs = 2048;  // 16-byte vectors of one tensor that a CTA takes at a time
+struct GradTensor {
+  const void* in[16];
+  void* out;
+  int32_t dtype;
+  int32_t head;  // elements before the first 16-byte boundary that all pointers share; -1: they share none
+};
+struct GradChunk {  // elements [begin, begin + count) of one tensor
+  int64_t begin;
+  int32_t count;
+  int32_t tensor;
+};
+struct GradPlan {
+  const GradTensor* tensors;
+  const GradChunk* chunks;
+  int64_t n_chunks;
+  int W;
+  double* partial;        // [grid]
+  double* sumsq;          // the handle's own
+  unsigned int* arrived;  // CTAs of the reduce that have written their partial
+};
+cudaError_t grads_occupancy(int W, int* reduce_blocks_per_sm, int* clip_blocks_per_sm);
+cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, double* sumsq, int grid, cudaStream_t s);
+cudaError_t launch_grads_clip(const GradPlan& plan, const double* sumsq, float max_norm, float* norm_out, int grid,
+                              cudaStream_t s);
 
 // ---- LL128 (ll128.cu) ----
 constexpr int kWireThreads = 256;

@@ -1,0 +1,344 @@
+// norm_backward.cu -- backward of rank sum + residual add + RMSNorm.
+//
+// Forward (fused_rows.cuh): h = sum_r x_r + residual, rms = rsqrt(mean(h^2) +
+// eps), out = h * rms * w.  Given the W rank contributions dy_r of the
+// gradient of `out` (a column-parallel product behind the norm leaves one per
+// rank), the stored h and the gradient `dres` of residual_out that arrives on
+// the skip path:
+//   g  = sum_r dy_r                     (fp32, rank order, as the forward's sum)
+//   u  = h * rms                        (the normalised row)
+//   m  = mean_j(g_j w_j u_j)
+//   dx = rms * (g w - u m) + dres       the gradient of residual and of every x_r
+//   dw = sum over rows of g * u
+// rms and m need two sums over the row, h^2 and g w h, which share one
+// exchange; g, h and dres stay in registers across it, so every input is read
+// once.  dw is summed over a CTA's rows in fp32 registers; the CTAs' partials
+// go to the caller's workspace and a second kernel adds them in a fixed order
+// (no float atomics: the same call gives the same bits).
+//
+// Row split, clusters, PDL and L2 prefetch as in the forward's row kernel.
+// Roofline: HBM, (W + 3) * 16 bytes per vector with a skip gradient, and
+// 4 * N * groups bytes of partials written and read again (L2).
+#include "car_device.cuh"
+#include "car_launch.h"
+
+namespace car {
+namespace {
+
+struct BackwardParams {
+  RankPtrs dy;
+  const uint4* h;
+  const uint4* dres;   // may be null
+  const uint4* weight;
+  uint4* dx;
+  float* partial;      // [groups, N], or dweight itself with one group; null: no weight gradient
+  unsigned int* err;   // as in the forward's row kernel
+  float eps;
+  float cols;
+  int64_t rows;
+  int vec_per_row;
+  int chunk;           // 16-byte vectors of a row handled by one CTA
+  int cluster;
+  int nranks;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// This CTA's piece of `row` -- the n rank slices, h, dres, and the weight with
+// `weight` -- into L2, one bulk prefetch per slice.
+__device__ __forceinline__ void prefetch_row(const BackwardParams& p, int n, int64_t row, int col0, bool weight) {
+  const int nvec = min(p.chunk, p.vec_per_row - col0);
+  const int t = threadIdx.x;
+  if (row >= p.rows || nvec <= 0 || t > n + 2) return;
+  const int64_t off = row * (int64_t)p.vec_per_row + col0;
+  const uint4* src;
+  if (t < n) {
+    src = static_cast<const uint4*>(p.dy.p[t]) + off;
+  } else if (t == n) {
+    src = p.h + off;
+  } else if (t == n + 1) {
+    if (!p.dres) return;
+    src = p.dres + off;
+  } else {
+    if (!weight) return;
+    src = p.weight + col0;
+  }
+  prefetch_l2(src, (uint32_t)nvec * 16u);
+}
+
+template <int DT, int W, int VPT>
+__global__ void __launch_bounds__(kBackwardThreads) reduce_rmsnorm_backward_kernel(const BackwardParams p) {
+  constexpr int E = Pack<DT>::kN;
+  constexpr int R = W > 0 ? W : kMaxRanks;
+  const int n = W > 0 ? W : p.nranks;
+  __shared__ float2 s_warp[2][kBackwardThreads / 32];  // warp partials (h^2, g w h), by row parity
+  __shared__ __align__(8) float2 s_part[2][8];         // the cluster's CTA partials, by row parity
+  __shared__ __align__(8) uint64_t s_xbar[2];
+
+  const int C = p.cluster;
+  const int crank = C > 1 ? (int)cluster_rank() : 0;
+  const int64_t group = blockIdx.x / C, ngroups = gridDim.x / C;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  const int col0 = crank * p.chunk;
+  uint32_t it = 0;
+  bool peers_ready = C == 1;
+  if (C > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(&s_xbar[0], 1);
+      mbar_init(&s_xbar[1], 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    cluster_arrive();
+  }
+  prefetch_row(p, n, group, col0, true);
+  pdl_wait_and_release();
+
+  bool ok[VPT];
+  uint4 wv[VPT];
+  float dw[VPT][E];
+#pragma unroll
+  for (int k = 0; k < VPT; k++) {
+    const int v = threadIdx.x + k * blockDim.x;
+    ok[k] = v < p.chunk && col0 + v < p.vec_per_row;
+    wv[k] = ok[k] ? __ldg(p.weight + col0 + v) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int e = 0; e < E; e++) dw[k][e] = 0.f;
+  }
+
+  for (int64_t row = group; row < p.rows; row += ngroups, it++) {
+    const int64_t rbase = row * (int64_t)p.vec_per_row + col0;
+    prefetch_row(p, n, row + ngroups, col0, false);
+    uint4 hv[VPT], dv[VPT];
+    float g[VPT][E];
+    float ss = 0.f, c = 0.f;
+    {
+      uint4 raw[VPT][R];
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        if (ok[k]) {
+          const int64_t off = rbase + threadIdx.x + k * blockDim.x;
+#pragma unroll
+          for (int r = 0; r < R; r++)
+            if (r < n) raw[k][r] = ld_stream(static_cast<const uint4*>(p.dy.p[r]) + off);
+          hv[k] = ld_stream(p.h + off);
+          dv[k] = p.dres ? ld_stream(p.dres + off) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        if (ok[k]) {
+          rank_sum<DT, R>(raw[k], n, g[k]);
+          float hf[E], wf[E];
+          Pack<DT>::widen(hv[k], hf);
+          Pack<DT>::widen(wv[k], wf);
+#pragma unroll
+          for (int e = 0; e < E; e++) {
+            ss = fmaf(hf[e], hf[e], ss);
+            c = fmaf(__fmul_rn(g[k][e], wf[e]), hf[e], c);
+          }
+        }
+      }
+    }
+    // Row statistics: warp, CTA, cluster.  Every warp adds the warp partials
+    // itself, in the same order, so one barrier per row is enough: s_warp[b]
+    // is next written for row it + 2, after the barrier of row it + 1.
+    ss = warp_sum(ss);
+    c = warp_sum(c);
+    const uint32_t b = it & 1u;
+    if (lane == 0) s_warp[b][warp] = make_float2(ss, c);
+    if (!peers_ready) {
+      cluster_wait();
+      peers_ready = true;
+    }
+    __syncthreads();
+    const float2 mine = lane < nwarps ? s_warp[b][lane] : make_float2(0.f, 0.f);
+    ss = warp_sum(mine.x);
+    c = warp_sum(mine.y);
+    if (C > 1) {
+      const uint32_t par = (it >> 1) & 1u;
+      if (warp == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(&s_xbar[b], 8u * (uint32_t)C);
+        if (lane < C)
+          st_async_v2_b32(map_rank(&s_part[b][crank], (uint32_t)lane), __float_as_uint(ss), __float_as_uint(c),
+                          map_rank(&s_xbar[b], (uint32_t)lane));
+      }
+      if (wait_cluster_phase(&s_xbar[b], par)) {
+        ss = s_part[b][0].x;
+        c = s_part[b][0].y;
+        for (int r = 1; r < C; r++) {
+          ss += s_part[b][r].x;
+          c += s_part[b][r].y;
+        }
+      } else {
+        atomicOr(p.err, 1u);
+        ss = __int_as_float(0x7fc00000);  // NaN: this row's gradients are not usable
+        if (!wait_cluster_phase(&s_xbar[b], par)) atomicOr(p.err, 2u);
+      }
+    }
+    const float rms = rsqrtf(__fdiv_rn(ss, p.cols) + p.eps);
+    const float m = __fdiv_rn(__fmul_rn(c, rms), p.cols);
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+      if (ok[k]) {
+        float hf[E], wf[E], df[E], o[E];
+        Pack<DT>::widen(hv[k], hf);
+        Pack<DT>::widen(wv[k], wf);
+        Pack<DT>::widen(dv[k], df);
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          const float u = __fmul_rn(hf[e], rms);
+          dw[k][e] = fmaf(g[k][e], u, dw[k][e]);
+          o[e] = fmaf(rms, fmaf(-u, m, __fmul_rn(g[k][e], wf[e])), df[e]);
+        }
+        st16(p.dx + rbase + threadIdx.x + k * blockDim.x, Pack<DT>::narrow(o));
+      }
+    }
+  }
+  if (p.partial) {
+    float* to = p.partial + group * (int64_t)p.vec_per_row * E;
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+      if (ok[k]) {
+        const int col = (col0 + threadIdx.x + k * blockDim.x) * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+          *reinterpret_cast<float4*>(to + col + e) = make_float4(dw[k][e], dw[k][e + 1], dw[k][e + 2], dw[k][e + 3]);
+      }
+    }
+  }
+  if (!peers_ready) cluster_wait();
+}
+
+// dweight[j] = sum over groups of partial[g][j], in a fixed order: a warp
+// takes every kSumWarps-th group of 128 columns, the warps' sums are added in
+// warp order.  The partials are a few MB and were just written, so they come
+// from L2.
+constexpr int kSumWarps = 8;
+__global__ void __launch_bounds__(32 * kSumWarps)
+    sum_partials_kernel(const float4* __restrict__ partial, float4* __restrict__ out, const int groups, const int vecs) {
+  __shared__ float4 s[kSumWarps][32];
+  pdl_wait_and_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int v = blockIdx.x * 32 + lane;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (v < vecs) {
+#pragma unroll 4
+    for (int g = warp; g < groups; g += kSumWarps) {
+      const float4 x = __ldcg(partial + (int64_t)g * vecs + v);
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
+    }
+  }
+  s[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0 && v < vecs) {
+#pragma unroll
+    for (int w = 1; w < kSumWarps; w++) {
+      const float4 x = s[w][lane];
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
+    }
+    out[v] = a;
+  }
+}
+
+using BackwardFn = void (*)(const BackwardParams);
+
+template <int DT>
+BackwardFn pick_dt(int W, int vpt) {
+  if (vpt == 2) {
+    switch (W) {
+      case 1: return reduce_rmsnorm_backward_kernel<DT, 1, 2>;
+      case 2: return reduce_rmsnorm_backward_kernel<DT, 2, 2>;
+      case 4: return reduce_rmsnorm_backward_kernel<DT, 4, 2>;
+      case 8: return reduce_rmsnorm_backward_kernel<DT, 8, 2>;
+      default: return nullptr;
+    }
+  }
+  if (vpt != 1) return nullptr;
+  switch (W) {
+    case 1: return reduce_rmsnorm_backward_kernel<DT, 1, 1>;
+    case 2: return reduce_rmsnorm_backward_kernel<DT, 2, 1>;
+    case 4: return reduce_rmsnorm_backward_kernel<DT, 4, 1>;
+    case 8: return reduce_rmsnorm_backward_kernel<DT, 8, 1>;
+    case 16: return reduce_rmsnorm_backward_kernel<DT, 16, 1>;
+    default: return reduce_rmsnorm_backward_kernel<DT, 0, 1>;
+  }
+}
+
+BackwardFn pick_backward(int dtype, int W, int vpt) {
+  switch (dtype) {
+    case kBF16: return pick_dt<kBF16>(W, vpt);
+    case kFP16: return pick_dt<kFP16>(W, vpt);
+    default: return pick_dt<kFP32>(W, vpt);
+  }
+}
+
+}  // namespace
+
+bool backward_has_variant(int W, int vpt) {
+  return vpt == 1 || (vpt == 2 && (W == 1 || W == 2 || W == 4 || W == 8));
+}
+int backward_max_threads(int, int) { return kBackwardThreads; }
+
+cudaError_t backward_resident_groups(int dtype, int W, const FusedShape& sh, int num_sms, int* groups) {
+  *groups = 0;
+  BackwardFn fn = pick_backward(dtype, W, sh.vpt);
+  if (!fn) return cudaErrorInvalidValue;
+  const void* f = reinterpret_cast<const void*>(fn);
+  if (sh.cluster == 1) {
+    int per_sm = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f, sh.threads, 0);
+    *groups = per_sm * num_sms;
+    return e;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)sh.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sh.cluster, 1, 1);
+  cfg.blockDim = dim3((unsigned)sh.threads, 1, 1);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(groups, f, &cfg);
+}
+
+cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
+                            const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
+                            int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh, cudaStream_t s) {
+  BackwardFn fn = pick_backward(dtype, W, sh.vpt);
+  if (!fn) return cudaErrorInvalidValue;
+  BackwardParams p;
+  p.dy = dy;
+  p.h = static_cast<const uint4*>(h);
+  p.dres = static_cast<const uint4*>(dres);
+  p.weight = static_cast<const uint4*>(weight);
+  p.dx = static_cast<uint4*>(dx);
+  p.partial = dweight ? (sh.groups > 1 ? workspace : dweight) : nullptr;
+  p.err = err;
+  p.eps = eps;
+  p.cols = (float)cols;
+  p.rows = rows;
+  p.vec_per_row = vec_per_row;
+  p.chunk = (vec_per_row + sh.cluster - 1) / sh.cluster;
+  p.cluster = sh.cluster;
+  p.nranks = W;
+  cudaError_t e = launch_pdl(fn, (unsigned)(sh.groups * sh.cluster), (unsigned)sh.threads, 0, s, (unsigned)sh.cluster, p);
+  if (e != cudaSuccess || !dweight || sh.groups == 1) return e;
+  const int vecs = (int)(cols / 4);
+  return launch_pdl(sum_partials_kernel, (unsigned)((vecs + 31) / 32), 32u * kSumWarps, 0, s, 1,
+                    reinterpret_cast<const float4*>(workspace), reinterpret_cast<float4*>(dweight), sh.groups, vecs);
+}
+
+}  // namespace car
