@@ -51,6 +51,8 @@ struct car_ctx {
   car::FusedTmaShape tma_auto;
   car::FusedTmaShape tma;
   car::FusedShape quant;     // row kernel with an 8-bit output: the automatic shape, its own resident count
+  car::FusedTmaShape quant_tma;
+  bool quant_pipeline;       // the 8-bit output runs the pipeline kernel
   car::FusedShape backward;  // backward of the fused op
   int fused_kernel_auto;  // CAR_FUSED_ROWS or CAR_FUSED_PIPELINE
   int fused_kernel;
@@ -392,6 +394,10 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
     if ((e = car::fused_quant_resident_groups(h->dtype, W, h->quant, h->num_sms, &groups)) != cudaSuccess)
       return fail(e, "8-bit output occupancy");
     h->quant.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
+    h->quant_pipeline = h->fused_kernel_auto == CAR_FUSED_PIPELINE;
+    h->quant_tma = h->tma_auto;
+    if (h->quant_pipeline && (e = car::fused_tma_quant_prepare(h->dtype, W, &h->quant_tma)) != cudaSuccess)
+      return fail(e, "8-bit output pipeline smem");
     h->backward = row_split_shape(W, M, h->vec_per_row, h->num_sms, car::backward_has_variant, car::backward_max_threads, false);
     if ((e = car::backward_resident_groups(h->dtype, W, h->backward, h->num_sms, &groups)) != cudaSuccess)
       return fail(e, "backward occupancy");
@@ -588,9 +594,14 @@ car_status car_reduce_residual_rmsnorm_quant(car_ctx* h, const void* const* inpu
   out.scales = scales;
   out.kind = (int)kind;
   out.groups = scale_groups(h, kind);
-  cudaError_t e = car::launch_fused_quant(h->dtype, h->W, tbl, residual, weight, eps, residual_out, out, norm_out, ar_out,
-                                          h->d_err, h->M, h->N, h->vec_per_row, h->quant, h->hook,
-                                          static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (h->quant_pipeline)
+    e = car::launch_fused_tma_quant(h->dtype, h->W, tbl, residual, weight, eps, residual_out, out, norm_out, ar_out,
+                                    h->d_err, h->M, h->N, h->vec_per_row, h->quant_tma, s);
+  else
+    e = car::launch_fused_quant(h->dtype, h->W, tbl, residual, weight, eps, residual_out, out, norm_out, ar_out, h->d_err,
+                                h->M, h->N, h->vec_per_row, h->quant, h->hook, s);
   return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_residual_rmsnorm_quant launch");
 }
 

@@ -76,6 +76,13 @@ cudaError_t launch_fused_tma(int dtype, int W, const RankPtrs& in, const void* r
                              int64_t rows, int64_t cols, int vec_per_row, const FusedTmaShape& sh,
                              cudaStream_t s);
 
+// The same with an 8-bit output and scales (fused_tma_quant.cu); sh with cluster 1, whose smem grows.
+cudaError_t fused_tma_quant_prepare(int dtype, int W, FusedTmaShape* sh);
+cudaError_t launch_fused_tma_quant(int dtype, int W, const RankPtrs& in, const void* residual, const void* weight,
+                                   float eps, void* residual_out, const QuantOut& out, void* norm_out, void* ar_out,
+                                   unsigned int* err, int64_t rows, int64_t cols, int vec_per_row,
+                                   const FusedTmaShape& sh, cudaStream_t s);
+
 // ---- backward of the fused op (norm_backward.cu) ----
 constexpr int kBackwardThreads = 512;
 bool backward_has_variant(int W, int vpt);

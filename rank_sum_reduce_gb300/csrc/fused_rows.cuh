@@ -179,18 +179,14 @@ __global__ void __launch_bounds__(max_threads<W, VPT>(), MINB)
           float wf[E];
           Pack<DT>::widen(wv[k], wf);
 #pragma unroll
-          for (int e = 0; e < E; e++) {
-            h[k][e] = __fmul_rn(h[k][e], wf[e]);
-            gmax[k] = max(gmax[k], abs_bits(h[k][e]));
-          }
-        }
-        if (p.out.kind == kScaleRow) {
-          tmax = max(tmax, gmax[k]);
-        } else if (p.out.kind != kScaleStatic) {
-          gmax[k] = group_max(gmax[k], group_lanes<E>(p.out.kind));
+          for (int e = 0; e < E; e++) h[k][e] = __fmul_rn(h[k][e], wf[e]);
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) m = max_abs(m, h[k][e], h[k][e + 1]);
+          gmax[k] = abs_bits(m);
         }
       }
-      if (p.out.kind == kScaleRow) tmax = warp_max(tmax);
+      tmax = spread_max<E>(p.out.kind, gmax);
     }
 
     // 3. row statistic: warp shuffle, then shared memory across warps.
@@ -280,11 +276,13 @@ __global__ void __launch_bounds__(max_threads<W, VPT>(), MINB)
         const bool grouped = p.out.kind == kScaleGroup128 || p.out.kind == kScaleMx32;
         const float inv = grouped ? group_inverse<E>(p.out, row, v, rms, gmax[k], ok[k]) : inv_row;
         if (ok[k]) {
-          float y[E];
+          store_e4m3<E>(p.out.q + rbase * E, v, h[k], rms, inv);
+          if (p.norm_out) {
+            float y[E];
 #pragma unroll
-          for (int e = 0; e < E; e++) y[e] = __fmul_rn(h[k][e], rms);
-          if (p.norm_out) st16(p.norm_out + rbase + v, Pack<DT>::narrow(y));
-          store_e4m3(p.out.q + rbase * E, v, y, inv);
+            for (int e = 0; e < E; e++) y[e] = __fmul_rn(h[k][e], rms);
+            st16(p.norm_out + rbase + v, Pack<DT>::narrow(y));
+          }
         }
       }
     } else {

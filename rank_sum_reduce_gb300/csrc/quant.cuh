@@ -7,9 +7,8 @@
 // row-wide scale it travels with the sum of squares) and the scales cost no
 // exchange of their own.
 //
-// Rounding: s is rounded once to its stored type, q = e4m3(y * (1 / s)) with
-// 1 / s rounded once, both in fp32 (two roundings of 2^-24 before the one of
-// 2^-4 to e4m3).  The largest |y| of a group lands on 448, or below it for a
+// Rounding: s is stored in fp32 or as a power of two; t * (rms * (1 / s)) is
+// formed in fp32 (a few roundings of 2^-24 before the one of 2^-4 to e4m3).  The largest |y| of a group lands on 448, or below it for a
 // power-of-two s; the conversion saturates.
 #pragma once
 
@@ -33,29 +32,62 @@ struct QuantOut {
 
 constexpr float kE4m3Max = 448.f;
 
-// |t| as bits: unsigned order is the order of magnitudes, infinity and then
-// NaN on top, so one integer maximum also carries "not finite".
+// Largest magnitude so far, over two more values; NaN once one is NaN (the
+// three-operand form halves the instructions).
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+// As bits, magnitudes order as unsigned integers, with infinity and then NaN
+// on top: one integer maximum across lanes also carries "not finite".
 __device__ __forceinline__ uint32_t abs_bits(float t) { return __float_as_uint(t) & 0x7FFFFFFFu; }
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t m) { return __reduce_max_sync(0xFFFFFFFFu, m); }
 
-// Lanes (each with one 16-byte vector of E elements) that share a scale.
-template <int E>
-__device__ __forceinline__ int group_lanes(int kind) {
-  return (kind == kScaleGroup128 ? 128 : 32) / E;
+// Lanes, each with one 16-byte vector of E elements, that share a scale.
+template <int E, int KIND>
+constexpr int kGroupLanes = (KIND == kScaleGroup128 ? 128 : 32) / E;
+
+// Maximum of each m[k] over the neighbouring lanes of its group.
+template <int E, int KIND, int VPT>
+__device__ __forceinline__ void group_max(uint32_t (&m)[VPT]) {
+#pragma unroll
+  for (int o = 1; o < kGroupLanes<E, KIND>; o <<= 1) {
+#pragma unroll
+    for (int k = 0; k < VPT; k++) m[k] = max(m[k], __shfl_xor_sync(0xFFFFFFFFu, m[k], o));
+  }
 }
 
-// Maximum over the `lanes` (a power of two) neighbouring lanes of a group.
-__device__ __forceinline__ uint32_t group_max(uint32_t m, int lanes) {
-  for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return m;
+// From each vector's own max |t| to its group's (group kinds), or to the
+// warp's over all its vectors, which is returned (row scale).
+template <int E, int VPT>
+__device__ __forceinline__ uint32_t spread_max(int kind, uint32_t (&m)[VPT]) {
+  if (kind == kScaleGroup128) {
+    group_max<E, kScaleGroup128>(m);
+  } else if (kind == kScaleMx32) {
+    group_max<E, kScaleMx32>(m);
+  } else if (kind == kScaleRow) {
+    uint32_t all = 0u;
+#pragma unroll
+    for (int k = 0; k < VPT; k++) all = max(all, m[k]);
+    return warp_max(all);
+  }
+  return 0u;
 }
 
-// fp32 scale of a group: amax / 448, at least 2^-126 so that 1 / s is finite;
-// NaN when amax is not finite.
+// fp32 scale of a group: amax / 448 (as a product with 1 / 448: within 2^-23
+// of the quotient), at least 2^-126 so that 1 / s is finite; NaN when amax is
+// not finite.
 __device__ __forceinline__ float scale_f32(float amax) {
-  if (!(amax <= 3.402823466e38f)) return __int_as_float(0x7fc00000);
-  return fmaxf(__fdiv_rn(amax, kE4m3Max), 1.17549435e-38f);
+  const float s = fmaxf(__fmul_rn(amax, 1.f / kE4m3Max), 1.17549435e-38f);
+  return amax <= 3.402823466e38f ? s : __int_as_float(0x7fc00000);
+}
+// 1 / s of a normal s within one unit of 2^-23, in one instruction.
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
 }
 
 // e8m0 scale: the smallest 2^(k - 127) that is not below amax / 448, 1 <= k;
@@ -77,26 +109,37 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// Vector `v` (E elements from column v * E) of a row of e4m3 codes.
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int v, const float (&y)[8], float inv) {
-  uint2 o;
-  o.x = e4m3x4(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv), __fmul_rn(y[2], inv), __fmul_rn(y[3], inv));
-  o.y = e4m3x4(__fmul_rn(y[4], inv), __fmul_rn(y[5], inv), __fmul_rn(y[6], inv), __fmul_rn(y[7], inv));
-  *reinterpret_cast<uint2*>(row + (int64_t)v * 8) = o;
-}
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int v, const float (&y)[4], float inv) {
-  *reinterpret_cast<uint32_t*>(row + (int64_t)v * 4) =
-      e4m3x4(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv), __fmul_rn(y[2], inv), __fmul_rn(y[3], inv));
+// Vector `v` (E elements from column v * E) of a row of e4m3 codes of
+// t * rms / s.  The two factors are multiplied first; where that product
+// leaves the finite range (a huge rms over a tiny scale) or is NaN, they are
+// applied one after the other.
+template <int E>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int v, const float (&t)[E], float rms, float inv) {
+  const float f = __fmul_rn(rms, inv);
+  float y[E];
+  if (f <= 3.402823466e38f) {
+#pragma unroll
+    for (int e = 0; e < E; e++) y[e] = __fmul_rn(t[e], f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e++) y[e] = __fmul_rn(__fmul_rn(t[e], rms), inv);
+  }
+  if constexpr (E == 8) {
+    *reinterpret_cast<uint2*>(row + (int64_t)v * 8) =
+        make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+  } else {
+    *reinterpret_cast<uint32_t*>(row + (int64_t)v * 4) = e4m3x4(y[0], y[1], y[2], y[3]);
+  }
 }
 
 // 1 / s for the whole row: its scale from the row's max |t| (stored by the
 // one thread that has `first`), or the caller's.  Unused by the group kinds.
 __device__ __forceinline__ float row_inverse(const QuantOut& o, int64_t row, float rms, uint32_t tmax, bool first) {
-  if (o.kind == kScaleStatic) return __frcp_rn(__ldg(static_cast<const float*>(o.scales)));
+  if (o.kind == kScaleStatic) return __frcp_rn(__ldg(static_cast<const float*>(o.scales)));  // any finite s > 0
   if (o.kind != kScaleRow) return 0.f;
   const float s = scale_f32(__fmul_rn(rms, __uint_as_float(tmax)));
   if (first) static_cast<float*>(o.scales)[row] = s;
-  return __frcp_rn(s);
+  return reciprocal(s);
 }
 
 // 1 / s of the group that holds vector v, given max |t| of the group; the
@@ -104,17 +147,17 @@ __device__ __forceinline__ float row_inverse(const QuantOut& o, int64_t row, flo
 template <int E>
 __device__ __forceinline__ float group_inverse(const QuantOut& o, int64_t row, int v, float rms, uint32_t gmax, bool ok) {
   const float amax = __fmul_rn(rms, __uint_as_float(gmax));
-  const int lanes = group_lanes<E>(o.kind);
-  const bool first = ok && (v & (lanes - 1)) == 0;
-  const int64_t at = row * (int64_t)o.groups + v / lanes;
+  const int64_t at = row * (int64_t)o.groups;
   if (o.kind == kScaleMx32) {
+    constexpr int L = kGroupLanes<E, kScaleMx32>;
     const uint32_t k = scale_e8m0(amax);
-    if (first) static_cast<uint8_t*>(o.scales)[at] = (uint8_t)k;
+    if (ok && v % L == 0) static_cast<uint8_t*>(o.scales)[at + v / L] = (uint8_t)k;
     return inverse_e8m0(k);
   }
+  constexpr int L = kGroupLanes<E, kScaleGroup128>;
   const float s = scale_f32(amax);
-  if (first) static_cast<float*>(o.scales)[at] = s;
-  return __frcp_rn(s);
+  if (ok && v % L == 0) static_cast<float*>(o.scales)[at + v / L] = s;
+  return reciprocal(s);
 }
 
 }  // namespace car
