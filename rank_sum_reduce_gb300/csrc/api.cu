@@ -53,7 +53,10 @@ struct car_ctx {
   car::FusedShape quant;     // row kernel with an 8-bit output: the automatic shape, its own resident count
   car::FusedTmaShape quant_tma;
   bool quant_pipeline;       // the 8-bit output runs the pipeline kernel
-  car::FusedShape backward;  // backward of the fused op
+  car::FusedShape backward;  // backward of the fused op: row kernel
+  car::FusedTmaShape backward_tma;
+  bool backward_pipeline;
+  int backward_groups;       // CTAs (or clusters) with a partial weight gradient each
   int fused_kernel_auto;  // CAR_FUSED_ROWS or CAR_FUSED_PIPELINE
   int fused_kernel;
   unsigned int* d_err;  // bounded-wait failures reported by kernels (device)
@@ -402,6 +405,11 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
     if ((e = car::backward_resident_groups(h->dtype, W, h->backward, h->num_sms, &groups)) != cudaSuccess)
       return fail(e, "backward occupancy");
     h->backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
+    h->backward_pipeline = M > h->num_sms && N * es > 8192 &&
+                           car::backward_tma_shape(M, h->vec_per_row, h->num_sms, W, &h->backward_tma);
+    if (h->backward_pipeline && (e = car::backward_tma_prepare(h->dtype, W, h->backward_tma)) != cudaSuccess)
+      return fail(e, "backward pipeline smem");
+    h->backward_groups = h->backward_pipeline ? h->backward_tma.grid : h->backward.groups;
   }
 
   h->lamport_ok = h->fused_ok && dtype == CAR_BF16;
@@ -606,8 +614,8 @@ car_status car_reduce_residual_rmsnorm_quant(car_ctx* h, const void* const* inpu
 }
 
 size_t car_backward_workspace_bytes(car_ctx* h) {
-  if (!live(h) || !h->fused_ok || h->backward.groups == 1) return 0;
-  return (size_t)h->backward.groups * (size_t)h->N * sizeof(float);
+  if (!live(h) || !h->fused_ok || h->backward_groups == 1) return 0;
+  return (size_t)h->backward_groups * (size_t)h->N * sizeof(float);
 }
 
 car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const void* residual_out,
@@ -623,10 +631,16 @@ car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* d
   if ((st = check_dev(dx)) != CAR_OK) return st;
   if ((dresidual_out && !aligned16(dresidual_out)) || (dweight && !aligned16(dweight))) return CAR_ERR_ALIGN;
   if (!h->fused_ok) return CAR_ERR_SIZE;
-  if (dweight && h->backward.groups > 1 && (st = check_dev(workspace)) != CAR_OK) return st;
-  cudaError_t e = car::launch_backward(h->dtype, h->W, tbl, residual_out, weight, eps, dresidual_out, dx,
-                                       static_cast<float*>(dweight), static_cast<float*>(workspace), h->d_err, h->M, h->N,
-                                       h->vec_per_row, h->backward, static_cast<cudaStream_t>(stream));
+  if (dweight && h->backward_groups > 1 && (st = check_dev(workspace)) != CAR_OK) return st;
+  float *dw = static_cast<float*>(dweight), *ws = static_cast<float*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (h->backward_pipeline)
+    e = car::launch_backward_tma(h->dtype, h->W, tbl, residual_out, weight, eps, dresidual_out, dx, dw, ws, h->d_err, h->M,
+                                 h->N, h->vec_per_row, h->backward_tma, s);
+  else
+    e = car::launch_backward(h->dtype, h->W, tbl, residual_out, weight, eps, dresidual_out, dx, dw, ws, h->d_err, h->M,
+                             h->N, h->vec_per_row, h->backward, s);
   return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_residual_rmsnorm_backward launch");
 }
 

@@ -93,6 +93,14 @@ cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h,
                             const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
                             int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh, cudaStream_t s);
 
+cudaError_t launch_sum_partials(const float* partial, float* out, int groups, int64_t cols, cudaStream_t s);
+// The pipeline form for many rows (norm_backward_tma.cu); false when a row is too long for it.
+bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, FusedTmaShape* out);
+cudaError_t backward_tma_prepare(int dtype, int W, const FusedTmaShape& sh);
+cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
+                                const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
+                                int64_t rows, int64_t cols, int vec_per_row, const FusedTmaShape& sh, cudaStream_t s);
+
 // ---- gradients of many tensors: rank sum, global norm, clipping (grads.cu) ----
 constexpr int kGradThreads = 256;
 constexpr int kGradChunkVecs = 2048;  // 16-byte vectors of one tensor that a CTA takes at a time

@@ -336,9 +336,13 @@ cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h,
   p.nranks = W;
   cudaError_t e = launch_pdl(fn, (unsigned)(sh.groups * sh.cluster), (unsigned)sh.threads, 0, s, (unsigned)sh.cluster, p);
   if (e != cudaSuccess || !dweight || sh.groups == 1) return e;
+  return launch_sum_partials(workspace, dweight, sh.groups, cols, s);
+}
+
+cudaError_t launch_sum_partials(const float* partial, float* out, int groups, int64_t cols, cudaStream_t s) {
   const int vecs = (int)(cols / 4);
   return launch_pdl(sum_partials_kernel, (unsigned)((vecs + 31) / 32), 32u * kSumWarps, 0, s, 1,
-                    reinterpret_cast<const float4*>(workspace), reinterpret_cast<float4*>(dweight), sh.groups, vecs);
+                    reinterpret_cast<const float4*>(partial), reinterpret_cast<float4*>(out), groups, vecs);
 }
 
 }  // namespace car

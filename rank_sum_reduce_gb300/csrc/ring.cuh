@@ -1,0 +1,58 @@
+// ring.cuh -- bounded waits and bulk copies of the kernels that stream row
+// slices through a ring of shared-memory slots (fused_tma.cuh,
+// norm_backward_tma.cu).
+#pragma once
+
+#include "car_device.cuh"
+
+namespace car {
+namespace {
+
+// Wait for the barrier phase with the given parity; false when the CTA is
+// aborting or the wait ran past kWaitLimitNs.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t i = 1; i < (1u << 30); i++) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0 && (*abort || globaltimer() - t0 > kWaitLimitNs)) return false;
+  }
+  return false;
+}
+// Same, ignoring the abort flag (used while draining on the way out).
+__device__ __forceinline__ bool wait_bounded_cluster(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t i = 1; i < (1u << 30); i++) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((i & 63u) == 0 && (*abort || globaltimer() - t0 > kWaitLimitNs)) return false;
+  }
+  return false;
+}
+__device__ __forceinline__ bool wait_bounded_drain(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t i = 1; i < (1u << 30); i++) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0 && globaltimer() - t0 > kWaitLimitNs) return false;
+  }
+  return false;
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds16(const uint8_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+}  // namespace
+}  // namespace car
