@@ -54,7 +54,7 @@ struct car_ctx {
   car::FusedTmaShape quant_tma;
   bool quant_pipeline;       // the 8-bit output runs the pipeline kernel
   car::FusedShape backward;  // backward of the fused op: row kernel
-  car::FusedTmaShape backward_tma;
+  car::BackwardTmaShape backward_tma;
   bool backward_pipeline;
   int backward_groups;       // CTAs (or clusters) with a partial weight gradient each
   int fused_kernel_auto;  // CAR_FUSED_ROWS or CAR_FUSED_PIPELINE
@@ -226,6 +226,22 @@ int auto_fused_kernel(const car_ctx* h) {
 // row kernel, within the Lamport kernel's compiled instances.
 car::FusedShape auto_lamport_shape(int W, int64_t M, int V, int num_sms) {
   return row_split_shape(W, M, V, num_sms, car::lamport_has_variant, car::lamport_max_threads, false);
+}
+
+// When the backward's pipeline kernel is faster than its row kernel.  Measured
+// on GB300 (graph replay over cold inputs, bf16, us per call with a weight
+// gradient, pipeline / rows): one or two ranks, rows short enough for several
+// teams: W = 1, N = 1024, M = 640 5.6 / 6.2, M = 3648 10.3 / 11.0; N = 4096,
+// M = 912 10.4 / 11.3, M = 16389 88 / 104.  With one team (N = 8192) the row
+// kernel, which holds two rows' loads in registers there, stays ahead: M = 456
+// 11.4 / 10.3, M = 2048 28.3 / 28.0.  More ranks pay the ring's start and its
+// one issuing thread until a CTA has two to three tiles: W = 8, N = 4096, M =
+// 400 12.2 / 10.7, M = 912 16.9 / 18.2; W = 4, N = 8192, M = 200 10.3 / 9.5,
+// M = 456 13.7 / 14.2; W = 8, N = 8192, M = 304 14.2 / 16.5.
+bool backward_pipeline_pays(int W, int64_t M, int num_sms, const car::BackwardTmaShape& sh) {
+  const int64_t tiles = (M + sh.teams - 1) / sh.teams;
+  if (W <= 2) return sh.teams > 1 && 2 * tiles >= num_sms;
+  return 2 * tiles >= (sh.teams > 1 ? 5 : 4) * (int64_t)num_sms;
 }
 
 car_status finish_fused_shape(car_ctx* h, car::FusedShape sh) {
@@ -404,10 +420,11 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
     h->backward = row_split_shape(W, M, h->vec_per_row, h->num_sms, car::backward_has_variant, car::backward_max_threads, false);
     if ((e = car::backward_resident_groups(h->dtype, W, h->backward, h->num_sms, &groups)) != cudaSuccess)
       return fail(e, "backward occupancy");
-    h->backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
-    h->backward_pipeline = M > h->num_sms && N * es > 8192 &&
-                           car::backward_tma_shape(M, h->vec_per_row, h->num_sms, W, &h->backward_tma);
-    if (h->backward_pipeline && (e = car::backward_tma_prepare(h->dtype, W, h->backward_tma)) != cudaSuccess)
+    const int64_t teams = car::backward_teams(h->backward);
+    h->backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>((M + teams - 1) / teams, std::max(groups, 1)));
+    h->backward_pipeline = car::backward_tma_shape(M, h->vec_per_row, h->num_sms, W, &h->backward_tma) &&
+                           backward_pipeline_pays(W, M, h->num_sms, h->backward_tma);
+    if (h->backward_pipeline && (e = car::backward_tma_prepare(h->dtype, h->backward_tma)) != cudaSuccess)
       return fail(e, "backward pipeline smem");
     h->backward_groups = h->backward_pipeline ? h->backward_tma.grid : h->backward.groups;
   }

@@ -87,6 +87,7 @@ cudaError_t launch_fused_tma_quant(int dtype, int W, const RankPtrs& in, const v
 constexpr int kBackwardThreads = 512;
 bool backward_has_variant(int W, int vpt);
 int backward_max_threads(int W, int vpt);
+int backward_teams(const FusedShape& sh);  // rows a CTA works on at a time; sh.groups counts CTAs (or clusters)
 cudaError_t backward_resident_groups(int dtype, int W, const FusedShape& sh, int num_sms, int* groups);
 // workspace: groups * cols floats when groups > 1 and dweight is wanted.
 cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
@@ -95,11 +96,18 @@ cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h,
 
 cudaError_t launch_sum_partials(const float* partial, float* out, int groups, int64_t cols, cudaStream_t s);
 // The pipeline form for many rows (norm_backward_tma.cu); false when a row is too long for it.
-bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, FusedTmaShape* out);
-cudaError_t backward_tma_prepare(int dtype, int W, const FusedTmaShape& sh);
+struct BackwardTmaShape {
+  int team_threads;  // consumer threads of a row
+  int teams;         // rows a CTA works on at a time
+  int slots;         // ring depth, in slices of `teams` rows
+  int grid;
+  int smem;
+};
+bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BackwardTmaShape* out);
+cudaError_t backward_tma_prepare(int dtype, const BackwardTmaShape& sh);
 cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
                                 const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
-                                int64_t rows, int64_t cols, int vec_per_row, const FusedTmaShape& sh, cudaStream_t s);
+                                int64_t rows, int64_t cols, int vec_per_row, const BackwardTmaShape& sh, cudaStream_t s);
 
 // ---- gradients of many tensors: rank sum, global norm, clipping (grads.cu) ----
 constexpr int kGradThreads = 256;

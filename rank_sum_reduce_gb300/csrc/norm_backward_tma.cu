@@ -1,18 +1,26 @@
 // norm_backward_tma.cu -- backward of rank sum + residual add + RMSNorm for
-// many rows, with the row slices streamed into shared memory by TMA bulk
-// copies.  Same operation as norm_backward.cu, organised as the forward's
-// pipeline kernel (fused_tma.cuh): one persistent CTA per SM takes rows
-// blockIdx.x, blockIdx.x + grid, ...; a producer thread keeps a ring of about
-// one row's slices in flight -- dy_0 .. dy_{W-1}, h, dres -- while the
-// consumer warps fold them into fp32 accumulators in rank order.
+// many rows, with the rows streamed into shared memory by TMA bulk copies.
+// Same operation as norm_backward.cu, in the manner of the forward's pipeline
+// kernel (fused_tma.cuh): one persistent CTA per SM, a producer thread that
+// keeps a ring of slices in flight -- dy_0 .. dy_{W-1}, h, dres -- and
+// consumer warps that fold them into fp32 accumulators in rank order.
+//
+// A CTA takes tiles of `teams` consecutive rows (tile blockIdx.x, blockIdx.x +
+// grid, ...).  A tile's rows lie next to each other in every buffer, so one
+// bulk copy brings the same slice of all of them: one thread issues about one
+// copy per 0.3 us whatever its size, so short rows need their slices joined to
+// keep HBM busy.  Each team of consumer warps owns one row of the tile, with
+// its own statistic and barrier: while one team is in the serial part of its
+// row another folds.
 //
 // h stays in registers (packed) from the statistic to the gradient; the dres
 // slice is only waited for after the statistic and is read from its slot
-// there.  The weight row and the weight gradient of the CTA's rows stay in
-// registers for the whole kernel.  Every mbarrier wait is bounded, as in the
-// forward.
-#include "ring.cuh"
+// there.  The weight row lies in shared memory, the weight gradient of a
+// team's rows in its registers for the whole kernel; the teams' are added in
+// shared memory at the end, one partial per CTA.  Every mbarrier wait is
+// bounded, as in the forward.
 #include "car_launch.h"
+#include "ring.cuh"
 
 namespace car {
 namespace {
@@ -31,34 +39,43 @@ struct BackwardTmaParams {
   int row_bytes;
   int vec_per_row;
   int slots;
-  int slices;           // per row: W ranks, h, dres
-  int consumers;        // consumer threads (multiple of 32)
+  int slices;           // of a tile: W ranks, h, dres
+  int teams;            // rows of a tile
+  int team_threads;     // multiple of 32
   int nranks;
 };
 
-__device__ __forceinline__ const uint8_t* slice_source(const BackwardTmaParams& p, int q, int n) {
-  return q < n ? static_cast<const uint8_t*>(p.dy.p[q]) : (q == n ? p.h : p.dres);
+__device__ __forceinline__ const uint8_t* slice_source(const BackwardTmaParams& p, int q) {
+  return q < p.nranks ? static_cast<const uint8_t*>(p.dy.p[q]) : (q == p.nranks ? p.h : p.dres);
+}
+// Bytes of one slice of the tile that starts at `row`.
+__device__ __forceinline__ uint32_t tile_bytes(const BackwardTmaParams& p, int64_t row) {
+  const int64_t left = p.rows - row;
+  return (uint32_t)(left < p.teams ? left : p.teams) * (uint32_t)p.row_bytes;
 }
 
 // As the forward's producer: keeps the ring full, then waits for every copy
-// that it issued.
+// that it issued.  (Two or four producer threads measured the same or slower,
+// and so did h and dres loaded by the consumers instead: W = 8, M = 512, N =
+// 8192 bf16 21.2 us against 21.4 and 22.1.)
 __device__ __forceinline__ void produce(const BackwardTmaParams& p, uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                        volatile int* s_abort, int n) {
+                                        volatile int* s_abort) {
   const int S = p.slots;
-  const uint32_t slice = (uint32_t)p.row_bytes;
+  const size_t stride = (size_t)p.teams * p.row_bytes;
   int slot = 0;
   uint32_t phase = 0;
   uint64_t issued = 0;
   bool ok = true;
-  for (int64_t row = blockIdx.x; row < p.rows && ok; row += gridDim.x) {
+  for (int64_t row = (int64_t)blockIdx.x * p.teams; row < p.rows && ok; row += (int64_t)gridDim.x * p.teams) {
     const int64_t off = row * (int64_t)p.row_bytes;
+    const uint32_t bytes = tile_bytes(p, row);
     for (int q = 0; q < p.slices; q++) {
       if (issued >= (uint64_t)S && !wait_bounded(&empty[slot], phase ^ 1u, s_abort)) {
         ok = false;
         break;
       }
-      mbar_arrive_expect_tx(&full[slot], slice);
-      bulk_load(ring + (size_t)slot * slice, slice_source(p, q, n) + off, slice, &full[slot]);
+      mbar_arrive_expect_tx(&full[slot], bytes);
+      bulk_load(ring + slot * stride, slice_source(p, q) + off, bytes, &full[slot]);
       issued++;
       if (++slot == S) {
         slot = 0;
@@ -77,22 +94,30 @@ __device__ __forceinline__ void produce(const BackwardTmaParams& p, uint8_t* rin
   }
 }
 
-template <int DT, int VPT>
-__device__ __forceinline__ void consume(const BackwardTmaParams& p, const uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                        uint64_t* rowbar, float2* s_warp, volatile int* s_abort, int n, int nwarps) {
+// Vectors per consumer thread.  Two: with one, the fixed work of a row (two
+// sums over the warp, a division, addresses) is done twice as often (W = 1,
+// N = 4096 bf16: 89 against 135 us); four spill.
+constexpr int VPT = 2;
+
+template <int DT>
+__device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* ring, const uint8_t* s_weight, uint64_t* full,
+                                        uint64_t* empty, uint64_t* rowbar, uint64_t* done, float2* s_warp,
+                                        volatile int* s_abort) {
   constexpr int E = Pack<DT>::kN;
-  const int S = p.slots, slice = p.row_bytes, T = p.consumers;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint4 wv[VPT];
-  float dw[VPT][E];
+  const int S = p.slots, T = p.team_threads, n = p.nranks;
+  const int team = threadIdx.x / T, tid = threadIdx.x - team * T;
+  const int warp = tid >> 5, lane = threadIdx.x & 31, nwarps = T >> 5;
+  const size_t stride = (size_t)p.teams * p.row_bytes;
+  const uint8_t* mine = ring + (size_t)team * p.row_bytes + 16 * tid;  // this thread's first vector in slot 0
+  rowbar += team;
+  s_warp += team * 2 * nwarps;
+  float2 dw[VPT][E / 2];
   bool ok[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
-    const int v = threadIdx.x + k * T;
-    ok[k] = v < p.vec_per_row;
-    wv[k] = ok[k] ? __ldg(p.weight + v) : make_uint4(0u, 0u, 0u, 0u);
+    ok[k] = tid + k * T < p.vec_per_row;
 #pragma unroll
-    for (int e = 0; e < E; e++) dw[k][e] = 0.f;
+    for (int e = 0; e < E / 2; e++) dw[k][e] = make_float2(0.f, 0.f);
   }
   int slot = 0;
   uint32_t phase = 0, it = 0;
@@ -105,23 +130,37 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, const uint8_
       phase ^= 1u;
     }
   };
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, it++) {
-    float g[VPT][E];
+  auto widen2 = [](uint4 v, float2 (&f)[E / 2]) {
+    float t[E];
+    Pack<DT>::widen(v, t);
+#pragma unroll
+    for (int e = 0; e < E / 2; e++) f[e] = make_float2(t[2 * e], t[2 * e + 1]);
+  };
+  for (int64_t tile = (int64_t)blockIdx.x * p.teams; tile < p.rows; tile += (int64_t)gridDim.x * p.teams) {
+    const int64_t row = tile + team;
+    if (row >= p.rows) {  // a team without a row in the last tile only lets the slots go
+      for (int q = 0; q < p.slices && !failed; q++) {
+        failed = !wait_bounded(&full[slot], phase, s_abort);
+        if (!failed) release();
+      }
+      break;
+    }
+    float2 g[VPT][E / 2];
     uint4 hv[VPT];
-    float ss = 0.f, c = 0.f;
+    float2 ss = make_float2(0.f, 0.f), c = make_float2(0.f, 0.f);
     for (int q = 0; q < n; q++) {
       if (!wait_bounded(&full[slot], phase, s_abort)) {
         failed = true;
         break;
       }
-      const uint8_t* sl = ring + (size_t)slot * slice;
+      const uint8_t* sl = mine + slot * stride;
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
         if (ok[k]) {
-          float t[E];
-          Pack<DT>::widen(lds16(sl + 16 * (threadIdx.x + k * T)), t);
+          float2 t[E / 2];
+          widen2(lds16(sl + 16 * k * T), t);
 #pragma unroll
-          for (int e = 0; e < E; e++) g[k][e] = q == 0 ? t[e] : __fadd_rn(g[k][e], t[e]);
+          for (int e = 0; e < E / 2; e++) g[k][e] = q == 0 ? t[e] : add2(g[k][e], t[e]);
         }
       }
       release();
@@ -133,34 +172,38 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, const uint8_
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       if (ok[k]) {
-        hv[k] = lds16(ring + (size_t)slot * slice + 16 * (threadIdx.x + k * T));
-        float hf[E], wf[E];
-        Pack<DT>::widen(hv[k], hf);
-        Pack<DT>::widen(wv[k], wf);
+        hv[k] = lds16(mine + slot * stride + 16 * k * T);
+        float2 hf[E / 2], wf[E / 2];
+        widen2(hv[k], hf);
+        widen2(lds16(s_weight + 16 * (tid + k * T)), wf);
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-          ss = fmaf(hf[e], hf[e], ss);
-          c = fmaf(__fmul_rn(g[k][e], wf[e]), hf[e], c);
+        for (int e = 0; e < E / 2; e++) {
+          ss = fma2(hf[e], hf[e], ss);
+          c = fma2(mul2(g[k][e], wf[e]), hf[e], c);
         }
       }
     }
     release();
-    // row statistics: every warp adds the warp partials itself, in the same
-    // order; they are double-buffered by row parity
-    ss = warp_sum(ss);
-    c = warp_sum(c);
-    float2* sw = s_warp + 16 * (it & 1u);
-    if (lane == 0) {
-      sw[warp] = make_float2(ss, c);
-      mbar_arrive(rowbar);
+    // row statistics: every warp adds the team's warp partials itself, in the
+    // same order; they are double-buffered by row parity
+    float2 sum = make_float2(warp_sum(ss.x + ss.y), warp_sum(c.x + c.y));
+    if (nwarps > 1) {
+      float2* sw = s_warp + nwarps * (it & 1u);
+      if (lane == 0) {
+        sw[warp] = sum;
+        mbar_arrive(rowbar);
+      }
+      if (!wait_bounded(rowbar, it & 1u, s_abort)) {
+        failed = true;
+        break;
+      }
+      sum = lane < nwarps ? sw[lane] : make_float2(0.f, 0.f);
+      sum = make_float2(warp_sum(sum.x), warp_sum(sum.y));
     }
-    if (!wait_bounded(rowbar, it & 1u, s_abort)) {
-      failed = true;
-      break;
-    }
-    const float2 mine = lane < nwarps ? sw[lane] : make_float2(0.f, 0.f);
-    const float rms = rsqrtf(__fdiv_rn(warp_sum(mine.x), p.cols) + p.eps);
-    const float m = __fdiv_rn(__fmul_rn(warp_sum(mine.y), rms), p.cols);
+    it++;
+    const float rms = rsqrtf(__fdiv_rn(sum.x, p.cols) + p.eps);
+    const float m = __fdiv_rn(__fmul_rn(sum.y, rms), p.cols);
+    const float2 rms2 = make_float2(rms, rms), m2 = make_float2(-m, -m);
     if (p.dres && !wait_bounded(&full[slot], phase, s_abort)) {
       failed = true;
       break;
@@ -168,96 +211,126 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, const uint8_
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       if (ok[k]) {
-        const int v = threadIdx.x + k * T;
-        float hf[E], wf[E], df[E], o[E];
-        Pack<DT>::widen(hv[k], hf);
-        Pack<DT>::widen(wv[k], wf);
-        Pack<DT>::widen(p.dres ? lds16(ring + (size_t)slot * slice + 16 * v) : make_uint4(0u, 0u, 0u, 0u), df);
+        float2 hf[E / 2], wf[E / 2], df[E / 2];
+        float o[E];
+        widen2(hv[k], hf);
+        widen2(lds16(s_weight + 16 * (tid + k * T)), wf);
+        widen2(p.dres ? lds16(mine + slot * stride + 16 * k * T) : make_uint4(0u, 0u, 0u, 0u), df);
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-          const float u = __fmul_rn(hf[e], rms);
-          dw[k][e] = fmaf(g[k][e], u, dw[k][e]);
-          o[e] = fmaf(rms, fmaf(-u, m, __fmul_rn(g[k][e], wf[e])), df[e]);
+        for (int e = 0; e < E / 2; e++) {
+          const float2 u = mul2(hf[e], rms2);
+          dw[k][e] = fma2(g[k][e], u, dw[k][e]);
+          const float2 x = fma2(rms2, fma2(u, m2, mul2(g[k][e], wf[e])), df[e]);
+          o[2 * e] = x.x;
+          o[2 * e + 1] = x.y;
         }
-        st16(p.dx + row * (int64_t)p.vec_per_row + v, Pack<DT>::narrow(o));
+        st16(p.dx + row * (int64_t)p.vec_per_row + tid + k * T, Pack<DT>::narrow(o));
       }
     }
     if (p.dres) release();
+  }
+  if (!p.partial) {
+    if (failed) {
+      atomicOr(p.err, 1u);
+      *s_abort = 1;
+    }
+    return;
+  }
+  // The weight gradients of the teams, added in team order by the first one:
+  // the others leave theirs in the ring once every team is past its last slot.
+  if (p.teams > 1 && !failed) {
+    if (lane == 0) mbar_arrive(&done[0]);
+    failed = !wait_bounded(&done[0], 0u, s_abort);
+    if (!failed) {
+      float* at = reinterpret_cast<float*>(ring) + (size_t)(team - 1) * p.vec_per_row * E;
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        if (ok[k] && team > 0) {
+#pragma unroll
+          for (int e = 0; e < E / 2; e += 2)
+            *reinterpret_cast<float4*>(at + (tid + k * T) * E + 2 * e) =
+                make_float4(dw[k][e].x, dw[k][e].y, dw[k][e + 1].x, dw[k][e + 1].y);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&done[1]);
+      failed = !wait_bounded(&done[1], 0u, s_abort);
+    }
   }
   if (failed) {
     atomicOr(p.err, 1u);
     *s_abort = 1;
     return;
   }
-  if (p.partial) {
-    float* to = p.partial + blockIdx.x * (int64_t)p.vec_per_row * E;
+  if (team > 0) return;
+  float* to = p.partial + blockIdx.x * (int64_t)p.vec_per_row * E;
 #pragma unroll
-    for (int k = 0; k < VPT; k++) {
-      if (ok[k]) {
+  for (int k = 0; k < VPT; k++) {
+    if (ok[k]) {
+      const int col = (tid + k * T) * E;
 #pragma unroll
-        for (int e = 0; e < E; e += 4)
-          *reinterpret_cast<float4*>(to + (threadIdx.x + k * T) * E + e) =
-              make_float4(dw[k][e], dw[k][e + 1], dw[k][e + 2], dw[k][e + 3]);
+      for (int e = 0; e < E / 2; e += 2) {
+        float4 a = make_float4(dw[k][e].x, dw[k][e].y, dw[k][e + 1].x, dw[k][e + 1].y);
+        for (int t = 1; t < p.teams; t++) {
+          const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring) +
+                                                            (size_t)(t - 1) * p.vec_per_row * E + col + 2 * e);
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        *reinterpret_cast<float4*>(to + col + 2 * e) = a;
       }
     }
   }
 }
 
-template <int DT, int W, int VPT>
+template <int DT>
 __global__ void __launch_bounds__(544, 1) reduce_rmsnorm_backward_tma_kernel(const BackwardTmaParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int S = p.slots;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)S * p.row_bytes);
+  uint8_t* s_weight = smem + (size_t)S * p.teams * p.row_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + p.row_bytes);
   uint64_t* empty = full + S;
-  uint64_t* rowbar = empty + S;
-  float2* s_warp = reinterpret_cast<float2*>(rowbar + 1);  // [2][16]
+  uint64_t* rowbar = empty + S;             // [16], by team
+  uint64_t* done = rowbar + 16;             // [2]
+  float2* s_warp = reinterpret_cast<float2*>(done + 2);  // [teams][2][warps of a team]: 32 at most
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_warp + 32);
-  const int n = W > 0 ? W : p.nranks;
-  const int nwarps = p.consumers >> 5;
+  const int consumers = p.teams * p.team_threads, nwarps = consumers >> 5;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; s++) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], (uint32_t)nwarps);
     }
-    mbar_init(rowbar, (uint32_t)nwarps);
+    for (int t = 0; t < p.teams; t++) mbar_init(&rowbar[t], (uint32_t)(p.team_threads >> 5));
+    mbar_init(&done[0], (uint32_t)nwarps);
+    mbar_init(&done[1], (uint32_t)nwarps);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // the first row into L2 while the previous grid of the stream finishes
+  // the first tile into L2 while the previous grid of the stream finishes
+  const int64_t first = (int64_t)blockIdx.x * p.teams;
   if (warp == nwarps && lane < p.slices)
-    prefetch_l2(slice_source(p, lane, n) + blockIdx.x * (int64_t)p.row_bytes, (uint32_t)p.row_bytes);
+    prefetch_l2(slice_source(p, lane) + first * (int64_t)p.row_bytes, tile_bytes(p, first));
   __syncthreads();
   pdl_wait_and_release();
   if (warp == nwarps) {
-    if (lane == 0) produce(p, smem, full, empty, s_abort, n);
+    if (lane == 0) produce(p, smem, full, empty, s_abort);
   } else {
-    consume<DT, VPT>(p, smem, full, empty, rowbar, s_warp, s_abort, n, nwarps);
+    for (int v = threadIdx.x; v < p.vec_per_row; v += consumers) reinterpret_cast<uint4*>(s_weight)[v] = __ldg(p.weight + v);
+    asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
+    consume<DT>(p, smem, s_weight, full, empty, rowbar, done, s_warp, s_abort);
   }
 }
 
 using BackwardTmaFn = void (*)(const BackwardTmaParams);
 
-template <int DT, int VPT>
-BackwardTmaFn pick_w(int W) {
-  switch (W) {
-    case 1: return reduce_rmsnorm_backward_tma_kernel<DT, 1, VPT>;
-    case 2: return reduce_rmsnorm_backward_tma_kernel<DT, 2, VPT>;
-    case 4: return reduce_rmsnorm_backward_tma_kernel<DT, 4, VPT>;
-    case 8: return reduce_rmsnorm_backward_tma_kernel<DT, 8, VPT>;
-    case 16: return reduce_rmsnorm_backward_tma_kernel<DT, 16, VPT>;
-    default: return reduce_rmsnorm_backward_tma_kernel<DT, 0, VPT>;
-  }
-}
-template <int DT>
-BackwardTmaFn pick_vpt(int W, int vpt) {
-  return vpt == 1 ? pick_w<DT, 1>(W) : vpt == 2 ? pick_w<DT, 2>(W) : nullptr;
-}
-BackwardTmaFn pick(int dtype, int W, int vpt) {
+BackwardTmaFn pick(int dtype) {
   switch (dtype) {
-    case kBF16: return pick_vpt<kBF16>(W, vpt);
-    case kFP16: return pick_vpt<kFP16>(W, vpt);
-    default: return pick_vpt<kFP32>(W, vpt);
+    case kBF16: return reduce_rmsnorm_backward_tma_kernel<kBF16>;
+    case kFP16: return reduce_rmsnorm_backward_tma_kernel<kFP16>;
+    default: return reduce_rmsnorm_backward_tma_kernel<kFP32>;
   }
 }
 
@@ -265,33 +338,32 @@ constexpr int kRingBudget = 200 * 1024;
 
 }  // namespace
 
-bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, FusedTmaShape* out) {
-  if (vec_per_row > 1024) return false;  // two vectors per thread at most: accumulators, h and dweight share 120 registers
-  const int slice = vec_per_row * 16;
-  out->cluster = 1;
-  out->ls = 0;
-  out->vpt = vec_per_row > 512 ? 2 : 1;
-  const int per = (vec_per_row + out->vpt - 1) / out->vpt;
-  out->consumers = (per + 31) / 32 * 32;
+bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BackwardTmaShape* out) {
+  const int row_bytes = vec_per_row * 16;
+  out->team_threads = ((vec_per_row + VPT - 1) / VPT + 31) / 32 * 32;
+  if (out->team_threads > 512) return false;
+  const int teams = 512 / out->team_threads;
+  out->teams = teams;
+  // about one tile's slices in flight, as in the forward
+  const int slice = teams * row_bytes;
   int slots = W + 2 < 6 ? 6 : W + 2;
   if (slots > kRingBudget / slice) slots = kRingBudget / slice;
   out->slots = slots;
-  out->grid = (int)(rows < num_sms ? rows : num_sms);
-  out->smem = slots * slice + (2 * slots + 1) * 8 + 32 * 8 + 16;
-  return slots >= 2;
+  const int64_t tiles = (rows + teams - 1) / teams;
+  out->grid = (int)(tiles < num_sms ? tiles : num_sms);
+  // the ring also takes the teams' weight gradients at the end
+  if (slots < 2 || (int64_t)(teams - 1) * vec_per_row * 8 * 4 > (int64_t)slots * slice) return false;
+  out->smem = slots * slice + row_bytes + (2 * slots + 18) * 8 + 32 * 8 + 16;
+  return true;
 }
 
-cudaError_t backward_tma_prepare(int dtype, int W, const FusedTmaShape& sh) {
-  BackwardTmaFn fn = pick(dtype, W, sh.vpt);
-  if (!fn) return cudaErrorInvalidValue;
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
+cudaError_t backward_tma_prepare(int dtype, const BackwardTmaShape& sh) {
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
 }
 
 cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
                                 const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
-                                int64_t rows, int64_t cols, int vec_per_row, const FusedTmaShape& sh, cudaStream_t s) {
-  BackwardTmaFn fn = pick(dtype, W, sh.vpt);
-  if (!fn) return cudaErrorInvalidValue;
+                                int64_t rows, int64_t cols, int vec_per_row, const BackwardTmaShape& sh, cudaStream_t s) {
   BackwardTmaParams p;
   p.dy = dy;
   p.h = static_cast<const uint8_t*>(h);
@@ -307,9 +379,10 @@ cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void
   p.vec_per_row = vec_per_row;
   p.slots = sh.slots;
   p.slices = W + 1 + (dres ? 1 : 0);
-  p.consumers = sh.consumers;
+  p.teams = sh.teams;
+  p.team_threads = sh.team_threads;
   p.nranks = W;
-  cudaError_t e = launch_pdl(fn, (unsigned)sh.grid, (unsigned)(sh.consumers + 32), (size_t)sh.smem, s, 1, p);
+  cudaError_t e = launch_pdl(pick(dtype), (unsigned)sh.grid, (unsigned)(sh.teams * sh.team_threads + 32), (size_t)sh.smem, s, 1, p);
   if (e != cudaSuccess || !dweight || sh.grid == 1) return e;
   return launch_sum_partials(workspace, dweight, sh.grid, cols, s);
 }
