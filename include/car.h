@@ -240,8 +240,9 @@ size_t car_backward_workspace_bytes(car_ctx* h);
  * the same address modulo 16 moves in 16-byte vectors, others element by
  * element.  The pointers are kept: the buffers must stay where they are until
  * the handle is destroyed.  The handle owns its plan and scratch on the
- * current device (about 16 bytes per 32 KB of a tensor, 144 per tensor); it
- * allocates and copies, so create it outside stream capture.  Its calls must
+ * current device (16 + 8 W bytes per 32 KB of a tensor, per 8 KB with eight
+ * ranks and more); it allocates and copies, so create it outside stream
+ * capture.  Its calls must
  * not overlap on the GPU (one scratch; the outputs are the same anyway), and
  * one handle must not be used by two threads at once.
  * Errors: CAR_ERR_ARG (NULL, W not in 1..16, n < 1, numel < 0, unknown type,
@@ -272,7 +273,9 @@ car_status car_grads_reduce(car_grads* g, float scale, double* sumsq, void* stre
  *   norm_out : dev, one float (the norm before clipping), or NULL. */
 car_status car_grads_clip(car_grads* g, const double* sumsq, float max_norm, float* norm_out, void* stream);
 
-/* Both halves for a step whose gradients are all in this handle.
+/* Both halves for a step whose gradients are all in this handle.  With one
+ * rank the unclipped values are not stored in between (one rounding, not two;
+ * in place, a scale of 1 and a norm within the limit write nothing).
  * Errors of the three calls: CAR_ERR_HANDLE, CAR_ERR_ARG (NULL sumsq, scale
  * not finite, max_norm < 0 or NaN, another current device), CAR_ERR_ALIGN,
  * CAR_ERR_CUDA. */

@@ -293,8 +293,15 @@ class CarError(RuntimeError):
 
 
 def check(status: int, what: str = "car") -> None:
-    if status != CAR_OK:
+    if status:  # not CAR_OK
         raise CarError(status, what)
+
+
+@functools.lru_cache(maxsize=1)
+def _cuda():
+    import torch
+
+    return torch.cuda
 
 
 @functools.lru_cache(maxsize=1)
@@ -308,9 +315,7 @@ def _raw_stream():
 
 def _stream(stream):
     if stream is None:
-        import torch
-
-        return _raw_stream()(torch.cuda.current_device())
+        return _raw_stream()(_cuda().current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -318,7 +323,7 @@ def _ptr(t, nbytes: int, what: str, device=None) -> int:
     """Device pointer of a tensor the library will read or write `nbytes` of:
     it must be a contiguous CUDA tensor at least that large, on `device` when
     given (any dtype: the library sees bytes)."""
-    if t.is_cuda and t.is_contiguous() and t.nbytes >= nbytes and (device is None or t.get_device() == device):
+    if (t.get_device() == device if device is not None else t.is_cuda) and t.is_contiguous() and t.nbytes >= nbytes:
         return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
@@ -341,6 +346,8 @@ class Car:
         check(st, "car_create")
         self.h, self.W, self.M, self.N, self.dtype = h, W, M, N, dtype
         self.D = M * N * ELEM_SIZE[dtype]      # bytes per rank
+        self._scale_bytes = [car_quant_scale_bytes(h, k) for k in range(len(SCALE_CODE))]
+        self._workspace_bytes = car_backward_workspace_bytes(h)
         import torch
 
         self.device = torch.cuda.current_device()
@@ -352,7 +359,7 @@ class Car:
         if len(ts) != self.W:
             raise ValueError(f"{what}: {len(ts)} tensors for W = {self.W}")
         dev = self.device  # one test for all is quicker than _ptr for each, which then names the one that failed
-        got = [t.data_ptr() for t in ts if t.is_cuda and t.get_device() == dev and t.is_contiguous() and t.nbytes >= nbytes]
+        got = [t.data_ptr() for t in ts if t.get_device() == dev and t.is_contiguous() and t.nbytes >= nbytes]
         if len(got) == self.W:
             return got
         return [self._p(t, nbytes, f"{what}[{r}]") for r, t in enumerate(ts)]
@@ -403,45 +410,51 @@ class Car:
         groups = {"row": 1, "group128": -(-self.N // 128), "mx32": -(-self.N // 32)}
         return (1,) if kind == "static" else (self.M, groups[kind])
 
+    def _ptrs(self, ts, sizes, names):
+        """Device pointers of several tensors, each checked as by _ptr (None stays None)."""
+        dev = self.device  # one test for all is quicker than _ptr for each, which then names the one that failed
+        got = [None if t is None else t.data_ptr() if t.get_device() == dev and t.is_contiguous() and t.nbytes >= n else 0
+               for t, n in zip(ts, sizes)]
+        if 0 in got:
+            got = [None if t is None else _ptr(t, n, what, dev) for t, n, what in zip(ts, sizes, names)]
+        return got
+
     def reduce_residual_rmsnorm_quant(self, xs, residual, weight, eps, kind, residual_out, q_out, scales,
                                       norm_out=None, ar_out=None, stream=None):
         """kind: "row", "group128", "mx32" or "static" (see car_scale_kind).  q_out: M * N bytes (float8_e4m3fn or
         uint8); scales: quant_scales_shape(kind), written, or read for "static"."""
-        if kind not in SCALE_CODE:
+        code = SCALE_CODE.get(kind)
+        if code is None:
             raise ValueError(f"kind: {kind!r} is none of {', '.join(SCALE_CODE)}")
-        D, code = self.D, SCALE_CODE[kind]
-        check(car_reduce_residual_rmsnorm_quant(
-            self.h, self._ranks(xs, D, "inputs"), self._p(residual, D, "residual"), self._p(weight, D // self.M, "weight"),
-            eps, code, self._p(residual_out, D, "residual_out"), self._p(q_out, self.M * self.N, "q_out"),
-            self._p(scales, car_quant_scale_bytes(self.h, code), "scales"),
-            self._p(norm_out, D, "norm_out") if norm_out is not None else None,
-            self._p(ar_out, D, "ar_out") if ar_out is not None else None, _stream(stream)),
-            "car_reduce_residual_rmsnorm_quant")
+        D = self.D
+        res, w, ro, q, sc, no, ar = self._ptrs(
+            (residual, weight, residual_out, q_out, scales, norm_out, ar_out),
+            (D, D // self.M, D, self.M * self.N, self._scale_bytes[code], D, D),
+            ("residual", "weight", "residual_out", "q_out", "scales", "norm_out", "ar_out"))
+        check(_lib.car_reduce_residual_rmsnorm_quant(self.h, _table(self._ranks(xs, D, "inputs")), res, w, eps, code, ro, q,
+                                                     sc, no, ar, _stream(stream)), "car_reduce_residual_rmsnorm_quant")
 
     @property
     def backward_workspace_bytes(self) -> int:
-        return car_backward_workspace_bytes(self.h)
+        return self._workspace_bytes
 
     def reduce_residual_rmsnorm_backward(self, dnorm, residual_out, weight, eps, dresidual_out, dx, dweight=None,
                                          workspace=None, stream=None):
         """dresidual_out and dweight may be None; dweight is fp32.  With a dweight, workspace (backward_workspace_bytes
         bytes) is taken from torch's allocator on the current stream when none is given."""
-        D, ws = self.D, None
-        if dweight is not None:
-            need = self.backward_workspace_bytes
-            if workspace is None and need:
-                import torch
+        D, need = self.D, self._workspace_bytes if dweight is not None else 0
+        if need and workspace is None:
+            import torch
 
-                if stream is not None and _stream(stream) != torch.cuda.current_stream().cuda_stream:
-                    raise ValueError("workspace: give one for a call on another stream than the current one")
-                workspace = torch.empty(need, dtype=torch.uint8, device=dx.device)
-            ws = self._p(workspace, need, "workspace") if need else None
-        check(car_reduce_residual_rmsnorm_backward(
-            self.h, self._ranks(dnorm, D, "dnorm"), self._p(residual_out, D, "residual_out"),
-            self._p(weight, D // self.M, "weight"), eps,
-            self._p(dresidual_out, D, "dresidual_out") if dresidual_out is not None else None, self._p(dx, D, "dx"),
-            self._p(dweight, 4 * self.N, "dweight") if dweight is not None else None, ws, _stream(stream)),
-            "car_reduce_residual_rmsnorm_backward")
+            if stream is not None and _stream(stream) != torch.cuda.current_stream().cuda_stream:
+                raise ValueError("workspace: give one for a call on another stream than the current one")
+            workspace = torch.empty(need, dtype=torch.uint8, device=dx.device)
+        h, w, dro, out, dw, ws = self._ptrs(
+            (residual_out, weight, dresidual_out, dx, dweight, workspace if need else None),
+            (D, D // self.M, D, D, 4 * self.N, need),
+            ("residual_out", "weight", "dresidual_out", "dx", "dweight", "workspace"))
+        check(_lib.car_reduce_residual_rmsnorm_backward(self.h, _table(self._ranks(dnorm, D, "dnorm")), h, w, eps, dro, out,
+                                                        dw, ws, _stream(stream)), "car_reduce_residual_rmsnorm_backward")
 
     def ll128_encode(self, data, flag, wire, stream=None):
         check(car_ll128_encode(self.h, self._p(data, self.D, "data"), flag, self._p(wire, self.ll128_wire_bytes, "wire"),

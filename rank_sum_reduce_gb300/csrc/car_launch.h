@@ -111,31 +111,36 @@ cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void
 
 // ---- gradients of many tensors: rank sum, global norm, clipping (grads.cu) ----
 constexpr int kGradThreads = 256;
-constexpr int kGradChunkVecs = 2048;  // 16-byte vectors of one tensor that a CTA takes at a time
-struct GradTensor {
-  const void* in[16];
+constexpr int kGradChunkVecs = 2048;  // most 16-byte vectors of one tensor that a CTA takes at a time
+// With eight ranks and more the first pass takes shorter chunks: 608 CTAs then
+// read fewer distant places of each rank at a time (W = 8, 400 MB: 592 -> 531
+// us); with fewer ranks a thread's several vectors need the length.
+constexpr int kGradChunkVecsWide = 512;
+// Elements of one tensor, followed in memory by the W input pointers; all
+// pointers are at the chunk's first element.
+struct GradChunk {
   void* out;
-  int32_t dtype;
-  int32_t head;  // elements before the first 16-byte boundary that all pointers share; -1: they share none
-};
-struct GradChunk {  // elements [begin, begin + count) of one tensor
-  int64_t begin;
   int32_t count;
-  int32_t tensor;
+  int16_t dtype;
+  int16_t head;  // elements before the first 16-byte boundary that all pointers share; -1: they share none
+};
+struct GradList {
+  const uint8_t* chunks;  // descriptors of sizeof(GradChunk) + 8 W bytes
+  int n;
 };
 struct GradPlan {
-  const GradTensor* tensors;
-  const GradChunk* chunks;
-  int64_t n_chunks;
+  GradList reduce, clip;  // the same list but for eight ranks and more
   int W;
+  bool evict_first;       // the ranks' values give way to the outputs in L2
   double* partial;        // [grid]
   double* sumsq;          // the handle's own
   unsigned int* arrived;  // CTAs of the reduce that have written their partial
 };
-cudaError_t grads_occupancy(int W, int* reduce_blocks_per_sm, int* clip_blocks_per_sm);
-cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, double* sumsq, int grid, cudaStream_t s);
-cudaError_t launch_grads_clip(const GradPlan& plan, const double* sumsq, float max_norm, float* norm_out, int grid,
-                              cudaStream_t s);
+cudaError_t grads_occupancy(int W, int* reduce_per_sm, int* clip_per_sm);
+// store: write the sums (always with W > 1); without, launch_grads_clip takes the values from_input.
+cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s);
+cudaError_t launch_grads_clip(const GradPlan& plan, const double* sumsq, float scale, bool from_input, float max_norm,
+                              float* norm_out, int grid, cudaStream_t s);
 
 // ---- LL128 (ll128.cu) ----
 constexpr int kWireThreads = 256;

@@ -9,14 +9,29 @@
 // and does nothing when the norm is within the limit.  Keeping G in its type
 // between the passes costs a clipped value one more rounding of half a step
 // (what calling a reduce and then a clip would give) and keeps the second
-// pass at one read and one write of the tensors, from L2 where they fit:
-// chunks are taken in the opposite order, the last written first.
+// pass at one read and one write of the tensors.  With one rank the first pass
+// of car_grads_reduce_clip only reads: the second reads the input again, so
+// that a clipped step moves 3 tensors' bytes instead of 4 (and rounds once),
+// and one in place that needs no clipping moves 1.
 //
-// Work is cut into chunks of one tensor each; a CTA takes a contiguous share
-// of them.  Squares are summed in fp32 over a thread's part of one chunk
-// (at most 64 vectors) and in 64 bits from there on; the CTAs' partials are
-// added by the last CTA to arrive, in the order of their index, so the same
-// call gives the same bits.  Roofline: HBM, (W + 1) * 16 bytes per vector.
+// Work is cut into chunks of one tensor each, all of about the same length; a
+// wave of CTAs takes them in order, the second pass in the opposite order, the
+// last written first: what the first pass left in L2 (129 MB) is read from
+// there, and written over before it goes to HBM.  Where the outputs are not
+// much larger than L2 the ranks' values are read with an evict-first hint, so
+// that they do not push them out (W = 4, 134 MB: the second pass 42 -> 34 us);
+// where they are, that only costs (W = 8, 400 MB: the first pass 531 -> 572).
+//
+// A chunk's descriptor holds its pointers.  The plan never changes, so the
+// first descriptor, and a prefetch of the first 8 KB per rank into L2, come
+// before the PDL wait (W = 4, 8 MB: 11.0 -> 9.3 us).  Squares are summed in
+// fp32 over a thread's part of one chunk (kGradChunkVecs / kGradThreads = 8
+// vectors, 64 values) and over its warp, and in 64 bits from there on; the
+// CTAs' partials are added by the last CTA to arrive, in the order of their
+// index, so the same call gives the same bits.  Roofline: HBM, (W + 1) * 16
+// bytes per vector: 531 us for W = 8, 400 MB (1.00 of the copy peak).
+#include <stdint.h>
+
 #include "car_device.cuh"
 #include "car_launch.h"
 
@@ -44,15 +59,52 @@ struct Scalar<kFP32> {
   __device__ __forceinline__ static T down(float v) { return v; }
 };
 
-__device__ __forceinline__ double block_sum(double v, double* s_warp) {
+// 64-bit arithmetic is scarce on this part (about two operations a clock per
+// SM): each warp adds one 64-bit term per chunk, the block sum is one thread's
+// eight additions, and the square root and the quotient are fp32.  With every
+// thread doing these in 64 bits a clip that had nothing to do took 12 us.
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+// Sum over the block of a value that lane 0 of each warp holds; in thread 0.
+__device__ __forceinline__ double block_sum(double v, double* s_warp) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.0;
+  if (threadIdx.x == 0) {
 #pragma unroll
-  for (int w = 0; w < kGradThreads / 32; w++) v += s_warp[w];
+    for (int w = 0; w < kGradThreads / 32; w++) v += s_warp[w];
+  }
+  return v;
+}
+// sqrt(sumsq) in fp32, over the whole range of a sum of fp32 squares.
+__device__ __forceinline__ float norm_of(double sumsq) {
+  float post = 1.f;
+  if (sumsq > 0x1p+100) {
+    sumsq *= 0x1p-120;
+    post = 0x1p+60f;
+  } else if (sumsq < 0x1p-100) {
+    sumsq *= 0x1p+120;
+    post = 0x1p-60f;
+  }
+  return __fmul_rn(sqrtf((float)sumsq), post);
+}
+
+// L2 priority of values that are read once: first to be evicted, or as any.
+__device__ __forceinline__ uint64_t read_policy(bool evict_first) {
+  uint64_t first, normal;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+  return evict_first ? first : normal;
+}
+__device__ __forceinline__ uint4 ld_hint(const void* p, uint64_t policy) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p), "l"(policy));
   return v;
 }
 
@@ -62,98 +114,173 @@ struct Span {
   int head, vecs, tail;
 };
 template <int DT>
-__device__ __forceinline__ Span span_of(const GradTensor& t, const GradChunk& c) {
+__device__ __forceinline__ Span span_of(const GradChunk& c) {
   constexpr int E = Pack<DT>::kN;
-  if (t.head < 0) return Span{0, 0, c.count};
-  const int head = c.begin == 0 ? min(t.head, c.count) : 0;
+  if (c.head < 0) return Span{0, 0, c.count};
+  const int head = min((int)c.head, c.count);
   const int vecs = (c.count - head) / E;
   return Span{head, vecs, c.count - head - vecs * E};
 }
 
-template <int DT, int W>
-__device__ __forceinline__ float sum_chunk(const GradTensor& t, const GradChunk& c, int n, float scale) {
+// Vectors per thread per iteration, for 8 to 32 loads in flight per thread
+// (as the plain rank sum).
+template <int W>
+constexpr int kGradVectors = W >= 5 ? 1 : W >= 3 ? 2 : 4;
+
+template <int DT, int W, bool STORE>
+__device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const* __restrict__ in, int n, float scale,
+                                           uint64_t policy) {
   using S = Scalar<DT>;
   using T = typename S::T;
   constexpr int E = Pack<DT>::kN;
-  constexpr int R = W > 0 ? W : kMaxRanks;
-  const Span sp = span_of<DT>(t, c);
+  constexpr int R = W > 0 ? W : 1;
+  constexpr int U = kGradVectors<W>;
+  const Span sp = span_of<DT>(c);
+  const uint8_t* x[R];  // the whole vectors (of rank 0 where W is not compiled in)
+#pragma unroll
+  for (int r = 0; r < R; r++) x[r] = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
+  T* out = static_cast<T*>(c.out);
+  uint8_t* to = reinterpret_cast<uint8_t*>(out + sp.head);
   float ss = 0.f;
-  T* out = static_cast<T*>(t.out) + c.begin;
-  const int64_t body = c.begin + sp.head;
-  for (int v = threadIdx.x; v < sp.vecs; v += kGradThreads) {
-    uint4 raw[R];
+#pragma unroll 1
+  for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
+    // past the chunk's end the last vector is loaded again, and dropped below
+    uint32_t at[U];
+    float acc[U][E];
+    uint4 raw[U][R];
 #pragma unroll
-    for (int r = 0; r < R; r++)
-      if (r < n) raw[r] = ld_stream(reinterpret_cast<const uint4*>(static_cast<const T*>(t.in[r]) + body) + v);
-    float acc[E];
-    rank_sum<DT, R>(raw, n, acc);
+    for (int u = 0; u < U; u++) {
+      at[u] = (uint32_t)min(v0 + u * kGradThreads, sp.vecs - 1) * 16u;
 #pragma unroll
-    for (int e = 0; e < E; e++) {
-      acc[e] = __fmul_rn(acc[e], scale);
-      ss = fmaf(acc[e], acc[e], ss);
+      for (int r = 0; r < R; r++) raw[u][r] = ld_hint(x[r] + at[u], policy);
     }
-    st16(reinterpret_cast<uint4*>(out + sp.head) + v, Pack<DT>::narrow(acc));
+    if constexpr (W > 0) {
+#pragma unroll
+      for (int u = 0; u < U; u++) rank_sum<DT, R>(raw[u], W, acc[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; u++) Pack<DT>::widen(raw[u][0], acc[u]);
+#pragma unroll 1
+      for (int r = 1; r < n; r++) {
+        const uint8_t* from = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
+#pragma unroll
+        for (int u = 0; u < U; u++) raw[u][0] = ld_hint(from + at[u], policy);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          float f[E];
+          Pack<DT>::widen(raw[u][0], f);
+#pragma unroll
+          for (int e = 0; e < E; e++) acc[u][e] = __fadd_rn(acc[u][e], f[e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (v0 + u * kGradThreads < sp.vecs) {
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          acc[u][e] = __fmul_rn(acc[u][e], scale);
+          ss = fmaf(acc[u][e], acc[u][e], ss);
+        }
+        if constexpr (STORE) st16(to + at[u], Pack<DT>::narrow(acc[u]));
+      }
+    }
   }
   // the ragged ends
+#pragma unroll 1
   for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
     const int at = i < sp.head ? i : i + sp.vecs * E;
-    float acc = S::up(static_cast<const T*>(t.in[0])[c.begin + at]);
-    for (int r = 1; r < n; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(t.in[r])[c.begin + at]));
+    float acc = S::up(static_cast<const T*>(in[0])[at]);
+    for (int r = 1; r < n; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(in[r])[at]));
     acc = __fmul_rn(acc, scale);
     ss = fmaf(acc, acc, ss);
-    out[at] = S::down(acc);
+    if constexpr (STORE) out[at] = S::down(acc);
   }
   return ss;
 }
 
+// out = (from * scale) * coef, from being out itself or rank 0's input
 template <int DT>
-__device__ __forceinline__ void clip_chunk(const GradTensor& t, const GradChunk& c, float coef) {
+__device__ __forceinline__ void clip_chunk(const GradChunk& c, const void* from, float scale, float coef) {
   using S = Scalar<DT>;
   using T = typename S::T;
   constexpr int E = Pack<DT>::kN;
-  const Span sp = span_of<DT>(t, c);
-  T* out = static_cast<T*>(t.out) + c.begin;
-  uint4* body = reinterpret_cast<uint4*>(out + sp.head);
-  for (int v = threadIdx.x; v < sp.vecs; v += kGradThreads) {
-    float f[E];
-    Pack<DT>::widen(body[v], f);
+  constexpr int U = 4;
+  const Span sp = span_of<DT>(c);
+  T* out = static_cast<T*>(c.out);
+  const T* x = static_cast<const T*>(from);
+  uint4* to = reinterpret_cast<uint4*>(out + sp.head);
+  const uint4* body = reinterpret_cast<const uint4*>(x + sp.head);
+#pragma unroll 1
+  for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
+    uint4 raw[U];
 #pragma unroll
-    for (int e = 0; e < E; e++) f[e] = __fmul_rn(f[e], coef);
-    st16(body + v, Pack<DT>::narrow(f));
+    for (int u = 0; u < U; u++) raw[u] = ld_stream(body + min(v0 + u * kGradThreads, sp.vecs - 1));
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (v0 + u * kGradThreads < sp.vecs) {
+        float f[E];
+        Pack<DT>::widen(raw[u], f);
+#pragma unroll
+        for (int e = 0; e < E; e++) f[e] = __fmul_rn(__fmul_rn(f[e], scale), coef);
+        st16(to + v0 + u * kGradThreads, Pack<DT>::narrow(f));
+      }
+    }
   }
+#pragma unroll 1
   for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
     const int at = i < sp.head ? i : i + sp.vecs * E;
-    out[at] = S::down(__fmul_rn(S::up(out[at]), coef));
+    out[at] = S::down(__fmul_rn(__fmul_rn(S::up(x[at]), scale), coef));
   }
 }
 
-// This CTA's share [lo, hi) of the chunks.
-__device__ __forceinline__ void chunk_share(int64_t n, int64_t* lo, int64_t* hi) {
-  const int64_t share = n / gridDim.x, extra = n % gridDim.x;
-  *lo = share * blockIdx.x + (blockIdx.x < extra ? blockIdx.x : extra);
-  *hi = *lo + share + (blockIdx.x < extra ? 1 : 0);
+// Chunk i's descriptor: GradChunk, then the W input pointers.
+__device__ __forceinline__ const GradChunk* chunk_at(const GradList& l, int stride, int i) {
+  return reinterpret_cast<const GradChunk*>(l.chunks + (int64_t)i * stride);
+}
+__device__ __forceinline__ const void* const* inputs_of(const GradChunk* c) {
+  return reinterpret_cast<const void* const*>(c + 1);
 }
 
-template <int W>
-__global__ void __launch_bounds__(kGradThreads)
+// Asks L2 for the first vectors (8 KB at most) of one of a chunk's buffers.
+__device__ __forceinline__ void prefetch_chunk(const GradChunk& c, const void* from) {
+  const uintptr_t size = (uintptr_t)c.count * (c.dtype == kFP32 ? 4u : 2u);
+  const uintptr_t lo = (reinterpret_cast<uintptr_t>(from) + 15u) & ~(uintptr_t)15u;
+  const uintptr_t hi = (reinterpret_cast<uintptr_t>(from) + size) & ~(uintptr_t)15u;
+  if (hi > lo) prefetch_l2(reinterpret_cast<const void*>(lo), hi - lo < 8192u ? (uint32_t)(hi - lo) : 8192u);
+}
+
+template <int W, bool STORE>
+__global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
     grads_reduce_kernel(const GradPlan p, const float scale, double* __restrict__ sumsq) {
   __shared__ double s_warp[kGradThreads / 32];
   __shared__ bool s_last;
   const int n = W > 0 ? W : p.W;
-  int64_t lo, hi;
-  chunk_share(p.n_chunks, &lo, &hi);
+  const uint64_t policy = read_policy(STORE && p.evict_first);
+  const int first = blockIdx.x, last = p.reduce.n, stride = (int)sizeof(GradChunk) + 8 * n;
+  const GradChunk* d = chunk_at(p.reduce, stride, first);
+  GradChunk c = {};
+  if (first < last) {
+    c = *d;
+    if ((int)threadIdx.x < n) prefetch_chunk(c, inputs_of(d)[threadIdx.x]);
+  }
   pdl_wait_and_release();
   double total = 0.0;
-  for (int64_t i = lo; i < hi; i++) {
-    const GradChunk c = p.chunks[i];
-    const GradTensor& t = p.tensors[c.tensor];
-    float ss;
-    switch (t.dtype) {
-      case kBF16: ss = sum_chunk<kBF16, W>(t, c, n, scale); break;
-      case kFP16: ss = sum_chunk<kFP16, W>(t, c, n, scale); break;
-      default: ss = sum_chunk<kFP32, W>(t, c, n, scale); break;
+  for (int i = first; i < last; i += gridDim.x) {
+    const void* const* in = inputs_of(d);
+    const GradChunk cur = c;
+    if (i + (int)gridDim.x < last) {  // the next descriptor while this chunk is summed
+      d = chunk_at(p.reduce, stride, i + (int)gridDim.x);
+      c = *d;
     }
-    total += (double)ss;
+    float ss;
+    switch (cur.dtype) {
+      case kBF16: ss = sum_chunk<kBF16, W, STORE>(cur, in, n, scale, policy); break;
+      case kFP16: ss = sum_chunk<kFP16, W, STORE>(cur, in, n, scale, policy); break;
+      default: ss = sum_chunk<kFP32, W, STORE>(cur, in, n, scale, policy); break;
+    }
+    ss = warp_sum(ss);
+    if ((threadIdx.x & 31) == 0) total += (double)ss;
   }
   total = block_sum(total, s_warp);
   if (threadIdx.x == 0) {
@@ -166,6 +293,8 @@ __global__ void __launch_bounds__(kGradThreads)
     __threadfence();
     total = 0.0;
     for (unsigned i = threadIdx.x; i < gridDim.x; i += kGradThreads) total += __ldcg(p.partial + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     total = block_sum(total, s_warp);
     if (threadIdx.x == 0) {
       *sumsq = total;
@@ -174,57 +303,85 @@ __global__ void __launch_bounds__(kGradThreads)
   }
 }
 
+// FROM_INPUT: the values come from the one rank's input and the first pass
+// stored nothing.
+template <bool FROM_INPUT>
 __global__ void __launch_bounds__(kGradThreads)
-    grads_clip_kernel(const GradPlan p, const double* __restrict__ sumsq, const float max_norm, float* __restrict__ norm_out) {
-  pdl_wait_and_release();
-  const double norm = sqrt(*sumsq);
-  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  const double ratio = (double)max_norm / (norm + 1e-6);
+    grads_clip_kernel(const GradPlan p, const double* __restrict__ sumsq, const float scale, const float max_norm,
+                      float* __restrict__ norm_out) {
+  const int stride = (int)sizeof(GradChunk) + 8 * p.W;
+  int i = p.clip.n - 1 - (int)blockIdx.x;
+  GradChunk c = {};
+  const void* from = nullptr;
+  if (i >= 0) {
+    const GradChunk* d = chunk_at(p.clip, stride, i);
+    c = *d;
+    from = FROM_INPUT ? inputs_of(d)[0] : c.out;
+  }
+  // Released before the wait: where there is nothing to clip, the next
+  // kernel's prologue runs in the tail of the first pass.  It waits for this
+  // grid, and is only launched once every CTA here is resident.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float norm = norm_of(__ldcg(sumsq));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+  const float ratio = __fdiv_rn(max_norm, norm + 1e-6f);
   // within the limit, or no limit (false for a NaN norm, which then reaches every value)
-  if (ratio >= 1.0 || isinf(max_norm)) return;
-  const float coef = (float)ratio;
-  int64_t lo, hi;
-  chunk_share(p.n_chunks, &lo, &hi);
-  for (int64_t i = hi - 1; i >= lo; i--) {
-    const GradChunk c = p.chunks[i];
-    const GradTensor& t = p.tensors[c.tensor];
-    switch (t.dtype) {
-      case kBF16: clip_chunk<kBF16>(t, c, coef); break;
-      case kFP16: clip_chunk<kFP16>(t, c, coef); break;
-      default: clip_chunk<kFP32>(t, c, coef); break;
+  const bool whole = ratio >= 1.f || isinf(max_norm);
+  if (whole && !FROM_INPUT) return;
+  const float coef = whole ? 1.f : ratio;
+  for (; i >= 0; i -= (int)gridDim.x) {
+    const GradChunk cur = c;
+    const void* x = from;
+    if (i >= (int)gridDim.x) {
+      const GradChunk* d = chunk_at(p.clip, stride, i - (int)gridDim.x);
+      c = *d;
+      from = FROM_INPUT ? inputs_of(d)[0] : c.out;
+    }
+    if (FROM_INPUT && x == cur.out && whole && scale == 1.f) continue;  // already there
+    switch (cur.dtype) {
+      case kBF16: clip_chunk<kBF16>(cur, x, scale, coef); break;
+      case kFP16: clip_chunk<kFP16>(cur, x, scale, coef); break;
+      default: clip_chunk<kFP32>(cur, x, scale, coef); break;
     }
   }
 }
 
 using GradsFn = void (*)(const GradPlan, const float, double*);
-GradsFn pick_grads(int W) {
+GradsFn pick_grads(int W, bool store) {
+  if (!store) return W == 1 ? grads_reduce_kernel<1, false> : nullptr;
   switch (W) {
-    case 1: return grads_reduce_kernel<1>;
-    case 2: return grads_reduce_kernel<2>;
-    case 4: return grads_reduce_kernel<4>;
-    case 8: return grads_reduce_kernel<8>;
-    case 16: return grads_reduce_kernel<16>;
-    default: return grads_reduce_kernel<0>;
+    case 1: return grads_reduce_kernel<1, true>;
+    case 2: return grads_reduce_kernel<2, true>;
+    case 3: return grads_reduce_kernel<3, true>;
+    case 4: return grads_reduce_kernel<4, true>;
+    case 6: return grads_reduce_kernel<6, true>;
+    case 8: return grads_reduce_kernel<8, true>;
+    case 16: return grads_reduce_kernel<16, true>;
+    default: return grads_reduce_kernel<0, true>;
   }
 }
 
 }  // namespace
 
-cudaError_t grads_occupancy(int W, int* reduce_blocks_per_sm, int* clip_blocks_per_sm) {
+cudaError_t grads_occupancy(int W, int* reduce_per_sm, int* clip_per_sm) {
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      reduce_blocks_per_sm, reinterpret_cast<const void*>(pick_grads(W)), kGradThreads, 0);
+      reduce_per_sm, reinterpret_cast<const void*>(pick_grads(W, true)), kGradThreads, 0);
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(clip_blocks_per_sm,
-                                                       reinterpret_cast<const void*>(grads_clip_kernel), kGradThreads, 0);
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+      clip_per_sm, reinterpret_cast<const void*>(W == 1 ? grads_clip_kernel<true> : grads_clip_kernel<false>), kGradThreads, 0);
 }
 
-cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, double* sumsq, int grid, cudaStream_t s) {
-  return launch_pdl(pick_grads(plan.W), (unsigned)grid, kGradThreads, 0, s, 1, plan, scale, sumsq);
+cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s) {
+  GradsFn fn = pick_grads(plan.W, store);
+  if (!fn) return cudaErrorInvalidValue;
+  return launch_pdl(fn, (unsigned)grid, kGradThreads, 0, s, 1, plan, scale, sumsq);
 }
 
-cudaError_t launch_grads_clip(const GradPlan& plan, const double* sumsq, float max_norm, float* norm_out, int grid,
-                              cudaStream_t s) {
-  return launch_pdl(grads_clip_kernel, (unsigned)grid, kGradThreads, 0, s, 1, plan, sumsq, max_norm, norm_out);
+cudaError_t launch_grads_clip(const GradPlan& plan, const double* sumsq, float scale, bool from_input, float max_norm,
+                              float* norm_out, int grid, cudaStream_t s) {
+  return launch_pdl(from_input ? grads_clip_kernel<true> : grads_clip_kernel<false>, (unsigned)grid, kGradThreads, 0, s, 1,
+                    plan, sumsq, scale, max_norm, norm_out);
 }
 
 }  // namespace car

@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <unordered_set>
 #include <vector>
 
@@ -17,8 +18,8 @@
 
 struct car_grads {
   int device;
-  int reduce_grid, clip_grid;
-  void* memory;  // one allocation: tensors, chunks, partials, sum, counter
+  int grid, clip_grid;
+  void* memory;  // one allocation: chunks, partials, sum, counter
   car::GradPlan plan;
 };
 
@@ -85,14 +86,14 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   if (W < 1 || W > car::kMaxRanks || n < 1 || !numel || !dtypes || !inputs || !outs) return CAR_ERR_ARG;
   if (n > INT32_MAX / car::kMaxRanks) return CAR_ERR_SIZE;
   std::vector<int64_t> bytes((size_t)n);
-  int64_t n_chunks = 0;
+  int64_t vecs = 0;
   for (int64_t t = 0; t < n; t++) {
     if (dtypes[t] != CAR_BF16 && dtypes[t] != CAR_FP16 && dtypes[t] != CAR_FP32) return CAR_ERR_ARG;
     if (numel[t] < 0) return CAR_ERR_ARG;
     if (numel[t] > ((int64_t)1 << 48)) return CAR_ERR_SIZE;
     const int es = dtypes[t] == CAR_FP32 ? 4 : 2;
     bytes[t] = numel[t] * es;
-    n_chunks += bytes[t] / (16 * car::kGradChunkVecs) + 2;
+    vecs += bytes[t] / 16 + 1;
     if (!bytes[t]) continue;
     if (!outs[t] || reinterpret_cast<uintptr_t>(outs[t]) % es) return outs[t] ? CAR_ERR_ALIGN : CAR_ERR_ARG;
     for (int r = 0; r < W; r++) {
@@ -100,74 +101,97 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
       if (!p || reinterpret_cast<uintptr_t>(p) % es) return p ? CAR_ERR_ALIGN : CAR_ERR_ARG;
     }
   }
-  if (n_chunks > ((int64_t)1 << 31)) return CAR_ERR_SIZE;
+  if (vecs / car::kGradThreads > ((int64_t)1 << 30)) return CAR_ERR_SIZE;
   car_status st = check_overlap(W, n, bytes, inputs, outs);
   if (st != CAR_OK) return st;
 
-  std::vector<car::GradTensor> tensors((size_t)n);
-  std::vector<car::GradChunk> chunks;
-  chunks.reserve((size_t)n_chunks);
-  for (int64_t t = 0; t < n; t++) {
-    car::GradTensor& g = tensors[t];
-    std::memset(&g, 0, sizeof(g));
-    if (!bytes[t]) continue;
-    const int es = dtypes[t] == CAR_FP32 ? 4 : 2, E = 16 / es;
-    const uintptr_t off = reinterpret_cast<uintptr_t>(outs[t]) & 15u;
-    bool shared = true;
-    for (int r = 0; r < W; r++) {
-      g.in[r] = inputs[r * n + t];
-      shared = shared && (reinterpret_cast<uintptr_t>(g.in[r]) & 15u) == off;
-    }
-    g.out = outs[t];
-    g.dtype = (int32_t)dtypes[t];
-    const int head = (int)((16 - off) & 15u) / es;
-    g.head = shared ? head : -1;
-    // chunks start on a 16-byte boundary, but for the first, which takes the head too
-    const int64_t per = (int64_t)car::kGradChunkVecs * E;
-    for (int64_t b = 0; b < numel[t];) {
-      const int64_t count = std::min(numel[t] - b, per + (b == 0 && shared ? head : 0));
-      chunks.push_back(car::GradChunk{b, (int32_t)count, (int32_t)t});
-      b += count;
-    }
-  }
-
-  car_grads* g = new car_grads();
-  g->memory = nullptr;
-  cudaError_t e = cudaGetDevice(&g->device);
-  int num_sms = 0, per_reduce = 0, per_clip = 0;
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, g->device);
+  int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_clip = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, device);
   if (e == cudaSuccess) e = car::grads_occupancy(W, &per_reduce, &per_clip);
-  if (e != cudaSuccess) {
-    delete g;
-    return fail(e, "gradient launch sizes");
-  }
-  const int64_t most = std::max<int64_t>(1, (int64_t)chunks.size());
-  g->reduce_grid = (int)std::min<int64_t>(most, (int64_t)std::max(1, per_reduce) * num_sms);
-  g->clip_grid = (int)std::min<int64_t>(most, (int64_t)std::max(1, per_clip) * num_sms);
-  const size_t tb = tensors.size() * sizeof(car::GradTensor), cb = chunks.size() * sizeof(car::GradChunk);
-  const size_t pb = (size_t)g->reduce_grid * sizeof(double);
-  e = cudaMalloc(&g->memory, tb + cb + pb + 16);
-  if (e != cudaSuccess) {
-    delete g;
-    return fail(e, "cudaMalloc gradient plan");
-  }
-  uint8_t* m = static_cast<uint8_t*>(g->memory);
-  e = cudaMemcpy(m, tensors.data(), tb, cudaMemcpyHostToDevice);
-  if (e == cudaSuccess && cb) e = cudaMemcpy(m + tb, chunks.data(), cb, cudaMemcpyHostToDevice);
-  if (e == cudaSuccess) e = cudaMemset(m + tb + cb, 0, pb + 16);
+  if (e != cudaSuccess) return fail(e, "gradient launch sizes");
+  const int64_t reduce_cap = (int64_t)std::max(1, per_reduce) * num_sms, clip_cap = (int64_t)std::max(1, per_clip) * num_sms;
+  const size_t stride = sizeof(car::GradChunk) + (size_t)W * sizeof(void*);
+  std::vector<uint8_t> chunks;  // the reduce's list, then the clip's where that is another
+  // Appends chunks of one length, so many to each CTA of a resident wave: as
+  // long as `limit` vectors allow, and one pass of a CTA's threads at least.
+  // Tensors end inside a chunk, so the length grows (or a chunk each is added)
+  // until the chunks fill no more than whole waves: one chunk over would cost
+  // the time of a wave.  Many tensors shorter than a chunk cannot be evened out.
+  auto cut = [&](int64_t limit) {
+    int64_t each = std::max<int64_t>(1, (vecs + reduce_cap * limit - 1) / (reduce_cap * limit)), per_vecs = 0;
+    for (int tries = 0; tries < 64; tries++) {
+      if (per_vecs == 0) {
+        per_vecs = std::max<int64_t>(car::kGradThreads, (vecs + reduce_cap * each - 1) / (reduce_cap * each));
+      } else if (per_vecs + per_vecs / 64 + 1 <= limit) {
+        per_vecs += per_vecs / 64 + 1;
+      } else {
+        each++;
+        per_vecs = 0;
+        continue;
+      }
+      int64_t count = 0;
+      for (int64_t t = 0; t < n; t++) count += (bytes[t] / 16 + per_vecs) / per_vecs;
+      if (count <= reduce_cap * each) break;
+    }
+    if (per_vecs == 0) per_vecs = limit;
+    const size_t from = chunks.size();
+    for (int64_t t = 0; t < n; t++) {
+      if (!bytes[t]) continue;
+      const int es = dtypes[t] == CAR_FP32 ? 4 : 2, E = 16 / es;
+      const uintptr_t off = reinterpret_cast<uintptr_t>(outs[t]) & 15u;
+      bool shared = true;
+      for (int r = 0; r < W; r++) shared = shared && (reinterpret_cast<uintptr_t>(inputs[r * n + t]) & 15u) == off;
+      const int head = (int)((16 - off) & 15u) / es;
+      // chunks start on a 16-byte boundary, but for the first, which takes the head too
+      for (int64_t b = 0; b < numel[t];) {
+        car::GradChunk c;
+        c.out = static_cast<uint8_t*>(outs[t]) + b * es;
+        c.count = (int32_t)std::min(numel[t] - b, per_vecs * E + (b == 0 && shared ? head : 0));
+        c.dtype = (int16_t)dtypes[t];
+        c.head = (int16_t)(!shared ? -1 : b == 0 ? head : 0);
+        const size_t at = chunks.size();
+        chunks.resize(at + stride);
+        std::memcpy(chunks.data() + at, &c, sizeof(c));
+        for (int r = 0; r < W; r++) {
+          const void* p = static_cast<const uint8_t*>(inputs[r * n + t]) + b * es;
+          std::memcpy(chunks.data() + at + sizeof(c) + r * sizeof(p), &p, sizeof(p));
+        }
+        b += c.count;
+      }
+    }
+    return (int64_t)((chunks.size() - from) / stride);
+  };
+  const int64_t n_reduce = cut(W >= 8 ? car::kGradChunkVecsWide : car::kGradChunkVecs);
+  const size_t clip_at = W >= 8 ? chunks.size() : 0;
+  const int64_t n_clip = W >= 8 ? cut(car::kGradChunkVecs) : n_reduce;
+  const int grid = (int)std::max<int64_t>(1, std::min(n_reduce, reduce_cap));
+  const int clip_grid = (int)std::max<int64_t>(1, std::min(n_clip, clip_cap));
+  const size_t cb = chunks.size(), pb = (size_t)grid * sizeof(double);
+  void* memory = nullptr;
+  e = cudaMalloc(&memory, cb + pb + 16);
+  if (e != cudaSuccess) return fail(e, "cudaMalloc gradient plan");
+  uint8_t* m = static_cast<uint8_t*>(memory);
+  if (cb) e = cudaMemcpy(m, chunks.data(), cb, cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaMemset(m + cb, 0, pb + 16);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the plan is in place for calls on any stream
-  if (e != cudaSuccess) {
-    cudaFree(g->memory);
-    delete g;
-    return fail(e, "copy gradient plan");
+  car_grads* g = e == cudaSuccess ? new (std::nothrow) car_grads() : nullptr;
+  if (!g) {
+    cudaFree(memory);
+    return e == cudaSuccess ? refuse("out of host memory") : fail(e, "copy gradient plan");
   }
-  g->plan.tensors = reinterpret_cast<const car::GradTensor*>(m);
-  g->plan.chunks = reinterpret_cast<const car::GradChunk*>(m + tb);
-  g->plan.n_chunks = (int64_t)chunks.size();
+  g->device = device;
+  g->grid = grid;
+  g->clip_grid = clip_grid;
+  g->memory = memory;
+  g->plan.reduce = car::GradList{m, (int)n_reduce};
+  g->plan.clip = car::GradList{m + clip_at, (int)n_clip};
   g->plan.W = W;
-  g->plan.partial = reinterpret_cast<double*>(m + tb + cb);
-  g->plan.sumsq = reinterpret_cast<double*>(m + tb + cb + pb);
-  g->plan.arrived = reinterpret_cast<unsigned int*>(m + tb + cb + pb + 8);
+  g->plan.evict_first = 16 * vecs < 2 * (int64_t)l2;
+  g->plan.partial = reinterpret_cast<double*>(m + cb);
+  g->plan.sumsq = reinterpret_cast<double*>(m + cb + pb);
+  g->plan.arrived = reinterpret_cast<unsigned int*>(m + cb + pb + 8);
   {
     std::lock_guard<std::mutex> lk(g_mu);
     g_live.insert(g);
@@ -209,7 +233,7 @@ car_status car_grads_reduce(car_grads* g, float scale, double* sumsq, void* stre
   if (st != CAR_OK) return st;
   if (!sumsq || !std::isfinite(scale)) return CAR_ERR_ARG;
   if (!aligned(sumsq, 8)) return CAR_ERR_ALIGN;
-  cudaError_t e = car::launch_grads_reduce(g->plan, scale, sumsq, g->reduce_grid, static_cast<cudaStream_t>(stream));
+  cudaError_t e = car::launch_grads_reduce(g->plan, scale, true, sumsq, g->grid, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_reduce launch");
 }
 
@@ -218,7 +242,8 @@ car_status car_grads_clip(car_grads* g, const double* sumsq, float max_norm, flo
   if (st != CAR_OK) return st;
   if (!sumsq || !(max_norm >= 0.f)) return CAR_ERR_ARG;
   if (!aligned(sumsq, 8) || !aligned(norm_out, 4)) return CAR_ERR_ALIGN;
-  cudaError_t e = car::launch_grads_clip(g->plan, sumsq, max_norm, norm_out, g->clip_grid, static_cast<cudaStream_t>(stream));
+  cudaError_t e = car::launch_grads_clip(g->plan, sumsq, 1.f, false, max_norm, norm_out, g->clip_grid,
+                                         static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_clip launch");
 }
 
@@ -228,8 +253,10 @@ car_status car_grads_reduce_clip(car_grads* g, float scale, float max_norm, floa
   if (!std::isfinite(scale) || !(max_norm >= 0.f)) return CAR_ERR_ARG;
   if (!aligned(norm_out, 4)) return CAR_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = car::launch_grads_reduce(g->plan, scale, g->plan.sumsq, g->reduce_grid, s);
-  if (e == cudaSuccess) e = car::launch_grads_clip(g->plan, g->plan.sumsq, max_norm, norm_out, g->clip_grid, s);
+  const bool one = g->plan.W == 1;  // the first pass then only reads (see grads.cu)
+  cudaError_t e = car::launch_grads_reduce(g->plan, scale, !one, g->plan.sumsq, g->grid, s);
+  if (e == cudaSuccess)
+    e = car::launch_grads_clip(g->plan, g->plan.sumsq, one ? scale : 1.f, one, max_norm, norm_out, g->clip_grid, s);
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_reduce_clip launch");
 }
 
