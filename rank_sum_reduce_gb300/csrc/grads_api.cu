@@ -116,26 +116,11 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   std::vector<uint8_t> chunks;  // the reduce's list, then the clip's where that is another
   // Appends chunks of one length, so many to each CTA of a resident wave: as
   // long as `limit` vectors allow, and one pass of a CTA's threads at least.
-  // Tensors end inside a chunk, so the length grows (or a chunk each is added)
-  // until the chunks fill no more than whole waves: one chunk over would cost
-  // the time of a wave.  Many tensors shorter than a chunk cannot be evened out.
+  // (Stretching it until ragged tensor ends fit whole waves too measured no
+  // better.)
   auto cut = [&](int64_t limit) {
-    int64_t each = std::max<int64_t>(1, (vecs + reduce_cap * limit - 1) / (reduce_cap * limit)), per_vecs = 0;
-    for (int tries = 0; tries < 64; tries++) {
-      if (per_vecs == 0) {
-        per_vecs = std::max<int64_t>(car::kGradThreads, (vecs + reduce_cap * each - 1) / (reduce_cap * each));
-      } else if (per_vecs + per_vecs / 64 + 1 <= limit) {
-        per_vecs += per_vecs / 64 + 1;
-      } else {
-        each++;
-        per_vecs = 0;
-        continue;
-      }
-      int64_t count = 0;
-      for (int64_t t = 0; t < n; t++) count += (bytes[t] / 16 + per_vecs) / per_vecs;
-      if (count <= reduce_cap * each) break;
-    }
-    if (per_vecs == 0) per_vecs = limit;
+    const int64_t each = std::max<int64_t>(1, (vecs + reduce_cap * limit - 1) / (reduce_cap * limit));
+    const int64_t per_vecs = std::max<int64_t>(car::kGradThreads, (vecs + reduce_cap * each - 1) / (reduce_cap * each));
     const size_t from = chunks.size();
     for (int64_t t = 0; t < n; t++) {
       if (!bytes[t]) continue;
