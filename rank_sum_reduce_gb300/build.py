@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libcar.so")
 
-SOURCES = ["api.cu", "reduce.cu", "fused.cu", "fused_quant.cu", "fused_tma.cu", "fused_tma_quant.cu", "norm_backward.cu",
+SOURCES = ["api.cu", "reduce.cu", "fused.cu", "fused_quant.cu", "fused_tma.cu", "quant_tma.cu", "norm_backward.cu",
            "norm_backward_tma.cu", "grads.cu", "grads_api.cu", "ll128.cu", "ll.cu", "ll128_noalloc.cu", "lamport.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

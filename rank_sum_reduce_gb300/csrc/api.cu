@@ -51,10 +51,10 @@ struct car_ctx {
   car::FusedTmaShape tma_auto;
   car::FusedTmaShape tma;
   car::FusedShape quant;     // row kernel with an 8-bit output: the automatic shape, its own resident count
-  car::FusedTmaShape quant_tma;
+  car::TeamShape quant_tma;
   bool quant_pipeline;       // the 8-bit output runs the pipeline kernel
   car::FusedShape backward;  // backward of the fused op: row kernel
-  car::BackwardTmaShape backward_tma;
+  car::TeamShape backward_tma;
   bool backward_pipeline;
   int backward_groups;       // CTAs (or clusters) with a partial weight gradient each
   int fused_kernel_auto;  // CAR_FUSED_ROWS or CAR_FUSED_PIPELINE
@@ -228,6 +228,27 @@ car::FusedShape auto_lamport_shape(int W, int64_t M, int V, int num_sms) {
   return row_split_shape(W, M, V, num_sms, car::lamport_has_variant, car::lamport_max_threads, false);
 }
 
+// When the 8-bit output's pipeline kernel is faster than its row kernel.
+// Measured on GB300 (graph replay over cold inputs, bf16, scales of 128
+// columns, us per call, pipeline / rows).  One row at a time (N = 8192): W =
+// 8, M = 304 10.6 / 10.8, M = 456 14.2 / 15.2; W = 4, M = 304 7.5 / 6.8, M =
+// 456 10.0 / 10.7; W = 2, M = 456 8.0 / 8.1, M = 608 9.7 / 10.8.  Several
+// teams, one rank: N = 4096, M = 306 4.0 / 3.8, M = 400 4.1 / 4.3, M = 4096
+// 23.1 / 26.3.  More ranks: W = 4, N = 4096, M = 912 9.8 / 9.4, M = 1024 11.3
+// / 11.8; W = 2, N = 2048, M = 1824 7.8 / 7.6, M = 2432 9.5 / 10.0.  Eight
+// ranks and rows of 4 KB and more stay with the rows (N = 4096, M = 1216 17.2
+// / 16.2), shorter ones do not (N = 1024, M = 3648 13.8 / 14.1).  Rank counts
+// that the row kernel is not compiled for leave it early (W = 6, N = 4096, M =
+// 4096 45 / 65).
+bool quant_pipeline_pays(int W, int64_t M, int num_sms, const car::TeamShape& sh) {
+  const int64_t tiles = (M + sh.teams - 1) / sh.teams;
+  const bool compiled = W <= 2 || W == 4 || W == 8 || W == 16;  // the row kernel's instances
+  if (sh.teams == 1 || !compiled) return 2 * tiles >= 5 * (int64_t)num_sms;
+  if (W == 1) return 4 * tiles >= 5 * (int64_t)num_sms;
+  if (W == 16 || (W == 8 && sh.teams < 8)) return false;
+  return 3 * tiles >= 10 * (int64_t)num_sms || (sh.teams >= 8 && tiles >= 3 * (int64_t)num_sms);
+}
+
 // When the backward's pipeline kernel is faster than its row kernel.  Measured
 // on GB300 (graph replay over cold inputs, bf16, us per call with a weight
 // gradient, pipeline / rows): one or two ranks, rows short enough for several
@@ -238,7 +259,7 @@ car::FusedShape auto_lamport_shape(int W, int64_t M, int V, int num_sms) {
 // one issuing thread until a CTA has two to three tiles: W = 8, N = 4096, M =
 // 400 12.2 / 10.7, M = 912 16.9 / 18.2; W = 4, N = 8192, M = 200 10.3 / 9.5,
 // M = 456 13.7 / 14.2; W = 8, N = 8192, M = 304 14.2 / 16.5.
-bool backward_pipeline_pays(int W, int64_t M, int num_sms, const car::BackwardTmaShape& sh) {
+bool backward_pipeline_pays(int W, int64_t M, int num_sms, const car::TeamShape& sh) {
   const int64_t tiles = (M + sh.teams - 1) / sh.teams;
   if (W <= 2) return sh.teams > 1 && 2 * tiles >= num_sms;
   return 2 * tiles >= (sh.teams > 1 ? 5 : 4) * (int64_t)num_sms;
@@ -413,9 +434,9 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
     if ((e = car::fused_quant_resident_groups(h->dtype, W, h->quant, h->num_sms, &groups)) != cudaSuccess)
       return fail(e, "8-bit output occupancy");
     h->quant.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
-    h->quant_pipeline = h->fused_kernel_auto == CAR_FUSED_PIPELINE;
-    h->quant_tma = h->tma_auto;
-    if (h->quant_pipeline && (e = car::fused_tma_quant_prepare(h->dtype, W, &h->quant_tma)) != cudaSuccess)
+    h->quant_pipeline = car::quant_tma_shape(M, h->vec_per_row, h->num_sms, W, &h->quant_tma) &&
+                        quant_pipeline_pays(W, M, h->num_sms, h->quant_tma);
+    if (h->quant_pipeline && (e = car::quant_tma_prepare(h->dtype, h->quant_tma)) != cudaSuccess)
       return fail(e, "8-bit output pipeline smem");
     h->backward = row_split_shape(W, M, h->vec_per_row, h->num_sms, car::backward_has_variant, car::backward_max_threads, false);
     if ((e = car::backward_resident_groups(h->dtype, W, h->backward, h->num_sms, &groups)) != cudaSuccess)
@@ -622,8 +643,8 @@ car_status car_reduce_residual_rmsnorm_quant(car_ctx* h, const void* const* inpu
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (h->quant_pipeline)
-    e = car::launch_fused_tma_quant(h->dtype, h->W, tbl, residual, weight, eps, residual_out, out, norm_out, ar_out,
-                                    h->d_err, h->M, h->N, h->vec_per_row, h->quant_tma, s);
+    e = car::launch_quant_tma(h->dtype, h->W, tbl, residual, weight, eps, residual_out, out, norm_out, ar_out, h->d_err,
+                              h->M, h->N, h->vec_per_row, h->quant_tma, s);
   else
     e = car::launch_fused_quant(h->dtype, h->W, tbl, residual, weight, eps, residual_out, out, norm_out, ar_out, h->d_err,
                                 h->M, h->N, h->vec_per_row, h->quant, h->hook, s);

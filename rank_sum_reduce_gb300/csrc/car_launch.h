@@ -76,12 +76,20 @@ cudaError_t launch_fused_tma(int dtype, int W, const RankPtrs& in, const void* r
                              int64_t rows, int64_t cols, int vec_per_row, const FusedTmaShape& sh,
                              cudaStream_t s);
 
-// The same with an 8-bit output and scales (fused_tma_quant.cu); sh with cluster 1, whose smem grows.
-cudaError_t fused_tma_quant_prepare(int dtype, int W, FusedTmaShape* sh);
-cudaError_t launch_fused_tma_quant(int dtype, int W, const RankPtrs& in, const void* residual, const void* weight,
-                                   float eps, void* residual_out, const QuantOut& out, void* norm_out, void* ar_out,
-                                   unsigned int* err, int64_t rows, int64_t cols, int vec_per_row,
-                                   const FusedTmaShape& sh, cudaStream_t s);
+// ---- pipeline kernels whose CTAs work on several rows at a time ----
+struct TeamShape {
+  int team_threads;  // consumer threads of a row
+  int teams;         // rows a CTA works on at a time
+  int slots;         // ring depth, in slices of `teams` rows
+  int grid;
+  int smem;
+};
+// 8-bit output for many rows (quant_tma.cu); false when a row is too long for it.
+bool quant_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out);
+cudaError_t quant_tma_prepare(int dtype, const TeamShape& sh);
+cudaError_t launch_quant_tma(int dtype, int W, const RankPtrs& in, const void* residual, const void* weight, float eps,
+                             void* residual_out, const QuantOut& out, void* norm_out, void* ar_out, unsigned int* err,
+                             int64_t rows, int64_t cols, int vec_per_row, const TeamShape& sh, cudaStream_t s);
 
 // ---- backward of the fused op (norm_backward.cu) ----
 constexpr int kBackwardThreads = 512;
@@ -96,18 +104,11 @@ cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h,
 
 cudaError_t launch_sum_partials(const float* partial, float* out, int groups, int64_t cols, cudaStream_t s);
 // The pipeline form for many rows (norm_backward_tma.cu); false when a row is too long for it.
-struct BackwardTmaShape {
-  int team_threads;  // consumer threads of a row
-  int teams;         // rows a CTA works on at a time
-  int slots;         // ring depth, in slices of `teams` rows
-  int grid;
-  int smem;
-};
-bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BackwardTmaShape* out);
-cudaError_t backward_tma_prepare(int dtype, const BackwardTmaShape& sh);
+bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out);
+cudaError_t backward_tma_prepare(int dtype, const TeamShape& sh);
 cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
                                 const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
-                                int64_t rows, int64_t cols, int vec_per_row, const BackwardTmaShape& sh, cudaStream_t s);
+                                int64_t rows, int64_t cols, int vec_per_row, const TeamShape& sh, cudaStream_t s);
 
 // ---- gradients of many tensors: rank sum, global norm, clipping (grads.cu) ----
 constexpr int kGradThreads = 256;

@@ -1,7 +1,7 @@
 // norm_backward_tma.cu -- backward of rank sum + residual add + RMSNorm for
 // many rows, with the rows streamed into shared memory by TMA bulk copies.
 // Same operation as norm_backward.cu, in the manner of the forward's pipeline
-// kernel (fused_tma.cuh): one persistent CTA per SM, a producer thread that
+// kernel (fused_tma.cu): one persistent CTA per SM, a producer thread that
 // keeps a ring of slices in flight -- dy_0 .. dy_{W-1}, h, dres -- and
 // consumer warps that fold them into fp32 accumulators in rank order.
 //
@@ -338,7 +338,7 @@ constexpr int kRingBudget = 200 * 1024;
 
 }  // namespace
 
-bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BackwardTmaShape* out) {
+bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
   out->team_threads = ((vec_per_row + VPT - 1) / VPT + 31) / 32 * 32;
   if (out->team_threads > 512) return false;
@@ -357,13 +357,13 @@ bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, Backw
   return true;
 }
 
-cudaError_t backward_tma_prepare(int dtype, const BackwardTmaShape& sh) {
+cudaError_t backward_tma_prepare(int dtype, const TeamShape& sh) {
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
 }
 
 cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
                                 const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
-                                int64_t rows, int64_t cols, int vec_per_row, const BackwardTmaShape& sh, cudaStream_t s) {
+                                int64_t rows, int64_t cols, int vec_per_row, const TeamShape& sh, cudaStream_t s) {
   BackwardTmaParams p;
   p.dy = dy;
   p.h = static_cast<const uint8_t*>(h);

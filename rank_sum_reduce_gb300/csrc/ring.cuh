@@ -1,5 +1,5 @@
 // ring.cuh -- bounded waits and bulk copies of the kernels that stream row
-// slices through a ring of shared-memory slots (fused_tma.cuh,
+// slices through a ring of shared-memory slots (fused_tma.cu, quant_tma.cu,
 // norm_backward_tma.cu).
 #pragma once
 
