@@ -215,9 +215,10 @@ size_t car_quant_scale_bytes(car_ctx* h, car_scale_kind kind);
  *                   that is 0 or dweight is NULL.
  * The same call on the same data gives the same bits (no float atomics).
  * Errors: CAR_ERR_HANDLE, CAR_ERR_ARG (NULL, eps not finite or < 0),
- * CAR_ERR_ALIGN, CAR_ERR_SIZE (N*s > CAR_MAX_ROW_BYTES), CAR_ERR_CUDA; a
- * bounded wait that ran out is reported by car_sync (the row's dx is then
- * NaN). */
+ * CAR_ERR_ALIGN, CAR_ERR_SIZE (N*s > CAR_MAX_ROW_BYTES), CAR_ERR_CUDA.  The
+ * kernel and launch shape are chosen automatically.  Bounded waits that run
+ * out are reported by car_sync: in the columns of the threads that gave up
+ * the row's dx is then NaN, and so is dweight. */
 car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const void* residual_out,
                                                 const void* weight, float eps, const void* dresidual_out, void* dx,
                                                 void* dweight, void* workspace, void* stream);
@@ -463,8 +464,9 @@ car_status car_tune_fused(car_ctx* h, int kernel, int cluster, int threads, int 
  * of its bounded waits since the last car_sync (CAR_ERR_TIMEOUT; the flag is
  * then cleared).  Each wait is bounded to about one second: the pipelined
  * fused kernel's waits on its shared-memory barriers (it then stops and
- * leaves its remaining rows unwritten), and the waits of the fused row kernel
- * and the Lamport receive for the partials of a split row's other CTAs (each
+ * leaves its remaining rows unwritten; the pipelines of the 8-bit output and
+ * of the backward do the same), and the waits of the fused row kernel (with
+ * either output), the backward's row kernel and the Lamport receive for the partials of a split row's other CTAs (each
  * thread waits for itself: the row's norm_out is then NaN in the columns of
  * every thread whose wait ran out, or those columns of the Lamport row are
  * zeroed and the row is reported stale for every rank).  None of these waits
@@ -485,7 +487,10 @@ car_status car_sync(car_ctx* h, void* stream);
  * row's norm_out, and then waits (bounded by about one second) until the late
  * partial has landed before it goes on, so no partial reaches a CTA that has
  * exited.  Every other output is
- * unaffected.  With cta = -1 (and the other arguments 0) the default returns.
+ * unaffected.  The hook acts in the same way on rows that
+ * car_reduce_residual_rmsnorm_quant (NaN codes and scales) and
+ * car_reduce_residual_rmsnorm_backward (NaN in dx and dweight) split over a
+ * cluster.  With cta = -1 (and the other arguments 0) the default returns.
  * Errors: CAR_ERR_ARG for values out of range, CAR_ERR_HANDLE. */
 #define CAR_TEST_MAX_DELAY_NS 100000000ull /* 100 ms */
 car_status car_test_delay_partial(car_ctx* h, uint64_t wait_limit_ns, int cta, int64_t row, uint64_t delay_ns);

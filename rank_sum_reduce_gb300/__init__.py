@@ -313,9 +313,10 @@ def _raw_stream():
     return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """Handle of `stream`, or of torch's current stream on `device` (by default the current one)."""
     if stream is None:
-        return _raw_stream()(_cuda().current_device())
+        return _raw_stream()(_cuda().current_device() if device is None else device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -346,8 +347,11 @@ class Car:
         check(st, "car_create")
         self.h, self.W, self.M, self.N, self.dtype = h, W, M, N, dtype
         self.D = M * N * ELEM_SIZE[dtype]      # bytes per rank
-        self._scale_bytes = [car_quant_scale_bytes(h, k) for k in range(len(SCALE_CODE))]
+        D, Nw = self.D, N * ELEM_SIZE[dtype]
+        # bytes that the tensors of a call need, in the order of its arguments
+        self._quant_sizes = [(D, Nw, D, M * N, car_quant_scale_bytes(h, k), D, D) for k in range(len(SCALE_CODE))]
         self._workspace_bytes = car_backward_workspace_bytes(h)
+        self._backward_sizes = (D, Nw, D, D, 4 * N, self._workspace_bytes)
         import torch
 
         self.device = torch.cuda.current_device()
@@ -426,13 +430,12 @@ class Car:
         code = SCALE_CODE.get(kind)
         if code is None:
             raise ValueError(f"kind: {kind!r} is none of {', '.join(SCALE_CODE)}")
-        D = self.D
         res, w, ro, q, sc, no, ar = self._ptrs(
-            (residual, weight, residual_out, q_out, scales, norm_out, ar_out),
-            (D, D // self.M, D, self.M * self.N, self._scale_bytes[code], D, D),
+            (residual, weight, residual_out, q_out, scales, norm_out, ar_out), self._quant_sizes[code],
             ("residual", "weight", "residual_out", "q_out", "scales", "norm_out", "ar_out"))
-        check(_lib.car_reduce_residual_rmsnorm_quant(self.h, _table(self._ranks(xs, D, "inputs")), res, w, eps, code, ro, q,
-                                                     sc, no, ar, _stream(stream)), "car_reduce_residual_rmsnorm_quant")
+        check(_lib.car_reduce_residual_rmsnorm_quant(self.h, _table(self._ranks(xs, self.D, "inputs")), res, w, eps, code,
+                                                     ro, q, sc, no, ar, _stream(stream, self.device)),
+              "car_reduce_residual_rmsnorm_quant")
 
     @property
     def backward_workspace_bytes(self) -> int:
@@ -442,7 +445,7 @@ class Car:
                                          workspace=None, stream=None):
         """dresidual_out and dweight may be None; dweight is fp32.  With a dweight, workspace (backward_workspace_bytes
         bytes) is taken from torch's allocator on the current stream when none is given."""
-        D, need = self.D, self._workspace_bytes if dweight is not None else 0
+        need = self._workspace_bytes if dweight is not None else 0
         if need and workspace is None:
             import torch
 
@@ -450,11 +453,11 @@ class Car:
                 raise ValueError("workspace: give one for a call on another stream than the current one")
             workspace = torch.empty(need, dtype=torch.uint8, device=dx.device)
         h, w, dro, out, dw, ws = self._ptrs(
-            (residual_out, weight, dresidual_out, dx, dweight, workspace if need else None),
-            (D, D // self.M, D, D, 4 * self.N, need),
+            (residual_out, weight, dresidual_out, dx, dweight, workspace if need else None), self._backward_sizes,
             ("residual_out", "weight", "dresidual_out", "dx", "dweight", "workspace"))
-        check(_lib.car_reduce_residual_rmsnorm_backward(self.h, _table(self._ranks(dnorm, D, "dnorm")), h, w, eps, dro, out,
-                                                        dw, ws, _stream(stream)), "car_reduce_residual_rmsnorm_backward")
+        check(_lib.car_reduce_residual_rmsnorm_backward(self.h, _table(self._ranks(dnorm, self.D, "dnorm")), h, w, eps, dro,
+                                                        out, dw, ws, _stream(stream, self.device)),
+              "car_reduce_residual_rmsnorm_backward")
 
     def ll128_encode(self, data, flag, wire, stream=None):
         check(car_ll128_encode(self.h, self._p(data, self.D, "data"), flag, self._p(wire, self.ll128_wire_bytes, "wire"),

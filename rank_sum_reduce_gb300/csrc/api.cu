@@ -678,7 +678,7 @@ car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* d
                                  h->N, h->vec_per_row, h->backward_tma, s);
   else
     e = car::launch_backward(h->dtype, h->W, tbl, residual_out, weight, eps, dresidual_out, dx, dw, ws, h->d_err, h->M,
-                             h->N, h->vec_per_row, h->backward, s);
+                             h->N, h->vec_per_row, h->backward, h->hook, s);
   return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_residual_rmsnorm_backward launch");
 }
 

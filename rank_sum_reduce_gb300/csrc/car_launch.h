@@ -100,7 +100,8 @@ cudaError_t backward_resident_groups(int dtype, int W, const FusedShape& sh, int
 // workspace: groups * cols floats when groups > 1 and dweight is wanted.
 cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
                             const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
-                            int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh, cudaStream_t s);
+                            int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh, const WaitHook& hook,
+                            cudaStream_t s);
 
 cudaError_t launch_sum_partials(const float* partial, float* out, int groups, int64_t cols, cudaStream_t s);
 // The pipeline form for many rows (norm_backward_tma.cu); false when a row is too long for it.

@@ -47,6 +47,10 @@ struct BackwardParams {
   int cluster;
   int teams;           // rows a CTA works on at a time (1 with a cluster)
   int nranks;
+  unsigned long long wait_ns;   // as in the forward's row kernel (car_test_delay_partial)
+  unsigned long long delay_ns;
+  int64_t delay_row;
+  int delay_cta;
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -188,13 +192,15 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardMinCtas<W, VPT>) re
     }
     if (C > 1) {
       const uint32_t par = (it >> 1) & 1u;
+      // test hook: this whole CTA reaches the exchange late
+      if (crank == p.delay_cta && row == p.delay_row) spin_ns(p.delay_ns);
       if (warp == 0) {
         if (lane == 0) mbar_arrive_expect_tx(&s_xbar[b], 8u * (uint32_t)C);
         if (lane < C)
           st_async_v2_b32(map_rank(&s_part[b][crank], (uint32_t)lane), __float_as_uint(ss), __float_as_uint(c),
                           map_rank(&s_xbar[b], (uint32_t)lane));
       }
-      if (wait_cluster_phase(&s_xbar[b], par)) {
+      if (wait_cluster_phase(&s_xbar[b], par, p.wait_ns)) {
         ss = s_part[b][0].x;
         c = s_part[b][0].y;
         for (int r = 1; r < C; r++) {
@@ -204,6 +210,8 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardMinCtas<W, VPT>) re
       } else {
         atomicOr(p.err, 1u);
         ss = __int_as_float(0x7fc00000);  // NaN: this row's gradients are not usable
+        // the late partials are still waited for, so that none reaches a CTA
+        // that has exited and the phases stay in step
         if (!wait_cluster_phase(&s_xbar[b], par)) atomicOr(p.err, 2u);
       }
     }
@@ -368,7 +376,8 @@ cudaError_t backward_resident_groups(int dtype, int W, const FusedShape& sh, int
 
 cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
                             const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,
-                            int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh, cudaStream_t s) {
+                            int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh, const WaitHook& hook,
+                            cudaStream_t s) {
   BackwardFn fn = pick_backward(dtype, W, sh.vpt);
   if (!fn) return cudaErrorInvalidValue;
   BackwardParams p;
@@ -387,6 +396,10 @@ cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h,
   p.cluster = sh.cluster;
   p.teams = backward_teams(sh);
   p.nranks = W;
+  p.wait_ns = hook.wait_ns;
+  p.delay_ns = hook.delay_ns;
+  p.delay_row = hook.delay_row;
+  p.delay_cta = hook.delay_cta;
   cudaError_t e = launch_pdl(fn, (unsigned)(sh.groups * sh.cluster), (unsigned)(sh.threads * p.teams), 0, s, (unsigned)sh.cluster, p);
   if (e != cudaSuccess || !dweight || sh.groups == 1) return e;
   return launch_sum_partials(workspace, dweight, sh.groups, cols, s);
