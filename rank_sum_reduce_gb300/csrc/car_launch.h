@@ -134,6 +134,7 @@ struct GradPlan {
   GradList reduce, clip;  // the same list but for eight ranks and more
   int W;
   bool evict_first;       // the ranks' values give way to the outputs in L2
+  bool pass_on;           // so do the clip's outputs, to what it has yet to read
   double* partial;        // [grid]
   double* sumsq;          // the handle's own
   unsigned int* arrived;  // CTAs of the reduce that have written their partial

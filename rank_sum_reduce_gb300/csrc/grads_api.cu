@@ -174,6 +174,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   g->plan.clip = car::GradList{m + clip_at, (int)n_clip};
   g->plan.W = W;
   g->plan.evict_first = 16 * vecs < 2 * (int64_t)l2;
+  g->plan.pass_on = 16 * vecs > (int64_t)l2 / 4;
   g->plan.partial = reinterpret_cast<double*>(m + cb);
   g->plan.sumsq = reinterpret_cast<double*>(m + cb + pb);
   g->plan.arrived = reinterpret_cast<unsigned int*>(m + cb + pb + 8);
