@@ -78,6 +78,7 @@ cudaError_t launch_fused_tma(int dtype, int W, const RankPtrs& in, const void* r
 
 // ---- pipeline kernels whose CTAs work on several rows at a time ----
 struct TeamShape {
+  int vpt;           // 16-byte vectors per consumer thread (2, 4, 8)
   int team_threads;  // consumer threads of a row
   int teams;         // rows a CTA works on at a time
   int slots;         // ring depth, in slices of `teams` rows
@@ -105,7 +106,7 @@ cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h,
 
 cudaError_t launch_sum_partials(const float* partial, float* out, int groups, int64_t cols, cudaStream_t s);
 // The pipeline form for many rows (norm_backward_tma.cu); false when a row is too long for it.
-bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out);
+bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out);
 cudaError_t backward_tma_prepare(int dtype, const TeamShape& sh);
 cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
                                 const void* dres, void* dx, float* dweight, float* workspace, unsigned int* err,

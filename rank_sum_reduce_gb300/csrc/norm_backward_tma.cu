@@ -13,9 +13,9 @@
 // its own statistic and barrier: while one team is in the serial part of its
 // row another folds.
 //
-// h stays in registers (packed) from the statistic to the gradient; the dres
-// slice is only waited for after the statistic and is read from its slot
-// there.  The weight row lies in shared memory, the weight gradient of a
+// h stays in registers (packed) from the statistic to the gradient, or, with
+// more than two vectors per thread, in its slot; the dres slice is only waited
+// for after the statistic and is read from its slot there.  The weight row lies in shared memory, the weight gradient of a
 // team's rows in its registers for the whole kernel; the teams' are added in
 // shared memory at the end, one partial per CTA.  Every mbarrier wait is
 // bounded, as in the forward.
@@ -94,12 +94,12 @@ __device__ __forceinline__ void produce(const BackwardTmaParams& p, uint8_t* rin
   }
 }
 
-// Vectors per consumer thread.  Two: with one, the fixed work of a row (two
-// sums over the warp, a division, addresses) is done twice as often (W = 1,
-// N = 4096 bf16: 89 against 135 us); four spill.
-constexpr int VPT = 2;
-
-template <int DT>
+// VPT: vectors per consumer thread.  Two for rows of up to 1024 vectors: with
+// one, the fixed work of a row (two sums over the warp, a division, addresses)
+// is done twice as often (W = 1, N = 4096 bf16: 89 against 135 us).  Longer
+// rows take four, and fp32 ones eight; the accumulators of eight 16-bit
+// vectors would not fit in registers.
+template <int DT, int VPT>
 __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* ring, const uint8_t* s_weight, uint64_t* full,
                                         uint64_t* empty, uint64_t* rowbar, uint64_t* done, float2* s_warp,
                                         volatile int* s_abort) {
@@ -122,13 +122,19 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
   int slot = 0;
   uint32_t phase = 0, it = 0;
   bool failed = false;
-  auto release = [&] {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[slot]);
+  auto advance = [&] {
     if (++slot == S) {
       slot = 0;
       phase ^= 1u;
     }
+  };
+  auto release = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    advance();
+  };
+  auto weight = [&](int k) {
+    return VPT == 8 ? __ldg(p.weight + tid + k * T) : lds16(s_weight + 16 * (tid + k * T));
   };
   auto widen2 = [](uint4 v, float2 (&f)[E / 2]) {
     float t[E];
@@ -145,8 +151,9 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
       }
       break;
     }
+    constexpr bool HELD = VPT > 2;  // h is read again from its slot
     float2 g[VPT][E / 2];
-    uint4 hv[VPT];
+    uint4 hv[HELD ? 1 : VPT];
     float2 ss = make_float2(0.f, 0.f), c = make_float2(0.f, 0.f);
     for (int q = 0; q < n; q++) {
       if (!wait_bounded(&full[slot], phase, s_abort)) {
@@ -172,10 +179,11 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       if (ok[k]) {
-        hv[k] = lds16(mine + slot * stride + 16 * k * T);
+        const uint4 v = lds16(mine + slot * stride + 16 * k * T);
+        if constexpr (!HELD) hv[k] = v;
         float2 hf[E / 2], wf[E / 2];
-        widen2(hv[k], hf);
-        widen2(lds16(s_weight + 16 * (tid + k * T)), wf);
+        widen2(v, hf);
+        widen2(weight(k), wf);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) {
           ss = fma2(hf[e], hf[e], ss);
@@ -183,7 +191,12 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
         }
       }
     }
-    release();
+    const int hslot = slot;
+    if constexpr (HELD) {
+      advance();
+    } else {
+      release();
+    }
     // row statistics: every warp adds the team's warp partials itself, in the
     // same order; they are double-buffered by row parity
     float2 sum = make_float2(warp_sum(ss.x + ss.y), warp_sum(c.x + c.y));
@@ -213,8 +226,8 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
       if (ok[k]) {
         float2 hf[E / 2], wf[E / 2], df[E / 2];
         float o[E];
-        widen2(hv[k], hf);
-        widen2(lds16(s_weight + 16 * (tid + k * T)), wf);
+        widen2(HELD ? lds16(mine + hslot * stride + 16 * k * T) : hv[HELD ? 0 : k], hf);
+        widen2(weight(k), wf);
         widen2(p.dres ? lds16(mine + slot * stride + 16 * k * T) : make_uint4(0u, 0u, 0u, 0u), df);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) {
@@ -226,6 +239,10 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
         }
         st16(p.dx + row * (int64_t)p.vec_per_row + tid + k * T, Pack<DT>::narrow(o));
       }
+    }
+    if constexpr (HELD) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[hslot]);
     }
     if (p.dres) release();
   }
@@ -285,12 +302,12 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
   }
 }
 
-template <int DT>
+template <int DT, int VPT>
 __global__ void __launch_bounds__(544, 1) reduce_rmsnorm_backward_tma_kernel(const BackwardTmaParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int S = p.slots;
   uint8_t* s_weight = smem + (size_t)S * p.teams * p.row_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + p.row_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + (VPT == 8 ? 0 : p.row_bytes));
   uint64_t* empty = full + S;
   uint64_t* rowbar = empty + S;             // [16], by team
   uint64_t* done = rowbar + 16;             // [2]
@@ -318,47 +335,59 @@ __global__ void __launch_bounds__(544, 1) reduce_rmsnorm_backward_tma_kernel(con
   if (warp == nwarps) {
     if (lane == 0) produce(p, smem, full, empty, s_abort);
   } else {
-    for (int v = threadIdx.x; v < p.vec_per_row; v += consumers) reinterpret_cast<uint4*>(s_weight)[v] = __ldg(p.weight + v);
-    asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
-    consume<DT>(p, smem, s_weight, full, empty, rowbar, done, s_warp, s_abort);
+    if constexpr (VPT != 8) {
+      for (int v = threadIdx.x; v < p.vec_per_row; v += consumers) reinterpret_cast<uint4*>(s_weight)[v] = __ldg(p.weight + v);
+      asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
+    }
+    consume<DT, VPT>(p, smem, s_weight, full, empty, rowbar, done, s_warp, s_abort);
   }
 }
 
 using BackwardTmaFn = void (*)(const BackwardTmaParams);
 
-BackwardTmaFn pick(int dtype) {
+template <int DT>
+BackwardTmaFn pick_vpt(int vpt) {
+  if (vpt == 2) return reduce_rmsnorm_backward_tma_kernel<DT, 2>;
+  if (vpt == 4) return reduce_rmsnorm_backward_tma_kernel<DT, 4>;
+  if constexpr (DT == kFP32) return reduce_rmsnorm_backward_tma_kernel<DT, 8>;
+  return nullptr;
+}
+BackwardTmaFn pick(int dtype, int vpt) {
   switch (dtype) {
-    case kBF16: return reduce_rmsnorm_backward_tma_kernel<kBF16>;
-    case kFP16: return reduce_rmsnorm_backward_tma_kernel<kFP16>;
-    default: return reduce_rmsnorm_backward_tma_kernel<kFP32>;
+    case kBF16: return pick_vpt<kBF16>(vpt);
+    case kFP16: return pick_vpt<kFP16>(vpt);
+    default: return pick_vpt<kFP32>(vpt);
   }
 }
 
-constexpr int kRingBudget = 200 * 1024;
+constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 }  // namespace
 
-bool backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
+bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  out->team_threads = ((vec_per_row + VPT - 1) / VPT + 31) / 32 * 32;
+  const int vpt = vec_per_row <= 1024 ? 2 : vec_per_row <= 2048 ? 4 : 8;
+  if (vpt == 8 && dtype != kFP32) return false;
+  out->vpt = vpt;
+  out->team_threads = ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32;
   if (out->team_threads > 512) return false;
-  const int teams = 512 / out->team_threads;
+  const int teams = vpt > 2 ? 1 : 512 / out->team_threads;
   out->teams = teams;
   // about one tile's slices in flight, as in the forward
-  const int slice = teams * row_bytes;
+  const int slice = teams * row_bytes, weights = vpt == 8 ? 0 : row_bytes;
   int slots = W + 2 < 6 ? 6 : W + 2;
-  if (slots > kRingBudget / slice) slots = kRingBudget / slice;
+  if (slots > (kRingBudget - weights) / slice) slots = (kRingBudget - weights) / slice;
   out->slots = slots;
   const int64_t tiles = (rows + teams - 1) / teams;
   out->grid = (int)(tiles < num_sms ? tiles : num_sms);
   // the ring also takes the teams' weight gradients at the end
   if (slots < 2 || (int64_t)(teams - 1) * vec_per_row * 8 * 4 > (int64_t)slots * slice) return false;
-  out->smem = slots * slice + row_bytes + (2 * slots + 18) * 8 + 32 * 8 + 16;
+  out->smem = slots * slice + weights + (2 * slots + 18) * 8 + 32 * 8 + 16;
   return true;
 }
 
 cudaError_t backward_tma_prepare(int dtype, const TeamShape& sh) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
 }
 
 cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,
@@ -382,7 +411,7 @@ cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void
   p.teams = sh.teams;
   p.team_threads = sh.team_threads;
   p.nranks = W;
-  cudaError_t e = launch_pdl(pick(dtype), (unsigned)sh.grid, (unsigned)(sh.teams * sh.team_threads + 32), (size_t)sh.smem, s, 1, p);
+  cudaError_t e = launch_pdl(pick(dtype, sh.vpt), (unsigned)sh.grid, (unsigned)(sh.teams * sh.team_threads + 32), (size_t)sh.smem, s, 1, p);
   if (e != cudaSuccess || !dweight || sh.grid == 1) return e;
   return launch_sum_partials(workspace, dweight, sh.grid, cols, s);
 }

@@ -5,8 +5,15 @@
 // of `teams` consecutive rows; one bulk copy brings the same slice -- x_0 ..
 // x_{W-1}, residual -- of all rows of a tile, and each team of consumer warps
 // owns one row.  max |t| is found before the row statistic's barrier and
-// crosses it with the sum of squares (quant.cuh).  The weight row stays in
-// registers.  Every mbarrier wait is bounded.
+// crosses it with the sum of squares (quant.cuh).  Every mbarrier wait is
+// bounded.
+//
+// VPT: vectors per consumer thread.  Two for rows of up to 1024 vectors, with
+// the weight row in registers: with one, the fixed work of a row (sums over
+// the warp, a division, addresses) is done twice as often.  Longer rows take
+// one team with four, the weight row in shared memory, or eight, the weight
+// read from L2 once per row (64 KB of it beside the ring would leave two
+// slots).
 #include "car_launch.h"
 #include "quant.cuh"
 #include "ring.cuh"
@@ -80,11 +87,9 @@ __device__ __forceinline__ void produce(const QuantTmaParams& p, uint8_t* ring, 
   }
 }
 
-constexpr int VPT = 2;  // vectors per consumer thread (see norm_backward_tma.cu)
-
-template <int DT>
-__device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                        uint64_t* rowbar, float2* s_warp, volatile int* s_abort) {
+template <int DT, int VPT>
+__device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* ring, const uint8_t* s_weight, uint64_t* full,
+                                        uint64_t* empty, uint64_t* rowbar, float2* s_warp, volatile int* s_abort) {
   constexpr int E = Pack<DT>::kN;
   const int S = p.slots, T = p.team_threads, n = p.nranks;
   const int team = threadIdx.x / T, tid = threadIdx.x - team * T;
@@ -98,8 +103,13 @@ __device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* 
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     ok[k] = tid + k * T < p.vec_per_row;
-    wv[k] = ok[k] ? __ldg(p.weight + tid + k * T) : make_uint4(0u, 0u, 0u, 0u);
+    if (VPT == 2) wv[k] = ok[k] ? __ldg(p.weight + tid + k * T) : make_uint4(0u, 0u, 0u, 0u);
   }
+  auto weight = [&](int k) {
+    if constexpr (VPT == 2) return wv[k];
+    if constexpr (VPT == 4) return lds16(s_weight + 16 * (tid + k * T));
+    return __ldg(p.weight + tid + k * T);
+  };
   auto widen2 = [](uint4 v, float2 (&f)[E / 2]) {
     float t[E];
     Pack<DT>::widen(v, t);
@@ -163,7 +173,7 @@ __device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* 
           for (int e = 0; e < E / 2; e++) o[2 * e] = h[k][e].x, o[2 * e + 1] = h[k][e].y;
           st16(p.ar_out + rbase + k * T, Pack<DT>::narrow(o));
         }
-        widen2(wv[k], wf);
+        widen2(weight(k), wf);
         float m = 0.f;
 #pragma unroll
         for (int e = 0; e < E / 2; e++) {
@@ -224,11 +234,12 @@ __device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* 
   }
 }
 
-template <int DT>
+template <int DT, int VPT>
 __global__ void __launch_bounds__(544, 1) reduce_residual_rmsnorm_quant_tma_kernel(const QuantTmaParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int S = p.slots;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)S * p.teams * p.row_bytes);
+  uint8_t* s_weight = smem + (size_t)S * p.teams * p.row_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + (VPT == 4 ? p.row_bytes : 0));
   uint64_t* empty = full + S;
   uint64_t* rowbar = empty + S;                            // [16], by team
   float2* s_warp = reinterpret_cast<float2*>(rowbar + 16);  // [teams][2][warps of a team]: 32 at most
@@ -253,41 +264,56 @@ __global__ void __launch_bounds__(544, 1) reduce_residual_rmsnorm_quant_tma_kern
   if (warp == nwarps) {
     if (lane == 0) produce(p, smem, full, empty, s_abort);
   } else {
-    consume<DT>(p, smem, full, empty, rowbar, s_warp, s_abort);
+    if constexpr (VPT == 4) {
+      const int consumers = p.teams * p.team_threads;
+      for (int v = threadIdx.x; v < p.vec_per_row; v += consumers) reinterpret_cast<uint4*>(s_weight)[v] = __ldg(p.weight + v);
+      asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
+    }
+    consume<DT, VPT>(p, smem, s_weight, full, empty, rowbar, s_warp, s_abort);
   }
 }
 
 using QuantTmaFn = void (*)(const QuantTmaParams);
 
-QuantTmaFn pick(int dtype) {
+template <int DT>
+QuantTmaFn pick_vpt(int vpt) {
+  return vpt == 2   ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 2>
+         : vpt == 4 ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 4>
+                    : reduce_residual_rmsnorm_quant_tma_kernel<DT, 8>;
+}
+QuantTmaFn pick(int dtype, int vpt) {
   switch (dtype) {
-    case kBF16: return reduce_residual_rmsnorm_quant_tma_kernel<kBF16>;
-    case kFP16: return reduce_residual_rmsnorm_quant_tma_kernel<kFP16>;
-    default: return reduce_residual_rmsnorm_quant_tma_kernel<kFP32>;
+    case kBF16: return pick_vpt<kBF16>(vpt);
+    case kFP16: return pick_vpt<kFP16>(vpt);
+    default: return pick_vpt<kFP32>(vpt);
   }
 }
 
-constexpr int kRingBudget = 200 * 1024;
+constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 }  // namespace
 
 bool quant_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  out->team_threads = ((vec_per_row + VPT - 1) / VPT + 31) / 32 * 32;
+  const int vpt = vec_per_row <= 1024 ? 2 : vec_per_row <= 2048 ? 4 : 8;
+  out->vpt = vpt;
+  out->team_threads = ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32;
   if (out->team_threads > 512) return false;
   out->teams = 512 / out->team_threads;
-  const int slice = out->teams * row_bytes;
+  if (vpt > 2) out->teams = 1;
+  // about one tile's slices in flight, as in the other pipelines
+  const int slice = out->teams * row_bytes, weights = vpt == 4 ? row_bytes : 0;
   int slots = W + 1 < 6 ? 6 : W + 1;
-  if (slots > kRingBudget / slice) slots = kRingBudget / slice;
+  if (slots > (kRingBudget - weights) / slice) slots = (kRingBudget - weights) / slice;
   out->slots = slots;
   const int64_t tiles = (rows + out->teams - 1) / out->teams;
   out->grid = (int)(tiles < num_sms ? tiles : num_sms);
-  out->smem = slots * slice + (2 * slots + 16) * 8 + 32 * 8 + 16;
+  out->smem = slots * slice + weights + (2 * slots + 16) * 8 + 32 * 8 + 16;
   return slots >= 2;
 }
 
 cudaError_t quant_tma_prepare(int dtype, const TeamShape& sh) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
 }
 
 cudaError_t launch_quant_tma(int dtype, int W, const RankPtrs& in, const void* residual, const void* weight, float eps,
@@ -311,7 +337,7 @@ cudaError_t launch_quant_tma(int dtype, int W, const RankPtrs& in, const void* r
   p.teams = sh.teams;
   p.team_threads = sh.team_threads;
   p.nranks = W;
-  return launch_pdl(pick(dtype), (unsigned)sh.grid, (unsigned)(sh.teams * sh.team_threads + 32), (size_t)sh.smem, s, 1, p);
+  return launch_pdl(pick(dtype, sh.vpt), (unsigned)sh.grid, (unsigned)(sh.teams * sh.team_threads + 32), (size_t)sh.smem, s, 1, p);
 }
 
 }  // namespace car

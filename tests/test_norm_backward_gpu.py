@@ -60,6 +60,9 @@ CASES = [
     (16, 2, 4100, "fp32"), (16, 9, 1544, "bf16"), (5, 2, 32768, "bf16"), (2, 4, 16384, "fp32"), (1, 33, 4, "fp32"),
     (4, 400, 4096, "fp32"), (8, 600, 132, "fp32"), (8, 400, 8192, "bf16"), (4, 500, 5000, "fp16"), (1, 700, 16384, "bf16"),
     (1, 600, 4096, "bf16"), (6, 200, 8200, "bf16"), (2, 330, 32768, "fp16"), (16, 170, 4224, "fp32"), (8, 310, 16384, "bf16"),
+    # the pipeline kernel with four and eight vectors per thread, and with several teams whose last tile is not full
+    (3, 401, 10000, "bf16"), (1, 311, 8192, "fp32"), (6, 230, 16384, "fp32"), (5, 197, 16384, "fp16"), (1, 1301, 1024, "bf16"),
+    (3, 1001, 2056, "fp16"), (2, 901, 1000, "fp32"),
 ]
 
 

@@ -77,6 +77,9 @@ CASES = [
     (16, 2, 4100, "fp32"), (16, 9, 1544, "bf16"), (5, 2, 32768, "bf16"), (2, 4, 16384, "fp32"), (1, 33, 4, "fp32"),
     (4, 40, 1028, "fp32"), (8, 600, 132, "fp32"), (8, 400, 8192, "bf16"), (4, 500, 5000, "fp16"), (8, 320, 4096, "fp32"),
     (6, 200, 8200, "bf16"), (16, 170, 4224, "fp32"), (1, 400, 16392, "bf16"),
+    # the pipeline kernel with four and eight vectors per thread, and with several teams whose last tile is not full
+    (4, 391, 16384, "fp16"), (3, 401, 10000, "bf16"), (2, 303, 8192, "fp32"), (2, 231, 16384, "fp32"), (1, 301, 32768, "bf16"),
+    (1, 4099, 1024, "bf16"), (3, 1001, 2056, "fp16"), (2, 2601, 1000, "fp32"),
 ]
 
 
