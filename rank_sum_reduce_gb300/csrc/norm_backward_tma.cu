@@ -387,7 +387,8 @@ bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, i
 }
 
 cudaError_t backward_tma_prepare(int dtype, const TeamShape& sh) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt)), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kMaxDynamicSmem);
 }
 
 cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void* h, const void* weight, float eps,

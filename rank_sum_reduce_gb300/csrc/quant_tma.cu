@@ -313,7 +313,8 @@ bool quant_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShap
 }
 
 cudaError_t quant_tma_prepare(int dtype, const TeamShape& sh) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt)), cudaFuncAttributeMaxDynamicSharedMemorySize, sh.smem);
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt)), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kMaxDynamicSmem);
 }
 
 cudaError_t launch_quant_tma(int dtype, int W, const RankPtrs& in, const void* residual, const void* weight, float eps,

@@ -8,6 +8,12 @@
 namespace car {
 namespace {
 
+// Dynamic shared memory that the pipeline kernels' instances are allowed, the
+// most a CTA can have.  The allowance belongs to the kernel, not to a handle:
+// were it each handle's own need, a handle made later with a smaller ring
+// would take it from the earlier ones.
+constexpr int kMaxDynamicSmem = 227 * 1024;
+
 // Wait for the barrier phase with the given parity; false when the CTA is
 // aborting or the wait ran past kWaitLimitNs.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const volatile int* abort) {

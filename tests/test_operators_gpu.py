@@ -304,3 +304,21 @@ def test_quantised_calls_of_one_handle_on_two_streams(car):
     for o, v in zip(res, want):
         assert torch.equal(o[0], v[0]) and torch.equal(o[1].view(torch.uint8), v[1].view(torch.uint8)) and torch.equal(o[2], v[2])
     out.check()
+
+
+def test_handles_of_different_shapes_share_the_kernels(car):
+    """Handles whose pipelines run the same kernel instances with other ring sizes, made in every order: each still
+    launches after the others exist."""
+    shapes = [(8, 512, 8192, "bf16"), (1, 2500, 4096, "bf16"), (4, 700, 6144, "bf16"), (2, 2600, 2048, "bf16")]
+    for order in (shapes, shapes[::-1]):
+        cs = [car.Car(*s) for s in order]
+        for c, (W, M, N, _) in zip(cs, order):
+            g = gen(W + M)
+            xs, h = [randn(g, (M, N), "bf16") for _ in range(W)], randn(g, (M, N), "bf16")
+            w, ro, q = torch.ones(N, device=DEV).bfloat16(), torch.empty_like(h), torch.empty(M, N, dtype=torch.uint8, device=DEV)
+            c.reduce_residual_rmsnorm_quant(xs, h, w, 1e-6, "row", ro, q, torch.empty(M, 1, device=DEV))
+            c.reduce_residual_rmsnorm_backward(xs, h, w, 1e-6, None, torch.empty_like(h), torch.empty(N, device=DEV))
+            c.sync()
+            assert torch.equal(ro, (rank_sum(xs) + h.float()).bfloat16())
+        for c in cs:
+            c.close()
