@@ -233,35 +233,35 @@ car::FusedShape auto_lamport_shape(int W, int64_t M, int V, int num_sms) {
 bool rows_compiled(int W) { return W <= 2 || W == 4 || W == 8 || W == 16; }
 
 // When the 8-bit output's pipeline kernel is faster than its row kernel.
-// Measured on GB300 (graph replay over cold inputs, bf16 unless noted, us per
-// call, pipeline / rows).
-//  * Rows of up to 1024 vectors, one at a time (N = 8192, scales of 128
-//    columns): W = 8, M = 304 10.6 / 10.8, M = 456 14.2 / 15.2; W = 4, M = 304
-//    7.5 / 6.8, M = 456 10.0 / 10.7; W = 2, M = 456 8.0 / 8.1, M = 608 9.7 /
-//    10.8.
-//  * Shorter rows, several teams: one rank, N = 4096, M = 306 4.0 / 3.8, M =
-//    400 4.1 / 4.3, M = 4096 23.1 / 26.3; W = 4, N = 4096, M = 912 9.8 / 9.4, M
-//    = 1024 11.3 / 11.8; W = 2, N = 2048, M = 1824 7.8 / 7.6, M = 2432 9.5 /
-//    10.0.  Eight ranks and rows of 4 KB and more stay with the rows (N = 4096,
-//    M = 1216 17.2 / 16.2), shorter ones do not (N = 1024, M = 3648 13.8 /
-//    14.1).
-//  * Longer rows, four vectors per thread (N = 16384, one scale per row): W =
-//    4, M = 2000 63.9 / 78.5; W = 1, M = 4000 76 / 108; W = 8, M = 300 18.7 /
-//    20.3.  Eight vectors: fp32, N = 16384, W = 2, M = 2000 89 / 123; 16-bit
-//    types spill and have three ring slots only, N = 32768, W = 2, M = 1000 64
-//    / 69, but W = 8, M = 500 76 / 61.
+// Measured on GB300 (graph replay over cold inputs, bf16 unless noted, scales
+// of 128 columns, us per call, pipeline / rows).
+//  * One or two ranks: from two tiles per SM on.  W = 1, N = 4096, M = 912 6.9 /
+//    6.8, M = 1216 7.9 / 9.2; W = 2, N = 8192, M = 456 8.9 / 8.1, M = 608 10.2 /
+//    11.1.  Rows of at most 128 vectors (a warp each, no barrier) earlier: N =
+//    1024, W = 1, M = 1456 3.6 / 4.8, W = 2 4.0 / 4.9.
+//  * Four ranks: N = 8192, M = 304 7.5 / 6.8, M = 456 10.0 / 10.7; N = 4096, M =
+//    912 9.8 / 9.4, M = 1216 12.2 / 12.0, M = 2000 17.8 / 18.9; N = 1024, M =
+//    2432 7.3 / 6.9, M = 3648 9.7 / 11.3.
+//  * Eight ranks: N = 8192, M = 304 10.6 / 10.8, M = 456 14.2 / 15.2; rows of 4
+//    and 8 KB stay with the row kernel (N = 4096, M = 1216 17.2 / 16.2),
+//    shorter ones do not (N = 1024, M = 3648 13.8 / 14.1).
+//  * Rows of more than 1024 vectors (N = 16384, one scale per row): W = 4, M =
+//    2000 63.9 / 78.5; W = 1, M = 4000 76 / 108; W = 8, M = 300 18.7 / 20.3.
+//    More than 2048: fp32, N = 16384, W = 2, M = 2000 89 / 123; 16-bit types
+//    spill and have three ring slots only, N = 32768, W = 2, M = 1000 64 / 69,
+//    but W = 8, M = 500 76 / 61.
 //  * Rank counts that the row kernel is not compiled for: W = 6, N = 4096, M =
 //    4096 43 / 65; W = 3, N = 10000, M = 2000 40 / 118, N = 8192, M = 200 5.3 /
 //    7.1, N = 2048, M = 200 3.0 / 2.4.
-bool quant_pipeline_pays(int dtype, int W, int64_t M, int num_sms, const car::TeamShape& sh) {
-  const int64_t tiles = (M + sh.teams - 1) / sh.teams;
-  if (!rows_compiled(W)) return 4 * tiles >= 5 * (int64_t)num_sms;
-  if (sh.vpt == 8 && dtype != CAR_FP32 && W > 2) return false;
-  if (sh.vpt > 2) return 2 * tiles >= 3 * (int64_t)num_sms;
-  if (sh.teams == 1) return 2 * tiles >= 5 * (int64_t)num_sms;
-  if (W == 1) return 4 * tiles >= 5 * (int64_t)num_sms;
-  if (W == 16 || (W == 8 && sh.teams < 8)) return false;
-  return 3 * tiles >= 10 * (int64_t)num_sms || (sh.teams >= 8 && tiles >= 3 * (int64_t)num_sms);
+bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
+  const int64_t tiles = (h->M + sh.teams - 1) / sh.teams, sms = h->num_sms;
+  if (!rows_compiled(h->W)) return 2 * tiles >= sms;
+  if (h->vec_per_row > 2048) return (h->dtype == CAR_FP32 || h->W <= 2) && 2 * tiles >= 3 * sms;
+  if (h->vec_per_row > 1024) return 2 * tiles >= 3 * sms;
+  if (h->W <= 2) return tiles >= 2 * sms || (sh.teams >= 16 && 2 * tiles >= sms);
+  if (h->W == 4) return 2 * tiles >= (sh.teams == 1 ? 5 : sh.teams >= 8 ? 6 : 8) * sms;
+  if (h->vec_per_row > 512) return 2 * h->M >= 5 * sms;
+  return h->W == 8 && sh.teams >= 8 && tiles >= 3 * sms;
 }
 
 // When the backward's pipeline kernel is faster than its row kernel.  Measured
@@ -282,12 +282,12 @@ bool quant_pipeline_pays(int dtype, int W, int64_t M, int num_sms, const car::Te
 //  * Rank counts that the row kernel is not compiled for: W = 3, N = 10000, M =
 //    2000 57 / 127; W = 6, N = 16384 fp32, M = 500 65 / 80; W = 3, N = 8192, M =
 //    200 9.9 / 10.3.
-bool backward_pipeline_pays(int dtype, int W, int64_t M, int num_sms, const car::TeamShape& sh) {
-  const int64_t tiles = (M + sh.teams - 1) / sh.teams;
-  if (!rows_compiled(W)) return 4 * tiles >= 5 * (int64_t)num_sms;
-  if (sh.vpt > 2) return sh.vpt == 4 && dtype == CAR_FP32 && tiles >= 2 * (int64_t)num_sms;
-  if (W <= 2) return sh.teams > 1 && 2 * tiles >= num_sms;
-  return 2 * tiles >= (sh.teams > 1 ? 5 : 4) * (int64_t)num_sms;
+bool backward_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
+  const int64_t tiles = (h->M + sh.teams - 1) / sh.teams, sms = h->num_sms;
+  if (!rows_compiled(h->W)) return 4 * tiles >= 5 * sms;
+  if (h->vec_per_row > 1024) return sh.vpt == 4 && h->dtype == CAR_FP32 && tiles >= 2 * sms;
+  if (h->W <= 2) return sh.teams > 1 && 2 * tiles >= sms;
+  return 2 * tiles >= (sh.teams > 1 ? 5 : 4) * sms;
 }
 
 car_status finish_fused_shape(car_ctx* h, car::FusedShape sh) {
@@ -460,7 +460,7 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
       return fail(e, "8-bit output occupancy");
     h->quant.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
     h->quant_pipeline = car::quant_tma_shape(M, h->vec_per_row, h->num_sms, W, &h->quant_tma) &&
-                        quant_pipeline_pays(h->dtype, W, M, h->num_sms, h->quant_tma);
+                        quant_pipeline_pays(h, h->quant_tma);
     if (h->quant_pipeline && (e = car::quant_tma_prepare(h->dtype, h->quant_tma)) != cudaSuccess)
       return fail(e, "8-bit output pipeline smem");
     h->backward = row_split_shape(W, M, h->vec_per_row, h->num_sms, car::backward_has_variant, car::backward_max_threads, false);
@@ -469,7 +469,7 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
     const int64_t teams = car::backward_teams(h->backward);
     h->backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>((M + teams - 1) / teams, std::max(groups, 1)));
     h->backward_pipeline = car::backward_tma_shape(h->dtype, M, h->vec_per_row, h->num_sms, W, &h->backward_tma) &&
-                           backward_pipeline_pays(h->dtype, W, M, h->num_sms, h->backward_tma);
+                           backward_pipeline_pays(h, h->backward_tma);
     if (h->backward_pipeline && (e = car::backward_tma_prepare(h->dtype, h->backward_tma)) != cudaSuccess)
       return fail(e, "backward pipeline smem");
     h->backward_groups = h->backward_pipeline ? h->backward_tma.grid : h->backward.groups;

@@ -41,6 +41,7 @@ struct BackwardTmaParams {
   int slots;
   int slices;           // of a tile: W ranks, h, dres
   int teams;            // rows of a tile
+  uint32_t producers;   // 1 or 2
   int team_threads;     // multiple of 32
   int nranks;
 };
@@ -54,12 +55,17 @@ __device__ __forceinline__ uint32_t tile_bytes(const BackwardTmaParams& p, int64
   return (uint32_t)(left < p.teams ? left : p.teams) * (uint32_t)p.row_bytes;
 }
 
-// As the forward's producer: keeps the ring full, then waits for every copy
-// that it issued.  (Two or four producer threads measured the same or slower,
-// and so did h and dres loaded by the consumers instead: W = 8, M = 512, N =
-// 8192 bf16 21.2 us against 21.4 and 22.1.)
+// Producer `who` of p.producers, each in a warp of its own: issues every
+// p.producers-th copy of the CTA's sequence (copy c fills slot c % S as its use
+// c / S), then waits for the copies that it issued.  S is a multiple of
+// p.producers, so a slot is always filled by the same one: a producer that
+// could run ahead of a slot's previous use would take that use's parity for
+// its own.  Two measured up to 4 % faster than one with eight ranks and more,
+// four slower (W = 16, M = 512, N = 8192 bf16 31.4 / 30.9 / 30.9 us, W = 4, M =
+// 2000 40.7 / 40.8 / 45.9); h and dres loaded by the consumers instead were
+// slower too (W = 8, M = 512 20.4 against 19.8).
 __device__ __forceinline__ void produce(const BackwardTmaParams& p, uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                        volatile int* s_abort) {
+                                        volatile int* s_abort, uint32_t who) {
   const int S = p.slots;
   const size_t stride = (size_t)p.teams * p.row_bytes;
   int slot = 0;
@@ -70,12 +76,14 @@ __device__ __forceinline__ void produce(const BackwardTmaParams& p, uint8_t* rin
     const int64_t off = row * (int64_t)p.row_bytes;
     const uint32_t bytes = tile_bytes(p, row);
     for (int q = 0; q < p.slices; q++) {
-      if (issued >= (uint64_t)S && !wait_bounded(&empty[slot], phase ^ 1u, s_abort)) {
-        ok = false;
-        break;
+      if (((uint32_t)issued & (p.producers - 1u)) == who) {
+        if (issued >= (uint64_t)S && !wait_bounded(&empty[slot], phase ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&full[slot], bytes);
+        bulk_load(ring + slot * stride, slice_source(p, q) + off, bytes, &full[slot]);
       }
-      mbar_arrive_expect_tx(&full[slot], bytes);
-      bulk_load(ring + slot * stride, slice_source(p, q) + off, bytes, &full[slot]);
       issued++;
       if (++slot == S) {
         slot = 0;
@@ -90,15 +98,18 @@ __device__ __forceinline__ void produce(const BackwardTmaParams& p, uint8_t* rin
   const int used = issued < (uint64_t)S ? (int)issued : S;
   for (int k = 0; k < used; k++) {  // copy number c is use c / S of slot c % S
     const uint64_t c = issued - 1 - (uint64_t)k;
+    if (((uint32_t)c & (p.producers - 1u)) != who) continue;
     if (!wait_bounded_drain(&full[c % (uint64_t)S], (uint32_t)((c / (uint64_t)S) & 1u))) atomicOr(p.err, 1u);
   }
 }
 
 // VPT: vectors per consumer thread.  Two for rows of up to 1024 vectors: with
 // one, the fixed work of a row (two sums over the warp, a division, addresses)
-// is done twice as often (W = 1, N = 4096 bf16: 89 against 135 us).  Longer
-// rows take four, and fp32 ones eight; the accumulators of eight 16-bit
-// vectors would not fit in registers.
+// is done twice as often (W = 1, M = 16389, N = 4096 bf16: 89 against 135 us),
+// with four the accumulators leave little room to overlap (108) -- unless two
+// would leave a third of the threads without a row (W = 3, M = 4000, N = 5000:
+// 53.9 against 49.4).  Longer rows take four, and fp32 ones eight; the
+// accumulators of eight 16-bit vectors would not fit in registers.
 template <int DT, int VPT>
 __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* ring, const uint8_t* s_weight, uint64_t* full,
                                         uint64_t* empty, uint64_t* rowbar, uint64_t* done, float2* s_warp,
@@ -303,7 +314,7 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
 }
 
 template <int DT, int VPT>
-__global__ void __launch_bounds__(544, 1) reduce_rmsnorm_backward_tma_kernel(const BackwardTmaParams p) {
+__global__ void __launch_bounds__(512 + 32 * kProducers, 1) reduce_rmsnorm_backward_tma_kernel(const BackwardTmaParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int S = p.slots;
   uint8_t* s_weight = smem + (size_t)S * p.teams * p.row_bytes;
@@ -332,8 +343,8 @@ __global__ void __launch_bounds__(544, 1) reduce_rmsnorm_backward_tma_kernel(con
     prefetch_l2(slice_source(p, lane) + first * (int64_t)p.row_bytes, tile_bytes(p, first));
   __syncthreads();
   pdl_wait_and_release();
-  if (warp == nwarps) {
-    if (lane == 0) produce(p, smem, full, empty, s_abort);
+  if (warp >= nwarps) {
+    if (lane == 0) produce(p, smem, full, empty, s_abort, warp - nwarps);
   } else {
     if constexpr (VPT != 8) {
       for (int v = threadIdx.x; v < p.vec_per_row; v += consumers) reinterpret_cast<uint4*>(s_weight)[v] = __ldg(p.weight + v);
@@ -366,17 +377,25 @@ constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  const int vpt = vec_per_row <= 1024 ? 2 : vec_per_row <= 2048 ? 4 : 8;
+  auto threads = [&](int vpt) { return ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32; };
+  int vpt = 2;
+  if (vec_per_row > 2048) {
+    vpt = 8;
+  } else if (vec_per_row > 1024 || 512 / threads(2) * threads(2) < 352) {
+    vpt = 4;
+  }
   if (vpt == 8 && dtype != kFP32) return false;
   out->vpt = vpt;
-  out->team_threads = ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32;
+  out->team_threads = threads(vpt);
   if (out->team_threads > 512) return false;
-  const int teams = vpt > 2 ? 1 : 512 / out->team_threads;
+  const int teams = 512 / out->team_threads;
   out->teams = teams;
-  // about one tile's slices in flight, as in the forward
+  // about one tile's slices in flight, as in the forward, and an even number
   const int slice = teams * row_bytes, weights = vpt == 8 ? 0 : row_bytes;
-  int slots = W + 2 < 6 ? 6 : W + 2;
+  int slots = W + 2 < 6 ? 6 : (W + 3) / 2 * 2;
   if (slots > (kRingBudget - weights) / slice) slots = (kRingBudget - weights) / slice;
+  if (slots > 4) slots -= slots % kProducers;
+  out->producers = slots % kProducers == 0 ? kProducers : 1;
   out->slots = slots;
   const int64_t tiles = (rows + teams - 1) / teams;
   out->grid = (int)(tiles < num_sms ? tiles : num_sms);
@@ -410,9 +429,11 @@ cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void
   p.slots = sh.slots;
   p.slices = W + 1 + (dres ? 1 : 0);
   p.teams = sh.teams;
+  p.producers = (uint32_t)sh.producers;
   p.team_threads = sh.team_threads;
   p.nranks = W;
-  cudaError_t e = launch_pdl(pick(dtype, sh.vpt), (unsigned)sh.grid, (unsigned)(sh.teams * sh.team_threads + 32), (size_t)sh.smem, s, 1, p);
+  const unsigned threads = (unsigned)(sh.teams * sh.team_threads + 32 * sh.producers);
+  cudaError_t e = launch_pdl(pick(dtype, sh.vpt), (unsigned)sh.grid, threads, (size_t)sh.smem, s, 1, p);
   if (e != cudaSuccess || !dweight || sh.grid == 1) return e;
   return launch_sum_partials(workspace, dweight, sh.grid, cols, s);
 }

@@ -8,12 +8,17 @@
 // crosses it with the sum of squares (quant.cuh).  Every mbarrier wait is
 // bounded.
 //
-// VPT: vectors per consumer thread.  Two for rows of up to 1024 vectors, with
-// the weight row in registers: with one, the fixed work of a row (sums over
-// the warp, a division, addresses) is done twice as often.  Longer rows take
-// one team with four, the weight row in shared memory, or eight, the weight
-// read from L2 once per row (64 KB of it beside the ring would leave two
-// slots).
+// VPT: vectors per consumer thread.  Four (the weight row in shared memory) or
+// two (in registers): more of them divide the fixed work of a row (sums over
+// the warp, a division, addresses) and make room for more teams, fewer keep a
+// row's chain short.  Up to three ranks the CTA is bound by that work, and four
+// are faster (W = 1, M = 16389, N = 4096 bf16: 84 -> 70 us; W = 2, M = 2000, N
+// = 8192: 26.5 -> 23.9); with more the row waits for its slices and two are (W
+// = 8, M = 512, N = 8192: 15.9 against 16.9; W = 4, M = 2000, N = 4096 17.8
+// with six slots against 19.0 with four), unless they leave threads without a
+// row (W = 4, M = 8191, N = 6144: 112 against 95).  Rows of more than 2048
+// vectors take eight, the weight read from L2 once per row (64 KB of it beside
+// the ring would leave two slots).
 #include "car_launch.h"
 #include "quant.cuh"
 #include "ring.cuh"
@@ -37,6 +42,7 @@ struct QuantTmaParams {
   int vec_per_row;
   int slots;
   int teams;         // rows of a tile
+  uint32_t producers;   // 1 or 2
   int team_threads;  // multiple of 32
   int nranks;
 };
@@ -49,10 +55,10 @@ __device__ __forceinline__ uint32_t tile_bytes(const QuantTmaParams& p, int64_t 
   return (uint32_t)(left < p.teams ? left : p.teams) * (uint32_t)p.row_bytes;
 }
 
-// As the other pipeline kernels' producer: keeps the ring full, then waits
-// for every copy that it issued.
+// Producer `who`: every p.producers-th copy of the CTA's sequence; then it waits
+// for the copies that it issued (see norm_backward_tma.cu).
 __device__ __forceinline__ void produce(const QuantTmaParams& p, uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                        volatile int* s_abort) {
+                                        volatile int* s_abort, uint32_t who) {
   const int S = p.slots;
   const size_t stride = (size_t)p.teams * p.row_bytes;
   int slot = 0;
@@ -63,12 +69,14 @@ __device__ __forceinline__ void produce(const QuantTmaParams& p, uint8_t* ring, 
     const int64_t off = row * (int64_t)p.row_bytes;
     const uint32_t bytes = tile_bytes(p, row);
     for (int q = 0; q <= p.nranks; q++) {
-      if (issued >= (uint64_t)S && !wait_bounded(&empty[slot], phase ^ 1u, s_abort)) {
-        ok = false;
-        break;
+      if (((uint32_t)issued & (p.producers - 1u)) == who) {
+        if (issued >= (uint64_t)S && !wait_bounded(&empty[slot], phase ^ 1u, s_abort)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&full[slot], bytes);
+        bulk_load(ring + slot * stride, slice_source(p, q) + off, bytes, &full[slot]);
       }
-      mbar_arrive_expect_tx(&full[slot], bytes);
-      bulk_load(ring + slot * stride, slice_source(p, q) + off, bytes, &full[slot]);
       issued++;
       if (++slot == S) {
         slot = 0;
@@ -83,6 +91,7 @@ __device__ __forceinline__ void produce(const QuantTmaParams& p, uint8_t* ring, 
   const int used = issued < (uint64_t)S ? (int)issued : S;
   for (int k = 0; k < used; k++) {  // copy number c is use c / S of slot c % S
     const uint64_t c = issued - 1 - (uint64_t)k;
+    if (((uint32_t)c & (p.producers - 1u)) != who) continue;
     if (!wait_bounded_drain(&full[c % (uint64_t)S], (uint32_t)((c / (uint64_t)S) & 1u))) atomicOr(p.err, 1u);
   }
 }
@@ -235,7 +244,7 @@ __device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* 
 }
 
 template <int DT, int VPT>
-__global__ void __launch_bounds__(544, 1) reduce_residual_rmsnorm_quant_tma_kernel(const QuantTmaParams p) {
+__global__ void __launch_bounds__(512 + 32 * kProducers, 1) reduce_residual_rmsnorm_quant_tma_kernel(const QuantTmaParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int S = p.slots;
   uint8_t* s_weight = smem + (size_t)S * p.teams * p.row_bytes;
@@ -261,8 +270,8 @@ __global__ void __launch_bounds__(544, 1) reduce_residual_rmsnorm_quant_tma_kern
     prefetch_l2(slice_source(p, lane) + first * (int64_t)p.row_bytes, tile_bytes(p, first));
   __syncthreads();
   pdl_wait_and_release();
-  if (warp == nwarps) {
-    if (lane == 0) produce(p, smem, full, empty, s_abort);
+  if (warp >= nwarps) {
+    if (lane == 0) produce(p, smem, full, empty, s_abort, warp - nwarps);
   } else {
     if constexpr (VPT == 4) {
       const int consumers = p.teams * p.team_threads;
@@ -295,16 +304,26 @@ constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 bool quant_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  const int vpt = vec_per_row <= 1024 ? 2 : vec_per_row <= 2048 ? 4 : 8;
+  auto threads = [&](int vpt) { return ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32; };
+  int vpt = 2;
+  if (vec_per_row > 2048) {
+    vpt = 8;
+  } else if (vec_per_row > 1024 || W <= 3 || 512 / threads(2) * threads(2) < 448) {
+    vpt = 4;
+  }
   out->vpt = vpt;
-  out->team_threads = ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32;
+  out->team_threads = threads(vpt);
   if (out->team_threads > 512) return false;
   out->teams = 512 / out->team_threads;
-  if (vpt > 2) out->teams = 1;
-  // about one tile's slices in flight, as in the other pipelines
+  // About one tile's slices in flight, as in the other pipelines: more bulk
+  // copies at a time are slower (W = 1, M = 4096, N = 4096: 4 slots 19.3 us, 6
+  // 20.5; W = 4, M = 8191, N = 8192 with two vectors: 6 124, 4 146).  An even
+  // number: two producers.
   const int slice = out->teams * row_bytes, weights = vpt == 4 ? row_bytes : 0;
-  int slots = W + 1 < 6 ? 6 : W + 1;
+  int slots = W < 4 ? 4 : (W + 2) / 2 * 2;
   if (slots > (kRingBudget - weights) / slice) slots = (kRingBudget - weights) / slice;
+  if (slots > 4) slots -= slots % kProducers;
+  out->producers = slots % kProducers == 0 ? kProducers : 1;
   out->slots = slots;
   const int64_t tiles = (rows + out->teams - 1) / out->teams;
   out->grid = (int)(tiles < num_sms ? tiles : num_sms);
@@ -336,9 +355,11 @@ cudaError_t launch_quant_tma(int dtype, int W, const RankPtrs& in, const void* r
   p.vec_per_row = vec_per_row;
   p.slots = sh.slots;
   p.teams = sh.teams;
+  p.producers = (uint32_t)sh.producers;
   p.team_threads = sh.team_threads;
   p.nranks = W;
-  return launch_pdl(pick(dtype, sh.vpt), (unsigned)sh.grid, (unsigned)(sh.teams * sh.team_threads + 32), (size_t)sh.smem, s, 1, p);
+  const unsigned threads = (unsigned)(sh.teams * sh.team_threads + 32 * sh.producers);
+  return launch_pdl(pick(dtype, sh.vpt), (unsigned)sh.grid, threads, (size_t)sh.smem, s, 1, p);
 }
 
 }  // namespace car

@@ -14,6 +14,10 @@ namespace {
 // would take it from the earlier ones.
 constexpr int kMaxDynamicSmem = 227 * 1024;
 
+// Threads that issue the bulk copies of a CTA in the kernels whose CTAs work on
+// several rows at a time, where it divides the ring's slots.
+constexpr int kProducers = 2;
+
 // Wait for the barrier phase with the given parity; false when the CTA is
 // aborting or the wait ran past kWaitLimitNs.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const volatile int* abort) {
