@@ -424,7 +424,7 @@ cudaError_t fused_tma_prepare(int dtype, int W, const FusedTmaShape& sh) {
   TmaFn fn = pick_tma(dtype, W, sh.vpt, sh.ls);
   if (!fn) return cudaErrorInvalidValue;
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              sh.smem);
+                              kMaxDynamicSmem);  // not sh.smem: other handles launch the same kernel
 }
 
 bool fused_tma_shape(int64_t rows, int vec_per_row, int num_sms, int cluster, int W, FusedTmaShape* out) {

@@ -322,3 +322,20 @@ def test_handles_of_different_shapes_share_the_kernels(car):
             assert torch.equal(ro, (rank_sum(xs) + h.float()).bfloat16())
         for c in cs:
             c.close()
+
+
+def test_plain_pipeline_handles_share_their_kernels(car):
+    """The same for the fused op's pipeline: a handle with a smaller ring made later, or in between."""
+    W, M = 8, 300
+    big, small = car.Car(W, M, 8192, "bf16"), car.Car(W, M, 6144, "bf16")
+    for c in (big, small, big):
+        g = gen(c.N)
+        xs, res = [randn(g, (M, c.N), "bf16") for _ in range(W)], randn(g, (M, c.N), "bf16")
+        ro, no = torch.empty_like(res), torch.empty_like(res)
+        c.tune_fused(car.CAR_FUSED_PIPELINE)
+        small.tune_fused(car.CAR_FUSED_PIPELINE)
+        c.reduce_residual_rmsnorm(xs, res, torch.ones(c.N, device=DEV).bfloat16(), 1e-6, ro, no)
+        c.sync()
+        assert torch.equal(ro, (rank_sum(xs) + res.float()).bfloat16())
+    big.close()
+    small.close()
