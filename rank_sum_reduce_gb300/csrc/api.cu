@@ -242,9 +242,13 @@ bool rows_compiled(int W) { return W <= 2 || W == 4 || W == 8 || W == 16; }
 //  * Four ranks: N = 8192, M = 304 7.5 / 6.8, M = 456 10.0 / 10.7; N = 4096, M =
 //    912 9.8 / 9.4, M = 1216 12.2 / 12.0, M = 2000 17.8 / 18.9; N = 1024, M =
 //    2432 7.3 / 6.9, M = 3648 9.7 / 11.3.
+//    Where the row kernel's threads fit a row much better it stays ahead: N =
+//    1248 (156 vectors; 5 teams of 96 threads), M = 5950 19.4 / 18.3.
 //  * Eight ranks: N = 8192, M = 304 10.6 / 10.8, M = 456 14.2 / 15.2; rows of 4
-//    and 8 KB stay with the row kernel (N = 4096, M = 1216 17.2 / 16.2),
-//    shorter ones do not (N = 1024, M = 3648 13.8 / 14.1).
+//    and 8 KB stay with the row kernel (N = 4096, M = 1216 17.2 / 16.2, M = 6000
+//    78.9 / 76.9), shorter ones do not (N = 1024, M = 3648 13.8 / 14.1).
+//  * Sixteen: N = 2192, M = 2000 28 / 37; N = 4096, M = 1000 26.0 / 26.3; N =
+//    2776, M = 531 11.2 / 10.9.
 //  * Rows of more than 1024 vectors (N = 16384, one scale per row): W = 4, M =
 //    2000 63.9 / 78.5; W = 1, M = 4000 76 / 108; W = 8, M = 300 18.7 / 20.3.
 //    More than 2048: fp32, N = 16384, W = 2, M = 2000 89 / 123; 16-bit types
@@ -259,34 +263,42 @@ bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   if (h->vec_per_row > 2048) return (h->dtype == CAR_FP32 || h->W <= 2) && 2 * tiles >= 3 * sms;
   if (h->vec_per_row > 1024) return 2 * tiles >= 3 * sms;
   if (h->W <= 2) return tiles >= 2 * sms || (sh.teams >= 16 && 2 * tiles >= sms);
-  if (h->W == 4) return 2 * tiles >= (sh.teams == 1 ? 5 : sh.teams >= 8 ? 6 : 8) * sms;
   if (h->vec_per_row > 512) return 2 * h->M >= 5 * sms;
-  return h->W == 8 && sh.teams >= 8 && tiles >= 3 * sms;
+  if (sh.use < 0.8) return false;
+  if (h->W == 4) return tiles >= (sh.teams >= 8 ? 3 : 4) * sms;
+  if (h->W == 8) return sh.teams >= 8 && tiles >= 3 * sms;
+  return 2 * tiles >= 5 * sms;
 }
 
 // When the backward's pipeline kernel is faster than its row kernel.  Measured
 // as above, with a weight gradient, pipeline / rows.
 //  * One or two ranks, rows short enough for several teams: W = 1, N = 1024, M
 //    = 640 5.6 / 6.2, M = 3648 10.3 / 11.0; N = 4096, M = 912 10.4 / 11.3, M =
-//    16389 88 / 104.  With one team (N = 8192) the row kernel, which holds two
-//    rows' loads in registers there, stays ahead: M = 456 11.4 / 10.3, M = 2048
-//    28.3 / 28.0.
-//  * More ranks pay the ring's start and its one issuing thread until a CTA has
-//    two to three tiles: W = 8, N = 4096, M = 400 12.2 / 10.7, M = 912 16.9 /
-//    18.2; W = 4, N = 8192, M = 200 10.3 / 9.5, M = 456 13.7 / 14.2; W = 8, N =
-//    8192, M = 304 14.2 / 16.5.
-//  * Rows of more than 1024 vectors: four per thread pay in fp32 (N = 8192, W =
-//    1, M = 3000 62 / 80) and not in 16 bits, whose accumulators spill (N =
-//    16384, W = 4, M = 2000 87 / 79); eight do not (fp32, N = 16384, W = 2, M =
-//    2000 127 / 118).
+//    16389 88 / 104.  With one team the row kernel, which holds two rows' loads
+//    in registers there, stays ahead in 16 bits (N = 8192, M = 456 11.4 / 10.3,
+//    M = 2048 28.3 / 28.0) and not in fp32 (N = 4096, M = 1000 14.3 / 16.6).
+//  * More ranks pay the ring's start and its issuing threads until a CTA has two
+//    to three tiles: W = 8, N = 4096, M = 400 12.2 / 10.7, M = 912 16.9 / 18.2;
+//    W = 4, N = 8192, M = 200 10.3 / 9.5, M = 456 13.7 / 14.2; W = 8, N = 8192, M
+//    = 304 14.2 / 16.5.
+//  * Rows of more than 1024 vectors, three per thread: W = 1, N = 11072, M = 1737
+//    36 / 42; W = 4, N = 10488, M = 4085 102 / 141; N = 10000, M = 300 13.9 /
+//    14.1; W = 8, M = 200 17.4 / 15.5.  Four: fp32 as three; in 16 bits the
+//    accumulators leave little room, W = 4, M = 4000 N = 14000 137 / 147, N =
+//    16384 153 / 149.  Eight (fp32): N = 12800, W = 1, M = 3000 138 / 153; N =
+//    12000, W = 4, M = 3000 182 / 190; N = 16384, W = 2, M = 2000 127 / 118; N =
+//    11840, W = 8, M = 664 69 / 64.
 //  * Rank counts that the row kernel is not compiled for: W = 3, N = 10000, M =
-//    2000 57 / 127; W = 6, N = 16384 fp32, M = 500 65 / 80; W = 3, N = 8192, M =
-//    200 9.9 / 10.3.
+//    2000 56 / 127; W = 6, N = 16384 fp32, M = 500 62 / 80; W = 3, N = 8192, M =
+//    200 9.7 / 10.3.
 bool backward_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int64_t tiles = (h->M + sh.teams - 1) / sh.teams, sms = h->num_sms;
-  if (!rows_compiled(h->W)) return 4 * tiles >= 5 * sms;
-  if (h->vec_per_row > 1024) return sh.vpt == 4 && h->dtype == CAR_FP32 && tiles >= 2 * sms;
-  if (h->W <= 2) return sh.teams > 1 && 2 * tiles >= sms;
+  const int V = h->vec_per_row;
+  if (!rows_compiled(h->W)) return 2 * tiles >= sms;
+  if (V > 2048) return V <= 3328 && h->W <= 4 && tiles >= 8 * sms;
+  if (V > 1024) return tiles >= 2 * sms && (h->dtype == CAR_FP32 || V <= 1792);
+  if (h->W <= 2 && sh.teams == 1) return h->dtype == CAR_FP32 && tiles >= 4 * sms;
+  if (h->W <= 2) return 2 * tiles >= sms;
   return 2 * tiles >= (sh.teams > 1 ? 5 : 4) * sms;
 }
 

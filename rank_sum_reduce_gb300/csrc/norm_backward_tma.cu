@@ -162,7 +162,7 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
       }
       break;
     }
-    constexpr bool HELD = VPT > 2;  // h is read again from its slot
+    constexpr bool HELD = VPT > 3;  // h is read again from its slot
     float2 g[VPT][E / 2];
     uint4 hv[HELD ? 1 : VPT];
     float2 ss = make_float2(0.f, 0.f), c = make_float2(0.f, 0.f);
@@ -359,6 +359,7 @@ using BackwardTmaFn = void (*)(const BackwardTmaParams);
 template <int DT>
 BackwardTmaFn pick_vpt(int vpt) {
   if (vpt == 2) return reduce_rmsnorm_backward_tma_kernel<DT, 2>;
+  if (vpt == 3) return reduce_rmsnorm_backward_tma_kernel<DT, 3>;
   if (vpt == 4) return reduce_rmsnorm_backward_tma_kernel<DT, 4>;
   if constexpr (DT == kFP32) return reduce_rmsnorm_backward_tma_kernel<DT, 8>;
   return nullptr;
@@ -377,16 +378,11 @@ constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  auto threads = [&](int vpt) { return ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32; };
-  int vpt = 2;
-  if (vec_per_row > 2048) {
-    vpt = 8;
-  } else if (vec_per_row > 1024 || 512 / threads(2) * threads(2) < 352) {
-    vpt = 4;
-  }
+  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, 2);
   if (vpt == 8 && dtype != kFP32) return false;
   out->vpt = vpt;
-  out->team_threads = threads(vpt);
+  out->use = team_use(vec_per_row, vpt);
+  out->team_threads = team_threads(vec_per_row, vpt);
   if (out->team_threads > 512) return false;
   const int teams = 512 / out->team_threads;
   out->teams = teams;

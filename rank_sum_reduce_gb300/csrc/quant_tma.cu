@@ -116,7 +116,7 @@ __device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* 
   }
   auto weight = [&](int k) {
     if constexpr (VPT == 2) return wv[k];
-    if constexpr (VPT == 4) return lds16(s_weight + 16 * (tid + k * T));
+    if constexpr (VPT < 8) return lds16(s_weight + 16 * (tid + k * T));
     return __ldg(p.weight + tid + k * T);
   };
   auto widen2 = [](uint4 v, float2 (&f)[E / 2]) {
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1) reduce_residual_rmsn
   extern __shared__ __align__(1024) uint8_t smem[];
   const int S = p.slots;
   uint8_t* s_weight = smem + (size_t)S * p.teams * p.row_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + (VPT == 4 ? p.row_bytes : 0));
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + (VPT == 3 || VPT == 4 ? p.row_bytes : 0));
   uint64_t* empty = full + S;
   uint64_t* rowbar = empty + S;                            // [16], by team
   float2* s_warp = reinterpret_cast<float2*>(rowbar + 16);  // [teams][2][warps of a team]: 32 at most
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1) reduce_residual_rmsn
   if (warp >= nwarps) {
     if (lane == 0) produce(p, smem, full, empty, s_abort, warp - nwarps);
   } else {
-    if constexpr (VPT == 4) {
+    if constexpr (VPT == 3 || VPT == 4) {
       const int consumers = p.teams * p.team_threads;
       for (int v = threadIdx.x; v < p.vec_per_row; v += consumers) reinterpret_cast<uint4*>(s_weight)[v] = __ldg(p.weight + v);
       asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
@@ -287,6 +287,7 @@ using QuantTmaFn = void (*)(const QuantTmaParams);
 template <int DT>
 QuantTmaFn pick_vpt(int vpt) {
   return vpt == 2   ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 2>
+         : vpt == 3 ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 3>
          : vpt == 4 ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 4>
                     : reduce_residual_rmsnorm_quant_tma_kernel<DT, 8>;
 }
@@ -304,22 +305,17 @@ constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 bool quant_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  auto threads = [&](int vpt) { return ((vec_per_row + vpt - 1) / vpt + 31) / 32 * 32; };
-  int vpt = 2;
-  if (vec_per_row > 2048) {
-    vpt = 8;
-  } else if (vec_per_row > 1024 || W <= 3 || 512 / threads(2) * threads(2) < 448) {
-    vpt = 4;
-  }
+  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, W <= 3 ? 4 : 2);
   out->vpt = vpt;
-  out->team_threads = threads(vpt);
+  out->use = team_use(vec_per_row, vpt);
+  out->team_threads = team_threads(vec_per_row, vpt);
   if (out->team_threads > 512) return false;
   out->teams = 512 / out->team_threads;
   // About one tile's slices in flight, as in the other pipelines: more bulk
   // copies at a time are slower (W = 1, M = 4096, N = 4096: 4 slots 19.3 us, 6
   // 20.5; W = 4, M = 8191, N = 8192 with two vectors: 6 124, 4 146).  An even
   // number: two producers.
-  const int slice = out->teams * row_bytes, weights = vpt == 4 ? row_bytes : 0;
+  const int slice = out->teams * row_bytes, weights = vpt == 3 || vpt == 4 ? row_bytes : 0;
   int slots = W < 4 ? 4 : (W + 2) / 2 * 2;
   if (slots > (kRingBudget - weights) / slice) slots = (kRingBudget - weights) / slice;
   if (slots > 4) slots -= slots % kProducers;

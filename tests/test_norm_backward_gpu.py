@@ -63,6 +63,8 @@ CASES = [
     # the pipeline kernel with four and eight vectors per thread, and with several teams whose last tile is not full
     (3, 401, 10000, "bf16"), (1, 311, 8192, "fp32"), (6, 230, 16384, "fp32"), (5, 197, 16384, "fp16"), (1, 1301, 1024, "bf16"),
     (3, 1001, 2056, "fp16"), (2, 901, 1000, "fp32"),
+    # three vectors per thread
+    (8, 401, 6144, "bf16"), (4, 331, 10488, "fp16"), (1, 311, 11072, "bf16"), (16, 307, 4656, "fp32"), (1, 1231, 12800, "fp32"),
 ]
 
 

@@ -80,6 +80,8 @@ CASES = [
     # the pipeline kernel with four and eight vectors per thread, and with several teams whose last tile is not full
     (4, 391, 16384, "fp16"), (3, 401, 10000, "bf16"), (2, 303, 8192, "fp32"), (2, 231, 16384, "fp32"), (1, 301, 32768, "bf16"),
     (1, 4099, 1024, "bf16"), (3, 1001, 2056, "fp16"), (2, 2601, 1000, "fp32"),
+    # three vectors per thread
+    (8, 411, 6144, "bf16"), (4, 391, 9352, "fp16"), (16, 803, 2192, "bf16"), (2, 401, 4728, "fp32"),
 ]
 
 
