@@ -1,7 +1,8 @@
 /*
  * car.h -- C ABI of libcar: one-shot rank-sum reduce, fused residual add +
- * RMSNorm, and LL / LL128 line encode, validate and decode-reduce, for one
- * GB300 (sm_103a).
+ * RMSNorm (also with an 8-bit output and scales, and its backward), rank sums
+ * of many gradient tensors with their global norm and clipping, and LL / LL128
+ * line encode, validate and decode-reduce, for one GB300 (sm_103a).
  *
  * The W "ranks" are W separate device buffers on the same GPU: they stand in
  * for the peer-mapped buffers a multi-GPU one-shot all-reduce reads.  There is

@@ -1,8 +1,8 @@
 """Rank sum, global norm and clipping of many gradient tensors (car_grads_*) against plain sums in 64 bits.
 
-Sums and their rounding are exact (fp32 in rank order, one product with the scale).  The norm: at most 64 squares are
-added in a row in fp32 (65 roundings of 2^-24 with the square's own), the rest in 64 bits; the root halves it: under
-2^-18 with the rounding to fp32.  A clipped value is the stored one times a factor known to 2^-18, rounded."""
+Sums and their rounding are exact (fp32 in rank order, one product with the scale).  The norm: at most 64 squares in
+a thread and then 32 threads' sums in five levels are added in fp32 (70 roundings of 2^-24 with the square's own), the
+rest in 64 bits; the root halves that: 35 * 2^-24, under 2^-18 with the rounding to fp32.  A clipped value is the stored one times a factor known to 2^-18, rounded."""
 import math
 
 import pytest
