@@ -103,11 +103,29 @@ __device__ __forceinline__ uint64_t read_policy(bool evict_first) {
   asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
   return evict_first ? first : normal;
 }
+// A pass that stores may store over an input, or over what the first pass
+// stored: its loads are ordinary ones.  Loads of data that the kernel never
+// writes may be called that, which lets them go ahead of anything (a clipped
+// step of W = 1, 152 MB 73.5 us against 74.8; the stores' pass measures the
+// same either way but for W = 4, 8 MB, 9.25 us against 9.02).
+template <bool READ_ONLY>
 __device__ __forceinline__ uint4 ld_hint(const void* p, uint64_t policy) {
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p), "l"(policy));
+  if constexpr (READ_ONLY)
+    asm("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p), "l"(policy));
+  else
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
   return v;
 }
 
@@ -161,7 +179,7 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
     for (int u = 0; u < U; u++) {
       at[u] = (uint32_t)min(v0 + u * kGradThreads, sp.vecs - 1) * 16u;
 #pragma unroll
-      for (int r = 0; r < R; r++) raw[u][r] = ld_hint(x[r] + at[u], policy);
+      for (int r = 0; r < R; r++) raw[u][r] = ld_hint<!STORE>(x[r] + at[u], policy);
     }
     if constexpr (W > 0) {
 #pragma unroll
@@ -173,7 +191,7 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
       for (int r = 1; r < n; r++) {
         const uint8_t* from = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
 #pragma unroll
-        for (int u = 0; u < U; u++) raw[u][0] = ld_hint(from + at[u], policy);
+        for (int u = 0; u < U; u++) raw[u][0] = ld_hint<!STORE>(from + at[u], policy);
 #pragma unroll
         for (int u = 0; u < U; u++) {
           float f[E];
@@ -224,7 +242,7 @@ __device__ __forceinline__ void clip_chunk(const GradChunk& c, const void* from,
   for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
     uint4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; u++) raw[u] = ld_stream(body + min(v0 + u * kGradThreads, sp.vecs - 1));
+    for (int u = 0; u < U; u++) raw[u] = ld_once(body + min(v0 + u * kGradThreads, sp.vecs - 1));
 #pragma unroll
     for (int u = 0; u < U; u++) {
       if (v0 + u * kGradThreads < sp.vecs) {
