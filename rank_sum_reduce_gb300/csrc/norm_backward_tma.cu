@@ -14,11 +14,11 @@
 // row another folds.
 //
 // h stays in registers (packed) from the statistic to the gradient, or, with
-// more than two vectors per thread, in its slot; the dres slice is only waited
-// for after the statistic and is read from its slot there.  The weight row lies in shared memory, the weight gradient of a
-// team's rows in its registers for the whole kernel; the teams' are added in
-// shared memory at the end, one partial per CTA.  Every mbarrier wait is
-// bounded, as in the forward.
+// more than three vectors per thread, in its slot; the dres slice is only
+// waited for after the statistic and is read from its slot there.  The weight
+// row lies in shared memory, the weight gradient of a team's rows in its
+// registers for the whole kernel; the teams' are added in shared memory at the
+// end, one partial per CTA.  Every mbarrier wait is bounded, as in the forward.
 #include "car_launch.h"
 #include "ring.cuh"
 
@@ -34,7 +34,7 @@ struct BackwardTmaParams {
   float* partial;       // [grid, N], or null
   unsigned int* err;
   float eps;
-  float cols;
+  float inv_cols;
   int64_t rows;
   int row_bytes;
   int vec_per_row;
@@ -103,9 +103,37 @@ __device__ __forceinline__ void produce(const BackwardTmaParams& p, uint8_t* rin
   }
 }
 
+// The lower half of the warp adds one sum, the upper half another; both to all
+// lanes: five shuffles where two sums after one another take eight.
+__device__ __forceinline__ float2 half_sums(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  const float other = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  return (threadIdx.x & 16) ? make_float2(other, v) : make_float2(v, other);
+}
+__device__ __forceinline__ float2 warp_sum2(float a, float b) {
+  const bool upper = threadIdx.x & 16;
+  const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
+  return half_sums(__fadd_rn(upper ? b : a, other));
+}
+
+// The weight row lies widened in shared memory where that costs no slots: every
+// vector is used twice, and widening takes eight instructions of the hundred or
+// so that a vector needs, where the instructions are what bounds rows of few
+// ranks (with the sums' shared shuffles W = 1, M = 16389, N = 4096 87.0 -> 82.5
+// us, W = 4, M = 4085, N = 10488 100.5 -> 92.2).  Three vectors per thread gain
+// nothing more by it (W = 3, N = 10000 43.4 / 43.3), four lose (W = 4, N = 14000
+// 138 / 168).
+template <int DT, int VPT>
+constexpr bool kWideWeight = DT != kFP32 && VPT == 2;
+template <int DT, int VPT>
+__device__ __forceinline__ int weight_row_bytes(int row_bytes) {
+  return VPT == 8 ? 0 : kWideWeight<DT, VPT> ? 2 * row_bytes : row_bytes;
+}
+
 // VPT: vectors per consumer thread.  Two for rows of up to 1024 vectors: with
 // one, the fixed work of a row (two sums over the warp, a division, addresses)
-// is done twice as often (W = 1, M = 16389, N = 4096 bf16: 89 against 135 us),
+// is done twice as often (W = 1, M = 16389, N = 4096 bf16: 82 against 135 us),
 // with four the accumulators leave little room to overlap (108) -- unless two
 // would leave a third of the threads without a row (W = 3, M = 4000, N = 5000:
 // 53.9 against 49.4).  Longer rows take four, and fp32 ones eight; the
@@ -144,14 +172,17 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
     if (lane == 0) mbar_arrive(&empty[slot]);
     advance();
   };
-  auto weight = [&](int k) {
-    return VPT == 8 ? __ldg(p.weight + tid + k * T) : lds16(s_weight + 16 * (tid + k * T));
-  };
   auto widen2 = [](uint4 v, float2 (&f)[E / 2]) {
     float t[E];
     Pack<DT>::widen(v, t);
 #pragma unroll
     for (int e = 0; e < E / 2; e++) f[e] = make_float2(t[2 * e], t[2 * e + 1]);
+  };
+  auto weight = [&](int k, float2 (&f)[E / 2]) {
+    const int v = tid + k * T;
+    if constexpr (kWideWeight<DT, VPT>) lds_wide(s_weight, p.vec_per_row, v, f);
+    else if constexpr (VPT < 8) widen2(lds16(s_weight + 16 * v), f);
+    else widen2(__ldg(p.weight + v), f);
   };
   for (int64_t tile = (int64_t)blockIdx.x * p.teams; tile < p.rows; tile += (int64_t)gridDim.x * p.teams) {
     const int64_t row = tile + team;
@@ -194,7 +225,7 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
         if constexpr (!HELD) hv[k] = v;
         float2 hf[E / 2], wf[E / 2];
         widen2(v, hf);
-        widen2(weight(k), wf);
+        weight(k, wf);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) {
           ss = fma2(hf[e], hf[e], ss);
@@ -210,7 +241,7 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
     }
     // row statistics: every warp adds the team's warp partials itself, in the
     // same order; they are double-buffered by row parity
-    float2 sum = make_float2(warp_sum(ss.x + ss.y), warp_sum(c.x + c.y));
+    float2 sum = warp_sum2(ss.x + ss.y, c.x + c.y);
     if (nwarps > 1) {
       float2* sw = s_warp + nwarps * (it & 1u);
       if (lane == 0) {
@@ -221,12 +252,11 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
         failed = true;
         break;
       }
-      sum = lane < nwarps ? sw[lane] : make_float2(0.f, 0.f);
-      sum = make_float2(warp_sum(sum.x), warp_sum(sum.y));
+      sum = half_sums((lane & 15) < nwarps ? reinterpret_cast<const float*>(sw)[2 * (lane & 15) + (lane >> 4)] : 0.f);
     }
     it++;
-    const float rms = rsqrtf(__fdiv_rn(sum.x, p.cols) + p.eps);
-    const float m = __fdiv_rn(__fmul_rn(sum.y, rms), p.cols);
+    const float rms = rsqrtf(fmaf(sum.x, p.inv_cols, p.eps));
+    const float m = __fmul_rn(__fmul_rn(sum.y, p.inv_cols), rms);
     const float2 rms2 = make_float2(rms, rms), m2 = make_float2(-m, -m);
     if (p.dres && !wait_bounded(&full[slot], phase, s_abort)) {
       failed = true;
@@ -238,7 +268,7 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
         float2 hf[E / 2], wf[E / 2], df[E / 2];
         float o[E];
         widen2(HELD ? lds16(mine + hslot * stride + 16 * k * T) : hv[HELD ? 0 : k], hf);
-        widen2(weight(k), wf);
+        weight(k, wf);
         widen2(p.dres ? lds16(mine + slot * stride + 16 * k * T) : make_uint4(0u, 0u, 0u, 0u), df);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) {
@@ -318,7 +348,7 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1) reduce_rmsnorm_backw
   extern __shared__ __align__(1024) uint8_t smem[];
   const int S = p.slots;
   uint8_t* s_weight = smem + (size_t)S * p.teams * p.row_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + (VPT == 8 ? 0 : p.row_bytes));
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_weight + weight_row_bytes<DT, VPT>(p.row_bytes));
   uint64_t* empty = full + S;
   uint64_t* rowbar = empty + S;             // [16], by team
   uint64_t* done = rowbar + 16;             // [2]
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1) reduce_rmsnorm_backw
     if (lane == 0) produce(p, smem, full, empty, s_abort, warp - nwarps);
   } else {
     if constexpr (VPT != 8) {
-      for (int v = threadIdx.x; v < p.vec_per_row; v += consumers) reinterpret_cast<uint4*>(s_weight)[v] = __ldg(p.weight + v);
+      weight_to_shared<DT, kWideWeight<DT, VPT>>(p.weight, p.vec_per_row, consumers, s_weight);
       asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
     }
     consume<DT, VPT>(p, smem, s_weight, full, empty, rowbar, done, s_warp, s_abort);
@@ -372,7 +402,7 @@ BackwardTmaFn pick(int dtype, int vpt) {
   }
 }
 
-constexpr int kRingBudget = 216 * 1024;  // ring and weight row
+constexpr int kRingBudget = 224 * 1024;  // ring and weight row
 
 }  // namespace
 
@@ -387,7 +417,7 @@ bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, i
   const int teams = 512 / out->team_threads;
   out->teams = teams;
   // about one tile's slices in flight, as in the forward, and an even number
-  const int slice = teams * row_bytes, weights = vpt == 8 ? 0 : row_bytes;
+  const int slice = teams * row_bytes, weights = vpt == 8 ? 0 : vpt == 2 && dtype != kFP32 ? 2 * row_bytes : row_bytes;
   int slots = W + 2 < 6 ? 6 : (W + 3) / 2 * 2;
   if (slots > (kRingBudget - weights) / slice) slots = (kRingBudget - weights) / slice;
   if (slots > 4) slots -= slots % kProducers;
@@ -418,7 +448,7 @@ cudaError_t launch_backward_tma(int dtype, int W, const RankPtrs& dy, const void
   p.partial = dweight ? (sh.grid > 1 ? workspace : dweight) : nullptr;
   p.err = err;
   p.eps = eps;
-  p.cols = (float)cols;
+  p.inv_cols = 1.f / (float)cols;
   p.rows = rows;
   p.row_bytes = vec_per_row * 16;
   p.vec_per_row = vec_per_row;

@@ -39,6 +39,31 @@ inline int team_vectors(int vecs, int prefer) {
   return best;
 }
 
+// A row of weights in shared memory, widened (WIDE, 16-bit types): the vectors'
+// halves lie in two planes of float4, so that a warp that takes consecutive
+// vectors reads either without bank conflicts.  By the first `threads` threads.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void weight_to_shared(const uint4* __restrict__ weight, int vecs, int threads, uint8_t* s) {
+  for (int v = threadIdx.x; v < vecs; v += threads) {
+    const uint4 w = __ldg(weight + v);
+    if constexpr (WIDE) {
+      float f[8];
+      Pack<DT>::widen(w, f);
+      reinterpret_cast<float4*>(s)[v] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(s)[vecs + v] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      reinterpret_cast<uint4*>(s)[v] = w;
+    }
+  }
+}
+__device__ __forceinline__ void lds_wide(const uint8_t* s, int vecs, int v, float2 (&f)[4]) {
+  const float4 a = reinterpret_cast<const float4*>(s)[v], b = reinterpret_cast<const float4*>(s)[vecs + v];
+  f[0] = make_float2(a.x, a.y);
+  f[1] = make_float2(a.z, a.w);
+  f[2] = make_float2(b.x, b.y);
+  f[3] = make_float2(b.z, b.w);
+}
+
 // Wait for the barrier phase with the given parity; false when the CTA is
 // aborting or the wait ran past kWaitLimitNs.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const volatile int* abort) {
