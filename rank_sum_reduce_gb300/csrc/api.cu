@@ -237,10 +237,18 @@ bool rows_compiled(int W) { return W <= 2 || W == 4 || W == 8 || W == 16; }
 // When the 8-bit output's pipeline kernel is faster than its row kernel.
 // Measured on GB300 (graph replay over cold inputs, bf16 unless noted, scales
 // of 128 columns, us per call, pipeline / rows).
-//  * One or two ranks: from two tiles per SM on.  W = 1, N = 4096, M = 912 6.9 /
-//    6.8, M = 1216 7.9 / 9.2; W = 2, N = 8192, M = 456 8.9 / 8.1, M = 608 10.2 /
-//    11.1.  Rows of at most 128 vectors (a warp each, no barrier) earlier: N =
-//    1024, W = 1, M = 1456 3.6 / 4.8, W = 2 4.0 / 4.9.
+//  * One or two ranks: once a tile keeps nearly every SM busy.  One scale per
+//    row, W = 1, N = 4096, M = 304 3.4 / 2.5, M = 608 3.6 / 4.2, M = 1000 7.0 /
+//    7.7; N = 5000, M = 304 3.9 / 3.6, M = 608 6.1 / 6.7; N = 2800, M = 1000 5.4
+//    / 6.6.  Eight and more rows a tile only where the last tiles fill the SMs
+//    too: W = 2, N = 2048, M = 1000 4.0 / 4.4, M = 1500 7.0 / 6.5, M = 3000 10.2
+//    / 11.2.  Rows of at most 128 vectors (a warp each, no barrier) from half a
+//    tile per SM: N = 1024, M = 1500, W = 1 3.3 / 4.4, W = 2 3.7 / 4.6.
+//  * Three vectors per thread (rows that two do not fit, and which the row
+//    kernel's threads do not fit either) from one and a half tiles per SM: N =
+//    2800, M = 608, W = 4 4.9 / 4.8, W = 8 8.6 / 6.8, M = 1000 8.4 / 8.9 and 11.5
+//    / 12.6; N = 5000, M = 304 4.5 / 4.9 and 9.1 / 6.9, M = 608 9.5 / 10.0 and
+//    13.4 / 14.9, M = 1500 17.3 / 23.6 and 25.7 / 32.5.
 //  * Four ranks: N = 8192, M = 304 7.5 / 6.8, M = 456 10.0 / 10.7; N = 4096, M =
 //    912 9.8 / 9.4, M = 1216 12.2 / 12.0, M = 2000 17.8 / 18.9; N = 1024, M =
 //    2432 7.3 / 6.9, M = 3648 9.7 / 11.3.
@@ -264,7 +272,11 @@ bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
   if (h->vec_per_row > 2048) return (h->dtype == CAR_FP32 || h->W <= 2) && 2 * tiles >= 3 * sms;
   if (h->vec_per_row > 1024) return 2 * tiles >= 3 * sms;
-  if (h->W <= 2) return tiles >= 2 * sms || (sh.teams >= 16 && 2 * tiles >= sms);
+  if (h->W <= 2) {
+    if (sh.teams >= 16) return 2 * tiles >= sms;
+    return 5 * tiles >= 4 * sms && (sh.teams < 8 || tiles <= sms || tiles >= 2 * sms);
+  }
+  if (sh.vpt == 3) return 2 * tiles >= 3 * sms;
   if (h->vec_per_row > 512) return 2 * h->M >= 5 * sms;
   if (sh.use < 0.8) return false;
   if (h->W == 4) return tiles >= (sh.teams >= 8 ? 3 : 4) * sms;
@@ -275,19 +287,26 @@ bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
 // When the backward's pipeline kernel is faster than its row kernel.  Measured
 // as above, with a weight gradient, pipeline / rows.
 //  * One or two ranks, rows short enough for several teams: W = 1, N = 1024, M
-//    = 640 5.6 / 6.2, M = 3648 10.3 / 11.0; N = 4096, M = 912 10.4 / 11.3, M =
-//    16389 88 / 104.  With one team the row kernel, which holds two rows' loads
-//    in registers there, stays ahead in 16 bits (N = 8192, M = 456 11.4 / 10.3,
-//    M = 2048 28.3 / 28.0) and not in fp32 (N = 4096, M = 1000 14.3 / 16.6).
+//    = 640 5.6 / 6.2, M = 3648 10.3 / 11.0; N = 4096, M = 152 5.7 / 5.9, M = 912
+//    10.2 / 10.9, M = 16389 82 / 104.  Three vectors per thread from five rows
+//    per SM: N = 6144, M = 456 10.2 / 9.1, M = 1200 15.4 / 16.5; W = 2, N = 5000,
+//    M = 608 11.3 / 10.7, M = 1500 18.2 / 20.2; fp32, N = 3000, M = 608 9.6 /
+//    10.5.  With one team the row kernel, which holds two rows' loads in
+//    registers there, keeps up for longer in 16 bits (N = 8192, M = 456 11.5 /
+//    10.2, M = 912 15.6 / 15.7, M = 6000 64.9 / 65.4) than in fp32 (N = 4096, M
+//    = 1000 14.3 / 16.6).
 //  * More ranks pay the ring's start and its issuing threads until a CTA has two
-//    to three tiles: W = 8, N = 4096, M = 400 12.2 / 10.7, M = 912 16.9 / 18.2;
-//    W = 4, N = 8192, M = 200 10.3 / 9.5, M = 456 13.7 / 14.2; W = 8, N = 8192, M
-//    = 304 14.2 / 16.5.
-//  * Rows of more than 1024 vectors, three per thread: W = 1, N = 11072, M = 1737
-//    36 / 42; W = 4, N = 10488, M = 4085 102 / 141; N = 10000, M = 300 13.9 /
-//    14.1; W = 8, M = 200 17.4 / 15.5.  Four: fp32 as three; in 16 bits the
-//    accumulators leave little room, W = 4, M = 4000 N = 14000 137 / 147, N =
-//    16384 153 / 149.  Eight (fp32): N = 12800, W = 1, M = 3000 138 / 153; N =
+//    tiles or three: N = 4096, W = 8, M = 400 12.2 / 10.7, M = 608 13.5 / 13.7,
+//    M = 912 16.8 / 18.3; W = 4, M = 456 10.0 / 9.5, M = 608 10.6 / 11.3; N =
+//    8192, W = 4, M = 304 11.4 / 10.7, M = 456 13.6 / 14.1, W = 8, M = 200 13.1 /
+//    13.2, M = 304 14.3 / 16.6; W = 16, N = 2048, M = 1200 19.3 / 18.9.
+//  * Rows of more than 1024 vectors, three per thread: W = 1, N = 11072, M = 304
+//    12.1 / 10.8, M = 608 16.1 / 17.6, M = 1737 31 / 42; N = 10488, W = 4, M = 200
+//    13.3 / 11.1, M = 304 13.9 / 14.6, M = 608 20 / 26.  Four: fp32 as three; in
+//    16 bits the accumulators leave little room, N = 13000, W = 2, M = 608 23.5 /
+//    21.6, W = 4, M = 608 29.1 / 27.8, M = 2000 73 / 77; N = 14336, W = 1, M =
+//    3000 86 / 75; N = 14000, W = 8, M = 608 40.5 / 44.1; N = 16384, W = 4, M =
+//    4000 180 / 148.  Eight (fp32): N = 12800, W = 1, M = 3000 138 / 153; N =
 //    12000, W = 4, M = 3000 182 / 190; N = 16384, W = 2, M = 2000 127 / 118; N =
 //    11840, W = 8, M = 664 69 / 64.
 //  * Rank counts that the row kernel is not compiled for: W = 3, N = 10000, M =
@@ -296,12 +315,15 @@ bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
 bool backward_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int64_t tiles = (h->M + sh.teams - 1) / sh.teams, sms = h->num_sms;
   const int V = h->vec_per_row;
+  const bool fp32 = h->dtype == CAR_FP32;
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
   if (V > 2048) return V <= 3328 && h->W <= 4 && tiles >= 8 * sms;
-  if (V > 1024) return tiles >= 2 * sms && (h->dtype == CAR_FP32 || V <= 1792);
-  if (h->W <= 2 && sh.teams == 1) return h->dtype == CAR_FP32 && tiles >= 4 * sms;
-  if (h->W <= 2) return 2 * tiles >= sms;
-  return 2 * tiles >= (sh.teams > 1 ? 5 : 4) * sms;
+  if (V > 1536) return fp32 ? tiles >= 2 * sms : V <= 1792 && h->W >= 4 && tiles >= (h->W < 8 ? 6 : 2) * sms;
+  if (V > 1024) return tiles >= (h->W <= 2 ? 3 : 2) * sms;
+  if (h->W <= 2 && sh.teams == 1) return tiles >= (fp32 ? 4 : 6) * sms;
+  if (h->W <= 2) return sh.vpt == 2 ? 2 * tiles >= sms : h->M >= 5 * sms;
+  if (sh.teams == 1) return tiles >= (h->W < 8 ? 3 : 2) * sms;
+  return 2 * tiles >= (h->W > 8 ? 5 : 4) * sms;
 }
 
 car_status finish_fused_shape(car_ctx* h, car::FusedShape sh) {

@@ -132,12 +132,14 @@ __device__ __forceinline__ int weight_row_bytes(int row_bytes) {
 }
 
 // VPT: vectors per consumer thread.  Two for rows of up to 1024 vectors: with
-// one, the fixed work of a row (two sums over the warp, a division, addresses)
-// is done twice as often (W = 1, M = 16389, N = 4096 bf16: 82 against 135 us),
-// with four the accumulators leave little room to overlap (108) -- unless two
-// would leave a third of the threads without a row (W = 3, M = 4000, N = 5000:
-// 53.9 against 49.4).  Longer rows take four, and fp32 ones eight; the
-// accumulators of eight 16-bit vectors would not fit in registers.
+// one, the fixed work of a row (two sums over the warp, a barrier, addresses)
+// is done twice as often (W = 1, M = 16389, N = 4096 bf16: 82 against 135 us).
+// Three for longer rows, and where two would leave a third of the threads
+// without a row (W = 8, M = 1500, N = 4400: 27.4 against 34.4; N = 7000, where
+// two fit better, 43.0 against 39.6).  Four only for rows that three do not
+// hold: in 16 bits the accumulators leave little room to overlap (N = 4400:
+// 36.3).  Eight above that, in fp32 alone: eight 16-bit vectors' accumulators
+// would not fit in registers.
 template <int DT, int VPT>
 __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* ring, const uint8_t* s_weight, uint64_t* full,
                                         uint64_t* empty, uint64_t* rowbar, uint64_t* done, float2* s_warp,
@@ -408,7 +410,7 @@ constexpr int kRingBudget = 224 * 1024;  // ring and weight row
 
 bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, 2);
+  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
   if (vpt == 8 && dtype != kFP32) return false;
   out->vpt = vpt;
   out->use = team_use(vec_per_row, vpt);

@@ -16,8 +16,9 @@
 // = 8192: 26.5 -> 23.9); with more the row waits for its slices and two are (W
 // = 8, M = 512, N = 8192: 15.9 against 16.9; W = 4, M = 2000, N = 4096 17.8
 // with six slots against 19.0 with four), unless they leave threads without a
-// row (W = 4, M = 8191, N = 6144: 112 against 95).  Rows of more than 2048
-// vectors take eight, the weight read from L2 once per row (64 KB of it beside
+// row, which three do not (W = 4, M = 8191, N = 6144: 112 against 95; W = 8, M =
+// 1500, N = 5000 31.7 against 25.7, four 27.5).  Rows of more than 2048 vectors
+// take eight, the weight read from L2 once per row (64 KB of it beside
 // the ring would leave two slots).
 #include "car_launch.h"
 #include "quant.cuh"
@@ -314,7 +315,7 @@ constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 bool quant_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, W <= 3 ? 4 : 2);
+  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, W <= 3 ? 4 : 2, W <= 3 || vec_per_row > 1536 ? 4 : 3);
   out->vpt = vpt;
   out->use = team_use(vec_per_row, vpt);
   out->team_threads = team_threads(vec_per_row, vpt);

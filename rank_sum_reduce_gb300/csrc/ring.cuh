@@ -20,17 +20,17 @@ constexpr int kProducers = 2;
 
 // 16-byte vectors per consumer thread for rows of `vecs` vectors (at most
 // 2048), where a CTA's 512 threads are cut into teams of whole warps, one row
-// each: the preferred number, unless another of 2, 3 and 4 leaves clearly
+// each: the preferred number, unless another of 2 to `most` leaves clearly
 // fewer of the threads' places empty (by a tenth).
 inline int team_threads(int vecs, int vpt) { return ((vecs + vpt - 1) / vpt + 31) / 32 * 32; }
 inline double team_use(int vecs, int vpt) {
   const int t = team_threads(vecs, vpt);
   return t > 512 ? 0.0 : (double)(512 / t) * vecs / (512.0 * vpt);
 }
-inline int team_vectors(int vecs, int prefer) {
+inline int team_vectors(int vecs, int prefer, int most) {
   int best = prefer;
   double use = team_use(vecs, prefer) + 0.1;
-  for (int vpt = 2; vpt <= 4; vpt++) {
+  for (int vpt = 2; vpt <= most; vpt++) {
     if (team_use(vecs, vpt) > use) {
       best = vpt;
       use = team_use(vecs, vpt);
