@@ -109,7 +109,10 @@ def _packer(n: int):
 
 def _table(ptrs):
     """Host array of device pointers, as bytes (a call reads it before it returns)."""
-    return _packer(len(ptrs))(*ptrs)
+    try:
+        return _packer(len(ptrs))(*ptrs)
+    except struct.error:  # not plain ints in range: as ctypes takes them
+        return bytes((ctypes.c_void_p * len(ptrs))(*[int(p) for p in ptrs]))
 
 
 # ---------------------------------------------------------------------------

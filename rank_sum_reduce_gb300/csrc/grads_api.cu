@@ -94,6 +94,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
     const int es = dtypes[t] == CAR_FP32 ? 4 : 2;
     bytes[t] = numel[t] * es;
     vecs += bytes[t] / 16 + 1;
+    if (vecs / car::kGradThreads > ((int64_t)1 << 30)) return CAR_ERR_SIZE;  // here, before a sum of many wraps
     if (!bytes[t]) continue;
     if (!outs[t] || reinterpret_cast<uintptr_t>(outs[t]) % es) return outs[t] ? CAR_ERR_ALIGN : CAR_ERR_ARG;
     for (int r = 0; r < W; r++) {
@@ -101,7 +102,6 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
       if (!p || reinterpret_cast<uintptr_t>(p) % es) return p ? CAR_ERR_ALIGN : CAR_ERR_ARG;
     }
   }
-  if (vecs / car::kGradThreads > ((int64_t)1 << 30)) return CAR_ERR_SIZE;
   car_status st = check_overlap(W, n, bytes, inputs, outs);
   if (st != CAR_OK) return st;
 

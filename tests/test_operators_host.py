@@ -24,6 +24,23 @@ def test_calls_on_bad_handles(car):
     assert car.car_grads_reduce_clip(bogus, 1.0, 1.0, None) == car.CAR_ERR_HANDLE
 
 
+def test_pointer_tables_take_what_ctypes_takes(car):
+    """Addresses of any integer type, wrapped into 64 bits; nothing else."""
+    import numpy as np
+
+    assert car.car_reduce(0x1000, [np.uint64(16), -16, 2**64 + 16, 16.0], 16) == car.CAR_ERR_HANDLE
+    with pytest.raises(TypeError):
+        car.car_reduce(0x1000, [16, None], 16)
+
+
+def test_grads_create_refuses_a_total_past_64_bits(car):
+    """2^18 tensors of 2^48 fp32 values: 2^64 vectors of 16 bytes, which must not wrap to a small number."""
+    n = 2**18
+    outs = [(t + 1) << 40 for t in range(n)]
+    st, h = car.car_grads_create(1, [2**48] * n, [2] * n, outs, outs)
+    assert st == car.CAR_ERR_SIZE and h is None
+
+
 BF16, FP32 = 0, 2
 A, B, C = 0x10000, 0x20000, 0x30000
 
