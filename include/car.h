@@ -169,7 +169,7 @@ car_status car_reduce_residual_rmsnorm(car_ctx* h, const void* const* inputs, co
  *       row, group128: max(amax / 448, 2^-126), amax = max |y| of the group
  *       mx32: 2^k, the smallest power of two >= amax / 448, k >= -126, stored
  *             as the byte k + 127
- *       static: read from scales[0] (finite, > 0)
+ *       static: read from scales[0] (finite, >= 2^-126)
  *   q_out[m,j] = e4m3_rne( saturate( y / s ) )           (y * (1/s) in fp32)
  * so that q * s stands for y.  The last group of a row may be short.  amax is
  * rms * max |t|, so a scale costs no pass of its own.  A group with a value

@@ -139,14 +139,14 @@ struct GradPlan {
   bool evict_first;       // the ranks' values give way to the outputs in L2
   bool pass_on;           // so do the clip's outputs, to what it has yet to read
   double* partial;        // [grid]
-  double* sumsq;          // the handle's own
   unsigned int* arrived;  // CTAs of the reduce that have written their partial
 };
 cudaError_t grads_occupancy(int W, int* reduce_per_sm, int* clip_per_sm);
-// store: write the sums (always with W > 1); without, launch_grads_clip takes the values from_input.
+// store: write the sums (always with W > 1); without, launch_grads_clip takes the values from_input.  sumsq may be
+// null; launch_grads_clip then adds plan.partial[0 .. reduce's grid - 1] (sums, n_sums).
 cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s);
-cudaError_t launch_grads_clip(const GradPlan& plan, const double* sumsq, float scale, bool from_input, float max_norm,
-                              float* norm_out, int grid, cudaStream_t s);
+cudaError_t launch_grads_clip(const GradPlan& plan, const double* sums, int n_sums, float scale, bool from_input,
+                              float max_norm, float* norm_out, int grid, cudaStream_t s);
 
 // ---- LL128 (ll128.cu) ----
 constexpr int kWireThreads = 256;

@@ -29,9 +29,12 @@
 // first descriptor, and a prefetch of the first 8 KB per rank into L2, come
 // before the PDL wait (W = 4, 8 MB: 11.0 -> 9.3 us).  Squares are summed in
 // fp32 over a thread's part of one chunk (kGradChunkVecs / kGradThreads = 8
-// vectors, 64 values) and over its warp, and in 64 bits from there on; the
-// CTAs' partials are added by the last CTA to arrive, in the order of their
-// index, so the same call gives the same bits.  Roofline: HBM, (W + 1) * 16
+// vectors, 64 values) and over its warp, and in 64 bits from there on.  The
+// CTAs' partials are added in the order of their index, so the same call gives
+// the same bits: by the last CTA to arrive where the caller wants the sum, and
+// by every CTA of the second pass where that follows (car_grads_reduce_clip):
+// the fence, the arrival and the partials' loads leave the tail of the first
+// pass (W = 2, 0.2 MB, clipped 6.3 -> 4.7 us; W = 4, 8 MB 13.7 -> 11.5).  Roofline: HBM, (W + 1) * 16
 // bytes per vector: 531 us for W = 8, 400 MB (1.00 of the copy peak).
 #include <stdint.h>
 
@@ -82,6 +85,36 @@ __device__ __forceinline__ double block_sum(double v, double* s_warp) {
     for (int w = 0; w < kGradThreads / 32; w++) v += s_warp[w];
   }
   return v;
+}
+// Sum of n values by the whole block, in every lane of its first warp: in the
+// same order wherever it is taken, with few additions after one another.
+__device__ __forceinline__ double sum_values(const double* __restrict__ v, int n, double* s_sum) {
+  double a = 0.0;
+  const int i0 = threadIdx.x;
+  if (i0 < n) a = __ldcg(v + i0);
+#pragma unroll 1
+  for (int i = i0 + kGradThreads; i < n; i += kGradThreads) a += __ldcg(v + i);
+  if (n <= 32) {
+    if (threadIdx.x >= 32) return 0.0;
+  } else {
+    s_sum[threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0.0;
+    double t[kGradThreads / 32];
+#pragma unroll
+    for (int w = 0; w < kGradThreads / 32; w++) t[w] = s_sum[threadIdx.x + 32 * w];
+#pragma unroll
+    for (int o = kGradThreads / 64; o > 0; o >>= 1) {
+#pragma unroll
+      for (int w = 0; w < o; w++) t[w] += t[w + o];
+    }
+    a = t[0];
+  }
+  if (n > 1) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  }
+  return a;
 }
 // sqrt(sumsq) in fp32, over the whole range of a sum of fp32 squares.
 __device__ __forceinline__ float norm_of(double sumsq) {
@@ -281,6 +314,7 @@ template <int W, bool STORE>
 __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
     grads_reduce_kernel(const GradPlan p, const float scale, double* __restrict__ sumsq) {
   __shared__ double s_warp[kGradThreads / 32];
+  __shared__ double s_sum[kGradThreads];
   __shared__ bool s_last;
   const int n = W > 0 ? W : p.W;
   const uint64_t policy = read_policy(STORE && p.evict_first);
@@ -310,6 +344,10 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
     if ((threadIdx.x & 31) == 0) total += (double)ss;
   }
   total = block_sum(total, s_warp);
+  if (!sumsq) {  // the second pass adds the partials
+    if (threadIdx.x == 0) p.partial[blockIdx.x] = total;
+    return;
+  }
   if (threadIdx.x == 0) {
     p.partial[blockIdx.x] = total;
     __threadfence();
@@ -318,11 +356,7 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
   __syncthreads();
   if (s_last) {
     __threadfence();
-    total = 0.0;
-    for (unsigned i = threadIdx.x; i < gridDim.x; i += kGradThreads) total += __ldcg(p.partial + i);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    total = block_sum(total, s_warp);
+    total = sum_values(p.partial, gridDim.x, s_sum);
     if (threadIdx.x == 0) {
       *sumsq = total;
       *p.arrived = 0u;  // for the next call, which waits for this grid
@@ -334,8 +368,10 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
 // stored nothing.
 template <bool FROM_INPUT>
 __global__ void __launch_bounds__(kGradThreads)
-    grads_clip_kernel(const GradPlan p, const double* __restrict__ sumsq, const float scale, const float max_norm,
-                      float* __restrict__ norm_out) {
+    grads_clip_kernel(const GradPlan p, const double* __restrict__ sums, const int n_sums, const float scale,
+                      const float max_norm, float* __restrict__ norm_out) {
+  __shared__ double s_sum[kGradThreads];
+  __shared__ float s_norm;
   const uint64_t policy = read_policy(p.pass_on);
   const int stride = (int)sizeof(GradChunk) + 8 * p.W;
   int i = p.clip.n - 1 - (int)blockIdx.x;
@@ -351,7 +387,10 @@ __global__ void __launch_bounds__(kGradThreads)
   // grid, and is only launched once every CTA here is resident.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float norm = norm_of(__ldcg(sumsq));
+  const double sumsq = sum_values(sums, n_sums, s_sum);
+  if (threadIdx.x == 0) s_norm = norm_of(sumsq);
+  __syncthreads();
+  const float norm = s_norm;
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float ratio = __fdiv_rn(max_norm, norm + 1e-6f);
   // within the limit, or no limit (false for a NaN norm, which then reaches every value)
@@ -406,10 +445,10 @@ cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, d
   return launch_pdl(fn, (unsigned)grid, kGradThreads, 0, s, 1, plan, scale, sumsq);
 }
 
-cudaError_t launch_grads_clip(const GradPlan& plan, const double* sumsq, float scale, bool from_input, float max_norm,
-                              float* norm_out, int grid, cudaStream_t s) {
+cudaError_t launch_grads_clip(const GradPlan& plan, const double* sums, int n_sums, float scale, bool from_input,
+                              float max_norm, float* norm_out, int grid, cudaStream_t s) {
   return launch_pdl(from_input ? grads_clip_kernel<true> : grads_clip_kernel<false>, (unsigned)grid, kGradThreads, 0, s, 1,
-                    plan, sumsq, scale, max_norm, norm_out);
+                    plan, sums, n_sums, scale, max_norm, norm_out);
 }
 
 }  // namespace car

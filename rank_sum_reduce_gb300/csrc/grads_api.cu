@@ -19,7 +19,7 @@
 struct car_grads {
   int device;
   int grid, clip_grid;
-  void* memory;  // one allocation: chunks, partials, sum, counter
+  void* memory;  // one allocation: chunks, partials, counter
   car::GradPlan plan;
 };
 
@@ -155,11 +155,11 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   const int clip_grid = (int)std::max<int64_t>(1, std::min(n_clip, clip_cap));
   const size_t cb = chunks.size(), pb = (size_t)grid * sizeof(double);
   void* memory = nullptr;
-  e = cudaMalloc(&memory, cb + pb + 16);
+  e = cudaMalloc(&memory, cb + pb + 8);
   if (e != cudaSuccess) return fail(e, "cudaMalloc gradient plan");
   uint8_t* m = static_cast<uint8_t*>(memory);
   if (cb) e = cudaMemcpy(m, chunks.data(), cb, cudaMemcpyHostToDevice);
-  if (e == cudaSuccess) e = cudaMemset(m + cb, 0, pb + 16);
+  if (e == cudaSuccess) e = cudaMemset(m + cb, 0, pb + 8);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the plan is in place for calls on any stream
   car_grads* g = e == cudaSuccess ? new (std::nothrow) car_grads() : nullptr;
   if (!g) {
@@ -176,8 +176,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   g->plan.evict_first = 16 * vecs < 2 * (int64_t)l2;
   g->plan.pass_on = 16 * vecs > (int64_t)l2 / 4;
   g->plan.partial = reinterpret_cast<double*>(m + cb);
-  g->plan.sumsq = reinterpret_cast<double*>(m + cb + pb);
-  g->plan.arrived = reinterpret_cast<unsigned int*>(m + cb + pb + 8);
+  g->plan.arrived = reinterpret_cast<unsigned int*>(m + cb + pb);
   {
     std::lock_guard<std::mutex> lk(g_mu);
     g_live.insert(g);
@@ -228,7 +227,7 @@ car_status car_grads_clip(car_grads* g, const double* sumsq, float max_norm, flo
   if (st != CAR_OK) return st;
   if (!sumsq || !(max_norm >= 0.f)) return CAR_ERR_ARG;
   if (!aligned(sumsq, 8) || !aligned(norm_out, 4)) return CAR_ERR_ALIGN;
-  cudaError_t e = car::launch_grads_clip(g->plan, sumsq, 1.f, false, max_norm, norm_out, g->clip_grid,
+  cudaError_t e = car::launch_grads_clip(g->plan, sumsq, 1, 1.f, false, max_norm, norm_out, g->clip_grid,
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_clip launch");
 }
@@ -240,9 +239,9 @@ car_status car_grads_reduce_clip(car_grads* g, float scale, float max_norm, floa
   if (!aligned(norm_out, 4)) return CAR_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool one = g->plan.W == 1;  // the first pass then only reads (see grads.cu)
-  cudaError_t e = car::launch_grads_reduce(g->plan, scale, !one, g->plan.sumsq, g->grid, s);
+  cudaError_t e = car::launch_grads_reduce(g->plan, scale, !one, nullptr, g->grid, s);
   if (e == cudaSuccess)
-    e = car::launch_grads_clip(g->plan, g->plan.sumsq, one ? scale : 1.f, one, max_norm, norm_out, g->clip_grid, s);
+    e = car::launch_grads_clip(g->plan, g->plan.partial, g->grid, one ? scale : 1.f, one, max_norm, norm_out, g->clip_grid, s);
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_reduce_clip launch");
 }
 

@@ -8,8 +8,9 @@
 // exchange of their own.
 //
 // Rounding: s is stored in fp32 or as a power of two; t * (rms * (1 / s)) is
-// formed in fp32 (a few roundings of 2^-24 before the one of 2^-4 to e4m3).  The largest |y| of a group lands on 448, or below it for a
-// power-of-two s; the conversion saturates.
+// formed in fp32 (a few roundings of 2^-24 before the one of 2^-4 to e4m3).
+// The largest |y| of a group lands on 448, or below it for a power-of-two s;
+// the conversion saturates.
 #pragma once
 
 #include <cuda_fp8.h>
