@@ -542,7 +542,7 @@ class Grads:
         self.inputs, self.outs, self.h = [list(ts) for ts in inputs], list(outs), None
         if not self.inputs or not self.outs:
             raise ValueError("inputs, outs: need at least one rank and one tensor")
-        self.device = self.outs[0].device.index
+        self.device, self._f32, self._f64 = self.outs[0].device.index, torch.float32, torch.float64
         for t, o in enumerate(self.outs):
             if o.dtype not in code:
                 raise ValueError(f"outs[{t}]: {o.dtype} is not bf16, fp16 or fp32")
@@ -580,24 +580,24 @@ class Grads:
         except Exception:
             pass
 
-    def _scalar(self, t, nbytes: int, what: str, dtype: str) -> int:
-        if str(t.dtype) != "torch." + dtype:
+    def _scalar(self, t, nbytes: int, what: str, dtype) -> int:
+        if t.dtype != dtype:
             raise ValueError(f"{what}: {t.dtype}, the call needs {dtype}")
         return _ptr(t, nbytes, what, self.device)
 
     def reduce(self, scale, sumsq, stream=None):
         """outs = scale * rank sums; sumsq (float64, one element) = the sum of their squares."""
-        check(car_grads_reduce(self.h, scale, self._scalar(sumsq, 8, "sumsq", "float64"), _stream(stream)),
+        check(car_grads_reduce(self.h, scale, self._scalar(sumsq, 8, "sumsq", self._f64), _stream(stream, self.device)),
               "car_grads_reduce")
 
     def clip(self, sumsq, max_norm, norm_out=None, stream=None):
         """outs *= min(1, max_norm / (sqrt(sumsq) + 1e-6)); norm_out (float32, one element) = sqrt(sumsq)."""
-        check(car_grads_clip(self.h, self._scalar(sumsq, 8, "sumsq", "float64"), max_norm,
-                             self._scalar(norm_out, 4, "norm_out", "float32") if norm_out is not None else None,
-                             _stream(stream)), "car_grads_clip")
+        check(car_grads_clip(self.h, self._scalar(sumsq, 8, "sumsq", self._f64), max_norm,
+                             self._scalar(norm_out, 4, "norm_out", self._f32) if norm_out is not None else None,
+                             _stream(stream, self.device)), "car_grads_clip")
 
     def reduce_clip(self, scale, max_norm, norm_out=None, stream=None):
         """Both, for gradients that are all in this object."""
         check(car_grads_reduce_clip(self.h, scale, max_norm,
-                                    self._scalar(norm_out, 4, "norm_out", "float32") if norm_out is not None else None,
-                                    _stream(stream)), "car_grads_reduce_clip")
+                                    self._scalar(norm_out, 4, "norm_out", self._f32) if norm_out is not None else None,
+                                    _stream(stream, self.device)), "car_grads_reduce_clip")

@@ -34,8 +34,9 @@
 // the same bits: by the last CTA to arrive where the caller wants the sum, and
 // by every CTA of the second pass where that follows (car_grads_reduce_clip):
 // the fence, the arrival and the partials' loads leave the tail of the first
-// pass (W = 2, 0.2 MB, clipped 6.3 -> 4.7 us; W = 4, 8 MB 13.7 -> 11.5).  Roofline: HBM, (W + 1) * 16
-// bytes per vector: 531 us for W = 8, 400 MB (1.00 of the copy peak).
+// pass (W = 2, 0.2 MB, clipped 6.3 -> 4.7 us; W = 4, 8 MB 13.7 -> 11.5).
+// Roofline: HBM, (W + 1) * 16 bytes per vector: 516 to 522 us for W = 8, 400 MB
+// (1.02 of the copy peak).
 #include <stdint.h>
 
 #include "car_device.cuh"
