@@ -129,6 +129,7 @@ struct GradChunk {
   int16_t dtype;
   int16_t head;  // elements before the first 16-byte boundary that all pointers share; -1: they share none
 };
+constexpr int kMaxGradCtas = 5 * kGradThreads;  // of the first pass: 8 on each of 152 SMs fit
 struct GradList {
   const uint8_t* chunks;  // descriptors of sizeof(GradChunk) + 8 W bytes
   int n;
@@ -141,7 +142,7 @@ struct GradPlan {
   double* partial;        // [grid]
   unsigned int* arrived;  // CTAs of the reduce that have written their partial
 };
-cudaError_t grads_occupancy(int W, int* reduce_per_sm, int* clip_per_sm);
+cudaError_t grads_occupancy(int W, bool store, int* reduce_per_sm, int* clip_per_sm);
 // store: write the sums (always with W > 1); without, launch_grads_clip takes the values from_input.  sumsq may be
 // null; launch_grads_clip then adds plan.partial[0 .. reduce's grid - 1] (sums, n_sums).
 cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s);

@@ -30,8 +30,8 @@
 // before the PDL wait (W = 4, 8 MB: 11.0 -> 9.3 us).  Squares are summed in
 // fp32 over a thread's part of one chunk (kGradChunkVecs / kGradThreads = 8
 // vectors, 64 values) and over its warp, and in 64 bits from there on.  The
-// CTAs' partials are added in the order of their index, so the same call gives
-// the same bits: by the last CTA to arrive where the caller wants the sum, and
+// CTAs' partials are added the same in any order, so the same call gives the
+// same bits: by the last CTA to arrive where the caller wants the sum, and
 // by every CTA of the second pass where that follows (car_grads_reduce_clip):
 // the fence, the arrival and the partials' loads leave the tail of the first
 // pass (W = 2, 0.2 MB, clipped 6.3 -> 4.7 us; W = 4, 8 MB 13.7 -> 11.5).
@@ -66,10 +66,12 @@ struct Scalar<kFP32> {
   __device__ __forceinline__ static T down(float v) { return v; }
 };
 
-// 64-bit arithmetic is scarce on this part (about two operations a clock per
-// SM): each warp adds one 64-bit term per chunk, the block sum is one thread's
-// eight additions, and the square root and the quotient are fp32.  With every
-// thread doing these in 64 bits a clip that had nothing to do took 12 us.
+// 64-bit floating point is scarce on this part (a warp's addition takes some
+// tens of cycles of the one unit of an SM): a warp adds one such term per
+// chunk, eight warps' sums are three additions of one warp, the partials' sum
+// is integer arithmetic, and the square root and the quotient are fp32.  With
+// every thread taking root and quotient in 64 bits a clip that had nothing to
+// do took 12 us.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -77,57 +79,87 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 // Sum over the block of a value that lane 0 of each warp holds; in thread 0.
 __device__ __forceinline__ double block_sum(double v, double* s_warp) {
-  __syncthreads();
+  constexpr int N = kGradThreads / 32;
   if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 32) {
+    v = s_warp[threadIdx.x % N];
 #pragma unroll
-    for (int w = 0; w < kGradThreads / 32; w++) v += s_warp[w];
+    for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
   return v;
 }
-// Sum of n values by the whole block, in every lane of its first warp: in the
-// same order wherever it is taken, with few additions after one another.
-__device__ __forceinline__ double sum_values(const double* __restrict__ v, int n, double* s_sum) {
-  double a = 0.0;
-  const int i0 = threadIdx.x;
-  if (i0 < n) a = __ldcg(v + i0);
-#pragma unroll 1
-  for (int i = i0 + kGradThreads; i < n; i += kGradThreads) a += __ldcg(v + i);
-  if (n <= 32) {
-    if (threadIdx.x >= 32) return 0.0;
-  } else {
-    s_sum[threadIdx.x] = a;
-    __syncthreads();
-    if (threadIdx.x >= 32) return 0.0;
-    double t[kGradThreads / 32];
+
+// Sum of n <= kMaxGradCtas values >= 0 by the whole block, in every thread:
+// mantissa * 2^exponent, or not finite.  The mantissas (53 bits) are shifted
+// to the largest exponent and added as integers: at most 2^11 of them, each
+// cut by less than one unit of the last place of the largest, so that the sum
+// is within 2^-41 of the exact one, and in any order the same.
+struct Total {
+  uint64_t mantissa;  // not finite: 0 for infinity, else NaN
+  int exponent;
+  bool finite;
+};
+struct TotalShared {
+  uint32_t top[kGradThreads / 32], part[3][kGradThreads / 32];
+};
+__device__ __forceinline__ Total sum_values(const double* __restrict__ v, int n, TotalShared& s) {
+  constexpr int K = kMaxGradCtas / kGradThreads, N = kGradThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t b[K];
+  uint32_t top = 0u;  // exponent field; above 2047 for what is negative
 #pragma unroll
-    for (int w = 0; w < kGradThreads / 32; w++) t[w] = s_sum[threadIdx.x + 32 * w];
+  for (int k = 0; k < K; k++) {
+    const int i = threadIdx.x + k * kGradThreads;
+    b[k] = i < n ? (uint64_t)__double_as_longlong(__ldcg(v + i)) : 0u;
+    if (b[k] << 1 == 0u) b[k] = 0u;  // -0
+    top = max(top, (uint32_t)(b[k] >> 52));
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (lane == 0) s.top[warp] = top;
+  __syncthreads();
 #pragma unroll
-    for (int o = kGradThreads / 64; o > 0; o >>= 1) {
+  for (int w = 0; w < N; w++) top = max(top, s.top[w]);
+  const bool finite = top < 2047u;
+  uint64_t sum = 0u;
 #pragma unroll
-      for (int w = 0; w < o; w++) t[w] += t[w + o];
+  for (int k = 0; k < K; k++) {
+    const uint32_t e = (uint32_t)(b[k] >> 52);
+    const uint64_t fraction = b[k] & ((1ull << 52) - 1u);
+    const uint64_t m = e > 0u ? fraction | (1ull << 52) : fraction << 1;  // m * 2^(e - 1075)
+    if (finite) {
+      sum += top - e < 64u ? m >> (top - e) : 0u;
+    } else if (e > 2047u || (e == 2047u && fraction != 0u)) {
+      sum = 1u;  // a NaN, or the root of what is negative
     }
-    a = t[0];
   }
-  if (n > 1) {
+  const uint32_t p0 = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)sum & 0xFFFFFFu);
+  const uint32_t p1 = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)(sum >> 24) & 0xFFFFFFu);
+  const uint32_t p2 = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)(sum >> 48));
+  if (lane == 0) {
+    s.part[0][warp] = p0;
+    s.part[1][warp] = p1;
+    s.part[2][warp] = p2;
+  }
+  __syncthreads();
+  uint32_t t0 = 0u, t1 = 0u, t2 = 0u;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  for (int w = 0; w < N; w++) {
+    t0 += s.part[0][w];
+    t1 += s.part[1][w];
+    t2 += s.part[2][w];
   }
-  return a;
+  return Total{(uint64_t)t0 + ((uint64_t)t1 << 24) + ((uint64_t)t2 << 48), (int)top - 1075, finite};
 }
-// sqrt(sumsq) in fp32, over the whole range of a sum of fp32 squares.
-__device__ __forceinline__ float norm_of(double sumsq) {
-  float post = 1.f;
-  if (sumsq > 0x1p+100) {
-    sumsq *= 0x1p-120;
-    post = 0x1p+60f;
-  } else if (sumsq < 0x1p-100) {
-    sumsq *= 0x1p+120;
-    post = 0x1p-60f;
-  }
-  return __fmul_rn(sqrtf((float)sumsq), post);
+__device__ __forceinline__ double to_double(const Total& t) {
+  if (!t.finite) return t.mantissa ? nan("") : (double)INFINITY;
+  return scalbn((double)t.mantissa, t.exponent);
+}
+// Its square root in fp32.
+__device__ __forceinline__ float root(const Total& t) {
+  if (!t.finite) return t.mantissa ? nanf("") : INFINITY;
+  const int odd = t.exponent & 1;
+  return scalbnf(sqrtf(__fmul_rn((float)t.mantissa, odd ? 2.f : 1.f)), (t.exponent - odd) / 2);
 }
 
 // L2 priority of values that are read once: first to be evicted, or as any.
@@ -146,9 +178,9 @@ template <bool READ_ONLY>
 __device__ __forceinline__ uint4 ld_hint(const void* p, uint64_t policy) {
   uint4 v;
   if constexpr (READ_ONLY)
-    asm("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
-        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-        : "l"(p), "l"(policy));
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
   else
     asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -315,7 +347,7 @@ template <int W, bool STORE>
 __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
     grads_reduce_kernel(const GradPlan p, const float scale, double* __restrict__ sumsq) {
   __shared__ double s_warp[kGradThreads / 32];
-  __shared__ double s_sum[kGradThreads];
+  __shared__ TotalShared s_total;
   __shared__ bool s_last;
   const int n = W > 0 ? W : p.W;
   const uint64_t policy = read_policy(STORE && p.evict_first);
@@ -357,9 +389,9 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
   __syncthreads();
   if (s_last) {
     __threadfence();
-    total = sum_values(p.partial, gridDim.x, s_sum);
+    const Total t = sum_values(p.partial, gridDim.x, s_total);
     if (threadIdx.x == 0) {
-      *sumsq = total;
+      *sumsq = to_double(t);
       *p.arrived = 0u;  // for the next call, which waits for this grid
     }
   }
@@ -371,8 +403,7 @@ template <bool FROM_INPUT>
 __global__ void __launch_bounds__(kGradThreads)
     grads_clip_kernel(const GradPlan p, const double* __restrict__ sums, const int n_sums, const float scale,
                       const float max_norm, float* __restrict__ norm_out) {
-  __shared__ double s_sum[kGradThreads];
-  __shared__ float s_norm;
+  __shared__ TotalShared s_total;
   const uint64_t policy = read_policy(p.pass_on);
   const int stride = (int)sizeof(GradChunk) + 8 * p.W;
   int i = p.clip.n - 1 - (int)blockIdx.x;
@@ -388,10 +419,7 @@ __global__ void __launch_bounds__(kGradThreads)
   // grid, and is only launched once every CTA here is resident.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const double sumsq = sum_values(sums, n_sums, s_sum);
-  if (threadIdx.x == 0) s_norm = norm_of(sumsq);
-  __syncthreads();
-  const float norm = s_norm;
+  const float norm = root(sum_values(sums, n_sums, s_total));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float ratio = __fdiv_rn(max_norm, norm + 1e-6f);
   // within the limit, or no limit (false for a NaN norm, which then reaches every value)
@@ -432,12 +460,12 @@ GradsFn pick_grads(int W, bool store) {
 
 }  // namespace
 
-cudaError_t grads_occupancy(int W, int* reduce_per_sm, int* clip_per_sm) {
+cudaError_t grads_occupancy(int W, bool store, int* reduce_per_sm, int* clip_per_sm) {
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      reduce_per_sm, reinterpret_cast<const void*>(pick_grads(W, true)), kGradThreads, 0);
+      reduce_per_sm, reinterpret_cast<const void*>(pick_grads(W, store)), kGradThreads, 0);
   if (e != cudaSuccess) return e;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      clip_per_sm, reinterpret_cast<const void*>(W == 1 ? grads_clip_kernel<true> : grads_clip_kernel<false>), kGradThreads, 0);
+      clip_per_sm, reinterpret_cast<const void*>(store ? grads_clip_kernel<false> : grads_clip_kernel<true>), kGradThreads, 0);
 }
 
 cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s) {

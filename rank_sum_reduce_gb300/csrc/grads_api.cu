@@ -18,7 +18,8 @@
 
 struct car_grads {
   int device;
-  int grid, clip_grid;
+  int grid, clip_grid;  // of car_grads_reduce_clip's two passes
+  int store_grid;       // of car_grads_reduce: with one rank another kernel than the first pass's
   void* memory;  // one allocation: chunks, partials, counter
   car::GradPlan plan;
 };
@@ -105,13 +106,14 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   car_status st = check_overlap(W, n, bytes, inputs, outs);
   if (st != CAR_OK) return st;
 
-  int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_clip = 0;
+  int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_clip = 0, per_store = 0, unused = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, device);
-  if (e == cudaSuccess) e = car::grads_occupancy(W, &per_reduce, &per_clip);
+  if (e == cudaSuccess) e = car::grads_occupancy(W, W > 1, &per_reduce, &per_clip);
+  if (e == cudaSuccess) e = car::grads_occupancy(W, true, &per_store, &unused);
   if (e != cudaSuccess) return fail(e, "gradient launch sizes");
-  const int64_t reduce_cap = (int64_t)std::max(1, per_reduce) * num_sms, clip_cap = (int64_t)std::max(1, per_clip) * num_sms;
+  const int64_t reduce_cap = std::min<int64_t>((int64_t)std::max(1, per_reduce) * num_sms, car::kMaxGradCtas), clip_cap = (int64_t)std::max(1, per_clip) * num_sms;
   const size_t stride = sizeof(car::GradChunk) + (size_t)W * sizeof(void*);
   std::vector<uint8_t> chunks;  // the reduce's list, then the clip's where that is another
   // Appends chunks of one length, so many to each CTA of a resident wave: as
@@ -152,6 +154,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   const size_t clip_at = W >= 8 ? chunks.size() : 0;
   const int64_t n_clip = W >= 8 ? cut(car::kGradChunkVecs) : n_reduce;
   const int grid = (int)std::max<int64_t>(1, std::min(n_reduce, reduce_cap));
+  const int store_grid = (int)std::min<int64_t>(grid, (int64_t)std::max(1, per_store) * num_sms);
   const int clip_grid = (int)std::max<int64_t>(1, std::min(n_clip, clip_cap));
   const size_t cb = chunks.size(), pb = (size_t)grid * sizeof(double);
   void* memory = nullptr;
@@ -169,6 +172,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   g->device = device;
   g->grid = grid;
   g->clip_grid = clip_grid;
+  g->store_grid = store_grid;
   g->memory = memory;
   g->plan.reduce = car::GradList{m, (int)n_reduce};
   g->plan.clip = car::GradList{m + clip_at, (int)n_clip};
@@ -218,7 +222,7 @@ car_status car_grads_reduce(car_grads* g, float scale, double* sumsq, void* stre
   if (st != CAR_OK) return st;
   if (!sumsq || !std::isfinite(scale)) return CAR_ERR_ARG;
   if (!aligned(sumsq, 8)) return CAR_ERR_ALIGN;
-  cudaError_t e = car::launch_grads_reduce(g->plan, scale, true, sumsq, g->grid, static_cast<cudaStream_t>(stream));
+  cudaError_t e = car::launch_grads_reduce(g->plan, scale, true, sumsq, g->store_grid, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_reduce launch");
 }
 

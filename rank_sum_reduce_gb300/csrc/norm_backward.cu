@@ -267,42 +267,59 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardMinCtas<W, VPT>) re
   if (!peers_ready) cluster_wait();
 }
 
-// dweight[j] = sum over groups of partial[g][j], in a fixed order: a warp
-// takes every kSumWarps-th group of 128 columns, all its loads in flight
-// together, and the warps' sums are added in warp order.  The partials are a
-// few MB and were just written, so they come from L2: the kernel is bound by
-// one L2 latency and its launch.
-constexpr int kSumWarps = 32;
-__global__ void __launch_bounds__(32 * kSumWarps)
+// dweight[j] = sum over groups of partial[g][j], in a fixed order: the block's
+// threads take VECS vectors of columns and every so-many-th group, all their
+// loads in flight together, and those sums are added in order.  The partials
+// are a few MB and were just written, so they come from L2: the kernel is
+// bound by one L2 latency and its launch.
+// The loads of BATCH groups are issued before the first is added: W = 8, M =
+// 512, N = 8192 19.8 -> 19.3 us, W = 1, M = 640, N = 1024 5.7 -> 5.1.  Blocks of
+// 8 warps and 32 columns while those are few: one fits beside a CTA of the
+// pipeline, so that the next call's CTAs need not wait for its end (with the
+// batches W = 2, M = 718, N = 4240 11.6 -> 10.2 us; W = 4, M = 2048, N = 4096
+// fp32 38.3 -> 36.8).  Otherwise 32 warps and 128 columns (W = 8, M = 200, N =
+// 16384 20.5 against 22.0).
+constexpr int kFewSumBlocks = 152;  // one per SM
+template <int WARPS, int VECS>
+__global__ void __launch_bounds__(32 * WARPS)
     sum_partials_kernel(const float4* __restrict__ partial, float4* __restrict__ out, const int groups, const int vecs) {
-  __shared__ float4 s[kSumWarps][32];
+  constexpr int PARTS = WARPS * 32 / VECS;  // 32 in both forms
+  constexpr int BATCH = 5;                  // one partial per SM at a time
+  __shared__ float4 s[PARTS][VECS];
   // Released before the wait: the next kernel's prologue and prefetch run in
   // the tail of the one before this.  It waits for this grid in turn, and it
   // is only launched once every CTA here is resident.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int v = blockIdx.x * 32 + lane;
+  const int col = threadIdx.x % VECS, part = threadIdx.x / VECS;
+  const int v = blockIdx.x * VECS + col;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (v < vecs) {
-#pragma unroll 8
-    for (int g = warp; g < groups; g += kSumWarps) {
-      const float4 x = __ldcg(partial + (int64_t)g * vecs + v);
-      a.x += x.x;
-      a.y += x.y;
-      a.z += x.z;
-      a.w += x.w;
+    for (int g0 = part; g0 < groups; g0 += BATCH * PARTS) {
+      float4 x[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; b++) {
+        const int g = g0 + b * PARTS;
+        x[b] = g < groups ? __ldcg(partial + (int64_t)g * vecs + v) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int b = 0; b < BATCH; b++) {
+        a.x += x[b].x;
+        a.y += x[b].y;
+        a.z += x[b].z;
+        a.w += x[b].w;
+      }
     }
   }
-  s[warp][lane] = a;
+  s[part][col] = a;
   __syncthreads();
-  // one thread per value: 128 of them, each adds the warps' sums in order
-  if (threadIdx.x < 128) {
-    const float* col = reinterpret_cast<const float*>(&s[0][0]) + threadIdx.x;
+  // one thread per value adds the parts in order
+  if (threadIdx.x < 4 * VECS) {
+    const float* c = reinterpret_cast<const float*>(&s[0][0]) + threadIdx.x;
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSumWarps; w++) sum += col[w * 128];
-    if (blockIdx.x * 32 + (threadIdx.x >> 2) < vecs) reinterpret_cast<float*>(out)[blockIdx.x * 128 + threadIdx.x] = sum;
+    for (int w = 0; w < PARTS; w++) sum += c[w * 4 * VECS];
+    if (blockIdx.x * VECS + (threadIdx.x >> 2) < vecs) reinterpret_cast<float*>(out)[blockIdx.x * 4 * VECS + threadIdx.x] = sum;
   }
 }
 
@@ -407,8 +424,10 @@ cudaError_t launch_backward(int dtype, int W, const RankPtrs& dy, const void* h,
 
 cudaError_t launch_sum_partials(const float* partial, float* out, int groups, int64_t cols, cudaStream_t s) {
   const int vecs = (int)(cols / 4);
-  return launch_pdl(sum_partials_kernel, (unsigned)((vecs + 31) / 32), 32u * kSumWarps, 0, s, 1,
-                    reinterpret_cast<const float4*>(partial), reinterpret_cast<float4*>(out), groups, vecs);
+  const bool few = vecs <= 8 * kFewSumBlocks;
+  return launch_pdl(few ? sum_partials_kernel<8, 8> : sum_partials_kernel<32, 32>, (unsigned)(few ? (vecs + 7) / 8 : (vecs + 31) / 32),
+                    few ? 8u * 32u : 32u * 32u, 0, s, 1, reinterpret_cast<const float4*>(partial),
+                    reinterpret_cast<float4*>(out), groups, vecs);
 }
 
 }  // namespace car
