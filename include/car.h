@@ -259,8 +259,10 @@ car_status car_grads_destroy(car_grads* g);
 
 /* First half: with G = scale * (fp32 rank sum, as in car_reduce),
  *   outs[t] = rne_T(G_t);   *sumsq = sum over all tensors of G^2
- * from the unrounded G (squares in fp32, sums in 64 bits beyond a few hundred
- * terms; the same call on the same data gives the same bits).  Where the
+ * from the unrounded G (squares in fp32, and sums of them over up to 64 values
+ * of a thread and over 32 threads; in 64 bits beyond that, and over the threads
+ * already where fp32 could overflow; the same call on the same data gives the
+ * same bits).  Where the
  * model is split over several handles or devices, add their sumsq and pass
  * the total to car_grads_clip.
  *   scale : finite, e.g. 1 / W for the mean.

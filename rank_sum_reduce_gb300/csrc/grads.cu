@@ -29,7 +29,8 @@
 // first descriptor, and a prefetch of the first 8 KB per rank into L2, come
 // before the PDL wait (W = 4, 8 MB: 11.0 -> 9.3 us).  Squares are summed in
 // fp32 over a thread's part of one chunk (kGradChunkVecs / kGradThreads = 8
-// vectors, 64 values) and over its warp, and in 64 bits from there on.  The
+// vectors, 64 values) and over its warp (in 64 bits near fp32's largest value),
+// and in 64 bits from there on.  The
 // CTAs' partials are added the same in any order, so the same call gives the
 // same bits: by the last CTA to arrive where the caller wants the sum, and
 // by every CTA of the second pass where that follows (car_grads_reduce_clip):
@@ -72,7 +73,14 @@ struct Scalar<kFP32> {
 // is integer arithmetic, and the square root and the quotient are fp32.  With
 // every thread taking root and quotient in 64 bits a clip that had nothing to
 // do took 12 us.
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the warp in fp32, or in 64 bits where that could overflow.
+__device__ __forceinline__ double warp_sum(float v) {
+  if (__any_sync(0xFFFFFFFFu, v >= 0x1p+122f)) {
+    double d = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+    return d;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
@@ -384,8 +392,8 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
       case kFP16: ss = sum_chunk<kFP16, W, STORE>(cur, in, n, scale, policy); break;
       default: ss = sum_chunk<kFP32, W, STORE>(cur, in, n, scale, policy); break;
     }
-    ss = warp_sum(ss);
-    if ((threadIdx.x & 31) == 0) total += (double)ss;
+    const double chunk = warp_sum(ss);
+    if ((threadIdx.x & 31) == 0) total += chunk;
   }
   total = block_sum(total, s_warp);
   if (!sumsq) {  // the second pass adds the partials

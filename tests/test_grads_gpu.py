@@ -215,3 +215,58 @@ def test_refusals(car):
         assert car.car_grads_clip(g.h, s.data_ptr(), 1.0, nb.data_ptr() + 2) == car.CAR_ERR_ALIGN
         h = g.h
     assert car.car_grads_reduce_clip(h, 1.0, 1.0, None) == car.CAR_ERR_HANDLE
+
+
+def test_norm_over_the_range_of_doubles(car):
+    """The root of a caller's sum: in fp32 with 2^-23 to lose (the mantissa's conversion, halved by the root, and the
+    root's own rounding), infinite or zero past its range, NaN for what has no root."""
+    out = torch.ones(8, device=DEV)
+    nb = torch.empty(1, device=DEV)
+    with car.Grads([[out]], [out]) as g:
+        for value in (0.0, -0.0, 5e-324, 2.0**-1040, 1e-90, 1e-77, 0.1, 1.0, 2.0, 3.0, 3.7e10, 1e70, 1.1e77, 1e80, 1e300, math.inf,
+                      math.nan, -1.0, -math.inf):
+            g.clip(torch.tensor([value], dtype=torch.float64, device=DEV), math.inf, nb)
+            got = nb.item()
+            if math.isnan(value) or value < 0:
+                assert math.isnan(got), value
+                continue
+            want = math.sqrt(value)
+            if want > 3.4028235677973366e38:  # rounds past the largest fp32
+                assert got == math.inf, value
+            else:
+                assert abs(got - want) <= 2.0**-23 * want + 2.0**-149, (value, got)
+
+
+@pytest.mark.parametrize("W,n,value", [(1, 1 << 22, 1e18), (2, 3_000_001, 5e17), (1, 1 << 22, 1e-18), (4, 777, 3e-20)])
+def test_sums_of_squares_past_the_range_of_fp32(car, W, n, value):
+    """Sums above fp32's largest value and squares near its smallest normal ones, over many CTAs: 2^-17 for the squares
+    in fp32 (their bound doubled: no root here) and the partials' sum within 2^-41."""
+    xs = [torch.full((n,), value, device=DEV) for _ in range(W)]
+    out = torch.empty(n, device=DEV)
+    sq, nb = torch.empty(1, dtype=torch.float64, device=DEV), torch.empty(1, device=DEV)
+    G = xs[0].clone()
+    for x in xs[1:]:
+        G += x
+    want = (G.double() ** 2).sum().item()
+    with car.Grads([[x] for x in xs], [out]) as g:
+        g.reduce(1.0, sq)
+        assert abs(sq.item() - want) <= 2.0**-17 * want
+        g.reduce_clip(1.0, math.inf, nb)
+        assert abs(nb.item() - math.sqrt(want)) <= NORM_REL * math.sqrt(want)
+
+
+def test_partials_of_different_size(car):
+    """One large value among CTAs of small ones, and an infinity or NaN in one CTA's part."""
+    n = 2_000_003
+    x = torch.full((n,), 1e-3, device=DEV)
+    sq, out = torch.empty(1, dtype=torch.float64, device=DEV), torch.empty(n, device=DEV)
+    with car.Grads([[x]], [out]) as g:
+        for at, value in ((1_234_567, 1e15), (n - 1, 1e3), (0, math.inf), (777_777, math.nan)):
+            x.fill_(1e-3)
+            x[at] = value
+            g.reduce(1.0, sq)
+            want = (x.double() ** 2).sum().item()
+            if math.isfinite(want):
+                assert abs(sq.item() - want) <= 2.0**-17 * want
+            else:
+                assert math.isnan(sq.item()) if math.isnan(want) else sq.item() == want
