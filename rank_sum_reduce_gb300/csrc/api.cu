@@ -261,16 +261,20 @@ bool rows_compiled(int W) { return W <= 2 || W == 4 || W == 8 || W == 16; }
 //    2776, M = 531 11.2 / 10.9.
 //  * Rows of more than 1024 vectors (N = 16384, one scale per row): W = 4, M =
 //    2000 63.9 / 78.5; W = 1, M = 4000 76 / 108; W = 8, M = 300 18.7 / 20.3.
-//    More than 2048: fp32, N = 16384, W = 2, M = 2000 89 / 123; 16-bit types
-//    spill and have three ring slots only, N = 32768, W = 2, M = 1000 64 / 69,
-//    but W = 8, M = 500 76 / 61.
+//    More than 2048, where the row kernel splits rows and waits for the parts:
+//    fp32, N = 9000, M = 100, W = 1 4.0 / 5.6, W = 4 5.3 / 6.9, W = 8 9.0 / 9.0, M
+//    = 600 15.8 / 30, 25.6 / 39 and 36 / 54; with seven vectors per thread N =
+//    12800, M = 100, W = 1 5.0 / 6.0, W = 4 9.1 / 8.0, M = 304 18.9 / 22.9; bf16,
+//    N = 27000, M = 100 7.8 / 7.0, M = 304 16.8 / 20.6; with eight, N = 16384,
+//    fp32, M = 2000, W = 4 133 / 150, W = 8 221 / 202.
 //  * Rank counts that the row kernel is not compiled for: W = 6, N = 4096, M =
 //    4096 43 / 65; W = 3, N = 10000, M = 2000 40 / 118, N = 8192, M = 200 5.3 /
 //    7.1, N = 2048, M = 200 3.0 / 2.4.
 bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int64_t tiles = (h->M + sh.teams - 1) / sh.teams, sms = h->num_sms;
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
-  if (h->vec_per_row > 2048) return (h->dtype == CAR_FP32 || h->W <= 2) && 2 * tiles >= 3 * sms;
+  if (h->vec_per_row > 3584 && h->W == 8) return false;
+  if (h->vec_per_row > 2048) return sh.vpt <= 6 ? 2 * tiles >= sms : tiles >= sms;
   if (h->vec_per_row > 1024) return 2 * tiles >= 3 * sms;
   if (h->W <= 2) {
     if (sh.teams >= 16) return 2 * tiles >= sms;
@@ -306,9 +310,13 @@ bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
 //    16 bits the accumulators leave little room, N = 13000, W = 2, M = 608 23.5 /
 //    21.6, W = 4, M = 608 29.1 / 27.8, M = 2000 73 / 77; N = 14336, W = 1, M =
 //    3000 86 / 75; N = 14000, W = 8, M = 608 40.5 / 44.1; N = 16384, W = 4, M =
-//    4000 180 / 148.  Eight (fp32): N = 12800, W = 1, M = 3000 138 / 153; N =
-//    12000, W = 4, M = 3000 182 / 190; N = 16384, W = 2, M = 2000 127 / 118; N =
-//    11840, W = 8, M = 664 69 / 64.
+//    4000 180 / 148.  More, in fp32:
+//    N = 9000, M = 100, W = 2 6.9 / 7.6, W = 8 11.4 / 11.6, M = 600, W = 2 25.8 /
+//    36.0, W = 8 44 / 53; N = 11000, M = 3000, W = 1 103 / 152, W = 8 228 / 264.
+//    Seven vectors per thread: N = 12800, W = 1, M = 152 11.3 / 12.0, W = 2, M =
+//    600 37.7 / 35.9, W = 4, M = 2000 129 / 141, W = 8 181 / 172, but N = 14000, M
+//    = 1500 147 / 158.  Eight: N = 16384, W = 1, M = 600 40 / 36, M = 2000 110 /
+//    115, W = 4 165 / 145.
 //  * Rank counts that the row kernel is not compiled for: W = 3, N = 10000, M =
 //    2000 56 / 127; W = 6, N = 16384 fp32, M = 500 62 / 80; W = 3, N = 8192, M =
 //    200 9.7 / 10.3.
@@ -317,7 +325,9 @@ bool backward_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int V = h->vec_per_row;
   const bool fp32 = h->dtype == CAR_FP32;
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
-  if (V > 2048) return V <= 3328 && h->W <= 4 && tiles >= 8 * sms;
+  if (V > 3584) return h->W == 1 && tiles >= 8 * sms;
+  if (V > 3072) return tiles >= sms && (h->W != 8 || V > 3328);
+  if (V > 2048) return 3 * tiles >= 2 * sms;
   if (V > 1536) return fp32 ? tiles >= 2 * sms : V <= 1792 && h->W >= 4 && tiles >= (h->W < 8 ? 6 : 2) * sms;
   if (V > 1024) return tiles >= (h->W <= 2 ? 3 : 2) * sms;
   if (h->W <= 2 && sh.teams == 1) return tiles >= (fp32 ? 4 : 6) * sms;

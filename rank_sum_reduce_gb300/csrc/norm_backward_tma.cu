@@ -128,7 +128,7 @@ template <int DT, int VPT>
 constexpr bool kWideWeight = DT != kFP32 && VPT == 2;
 template <int DT, int VPT>
 __device__ __forceinline__ int weight_row_bytes(int row_bytes) {
-  return VPT == 8 ? 0 : kWideWeight<DT, VPT> ? 2 * row_bytes : row_bytes;
+  return VPT > 4 ? 0 : kWideWeight<DT, VPT> ? 2 * row_bytes : row_bytes;
 }
 
 // VPT: vectors per consumer thread.  Two for rows of up to 1024 vectors: with
@@ -138,8 +138,9 @@ __device__ __forceinline__ int weight_row_bytes(int row_bytes) {
 // without a row (W = 8, M = 1500, N = 4400: 27.4 against 34.4; N = 7000, where
 // two fit better, 43.0 against 39.6).  Four only for rows that three do not
 // hold: in 16 bits the accumulators leave little room to overlap (N = 4400:
-// 36.3).  Eight above that, in fp32 alone: eight 16-bit vectors' accumulators
-// would not fit in registers.
+// 36.3).  Five to eight above that, as few as 512 threads need (W = 1, M = 3000,
+// N = 9000: five 81 us, six 98, eight 115), in fp32 alone: more than four
+// 16-bit vectors' accumulators would not fit in registers.
 template <int DT, int VPT>
 __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* ring, const uint8_t* s_weight, uint64_t* full,
                                         uint64_t* empty, uint64_t* rowbar, uint64_t* done, float2* s_warp,
@@ -183,7 +184,7 @@ __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* rin
   auto weight = [&](int k, float2 (&f)[E / 2]) {
     const int v = tid + k * T;
     if constexpr (kWideWeight<DT, VPT>) lds_wide(s_weight, p.vec_per_row, v, f);
-    else if constexpr (VPT < 8) widen2(lds16(s_weight + 16 * v), f);
+    else if constexpr (VPT <= 4) widen2(lds16(s_weight + 16 * v), f);
     else widen2(__ldg(p.weight + v), f);
   };
   for (int64_t tile = (int64_t)blockIdx.x * p.teams; tile < p.rows; tile += (int64_t)gridDim.x * p.teams) {
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1) reduce_rmsnorm_backw
   if (warp >= nwarps) {
     if (lane == 0) produce(p, smem, full, empty, s_abort, warp - nwarps);
   } else {
-    if constexpr (VPT != 8) {
+    if constexpr (VPT <= 4) {
       weight_to_shared<DT, kWideWeight<DT, VPT>>(p.weight, p.vec_per_row, consumers, s_weight);
       asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
     }
@@ -393,7 +394,12 @@ BackwardTmaFn pick_vpt(int vpt) {
   if (vpt == 2) return reduce_rmsnorm_backward_tma_kernel<DT, 2>;
   if (vpt == 3) return reduce_rmsnorm_backward_tma_kernel<DT, 3>;
   if (vpt == 4) return reduce_rmsnorm_backward_tma_kernel<DT, 4>;
-  if constexpr (DT == kFP32) return reduce_rmsnorm_backward_tma_kernel<DT, 8>;
+  if constexpr (DT == kFP32) {
+    if (vpt == 5) return reduce_rmsnorm_backward_tma_kernel<DT, 5>;
+    if (vpt == 6) return reduce_rmsnorm_backward_tma_kernel<DT, 6>;
+    if (vpt == 7) return reduce_rmsnorm_backward_tma_kernel<DT, 7>;
+    return reduce_rmsnorm_backward_tma_kernel<DT, 8>;
+  }
   return nullptr;
 }
 BackwardTmaFn pick(int dtype, int vpt) {
@@ -410,8 +416,8 @@ constexpr int kRingBudget = 224 * 1024;  // ring and weight row
 
 bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
-  if (vpt == 8 && dtype != kFP32) return false;
+  const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512 : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
+  if (vpt > (dtype == kFP32 ? 8 : 4)) return false;
   out->vpt = vpt;
   out->use = team_use(vec_per_row, vpt);
   out->team_threads = team_threads(vec_per_row, vpt);
@@ -419,7 +425,7 @@ bool backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, i
   const int teams = 512 / out->team_threads;
   out->teams = teams;
   // about one tile's slices in flight, as in the forward, and an even number
-  const int slice = teams * row_bytes, weights = vpt == 8 ? 0 : vpt == 2 && dtype != kFP32 ? 2 * row_bytes : row_bytes;
+  const int slice = teams * row_bytes, weights = vpt > 4 ? 0 : vpt == 2 && dtype != kFP32 ? 2 * row_bytes : row_bytes;
   int slots = W + 2 < 6 ? 6 : (W + 3) / 2 * 2;
   if (slots > (kRingBudget - weights) / slice) slots = (kRingBudget - weights) / slice;
   if (slots > 4) slots -= slots % kProducers;

@@ -18,8 +18,9 @@
 // with six slots against 19.0 with four), unless they leave threads without a
 // row, which three do not (W = 4, M = 8191, N = 6144: 112 against 95; W = 8, M =
 // 1500, N = 5000 31.7 against 25.7, four 27.5).  Rows of more than 2048 vectors
-// take eight, the weight read from L2 once per row (64 KB of it beside
-// the ring would leave two slots).
+// take five to eight, as few as 512 threads need (W = 1, M = 2000, N = 20000
+// bf16: five 52 us, six 65, eight 78), the weight read from L2 once per row (64
+// KB of it beside the ring would leave two slots).
 #include "car_launch.h"
 #include "quant.cuh"
 #include "ring.cuh"
@@ -132,7 +133,7 @@ __device__ __forceinline__ void consume(const QuantTmaParams& p, const uint8_t* 
   auto weight = [&](int k, float2 (&f)[E / 2]) {
     if constexpr (kWideWeight<DT, VPT>) lds_wide(s_weight, p.vec_per_row, tid + k * T, f);
     else if constexpr (VPT == 2) widen2(wv[k], f);
-    else if constexpr (VPT < 8) widen2(lds16(s_weight + 16 * (tid + k * T)), f);
+    else if constexpr (VPT <= 4) widen2(lds16(s_weight + 16 * (tid + k * T)), f);
     else widen2(__ldg(p.weight + tid + k * T), f);
   };
   int slot = 0;
@@ -296,10 +297,15 @@ using QuantTmaFn = void (*)(const QuantTmaParams);
 
 template <int DT>
 QuantTmaFn pick_vpt(int vpt) {
-  return vpt == 2   ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 2>
-         : vpt == 3 ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 3>
-         : vpt == 4 ? reduce_residual_rmsnorm_quant_tma_kernel<DT, 4>
-                    : reduce_residual_rmsnorm_quant_tma_kernel<DT, 8>;
+  switch (vpt) {
+    case 2: return reduce_residual_rmsnorm_quant_tma_kernel<DT, 2>;
+    case 3: return reduce_residual_rmsnorm_quant_tma_kernel<DT, 3>;
+    case 4: return reduce_residual_rmsnorm_quant_tma_kernel<DT, 4>;
+    case 5: return reduce_residual_rmsnorm_quant_tma_kernel<DT, 5>;
+    case 6: return reduce_residual_rmsnorm_quant_tma_kernel<DT, 6>;
+    case 7: return reduce_residual_rmsnorm_quant_tma_kernel<DT, 7>;
+    default: return reduce_residual_rmsnorm_quant_tma_kernel<DT, 8>;
+  }
 }
 QuantTmaFn pick(int dtype, int vpt) {
   switch (dtype) {
@@ -315,7 +321,7 @@ constexpr int kRingBudget = 216 * 1024;  // ring and weight row
 
 bool quant_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, TeamShape* out) {
   const int row_bytes = vec_per_row * 16;
-  const int vpt = vec_per_row > 2048 ? 8 : team_vectors(vec_per_row, W <= 3 ? 4 : 2, W <= 3 || vec_per_row > 1536 ? 4 : 3);
+  const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512 : team_vectors(vec_per_row, W <= 3 ? 4 : 2, W <= 3 || vec_per_row > 1536 ? 4 : 3);
   out->vpt = vpt;
   out->use = team_use(vec_per_row, vpt);
   out->team_threads = team_threads(vec_per_row, vpt);

@@ -65,6 +65,11 @@ CASES = [
     (3, 1001, 2056, "fp16"), (2, 901, 1000, "fp32"),
     # three vectors per thread
     (8, 401, 6144, "bf16"), (4, 331, 10488, "fp16"), (1, 311, 11072, "bf16"), (16, 307, 4656, "fp32"), (1, 1231, 12800, "fp32"),
+    # four to eight, rows of more than 24 KB
+    (8, 333, 13000, "bf16"), (1, 111, 9000, "fp32"), (8, 203, 10004, "fp32"), (2, 167, 11004, "fp32"), (6, 95, 12288, "fp32"),
+    (4, 161, 13004, "fp32"), (1, 1301, 15000, "fp32"), (3, 91, 16384, "fp32"),
+    # partials of several CTAs per SM, and more columns than blocks of 32 cover
+    (2, 3001, 264, "fp16"), (8, 170, 4872, "bf16"),
 ]
 
 

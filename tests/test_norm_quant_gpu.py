@@ -82,6 +82,9 @@ CASES = [
     (1, 4099, 1024, "bf16"), (3, 1001, 2056, "fp16"), (2, 2601, 1000, "fp32"),
     # three vectors per thread
     (8, 411, 6144, "bf16"), (4, 391, 9352, "fp16"), (16, 803, 2192, "bf16"), (2, 401, 4728, "fp32"),
+    # five to eight, rows of more than 32 KB
+    (1, 201, 9000, "fp32"), (8, 111, 18000, "bf16"), (2, 167, 11004, "fp32"), (6, 83, 24008, "fp16"), (4, 161, 13004, "fp32"),
+    (1, 333, 27000, "bf16"), (4, 171, 16384, "fp32"), (16, 160, 30008, "bf16"),
 ]
 
 
