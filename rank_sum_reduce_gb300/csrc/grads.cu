@@ -30,12 +30,12 @@
 // before the PDL wait (W = 4, 8 MB: 11.0 -> 9.3 us).  Squares are summed in
 // fp32 over a thread's part of one chunk (kGradChunkVecs / kGradThreads = 8
 // vectors, 64 values) and over its warp (in 64 bits near fp32's largest value),
-// and in 64 bits from there on.  The
-// CTAs' partials are added the same in any order, so the same call gives the
-// same bits: by the last CTA to arrive where the caller wants the sum, and
-// by every CTA of the second pass where that follows (car_grads_reduce_clip):
-// the fence, the arrival and the partials' loads leave the tail of the first
-// pass (W = 2, 0.2 MB, clipped 6.3 -> 4.7 us; W = 4, 8 MB 13.7 -> 11.5).
+// and in 64 bits from there on.  The CTAs' partials are added the same in any
+// order, so the same call gives the same bits: by the last CTA to arrive where
+// the caller wants the sum, and by every CTA of the second pass where that
+// follows (car_grads_reduce_clip): the fence, the arrival and the partials'
+// loads leave the tail of the first pass (W = 2, 0.2 MB, clipped 6.3 -> 4.0 us;
+// W = 4, 8 MB 13.7 -> 11.2).
 // Roofline: HBM, (W + 1) * 16 bytes per vector: 516 to 522 us for W = 8, 400 MB
 // (1.02 of the copy peak).
 #include <stdint.h>
@@ -178,10 +178,8 @@ __device__ __forceinline__ uint64_t read_policy(bool evict_first) {
   return evict_first ? first : normal;
 }
 // A pass that stores may store over an input, or over what the first pass
-// stored: its loads are ordinary ones.  Loads of data that the kernel never
-// writes may be called that, which lets them go ahead of anything (a clipped
-// step of W = 1, 152 MB 73.5 us against 74.8; the stores' pass measures the
-// same either way but for W = 4, 8 MB, 9.25 us against 9.02).
+// stored: its loads are ordinary ones.  (As loads of constant data they
+// measure the same but for W = 4, 8 MB, 9.02 against 9.25 us.)
 template <bool READ_ONLY>
 __device__ __forceinline__ uint4 ld_hint(const void* p, uint64_t policy) {
   uint4 v;

@@ -3,8 +3,8 @@ the forward's definition, and against differences.
 
 Tolerances (see operator_checks): with a = rms g w, b = rms u m and d the skip gradient, dx loses DELTA of each of
 |a| and |d| and, since m is a mean of terms that may cancel, DELTA of rms |u| mean|g w u| for b, twice for the two sums
-that enter it; plus its rounding.  dweight sums at most 14 rows in a register, 76 partials in a lane and 8 of warps:
-under 100 roundings of 2^-24, with those of g u under 2^-17 of sum |g u|."""
+that enter it; plus its rounding.  dweight sums at most 14 rows in a register, 16 teams of a CTA, 19 partials in a
+thread and 32 threads' sums: under 100 roundings of 2^-24, with those of g u under 2^-17 of sum |g u|."""
 import pytest
 import torch
 
