@@ -279,7 +279,12 @@ car_status car_grads_clip(car_grads* g, const double* sumsq, float max_norm, flo
 
 /* Both halves for a step whose gradients are all in this handle.  With one
  * rank the unclipped values are not stored in between (one rounding, not two;
- * in place, a scale of 1 and a norm within the limit write nothing).
+ * in place, a scale of 1 and a norm within the limit write nothing).  With
+ * more, a clipped value is rounded twice, as by the two calls, but an fp16 sum
+ * past 65504 is not lost in between: rne_T(G_t * factor) where rne_T(G_t) is
+ * infinite and G_t is not.  fp16 tensors whose output replaces an input are
+ * read twice for that (8 ranks, 64 M values: 359 us against 186 with an output
+ * of its own).
  * Errors of the three calls: CAR_ERR_HANDLE, CAR_ERR_ARG (NULL sumsq, scale
  * not finite, max_norm < 0 or NaN, another current device), CAR_ERR_ALIGN,
  * CAR_ERR_CUDA. */

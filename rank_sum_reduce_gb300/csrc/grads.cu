@@ -9,7 +9,11 @@
 // and does nothing when the norm is within the limit.  Keeping G in its type
 // between the passes costs a clipped value one more rounding of half a step
 // (what calling a reduce and then a clip would give) and keeps the second
-// pass at one read and one write of the tensors.  With one rank the first pass
+// pass at one read and one write of the tensors.  Only where that rounding would
+// lose the value is it not kept: an fp16 sum past 65504 is stored as infinity,
+// and the second pass adds the ranks again for the elements that it finds so.
+// Where the output replaces an fp16 input, which is gone by then, the first
+// pass stores nothing and the second adds the ranks of the whole tensor.  With one rank the first pass
 // of car_grads_reduce_clip only reads: the second reads the input again, so
 // that a clipped step moves 3 tensors' bytes instead of 4 (and rounds once),
 // and one in place that needs no clipping moves 1.
@@ -320,6 +324,134 @@ __device__ __forceinline__ void clip_vectors(uint4* to, const uint4* from, int v
   }
 }
 
+// G of one element, as sum_chunk forms it.
+template <int DT>
+__device__ __forceinline__ float sum_element(const void* const* __restrict__ in, int n, int at, float scale) {
+  using S = Scalar<DT>;
+  using T = typename S::T;
+  float acc = S::up(static_cast<const T*>(in[0])[at]);
+  for (int r = 1; r < n; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(in[r])[at]));
+  return __fmul_rn(acc, scale);
+}
+
+// The same for U vectors at the byte offsets `at` of every rank.
+template <int DT, int U>
+__device__ __forceinline__ void sum_vectors(const void* const* __restrict__ in, int n, const uint32_t (&at)[U], float scale,
+                                            float (&acc)[U][Pack<DT>::kN]) {
+  constexpr int E = Pack<DT>::kN;
+#pragma unroll 1
+  for (int r = 0; r < n; r++) {
+    const uint8_t* from = static_cast<const uint8_t*>(in[r]);
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) raw[u] = ld_once(from + at[u]);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      float f[E];
+      Pack<DT>::widen(raw[u], f);
+#pragma unroll
+      for (int e = 0; e < E; e++) acc[u][e] = r == 0 ? f[e] : __fadd_rn(acc[u][e], f[e]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+#pragma unroll
+    for (int e = 0; e < E; e++) acc[u][e] = __fmul_rn(acc[u][e], scale);
+  }
+}
+
+// The clipped value of a sum whose stored form is `stored`: the sum itself
+// counts where that is infinite, since a factor below 1 may bring it back.
+__device__ __forceinline__ float clip_half(float stored, float sum, float coef) {
+  return __fmul_rn(isinf(stored) ? sum : stored, coef);
+}
+
+__device__ __forceinline__ bool in_place(const GradChunk& c, const void* const* __restrict__ in, int n) {
+  bool hit = false;
+  for (int r = 0; r < n; r++) hit = hit || in[r] == c.out;
+  return hit;
+}
+
+// fp16, two and more ranks, the first pass's sums in out: infinite ones are
+// added again.
+__device__ __forceinline__ void clip_half_chunk(const GradChunk& c, const void* const* __restrict__ in, int n, float scale,
+                                                float coef, uint64_t policy) {
+  constexpr int E = Pack<kFP16>::kN;
+  const Span sp = span_of<kFP16>(c);
+  __half* out = static_cast<__half*>(c.out);
+  uint4* to = reinterpret_cast<uint4*>(out + sp.head);
+  constexpr int U = 4;
+#pragma unroll 1
+  for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) raw[u] = ld_once(to + min(v0 + u * kGradThreads, sp.vecs - 1));
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int v = v0 + u * kGradThreads;
+      if (v < sp.vecs) {
+        float f[E], o[E];
+        Pack<kFP16>::widen(raw[u], f);
+        bool lost = false;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          lost = lost || isinf(f[e]);
+          o[e] = __fmul_rn(f[e], coef);
+        }
+        if (lost) {
+          const uint32_t at[1] = {((uint32_t)sp.head + (uint32_t)v * E) * (uint32_t)sizeof(__half)};
+          float sum[1][E];
+          sum_vectors<kFP16, 1>(in, n, at, scale, sum);
+#pragma unroll
+          for (int e = 0; e < E; e++) o[e] = clip_half(f[e], sum[0][e], coef);
+        }
+        st_hint(to + v, Pack<kFP16>::narrow(o), policy);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
+    const int at = i < sp.head ? i : i + sp.vecs * E;
+    const float f = __half2float(out[at]);
+    out[at] = __float2half_rn(isinf(f) ? clip_half(f, sum_element<kFP16>(in, n, at, scale), coef) : __fmul_rn(f, coef));
+  }
+}
+
+// fp16 in place of an input, which the first pass left as it was: the sums
+// and their clipping at once, with the same two roundings.
+__device__ __forceinline__ void sum_clip_half_chunk(const GradChunk& c, const void* const* __restrict__ in, int n, float scale,
+                                                    float coef, uint64_t policy) {
+  constexpr int E = Pack<kFP16>::kN;
+  const Span sp = span_of<kFP16>(c);
+  __half* out = static_cast<__half*>(c.out);
+  constexpr int U = 2;
+#pragma unroll 1
+  for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
+    uint32_t at[U];
+    float acc[U][E];
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      at[u] = (uint32_t)sp.head * (uint32_t)sizeof(__half) + (uint32_t)min(v0 + u * kGradThreads, sp.vecs - 1) * 16u;
+    sum_vectors<kFP16, U>(in, n, at, scale, acc);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (v0 + u * kGradThreads < sp.vecs) {
+        float f[E];
+        Pack<kFP16>::widen(Pack<kFP16>::narrow(acc[u]), f);
+#pragma unroll
+        for (int e = 0; e < E; e++) f[e] = clip_half(f[e], acc[u][e], coef);
+        st_hint(reinterpret_cast<uint8_t*>(out) + at[u], Pack<kFP16>::narrow(f), policy);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
+    const int at = i < sp.head ? i : i + sp.vecs * E;
+    const float sum = sum_element<kFP16>(in, n, at, scale);
+    out[at] = __float2half_rn(clip_half(__half2float(__float2half_rn(sum)), sum, coef));
+  }
+}
+
 // One chunk of it, from being out itself or rank 0's input.  Eight loads in
 // flight per thread against four: W = 4, 8 MB 11.2 -> 10.7 us, W = 8, 400 MB
 // 680 -> 672; chunks of one vector per thread have no use for them.
@@ -387,7 +519,12 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
     float ss;
     switch (cur.dtype) {
       case kBF16: ss = sum_chunk<kBF16, W, STORE>(cur, in, n, scale, policy); break;
-      case kFP16: ss = sum_chunk<kFP16, W, STORE>(cur, in, n, scale, policy); break;
+      case kFP16:
+        if (STORE && W != 1 && !sumsq && in_place(cur, in, n))  // left to the second pass
+          ss = sum_chunk<kFP16, W, false>(cur, in, n, scale, policy);
+        else
+          ss = sum_chunk<kFP16, W, STORE>(cur, in, n, scale, policy);
+        break;
       default: ss = sum_chunk<kFP32, W, STORE>(cur, in, n, scale, policy); break;
     }
     const double chunk = warp_sum(ss);
@@ -414,20 +551,21 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
   }
 }
 
-// FROM_INPUT: the values come from the one rank's input and the first pass
-// stored nothing.
-template <bool FROM_INPUT>
-__global__ void __launch_bounds__(kGradThreads)
+// FROM: where the values come from (car_launch.h).
+template <GradSource FROM>
+__global__ void __launch_bounds__(kGradThreads, 4)
     grads_clip_kernel(const GradPlan p, const double* __restrict__ sums, const int n_sums, const float scale,
                       const float max_norm, float* __restrict__ norm_out) {
+  constexpr bool FROM_INPUT = FROM == GradSource::kInput;
   __shared__ TotalShared s_total;
   const uint64_t policy = read_policy(p.pass_on);
   const int stride = (int)sizeof(GradChunk) + 8 * p.W;
   int i = p.clip.n - 1 - (int)blockIdx.x;
   GradChunk c = {};
+  const GradChunk* d = nullptr;
   const void* from = nullptr;
   if (i >= 0) {
-    const GradChunk* d = chunk_at(p.clip, stride, i);
+    d = chunk_at(p.clip, stride, i);
     c = *d;
     from = FROM_INPUT ? inputs_of(d)[0] : c.out;
   }
@@ -441,22 +579,41 @@ __global__ void __launch_bounds__(kGradThreads)
   const float ratio = __fdiv_rn(max_norm, norm + 1e-6f);
   // within the limit, or no limit (false for a NaN norm, which then reaches every value)
   const bool whole = ratio >= 1.f || isinf(max_norm);
-  if (whole && !FROM_INPUT) return;
+  if (whole && !FROM_INPUT && !(FROM == GradSource::kSums && p.half_in_place)) return;
   const float coef = whole ? 1.f : ratio;
   for (; i >= 0; i -= (int)gridDim.x) {
     const GradChunk cur = c;
+    const void* const* in = inputs_of(d);
     const void* x = from;
     if (i >= (int)gridDim.x) {
-      const GradChunk* d = chunk_at(p.clip, stride, i - (int)gridDim.x);
+      d = chunk_at(p.clip, stride, i - (int)gridDim.x);
       c = *d;
       from = FROM_INPUT ? inputs_of(d)[0] : c.out;
     }
     if (FROM_INPUT && x == cur.out && whole && scale == 1.f) continue;  // already there
-    switch (cur.dtype) {
-      case kBF16: clip_chunk<kBF16>(cur, x, scale, coef, policy); break;
-      case kFP16: clip_chunk<kFP16>(cur, x, scale, coef, policy); break;
-      default: clip_chunk<kFP32>(cur, x, scale, coef, policy); break;
+    if (FROM == GradSource::kSums && cur.dtype == kFP16) {
+      if (p.half_in_place && in_place(cur, in, p.W))
+        sum_clip_half_chunk(cur, in, p.W, scale, coef, policy);
+      else if (!whole)
+        clip_half_chunk(cur, in, p.W, scale, coef, policy);
+      continue;
     }
+    if (FROM == GradSource::kSums && whole) continue;
+    const float once = FROM_INPUT ? scale : 1.f;  // what out holds is scaled
+    switch (cur.dtype) {
+      case kBF16: clip_chunk<kBF16>(cur, x, once, coef, policy); break;
+      case kFP16: clip_chunk<kFP16>(cur, x, once, coef, policy); break;
+      default: clip_chunk<kFP32>(cur, x, once, coef, policy); break;
+    }
+  }
+}
+
+using ClipFn = void (*)(const GradPlan, const double*, const int, const float, const float, float*);
+ClipFn pick_clip(GradSource from) {
+  switch (from) {
+    case GradSource::kOutput: return grads_clip_kernel<GradSource::kOutput>;
+    case GradSource::kSums: return grads_clip_kernel<GradSource::kSums>;
+    default: return grads_clip_kernel<GradSource::kInput>;
   }
 }
 
@@ -477,12 +634,13 @@ GradsFn pick_grads(int W, bool store) {
 
 }  // namespace
 
-cudaError_t grads_occupancy(int W, bool store, int* reduce_per_sm, int* clip_per_sm) {
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      reduce_per_sm, reinterpret_cast<const void*>(pick_grads(W, store)), kGradThreads, 0);
-  if (e != cudaSuccess) return e;
+cudaError_t grads_occupancy(int W, bool store, int* reduce_per_sm) {
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      clip_per_sm, reinterpret_cast<const void*>(store ? grads_clip_kernel<false> : grads_clip_kernel<true>), kGradThreads, 0);
+      reduce_per_sm, reinterpret_cast<const void*>(pick_grads(W, store)), kGradThreads, 0);
+}
+
+cudaError_t grads_clip_occupancy(GradSource from, int* per_sm) {
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, reinterpret_cast<const void*>(pick_clip(from)), kGradThreads, 0);
 }
 
 cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s) {
@@ -491,10 +649,9 @@ cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, d
   return launch_pdl(fn, (unsigned)grid, kGradThreads, 0, s, 1, plan, scale, sumsq);
 }
 
-cudaError_t launch_grads_clip(const GradPlan& plan, const double* sums, int n_sums, float scale, bool from_input,
+cudaError_t launch_grads_clip(const GradPlan& plan, const double* sums, int n_sums, float scale, GradSource from,
                               float max_norm, float* norm_out, int grid, cudaStream_t s) {
-  return launch_pdl(from_input ? grads_clip_kernel<true> : grads_clip_kernel<false>, (unsigned)grid, kGradThreads, 0, s, 1,
-                    plan, sums, n_sums, scale, max_norm, norm_out);
+  return launch_pdl(pick_clip(from), (unsigned)grid, kGradThreads, 0, s, 1, plan, sums, n_sums, scale, max_norm, norm_out);
 }
 
 }  // namespace car

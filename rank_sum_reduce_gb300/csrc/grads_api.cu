@@ -18,9 +18,11 @@
 
 struct car_grads {
   int device;
-  int grid, clip_grid;  // of car_grads_reduce_clip's two passes
+  int grid, sums_grid;  // of car_grads_reduce_clip's two passes
+  int clip_grid;        // of car_grads_clip
   int store_grid;       // of car_grads_reduce: with one rank another kernel than the first pass's
   void* memory;  // one allocation: chunks, partials, counter
+  car::GradSource source;  // of car_grads_reduce_clip's second pass
   car::GradPlan plan;
 };
 
@@ -106,14 +108,26 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   car_status st = check_overlap(W, n, bytes, inputs, outs);
   if (st != CAR_OK) return st;
 
-  int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_clip = 0, per_store = 0, unused = 0;
+  bool half = false, half_in_place = false;
+  for (int64_t k = 0; k < W * n && W > 1; k++) {
+    const bool is_half = dtypes[k % n] == CAR_FP16 && bytes[k % n];
+    half = half || is_half;
+    half_in_place = half_in_place || (is_half && inputs[k] == outs[k % n]);
+  }
+  // (kSums with nothing to add again is slower: W = 2, 64 M bf16 values 92.9
+  // against 90.1 us.)
+  const car::GradSource source = W == 1 ? car::GradSource::kInput : half ? car::GradSource::kSums : car::GradSource::kOutput;
+
+  int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_sums = 0, per_clip = 0, per_store = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, device);
-  if (e == cudaSuccess) e = car::grads_occupancy(W, W > 1, &per_reduce, &per_clip);
-  if (e == cudaSuccess) e = car::grads_occupancy(W, true, &per_store, &unused);
+  if (e == cudaSuccess) e = car::grads_occupancy(W, W > 1, &per_reduce);
+  if (e == cudaSuccess) e = car::grads_occupancy(W, true, &per_store);
+  if (e == cudaSuccess) e = car::grads_clip_occupancy(source, &per_sums);
+  if (e == cudaSuccess) e = car::grads_clip_occupancy(car::GradSource::kOutput, &per_clip);
   if (e != cudaSuccess) return fail(e, "gradient launch sizes");
-  const int64_t reduce_cap = std::min<int64_t>((int64_t)std::max(1, per_reduce) * num_sms, car::kMaxGradCtas), clip_cap = (int64_t)std::max(1, per_clip) * num_sms;
+  const int64_t reduce_cap = std::min<int64_t>((int64_t)std::max(1, per_reduce) * num_sms, car::kMaxGradCtas);
   const size_t stride = sizeof(car::GradChunk) + (size_t)W * sizeof(void*);
   std::vector<uint8_t> chunks;  // the reduce's list, then the clip's where that is another
   // Appends chunks of one length, so many to each CTA of a resident wave: as
@@ -155,7 +169,8 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   const int64_t n_clip = W >= 8 ? cut(car::kGradChunkVecs) : n_reduce;
   const int grid = (int)std::max<int64_t>(1, std::min(n_reduce, reduce_cap));
   const int store_grid = (int)std::min<int64_t>(grid, (int64_t)std::max(1, per_store) * num_sms);
-  const int clip_grid = (int)std::max<int64_t>(1, std::min(n_clip, clip_cap));
+  const int sums_grid = (int)std::max<int64_t>(1, std::min<int64_t>(n_clip, (int64_t)std::max(1, per_sums) * num_sms));
+  const int clip_grid = (int)std::max<int64_t>(1, std::min<int64_t>(n_clip, (int64_t)std::max(1, per_clip) * num_sms));
   const size_t cb = chunks.size(), pb = (size_t)grid * sizeof(double);
   void* memory = nullptr;
   e = cudaMalloc(&memory, cb + pb + 8);
@@ -171,6 +186,8 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   }
   g->device = device;
   g->grid = grid;
+  g->sums_grid = sums_grid;
+  g->source = source;
   g->clip_grid = clip_grid;
   g->store_grid = store_grid;
   g->memory = memory;
@@ -179,6 +196,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   g->plan.W = W;
   g->plan.evict_first = 16 * vecs < 2 * (int64_t)l2;
   g->plan.pass_on = 16 * vecs > (int64_t)l2 / 4;
+  g->plan.half_in_place = half_in_place;
   g->plan.partial = reinterpret_cast<double*>(m + cb);
   g->plan.arrived = reinterpret_cast<unsigned int*>(m + cb + pb);
   {
@@ -231,7 +249,7 @@ car_status car_grads_clip(car_grads* g, const double* sumsq, float max_norm, flo
   if (st != CAR_OK) return st;
   if (!sumsq || !(max_norm >= 0.f)) return CAR_ERR_ARG;
   if (!aligned(sumsq, 8) || !aligned(norm_out, 4)) return CAR_ERR_ALIGN;
-  cudaError_t e = car::launch_grads_clip(g->plan, sumsq, 1, 1.f, false, max_norm, norm_out, g->clip_grid,
+  cudaError_t e = car::launch_grads_clip(g->plan, sumsq, 1, 1.f, car::GradSource::kOutput, max_norm, norm_out, g->clip_grid,
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_clip launch");
 }
@@ -245,7 +263,8 @@ car_status car_grads_reduce_clip(car_grads* g, float scale, float max_norm, floa
   const bool one = g->plan.W == 1;  // the first pass then only reads (see grads.cu)
   cudaError_t e = car::launch_grads_reduce(g->plan, scale, !one, nullptr, g->grid, s);
   if (e == cudaSuccess)
-    e = car::launch_grads_clip(g->plan, g->plan.partial, g->grid, one ? scale : 1.f, one, max_norm, norm_out, g->clip_grid, s);
+    e = car::launch_grads_clip(g->plan, g->plan.partial, g->grid, scale, g->source,
+                               max_norm, norm_out, g->sums_grid, s);
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_reduce_clip launch");
 }
 
