@@ -262,7 +262,8 @@ car_status car_grads_destroy(car_grads* g);
  * from the unrounded G (squares in fp32, and sums of them over up to 64 values
  * of a thread and over 32 threads; in 64 bits beyond that, and over the threads
  * already where fp32 could overflow; the same call on the same data gives the
- * same bits).  Where the
+ * same bits).  A finite G past fp16's range, which is stored as infinity,
+ * counts as infinity: what is stored and its norm agree.  Where the
  * model is split over several handles or devices, add their sumsq and pass
  * the total to car_grads_clip.
  *   scale : finite, e.g. 1 / W for the mean.

@@ -230,9 +230,12 @@ __device__ __forceinline__ Span span_of(const GradChunk& c) {
 template <int W>
 constexpr int kGradVectors = W >= 5 ? 1 : W >= 3 ? 2 : 4;
 
+// Squares of the unrounded sums.  kept: what is stored is all that the caller
+// will have of a sum, so one that fp16 stores as infinity (from 65520 on, half
+// a step past its largest value) adds infinity.
 template <int DT, int W, bool STORE>
 __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const* __restrict__ in, int n, float scale,
-                                           uint64_t policy) {
+                                           uint64_t policy, bool kept) {
   using S = Scalar<DT>;
   using T = typename S::T;
   constexpr int E = Pack<DT>::kN;
@@ -244,7 +247,8 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
   for (int r = 0; r < R; r++) x[r] = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
   T* out = static_cast<T*>(c.out);
   uint8_t* to = reinterpret_cast<uint8_t*>(out + sp.head);
-  float ss = 0.f;
+  constexpr bool LOSES = DT == kFP16 && STORE;
+  float ss = 0.f, top = 0.f;
 #pragma unroll 1
   for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
     // past the chunk's end the last vector is loaded again, and dropped below
@@ -284,6 +288,7 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
         for (int e = 0; e < E; e++) {
           acc[u][e] = __fmul_rn(acc[u][e], scale);
           ss = fmaf(acc[u][e], acc[u][e], ss);
+          if constexpr (LOSES) top = fmaxf(top, fabsf(acc[u][e]));
         }
         if constexpr (STORE) st16(to + at[u], Pack<DT>::narrow(acc[u]));
       }
@@ -297,8 +302,10 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
     for (int r = 1; r < n; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(in[r])[at]));
     acc = __fmul_rn(acc, scale);
     ss = fmaf(acc, acc, ss);
+    if constexpr (LOSES) top = fmaxf(top, fabsf(acc));
     if constexpr (STORE) out[at] = S::down(acc);
   }
+  if (LOSES && kept && top >= 65520.f) ss += INFINITY;  // (a NaN stays one)
   return ss;
 }
 
@@ -500,6 +507,7 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
   __shared__ bool s_last;
   const int n = W > 0 ? W : p.W;
   const uint64_t policy = read_policy(STORE && p.evict_first);
+  const bool kept = sumsq != nullptr;  // else the second pass follows
   const int first = blockIdx.x, last = p.reduce.n, stride = (int)sizeof(GradChunk) + 8 * n;
   const GradChunk* d = chunk_at(p.reduce, stride, first);
   GradChunk c = {};
@@ -518,14 +526,14 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
     }
     float ss;
     switch (cur.dtype) {
-      case kBF16: ss = sum_chunk<kBF16, W, STORE>(cur, in, n, scale, policy); break;
+      case kBF16: ss = sum_chunk<kBF16, W, STORE>(cur, in, n, scale, policy, kept); break;
       case kFP16:
-        if (STORE && W != 1 && !sumsq && in_place(cur, in, n))  // left to the second pass
-          ss = sum_chunk<kFP16, W, false>(cur, in, n, scale, policy);
+        if (STORE && W != 1 && !kept && in_place(cur, in, n))  // left to the second pass
+          ss = sum_chunk<kFP16, W, false>(cur, in, n, scale, policy, kept);
         else
-          ss = sum_chunk<kFP16, W, STORE>(cur, in, n, scale, policy);
+          ss = sum_chunk<kFP16, W, STORE>(cur, in, n, scale, policy, kept);
         break;
-      default: ss = sum_chunk<kFP32, W, STORE>(cur, in, n, scale, policy); break;
+      default: ss = sum_chunk<kFP32, W, STORE>(cur, in, n, scale, policy, kept); break;
     }
     const double chunk = warp_sum(ss);
     if ((threadIdx.x & 31) == 0) total += chunk;

@@ -137,3 +137,40 @@ def test_captured_in_place(car):
                 torch.cuda.synchronize()
                 check(ranks[2], G, norm, max_norm, nb.item())
             del graph
+
+
+@pytest.mark.parametrize("W,offsets", [(1, None), (2, None), (2, [(0, 1), (0, 0)]), (5, None), (8, None)])
+@pytest.mark.parametrize("place", ["apart", "in place"])
+def test_stored_infinities_count_in_the_sum_of_squares(car, W, offsets, place):
+    """car_grads_reduce stores its sums, so one that is infinite in fp16 makes the sum of squares infinite too (it would
+    not tell otherwise of what car_grads_clip cannot bring back); 65519 is stored as 65504 and does not."""
+    sq = torch.empty(1, dtype=torch.float64, device=DEV)
+    for value in (65519.0, 65520.0, -65519.0, -65520.0, 1e18):
+        for at in (0, 4001, 4002):   # in a whole vector, in the tail, nowhere
+            ranks, outs, _ = make(W, [(4002, HF), (64, FP)], offsets, seed=2)
+            scale = 2 * abs(value)   # a half of it is exact
+            for r in range(W):
+                ranks[r][0].zero_()
+                ranks[r][1].div_(scale)
+            if at < 4002:
+                ranks[-1][0][at] = math.copysign(0.5, value)
+            G, norm = sums(ranks, scale)
+            outs = outs if place == "apart" else ranks[0]
+            with car.Grads(ranks, outs) as g:
+                g.reduce(scale, sq)
+                torch.cuda.synchronize()
+            assert torch.equal(outs[0], G[0].half()) and torch.equal(outs[1], G[1])
+            if at < 4002 and abs(value) >= 65520:
+                assert outs[0][at].isinf() and sq.item() == math.inf
+            else:
+                assert outs[0].isfinite().all() and abs(sq.item() - norm**2) <= 2.0**-17 * norm**2
+
+
+def test_a_nan_is_not_covered_by_an_infinity(car):
+    ranks, outs, _ = make(2, [(5000, HF)], None, seed=4)
+    ranks[0][0][17], ranks[1][0][4000] = math.nan, 6e4
+    sq = torch.empty(1, dtype=torch.float64, device=DEV)
+    with car.Grads(ranks, outs) as g:
+        g.reduce(4.0, sq)
+        torch.cuda.synchronize()
+    assert math.isnan(sq.item())
