@@ -323,6 +323,21 @@ def _stream(stream, device=None):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+@functools.lru_cache(maxsize=1)
+def _types():
+    """Types of the outputs that are not of the handle's own: q_out, scales by kind, dweight."""
+    import torch
+
+    f32 = (torch.float32,)
+    return ((torch.float8_e4m3fn, torch.uint8),
+            {k: (torch.uint8, torch.float8_e8m0fnu) if k == "mx32" else f32 for k in SCALE_CODE}, f32)
+
+
+def _check_type(t, allowed, what: str) -> None:
+    if t.dtype not in allowed:
+        raise ValueError(f"{what}: {t.dtype}, the call needs {' or '.join(str(d) for d in allowed)}")
+
+
 def _ptr(t, nbytes: int, what: str, device=None) -> int:
     """Device pointer of a tensor the library will read or write `nbytes` of:
     it must be a contiguous CUDA tensor at least that large, on `device` when
@@ -343,7 +358,8 @@ class Car:
 
     The methods take torch tensors and pass their device pointers to the C
     ABI; each tensor must be a contiguous CUDA tensor of at least the bytes
-    the call reads or writes (ValueError otherwise)."""
+    the call reads or writes (ValueError otherwise).  Tensors of the handle's
+    type are taken as bytes; those of another type are checked for it."""
 
     def __init__(self, W: int, M: int, N: int, dtype: str):
         st, h = car_create(W, M, N, DTYPE_CODE[dtype])
@@ -429,10 +445,14 @@ class Car:
     def reduce_residual_rmsnorm_quant(self, xs, residual, weight, eps, kind, residual_out, q_out, scales,
                                       norm_out=None, ar_out=None, stream=None):
         """kind: "row", "group128", "mx32" or "static" (see car_scale_kind).  q_out: M * N bytes (float8_e4m3fn or
-        uint8); scales: quant_scales_shape(kind), written, or read for "static"."""
+        uint8); scales: quant_scales_shape(kind), float32 (for "mx32" uint8 or float8_e8m0fnu), written, or read for
+        "static"."""
         code = SCALE_CODE.get(kind)
         if code is None:
             raise ValueError(f"kind: {kind!r} is none of {', '.join(SCALE_CODE)}")
+        q_types, scale_types, _ = _types()
+        _check_type(q_out, q_types, "q_out")
+        _check_type(scales, scale_types[kind], "scales")
         res, w, ro, q, sc, no, ar = self._ptrs(
             (residual, weight, residual_out, q_out, scales, norm_out, ar_out), self._quant_sizes[code],
             ("residual", "weight", "residual_out", "q_out", "scales", "norm_out", "ar_out"))
@@ -448,6 +468,8 @@ class Car:
                                          workspace=None, stream=None):
         """dresidual_out and dweight may be None; dweight is fp32.  With a dweight, workspace (backward_workspace_bytes
         bytes) is taken from torch's allocator on the current stream when none is given."""
+        if dweight is not None:
+            _check_type(dweight, _types()[2], "dweight")
         need = self._workspace_bytes if dweight is not None else 0
         if need and workspace is None:
             import torch
