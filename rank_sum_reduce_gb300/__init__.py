@@ -369,8 +369,7 @@ class Car:
         D, Nw = self.D, N * ELEM_SIZE[dtype]
         # bytes that the tensors of a call need, in the order of its arguments
         self._quant_sizes = [(D, Nw, D, M * N, car_quant_scale_bytes(h, k), D, D) for k in range(len(SCALE_CODE))]
-        self._workspace_bytes = car_backward_workspace_bytes(h)
-        self._backward_sizes = (D, Nw, D, D, 4 * N, self._workspace_bytes)
+        self._backward_sizes = None   # found when first asked for
         import torch
 
         self.device = torch.cuda.current_device()
@@ -462,7 +461,10 @@ class Car:
 
     @property
     def backward_workspace_bytes(self) -> int:
-        return self._workspace_bytes
+        if self._backward_sizes is None:
+            D, N = self.D, self.N
+            self._backward_sizes = (D, D // self.M, D, D, 4 * N, car_backward_workspace_bytes(self.h))
+        return self._backward_sizes[-1]
 
     def reduce_residual_rmsnorm_backward(self, dnorm, residual_out, weight, eps, dresidual_out, dx, dweight=None,
                                          workspace=None, stream=None):
@@ -470,7 +472,9 @@ class Car:
         bytes) is taken from torch's allocator on the current stream when none is given."""
         if dweight is not None:
             _check_type(dweight, _types()[2], "dweight")
-        need = self._workspace_bytes if dweight is not None else 0
+        need = self.backward_workspace_bytes
+        if dweight is None:
+            need = 0
         if need and workspace is None:
             import torch
 

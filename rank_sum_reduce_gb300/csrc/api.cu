@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -52,6 +53,10 @@ struct car_ctx {
   bool tma_ok;          // row fits the shared-memory ring of the pipelined kernel
   car::FusedTmaShape tma_auto;
   car::FusedTmaShape tma;
+  // The 8-bit output and the backward: found when first asked for, so that a
+  // handle that does without them pays nothing for them (see prepare_quant).
+  std::mutex shapes;
+  std::atomic<bool> quant_ready{false}, backward_ready{false};
   car::FusedShape quant;     // row kernel with an 8-bit output: the automatic shape, its own resident count
   car::TeamShape quant_tma;
   bool quant_pipeline;       // the 8-bit output runs the pipeline kernel
@@ -336,6 +341,62 @@ bool backward_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   return 2 * tiles >= (h->W > 8 ? 5 : 4) * sms;
 }
 
+// The handle's device as the current one while shapes are found for it.
+struct OnDevice {
+  int before = -1;
+  bool moved = false;
+  cudaError_t status;
+  explicit OnDevice(int device) {
+    status = cudaGetDevice(&before);
+    if (status != cudaSuccess || before == device) return;
+    status = cudaSetDevice(device);
+    moved = true;
+  }
+  ~OnDevice() {
+    if (moved) cudaSetDevice(before);
+  }
+};
+
+car_status prepare_quant(car_ctx* h) {
+  if (h->quant_ready.load(std::memory_order_acquire)) return CAR_OK;
+  std::lock_guard<std::mutex> lk(h->shapes);
+  if (h->quant_ready.load(std::memory_order_relaxed)) return CAR_OK;
+  const OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_fail(on.status, "device of the handle");
+  int groups = 0;
+  h->quant = auto_fused_shape(h->W, h->M, h->vec_per_row, h->num_sms);
+  cudaError_t e = car::fused_quant_resident_groups(h->dtype, h->W, h->quant, h->num_sms, &groups);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit output occupancy");
+  h->quant.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, std::max(groups, 1)));
+  h->quant_pipeline = car::quant_tma_shape(h->M, h->vec_per_row, h->num_sms, h->W, &h->quant_tma) &&
+                      quant_pipeline_pays(h, h->quant_tma);
+  if (h->quant_pipeline && (e = car::quant_tma_prepare(h->dtype, h->quant_tma)) != cudaSuccess)
+    return cuda_fail(e, "8-bit output pipeline smem");
+  h->quant_ready.store(true, std::memory_order_release);
+  return CAR_OK;
+}
+
+car_status prepare_backward(car_ctx* h) {
+  if (h->backward_ready.load(std::memory_order_acquire)) return CAR_OK;
+  std::lock_guard<std::mutex> lk(h->shapes);
+  if (h->backward_ready.load(std::memory_order_relaxed)) return CAR_OK;
+  const OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_fail(on.status, "device of the handle");
+  int groups = 0;
+  h->backward = row_split_shape(h->W, h->M, h->vec_per_row, h->num_sms, car::backward_has_variant, car::backward_max_threads, false);
+  cudaError_t e = car::backward_resident_groups(h->dtype, h->W, h->backward, h->num_sms, &groups);
+  if (e != cudaSuccess) return cuda_fail(e, "backward occupancy");
+  const int64_t teams = car::backward_teams(h->backward);
+  h->backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>((h->M + teams - 1) / teams, std::max(groups, 1)));
+  h->backward_pipeline = car::backward_tma_shape(h->dtype, h->M, h->vec_per_row, h->num_sms, h->W, &h->backward_tma) &&
+                         backward_pipeline_pays(h, h->backward_tma);
+  if (h->backward_pipeline && (e = car::backward_tma_prepare(h->dtype, h->backward_tma)) != cudaSuccess)
+    return cuda_fail(e, "backward pipeline smem");
+  h->backward_groups = h->backward_pipeline ? h->backward_tma.grid : h->backward.groups;
+  h->backward_ready.store(true, std::memory_order_release);
+  return CAR_OK;
+}
+
 car_status finish_fused_shape(car_ctx* h, car::FusedShape sh) {
   int groups = 0;
   cudaError_t e = car::fused_resident_groups(h->dtype, h->W, sh, h->num_sms, &groups);
@@ -497,28 +558,6 @@ car_status car_create(int W, int64_t M, int64_t N, car_dtype dtype, car_ctx** ou
       return st;
     }
     h->fused_auto = h->fused;
-  }
-
-  if (h->fused_ok) {
-    int groups = 0;
-    h->quant = auto_fused_shape(W, M, h->vec_per_row, h->num_sms);
-    if ((e = car::fused_quant_resident_groups(h->dtype, W, h->quant, h->num_sms, &groups)) != cudaSuccess)
-      return fail(e, "8-bit output occupancy");
-    h->quant.groups = (int)std::max<int64_t>(1, std::min<int64_t>(M, std::max(groups, 1)));
-    h->quant_pipeline = car::quant_tma_shape(M, h->vec_per_row, h->num_sms, W, &h->quant_tma) &&
-                        quant_pipeline_pays(h, h->quant_tma);
-    if (h->quant_pipeline && (e = car::quant_tma_prepare(h->dtype, h->quant_tma)) != cudaSuccess)
-      return fail(e, "8-bit output pipeline smem");
-    h->backward = row_split_shape(W, M, h->vec_per_row, h->num_sms, car::backward_has_variant, car::backward_max_threads, false);
-    if ((e = car::backward_resident_groups(h->dtype, W, h->backward, h->num_sms, &groups)) != cudaSuccess)
-      return fail(e, "backward occupancy");
-    const int64_t teams = car::backward_teams(h->backward);
-    h->backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>((M + teams - 1) / teams, std::max(groups, 1)));
-    h->backward_pipeline = car::backward_tma_shape(h->dtype, M, h->vec_per_row, h->num_sms, W, &h->backward_tma) &&
-                           backward_pipeline_pays(h, h->backward_tma);
-    if (h->backward_pipeline && (e = car::backward_tma_prepare(h->dtype, h->backward_tma)) != cudaSuccess)
-      return fail(e, "backward pipeline smem");
-    h->backward_groups = h->backward_pipeline ? h->backward_tma.grid : h->backward.groups;
   }
 
   h->lamport_ok = h->fused_ok && dtype == CAR_BF16;
@@ -706,6 +745,7 @@ car_status car_reduce_residual_rmsnorm_quant(car_ctx* h, const void* const* inpu
   if ((st = check_dev_elem(scales, kind == CAR_SCALE_MX32 ? 1 : 4)) != CAR_OK) return st;
   if ((norm_out && !aligned16(norm_out)) || (ar_out && !aligned16(ar_out))) return CAR_ERR_ALIGN;
   if (!h->fused_ok) return CAR_ERR_SIZE;
+  if ((st = prepare_quant(h)) != CAR_OK) return st;
   car::QuantOut out;
   out.q = static_cast<uint8_t*>(q_out);
   out.scales = scales;
@@ -723,7 +763,7 @@ car_status car_reduce_residual_rmsnorm_quant(car_ctx* h, const void* const* inpu
 }
 
 size_t car_backward_workspace_bytes(car_ctx* h) {
-  if (!live(h) || !h->fused_ok || h->backward_groups == 1) return 0;
+  if (!live(h) || !h->fused_ok || prepare_backward(h) != CAR_OK || h->backward_groups == 1) return 0;
   return (size_t)h->backward_groups * (size_t)h->N * sizeof(float);
 }
 
@@ -740,6 +780,7 @@ car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* d
   if ((st = check_dev(dx)) != CAR_OK) return st;
   if ((dresidual_out && !aligned16(dresidual_out)) || (dweight && !aligned16(dweight))) return CAR_ERR_ALIGN;
   if (!h->fused_ok) return CAR_ERR_SIZE;
+  if ((st = prepare_backward(h)) != CAR_OK) return st;
   if (dweight && h->backward_groups > 1 && (st = check_dev(workspace)) != CAR_OK) return st;
   float *dw = static_cast<float*>(dweight), *ws = static_cast<float*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
