@@ -102,13 +102,16 @@ def code_digest(texts):
     return h.hexdigest()[:16]
 
 
+KERNEL_SOURCES = ("fused_tma.cu", "ring.cuh", "car_device.cuh")
+
+
 def kernel_source_hash():
     """Digest of the dominant kernel's code: fused_tma.cu (the pipelined fused
-    kernel, its launch shape and launcher) and car_device.cuh (the device
-    helpers it is built with).  The key under which
+    kernel, its launch shape and launcher) and the headers with the device
+    helpers it is built with (KERNEL_SOURCES).  The key under which
     profiles/dram_traffic.json holds the ncu counters taken on that code."""
     texts = []
-    for f in ("fused_tma.cu", "car_device.cuh"):
+    for f in KERNEL_SOURCES:
         with open(os.path.join(ROOT, "rank_sum_reduce_gb300", "csrc", f)) as fh:
             texts.append(fh.read())
     return code_digest(texts)
