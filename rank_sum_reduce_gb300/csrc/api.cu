@@ -270,15 +270,16 @@ bool rows_compiled(int W) { return W <= 2 || W == 4 || W == 8 || W == 16; }
 //    fp32, N = 9000, M = 100, W = 1 4.0 / 5.6, W = 4 5.3 / 6.9, W = 8 9.0 / 9.0, M
 //    = 600 15.8 / 30, 25.6 / 39 and 36 / 54; with seven vectors per thread N =
 //    12800, M = 100, W = 1 5.0 / 6.0, W = 4 9.1 / 8.0, M = 304 18.9 / 22.9; bf16,
-//    N = 27000, M = 100 7.8 / 7.0, M = 304 16.8 / 20.6; with eight, N = 16384,
-//    fp32, M = 2000, W = 4 133 / 150, W = 8 221 / 202.
+//    N = 27000, M = 100 7.8 / 7.0, M = 304 16.8 / 20.6.  With eight (3600, 3900
+//    and 4096 vectors, fp32 and bf16, M from 152 to 2432) the quotient is 0.60
+//    to 0.85 for W = 1, 0.64 to 0.87 for 2, 0.75 to 1.00 for 4, 0.83 to 1.11
+//    (mean 0.97) for 8 and 0.80 to 0.96 for 16; at M = 100 0.92 to 1.26.
 //  * Rank counts that the row kernel is not compiled for: W = 6, N = 4096, M =
 //    4096 43 / 65; W = 3, N = 10000, M = 2000 40 / 118, N = 8192, M = 200 5.3 /
 //    7.1, N = 2048, M = 200 3.0 / 2.4.
 bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int64_t tiles = (h->M + sh.teams - 1) / sh.teams, sms = h->num_sms;
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
-  if (h->vec_per_row > 3584 && h->W == 8) return false;
   if (h->vec_per_row > 2048) return sh.vpt <= 6 ? 2 * tiles >= sms : tiles >= sms;
   if (h->vec_per_row > 1024) return 2 * tiles >= 3 * sms;
   if (h->W <= 2) {
@@ -311,17 +312,21 @@ bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
 //    13.2, M = 304 14.3 / 16.6; W = 16, N = 2048, M = 1200 19.3 / 18.9.
 //  * Rows of more than 1024 vectors, three per thread: W = 1, N = 11072, M = 304
 //    12.1 / 10.8, M = 608 16.1 / 17.6, M = 1737 31 / 42; N = 10488, W = 4, M = 200
-//    13.3 / 11.1, M = 304 13.9 / 14.6, M = 608 20 / 26.  Four: fp32 as three; in
-//    16 bits the accumulators leave little room, N = 13000, W = 2, M = 608 23.5 /
-//    21.6, W = 4, M = 608 29.1 / 27.8, M = 2000 73 / 77; N = 14336, W = 1, M =
-//    3000 86 / 75; N = 14000, W = 8, M = 608 40.5 / 44.1; N = 16384, W = 4, M =
-//    4000 180 / 148.  More, in fp32:
-//    N = 9000, M = 100, W = 2 6.9 / 7.6, W = 8 11.4 / 11.6, M = 600, W = 2 25.8 /
-//    36.0, W = 8 44 / 53; N = 11000, M = 3000, W = 1 103 / 152, W = 8 228 / 264.
-//    Seven vectors per thread: N = 12800, W = 1, M = 152 11.3 / 12.0, W = 2, M =
-//    600 37.7 / 35.9, W = 4, M = 2000 129 / 141, W = 8 181 / 172, but N = 14000, M
-//    = 1500 147 / 158.  Eight: N = 16384, W = 1, M = 600 40 / 36, M = 2000 110 /
-//    115, W = 4 165 / 145.
+//    13.3 / 11.1, M = 304 13.9 / 14.6, M = 608 20 / 26.  Four: fp32 as three.  In
+//    16 bits the accumulators leave little room, and from the 17th warp on one
+//    of the SM's four schedulers has five: W = 1, M = 2432, 1740 vectors (16
+//    warps) 61 / 63, 1800 vectors 72 / 63; W = 4 88 / 93 and 108 / 92.  Up to 16
+//    warps (1540, 1640 and 1740 vectors) the quotient is 1.01 to 1.13 for W = 1
+//    and 2 below M = 2432, 0.94 to 1.07 for W = 4 below M = 1216 and 0.91 to 1.00
+//    from there, 0.80 to 0.97 for W = 8 and 0.85 to 0.95 for W = 16 from M = 152.
+//    More, in fp32: N = 9000, M = 100, W = 2 6.9 / 7.6, W = 8 11.4 / 11.6, M =
+//    600, W = 2 25.8 / 36.0, W = 8 44 / 53; N = 11000, M = 3000, W = 1 103 / 152,
+//    W = 8 228 / 264.  Seven vectors per thread (3150, 3300 and 3400 vectors, M
+//    from 152 to 2432): 0.80 to 0.91 for W = 1, 0.87 to 0.99 for 2, 0.91 to 1.06
+//    for 4, 0.89 to 0.94 for 8, 0.68 to 1.01 for 16.  Eight (3600, 3900 and 4096,
+//    M = 1216 and 2432): 0.90 to 1.02 for W = 1, whose tile fits the ring whole,
+//    0.83 to 0.95 for W = 16, whose row kernel takes one vector per thread, 0.96
+//    to 1.15 for the others; below M = 1216 0.90 to 1.33.
 //  * Rank counts that the row kernel is not compiled for: W = 3, N = 10000, M =
 //    2000 56 / 127; W = 6, N = 16384 fp32, M = 500 62 / 80; W = 3, N = 8192, M =
 //    200 9.7 / 10.3.
@@ -330,10 +335,11 @@ bool backward_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int V = h->vec_per_row;
   const bool fp32 = h->dtype == CAR_FP32;
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
-  if (V > 3584) return h->W == 1 && tiles >= 8 * sms;
-  if (V > 3072) return tiles >= sms && (h->W != 8 || V > 3328);
+  if (V > 3584) return tiles >= 8 * sms && (sh.slots >= h->W + 2 || !car::backward_has_variant(h->W, 2));
+  if (V > 3072) return tiles >= sms;
   if (V > 2048) return 3 * tiles >= 2 * sms;
-  if (V > 1536) return fp32 ? tiles >= 2 * sms : V <= 1792 && h->W >= 4 && tiles >= (h->W < 8 ? 6 : 2) * sms;
+  if (V > 1536 && fp32) return tiles >= 2 * sms;
+  if (V > 1536) return sh.team_threads + 32 * sh.producers <= 512 && h->W >= 4 && tiles >= (h->W < 8 ? 6 : 1) * sms;
   if (V > 1024) return tiles >= (h->W <= 2 ? 3 : 2) * sms;
   if (h->W <= 2 && sh.teams == 1) return tiles >= (fp32 ? 4 : 6) * sms;
   if (h->W <= 2) return sh.vpt == 2 ? 2 * tiles >= sms : h->M >= 5 * sms;
