@@ -225,8 +225,12 @@ __device__ __forceinline__ Span span_of(const GradChunk& c) {
   return Span{head, vecs, c.count - head - vecs * E};
 }
 
-// Vectors per thread per iteration, for 8 to 32 loads in flight per thread
-// (as the plain rank sum).
+// Vectors per thread per iteration: 4 to 16 loads in flight per thread (4, 8,
+// 6, 8, then W).  Every rank count has its instance, compiled for as many CTAs
+// per SM as its registers allow without spills.  One that takes the count at
+// run time, a rank's four vectors at a time, is slower: W = 12, 32 M bf16 values
+// 187 against 130 us, W = 9 146 / 103, W = 5 70.5 / 68.2; 0.24 M, W = 12 7.7 /
+// 5.0, W = 5 5.5 / 4.1.
 template <int W>
 constexpr int kGradVectors = W >= 5 ? 1 : W >= 3 ? 2 : 4;
 
@@ -234,17 +238,16 @@ constexpr int kGradVectors = W >= 5 ? 1 : W >= 3 ? 2 : 4;
 // will have of a sum, so one that fp16 stores as infinity (from 65520 on, half
 // a step past its largest value) adds infinity.
 template <int DT, int W, bool STORE>
-__device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const* __restrict__ in, int n, float scale,
+__device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const* __restrict__ in, float scale,
                                            uint64_t policy, bool kept) {
   using S = Scalar<DT>;
   using T = typename S::T;
   constexpr int E = Pack<DT>::kN;
-  constexpr int R = W > 0 ? W : 1;
   constexpr int U = kGradVectors<W>;
   const Span sp = span_of<DT>(c);
-  const uint8_t* x[R];  // the whole vectors (of rank 0 where W is not compiled in)
+  const uint8_t* x[W];  // the whole vectors
 #pragma unroll
-  for (int r = 0; r < R; r++) x[r] = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
+  for (int r = 0; r < W; r++) x[r] = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
   T* out = static_cast<T*>(c.out);
   uint8_t* to = reinterpret_cast<uint8_t*>(out + sp.head);
   constexpr bool LOSES = DT == kFP16 && STORE;
@@ -254,33 +257,15 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
     // past the chunk's end the last vector is loaded again, and dropped below
     uint32_t at[U];
     float acc[U][E];
-    uint4 raw[U][R];
+    uint4 raw[U][W];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       at[u] = (uint32_t)min(v0 + u * kGradThreads, sp.vecs - 1) * 16u;
 #pragma unroll
-      for (int r = 0; r < R; r++) raw[u][r] = ld_hint<!STORE>(x[r] + at[u], policy);
+      for (int r = 0; r < W; r++) raw[u][r] = ld_hint<!STORE>(x[r] + at[u], policy);
     }
-    if constexpr (W > 0) {
 #pragma unroll
-      for (int u = 0; u < U; u++) rank_sum<DT, R>(raw[u], W, acc[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; u++) Pack<DT>::widen(raw[u][0], acc[u]);
-#pragma unroll 1
-      for (int r = 1; r < n; r++) {
-        const uint8_t* from = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
-#pragma unroll
-        for (int u = 0; u < U; u++) raw[u][0] = ld_hint<!STORE>(from + at[u], policy);
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-          float f[E];
-          Pack<DT>::widen(raw[u][0], f);
-#pragma unroll
-          for (int e = 0; e < E; e++) acc[u][e] = __fadd_rn(acc[u][e], f[e]);
-        }
-      }
-    }
+    for (int u = 0; u < U; u++) rank_sum<DT, W>(raw[u], W, acc[u]);
 #pragma unroll
     for (int u = 0; u < U; u++) {
       if (v0 + u * kGradThreads < sp.vecs) {
@@ -299,7 +284,7 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
   for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
     const int at = i < sp.head ? i : i + sp.vecs * E;
     float acc = S::up(static_cast<const T*>(in[0])[at]);
-    for (int r = 1; r < n; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(in[r])[at]));
+    for (int r = 1; r < W; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(in[r])[at]));
     acc = __fmul_rn(acc, scale);
     ss = fmaf(acc, acc, ss);
     if constexpr (LOSES) top = fmaxf(top, fabsf(acc));
@@ -500,20 +485,19 @@ __device__ __forceinline__ void prefetch_chunk(const GradChunk& c, const void* f
 }
 
 template <int W, bool STORE>
-__global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
+__global__ void __launch_bounds__(kGradThreads, W > 11 ? 2 : W > 8 ? 3 : 4)
     grads_reduce_kernel(const GradPlan p, const float scale, double* __restrict__ sumsq) {
   __shared__ double s_warp[kGradThreads / 32];
   __shared__ TotalShared s_total;
   __shared__ bool s_last;
-  const int n = W > 0 ? W : p.W;
   const uint64_t policy = read_policy(STORE && p.evict_first);
   const bool kept = sumsq != nullptr;  // else the second pass follows
-  const int first = blockIdx.x, last = p.reduce.n, stride = (int)sizeof(GradChunk) + 8 * n;
+  const int first = blockIdx.x, last = p.reduce.n, stride = (int)sizeof(GradChunk) + 8 * W;
   const GradChunk* d = chunk_at(p.reduce, stride, first);
   GradChunk c = {};
   if (first < last) {
     c = *d;
-    if ((int)threadIdx.x < n) prefetch_chunk(c, inputs_of(d)[threadIdx.x]);
+    if (threadIdx.x < W) prefetch_chunk(c, inputs_of(d)[threadIdx.x]);
   }
   pdl_wait_and_release();
   double total = 0.0;
@@ -526,14 +510,14 @@ __global__ void __launch_bounds__(kGradThreads, W == 16 ? 2 : W == 0 ? 3 : 4)
     }
     float ss;
     switch (cur.dtype) {
-      case kBF16: ss = sum_chunk<kBF16, W, STORE>(cur, in, n, scale, policy, kept); break;
+      case kBF16: ss = sum_chunk<kBF16, W, STORE>(cur, in, scale, policy, kept); break;
       case kFP16:
-        if (STORE && W != 1 && !kept && in_place(cur, in, n))  // left to the second pass
-          ss = sum_chunk<kFP16, W, false>(cur, in, n, scale, policy, kept);
+        if (STORE && W != 1 && !kept && in_place(cur, in, W))  // left to the second pass
+          ss = sum_chunk<kFP16, W, false>(cur, in, scale, policy, kept);
         else
-          ss = sum_chunk<kFP16, W, STORE>(cur, in, n, scale, policy, kept);
+          ss = sum_chunk<kFP16, W, STORE>(cur, in, scale, policy, kept);
         break;
-      default: ss = sum_chunk<kFP32, W, STORE>(cur, in, n, scale, policy, kept); break;
+      default: ss = sum_chunk<kFP32, W, STORE>(cur, in, scale, policy, kept); break;
     }
     const double chunk = warp_sum(ss);
     if ((threadIdx.x & 31) == 0) total += chunk;
@@ -633,10 +617,19 @@ GradsFn pick_grads(int W, bool store) {
     case 2: return grads_reduce_kernel<2, true>;
     case 3: return grads_reduce_kernel<3, true>;
     case 4: return grads_reduce_kernel<4, true>;
+    case 5: return grads_reduce_kernel<5, true>;
     case 6: return grads_reduce_kernel<6, true>;
+    case 7: return grads_reduce_kernel<7, true>;
     case 8: return grads_reduce_kernel<8, true>;
+    case 9: return grads_reduce_kernel<9, true>;
+    case 10: return grads_reduce_kernel<10, true>;
+    case 11: return grads_reduce_kernel<11, true>;
+    case 12: return grads_reduce_kernel<12, true>;
+    case 13: return grads_reduce_kernel<13, true>;
+    case 14: return grads_reduce_kernel<14, true>;
+    case 15: return grads_reduce_kernel<15, true>;
     case 16: return grads_reduce_kernel<16, true>;
-    default: return grads_reduce_kernel<0, true>;
+    default: return nullptr;
   }
 }
 
