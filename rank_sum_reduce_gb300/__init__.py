@@ -67,6 +67,7 @@ _SIGS = {
     "car_grads_reduce": (ctypes.c_int, [_vp, ctypes.c_float, _vp, _vp]),
     "car_grads_clip": (ctypes.c_int, [_vp, _vp, ctypes.c_float, _vp, _vp]),
     "car_grads_reduce_clip": (ctypes.c_int, [_vp, ctypes.c_float, ctypes.c_float, _vp, _vp]),
+    "car_grads_reduce_clip_once": (ctypes.c_int, [_vp, ctypes.c_float, ctypes.c_float, _vp, _vp]),
     "car_ll128_wire_bytes": (ctypes.c_size_t, [_vp]),
     "car_ll128_encode": (ctypes.c_int, [_vp, _vp, ctypes.c_uint64, _vp, _vp]),
     "car_ll128_decode_reduce": (ctypes.c_int, [_vp, _pvp, ctypes.c_uint64, ctypes.c_int, _vp, _vp]),
@@ -189,6 +190,10 @@ def car_grads_clip(g, sumsq: int, max_norm: float, norm_out: int | None, stream:
 
 def car_grads_reduce_clip(g, scale: float, max_norm: float, norm_out: int | None, stream: int = 0) -> int:
     return _lib.car_grads_reduce_clip(g, scale, max_norm, norm_out, stream)
+
+
+def car_grads_reduce_clip_once(g, scale: float, max_norm: float, norm_out: int | None, stream: int = 0) -> int:
+    return _lib.car_grads_reduce_clip_once(g, scale, max_norm, norm_out, stream)
 
 
 def car_ll128_wire_bytes(h) -> int:
@@ -622,8 +627,9 @@ class Grads:
                              self._scalar(norm_out, 4, "norm_out", self._f32) if norm_out is not None else None,
                              _stream(stream, self.device)), "car_grads_clip")
 
-    def reduce_clip(self, scale, max_norm, norm_out=None, stream=None):
-        """Both, for gradients that are all in this object."""
-        check(car_grads_reduce_clip(self.h, scale, max_norm,
-                                    self._scalar(norm_out, 4, "norm_out", self._f32) if norm_out is not None else None,
-                                    _stream(stream, self.device)), "car_grads_reduce_clip")
+    def reduce_clip(self, scale, max_norm, norm_out=None, stream=None, once=False):
+        """Both, for gradients that are all in this object.  once: no sum is rounded to its type before it is clipped,
+        at the cost of reading the ranks' 16-bit tensors again when it is."""
+        call = car_grads_reduce_clip_once if once else car_grads_reduce_clip
+        check(call(self.h, scale, max_norm, self._scalar(norm_out, 4, "norm_out", self._f32) if norm_out is not None else None,
+                   _stream(stream, self.device)), "car_grads_reduce_clip")

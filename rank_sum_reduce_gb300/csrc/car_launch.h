@@ -140,6 +140,7 @@ struct GradPlan {
   bool evict_first;       // the ranks' values give way to the outputs in L2
   bool pass_on;           // so do the clip's outputs, to what it has yet to read
   bool half_in_place;     // two and more ranks, and an fp16 output replaces an input
+  bool narrow_in_place;   // the same for an output of 16 bits
   double* partial;        // [grid]
   unsigned int* arrived;  // CTAs of the reduce that have written their partial
 };
@@ -147,14 +148,16 @@ struct GradPlan {
 enum class GradSource {
   kOutput,  // what the outputs hold
   kSums,    // the same, left there by the reduce of the same call, whose scale and inputs are at hand: for fp16
+  kOnce,    // 16-bit types: the sums formed again from the inputs; fp32: as kOutput
   kInput    // scale * the one rank's input
 };
 cudaError_t grads_occupancy(int W, bool store, int* reduce_per_sm);
-cudaError_t grads_clip_occupancy(GradSource from, int* per_sm);
-// store: write the sums (always with W > 1, but for fp16 in place of an input when sumsq is null); without,
-// launch_grads_clip takes the values from the input.  sumsq may be null; launch_grads_clip then adds
-// plan.partial[0 .. reduce's grid - 1] (sums, n_sums).
-cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s);
+cudaError_t grads_clip_occupancy(int W, GradSource from, int* per_sm);
+// store: write the sums (always with W > 1, but in place of an input for fp16 when sumsq is null, and for both 16-bit
+// types when `once` says that kOnce follows); without, launch_grads_clip takes the values from the input.  sumsq may be
+// null; launch_grads_clip then adds plan.partial[0 .. reduce's grid - 1] (sums, n_sums).
+cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, bool once, int grid,
+                                cudaStream_t s);
 cudaError_t launch_grads_clip(const GradPlan& plan, const double* sums, int n_sums, float scale, GradSource from,
                               float max_norm, float* norm_out, int grid, cudaStream_t s);
 

@@ -18,6 +18,13 @@
 // that a clipped step moves 3 tensors' bytes instead of 4 (and rounds once),
 // and one in place that needs no clipping moves 1.
 //
+// Where every value has to be rounded once (car_grads_reduce_clip_once), the
+// second pass adds the ranks' 16-bit tensors again, if there is anything to
+// clip: 64 M bf16 values, W = 4, clipped 187 us against 131, W = 8 347 against
+// 218.  The first pass then reads without the hint below, since what L2 keeps of
+// the ranks is of use too, and what it costs where nothing is clipped falls
+// away (W = 4 94 against 101 us).
+//
 // Work is cut into chunks of one tensor each, all of about the same length; a
 // wave of CTAs takes them in order, the second pass in the opposite order, the
 // last written first: what the first pass left in L2 (129 MB) is read from
@@ -234,12 +241,24 @@ __device__ __forceinline__ Span span_of(const GradChunk& c) {
 template <int W>
 constexpr int kGradVectors = W >= 5 ? 1 : W >= 3 ? 2 : 4;
 
+// CTAs per SM that the instances for W ranks are compiled for.
+template <int W>
+constexpr int kGradMinCtas = W > 11 ? 2 : W > 8 ? 3 : 4;
+
+// What a pass does with a chunk's sums G.
+enum class SumUse {
+  kSquare,  // adds their squares
+  kStore,   // and stores them
+  kClip     // stores G * coef
+};
+
 // Squares of the unrounded sums.  kept: what is stored is all that the caller
 // will have of a sum, so one that fp16 stores as infinity (from 65520 on, half
 // a step past its largest value) adds infinity.
-template <int DT, int W, bool STORE>
+template <int DT, int W, SumUse USE>
 __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const* __restrict__ in, float scale,
-                                           uint64_t policy, bool kept) {
+                                           uint64_t policy, bool kept, float coef = 1.f) {
+  constexpr bool STORE = USE != SumUse::kSquare, CLIP = USE == SumUse::kClip;
   using S = Scalar<DT>;
   using T = typename S::T;
   constexpr int E = Pack<DT>::kN;
@@ -250,7 +269,7 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
   for (int r = 0; r < W; r++) x[r] = static_cast<const uint8_t*>(in[r]) + sp.head * sizeof(T);
   T* out = static_cast<T*>(c.out);
   uint8_t* to = reinterpret_cast<uint8_t*>(out + sp.head);
-  constexpr bool LOSES = DT == kFP16 && STORE;
+  constexpr bool LOSES = DT == kFP16 && USE == SumUse::kStore;
   float ss = 0.f, top = 0.f;
 #pragma unroll 1
   for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
@@ -272,7 +291,10 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
 #pragma unroll
         for (int e = 0; e < E; e++) {
           acc[u][e] = __fmul_rn(acc[u][e], scale);
-          ss = fmaf(acc[u][e], acc[u][e], ss);
+          if constexpr (CLIP)
+            acc[u][e] = __fmul_rn(acc[u][e], coef);
+          else
+            ss = fmaf(acc[u][e], acc[u][e], ss);
           if constexpr (LOSES) top = fmaxf(top, fabsf(acc[u][e]));
         }
         if constexpr (STORE) st16(to + at[u], Pack<DT>::narrow(acc[u]));
@@ -286,7 +308,10 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
     float acc = S::up(static_cast<const T*>(in[0])[at]);
     for (int r = 1; r < W; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(in[r])[at]));
     acc = __fmul_rn(acc, scale);
-    ss = fmaf(acc, acc, ss);
+    if constexpr (CLIP)
+      acc = __fmul_rn(acc, coef);
+    else
+      ss = fmaf(acc, acc, ss);
     if constexpr (LOSES) top = fmaxf(top, fabsf(acc));
     if constexpr (STORE) out[at] = S::down(acc);
   }
@@ -485,12 +510,12 @@ __device__ __forceinline__ void prefetch_chunk(const GradChunk& c, const void* f
 }
 
 template <int W, bool STORE>
-__global__ void __launch_bounds__(kGradThreads, W > 11 ? 2 : W > 8 ? 3 : 4)
-    grads_reduce_kernel(const GradPlan p, const float scale, double* __restrict__ sumsq) {
+__global__ void __launch_bounds__(kGradThreads, kGradMinCtas<W>)
+    grads_reduce_kernel(const GradPlan p, const float scale, double* __restrict__ sumsq, const bool once) {
   __shared__ double s_warp[kGradThreads / 32];
   __shared__ TotalShared s_total;
   __shared__ bool s_last;
-  const uint64_t policy = read_policy(STORE && p.evict_first);
+  const uint64_t policy = read_policy(STORE && p.evict_first && !once);
   const bool kept = sumsq != nullptr;  // else the second pass follows
   const int first = blockIdx.x, last = p.reduce.n, stride = (int)sizeof(GradChunk) + 8 * W;
   const GradChunk* d = chunk_at(p.reduce, stride, first);
@@ -500,6 +525,7 @@ __global__ void __launch_bounds__(kGradThreads, W > 11 ? 2 : W > 8 ? 3 : 4)
     if (threadIdx.x < W) prefetch_chunk(c, inputs_of(d)[threadIdx.x]);
   }
   pdl_wait_and_release();
+  constexpr SumUse USE = STORE ? SumUse::kStore : SumUse::kSquare;
   double total = 0.0;
   for (int i = first; i < last; i += gridDim.x) {
     const void* const* in = inputs_of(d);
@@ -510,14 +536,19 @@ __global__ void __launch_bounds__(kGradThreads, W > 11 ? 2 : W > 8 ? 3 : 4)
     }
     float ss;
     switch (cur.dtype) {
-      case kBF16: ss = sum_chunk<kBF16, W, STORE>(cur, in, scale, policy, kept); break;
-      case kFP16:
-        if (STORE && W != 1 && !kept && in_place(cur, in, W))  // left to the second pass
-          ss = sum_chunk<kFP16, W, false>(cur, in, scale, policy, kept);
+      case kBF16:
+        if (STORE && W != 1 && once && in_place(cur, in, W))  // left to the second pass
+          ss = sum_chunk<kBF16, W, SumUse::kSquare>(cur, in, scale, policy, kept);
         else
-          ss = sum_chunk<kFP16, W, STORE>(cur, in, scale, policy, kept);
+          ss = sum_chunk<kBF16, W, USE>(cur, in, scale, policy, kept);
         break;
-      default: ss = sum_chunk<kFP32, W, STORE>(cur, in, scale, policy, kept); break;
+      case kFP16:
+        if (STORE && W != 1 && !kept && in_place(cur, in, W))  // so is this one
+          ss = sum_chunk<kFP16, W, SumUse::kSquare>(cur, in, scale, policy, kept);
+        else
+          ss = sum_chunk<kFP16, W, USE>(cur, in, scale, policy, kept);
+        break;
+      default: ss = sum_chunk<kFP32, W, USE>(cur, in, scale, policy, kept); break;
     }
     const double chunk = warp_sum(ss);
     if ((threadIdx.x & 31) == 0) total += chunk;
@@ -543,21 +574,22 @@ __global__ void __launch_bounds__(kGradThreads, W > 11 ? 2 : W > 8 ? 3 : 4)
   }
 }
 
-// FROM: where the values come from (car_launch.h).
-template <GradSource FROM>
-__global__ void __launch_bounds__(kGradThreads, 4)
+// FROM: where the values come from (car_launch.h); W: the ranks for kOnce.
+template <GradSource FROM, int W>
+__global__ void __launch_bounds__(kGradThreads, kGradMinCtas<W>)
     grads_clip_kernel(const GradPlan p, const double* __restrict__ sums, const int n_sums, const float scale,
                       const float max_norm, float* __restrict__ norm_out) {
   constexpr bool FROM_INPUT = FROM == GradSource::kInput;
   __shared__ TotalShared s_total;
   const uint64_t policy = read_policy(p.pass_on);
   const int stride = (int)sizeof(GradChunk) + 8 * p.W;
-  int i = p.clip.n - 1 - (int)blockIdx.x;
+  const GradList& list = FROM == GradSource::kOnce ? p.reduce : p.clip;  // (it reads what the reduce does)
+  int i = list.n - 1 - (int)blockIdx.x;
   GradChunk c = {};
   const GradChunk* d = nullptr;
   const void* from = nullptr;
   if (i >= 0) {
-    d = chunk_at(p.clip, stride, i);
+    d = chunk_at(list, stride, i);
     c = *d;
     from = FROM_INPUT ? inputs_of(d)[0] : c.out;
   }
@@ -571,27 +603,40 @@ __global__ void __launch_bounds__(kGradThreads, 4)
   const float ratio = __fdiv_rn(max_norm, norm + 1e-6f);
   // within the limit, or no limit (false for a NaN norm, which then reaches every value)
   const bool whole = ratio >= 1.f || isinf(max_norm);
-  if (whole && !FROM_INPUT && !(FROM == GradSource::kSums && p.half_in_place)) return;
+  const bool unsummed = FROM == GradSource::kOnce ? p.narrow_in_place : FROM == GradSource::kSums && p.half_in_place;
+  if (whole && !FROM_INPUT && !unsummed) return;
   const float coef = whole ? 1.f : ratio;
   for (; i >= 0; i -= (int)gridDim.x) {
     const GradChunk cur = c;
     const void* const* in = inputs_of(d);
     const void* x = from;
     if (i >= (int)gridDim.x) {
-      d = chunk_at(p.clip, stride, i - (int)gridDim.x);
+      d = chunk_at(list, stride, i - (int)gridDim.x);
       c = *d;
       from = FROM_INPUT ? inputs_of(d)[0] : c.out;
     }
     if (FROM_INPUT && x == cur.out && whole && scale == 1.f) continue;  // already there
     if (FROM == GradSource::kSums && cur.dtype == kFP16) {
-      if (p.half_in_place && in_place(cur, in, p.W))
+      if (unsummed && in_place(cur, in, p.W))
         sum_clip_half_chunk(cur, in, p.W, scale, coef, policy);
       else if (!whole)
         clip_half_chunk(cur, in, p.W, scale, coef, policy);
       continue;
     }
-    if (FROM == GradSource::kSums && whole) continue;
+    if (FROM == GradSource::kOnce && cur.dtype != kFP32) {
+      if (whole && !in_place(cur, in, W)) continue;
+      if (cur.dtype == kBF16)
+        sum_chunk<kBF16, W, SumUse::kClip>(cur, in, scale, policy, false, coef);
+      else
+        sum_chunk<kFP16, W, SumUse::kClip>(cur, in, scale, policy, false, coef);
+      continue;
+    }
+    if (!FROM_INPUT && whole) continue;
     const float once = FROM_INPUT ? scale : 1.f;  // what out holds is scaled
+    if (FROM == GradSource::kOnce) {
+      clip_chunk<kFP32>(cur, x, once, coef, policy);
+      continue;
+    }
     switch (cur.dtype) {
       case kBF16: clip_chunk<kBF16>(cur, x, once, coef, policy); break;
       case kFP16: clip_chunk<kFP16>(cur, x, once, coef, policy); break;
@@ -601,15 +646,34 @@ __global__ void __launch_bounds__(kGradThreads, 4)
 }
 
 using ClipFn = void (*)(const GradPlan, const double*, const int, const float, const float, float*);
-ClipFn pick_clip(GradSource from) {
+ClipFn pick_clip(int W, GradSource from) {
   switch (from) {
-    case GradSource::kOutput: return grads_clip_kernel<GradSource::kOutput>;
-    case GradSource::kSums: return grads_clip_kernel<GradSource::kSums>;
-    default: return grads_clip_kernel<GradSource::kInput>;
+    case GradSource::kOutput: return grads_clip_kernel<GradSource::kOutput, 1>;
+    case GradSource::kSums: return grads_clip_kernel<GradSource::kSums, 1>;
+    case GradSource::kInput: return grads_clip_kernel<GradSource::kInput, 1>;
+    case GradSource::kOnce: break;
+  }
+  switch (W) {
+    case 2: return grads_clip_kernel<GradSource::kOnce, 2>;
+    case 3: return grads_clip_kernel<GradSource::kOnce, 3>;
+    case 4: return grads_clip_kernel<GradSource::kOnce, 4>;
+    case 5: return grads_clip_kernel<GradSource::kOnce, 5>;
+    case 6: return grads_clip_kernel<GradSource::kOnce, 6>;
+    case 7: return grads_clip_kernel<GradSource::kOnce, 7>;
+    case 8: return grads_clip_kernel<GradSource::kOnce, 8>;
+    case 9: return grads_clip_kernel<GradSource::kOnce, 9>;
+    case 10: return grads_clip_kernel<GradSource::kOnce, 10>;
+    case 11: return grads_clip_kernel<GradSource::kOnce, 11>;
+    case 12: return grads_clip_kernel<GradSource::kOnce, 12>;
+    case 13: return grads_clip_kernel<GradSource::kOnce, 13>;
+    case 14: return grads_clip_kernel<GradSource::kOnce, 14>;
+    case 15: return grads_clip_kernel<GradSource::kOnce, 15>;
+    case 16: return grads_clip_kernel<GradSource::kOnce, 16>;
+    default: return nullptr;
   }
 }
 
-using GradsFn = void (*)(const GradPlan, const float, double*);
+using GradsFn = void (*)(const GradPlan, const float, double*, const bool);
 GradsFn pick_grads(int W, bool store) {
   if (!store) return W == 1 ? grads_reduce_kernel<1, false> : nullptr;
   switch (W) {
@@ -640,19 +704,22 @@ cudaError_t grads_occupancy(int W, bool store, int* reduce_per_sm) {
       reduce_per_sm, reinterpret_cast<const void*>(pick_grads(W, store)), kGradThreads, 0);
 }
 
-cudaError_t grads_clip_occupancy(GradSource from, int* per_sm) {
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, reinterpret_cast<const void*>(pick_clip(from)), kGradThreads, 0);
+cudaError_t grads_clip_occupancy(int W, GradSource from, int* per_sm) {
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, reinterpret_cast<const void*>(pick_clip(W, from)), kGradThreads, 0);
 }
 
-cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, int grid, cudaStream_t s) {
+cudaError_t launch_grads_reduce(const GradPlan& plan, float scale, bool store, double* sumsq, bool once, int grid,
+                                cudaStream_t s) {
   GradsFn fn = pick_grads(plan.W, store);
   if (!fn) return cudaErrorInvalidValue;
-  return launch_pdl(fn, (unsigned)grid, kGradThreads, 0, s, 1, plan, scale, sumsq);
+  return launch_pdl(fn, (unsigned)grid, kGradThreads, 0, s, 1, plan, scale, sumsq, once);
 }
 
 cudaError_t launch_grads_clip(const GradPlan& plan, const double* sums, int n_sums, float scale, GradSource from,
                               float max_norm, float* norm_out, int grid, cudaStream_t s) {
-  return launch_pdl(pick_clip(from), (unsigned)grid, kGradThreads, 0, s, 1, plan, sums, n_sums, scale, max_norm, norm_out);
+  ClipFn fn = pick_clip(plan.W, from);
+  if (!fn) return cudaErrorInvalidValue;
+  return launch_pdl(fn, (unsigned)grid, kGradThreads, 0, s, 1, plan, sums, n_sums, scale, max_norm, norm_out);
 }
 
 }  // namespace car

@@ -19,6 +19,7 @@
 struct car_grads {
   int device;
   int grid, sums_grid;  // of car_grads_reduce_clip's two passes
+  int once_grid;        // of car_grads_reduce_clip_once's second pass
   int clip_grid;        // of car_grads_clip
   int store_grid;       // of car_grads_reduce: with one rank another kernel than the first pass's
   void* memory;  // one allocation: chunks, partials, counter
@@ -108,24 +109,28 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   car_status st = check_overlap(W, n, bytes, inputs, outs);
   if (st != CAR_OK) return st;
 
-  bool half = false, half_in_place = false;
+  bool half = false, half_in_place = false, narrow_in_place = false;
   for (int64_t k = 0; k < W * n && W > 1; k++) {
-    const bool is_half = dtypes[k % n] == CAR_FP16 && bytes[k % n];
+    const int64_t t = k % n;
+    if (!bytes[t]) continue;
+    const bool is_half = dtypes[t] == CAR_FP16, replaced = inputs[k] == outs[t];
     half = half || is_half;
-    half_in_place = half_in_place || (is_half && inputs[k] == outs[k % n]);
+    half_in_place = half_in_place || (is_half && replaced);
+    narrow_in_place = narrow_in_place || (dtypes[t] != CAR_FP32 && replaced);
   }
   // (kSums with nothing to add again is slower: W = 2, 64 M bf16 values 92.9
   // against 90.1 us.)
   const car::GradSource source = W == 1 ? car::GradSource::kInput : half ? car::GradSource::kSums : car::GradSource::kOutput;
 
-  int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_sums = 0, per_clip = 0, per_store = 0;
+  int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_sums = 0, per_once = 0, per_clip = 0, per_store = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, device);
   if (e == cudaSuccess) e = car::grads_occupancy(W, W > 1, &per_reduce);
   if (e == cudaSuccess) e = car::grads_occupancy(W, true, &per_store);
-  if (e == cudaSuccess) e = car::grads_clip_occupancy(source, &per_sums);
-  if (e == cudaSuccess) e = car::grads_clip_occupancy(car::GradSource::kOutput, &per_clip);
+  if (e == cudaSuccess) e = car::grads_clip_occupancy(W, source, &per_sums);
+  if (e == cudaSuccess && W > 1) e = car::grads_clip_occupancy(W, car::GradSource::kOnce, &per_once);
+  if (e == cudaSuccess) e = car::grads_clip_occupancy(W, car::GradSource::kOutput, &per_clip);
   if (e != cudaSuccess) return fail(e, "gradient launch sizes");
   const int64_t reduce_cap = std::min<int64_t>((int64_t)std::max(1, per_reduce) * num_sms, car::kMaxGradCtas);
   const size_t stride = sizeof(car::GradChunk) + (size_t)W * sizeof(void*);
@@ -169,8 +174,9 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   const int64_t n_clip = W >= 8 ? cut(car::kGradChunkVecs) : n_reduce;
   const int grid = (int)std::max<int64_t>(1, std::min(n_reduce, reduce_cap));
   const int store_grid = (int)std::min<int64_t>(grid, (int64_t)std::max(1, per_store) * num_sms);
-  const int sums_grid = (int)std::max<int64_t>(1, std::min<int64_t>(n_clip, (int64_t)std::max(1, per_sums) * num_sms));
-  const int clip_grid = (int)std::max<int64_t>(1, std::min<int64_t>(n_clip, (int64_t)std::max(1, per_clip) * num_sms));
+  auto wave = [&](int64_t chunks, int per_sm) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)std::max(1, per_sm) * num_sms));
+  };
   const size_t cb = chunks.size(), pb = (size_t)grid * sizeof(double);
   void* memory = nullptr;
   e = cudaMalloc(&memory, cb + pb + 8);
@@ -186,9 +192,10 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   }
   g->device = device;
   g->grid = grid;
-  g->sums_grid = sums_grid;
+  g->sums_grid = wave(n_clip, per_sums);
+  g->once_grid = wave(n_reduce, per_once);
   g->source = source;
-  g->clip_grid = clip_grid;
+  g->clip_grid = wave(n_clip, per_clip);
   g->store_grid = store_grid;
   g->memory = memory;
   g->plan.reduce = car::GradList{m, (int)n_reduce};
@@ -197,6 +204,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   g->plan.evict_first = 16 * vecs < 2 * (int64_t)l2;
   g->plan.pass_on = 16 * vecs > (int64_t)l2 / 4;
   g->plan.half_in_place = half_in_place;
+  g->plan.narrow_in_place = narrow_in_place;
   g->plan.partial = reinterpret_cast<double*>(m + cb);
   g->plan.arrived = reinterpret_cast<unsigned int*>(m + cb + pb);
   {
@@ -240,7 +248,7 @@ car_status car_grads_reduce(car_grads* g, float scale, double* sumsq, void* stre
   if (st != CAR_OK) return st;
   if (!sumsq || !std::isfinite(scale)) return CAR_ERR_ARG;
   if (!aligned(sumsq, 8)) return CAR_ERR_ALIGN;
-  cudaError_t e = car::launch_grads_reduce(g->plan, scale, true, sumsq, g->store_grid, static_cast<cudaStream_t>(stream));
+  cudaError_t e = car::launch_grads_reduce(g->plan, scale, true, sumsq, false, g->store_grid, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_reduce launch");
 }
 
@@ -254,18 +262,27 @@ car_status car_grads_clip(car_grads* g, const double* sumsq, float max_norm, flo
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_clip launch");
 }
 
-car_status car_grads_reduce_clip(car_grads* g, float scale, float max_norm, float* norm_out, void* stream) {
+static car_status reduce_clip(car_grads* g, float scale, float max_norm, float* norm_out, bool once, void* stream) {
   car_status st = check(g);
   if (st != CAR_OK) return st;
   if (!std::isfinite(scale) || !(max_norm >= 0.f)) return CAR_ERR_ARG;
   if (!aligned(norm_out, 4)) return CAR_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool one = g->plan.W == 1;  // the first pass then only reads (see grads.cu)
-  cudaError_t e = car::launch_grads_reduce(g->plan, scale, !one, nullptr, g->grid, s);
+  once = once && !one;  // one rank's values are rounded once as it is
+  cudaError_t e = car::launch_grads_reduce(g->plan, scale, !one, nullptr, once, g->grid, s);
   if (e == cudaSuccess)
-    e = car::launch_grads_clip(g->plan, g->plan.partial, g->grid, scale, g->source,
-                               max_norm, norm_out, g->sums_grid, s);
+    e = car::launch_grads_clip(g->plan, g->plan.partial, g->grid, scale, once ? car::GradSource::kOnce : g->source, max_norm,
+                               norm_out, once ? g->once_grid : g->sums_grid, s);
   return e == cudaSuccess ? CAR_OK : fail(e, "grads_reduce_clip launch");
+}
+
+car_status car_grads_reduce_clip(car_grads* g, float scale, float max_norm, float* norm_out, void* stream) {
+  return reduce_clip(g, scale, max_norm, norm_out, false, stream);
+}
+
+car_status car_grads_reduce_clip_once(car_grads* g, float scale, float max_norm, float* norm_out, void* stream) {
+  return reduce_clip(g, scale, max_norm, norm_out, true, stream);
 }
 
 }  // extern "C"
