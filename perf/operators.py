@@ -241,7 +241,7 @@ def run(state):
     if not own:
         return _plain_norm8(s) if op == "norm8" else _plain_normgrad(s) if op == "normgrad" else _plain_grads(s)
     if op == "grads":
-        s["grads"].reduce_clip(s["scale"], s["max_norm"], s["norm"])
+        s["grads"].reduce_clip(s["scale"], s["max_norm"], s["norm"], once=True)
         return {"norm": s["norm"], "grads": [b["out"] for b in s["buckets"]]}
     if op == "normgrad":
         s["car"].reduce_residual_rmsnorm_backward(s["ranks"], s["h"], s["weight"], s["eps"], s["dres"], s["dx"],
