@@ -78,7 +78,7 @@ cudaError_t launch_fused_tma(int dtype, int W, const RankPtrs& in, const void* r
 
 // ---- pipeline kernels whose CTAs work on several rows at a time ----
 struct TeamShape {
-  int vpt;           // 16-byte vectors per consumer thread (2, 3, 4, 8)
+  int vpt;           // 16-byte vectors per consumer thread (2 to 8)
   double use;        // share of 512 threads' places that hold a vector of a row
   int producers;     // threads that issue the bulk copies
   int team_threads;  // consumer threads of a row

@@ -84,7 +84,8 @@ constexpr int max_threads() {
 
 // MINB: CTAs per SM the instance is compiled for.  W = 8 with one vector per
 // thread has a second instance held to two 512-thread CTAs per SM (64
-// registers, no spills) for one CTA per row over many rows, where a second
+// registers; no spills, but 32 bytes in the 16-bit instances with an 8-bit
+// output) for one CTA per row over many rows, where a second
 // resident row pays: N = 4096 bf16, M = 256 5.40 -> 4.70 us, M = 1024 15.5 ->
 // 14.7 us.  Split rows keep the unbounded instance, whose latency is lower
 // (W = 8, M = 1, N = 8192: 1.92 against 2.02 us).

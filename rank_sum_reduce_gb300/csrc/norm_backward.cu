@@ -84,7 +84,9 @@ __device__ __forceinline__ void team_barrier(int team, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
 }
 
-// CTAs per SM that an instance is compiled for.
+// CTAs per SM that an instance is compiled for.  The ones held to two spill up
+// to 32 bytes, and with eight ranks and two vectors per thread, where 16 loaded
+// vectors, g and the weight gradient share 128 registers, 32 (fp32) to 156.
 template <int W, int VPT>
 constexpr int kBackwardMinCtas = VPT == 1 && (W == 1 || W == 2) ? 2 : 1;
 

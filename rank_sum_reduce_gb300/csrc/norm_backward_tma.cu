@@ -140,7 +140,9 @@ __device__ __forceinline__ int weight_row_bytes(int row_bytes) {
 // hold: in 16 bits the accumulators leave little room to overlap (N = 4400:
 // 36.3).  Five to eight above that, as few as 512 threads need (W = 1, M = 3000,
 // N = 9000: five 81 us, six 98, eight 115), in fp32 alone: more than four
-// 16-bit vectors' accumulators would not fit in registers.
+// 16-bit vectors' accumulators would not fit in registers.  Of 96, which leave
+// room for a CTA of 18 warps, four 16-bit vectors spill 36 bytes, six, seven and
+// eight fp32 ones 28, 52 and 340.
 template <int DT, int VPT>
 __device__ __forceinline__ void consume(const BackwardTmaParams& p, uint8_t* ring, const uint8_t* s_weight, uint64_t* full,
                                         uint64_t* empty, uint64_t* rowbar, uint64_t* done, float2* s_warp,

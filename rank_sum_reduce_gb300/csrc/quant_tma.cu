@@ -20,7 +20,10 @@
 // 1500, N = 5000 31.7 against 25.7, four 27.5).  Rows of more than 2048 vectors
 // take five to eight, as few as 512 threads need (W = 1, M = 2000, N = 20000
 // bf16: five 52 us, six 65, eight 78), the weight read from L2 once per row (64
-// KB of it beside the ring would leave two slots).
+// KB of it beside the ring would leave two slots).  The instances for six, seven
+// and eight 16-bit vectors spill 24 to 116 bytes (96 registers).  A
+// thread's squares are then up to 32 fmas in a row, with 10 levels of additions
+// behind them (the halves', a warp's, 16 warps').
 #include "car_launch.h"
 #include "quant.cuh"
 #include "ring.cuh"
