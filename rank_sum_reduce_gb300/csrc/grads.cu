@@ -20,10 +20,10 @@
 //
 // Where every value has to be rounded once (car_grads_reduce_clip_once), the
 // second pass adds the ranks' 16-bit tensors again, if there is anything to
-// clip: 64 M bf16 values, W = 4, clipped 187 us against 131, W = 8 347 against
-// 218.  The first pass then reads without the hint below, since what L2 keeps of
-// the ranks is of use too, and what it costs where nothing is clipped falls
-// away (W = 4 94 against 101 us).
+// clip: 64 M bf16 values, W = 4, clipped 182 us against 131, W = 8 329 against
+// 218.  Both passes then read without the hints below, since what L2 keeps of
+// the ranks is of use too (with them 192 and 355 us), and what they cost where
+// nothing is clipped falls away (W = 4 94 against 101 us).
 //
 // Work is cut into chunks of one tensor each, all of about the same length; a
 // wave of CTAs takes them in order, the second pass in the opposite order, the
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradMinCtas<W>)
                       const float max_norm, float* __restrict__ norm_out) {
   constexpr bool FROM_INPUT = FROM == GradSource::kInput;
   __shared__ TotalShared s_total;
-  const uint64_t policy = read_policy(p.pass_on);
+  const uint64_t policy = read_policy(FROM != GradSource::kOnce && p.pass_on);
   const int stride = (int)sizeof(GradChunk) + 8 * p.W;
   const GradList& list = FROM == GradSource::kOnce ? p.reduce : p.clip;  // (it reads what the reduce does)
   int i = list.n - 1 - (int)blockIdx.x;

@@ -20,6 +20,7 @@ struct car_grads {
   int device;
   int grid, sums_grid;  // of car_grads_reduce_clip's two passes
   int once_grid;        // of car_grads_reduce_clip_once's second pass
+  bool twice;           // a clipped value of car_grads_reduce_clip may be rounded twice
   int clip_grid;        // of car_grads_clip
   int store_grid;       // of car_grads_reduce: with one rank another kernel than the first pass's
   void* memory;  // one allocation: chunks, partials, counter
@@ -109,12 +110,13 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   car_status st = check_overlap(W, n, bytes, inputs, outs);
   if (st != CAR_OK) return st;
 
-  bool half = false, half_in_place = false, narrow_in_place = false;
+  bool half = false, half_in_place = false, narrow = false, narrow_in_place = false;
   for (int64_t k = 0; k < W * n && W > 1; k++) {
     const int64_t t = k % n;
     if (!bytes[t]) continue;
     const bool is_half = dtypes[t] == CAR_FP16, replaced = inputs[k] == outs[t];
     half = half || is_half;
+    narrow = narrow || dtypes[t] != CAR_FP32;
     half_in_place = half_in_place || (is_half && replaced);
     narrow_in_place = narrow_in_place || (dtypes[t] != CAR_FP32 && replaced);
   }
@@ -195,6 +197,7 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
   g->sums_grid = wave(n_clip, per_sums);
   g->once_grid = wave(n_reduce, per_once);
   g->source = source;
+  g->twice = narrow;
   g->clip_grid = wave(n_clip, per_clip);
   g->store_grid = store_grid;
   g->memory = memory;
@@ -269,7 +272,7 @@ static car_status reduce_clip(car_grads* g, float scale, float max_norm, float* 
   if (!aligned(norm_out, 4)) return CAR_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool one = g->plan.W == 1;  // the first pass then only reads (see grads.cu)
-  once = once && !one;  // one rank's values are rounded once as it is
+  once = once && g->twice;  // one rank's values are rounded once as it is, and fp32 sums not at all
   cudaError_t e = car::launch_grads_reduce(g->plan, scale, !one, nullptr, once, g->grid, s);
   if (e == cudaSuccess)
     e = car::launch_grads_clip(g->plan, g->plan.partial, g->grid, scale, once ? car::GradSource::kOnce : g->source, max_norm,
