@@ -11,12 +11,12 @@
 // (what calling a reduce and then a clip would give) and keeps the second
 // pass at one read and one write of the tensors.  Only where that rounding would
 // lose the value is it not kept: an fp16 sum past 65504 is stored as infinity,
-// and the second pass adds the ranks again for the elements that it finds so.
-// Where the output replaces an fp16 input, which is gone by then, the first
-// pass stores nothing and the second adds the ranks of the whole tensor.  With one rank the first pass
-// of car_grads_reduce_clip only reads: the second reads the input again, so
-// that a clipped step moves 3 tensors' bytes instead of 4 (and rounds once),
-// and one in place that needs no clipping moves 1.
+// and the second pass adds the ranks again for the vectors that hold one.  Where
+// the output replaces an fp16 input, which is gone by then, the first pass
+// stores nothing and the second adds the ranks of the whole tensor.  With one
+// rank the first pass of car_grads_reduce_clip only reads: the second reads the
+// input again, so that a clipped step moves 3 tensors' bytes instead of 4 (and
+// rounds once), and one in place that needs no clipping moves 1.
 //
 // Where every value has to be rounded once (car_grads_reduce_clip_once), the
 // second pass adds the ranks' 16-bit tensors again, if there is anything to
@@ -241,15 +241,23 @@ __device__ __forceinline__ Span span_of(const GradChunk& c) {
 template <int W>
 constexpr int kGradVectors = W >= 5 ? 1 : W >= 3 ? 2 : 4;
 
-// CTAs per SM that the instances for W ranks are compiled for.
+// CTAs per SM that the instances for W ranks are compiled for.  (The clip's
+// kSums instances for 2, 8, 10 and 11 spill 12 to 40 bytes.)
 template <int W>
 constexpr int kGradMinCtas = W > 11 ? 2 : W > 8 ? 3 : 4;
+
+// The clipped value of a sum whose stored form is `stored`: the sum itself
+// counts where that is infinite, since a factor below 1 may bring it back.
+__device__ __forceinline__ float clip_half(float stored, float sum, float coef) {
+  return __fmul_rn(isinf(stored) ? sum : stored, coef);
+}
 
 // What a pass does with a chunk's sums G.
 enum class SumUse {
   kSquare,  // adds their squares
   kStore,   // and stores them
-  kClip     // stores G * coef
+  kClip,    // stores G * coef
+  kClipRounded  // the same, of G as kStore would have left it
 };
 
 // Squares of the unrounded sums.  kept: what is stored is all that the caller
@@ -258,7 +266,7 @@ enum class SumUse {
 template <int DT, int W, SumUse USE>
 __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const* __restrict__ in, float scale,
                                            uint64_t policy, bool kept, float coef = 1.f) {
-  constexpr bool STORE = USE != SumUse::kSquare, CLIP = USE == SumUse::kClip;
+  constexpr bool STORE = USE != SumUse::kSquare, CLIP = USE == SumUse::kClip || USE == SumUse::kClipRounded;
   using S = Scalar<DT>;
   using T = typename S::T;
   constexpr int E = Pack<DT>::kN;
@@ -291,11 +299,15 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
 #pragma unroll
         for (int e = 0; e < E; e++) {
           acc[u][e] = __fmul_rn(acc[u][e], scale);
-          if constexpr (CLIP)
-            acc[u][e] = __fmul_rn(acc[u][e], coef);
-          else
-            ss = fmaf(acc[u][e], acc[u][e], ss);
+          if constexpr (USE == SumUse::kClip) acc[u][e] = __fmul_rn(acc[u][e], coef);
+          if constexpr (!CLIP) ss = fmaf(acc[u][e], acc[u][e], ss);
           if constexpr (LOSES) top = fmaxf(top, fabsf(acc[u][e]));
+        }
+        if constexpr (USE == SumUse::kClipRounded) {
+          float f[E];
+          Pack<DT>::widen(Pack<DT>::narrow(acc[u]), f);
+#pragma unroll
+          for (int e = 0; e < E; e++) acc[u][e] = clip_half(f[e], acc[u][e], coef);
         }
         if constexpr (STORE) st16(to + at[u], Pack<DT>::narrow(acc[u]));
       }
@@ -308,37 +320,14 @@ __device__ __forceinline__ float sum_chunk(const GradChunk& c, const void* const
     float acc = S::up(static_cast<const T*>(in[0])[at]);
     for (int r = 1; r < W; r++) acc = __fadd_rn(acc, S::up(static_cast<const T*>(in[r])[at]));
     acc = __fmul_rn(acc, scale);
-    if constexpr (CLIP)
-      acc = __fmul_rn(acc, coef);
-    else
-      ss = fmaf(acc, acc, ss);
+    if constexpr (USE == SumUse::kClip) acc = __fmul_rn(acc, coef);
+    if constexpr (USE == SumUse::kClipRounded) acc = clip_half(S::up(S::down(acc)), acc, coef);
+    if constexpr (!CLIP) ss = fmaf(acc, acc, ss);
     if constexpr (LOSES) top = fmaxf(top, fabsf(acc));
     if constexpr (STORE) out[at] = S::down(acc);
   }
   if (LOSES && kept && top >= 65520.f) ss += INFINITY;  // (a NaN stays one)
   return ss;
-}
-
-// Whole vectors of out = (from * scale) * coef; from may be out itself.
-template <int DT, int U>
-__device__ __forceinline__ void clip_vectors(uint4* to, const uint4* from, int vecs, float scale, float coef, uint64_t policy) {
-  constexpr int E = Pack<DT>::kN;
-#pragma unroll 1
-  for (int v0 = threadIdx.x; v0 < vecs; v0 += kGradThreads * U) {
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; u++) raw[u] = ld_once(from + min(v0 + u * kGradThreads, vecs - 1));
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      if (v0 + u * kGradThreads < vecs) {
-        float f[E];
-        Pack<DT>::widen(raw[u], f);
-#pragma unroll
-        for (int e = 0; e < E; e++) f[e] = __fmul_rn(__fmul_rn(f[e], scale), coef);
-        st_hint(to + v0 + u * kGradThreads, Pack<DT>::narrow(f), policy);
-      }
-    }
-  }
 }
 
 // G of one element, as sum_chunk forms it.
@@ -351,36 +340,20 @@ __device__ __forceinline__ float sum_element(const void* const* __restrict__ in,
   return __fmul_rn(acc, scale);
 }
 
-// The same for U vectors at the byte offsets `at` of every rank.
-template <int DT, int U>
-__device__ __forceinline__ void sum_vectors(const void* const* __restrict__ in, int n, const uint32_t (&at)[U], float scale,
-                                            float (&acc)[U][Pack<DT>::kN]) {
+// The same for the vector at byte offset `at` of every rank.
+template <int DT>
+__device__ __forceinline__ void sum_vector(const void* const* __restrict__ in, int n, uint32_t at, float scale,
+                                           float (&acc)[Pack<DT>::kN]) {
   constexpr int E = Pack<DT>::kN;
 #pragma unroll 1
   for (int r = 0; r < n; r++) {
-    const uint8_t* from = static_cast<const uint8_t*>(in[r]);
-    uint4 raw[U];
+    float f[E];
+    Pack<DT>::widen(ld_once(static_cast<const uint8_t*>(in[r]) + at), f);
 #pragma unroll
-    for (int u = 0; u < U; u++) raw[u] = ld_once(from + at[u]);
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      float f[E];
-      Pack<DT>::widen(raw[u], f);
-#pragma unroll
-      for (int e = 0; e < E; e++) acc[u][e] = r == 0 ? f[e] : __fadd_rn(acc[u][e], f[e]);
-    }
+    for (int e = 0; e < E; e++) acc[e] = r == 0 ? f[e] : __fadd_rn(acc[e], f[e]);
   }
 #pragma unroll
-  for (int u = 0; u < U; u++) {
-#pragma unroll
-    for (int e = 0; e < E; e++) acc[u][e] = __fmul_rn(acc[u][e], scale);
-  }
-}
-
-// The clipped value of a sum whose stored form is `stored`: the sum itself
-// counts where that is infinite, since a factor below 1 may bring it back.
-__device__ __forceinline__ float clip_half(float stored, float sum, float coef) {
-  return __fmul_rn(isinf(stored) ? sum : stored, coef);
+  for (int e = 0; e < E; e++) acc[e] = __fmul_rn(acc[e], scale);
 }
 
 __device__ __forceinline__ bool in_place(const GradChunk& c, const void* const* __restrict__ in, int n) {
@@ -389,91 +362,66 @@ __device__ __forceinline__ bool in_place(const GradChunk& c, const void* const* 
   return hit;
 }
 
-// fp16, two and more ranks, the first pass's sums in out: infinite ones are
-// added again.
-__device__ __forceinline__ void clip_half_chunk(const GradChunk& c, const void* const* __restrict__ in, int n, float scale,
-                                                float coef, uint64_t policy) {
-  constexpr int E = Pack<kFP16>::kN;
-  const Span sp = span_of<kFP16>(c);
-  __half* out = static_cast<__half*>(c.out);
-  uint4* to = reinterpret_cast<uint4*>(out + sp.head);
-  constexpr int U = 4;
-#pragma unroll 1
-  for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; u++) raw[u] = ld_once(to + min(v0 + u * kGradThreads, sp.vecs - 1));
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int v = v0 + u * kGradThreads;
-      if (v < sp.vecs) {
-        float f[E], o[E];
-        Pack<kFP16>::widen(raw[u], f);
-        bool lost = false;
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-          lost = lost || isinf(f[e]);
-          o[e] = __fmul_rn(f[e], coef);
-        }
-        if (lost) {
-          const uint32_t at[1] = {((uint32_t)sp.head + (uint32_t)v * E) * (uint32_t)sizeof(__half)};
-          float sum[1][E];
-          sum_vectors<kFP16, 1>(in, n, at, scale, sum);
-#pragma unroll
-          for (int e = 0; e < E; e++) o[e] = clip_half(f[e], sum[0][e], coef);
-        }
-        st_hint(to + v, Pack<kFP16>::narrow(o), policy);
-      }
-    }
-  }
-#pragma unroll 1
-  for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
-    const int at = i < sp.head ? i : i + sp.vecs * E;
-    const float f = __half2float(out[at]);
-    out[at] = __float2half_rn(isinf(f) ? clip_half(f, sum_element<kFP16>(in, n, at, scale), coef) : __fmul_rn(f, coef));
-  }
+// Whether one of eight fp16 values is infinite.
+__device__ __forceinline__ bool any_infinite(uint4 v) {
+  auto top = [](uint32_t w) { return __habs2(*reinterpret_cast<const __half2*>(&w)); };
+  const __half2 m = __hmax2(__hmax2(top(v.x), top(v.y)), __hmax2(top(v.z), top(v.w)));
+  const uint32_t b = *reinterpret_cast<const uint32_t*>(&m);
+  return (b & 0xFFFFu) == 0x7C00u || (b >> 16) == 0x7C00u;
 }
 
-// fp16 in place of an input, which the first pass left as it was: the sums
-// and their clipping at once, with the same two roundings.
-__device__ __forceinline__ void sum_clip_half_chunk(const GradChunk& c, const void* const* __restrict__ in, int n, float scale,
-                                                    float coef, uint64_t policy) {
-  constexpr int E = Pack<kFP16>::kN;
-  const Span sp = span_of<kFP16>(c);
-  __half* out = static_cast<__half*>(c.out);
-  constexpr int U = 2;
+// What clipping needs to add fp16 sums again (AGAIN): they were formed from
+// these inputs with this scale.
+struct SumSource {
+  const void* const* in;
+  int n;
+  float scale;
+};
+
+// Whole vectors of out = (from * scale) * coef; from may be out itself.  AGAIN:
+// from holds sums, and those that are infinite in fp16 are added again.
+template <int DT, int U, bool AGAIN>
+__device__ __forceinline__ void clip_vectors(uint4* to, const uint4* from, int vecs, float scale, float coef, uint64_t policy,
+                                             const SumSource& src, int head) {
+  constexpr int E = Pack<DT>::kN;
 #pragma unroll 1
-  for (int v0 = threadIdx.x; v0 < sp.vecs; v0 += kGradThreads * U) {
-    uint32_t at[U];
-    float acc[U][E];
+  for (int v0 = threadIdx.x; v0 < vecs; v0 += kGradThreads * U) {
+    uint4 raw[U];
+    uint32_t lost = 0u;
 #pragma unroll
-    for (int u = 0; u < U; u++)
-      at[u] = (uint32_t)sp.head * (uint32_t)sizeof(__half) + (uint32_t)min(v0 + u * kGradThreads, sp.vecs - 1) * 16u;
-    sum_vectors<kFP16, U>(in, n, at, scale, acc);
+    for (int u = 0; u < U; u++) raw[u] = ld_once(from + min(v0 + u * kGradThreads, vecs - 1));
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      if (v0 + u * kGradThreads < sp.vecs) {
+      if (v0 + u * kGradThreads < vecs) {
         float f[E];
-        Pack<kFP16>::widen(Pack<kFP16>::narrow(acc[u]), f);
+        Pack<DT>::widen(raw[u], f);
 #pragma unroll
-        for (int e = 0; e < E; e++) f[e] = clip_half(f[e], acc[u][e], coef);
-        st_hint(reinterpret_cast<uint8_t*>(out) + at[u], Pack<kFP16>::narrow(f), policy);
+        for (int e = 0; e < E; e++) f[e] = __fmul_rn(__fmul_rn(f[e], scale), coef);
+        st_hint(to + v0 + u * kGradThreads, Pack<DT>::narrow(f), policy);
+        if constexpr (AGAIN) lost |= any_infinite(raw[u]) ? 1u << u : 0u;
       }
     }
-  }
+    if constexpr (AGAIN) {
 #pragma unroll 1
-  for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
-    const int at = i < sp.head ? i : i + sp.vecs * E;
-    const float sum = sum_element<kFP16>(in, n, at, scale);
-    out[at] = __float2half_rn(clip_half(__half2float(__float2half_rn(sum)), sum, coef));
+      for (; lost; lost &= lost - 1u) {
+        const int v = v0 + (__ffs((int)lost) - 1) * kGradThreads;
+        float sum[E], f[E];
+        sum_vector<DT>(src.in, src.n, ((uint32_t)head + (uint32_t)v * E) * (uint32_t)sizeof(__half), src.scale, sum);
+        Pack<DT>::widen(Pack<DT>::narrow(sum), f);  // as they were stored
+#pragma unroll
+        for (int e = 0; e < E; e++) f[e] = clip_half(f[e], sum[e], coef);
+        st_hint(to + v, Pack<DT>::narrow(f), policy);
+      }
+    }
   }
 }
 
 // One chunk of it, from being out itself or rank 0's input.  Eight loads in
 // flight per thread against four: W = 4, 8 MB 11.2 -> 10.7 us, W = 8, 400 MB
 // 680 -> 672; chunks of one vector per thread have no use for them.
-template <int DT>
-__device__ __forceinline__ void clip_chunk(const GradChunk& c, const void* from, float scale, float coef, uint64_t policy) {
+template <int DT, bool AGAIN = false>
+__device__ __forceinline__ void clip_chunk(const GradChunk& c, const void* from, float scale, float coef, uint64_t policy,
+                                           const SumSource& src = SumSource{}) {
   using S = Scalar<DT>;
   using T = typename S::T;
   constexpr int E = Pack<DT>::kN;
@@ -483,13 +431,15 @@ __device__ __forceinline__ void clip_chunk(const GradChunk& c, const void* from,
   uint4* to = reinterpret_cast<uint4*>(out + sp.head);
   const uint4* body = reinterpret_cast<const uint4*>(x + sp.head);
   if (sp.vecs <= kGradThreads)
-    clip_vectors<DT, 1>(to, body, sp.vecs, scale, coef, policy);
+    clip_vectors<DT, 1, AGAIN>(to, body, sp.vecs, scale, coef, policy, src, sp.head);
   else
-    clip_vectors<DT, 8>(to, body, sp.vecs, scale, coef, policy);
+    clip_vectors<DT, AGAIN ? 4 : 8, AGAIN>(to, body, sp.vecs, scale, coef, policy, src, sp.head);
 #pragma unroll 1
   for (int i = threadIdx.x; i < sp.head + sp.tail; i += kGradThreads) {
     const int at = i < sp.head ? i : i + sp.vecs * E;
-    out[at] = S::down(__fmul_rn(__fmul_rn(S::up(x[at]), scale), coef));
+    float f = __fmul_rn(S::up(x[at]), scale);
+    if (AGAIN && isinf(f)) f = sum_element<DT>(src.in, src.n, at, src.scale);
+    out[at] = S::down(__fmul_rn(f, coef));
   }
 }
 
@@ -574,7 +524,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradMinCtas<W>)
   }
 }
 
-// FROM: where the values come from (car_launch.h); W: the ranks for kOnce.
+// FROM: where the values come from (car_launch.h); W: the ranks for kSums and kOnce.
 template <GradSource FROM, int W>
 __global__ void __launch_bounds__(kGradThreads, kGradMinCtas<W>)
     grads_clip_kernel(const GradPlan p, const double* __restrict__ sums, const int n_sums, const float scale,
@@ -617,10 +567,10 @@ __global__ void __launch_bounds__(kGradThreads, kGradMinCtas<W>)
     }
     if (FROM_INPUT && x == cur.out && whole && scale == 1.f) continue;  // already there
     if (FROM == GradSource::kSums && cur.dtype == kFP16) {
-      if (unsummed && in_place(cur, in, p.W))
-        sum_clip_half_chunk(cur, in, p.W, scale, coef, policy);
+      if (unsummed && in_place(cur, in, W))
+        sum_chunk<kFP16, W, SumUse::kClipRounded>(cur, in, scale, policy, false, coef);
       else if (!whole)
-        clip_half_chunk(cur, in, p.W, scale, coef, policy);
+        clip_chunk<kFP16, true>(cur, x, 1.f, coef, policy, SumSource{in, W, scale});
       continue;
     }
     if (FROM == GradSource::kOnce && cur.dtype != kFP32) {
@@ -646,30 +596,33 @@ __global__ void __launch_bounds__(kGradThreads, kGradMinCtas<W>)
 }
 
 using ClipFn = void (*)(const GradPlan, const double*, const int, const float, const float, float*);
+template <GradSource FROM>
+ClipFn pick_clip_ranks(int W) {
+  switch (W) {
+    case 2: return grads_clip_kernel<FROM, 2>;
+    case 3: return grads_clip_kernel<FROM, 3>;
+    case 4: return grads_clip_kernel<FROM, 4>;
+    case 5: return grads_clip_kernel<FROM, 5>;
+    case 6: return grads_clip_kernel<FROM, 6>;
+    case 7: return grads_clip_kernel<FROM, 7>;
+    case 8: return grads_clip_kernel<FROM, 8>;
+    case 9: return grads_clip_kernel<FROM, 9>;
+    case 10: return grads_clip_kernel<FROM, 10>;
+    case 11: return grads_clip_kernel<FROM, 11>;
+    case 12: return grads_clip_kernel<FROM, 12>;
+    case 13: return grads_clip_kernel<FROM, 13>;
+    case 14: return grads_clip_kernel<FROM, 14>;
+    case 15: return grads_clip_kernel<FROM, 15>;
+    case 16: return grads_clip_kernel<FROM, 16>;
+    default: return nullptr;
+  }
+}
 ClipFn pick_clip(int W, GradSource from) {
   switch (from) {
     case GradSource::kOutput: return grads_clip_kernel<GradSource::kOutput, 1>;
-    case GradSource::kSums: return grads_clip_kernel<GradSource::kSums, 1>;
-    case GradSource::kInput: return grads_clip_kernel<GradSource::kInput, 1>;
-    case GradSource::kOnce: break;
-  }
-  switch (W) {
-    case 2: return grads_clip_kernel<GradSource::kOnce, 2>;
-    case 3: return grads_clip_kernel<GradSource::kOnce, 3>;
-    case 4: return grads_clip_kernel<GradSource::kOnce, 4>;
-    case 5: return grads_clip_kernel<GradSource::kOnce, 5>;
-    case 6: return grads_clip_kernel<GradSource::kOnce, 6>;
-    case 7: return grads_clip_kernel<GradSource::kOnce, 7>;
-    case 8: return grads_clip_kernel<GradSource::kOnce, 8>;
-    case 9: return grads_clip_kernel<GradSource::kOnce, 9>;
-    case 10: return grads_clip_kernel<GradSource::kOnce, 10>;
-    case 11: return grads_clip_kernel<GradSource::kOnce, 11>;
-    case 12: return grads_clip_kernel<GradSource::kOnce, 12>;
-    case 13: return grads_clip_kernel<GradSource::kOnce, 13>;
-    case 14: return grads_clip_kernel<GradSource::kOnce, 14>;
-    case 15: return grads_clip_kernel<GradSource::kOnce, 15>;
-    case 16: return grads_clip_kernel<GradSource::kOnce, 16>;
-    default: return nullptr;
+    case GradSource::kSums: return pick_clip_ranks<GradSource::kSums>(W);
+    case GradSource::kOnce: return pick_clip_ranks<GradSource::kOnce>(W);
+    default: return grads_clip_kernel<GradSource::kInput, 1>;
   }
 }
 

@@ -120,8 +120,8 @@ car_status create(int W, int64_t n, const int64_t* numel, const car_dtype* dtype
     half_in_place = half_in_place || (is_half && replaced);
     narrow_in_place = narrow_in_place || (dtypes[t] != CAR_FP32 && replaced);
   }
-  // (kSums with nothing to add again is slower: W = 2, 64 M bf16 values 92.9
-  // against 90.1 us.)
+  // (Without fp16 the second pass need not look for infinities: W = 2, 64 M
+  // values 89.7 against 91.0 us.)
   const car::GradSource source = W == 1 ? car::GradSource::kInput : half ? car::GradSource::kSums : car::GradSource::kOutput;
 
   int device = -1, num_sms = 0, l2 = 0, per_reduce = 0, per_sums = 0, per_once = 0, per_clip = 0, per_store = 0;
