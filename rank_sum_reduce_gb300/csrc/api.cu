@@ -217,7 +217,7 @@ bool shape_valid(int W, int V, const car::FusedShape& sh) {
 // (pipeline), W = 2 3.3 against 3.8; at M = 184, W = 8 8.2 against 7.5, W = 2
 // 5.3 against 4.5; at M = 456, W = 8 15.4 against 13.4; at M = 1024 28.2
 // (pipeline) against 32.3; 12 KB slices, W = 8, M = 1024, N = 6144 bf16: 21.7
-// against 25.9; W = 4, M = 1024, N = 3072 fp32: 14.9 against 18.2.  With 8 KB
+// against 25.9.  With 8 KB
 // slices and smaller the persistent CTA finishes its rows one after another
 // (each behind the row statistic's barriers), and the row kernel, many CTAs
 // per SM, keeps more rows in flight: W = 4,
@@ -280,7 +280,7 @@ bool rows_compiled(int W) { return W <= 2 || W == 4 || W == 8 || W == 16; }
 bool quant_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int64_t tiles = (h->M + sh.teams - 1) / sh.teams, sms = h->num_sms;
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
-  if (h->vec_per_row > 2048) return sh.vpt <= 6 ? 2 * tiles >= sms : tiles >= sms;
+  if (sh.vpt > 4) return sh.vpt <= 6 ? 2 * tiles >= sms : tiles >= sms;
   if (h->vec_per_row > 1024) return 2 * tiles >= 3 * sms;
   if (h->W <= 2) {
     if (sh.teams >= 16) return 2 * tiles >= sms;
@@ -335,9 +335,9 @@ bool backward_pipeline_pays(const car_ctx* h, const car::TeamShape& sh) {
   const int V = h->vec_per_row;
   const bool fp32 = h->dtype == CAR_FP32;
   if (!rows_compiled(h->W)) return 2 * tiles >= sms;
-  if (V > 3584) return tiles >= 8 * sms && (sh.slots >= h->W + 2 || !car::backward_has_variant(h->W, 2));
-  if (V > 3072) return tiles >= sms;
-  if (V > 2048) return 3 * tiles >= 2 * sms;
+  if (sh.vpt == 8) return tiles >= 8 * sms && (sh.slots >= h->W + 2 || !car::backward_has_variant(h->W, 2));
+  if (sh.vpt == 7) return tiles >= sms;
+  if (sh.vpt > 4) return 3 * tiles >= 2 * sms;
   if (V > 1536 && fp32) return tiles >= 2 * sms;
   if (V > 1536) return sh.team_threads + 32 * sh.producers <= 512 && h->W >= 4 && tiles >= (h->W < 8 ? 6 : 1) * sms;
   if (V > 1024) return tiles >= (h->W <= 2 ? 3 : 2) * sms;
