@@ -1,6 +1,7 @@
 /*
  * car.h -- C ABI of libcar: one-shot rank-sum reduce, fused residual add +
- * RMSNorm (also with an 8-bit output and scales, and its backward), rank sums
+ * RMSNorm (also with an 8-bit output and scales, and its backward; also with a
+ * norm, a gate and dropout between the sum and the residual add), rank sums
  * of many gradient tensors with their global norm and clipping, and LL / LL128
  * line encode, validate and decode-reduce, for one GB300 (sm_103a).
  *
@@ -229,6 +230,142 @@ car_status car_reduce_residual_rmsnorm_backward(car_ctx* h, const void* const* d
 
 /* Bytes of `workspace` above; 0 when none is needed or for an invalid handle. */
 size_t car_backward_workspace_bytes(car_ctx* h);
+
+/* ---------------------------------------------------------------------- */
+/* What lies between the rank sum and the residual add: a norm behind the  */
+/* block, a gate, dropout, the residual's scale                            */
+/* ---------------------------------------------------------------------- */
+
+/* Dropout whose mask is never stored: element i = m * N + j of the [M, N]
+ * problem is dropped when its 16 random bits are below t = round(65536 * p)
+ * (so p is rounded to a multiple of 2^-16, halves away from zero; t = 0 drops
+ * nothing, t = 65536 everything), and otherwise multiplied by
+ * 65536 / (65536 - t).  A dropped element is 0 whatever its value was.
+ * The bits are a function of (seed, offset, i) alone: Philox4x32-10 (Salmon,
+ * Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011)
+ * with the key {seed low, seed high} and the counter {i / 8 low, i / 8 high,
+ * offset low, offset high} (32-bit halves) gives four words for eight
+ * consecutive elements; element i takes the low (i even) or high (i odd) half
+ * of word (i % 8) / 2.  The same for every type, kernel and rank count, so a
+ * backward with the same fields sees the forward's mask.  Give each layer and
+ * step an offset of its own.
+ *   p          : in [0, 1].
+ *   seed, offset : any.
+ *   offset_dev : dev, one uint64 that is added to offset (mod 2^64) when the
+ *                kernel runs, 8-byte aligned, or NULL.  A captured call reads
+ *                it at each replay: advance it on the device in between. */
+typedef struct {
+  float p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_dev;
+} car_dropout;
+
+/* The branch that a block adds to the residual stream.  With acc the fp32 rank
+ * sum:
+ *   y = (acc * rsqrt(mean_j(acc^2) + norm_eps)) * norm_weight[j], or acc
+ *   z = dropout( y * gate[g, j] )
+ *   h = residual_scale * residual + z
+ * Zeroed fields other than residual_scale leave their part out.
+ *   norm_weight : dev [N], or NULL: no norm behind the block.
+ *   norm_eps    : finite, >= 0 (not read without a norm_weight).
+ *   gate        : dev, or NULL: no gate.
+ *   gate_rows   : G >= 1, a divisor of M: gate is [G, N], and row m takes its
+ *                 row g = m / (M / G) (1: one gate for all rows; G: one for each
+ *                 of G samples of M / G consecutive rows).  0: gate is [M, N],
+ *                 a row of its own for every row.  (Not read without a gate.)
+ *   residual_scale : finite.
+ *   dropout     : host, or NULL: none.
+ * Read during the call only. */
+typedef struct {
+  const void* norm_weight;
+  float norm_eps;
+  const void* gate;
+  int64_t gate_rows;
+  float residual_scale;
+  const car_dropout* dropout;
+} car_branch;
+
+/* The gradients that the backward writes; see below. */
+typedef struct {
+  void* dx;
+  void* dresidual;
+  float* dweight;
+  float* dnorm_weight;
+  void* dgate;
+} car_branch_grads;
+
+/* ar_out[i] = rne_T( dropout( fp32 rank sum ) ): dropout alone, e.g. behind an
+ * embedding that is split over the ranks.  Its gradient is the same call on the
+ * ranks' contributions to the gradient of ar_out.  Arguments and aliasing as
+ * car_reduce; drop: host, not NULL.
+ * Errors: CAR_ERR_HANDLE, CAR_ERR_ARG (NULL, p outside [0, 1]), CAR_ERR_ALIGN,
+ * CAR_ERR_CUDA. */
+car_status car_reduce_dropout(car_ctx* h, const void* const* inputs, const car_dropout* drop, void* ar_out,
+                              void* stream);
+
+/* car_reduce_residual_rmsnorm with a branch: with h as above,
+ *   residual_out[m,j] = rne_T(h);   ar_out[m,j] = rne_T(acc) when ar_out != NULL
+ *   norm_out[m,j]     = rne_T( (h * rsqrt( mean_j(h^2) + eps )) * weight[j] )
+ * Statistics in fp32 from the unrounded acc and h.  With no norm, gate and
+ * dropout and a residual_scale of 1, ar_out and residual_out have the bits of
+ * car_reduce_residual_rmsnorm.
+ *   residual_out : may equal residual.     ar_out : may equal one input.
+ * Every other overlap of an output with an output or an input is refused.  The
+ * kernel and launch shape are chosen automatically (car_tune_fused does not
+ * apply).
+ * Errors: CAR_ERR_HANDLE, CAR_ERR_ARG (NULL, a value out of its range, gate_rows
+ * does not divide M, overlap), CAR_ERR_ALIGN, CAR_ERR_SIZE (N*s >
+ * CAR_MAX_ROW_BYTES), CAR_ERR_CUDA. */
+car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inputs, const car_branch* branch,
+                                              const void* residual, const void* weight, float eps,
+                                              void* residual_out, void* norm_out, void* ar_out, void* stream);
+
+/* Its backward, from the rank sum `ar` and the residual_out that the forward
+ * stored, with the forward's branch.  The roundings to T of both are taken as
+ * they are.  Per row, with g the fp32 rank sum of dnorm_r:
+ *   r = rsqrt( mean_j(h^2) + eps );  u = h * r;  h = f32(residual_out)
+ *   dh = r * (g * weight - u * mean_j( g * weight * u )) + dresidual_out
+ *   dresidual = rne_T( residual_scale * dh );   dweight[j] = sum_m g * u
+ *   dz = dropout( dh )                          (the forward's mask)
+ *   q = rsqrt( mean_j(a^2) + norm_eps );  u1 = a * q;  a = f32(ar)
+ *   dgate = dz * u1 * norm_weight, summed over the rows that share a gate row
+ *   dnorm_weight[j] = sum_m dz * gate * u1;   v = dz * gate * norm_weight
+ *   dx = rne_T( q * (v - u1 * mean_j( v * u1 )) )
+ * and without a norm u1 = a, norm_weight = 1, dx = rne_T(dz * gate).  dx is the
+ * gradient of every rank's x_r.
+ *   dnorm         : host array of W dev pointers, each [M, N].
+ *   ar            : dev [M, N]; NULL where nothing reads it: no norm_weight, and
+ *                   no gate or no dgate.
+ *   residual_out  : dev [M, N].       weight : dev [N].
+ *   dresidual_out : dev [M, N], or NULL for none.
+ *   out->dx           : dev [M, N].
+ *   out->dresidual    : dev [M, N], or NULL.
+ *   out->dweight      : dev [N] fp32, or NULL.
+ *   out->dnorm_weight : dev [N] fp32, or NULL (must be NULL without a norm_weight).
+ *   out->dgate        : dev, or NULL (must be NULL without a gate): fp32 [G, N];
+ *                       with gate_rows 0 [M, N] of the handle's type.
+ *   workspace     : dev, car_branch_workspace_bytes(h, branch) bytes, 16-byte
+ *                   aligned; its contents do not matter before or after.  Calls
+ *                   that may overlap on the GPU need one each.  May be NULL when
+ *                   that is 0, or with none of dweight, dnorm_weight and a shared
+ *                   gate's dgate.
+ * dx and dresidual may each equal one of dnorm[k], ar, residual_out and
+ * dresidual_out; every other overlap of an output with an output, an input or
+ * the workspace is refused.  All outputs are overwritten.  The same call on the
+ * same data gives the same bits (no float atomics).
+ * Errors as the forward's.  Bounded waits that run out are reported by car_sync:
+ * as in car_reduce_residual_rmsnorm_backward, and likewise in the forward, where
+ * residual_out then holds NaN in those columns if there is a norm_weight. */
+car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const car_branch* branch,
+                                                       const void* ar, const void* residual_out, const void* weight,
+                                                       float eps, const void* dresidual_out,
+                                                       const car_branch_grads* out, void* workspace, void* stream);
+
+/* Bytes of `workspace` above for a branch with that gate and gate_rows (its
+ * other fields are not read; branch may be NULL: no gate); 0 when none is needed,
+ * for an invalid handle or for gate_rows that do not divide M. */
+size_t car_branch_workspace_bytes(car_ctx* h, const car_branch* branch);
 
 /* ---------------------------------------------------------------------- */
 /* Gradients of many tensors: rank sum, global norm, clipping              */

@@ -40,6 +40,20 @@ class car_stale_report(ctypes.Structure):
                 ("entries", ctypes.POINTER(ctypes.c_uint32 * 2))]
 
 
+class car_dropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("offset_dev", ctypes.c_void_p)]
+
+
+class car_branch(ctypes.Structure):
+    _fields_ = [("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float), ("gate", ctypes.c_void_p),
+                ("gate_rows", ctypes.c_int64), ("residual_scale", ctypes.c_float), ("dropout", ctypes.POINTER(car_dropout))]
+
+
+class car_branch_grads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("dresidual", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+                ("dnorm_weight", ctypes.c_void_p), ("dgate", ctypes.c_void_p)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libcar.so is not built ({LIB_PATH}); run `python -c 'import __graft_entry__ as g; "
                       "g.build()'` or `python rank_sum_reduce_gb300/build.py`")
@@ -61,6 +75,13 @@ _SIGS = {
     "car_reduce_residual_rmsnorm_backward": (ctypes.c_int, [_vp, _pvp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp,
                                                             _vp]),
     "car_backward_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "car_reduce_dropout": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_dropout), _vp, _vp]),
+    "car_reduce_branch_residual_rmsnorm": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_branch), _vp, _vp, ctypes.c_float,
+                                                          _vp, _vp, _vp, _vp]),
+    "car_reduce_branch_residual_rmsnorm_backward": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_branch), _vp, _vp, _vp,
+                                                                   ctypes.c_float, _vp, ctypes.POINTER(car_branch_grads),
+                                                                   _vp, _vp]),
+    "car_branch_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.POINTER(car_branch)]),
     "car_grads_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64),
                                         ctypes.POINTER(ctypes.c_int), _pvp, _pvp, _ctx_pp]),
     "car_grads_destroy": (ctypes.c_int, [_vp]),
@@ -164,6 +185,35 @@ def car_reduce_residual_rmsnorm_backward(h, dnorm, residual_out: int, weight: in
 
 def car_backward_workspace_bytes(h) -> int:
     return int(_lib.car_backward_workspace_bytes(h))
+
+
+def _ref(struct):
+    return ctypes.byref(struct) if struct is not None else None
+
+
+def car_reduce_dropout(h, inputs, drop, ar_out: int, stream: int = 0) -> int:
+    """drop: a car_dropout."""
+    return _lib.car_reduce_dropout(h, _table(inputs) if inputs is not None else None, _ref(drop), ar_out, stream)
+
+
+def car_reduce_branch_residual_rmsnorm(h, inputs, branch, residual: int, weight: int, eps: float, residual_out: int,
+                                       norm_out: int, ar_out: int | None, stream: int = 0) -> int:
+    """branch: a car_branch."""
+    return _lib.car_reduce_branch_residual_rmsnorm(h, _table(inputs) if inputs is not None else None, _ref(branch), residual,
+                                                   weight, eps, residual_out, norm_out, ar_out, stream)
+
+
+def car_reduce_branch_residual_rmsnorm_backward(h, dnorm, branch, ar: int | None, residual_out: int, weight: int,
+                                                eps: float, dresidual_out: int | None, out, workspace: int | None,
+                                                stream: int = 0) -> int:
+    """branch: a car_branch; out: a car_branch_grads."""
+    return _lib.car_reduce_branch_residual_rmsnorm_backward(h, _table(dnorm) if dnorm is not None else None, _ref(branch), ar,
+                                                            residual_out, weight, eps, dresidual_out, _ref(out), workspace,
+                                                            stream)
+
+
+def car_branch_workspace_bytes(h, branch) -> int:
+    return int(_lib.car_branch_workspace_bytes(h, _ref(branch)))
 
 
 def car_grads_create(W: int, numel, dtypes, inputs, outs):
@@ -358,6 +408,57 @@ def _ptr(t, nbytes: int, what: str, device=None) -> int:
     raise ValueError(f"{what}: {t.numel() * t.element_size()} bytes, the call needs {nbytes}")
 
 
+class Dropout:
+    """Dropout with probability p (rounded to a multiple of 2^-16) whose mask is a function of seed, offset and the
+    element's place alone (see car_dropout): a backward with the same object sees the forward's mask.  offset_dev, if
+    given, is a CUDA tensor of one 64-bit integer that is added to offset when a kernel runs, so that a captured call can
+    be given another mask at every replay.  seed and offset are any integers, taken mod 2^64, and may be set anew between
+    calls; p and offset_dev are fixed."""
+
+    def __init__(self, p, seed, offset=0, offset_dev=None):
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p: {p} is not in [0, 1]")
+        if offset_dev is not None:
+            import torch
+
+            _check_type(offset_dev, (torch.int64, torch.uint64), "offset_dev")
+            _ptr(offset_dev, 8, "offset_dev")
+        self.p, self.offset_dev = p, offset_dev
+        self.struct = car_dropout(p, seed % 2**64, offset % 2**64, offset_dev.data_ptr() if offset_dev is not None else None)
+
+    @property
+    def seed(self) -> int:
+        return self.struct.seed
+
+    @seed.setter
+    def seed(self, value: int):
+        self.struct.seed = value % 2**64
+
+    @property
+    def offset(self) -> int:
+        return self.struct.offset
+
+    @offset.setter
+    def offset(self, value: int):
+        self.struct.offset = value % 2**64
+
+
+class Branch:
+    """What a block adds to the residual stream (see car_branch): the rank sum, normalised if there is a norm_weight
+    [N], times the gate, dropped out; residual_scale multiplies the residual.  gate_rows: 1 for a gate [N] (or [1, N]) of
+    all rows, G for one row [G, N] for each of G samples of M / G consecutive rows, 0 for [M, N], a row of its own for
+    every row.  norm_weight and gate are contiguous CUDA tensors of the handle's type (taken as bytes); the object keeps
+    them."""
+
+    def __init__(self, norm_weight=None, norm_eps=1e-6, gate=None, gate_rows=1, residual_scale=1.0, dropout=None):
+        if gate_rows < 0:
+            raise ValueError(f"gate_rows: {gate_rows} is negative")
+        self.norm_weight, self.gate, self.gate_rows, self.dropout = norm_weight, gate, gate_rows, dropout
+        self.struct = car_branch(norm_weight.data_ptr() if norm_weight is not None else None, norm_eps,
+                                 gate.data_ptr() if gate is not None else None, gate_rows, residual_scale,
+                                 ctypes.pointer(dropout.struct) if dropout is not None else None)
+
+
 class Car:
     """A libcar handle for W rank buffers of [M, N] elements of one dtype.
 
@@ -372,6 +473,7 @@ class Car:
         self.h, self.W, self.M, self.N, self.dtype = h, W, M, N, dtype
         self.D = M * N * ELEM_SIZE[dtype]      # bytes per rank
         D, Nw = self.D, N * ELEM_SIZE[dtype]
+        self._row = Nw                         # bytes of one row
         # bytes that the tensors of a call need, in the order of its arguments
         self._quant_sizes = [(D, Nw, D, M * N, car_quant_scale_bytes(h, k), D, D) for k in range(len(SCALE_CODE))]
         self._backward_sizes = None   # found when first asked for
@@ -492,6 +594,71 @@ class Car:
         check(_lib.car_reduce_residual_rmsnorm_backward(self.h, _table(self._ranks(dnorm, self.D, "dnorm")), h, w, eps, dro,
                                                         out, dw, ws, _stream(stream, self.device)),
               "car_reduce_residual_rmsnorm_backward")
+
+    def _dropout(self, dropout):
+        if dropout.offset_dev is not None:
+            _ptr(dropout.offset_dev, 8, "offset_dev", self.device)
+        return dropout.struct
+
+    def _branch(self, branch):
+        """Its struct, once its tensors have been checked for this handle."""
+        row = self._row
+        if branch.norm_weight is not None:
+            _ptr(branch.norm_weight, row, "norm_weight", self.device)
+        if branch.gate is not None:
+            _ptr(branch.gate, (branch.gate_rows or self.M) * row, "gate", self.device)
+        if branch.dropout is not None:
+            self._dropout(branch.dropout)
+        return branch.struct
+
+    def reduce_dropout(self, xs, dropout, ar_out, stream=None):
+        """ar_out = dropout of the rank sum; its gradient is the same call on the gradient's rank contributions."""
+        check(_lib.car_reduce_dropout(self.h, _table(self._ranks(xs, self.D, "inputs")), ctypes.byref(self._dropout(dropout)),
+                                      self._p(ar_out, self.D, "ar_out"), _stream(stream, self.device)), "car_reduce_dropout")
+
+    def reduce_branch_residual_rmsnorm(self, xs, branch, residual, weight, eps, residual_out, norm_out, ar_out=None,
+                                       stream=None):
+        """reduce_residual_rmsnorm with a Branch between the rank sum and the residual add.  ar_out: the rank sum, which
+        the backward needs behind a norm and for the gate's gradient."""
+        D = self.D
+        res, w, ro, no, ar = self._ptrs((residual, weight, residual_out, norm_out, ar_out), (D, self._row, D, D, D),
+                                        ("residual", "weight", "residual_out", "norm_out", "ar_out"))
+        check(_lib.car_reduce_branch_residual_rmsnorm(self.h, _table(self._ranks(xs, D, "inputs")),
+                                                      ctypes.byref(self._branch(branch)), res, w, eps, ro, no, ar,
+                                                      _stream(stream, self.device)), "car_reduce_branch_residual_rmsnorm")
+
+    def branch_workspace_bytes(self, branch=None) -> int:
+        """Of the backward's workspace; depends on whether rows share a row of the branch's gate, and how many."""
+        return car_branch_workspace_bytes(self.h, branch.struct if branch is not None else None)
+
+    def reduce_branch_residual_rmsnorm_backward(self, dnorm, branch, ar, residual_out, weight, eps, dresidual_out, dx,
+                                                dresidual=None, dweight=None, dnorm_weight=None, dgate=None,
+                                                workspace=None, stream=None):
+        """Gradients of reduce_branch_residual_rmsnorm.  ar may be None without a norm and a dgate; dresidual_out and
+        every gradient but dx may be None.  dweight and dnorm_weight are fp32 [N]; dgate is fp32 like the gate, or with
+        gate_rows 0 [M, N] of the handle's type.  workspace (branch_workspace_bytes(branch) bytes) is taken from torch's
+        allocator on the current stream when one is needed and none is given."""
+        f32, D, N, shared = _types()[2], self.D, self.N, branch.gate_rows > 0
+        for t, what in ((dweight, "dweight"), (dnorm_weight, "dnorm_weight"), (dgate if shared else None, "dgate")):
+            if t is not None:
+                _check_type(t, f32, what)
+        need = 0
+        if dweight is not None or dnorm_weight is not None or (dgate is not None and shared):
+            need = self.branch_workspace_bytes(branch)
+        if need and workspace is None:
+            import torch
+
+            if stream is not None and _stream(stream) != torch.cuda.current_stream().cuda_stream:
+                raise ValueError("workspace: give one for a call on another stream than the current one")
+            workspace = torch.empty(need, dtype=torch.uint8, device=dx.device)
+        a, h, w, dro, out, dr, dw, dw1, dg, ws = self._ptrs(
+            (ar, residual_out, weight, dresidual_out, dx, dresidual, dweight, dnorm_weight, dgate, workspace if need else None),
+            (D, D, self._row, D, D, D, 4 * N, 4 * N, 4 * N * branch.gate_rows if shared else D, need),
+            ("ar", "residual_out", "weight", "dresidual_out", "dx", "dresidual", "dweight", "dnorm_weight", "dgate", "workspace"))
+        check(_lib.car_reduce_branch_residual_rmsnorm_backward(
+            self.h, _table(self._ranks(dnorm, D, "dnorm")), ctypes.byref(self._branch(branch)), a, h, w, eps, dro,
+            ctypes.byref(car_branch_grads(out, dr, dw, dw1, dg)), ws, _stream(stream, self.device)),
+            "car_reduce_branch_residual_rmsnorm_backward")
 
     def ll128_encode(self, data, flag, wire, stream=None):
         check(car_ll128_encode(self.h, self._p(data, self.D, "data"), flag, self._p(wire, self.ll128_wire_bytes, "wire"),

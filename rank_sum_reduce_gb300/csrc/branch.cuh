@@ -1,0 +1,147 @@
+// branch.cuh -- what the kernels of a block's branch share (branch_rows.cu,
+// branch_tma.cu, branch_backward.cu, branch_backward_tma.cu, dropout.cu): the
+// dropout's generator, gates, and the sums over a row that is split over warps
+// and a cluster of CTAs.
+#pragma once
+
+#include "branch.h"
+#include "car_device.cuh"
+
+namespace car {
+namespace {
+
+// One block of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011, section 4.3): ten rounds of two wide
+// products each.  The round keys depend on the launch alone, so they live in
+// uniform registers; a round costs a thread two wide products and two
+// three-input XORs, about 60 instructions for the 8 elements of a vector, a
+// quarter of what a branch's backward needs for them.
+__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int r = 0; r < 10; r++) {
+    const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
+    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return c;
+}
+
+// The generator's offset as the kernel runs; after the wait for the grids it
+// depends on.
+__device__ __forceinline__ uint64_t drop_offset(const DropParams& d) {
+  return d.offset + (d.offset_dev ? *static_cast<const volatile uint64_t*>(d.offset_dev) : 0ull);
+}
+
+// The 16 random bits of the E elements of the vector `v` of the [M, N] problem
+// (v counts 16-byte vectors), two in a word.  A 16-bit type has one counter per
+// vector; an fp32 vector is half of one's eight elements.
+template <int E>
+__device__ __forceinline__ void drop_bits(const DropParams& d, uint64_t offset, int64_t v, uint32_t (&bits)[E / 2]) {
+  const uint64_t c = (uint64_t)(E == 8 ? v : v >> 1);
+  const uint4 w = philox4x32_10(make_uint4((uint32_t)c, (uint32_t)(c >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)),
+                                d.key0, d.key1);
+  if constexpr (E == 8) {
+    bits[0] = w.x;
+    bits[1] = w.y;
+    bits[2] = w.z;
+    bits[3] = w.w;
+  } else {
+    bits[0] = (v & 1) ? w.z : w.x;
+    bits[1] = (v & 1) ? w.w : w.y;
+  }
+}
+
+// Element pair of a word: dropped below the threshold (selected, not
+// multiplied, so that what is dropped may be anything), else scaled.
+__device__ __forceinline__ float2 drop2(const DropParams& d, uint32_t bits, float2 x) {
+  const float2 s = mul2(x, make_float2(d.scale, d.scale));
+  return make_float2((bits & 0xFFFFu) >= d.threshold ? s.x : 0.f, (bits >> 16) >= d.threshold ? s.y : 0.f);
+}
+
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen2(uint4 v, float2 (&f)[Pack<DT>::kN / 2]) {
+  float t[Pack<DT>::kN];
+  Pack<DT>::widen(v, t);
+#pragma unroll
+  for (int e = 0; e < Pack<DT>::kN / 2; e++) f[e] = make_float2(t[2 * e], t[2 * e + 1]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 narrow2(const float2 (&f)[Pack<DT>::kN / 2]) {
+  float t[Pack<DT>::kN];
+#pragma unroll
+  for (int e = 0; e < Pack<DT>::kN / 2; e++) t[2 * e] = f[e].x, t[2 * e + 1] = f[e].y;
+  return Pack<DT>::narrow(t);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Sums over a row in the row kernels: warps, then the CTA, then the cluster's
+// CTAs, as in fused_rows.cuh.  Every warp adds the warp partials itself, and
+// every thread the CTAs', in the same order, so all of the row hold the same
+// bits.  `x` counts the exchanges of the CTA; what exchange x writes is next
+// written in exchange x + 2, after the CTA's barrier of x + 1, which a thread
+// reaches only once it has read x's.
+struct RowSums {
+  float warp[2][3][32];
+  float4 part[2][8];    // the cluster's partials
+  uint64_t bar[2];
+};
+
+__device__ __forceinline__ void row_sums_init(RowSums& s, int cluster) {  // one thread, before a barrier
+  if (cluster > 1) {
+    mbar_init(&s.bar[0], 1);
+    mbar_init(&s.bar[1], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+}
+
+// v becomes the sums over the row; NaN for a thread whose wait for its peers
+// runs out (it then waits until their partials have landed, bounded again, so
+// that none reaches a CTA that has exited and the phases stay in step).
+template <int NS>
+__device__ __forceinline__ void row_sums(RowSums& s, float (&v)[NS], uint32_t x, int cluster, int crank, uint64_t wait_ns,
+                                         unsigned int* err) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  const uint32_t b = x & 1u, par = (x >> 1) & 1u;
+#pragma unroll
+  for (int i = 0; i < NS; i++) {
+    v[i] = warp_total(v[i]);
+    if (lane == 0) s.warp[b][i][warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NS; i++) v[i] = warp_total(lane < nwarps ? s.warp[b][i][lane] : 0.f);
+  if (cluster == 1) return;
+  if (warp == 0) {
+    constexpr uint32_t bytes = NS == 1 ? 4u : NS == 2 ? 8u : 16u;
+    if (lane == 0) mbar_arrive_expect_tx(&s.bar[b], bytes * (uint32_t)cluster);
+    if (lane < cluster) {
+      const uint32_t to = map_rank(&s.part[b][crank], (uint32_t)lane), bar = map_rank(&s.bar[b], (uint32_t)lane);
+      if constexpr (NS == 1) st_async_f32(to, v[0], bar);
+      if constexpr (NS > 1) st_async_v2_b32(to, __float_as_uint(v[0]), __float_as_uint(v[1]), bar);
+      if constexpr (NS > 2) st_async_v2_b32(to + 8u, __float_as_uint(v[2]), 0u, bar);
+    }
+  }
+  if (wait_cluster_phase(&s.bar[b], par, wait_ns)) {
+#pragma unroll
+    for (int i = 0; i < NS; i++) v[i] = reinterpret_cast<const float*>(&s.part[b][0])[i];
+    for (int r = 1; r < cluster; r++) {
+#pragma unroll
+      for (int i = 0; i < NS; i++) v[i] += reinterpret_cast<const float*>(&s.part[b][r])[i];
+    }
+  } else {
+    atomicOr(err, 1u);
+#pragma unroll
+    for (int i = 0; i < NS; i++) v[i] = __int_as_float(0x7fc00000);
+    if (!wait_cluster_phase(&s.bar[b], par)) atomicOr(err, 2u);
+  }
+}
+
+}  // namespace
+}  // namespace car

@@ -1,0 +1,77 @@
+// branch.h -- launch entry points of the kernels of a block's branch: the norm
+// behind the block, gate, dropout and residual scale between rank sum and
+// residual add (internal; arguments are checked in branch_api.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "car_launch.h"
+
+namespace car {
+
+struct DropParams {
+  uint32_t key0, key1;
+  uint64_t offset;
+  const uint64_t* offset_dev;  // added to offset by the kernel; may be null
+  uint32_t threshold;          // of 65536; 0: nothing is dropped
+  float scale;                 // of what is kept
+};
+
+// Pointers are device memory; what may be null is missing then.
+struct BranchArgs {
+  const void* norm_weight;  // may be null
+  float norm_eps;
+  const void* gate;         // may be null
+  int64_t gate_span;        // rows that share a gate row; 0: each has its own
+  float residual_scale;
+  DropParams drop;
+};
+struct BranchGradArgs {
+  const void* ar;           // may be null where nothing reads it
+  const void* h;
+  const void* dres;         // may be null
+  void* dx;
+  void* dresidual;          // may be null
+  float* dweight;           // may be null
+  float* dnorm_weight;      // may be null
+  void* dgate;              // may be null
+  float* workspace;
+};
+
+// ---- dropout of the rank sum (dropout.cu) ----
+cudaError_t dropout_occupancy(int dtype, int W, int* blocks_per_sm);
+int dropout_vectors_per_thread(int W);
+cudaError_t launch_dropout(int dtype, int W, const RankPtrs& in, const DropParams& drop, void* out, int64_t nvec, int grid,
+                           cudaStream_t s);
+
+// ---- forward (branch_rows.cu) ----
+constexpr int kBranchThreads = 512;
+cudaError_t branch_resident_groups(int dtype, int W, const FusedShape& sh, int num_sms, int* groups);
+cudaError_t launch_branch(int dtype, int W, const RankPtrs& in, const BranchArgs& br, const void* residual,
+                          const void* weight, float eps, void* residual_out, void* norm_out, void* ar_out,
+                          unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh,
+                          const WaitHook& hook, cudaStream_t s);
+
+// ---- backward (branch_backward.cu) ----
+// CTAs (or clusters) take contiguous spans of rows: the g-th of n starts here.
+__host__ __device__ inline int64_t span_start(int64_t rows, int n, int g) {
+  return (int64_t)((uint64_t)rows * (uint64_t)g / (uint64_t)n);
+}
+// Most CTAs (or clusters) that leave partial sums.
+constexpr int kMaxBranchGroups = 304;
+// Floats of the workspace for `groups` of them (0 for one): partials of dweight
+// and dnorm_weight, and for a gate that rows share two partial rows of dgate
+// (the gate rows that the span's ends may cut).
+inline size_t branch_workspace_floats(int groups, int64_t cols, bool shared_gate) {
+  return groups == 1 ? 0 : (size_t)groups * (size_t)cols * (shared_gate ? 4 : 2);
+}
+cudaError_t branch_backward_resident_groups(int dtype, int W, const FusedShape& sh, int num_sms, int* groups);
+cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
+                                   const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
+                                   int vec_per_row, const FusedShape& sh, const WaitHook& hook, cudaStream_t s);
+// The sum of the groups' partials, behind either backward kernel.
+cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, int dtype, int groups, int64_t rows,
+                               int64_t cols, cudaStream_t s);
+
+}  // namespace car

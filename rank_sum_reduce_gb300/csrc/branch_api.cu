@@ -1,0 +1,246 @@
+// branch_api.cu -- C ABI of what lies between the rank sum and the residual add
+// (include/car.h: car_reduce_dropout, car_reduce_branch_*): argument checks and
+// launch shapes.  The kernels are in dropout.cu, branch_rows.cu and
+// branch_backward.cu.
+#include <cmath>
+#include <cstring>
+
+#include "branch.h"
+#include "handle.h"
+
+using namespace car;
+
+namespace {
+
+bool finite_eps(float eps) { return std::isfinite(eps) && eps >= 0.f; }
+
+car_status drop_params(const car_dropout* d, DropParams* out) {
+  *out = DropParams{0, 0, 0, nullptr, 0, 1.f};
+  if (!d) return CAR_OK;
+  if (!(d->p >= 0.f && d->p <= 1.f)) return CAR_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(d->offset_dev) & 7u) return CAR_ERR_ALIGN;
+  out->threshold = (uint32_t)std::floor((double)d->p * 65536.0 + 0.5);
+  out->scale = out->threshold == 65536u ? 0.f : (float)(65536.0 / (65536.0 - out->threshold));
+  out->key0 = (uint32_t)d->seed;
+  out->key1 = (uint32_t)(d->seed >> 32);
+  out->offset = d->offset;
+  out->offset_dev = d->offset_dev;
+  return CAR_OK;
+}
+
+// Rows that share a row of the gate (0: each has its own); -1: not a divisor.
+int64_t gate_span(const car_ctx* h, int64_t gate_rows) {
+  if (gate_rows == 0) return 0;
+  return gate_rows < 0 || gate_rows > h->M || h->M % gate_rows != 0 ? -1 : h->M / gate_rows;
+}
+
+car_status branch_args(const car_ctx* h, const car_branch* b, BranchArgs* out) {
+  if (!b) return CAR_ERR_ARG;
+  if (!std::isfinite(b->residual_scale) || (b->norm_weight && !finite_eps(b->norm_eps))) return CAR_ERR_ARG;
+  if (!aligned16(b->norm_weight) || !aligned16(b->gate)) return CAR_ERR_ALIGN;
+  out->norm_weight = b->norm_weight;
+  out->norm_eps = b->norm_weight ? b->norm_eps : 0.f;
+  out->gate = b->gate;
+  out->gate_span = b->gate ? gate_span(h, b->gate_rows) : 1;
+  if (out->gate_span < 0) return CAR_ERR_ARG;
+  out->residual_scale = b->residual_scale;
+  return drop_params(b->dropout, &out->drop);
+}
+
+size_t gate_bytes(const car_ctx* h, const BranchArgs& b) {
+  return b.gate ? (size_t)(b.gate_span == 0 ? h->M : h->M / b.gate_span) * (size_t)h->N * h->es : 0;
+}
+
+// Buffers of a call: every output must be apart from all others, but for the
+// inputs that it may replace (the same address, the same size).
+struct Buffers {
+  struct Range {
+    uintptr_t at;
+    size_t bytes;
+    bool output, replaceable;
+  };
+  Range r[2 * kMaxRanks];
+  int n = 0;
+  void add(const void* p, size_t bytes, bool output, bool replaceable = false) {
+    if (p && bytes) r[n++] = Range{reinterpret_cast<uintptr_t>(p), bytes, output, replaceable};
+  }
+  bool clash() const {
+    for (int i = 0; i < n; i++) {
+      if (!r[i].output) continue;
+      for (int j = 0; j < n; j++) {
+        if (i == j || r[j].at >= r[i].at + r[i].bytes || r[i].at >= r[j].at + r[j].bytes) continue;
+        if (r[j].output || !r[j].replaceable || !r[i].replaceable || r[i].at != r[j].at) return true;
+      }
+    }
+    return false;
+  }
+};
+
+car_status prepare_dropout(car_ctx* h) {
+  if (h->dropout_ready.load(std::memory_order_acquire)) return CAR_OK;
+  std::lock_guard<std::mutex> lk(h->shapes);
+  if (h->dropout_ready.load(std::memory_order_relaxed)) return CAR_OK;
+  const OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_fail(on.status, "device of the handle");
+  int per_sm = 0;
+  cudaError_t e = dropout_occupancy(h->dtype, h->W, &per_sm);
+  if (e != cudaSuccess) return cuda_fail(e, "dropout occupancy");
+  const int64_t per_cta = (int64_t)kReduceThreads * dropout_vectors_per_thread(h->W);
+  h->dropout_grid = (int)std::min<int64_t>((h->nvec + per_cta - 1) / per_cta, (int64_t)std::max(per_sm, 1) * h->num_sms);
+  h->dropout_ready.store(true, std::memory_order_release);
+  return CAR_OK;
+}
+
+bool one_vector(int, int vpt) { return vpt == 1; }
+int branch_threads(int, int) { return kBranchThreads; }
+
+car_status prepare_branch(car_ctx* h) {
+  if (h->branch_ready.load(std::memory_order_acquire)) return CAR_OK;
+  std::lock_guard<std::mutex> lk(h->shapes);
+  if (h->branch_ready.load(std::memory_order_relaxed)) return CAR_OK;
+  const OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_fail(on.status, "device of the handle");
+  int groups = 0;
+  h->branch = row_split_shape(h->W, h->M, h->vec_per_row, h->num_sms, one_vector, branch_threads, false);
+  cudaError_t e = branch_resident_groups(h->dtype, h->W, h->branch, h->num_sms, &groups);
+  if (e != cudaSuccess) return cuda_fail(e, "branch occupancy");
+  h->branch.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
+  h->branch_ready.store(true, std::memory_order_release);
+  return CAR_OK;
+}
+
+car_status prepare_branch_backward(car_ctx* h) {
+  if (h->branch_backward_ready.load(std::memory_order_acquire)) return CAR_OK;
+  std::lock_guard<std::mutex> lk(h->shapes);
+  if (h->branch_backward_ready.load(std::memory_order_relaxed)) return CAR_OK;
+  const OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_fail(on.status, "device of the handle");
+  int groups = 0;
+  h->branch_backward = row_split_shape(h->W, h->M, h->vec_per_row, h->num_sms, one_vector, branch_threads, false);
+  cudaError_t e = branch_backward_resident_groups(h->dtype, h->W, h->branch_backward, h->num_sms, &groups);
+  if (e != cudaSuccess) return cuda_fail(e, "branch backward occupancy");
+  h->branch_backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
+  h->branch_backward_ready.store(true, std::memory_order_release);
+  return CAR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+car_status car_reduce_dropout(car_ctx* h, const void* const* inputs, const car_dropout* drop, void* ar_out, void* stream) {
+  car_status st = check_handle(h);
+  if (st != CAR_OK) return st;
+  if (!drop) return CAR_ERR_ARG;
+  DropParams d;
+  if ((st = drop_params(drop, &d)) != CAR_OK) return st;
+  RankPtrs tbl;
+  if ((st = check_table(h, inputs, &tbl)) != CAR_OK) return st;
+  if ((st = check_dev(ar_out)) != CAR_OK) return st;
+  if ((st = prepare_dropout(h)) != CAR_OK) return st;
+  cudaError_t e = launch_dropout(h->dtype, h->W, tbl, d, ar_out, h->nvec, h->dropout_grid, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_dropout launch");
+}
+
+car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inputs, const car_branch* branch,
+                                              const void* residual, const void* weight, float eps, void* residual_out,
+                                              void* norm_out, void* ar_out, void* stream) {
+  car_status st = check_handle(h);
+  if (st != CAR_OK) return st;
+  if (!finite_eps(eps)) return CAR_ERR_ARG;
+  BranchArgs b;
+  if ((st = branch_args(h, branch, &b)) != CAR_OK) return st;
+  RankPtrs tbl;
+  if ((st = check_table(h, inputs, &tbl)) != CAR_OK) return st;
+  if ((st = check_dev(residual)) != CAR_OK) return st;
+  if ((st = check_dev(weight)) != CAR_OK) return st;
+  if ((st = check_dev(residual_out)) != CAR_OK) return st;
+  if ((st = check_dev(norm_out)) != CAR_OK) return st;
+  if (!aligned16(ar_out)) return CAR_ERR_ALIGN;
+  if (!h->fused_ok) return CAR_ERR_SIZE;
+  const size_t D = (size_t)h->D, row = (size_t)h->N * h->es;
+  // residual_out may replace residual, ar_out one input: anything else clashes
+  Buffers at;
+  for (int r = 0; r < h->W; r++) at.add(tbl.p[r] == ar_out ? nullptr : tbl.p[r], D, false);
+  at.add(residual == residual_out ? nullptr : residual, D, false);
+  at.add(weight, row, false);
+  at.add(b.norm_weight, row, false);
+  at.add(b.gate, gate_bytes(h, b), false);
+  at.add(b.drop.offset_dev, 8, false);
+  at.add(residual_out, D, true);
+  at.add(norm_out, D, true);
+  at.add(ar_out, D, true);
+  if (at.clash()) return CAR_ERR_ARG;
+  if ((st = prepare_branch(h)) != CAR_OK) return st;
+  cudaError_t e = launch_branch(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M,
+                                h->N, h->vec_per_row, h->branch, h->hook, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_branch_residual_rmsnorm launch");
+}
+
+size_t car_branch_workspace_bytes(car_ctx* h, const car_branch* branch) {
+  if (!live(h) || !h->fused_ok) return 0;
+  const bool gate = branch && branch->gate;
+  const int64_t span = gate ? gate_span(h, branch->gate_rows) : 0;
+  if (span < 0 || prepare_branch_backward(h) != CAR_OK) return 0;
+  return branch_workspace_floats(h->branch_backward.groups, h->N, span > 0) * sizeof(float);
+}
+
+car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const car_branch* branch,
+                                                       const void* ar, const void* residual_out, const void* weight,
+                                                       float eps, const void* dresidual_out, const car_branch_grads* out,
+                                                       void* workspace, void* stream) {
+  car_status st = check_handle(h);
+  if (st != CAR_OK) return st;
+  if (!finite_eps(eps) || !out) return CAR_ERR_ARG;
+  BranchArgs b;
+  if ((st = branch_args(h, branch, &b)) != CAR_OK) return st;
+  RankPtrs tbl;
+  if ((st = check_table(h, dnorm, &tbl)) != CAR_OK) return st;
+  if ((st = check_dev(residual_out)) != CAR_OK) return st;
+  if ((st = check_dev(weight)) != CAR_OK) return st;
+  if ((st = check_dev(out->dx)) != CAR_OK) return st;
+  if ((out->dnorm_weight && !b.norm_weight) || (out->dgate && !b.gate)) return CAR_ERR_ARG;
+  if (!ar && (b.norm_weight || out->dgate)) return CAR_ERR_ARG;
+  if (!aligned16(ar) || !aligned16(dresidual_out) || !aligned16(out->dresidual) || !aligned16(out->dweight) ||
+      !aligned16(out->dnorm_weight) || !aligned16(out->dgate) || !aligned16(workspace))
+    return CAR_ERR_ALIGN;
+  if (!h->fused_ok) return CAR_ERR_SIZE;
+  if ((st = prepare_branch_backward(h)) != CAR_OK) return st;
+  const int groups = h->branch_backward.groups;
+  const bool shared = b.gate && b.gate_span > 0;
+  const bool sums = out->dweight || out->dnorm_weight || (shared && out->dgate);
+  const size_t floats = sums ? branch_workspace_floats(groups, h->N, shared) : 0;
+  if (floats && !workspace) return CAR_ERR_ARG;
+  const size_t D = (size_t)h->D, row = (size_t)h->N * h->es;
+  Buffers at;
+  for (int r = 0; r < h->W; r++) at.add(tbl.p[r], D, false, true);
+  at.add(ar, D, false, true);
+  at.add(residual_out, D, false, true);
+  at.add(dresidual_out, D, false, true);
+  at.add(weight, row, false);
+  at.add(b.norm_weight, row, false);
+  at.add(b.gate, gate_bytes(h, b), false);
+  at.add(b.drop.offset_dev, 8, false);
+  at.add(out->dx, D, true, true);
+  at.add(out->dresidual, D, true, true);
+  at.add(out->dweight, (size_t)h->N * 4, true);
+  at.add(out->dnorm_weight, (size_t)h->N * 4, true);
+  at.add(out->dgate, shared ? gate_bytes(h, b) / h->es * 4 : gate_bytes(h, b), true);
+  at.add(workspace, floats * sizeof(float), true);
+  if (at.clash()) return CAR_ERR_ARG;
+  BranchGradArgs g;
+  g.ar = ar;
+  g.h = residual_out;
+  g.dres = dresidual_out;
+  g.dx = out->dx;
+  g.dresidual = out->dresidual;
+  g.dweight = out->dweight;
+  g.dnorm_weight = out->dnorm_weight;
+  g.dgate = out->dgate;
+  g.workspace = static_cast<float*>(workspace);
+  cudaError_t e = launch_branch_backward(h->dtype, h->W, tbl, b, g, weight, eps, h->d_err, h->M, h->N, h->vec_per_row,
+                                         h->branch_backward, h->hook, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_branch_residual_rmsnorm_backward launch");
+}
+
+}  // extern "C"
