@@ -10,37 +10,50 @@
 namespace car {
 namespace {
 
-// One block of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random
-// numbers: as easy as 1, 2, 3", SC 2011, section 4.3): ten rounds of two wide
-// products each.  The round keys depend on the launch alone, so they live in
-// uniform registers; a round costs a thread two wide products and two
-// three-input XORs, about 60 instructions for the 8 elements of a vector, a
-// quarter of what a branch's backward needs for them.
-__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy
+// as 1, 2, 3", SC 2011, section 4.3): ten rounds of two wide products, for the 8
+// elements of one counter.  A launch has one key and one offset, and there are
+// fewer than 2^32 counters (a handle's data is at most 2^35 bytes), so three of the
+// counter's four words are the same for all threads: one product of the first round
+// and one of the second are too.  They are taken out of the loops (DropState); the
+// other 18, at a quarter of the rate of other instructions, are what the generator
+// costs (W = 1, M = 16389, N = 4096 bf16, forward with both norms: see branch_tma.cu).
+struct DropState {
+  uint32_t k0, k1;   // the key
+  uint32_t z, y, hi, lo;
+};
+__device__ __forceinline__ DropState drop_state(const DropParams& d) {  // after the wait for the grids it depends on
+  const uint64_t offset = d.offset + (d.offset_dev ? *static_cast<const volatile uint64_t*>(d.offset_dev) : 0ull);
+  DropState s;
+  s.k0 = d.key0;
+  s.k1 = d.key1;
+  const uint64_t b = (uint64_t)(uint32_t)offset * 0xCD9E8D57u;
+  const uint64_t a = (uint64_t)((uint32_t)(b >> 32) ^ s.k0) * 0xD2511F53u;  // of the second round
+  s.z = (uint32_t)(offset >> 32) ^ s.k1;
+  s.y = (uint32_t)b ^ (s.k0 + 0x9E3779B9u);
+  s.hi = (uint32_t)(a >> 32) ^ (s.k1 + 0xBB67AE85u);
+  s.lo = (uint32_t)a;
+  return s;
+}
+__device__ __forceinline__ uint4 philox4x32_10(const DropState& s, uint32_t counter) {
+  const uint64_t a1 = (uint64_t)counter * 0xD2511F53u;
+  const uint64_t b2 = (uint64_t)((uint32_t)(a1 >> 32) ^ s.z) * 0xCD9E8D57u;
+  uint4 c = make_uint4((uint32_t)(b2 >> 32) ^ s.y, (uint32_t)b2, s.hi ^ (uint32_t)a1, s.lo);
 #pragma unroll
-  for (int r = 0; r < 10; r++) {
+  for (uint32_t r = 2; r < 10; r++) {
     const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
-    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ (s.k0 + r * 0x9E3779B9u), (uint32_t)b,
+                   (uint32_t)(a >> 32) ^ c.w ^ (s.k1 + r * 0xBB67AE85u), (uint32_t)a);
   }
   return c;
-}
-
-// The generator's offset as the kernel runs; after the wait for the grids it
-// depends on.
-__device__ __forceinline__ uint64_t drop_offset(const DropParams& d) {
-  return d.offset + (d.offset_dev ? *static_cast<const volatile uint64_t*>(d.offset_dev) : 0ull);
 }
 
 // The 16 random bits of the E elements of the vector `v` of the [M, N] problem
 // (v counts 16-byte vectors), two in a word.  A 16-bit type has one counter per
 // vector; an fp32 vector is half of one's eight elements.
 template <int E>
-__device__ __forceinline__ void drop_bits(const DropParams& d, uint64_t offset, int64_t v, uint32_t (&bits)[E / 2]) {
-  const uint64_t c = (uint64_t)(E == 8 ? v : v >> 1);
-  const uint4 w = philox4x32_10(make_uint4((uint32_t)c, (uint32_t)(c >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)),
-                                d.key0, d.key1);
+__device__ __forceinline__ void drop_bits(const DropState& s, int64_t v, uint32_t (&bits)[E / 2]) {
+  const uint4 w = philox4x32_10(s, (uint32_t)(E == 8 ? v : v >> 1));
   if constexpr (E == 8) {
     bits[0] = w.x;
     bits[1] = w.y;
@@ -52,11 +65,12 @@ __device__ __forceinline__ void drop_bits(const DropParams& d, uint64_t offset, 
   }
 }
 
-// Element pair of a word: dropped below the threshold (selected, not
-// multiplied, so that what is dropped may be anything), else scaled.
+// Element pair of a word: kept, and scaled, where its 16 bits as the upper half of
+// a word exceed the limit; else 0 (selected, not multiplied, so that what is
+// dropped may be anything).
 __device__ __forceinline__ float2 drop2(const DropParams& d, uint32_t bits, float2 x) {
   const float2 s = mul2(x, make_float2(d.scale, d.scale));
-  return make_float2((bits & 0xFFFFu) >= d.threshold ? s.x : 0.f, (bits >> 16) >= d.threshold ? s.y : 0.f);
+  return make_float2((bits << 16) > d.limit ? s.x : 0.f, bits > d.limit ? s.y : 0.f);
 }
 
 __device__ __forceinline__ float warp_total(float v) {

@@ -14,7 +14,8 @@ struct DropParams {
   uint32_t key0, key1;
   uint64_t offset;
   const uint64_t* offset_dev;  // added to offset by the kernel; may be null
-  uint32_t threshold;          // of 65536; 0: nothing is dropped
+  bool active;                 // something is dropped
+  uint32_t limit;              // 65536 t - 1, t of 65536 being dropped
   float scale;                 // of what is kept
 };
 
@@ -53,6 +54,39 @@ cudaError_t launch_branch(int dtype, int W, const RankPtrs& in, const BranchArgs
                           unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh,
                           const WaitHook& hook, cudaStream_t s);
 
+struct BranchTeams : TeamShape {
+  int tile_rows;  // rows of a tile, at most teams
+};
+// ---- forward, many rows (branch_tma.cu); false when a row is too long ----
+bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
+// Whether this call's slices and weights fit beside one another.
+bool branch_tma_fits(int dtype, int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh);
+cudaError_t branch_tma_prepare(int dtype, const BranchTeams& sh);
+cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const BranchArgs& br, const void* residual,
+                              const void* weight, float eps, void* residual_out, void* norm_out, void* ar_out,
+                              unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const BranchTeams& sh,
+                              cudaStream_t s);
+// The ring of either pipeline (branch_ring.cuh).
+constexpr int kMaxRingStages = 32;
+struct RingPlan {
+  int rows;
+  int row_bytes;
+  int vec_per_row;
+  int ranks;            // slices of a tile that are summed
+  int held;             // slices that a row needs to its end
+  int group;            // slices that a stage has room for
+  int tile_stages;      // stages of a tile
+  int stages;           // of the ring
+  int teams;            // teams of consumer warps, of which each takes a row of a tile
+  int tile_rows;        // at most teams
+  int producers;        // threads, each in a warp of its own, that issue a stage's copies
+  int team_threads;     // multiple of 32
+  uint32_t gate_span;   // tiles end where a gate row's rows end; 0: they need not
+};
+// Chooses group, tile_stages and stages for `budget` bytes; false when the ring
+// would be too small.
+bool branch_ring_fit(int budget, RingPlan* p);
+
 // ---- backward (branch_backward.cu) ----
 // CTAs (or clusters) take contiguous spans of rows: the g-th of n starts here.
 __host__ __device__ inline int64_t span_start(int64_t rows, int n, int g) {
@@ -70,6 +104,15 @@ cudaError_t branch_backward_resident_groups(int dtype, int W, const FusedShape& 
 cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                    const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
                                    int vec_per_row, const FusedShape& sh, const WaitHook& hook, cudaStream_t s);
+// Backward, many rows (branch_backward_tma.cu); false when a row is too long.
+bool branch_backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
+// Whether this call's slices and sums fit beside one another.
+bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
+                              const BranchTeams& sh);
+cudaError_t branch_backward_tma_prepare(int dtype, const BranchTeams& sh);
+cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
+                                       const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
+                                       int vec_per_row, const BranchTeams& sh, cudaStream_t s);
 // The sum of the groups' partials, behind either backward kernel.
 cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, int dtype, int groups, int64_t rows,
                                int64_t cols, cudaStream_t s);

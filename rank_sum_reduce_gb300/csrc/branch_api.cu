@@ -1,7 +1,7 @@
 // branch_api.cu -- C ABI of what lies between the rank sum and the residual add
 // (include/car.h: car_reduce_dropout, car_reduce_branch_*): argument checks and
-// launch shapes.  The kernels are in dropout.cu, branch_rows.cu and
-// branch_backward.cu.
+// launch shapes.  The kernels are in dropout.cu, branch_rows.cu, branch_tma.cu,
+// branch_backward.cu and branch_backward_tma.cu.
 #include <cmath>
 #include <cstring>
 
@@ -15,16 +15,18 @@ namespace {
 bool finite_eps(float eps) { return std::isfinite(eps) && eps >= 0.f; }
 
 car_status drop_params(const car_dropout* d, DropParams* out) {
-  *out = DropParams{0, 0, 0, nullptr, 0, 1.f};
+  *out = DropParams{0, 0, 0, nullptr, false, 0, 1.f};
   if (!d) return CAR_OK;
   if (!(d->p >= 0.f && d->p <= 1.f)) return CAR_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(d->offset_dev) & 7u) return CAR_ERR_ALIGN;
-  out->threshold = (uint32_t)std::floor((double)d->p * 65536.0 + 0.5);
-  out->scale = out->threshold == 65536u ? 0.f : (float)(65536.0 / (65536.0 - out->threshold));
+  const uint64_t t = (uint64_t)std::floor((double)d->p * 65536.0 + 0.5);
+  out->active = t > 0;
+  out->limit = t > 0 ? (uint32_t)((t << 16) - 1) : 0;
+  out->scale = t == 65536 ? 0.f : (float)(65536.0 / (65536.0 - (double)t));
   out->key0 = (uint32_t)d->seed;
   out->key1 = (uint32_t)(d->seed >> 32);
   out->offset = d->offset;
-  out->offset_dev = d->offset_dev;
+  out->offset_dev = out->active ? d->offset_dev : nullptr;
   return CAR_OK;
 }
 
@@ -94,6 +96,10 @@ car_status prepare_dropout(car_ctx* h) {
 bool one_vector(int, int vpt) { return vpt == 1; }
 int branch_threads(int, int) { return kBranchThreads; }
 
+// When the pipeline is faster than the row kernel.
+bool branch_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
+bool branch_backward_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
+
 car_status prepare_branch(car_ctx* h) {
   if (h->branch_ready.load(std::memory_order_acquire)) return CAR_OK;
   std::lock_guard<std::mutex> lk(h->shapes);
@@ -105,6 +111,9 @@ car_status prepare_branch(car_ctx* h) {
   cudaError_t e = branch_resident_groups(h->dtype, h->W, h->branch, h->num_sms, &groups);
   if (e != cudaSuccess) return cuda_fail(e, "branch occupancy");
   h->branch.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
+  h->branch_pipeline = branch_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_tma) && branch_pipeline_pays(h, h->branch_tma);
+  if (h->branch_pipeline && (e = branch_tma_prepare(h->dtype, h->branch_tma)) != cudaSuccess)
+    return cuda_fail(e, "branch pipeline smem");
   h->branch_ready.store(true, std::memory_order_release);
   return CAR_OK;
 }
@@ -120,8 +129,19 @@ car_status prepare_branch_backward(car_ctx* h) {
   cudaError_t e = branch_backward_resident_groups(h->dtype, h->W, h->branch_backward, h->num_sms, &groups);
   if (e != cudaSuccess) return cuda_fail(e, "branch backward occupancy");
   h->branch_backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
+  h->branch_backward_pipeline =
+      branch_backward_tma_shape(h->dtype, h->M, h->vec_per_row, h->num_sms, &h->branch_backward_tma) &&
+      branch_backward_pipeline_pays(h, h->branch_backward_tma);
+  if (h->branch_backward_pipeline && (e = branch_backward_tma_prepare(h->dtype, h->branch_backward_tma)) != cudaSuccess)
+    return cuda_fail(e, "branch backward pipeline smem");
   h->branch_backward_ready.store(true, std::memory_order_release);
   return CAR_OK;
+}
+
+// CTAs (or clusters) of whichever kernel a call runs: which one is, where the
+// pipeline pays, found at the call (its parts decide whether a row fits).
+int workspace_groups(const car_ctx* h) {
+  return std::max(h->branch_backward.groups, h->branch_backward_pipeline ? h->branch_backward_tma.grid : 0);
 }
 
 }  // namespace
@@ -172,8 +192,14 @@ car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inp
   at.add(ar_out, D, true);
   if (at.clash()) return CAR_ERR_ARG;
   if ((st = prepare_branch(h)) != CAR_OK) return st;
-  cudaError_t e = launch_branch(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M,
-                                h->N, h->vec_per_row, h->branch, h->hook, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (h->branch_pipeline && branch_tma_fits(h->dtype, h->W, b, h->M, h->vec_per_row, h->branch_tma))
+    e = launch_branch_tma(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M, h->N,
+                          h->vec_per_row, h->branch_tma, s);
+  else
+    e = launch_branch(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M, h->N,
+                      h->vec_per_row, h->branch, h->hook, s);
   return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_branch_residual_rmsnorm launch");
 }
 
@@ -182,7 +208,7 @@ size_t car_branch_workspace_bytes(car_ctx* h, const car_branch* branch) {
   const bool gate = branch && branch->gate;
   const int64_t span = gate ? gate_span(h, branch->gate_rows) : 0;
   if (span < 0 || prepare_branch_backward(h) != CAR_OK) return 0;
-  return branch_workspace_floats(h->branch_backward.groups, h->N, span > 0) * sizeof(float);
+  return branch_workspace_floats(workspace_groups(h), h->N, span > 0) * sizeof(float);
 }
 
 car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const car_branch* branch,
@@ -206,7 +232,7 @@ car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* c
     return CAR_ERR_ALIGN;
   if (!h->fused_ok) return CAR_ERR_SIZE;
   if ((st = prepare_branch_backward(h)) != CAR_OK) return st;
-  const int groups = h->branch_backward.groups;
+  const int groups = workspace_groups(h);
   const bool shared = b.gate && b.gate_span > 0;
   const bool sums = out->dweight || out->dnorm_weight || (shared && out->dgate);
   const size_t floats = sums ? branch_workspace_floats(groups, h->N, shared) : 0;
@@ -238,8 +264,14 @@ car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* c
   g.dnorm_weight = out->dnorm_weight;
   g.dgate = out->dgate;
   g.workspace = static_cast<float*>(workspace);
-  cudaError_t e = launch_branch_backward(h->dtype, h->W, tbl, b, g, weight, eps, h->d_err, h->M, h->N, h->vec_per_row,
-                                         h->branch_backward, h->hook, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (h->branch_backward_pipeline && branch_backward_tma_fits(h->dtype, h->W, b, g, h->M, h->vec_per_row, h->branch_backward_tma))
+    e = launch_branch_backward_tma(h->dtype, h->W, tbl, b, g, weight, eps, h->d_err, h->M, h->N, h->vec_per_row,
+                                   h->branch_backward_tma, s);
+  else
+    e = launch_branch_backward(h->dtype, h->W, tbl, b, g, weight, eps, h->d_err, h->M, h->N, h->vec_per_row,
+                               h->branch_backward, h->hook, s);
   return e == cudaSuccess ? CAR_OK : cuda_fail(e, "reduce_branch_residual_rmsnorm_backward launch");
 }
 

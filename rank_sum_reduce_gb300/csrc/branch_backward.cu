@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
   }
   prefetch_row(p, n, first, end, col0);
   pdl_wait_and_release();
-  const uint64_t offset = drop_offset(p.drop);
+  const DropState state = drop_state(p.drop);
   const int v = threadIdx.x;
   const bool ok = v < p.chunk && col0 + v < p.vec_per_row;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
       if (p.gate) gv = __ldg(p.gate + (int64_t)b * p.vec_per_row + col0 + v);
     }
     uint32_t bits[E / 2];
-    if (p.drop.threshold) drop_bits<E>(p.drop, offset, at, bits);
+    if (p.drop.active) drop_bits<E>(state, at, bits);
     float2 g[E / 2];
     float s[NORM ? 3 : 2] = {};
     if (ok) {
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
         hf[e] = mul2(g[e], both(p.residual_scale));
       }
       if (p.dresidual) st16(p.dresidual + at, narrow2<DT>(hf));
-      if (p.drop.threshold) {
+      if (p.drop.active) {
 #pragma unroll
         for (int e = 0; e < E / 2; e++) g[e] = drop2(p.drop, bits[e], g[e]);
       }

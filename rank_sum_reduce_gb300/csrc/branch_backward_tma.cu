@@ -1,0 +1,530 @@
+// branch_backward_tma.cu -- backward of a block's branch (branch_backward.cu)
+// for many rows: the slices dy_0 .. dy_{W-1}, h, the stored sum, the skip
+// gradient and a gate of each row's own stream through a ring of shared-memory
+// stages (branch_ring.cuh).  The sum of dy stays in registers and becomes dh, dz
+// and v in turn; the others are read again from their stage, which is held to the
+// row's end.
+//
+// Two vectors per thread: the weight and the factor norm_weight * gate (a gate of
+// all rows) lie in shared memory, in fp32.  Longer rows read the weights from
+// there packed, or from L2, and every gate row from L2.
+//
+// Column sums.  A thread sums g u and t (or gate t, where no gate row is shared)
+// over its team's rows in registers.  Where rows share a gate row, tiles end with
+// it: the teams' sums of t are then added in shared memory in team order, leave
+// as dgate or as a partial of the span (as in the row kernel), and gate * t goes
+// to dnorm_weight's sum in shared memory, where each column has one owner.
+#include <algorithm>
+
+#include "branch_ring.cuh"
+
+namespace car {
+namespace {
+
+
+struct BranchBackwardTmaParams {
+  RankPtrs dy;
+  const uint8_t* h;
+  const uint8_t* ar;         // may be null
+  const uint8_t* dres;       // may be null
+  const uint4* weight;
+  const uint4* norm_weight;
+  const uint4* gate;         // may be null
+  uint4* dx;
+  uint4* dresidual;          // may be null
+  uint4* dgate_own;          // [M, N], or null
+  float* dgate;              // as in the row kernel
+  float* part_w;
+  float* part_w1;
+  float* part_gate;
+  unsigned int* err;
+  DropParams drop;
+  float residual_scale;
+  float eps, norm_eps;
+  float inv_cols;
+  int gate_from;
+  uint32_t gate_span;        // rows that share a gate row
+  bool shared;               // t is summed by gate row
+  bool factor;               // dz is multiplied by a factor row: norm_weight, a gate of all rows or both
+  int weight_rows;           // rows of weights in shared memory, in fp32 or packed
+  int a_at, d_at, g_at;      // the stored sum, dres and gate behind h in their stage, in bytes
+  RingPlan ring;
+};
+
+// Slices of a tile: the ranks, h, then those of ar, dres and the gate that there are.
+__device__ __forceinline__ const uint8_t* slice_source(const BranchBackwardTmaParams& p, int q) {
+  if (q < p.ring.ranks) return static_cast<const uint8_t*>(p.dy.p[q]);
+  q -= p.ring.ranks;
+  if (q == 0) return p.h;
+  if (p.ar && --q == 0) return p.ar;
+  if (p.dres && --q == 0) return p.dres;
+  return reinterpret_cast<const uint8_t*>(p.gate);
+}
+
+template <int VPT>
+constexpr bool kWideRows = VPT == 2;
+
+// Weight row i (0: weight, 1: factor), vector v.
+template <int DT, int VPT>
+__device__ __forceinline__ void weight_at(const BranchBackwardTmaParams& p, const uint8_t* s_rows, int i, int v,
+                                          float2 (&f)[Pack<DT>::kN / 2]) {
+  const int V = p.ring.vec_per_row;
+  if constexpr (kWideRows<VPT>)
+    row_from_shared<DT>(s_rows + (size_t)i * V * Pack<DT>::kN * 4, V, v, f);
+  else
+    widen2<DT>(p.weight_rows ? lds16(s_rows + (size_t)i * p.ring.row_bytes + 16 * v) : __ldg((i == 0 ? p.weight : p.norm_weight) + v), f);
+}
+
+template <int DT, int VPT, bool NORM, int GATE, int DROP>
+__device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const uint8_t* ring, const uint8_t* s_rows,
+                                        float4* s_comb, float4* s_dw1, RingShared& s) {
+  constexpr int E = Pack<DT>::kN;
+  constexpr bool SHARED = GATE == kGateShared || GATE == kGateAny, OWN = GATE == kGateOwn || GATE == kGateAny;
+  const RingPlan& rp = p.ring;
+  const bool own = OWN && (GATE == kGateOwn || p.gate_from == kFromRing), shared = SHARED && p.shared;
+  const int T = rp.team_threads, V = rp.vec_per_row;
+  const int team = threadIdx.x / T, tid = threadIdx.x - team * T, lane = threadIdx.x & 31;
+  const uint8_t* mine = ring + (size_t)team * rp.row_bytes + 16 * tid;
+  const DropState state = drop_state(p.drop);
+  const int first = (int)span_start(rp.rows, gridDim.x, blockIdx.x);
+  float2 dw[VPT][E / 2], ts[VPT][E / 2];
+  bool ok[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; k++) {
+    ok[k] = tid + k * T < V;
+#pragma unroll
+    for (int e = 0; e < E / 2; e++) dw[k][e] = ts[k][e] = make_float2(0.f, 0.f);
+  }
+  // Adds the teams' sums of every column in team order and hands each column's
+  // four to `take`, in the same thread every time; false when a wait ran out.
+  // The wait before the teams' next sums are stored ends long before those come.
+  uint32_t combined = 0;
+  auto combine = [&](float2 (&acc)[VPT][E / 2], auto take) {
+    if (rp.teams == 1) {
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        if (ok[k]) {
+#pragma unroll
+          for (int e = 0; e < E / 2; e += 2)
+            take((tid + k * T) * (E / 4) + e / 2, make_float4(acc[k][e].x, acc[k][e].y, acc[k][e + 1].x, acc[k][e + 1].y));
+        }
+      }
+      return true;
+    }
+    if (combined && !wait_bounded(&s.done[1], (combined - 1u) & 1u, &s.abort)) return false;
+    float4* at = s_comb + (size_t)team * V * (E / 4);
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+      if (ok[k]) {
+#pragma unroll
+        for (int e = 0; e < E / 2; e += 2)
+          at[(tid + k * T) * (E / 4) + e / 2] = make_float4(acc[k][e].x, acc[k][e].y, acc[k][e + 1].x, acc[k][e + 1].y);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.done[0]);
+    if (!wait_bounded(&s.done[0], combined & 1u, &s.abort)) return false;
+    for (int i = threadIdx.x; i < V * (E / 4); i += rp.teams * T) {
+      float4 a = s_comb[i];
+      for (int k = 1; k < rp.teams; k++) {
+        const float4 b = s_comb[(size_t)k * V * (E / 4) + i];
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+      }
+      take(i, a);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.done[1]);
+    combined++;
+    return true;
+  };
+  // Columns 4 i .. 4 i + 3 of a row of T.
+  auto four = [&](const uint4* row, int i) {
+    if constexpr (E == 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(row) + i);
+      return f;
+    } else {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(row) + i);
+      float f[8];
+      Pack<DT>::widen(make_uint4(w.x, w.y, 0u, 0u), f);
+      return make_float4(f[0], f[1], f[2], f[3]);
+    }
+  };
+  // rows [from, to) of gate row b are in ts
+  auto flush = [&](uint32_t b, int from, int to) {
+    const int lo = (int)(b * p.gate_span);
+    const bool whole = from == lo && (uint32_t)(to - lo) == p.gate_span;
+    float4* out = nullptr;
+    if (p.dgate)
+      out = reinterpret_cast<float4*>(whole ? p.dgate : p.part_gate) +
+            (whole ? (int64_t)b : 2 * (int64_t)blockIdx.x + (from == first ? 0 : 1)) * V * (E / 4);
+    const bool done = combine(ts, [&](int i, float4 t) {
+      const float4 g = four(p.gate + (int64_t)b * V, i);
+      float4 d = s_dw1[i];
+      d.x = fmaf(g.x, t.x, d.x);
+      d.y = fmaf(g.y, t.y, d.y);
+      d.z = fmaf(g.z, t.z, d.z);
+      d.w = fmaf(g.w, t.w, d.w);
+      s_dw1[i] = d;
+      if (!out) return;
+      if (NORM && whole) {
+        const float4 w = four(p.norm_weight, i);
+        t = make_float4(t.x * w.x, t.y * w.y, t.z * w.z, t.w * w.w);
+      }
+      out[i] = t;
+    });
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+#pragma unroll
+      for (int e = 0; e < E / 2; e++) ts[k][e] = make_float2(0.f, 0.f);
+    }
+    return done;
+  };
+
+  RingReader in(rp, s);
+  uint32_t x = 0;
+  bool failed = false;
+  int from = first;
+  for (Tiles t(rp); t.more() && !failed;) {
+    const int tile = t.row;
+    if (team >= t.count(rp)) {
+      failed = !in.skip();
+    } else {
+      const int row = tile + team;
+      const int64_t at = (int64_t)row * V + tid;
+      float2 g[VPT][E / 2];
+      const uint8_t* held = ring_rank_sum<DT, VPT>(rp, in, mine, ok, g);
+      if (!held) {
+        failed = true;
+        break;
+      }
+      float2 hh = make_float2(0.f, 0.f), gwh = hh, aa = hh;
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        if (ok[k]) {
+          float2 hf[E / 2], wf[E / 2];
+          widen2<DT>(lds16(held + 16 * k * T), hf);
+          weight_at<DT, VPT>(p, s_rows, 0, tid + k * T, wf);
+#pragma unroll
+          for (int e = 0; e < E / 2; e++) {
+            hh = fma2(hf[e], hf[e], hh);
+            gwh = fma2(mul2(g[k][e], wf[e]), hf[e], gwh);
+          }
+          if constexpr (NORM) {
+            widen2<DT>(lds16(held + p.a_at + 16 * k * T), hf);
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) aa = fma2(hf[e], hf[e], aa);
+          }
+        }
+      }
+      float v[NORM ? 3 : 2];
+      v[0] = hh.x + hh.y;
+      v[1] = gwh.x + gwh.y;
+      if constexpr (NORM) v[NORM ? 2 : 0] = aa.x + aa.y;
+      if (!team_sums(rp, s, team, x++, v)) {
+        failed = true;
+        break;
+      }
+      const float r = rsqrtf(fmaf(v[0], p.inv_cols, p.eps));
+      const float2 m = both(-__fmul_rn(__fmul_rn(v[1], p.inv_cols), r));
+      const float2 qn = NORM ? both(rsqrtf(fmaf(v[NORM ? 2 : 0], p.inv_cols, p.norm_eps))) : both(1.f);
+      const uint4* grow = SHARED && p.gate_from == kFromRows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V + tid : nullptr;
+      float2 vu = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        if (ok[k]) {
+          float2 hf[E / 2], f[E / 2], d[E / 2];
+          widen2<DT>(lds16(held + 16 * k * T), hf);
+          weight_at<DT, VPT>(p, s_rows, 0, tid + k * T, f);
+          widen2<DT>(p.dres ? lds16(held + p.d_at + 16 * k * T) : make_uint4(0u, 0u, 0u, 0u), d);
+#pragma unroll
+          for (int e = 0; e < E / 2; e++) {
+            const float2 u = mul2(hf[e], both(r));
+            dw[k][e] = fma2(g[k][e], u, dw[k][e]);
+            g[k][e] = fma2(both(r), fma2(u, m, mul2(g[k][e], f[e])), d[e]);  // dh
+          }
+          if (p.dresidual) {
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) d[e] = mul2(g[k][e], both(p.residual_scale));
+            st16(p.dresidual + at + k * T, narrow2<DT>(d));
+          }
+          if (DROP == kDropYes || (DROP == kDropAny && p.drop.active)) {
+            uint32_t bits[E / 2];
+            drop_bits<E>(state, at + k * T, bits);
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) g[k][e] = drop2(p.drop, bits[e], g[k][e]);  // dz
+          }
+          float2 u1[E / 2];
+          if (NORM || (GATE && p.ar)) {
+            widen2<DT>(lds16(held + p.a_at + 16 * k * T), u1);
+            if constexpr (NORM) {
+#pragma unroll
+              for (int e = 0; e < E / 2; e++) u1[e] = mul2(u1[e], qn);
+            }
+          }
+          if (NORM || (SHARED && p.factor)) weight_at<DT, VPT>(p, s_rows, 1, tid + k * T, f);
+          if (own) {
+            widen2<DT>(lds16(held + p.g_at + 16 * k * T), d);
+            if (p.dgate_own) {
+#pragma unroll
+              for (int e = 0; e < E / 2; e++) {
+                const float2 dt = mul2(g[k][e], u1[e]);
+                hf[e] = NORM ? mul2(dt, f[e]) : dt;
+              }
+              st16(p.dgate_own + at + k * T, narrow2<DT>(hf));
+            }
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], d[e]);
+          }
+          if (NORM || shared) {
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) ts[k][e] = fma2(g[k][e], u1[e], ts[k][e]);
+          }
+          if (SHARED && p.gate_from == kFromRows) {
+            widen2<DT>(__ldg(grow + k * T), d);
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], d[e]);
+          }
+          if (NORM || (SHARED && p.factor)) {
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], f[e]);  // v
+          }
+          if constexpr (NORM) {
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) vu = fma2(g[k][e], u1[e], vu);
+          } else {
+            st16(p.dx + at + k * T, narrow2<DT>(g[k]));
+          }
+        }
+      }
+      if constexpr (NORM) {
+        float w[1] = {vu.x + vu.y};
+        if (!team_sums(rp, s, team, x++, w)) {
+          failed = true;
+          break;
+        }
+        // u1 * mean = a * (q * mean)
+        const float2 mean = both(-__fmul_rn(__fmul_rn(w[0], p.inv_cols), qn.x));
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+          if (ok[k]) {
+            float2 af[E / 2];
+            widen2<DT>(lds16(held + p.a_at + 16 * k * T), af);
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) af[e] = mul2(qn, fma2(af[e], mean, g[k][e]));
+            st16(p.dx + at + k * T, narrow2<DT>(af));
+          }
+        }
+      }
+      in.release();
+    }
+    if (failed) break;
+    const int cut = t.cut;
+    t.next(rp);
+    if (shared && (t.row == cut || !t.more())) {
+      if (!flush((uint32_t)tile / p.gate_span, from, t.row)) failed = true;
+      from = t.row;
+    }
+  }
+  const int64_t plane = (int64_t)blockIdx.x * V * (E / 4);
+  if (!failed && p.part_w)
+    failed = !combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane + i] = a; });
+  if (!failed && p.part_w1) {
+    float4* to = reinterpret_cast<float4*>(p.part_w1) + plane;
+    if (!shared)
+      failed = !combine(ts, [&](int i, float4 a) { to[i] = a; });
+    else if (rp.teams > 1)
+      for (int i = threadIdx.x; i < V * (E / 4); i += rp.teams * T) to[i] = s_dw1[i];
+    else
+      combine(ts, [&](int i, float4) { to[i] = s_dw1[i]; });
+  }
+  if (failed) {
+    atomicOr(p.err, 1u);
+    *static_cast<volatile int*>(&s.abort) = 1;
+  }
+}
+
+// 16-bit types with more than four vectors per thread and fp32 with more than six,
+// whose sums would not fit in registers, stay with the row kernel.
+template <int DT, int VPT, bool NORM, int GATE, int DROP>
+__global__ void __launch_bounds__(512 + 32 * kProducers, 1)
+    reduce_branch_rmsnorm_backward_tma_kernel(const __grid_constant__ BranchBackwardTmaParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ RingShared s;
+  const RingPlan& rp = p.ring;
+  constexpr int E = Pack<DT>::kN;
+  const int consumers = rp.teams * rp.team_threads, V = rp.vec_per_row;
+  uint8_t* s_rows = smem + (size_t)rp.stages * rp.group * rp.teams * rp.row_bytes;
+  float4* s_dw1 = reinterpret_cast<float4*>(s_rows + (size_t)p.weight_rows * (kWideRows<VPT> ? V * E * 4 : rp.row_bytes));
+  float4* s_comb = s_dw1 + (p.shared ? V * (E / 4) : 0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) ring_init(rp, s);
+  const Tiles first(rp);
+  if (warp == consumers >> 5 && lane < rp.ranks + rp.held && first.more())
+    prefetch_l2(slice_source(p, lane) + first.row * (int64_t)rp.row_bytes, (uint32_t)first.count(rp) * (uint32_t)rp.row_bytes);
+  __syncthreads();
+  pdl_wait_and_release();
+  if (warp >= consumers >> 5) {
+    if (lane == 0) ring_produce(rp, smem, s, warp - (consumers >> 5), p.err, [&](int q) { return slice_source(p, q); });
+  } else {
+    if constexpr (kWideRows<VPT>) {
+      row_to_shared<DT>(p.weight, nullptr, V, consumers, s_rows);
+      if (NORM || p.factor)
+        row_to_shared<DT>(NORM ? p.norm_weight : nullptr, p.gate_from == kFromFactor ? p.gate : nullptr, V, consumers,
+                          s_rows + (size_t)V * E * 4);
+    } else if (p.weight_rows) {
+      for (int v = threadIdx.x; v < V; v += consumers) {
+        reinterpret_cast<uint4*>(s_rows)[v] = __ldg(p.weight + v);
+        if constexpr (NORM) reinterpret_cast<uint4*>(s_rows)[V + v] = __ldg(p.norm_weight + v);
+      }
+    }
+    if (p.shared)
+      for (int i = threadIdx.x; i < V * (E / 4); i += consumers) s_dw1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
+    consume<DT, VPT, NORM, GATE, DROP>(p, smem, s_rows, s_comb, s_dw1, s);
+  }
+}
+
+using BackwardTmaFn = void (*)(const BranchBackwardTmaParams);
+
+template <int DT, int VPT, bool NORM>
+BackwardTmaFn pick_parts(int gate, bool drop) {
+  if constexpr (VPT == 2) {
+    if (gate == kGateNone)
+      return drop ? reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, NORM, kGateNone, kDropYes>
+                  : reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, NORM, kGateNone, kDropNone>;
+    if (gate == kGateShared)
+      return drop ? reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, NORM, kGateShared, kDropYes>
+                  : reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, NORM, kGateShared, kDropNone>;
+    return drop ? reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, NORM, kGateOwn, kDropYes>
+                : reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, NORM, kGateOwn, kDropNone>;
+  } else {
+    if (gate == kGateNone && !drop) return reduce_branch_rmsnorm_backward_tma_kernel<DT, VPT, NORM, kGateNone, kDropNone>;
+    return reduce_branch_rmsnorm_backward_tma_kernel<DT, VPT, NORM, kGateAny, kDropAny>;
+  }
+}
+template <int DT, bool NORM>
+BackwardTmaFn pick_vpt(int vpt, int gate, bool drop) {
+  if (vpt == 2) return pick_parts<DT, 2, NORM>(gate, drop);
+  if (vpt == 3) return pick_parts<DT, 3, NORM>(gate, drop);
+  if (vpt == 4) return pick_parts<DT, 4, NORM>(gate, drop);
+  if constexpr (DT == kFP32) {
+    if (vpt == 5) return pick_parts<DT, 5, NORM>(gate, drop);
+    if (vpt == 6) return pick_parts<DT, 6, NORM>(gate, drop);
+  }
+  return nullptr;
+}
+BackwardTmaFn pick(int dtype, int vpt, bool norm, int gate, bool drop) {
+  switch (dtype) {
+    case kBF16: return norm ? pick_vpt<kBF16, true>(vpt, gate, drop) : pick_vpt<kBF16, false>(vpt, gate, drop);
+    case kFP16: return norm ? pick_vpt<kFP16, true>(vpt, gate, drop) : pick_vpt<kFP16, false>(vpt, gate, drop);
+    default: return norm ? pick_vpt<kFP32, true>(vpt, gate, drop) : pick_vpt<kFP32, false>(vpt, gate, drop);
+  }
+}
+
+constexpr int kSharedBudget = 222 * 1024;  // ring and what lies beside it; RingShared is static
+
+// Where a call's weights and slices lie; the bytes beside the ring: the weights, the
+// sum of dnorm_weight behind a shared gate, the teams' sums.
+bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row, const BranchTeams& sh,
+         BranchBackwardTmaParams* p, int* beside) {
+  const bool norm = br.norm_weight != nullptr, wide = sh.vpt == 2, own = br.gate && br.gate_span == 0;
+  const bool column = br.gate && br.gate_span == rows;
+  p->gate_from = !br.gate ? kFromFactor : own ? kFromRing : wide && column ? kFromFactor : kFromRows;
+  p->factor = norm || (wide && column);
+  p->shared = br.gate && !own && (g.dgate || g.dnorm_weight);
+  RingPlan& rp = p->ring;
+  rp.rows = (int)rows;
+  rp.row_bytes = vec_per_row * 16;
+  rp.vec_per_row = vec_per_row;
+  rp.ranks = W;
+  rp.teams = sh.teams;
+  rp.tile_rows = sh.tile_rows;
+  rp.team_threads = sh.team_threads;
+  rp.gate_span = p->shared ? (uint32_t)br.gate_span : 0;
+  const int slice = sh.teams * rp.row_bytes, floats = dtype == kFP32 ? rp.row_bytes : 2 * rp.row_bytes;
+  rp.held = 1;
+  p->a_at = p->d_at = p->g_at = 0;
+  if (g.ar) p->a_at = slice * rp.held++;
+  if (g.dres) p->d_at = slice * rp.held++;
+  if (own) p->g_at = slice * rp.held++;
+  p->weight_rows = p->factor ? 2 : 1;
+  const int sums = (p->shared ? floats : 0) + (sh.teams > 1 ? sh.teams * floats : 0);
+  *beside = sums + p->weight_rows * (wide ? floats : rp.row_bytes);
+  if (branch_ring_fit(kSharedBudget - *beside, &rp)) return true;
+  if (wide) return false;
+  p->weight_rows = 0;
+  *beside = sums;
+  return branch_ring_fit(kSharedBudget - sums, &rp);
+}
+
+}  // namespace
+
+bool branch_backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, BranchTeams* out) {
+  const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512 : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
+  if (vpt > (dtype == kFP32 ? 6 : 4)) return false;
+  out->vpt = vpt;
+  out->use = team_use(vec_per_row, vpt);
+  out->team_threads = team_threads(vec_per_row, vpt);
+  if (out->team_threads > 512) return false;
+  out->teams = 512 / out->team_threads;
+  out->tile_rows = (int)std::min<int64_t>(out->teams, (rows + num_sms - 1) / num_sms);  // few rows: spread over the SMs
+  out->grid = (int)std::min<int64_t>((rows + out->tile_rows - 1) / out->tile_rows, num_sms);
+  return true;
+}
+
+bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
+                              const BranchTeams& sh) {
+  BranchBackwardTmaParams p;
+  int beside;
+  return fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside);
+}
+
+cudaError_t branch_backward_tma_prepare(int dtype, const BranchTeams& sh) {
+  for (int parts = 0; parts < 12; parts++) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt, parts & 1, parts >> 2, parts & 2)),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBudget);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
+                                       const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
+                                       int vec_per_row, const BranchTeams& sh, cudaStream_t s) {
+  BranchBackwardTmaParams p;
+  int beside;
+  if (!fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside)) return cudaErrorInvalidValue;
+  const bool one = sh.grid == 1, own = br.gate && br.gate_span == 0;
+  p.dy = dy;
+  p.h = static_cast<const uint8_t*>(g.h);
+  p.ar = static_cast<const uint8_t*>(g.ar);
+  p.dres = static_cast<const uint8_t*>(g.dres);
+  p.weight = static_cast<const uint4*>(weight);
+  p.norm_weight = static_cast<const uint4*>(br.norm_weight);
+  p.gate = static_cast<const uint4*>(br.gate);
+  p.dx = static_cast<uint4*>(g.dx);
+  p.dresidual = static_cast<uint4*>(g.dresidual);
+  p.dgate_own = own ? static_cast<uint4*>(g.dgate) : nullptr;
+  p.dgate = own ? nullptr : static_cast<float*>(g.dgate);
+  const size_t plane = (size_t)sh.grid * (size_t)cols;
+  p.part_w = g.dweight ? (one ? g.dweight : g.workspace) : nullptr;
+  p.part_w1 = g.dnorm_weight ? (one ? g.dnorm_weight : g.workspace + plane) : nullptr;
+  p.part_gate = one ? nullptr : g.workspace + 2 * plane;
+  p.err = err;
+  p.drop = br.drop;
+  p.residual_scale = br.residual_scale;
+  p.eps = eps;
+  p.norm_eps = br.norm_eps;
+  p.inv_cols = 1.f / (float)cols;
+  p.gate_span = (uint32_t)std::max<int64_t>(br.gate_span, 1);
+  const RingPlan& rp = p.ring;
+  cudaError_t e = launch_pdl(pick(dtype, sh.vpt, br.norm_weight != nullptr, gate_kind(br), br.drop.active), (unsigned)sh.grid,
+                             (unsigned)(sh.teams * sh.team_threads + 32 * rp.producers),
+                             (size_t)rp.stages * rp.group * rp.teams * rp.row_bytes + beside, s, 1, p);
+  return e == cudaSuccess ? launch_branch_sums(br, g, dtype, sh.grid, rows, cols, s) : e;
+}
+
+}  // namespace car

@@ -1,0 +1,269 @@
+// branch_ring.cuh -- what the two pipelines of a block's branch share
+// (branch_tma.cu, branch_backward_tma.cu): tiles of rows streamed through a ring
+// of shared-memory stages by TMA bulk copies.
+//
+// A CTA takes one contiguous span of rows, in tiles of `teams` consecutive rows
+// (the last one shorter; with a gate that rows share also the last one before a
+// gate row's end).  One bulk copy brings the same slice (a rank, the residual
+// ...) of all rows of a tile; each team of consumer warps owns one of them.
+// Spans and not every so-many-th tile: with fewer rows than a CTA has teams for,
+// the rows are spread over all SMs, and a gate row is cut by few CTAs.
+//
+// Slices travel in stages of up to `group`, with one full and one empty barrier
+// each: the ranks' in order, then those that a row needs to its end, which share
+// one stage, so a row waits for and frees few of them.  With few ranks a whole
+// tile is one stage (backward, W = 1: one wait and one release per row instead of
+// four; the instructions of a row are what bounds it there).
+#pragma once
+
+#include "branch.cuh"
+#include "ring.cuh"
+
+namespace car {
+namespace {
+
+// Instances of the pipelines: with two vectors per thread one for each kind of gate,
+// with dropout and without (what a row does not do costs it registers and
+// instructions all the same when it is found out at run time: backward, W = 1, M =
+// 16389, N = 4096 bf16 without a norm 145 us against 103), for longer rows one for
+// neither gate nor dropout and one for any.
+enum GateKind : int { kGateNone = 0, kGateShared = 1, kGateOwn = 2, kGateAny = 3 };
+enum DropKind : int { kDropNone = 0, kDropYes = 1, kDropAny = 2 };
+// Where a row's gate comes from: the factor row in shared memory (also: no gate),
+// the ring, L2.
+enum GateFrom : int { kFromFactor = 0, kFromRing = 1, kFromRows = 2 };
+inline int gate_kind(const BranchArgs& br) { return !br.gate ? kGateNone : br.gate_span == 0 ? kGateOwn : kGateShared; }
+
+// The tiles of this CTA in order.
+struct Tiles {
+  int row, end, cut, step;
+  __device__ __forceinline__ explicit Tiles(const RingPlan& p) {
+    if (p.gate_span) {
+      row = (int)span_start(p.rows, gridDim.x, blockIdx.x);
+      end = (int)span_start(p.rows, gridDim.x, blockIdx.x + 1);
+      cut = (int)(((uint32_t)row / p.gate_span + 1) * p.gate_span);
+      step = 0;
+    } else {
+      row = blockIdx.x * p.tile_rows;
+      end = cut = p.rows;
+      step = gridDim.x * p.tile_rows;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return row < end; }
+  __device__ __forceinline__ int count(const RingPlan& p) const { return min(min(end, cut) - row, p.tile_rows); }
+  __device__ __forceinline__ void next(const RingPlan& p) {
+    if (step) {
+      row += step;
+    } else {
+      row += count(p);
+      if (row == cut) cut += p.gate_span;
+    }
+  }
+};
+
+// Barriers and small arrays (static shared memory).
+struct RingShared {
+  uint64_t full[kMaxRingStages], empty[kMaxRingStages];
+  uint64_t rowbar[16];      // by team
+  uint64_t done[2];         // all consumer warps
+  float warp[96];           // [teams][2][3][warps of a team]
+  int abort;
+};
+
+__device__ __forceinline__ void ring_init(const RingPlan& p, RingShared& s) {  // one thread
+  const uint32_t nwarps = (uint32_t)(p.teams * p.team_threads) >> 5;
+  for (int i = 0; i < p.stages; i++) {
+    mbar_init(&s.full[i], p.producers);
+    mbar_init(&s.empty[i], nwarps);
+  }
+  for (int t = 0; t < p.teams; t++) mbar_init(&s.rowbar[t], (uint32_t)(p.team_threads >> 5));
+  mbar_init(&s.done[0], nwarps);
+  mbar_init(&s.done[1], nwarps);
+  s.abort = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// Producer `who` of p.producers: issues every p.producers-th slice of each stage,
+// then waits for the stages that were filled.  source(q): slice q of row 0.
+template <class Source>
+__device__ __forceinline__ void ring_produce(const RingPlan& p, uint8_t* ring, RingShared& s, int who, unsigned int* err,
+                                             Source source) {
+  const int S = p.stages, slices = p.ranks + p.held;
+  const uint32_t stride = (uint32_t)p.teams * (uint32_t)p.row_bytes;
+  int place = 0;
+  uint32_t phase = 0, issued = 0;
+  bool ok = true;
+  for (Tiles t(p); t.more() && ok; t.next(p)) {
+    const int64_t off = t.row * (int64_t)p.row_bytes;
+    const uint32_t bytes = (uint32_t)t.count(p) * (uint32_t)p.row_bytes;
+    for (int q = 0; q < slices;) {
+      // a stage ends with the ranks unless all of the tile is one
+      const int n = slices <= p.group ? slices : q < p.ranks ? min(p.group, p.ranks - q) : slices - q;
+      if (issued >= (uint32_t)S && !wait_bounded(&s.empty[place], phase ^ 1u, &s.abort)) {
+        ok = false;
+        break;
+      }
+      const int mine = (n - who + p.producers - 1) / p.producers;
+      mbar_arrive_expect_tx(&s.full[place], bytes * (uint32_t)mine);
+      uint8_t* to = ring + (size_t)place * p.group * stride;
+      for (int i = who; i < n; i += p.producers) bulk_load(to + (size_t)i * stride, source(q + i) + off, bytes, &s.full[place]);
+      q += n;
+      issued++;
+      if (++place == S) {
+        place = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  if (!ok) {
+    atomicOr(err, 1u);
+    *static_cast<volatile int*>(&s.abort) = 1;
+  }
+  // No copy may still be on its way into a CTA that has exited.  A stage that the
+  // other producer gave up on does not complete: that wait runs out.
+  const int used = issued < (uint32_t)S ? (int)issued : S;
+  for (int k = 0; k < used; k++) {
+    const uint32_t c = issued - 1u - (uint32_t)k;
+    if (!wait_bounded_drain(&s.full[c % (uint32_t)S], (c / (uint32_t)S) & 1u)) atomicOr(err, 1u);
+  }
+}
+
+// A consumer thread's place in the ring.
+struct RingReader {
+  const RingPlan& p;
+  RingShared& s;
+  int place = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ RingReader(const RingPlan& plan, RingShared& shared) : p(plan), s(shared) {}
+  __device__ __forceinline__ bool wait() { return wait_bounded(&s.full[place], phase, &s.abort); }
+  __device__ __forceinline__ void release() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&s.empty[place]);
+    if (++place == p.stages) {
+      place = 0;
+      phase ^= 1u;
+    }
+  }
+  // A tile in which this team has no row.
+  __device__ __forceinline__ bool skip() {
+    for (int k = 0; k < p.tile_stages; k++) {
+      if (!wait()) return false;
+      release();
+    }
+    return true;
+  }
+};
+
+// The rank sum of this thread's vectors of a row, from the stages that hold the
+// ranks; `mine` is its first vector in stage 0.  Leaves the reader at the stage
+// that holds the row's other slices, waited for, and returns where they begin;
+// null when a wait ran out.
+template <int DT, int VPT>
+__device__ __forceinline__ const uint8_t* ring_rank_sum(const RingPlan& p, RingReader& in, const uint8_t* mine,
+                                                        const bool (&ok)[VPT], float2 (&acc)[VPT][Pack<DT>::kN / 2]) {
+  constexpr int E = Pack<DT>::kN;
+  const uint32_t stride = (uint32_t)p.teams * (uint32_t)p.row_bytes;
+  const bool whole = p.tile_stages == 1;
+  int q = 0;
+  while (true) {
+    if (!in.wait()) return nullptr;
+    const uint8_t* at = mine + (uint32_t)in.place * (uint32_t)p.group * stride;
+    if (q == p.ranks) return at;
+    const int n = min(p.group, p.ranks - q);
+    for (int i = 0; i < n; i++, at += stride) {
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        if (ok[k]) {
+          float2 f[E / 2];
+          widen2<DT>(lds16(at + 16 * k * p.team_threads), f);
+#pragma unroll
+          for (int e = 0; e < E / 2; e++) acc[k][e] = q + i == 0 ? f[e] : add2(acc[k][e], f[e]);
+        }
+      }
+    }
+    if (whole) return at;
+    q += n;
+    in.release();
+  }
+}
+
+// The lower half of the warp adds one sum, the upper half another; both to all
+// lanes.
+__device__ __forceinline__ float2 half_totals(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  const float other = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  return (threadIdx.x & 16) ? make_float2(other, v) : make_float2(v, other);
+}
+
+// Sums over a row: the warps of a team.  Every warp adds the warps' partials
+// itself, in the same order; they are double-buffered by the parity of the
+// team's exchange number x (what exchange x wrote is overwritten by x + 2, after
+// the barrier of x + 1, which a warp reaches only once it has read x's).
+template <int NS>
+__device__ __forceinline__ bool team_sums(const RingPlan& p, RingShared& s, int team, uint32_t x, float (&v)[NS]) {
+  const int lane = threadIdx.x & 31, nwarps = p.team_threads >> 5, warp = (threadIdx.x - team * p.team_threads) >> 5;
+  const bool upper = threadIdx.x & 16;
+  if constexpr (NS >= 2) {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[1], 16);
+    const float2 t = half_totals(__fadd_rn(upper ? v[1] : v[0], other));
+    v[0] = t.x;
+    v[1] = t.y;
+  }
+  if constexpr (NS != 2) v[NS - 1] = warp_total(v[NS - 1]);
+  if (nwarps == 1) return true;
+  float* w = s.warp + (team * 2 + (x & 1u)) * 3 * nwarps;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < NS; i++) w[i * nwarps + warp] = v[i];
+    mbar_arrive(&s.rowbar[team]);
+  }
+  if (!wait_bounded(&s.rowbar[team], x & 1u, &s.abort)) return false;
+  const int part = lane & 15;
+  if constexpr (NS >= 2) {
+    const float2 t = half_totals(part < nwarps ? w[(lane >> 4) * nwarps + part] : 0.f);
+    v[0] = t.x;
+    v[1] = t.y;
+  }
+  if constexpr (NS != 2) {
+    float t = part < nwarps ? w[(NS - 1) * nwarps + part] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+    v[NS - 1] = t;
+  }
+  return true;
+}
+
+// Rows of factors in shared memory, in fp32: every vector of them is used once or
+// twice per row, and widening one takes eight instructions.  A vector of a 16-bit
+// type fills two float4, which lie in two planes so that a warp that takes
+// consecutive vectors reads either without bank conflicts.
+template <int DT>
+__device__ __forceinline__ void row_to_shared(const uint4* __restrict__ a, const uint4* __restrict__ b, int vecs, int threads,
+                                              uint8_t* to) {
+  constexpr int E = Pack<DT>::kN;
+  for (int v = threadIdx.x; v < vecs; v += threads) {
+    float2 f[E / 2], g[E / 2];
+    widen2<DT>(__ldg((a ? a : b) + v), f);
+    if (a && b) {
+      widen2<DT>(__ldg(b + v), g);
+#pragma unroll
+      for (int e = 0; e < E / 2; e++) f[e] = mul2(f[e], g[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E / 2; e += 2)
+      reinterpret_cast<float4*>(to)[(e / 2) * vecs + v] = make_float4(f[e].x, f[e].y, f[e + 1].x, f[e + 1].y);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void row_from_shared(const uint8_t* from, int vecs, int v, float2 (&f)[Pack<DT>::kN / 2]) {
+#pragma unroll
+  for (int e = 0; e < Pack<DT>::kN / 2; e += 2) {
+    const float4 x = reinterpret_cast<const float4*>(from)[(e / 2) * vecs + v];
+    f[e] = make_float2(x.x, x.y);
+    f[e + 1] = make_float2(x.z, x.w);
+  }
+}
+
+}  // namespace
+}  // namespace car

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_residual_rmsnorm
   }
   prefetch_row(p, n, blockIdx.x / C, col0, true);
   pdl_wait_and_release();
-  const uint64_t offset = drop_offset(p.drop);
+  const DropState state = drop_state(p.drop);
   const int v = threadIdx.x;
   const bool ok = v < p.chunk && col0 + v < p.vec_per_row;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_residual_rmsnorm
       if (p.gate) gv = __ldg(p.gate + (int64_t)((uint32_t)row / p.gate_span) * p.vec_per_row + col0 + v);
     }
     uint32_t bits[E / 2];
-    if (p.drop.threshold) drop_bits<E>(p.drop, offset, at, bits);
+    if (p.drop.active) drop_bits<E>(state, at, bits);
     float2 z[E / 2];
     float ss = 0.f;
     if (ok) {
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_residual_rmsnorm
 #pragma unroll
         for (int e = 0; e < E / 2; e++) z[e] = mul2(z[e], f[e]);
       }
-      if (p.drop.threshold) {
+      if (p.drop.active) {
 #pragma unroll
         for (int e = 0; e < E / 2; e++) z[e] = drop2(p.drop, bits[e], z[e]);
       }

@@ -5,8 +5,7 @@
 // vectors, a thread keeps U x W independent 16-byte loads in flight.  The mask
 // is computed where it is used (branch.cuh), from the vector's place in the
 // [M, N] problem, so it costs no bytes.  Roofline: HBM, (W + 1) * 16 bytes per
-// vector; the generator's 20 wide products per vector fill a tenth of the
-// integer pipe at that rate.
+// vector, next to the generator's 18 wide products.
 #include "branch.cuh"
 #include "car_launch.h"
 
@@ -24,7 +23,7 @@ __global__ void __launch_bounds__(kReduceThreads)
   const int64_t lo = share * blockIdx.x + (blockIdx.x < extra ? blockIdx.x : extra);
   const int64_t hi = lo + share + (blockIdx.x < extra ? 1 : 0);
   pdl_wait_and_release();
-  const uint64_t offset = drop_offset(drop);
+  const DropState state = drop_state(drop);
   for (int64_t base = lo + threadIdx.x; base < hi; base += kReduceThreads * U) {
     uint4 raw[U][R];
 #pragma unroll
@@ -40,13 +39,17 @@ __global__ void __launch_bounds__(kReduceThreads)
     for (int u = 0; u < U; u++) {
       const int64_t v = base + (int64_t)u * kReduceThreads;
       if (v < hi) {
-        uint32_t bits[E / 2];
-        drop_bits<E>(drop, offset, v, bits);
         float acc[E];
         rank_sum<DT, R>(raw[u], n, acc);
         float2 z[E / 2];
 #pragma unroll
-        for (int e = 0; e < E / 2; e++) z[e] = drop2(drop, bits[e], make_float2(acc[2 * e], acc[2 * e + 1]));
+        for (int e = 0; e < E / 2; e++) z[e] = make_float2(acc[2 * e], acc[2 * e + 1]);
+        if (drop.active) {
+          uint32_t bits[E / 2];
+          drop_bits<E>(state, v, bits);
+#pragma unroll
+          for (int e = 0; e < E / 2; e++) z[e] = drop2(drop, bits[e], z[e]);
+        }
         st16(out + v, narrow2<DT>(z));
       }
     }

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/car.h"
+#include "branch.h"
 #include "car_device.cuh"
 #include "car_launch.h"
 
@@ -43,7 +44,9 @@ struct car_ctx {
   int backward_groups;       // CTAs (or clusters) with a partial weight gradient each
   // The branch calls and dropout, the same way (branch_api.cu).
   std::atomic<bool> branch_ready{false}, branch_backward_ready{false}, dropout_ready{false};
-  car::FusedShape branch, branch_backward;
+  car::FusedShape branch, branch_backward;   // row kernels
+  car::BranchTeams branch_tma, branch_backward_tma;
+  bool branch_pipeline, branch_backward_pipeline;
   int dropout_grid;
   int fused_kernel_auto;  // CAR_FUSED_ROWS or CAR_FUSED_PIPELINE
   int fused_kernel;
