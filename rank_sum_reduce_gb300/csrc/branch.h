@@ -58,9 +58,9 @@ struct BranchTeams : TeamShape {
   int tile_rows;  // rows of a tile, at most teams
 };
 // ---- forward, many rows (branch_tma.cu); false when a row is too long ----
-bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
+bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BranchTeams* out);
 // Whether this call's slices and weights fit beside one another.
-bool branch_tma_fits(int dtype, int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh);
+bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh);
 cudaError_t branch_tma_prepare(int dtype, const BranchTeams& sh);
 cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const BranchArgs& br, const void* residual,
                               const void* weight, float eps, void* residual_out, void* norm_out, void* ar_out,

@@ -111,7 +111,7 @@ car_status prepare_branch(car_ctx* h) {
   cudaError_t e = branch_resident_groups(h->dtype, h->W, h->branch, h->num_sms, &groups);
   if (e != cudaSuccess) return cuda_fail(e, "branch occupancy");
   h->branch.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
-  h->branch_pipeline = branch_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_tma) && branch_pipeline_pays(h, h->branch_tma);
+  h->branch_pipeline = branch_tma_shape(h->M, h->vec_per_row, h->num_sms, h->W, &h->branch_tma) && branch_pipeline_pays(h, h->branch_tma);
   if (h->branch_pipeline && (e = branch_tma_prepare(h->dtype, h->branch_tma)) != cudaSuccess)
     return cuda_fail(e, "branch pipeline smem");
   h->branch_ready.store(true, std::memory_order_release);
@@ -194,7 +194,7 @@ car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inp
   if ((st = prepare_branch(h)) != CAR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (h->branch_pipeline && branch_tma_fits(h->dtype, h->W, b, h->M, h->vec_per_row, h->branch_tma))
+  if (h->branch_pipeline && branch_tma_fits(h->W, b, h->M, h->vec_per_row, h->branch_tma))
     e = launch_branch_tma(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M, h->N,
                           h->vec_per_row, h->branch_tma, s);
   else

@@ -243,9 +243,10 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
 }
 
 // Sums of partials, in a fixed order: block row 0 adds part_w over the groups, 1
-// part_w1, and 2 + i the partials of gate row cut[i], which lie in the spans of
-// the groups that its rows touch: in the second partial of the first of them if
-// the gate row begins inside that span, else in the first.  A block's threads
+// part_w1, and 2 + i the partials of a gate row, which lie in the spans of the
+// groups that its rows touch: in the second partial of the first of them if the
+// gate row begins inside that span, else in the first.  (Which groups: found on
+// the host; the divisions took 50 us here for a gate row of 152.)  A block's threads
 // take 8 float4 columns and 32 parts of the sum, their loads in flight in
 // batches, and those are added in order: the partials were just written and
 // come from L2, so the kernel is bound by one L2 latency and its launch.
@@ -260,10 +261,13 @@ struct BranchSums {
   int dtype;
   int groups;
   int vecs;                 // float4 in a row
-  int64_t rows;
-  uint32_t gate_span;
-  uint32_t cut[kMaxBranchGroups];
+  struct Cut {
+    uint32_t row;         // of the gate
+    uint16_t first, count;  // groups
+    bool inside;          // begins inside the first one's span
+  } cut[kMaxBranchGroups];
 };
+static_assert(sizeof(BranchSums) <= 4096, "kernel parameters");
 
 __device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i) {
   if (dtype == kFP32) return static_cast<const float*>(w)[i];
@@ -285,19 +289,12 @@ __global__ void __launch_bounds__(256) branch_sums_kernel(const __grid_constant_
     out = job == 0 ? p.dweight : p.dnorm_weight;
     count = p.groups;
   } else {
-    const uint32_t b = p.cut[job - 2];
-    const int64_t lo = (int64_t)b * p.gate_span, hi = lo + p.gate_span;
-    // the first group whose span ends behind lo, the last that starts before hi
-    int c0 = (int)((uint64_t)lo * (uint64_t)p.groups / (uint64_t)p.rows);
-    while (c0 > 0 && span_start(p.rows, p.groups, c0) > lo) c0--;
-    while (span_start(p.rows, p.groups, c0 + 1) <= lo) c0++;
-    int c1 = c0;
-    while (c1 + 1 < p.groups && span_start(p.rows, p.groups, c1 + 1) < hi) c1++;
-    count = c1 - c0 + 1;
+    const BranchSums::Cut& c = p.cut[job - 2];
+    count = c.count;
     stride = 2 * (int64_t)p.vecs;
-    head = p.part_gate + c0 * stride;
-    from = head + (span_start(p.rows, p.groups, c0) < lo ? p.vecs : 0);
-    out = p.dgate + (int64_t)b * p.vecs;
+    head = p.part_gate + c.first * stride;
+    from = head + (c.inside ? p.vecs : 0);
+    out = p.dgate + (int64_t)c.row * p.vecs;
     scale = p.norm_weight;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -446,15 +443,19 @@ cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, in
   p.dtype = dtype;
   p.groups = groups;
   p.vecs = (int)(cols / 4);
-  p.rows = rows;
-  p.gate_span = (uint32_t)std::max<int64_t>(br.gate_span, 1);
   // gate rows that an inner border of the spans cuts, each once
   int cuts = 0;
   if (gates) {
+    int64_t start = 0;  // of span c - 1
     for (int c = 1; c < groups; c++) {
-      const int64_t at = span_start(rows, groups, c);
-      const uint32_t b = (uint32_t)(at / br.gate_span);
-      if (at % br.gate_span != 0 && (cuts == 0 || p.cut[cuts - 1] != b)) p.cut[cuts++] = b;
+      const int64_t at = span_start(rows, groups, c), b = at / br.gate_span;
+      if (at % br.gate_span != 0) {
+        if (cuts > 0 && p.cut[cuts - 1].row == b)
+          p.cut[cuts - 1].count++;
+        else
+          p.cut[cuts++] = {(uint32_t)b, (uint16_t)(c - 1), 2, start < b * br.gate_span};
+      }
+      start = at;
     }
   }
   cudaLaunchConfig_t cfg = {};

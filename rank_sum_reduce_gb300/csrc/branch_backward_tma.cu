@@ -80,25 +80,27 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
                                         float4* s_comb, float4* s_dw1, RingShared& s) {
   constexpr int E = Pack<DT>::kN;
   constexpr bool SHARED = GATE == kGateShared || GATE == kGateAny, OWN = GATE == kGateOwn || GATE == kGateAny;
+  constexpr bool BRANCHES = VPT * E > 16 || (SHARED && E == 8);
   const RingPlan& rp = p.ring;
   const bool own = OWN && (GATE == kGateOwn || p.gate_from == kFromRing), shared = SHARED && p.shared;
   const int T = rp.team_threads, V = rp.vec_per_row;
-  const int team = threadIdx.x / T, tid = threadIdx.x - team * T, lane = threadIdx.x & 31;
-  const uint8_t* mine = ring + (size_t)team * rp.row_bytes + 16 * tid;
+  const int team = threadIdx.x / T, tid = threadIdx.x - team * T;
+  const uint8_t* mine = ring + (size_t)team * rp.row_bytes;  // the row in stage 0
   const DropState state = drop_state(p.drop);
   const int first = (int)span_start(rp.rows, gridDim.x, blockIdx.x);
   float2 dw[VPT][E / 2], ts[VPT][E / 2];
   bool ok[VPT];
+  int col[VPT], at[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     ok[k] = tid + k * T < V;
+    col[k] = min(tid + k * T, V - 1);
+    at[k] = 16 * col[k];
 #pragma unroll
     for (int e = 0; e < E / 2; e++) dw[k][e] = ts[k][e] = make_float2(0.f, 0.f);
   }
   // Adds the teams' sums of every column in team order and hands each column's
-  // four to `take`, in the same thread every time; false when a wait ran out.
-  // The wait before the teams' next sums are stored ends long before those come.
-  uint32_t combined = 0;
+  // four to `take`, in the same thread every time.
   auto combine = [&](float2 (&acc)[VPT][E / 2], auto take) {
     if (rp.teams == 1) {
 #pragma unroll
@@ -106,24 +108,21 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
         if (ok[k]) {
 #pragma unroll
           for (int e = 0; e < E / 2; e += 2)
-            take((tid + k * T) * (E / 4) + e / 2, make_float4(acc[k][e].x, acc[k][e].y, acc[k][e + 1].x, acc[k][e + 1].y));
+            take(col[k] * (E / 4) + e / 2, make_float4(acc[k][e].x, acc[k][e].y, acc[k][e + 1].x, acc[k][e + 1].y));
         }
       }
-      return true;
+      return;
     }
-    if (combined && !wait_bounded(&s.done[1], (combined - 1u) & 1u, &s.abort)) return false;
-    float4* at = s_comb + (size_t)team * V * (E / 4);
+    float4* to = s_comb + (size_t)team * V * (E / 4);
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       if (ok[k]) {
 #pragma unroll
         for (int e = 0; e < E / 2; e += 2)
-          at[(tid + k * T) * (E / 4) + e / 2] = make_float4(acc[k][e].x, acc[k][e].y, acc[k][e + 1].x, acc[k][e + 1].y);
+          to[col[k] * (E / 4) + e / 2] = make_float4(acc[k][e].x, acc[k][e].y, acc[k][e + 1].x, acc[k][e + 1].y);
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.done[0]);
-    if (!wait_bounded(&s.done[0], combined & 1u, &s.abort)) return false;
+    consumers_barrier(rp);
     for (int i = threadIdx.x; i < V * (E / 4); i += rp.teams * T) {
       float4 a = s_comb[i];
       for (int k = 1; k < rp.teams; k++) {
@@ -135,10 +134,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       }
       take(i, a);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.done[1]);
-    combined++;
-    return true;
+    consumers_barrier(rp);  // before the teams' next sums
   };
   // Columns 4 i .. 4 i + 3 of a row of T.
   auto four = [&](const uint4* row, int i) {
@@ -160,7 +156,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
     if (p.dgate)
       out = reinterpret_cast<float4*>(whole ? p.dgate : p.part_gate) +
             (whole ? (int64_t)b : 2 * (int64_t)blockIdx.x + (from == first ? 0 : 1)) * V * (E / 4);
-    const bool done = combine(ts, [&](int i, float4 t) {
+    combine(ts, [&](int i, float4 t) {
       const float4 g = four(p.gate + (int64_t)b * V, i);
       float4 d = s_dw1[i];
       d.x = fmaf(g.x, t.x, d.x);
@@ -180,65 +176,63 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
 #pragma unroll
       for (int e = 0; e < E / 2; e++) ts[k][e] = make_float2(0.f, 0.f);
     }
-    return done;
   };
 
-  RingReader in(rp, s);
+  RingReader in(rp, s, p.err);
   uint32_t x = 0;
-  bool failed = false;
   int from = first;
-  for (Tiles t(rp); t.more() && !failed;) {
+  for (Tiles t(rp); t.more();) {
     const int tile = t.row;
     if (team >= t.count(rp)) {
-      failed = !in.skip();
+      in.skip();
     } else {
       const int row = tile + team;
-      const int64_t at = (int64_t)row * V + tid;
+      const int64_t base = (int64_t)row * V;
       float2 g[VPT][E / 2];
-      const uint8_t* held = ring_rank_sum<DT, VPT>(rp, in, mine, ok, g);
-      if (!held) {
-        failed = true;
-        break;
+      const uint8_t* held = ring_rank_sum<DT, VPT, BRANCHES>(rp, in, mine, ok, at, g);
+      if (in.failed) {
+#pragma unroll
+        for (int k = 0; k < VPT; k++) ok[k] = false;
       }
-      float2 hh = make_float2(0.f, 0.f), gwh = hh, aa = hh;
+      float hh = 0.f, gwh = 0.f, aa = 0.f;
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
-        if (ok[k]) {
-          float2 hf[E / 2], wf[E / 2];
-          widen2<DT>(lds16(held + 16 * k * T), hf);
-          weight_at<DT, VPT>(p, s_rows, 0, tid + k * T, wf);
+        if (!BRANCHES || ok[k]) {
+          float2 hf[E / 2], wf[E / 2], sh = make_float2(0.f, 0.f), sg = sh, sa = sh;
+          widen2<DT>(lds16(held + at[k]), hf);
+          weight_at<DT, VPT>(p, s_rows, 0, col[k], wf);
 #pragma unroll
           for (int e = 0; e < E / 2; e++) {
-            hh = fma2(hf[e], hf[e], hh);
-            gwh = fma2(mul2(g[k][e], wf[e]), hf[e], gwh);
+            sh = fma2(hf[e], hf[e], sh);
+            sg = fma2(mul2(g[k][e], wf[e]), hf[e], sg);
           }
           if constexpr (NORM) {
-            widen2<DT>(lds16(held + p.a_at + 16 * k * T), hf);
+            widen2<DT>(lds16(held + p.a_at + at[k]), hf);
 #pragma unroll
-            for (int e = 0; e < E / 2; e++) aa = fma2(hf[e], hf[e], aa);
+            for (int e = 0; e < E / 2; e++) sa = fma2(hf[e], hf[e], sa);
           }
+          hh += ok[k] ? sh.x + sh.y : 0.f;
+          gwh += ok[k] ? sg.x + sg.y : 0.f;
+          aa += ok[k] ? sa.x + sa.y : 0.f;
         }
       }
       float v[NORM ? 3 : 2];
-      v[0] = hh.x + hh.y;
-      v[1] = gwh.x + gwh.y;
-      if constexpr (NORM) v[NORM ? 2 : 0] = aa.x + aa.y;
-      if (!team_sums(rp, s, team, x++, v)) {
-        failed = true;
-        break;
-      }
+      v[0] = hh;
+      v[1] = gwh;
+      if constexpr (NORM) v[NORM ? 2 : 0] = aa;
+      team_sums(rp, s, team, x++, v);
       const float r = rsqrtf(fmaf(v[0], p.inv_cols, p.eps));
       const float2 m = both(-__fmul_rn(__fmul_rn(v[1], p.inv_cols), r));
       const float2 qn = NORM ? both(rsqrtf(fmaf(v[NORM ? 2 : 0], p.inv_cols, p.norm_eps))) : both(1.f);
-      const uint4* grow = SHARED && p.gate_from == kFromRows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V + tid : nullptr;
-      float2 vu = make_float2(0.f, 0.f);
+      const uint4* grow = SHARED && p.gate_from == kFromRows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V : nullptr;
+      float vu = 0.f;
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
-        if (ok[k]) {
+        if (!BRANCHES || ok[k]) {
           float2 hf[E / 2], f[E / 2], d[E / 2];
-          widen2<DT>(lds16(held + 16 * k * T), hf);
-          weight_at<DT, VPT>(p, s_rows, 0, tid + k * T, f);
-          widen2<DT>(p.dres ? lds16(held + p.d_at + 16 * k * T) : make_uint4(0u, 0u, 0u, 0u), d);
+          widen2<DT>(lds16(held + at[k]), hf);
+          weight_at<DT, VPT>(p, s_rows, 0, col[k], f);
+          widen2<DT>(p.dres ? lds16(held + p.d_at + at[k]) : make_uint4(0u, 0u, 0u, 0u), d);
 #pragma unroll
           for (int e = 0; e < E / 2; e++) {
             const float2 u = mul2(hf[e], both(r));
@@ -248,32 +242,32 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
           if (p.dresidual) {
 #pragma unroll
             for (int e = 0; e < E / 2; e++) d[e] = mul2(g[k][e], both(p.residual_scale));
-            st16(p.dresidual + at + k * T, narrow2<DT>(d));
+            if (ok[k]) st16(p.dresidual + base + col[k], narrow2<DT>(d));
           }
           if (DROP == kDropYes || (DROP == kDropAny && p.drop.active)) {
             uint32_t bits[E / 2];
-            drop_bits<E>(state, at + k * T, bits);
+            drop_bits<E>(state, base + col[k], bits);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = drop2(p.drop, bits[e], g[k][e]);  // dz
           }
           float2 u1[E / 2];
           if (NORM || (GATE && p.ar)) {
-            widen2<DT>(lds16(held + p.a_at + 16 * k * T), u1);
+            widen2<DT>(lds16(held + p.a_at + at[k]), u1);
             if constexpr (NORM) {
 #pragma unroll
               for (int e = 0; e < E / 2; e++) u1[e] = mul2(u1[e], qn);
             }
           }
-          if (NORM || (SHARED && p.factor)) weight_at<DT, VPT>(p, s_rows, 1, tid + k * T, f);
+          if (NORM || (SHARED && p.factor)) weight_at<DT, VPT>(p, s_rows, 1, col[k], f);
           if (own) {
-            widen2<DT>(lds16(held + p.g_at + 16 * k * T), d);
+            widen2<DT>(lds16(held + p.g_at + at[k]), d);
             if (p.dgate_own) {
 #pragma unroll
               for (int e = 0; e < E / 2; e++) {
                 const float2 dt = mul2(g[k][e], u1[e]);
                 hf[e] = NORM ? mul2(dt, f[e]) : dt;
               }
-              st16(p.dgate_own + at + k * T, narrow2<DT>(hf));
+              if (ok[k]) st16(p.dgate_own + base + col[k], narrow2<DT>(hf));
             }
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], d[e]);
@@ -283,7 +277,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
             for (int e = 0; e < E / 2; e++) ts[k][e] = fma2(g[k][e], u1[e], ts[k][e]);
           }
           if (SHARED && p.gate_from == kFromRows) {
-            widen2<DT>(__ldg(grow + k * T), d);
+            widen2<DT>(__ldg(grow + col[k]), d);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], d[e]);
           }
@@ -292,64 +286,57 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
             for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], f[e]);  // v
           }
           if constexpr (NORM) {
+            float2 sv = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < E / 2; e++) vu = fma2(g[k][e], u1[e], vu);
+            for (int e = 0; e < E / 2; e++) sv = fma2(g[k][e], u1[e], sv);
+            vu += ok[k] ? sv.x + sv.y : 0.f;
           } else {
-            st16(p.dx + at + k * T, narrow2<DT>(g[k]));
+            if (ok[k]) st16(p.dx + base + col[k], narrow2<DT>(g[k]));
           }
         }
       }
       if constexpr (NORM) {
-        float w[1] = {vu.x + vu.y};
-        if (!team_sums(rp, s, team, x++, w)) {
-          failed = true;
-          break;
-        }
+        float w[1] = {vu};
+        team_sums(rp, s, team, x++, w);
         // u1 * mean = a * (q * mean)
         const float2 mean = both(-__fmul_rn(__fmul_rn(w[0], p.inv_cols), qn.x));
 #pragma unroll
         for (int k = 0; k < VPT; k++) {
-          if (ok[k]) {
+          if (!BRANCHES || ok[k]) {
             float2 af[E / 2];
-            widen2<DT>(lds16(held + p.a_at + 16 * k * T), af);
+            widen2<DT>(lds16(held + p.a_at + at[k]), af);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) af[e] = mul2(qn, fma2(af[e], mean, g[k][e]));
-            st16(p.dx + at + k * T, narrow2<DT>(af));
+            if (ok[k]) st16(p.dx + base + col[k], narrow2<DT>(af));
           }
         }
       }
       in.release();
     }
-    if (failed) break;
     const int cut = t.cut;
     t.next(rp);
     if (shared && (t.row == cut || !t.more())) {
-      if (!flush((uint32_t)tile / p.gate_span, from, t.row)) failed = true;
+      flush((uint32_t)tile / p.gate_span, from, t.row);
       from = t.row;
     }
   }
   const int64_t plane = (int64_t)blockIdx.x * V * (E / 4);
-  if (!failed && p.part_w)
-    failed = !combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane + i] = a; });
-  if (!failed && p.part_w1) {
+  if (p.part_w) combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane + i] = a; });
+  if (p.part_w1) {
     float4* to = reinterpret_cast<float4*>(p.part_w1) + plane;
     if (!shared)
-      failed = !combine(ts, [&](int i, float4 a) { to[i] = a; });
+      combine(ts, [&](int i, float4 a) { to[i] = a; });
     else if (rp.teams > 1)
       for (int i = threadIdx.x; i < V * (E / 4); i += rp.teams * T) to[i] = s_dw1[i];
     else
       combine(ts, [&](int i, float4) { to[i] = s_dw1[i]; });
-  }
-  if (failed) {
-    atomicOr(p.err, 1u);
-    *static_cast<volatile int*>(&s.abort) = 1;
   }
 }
 
 // 16-bit types with more than four vectors per thread and fp32 with more than six,
 // whose sums would not fit in registers, stay with the row kernel.
 template <int DT, int VPT, bool NORM, int GATE, int DROP>
-__global__ void __launch_bounds__(512 + 32 * kProducers, 1)
+__global__ void __launch_bounds__(kRingThreads, 1)
     reduce_branch_rmsnorm_backward_tma_kernel(const __grid_constant__ BranchBackwardTmaParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ RingShared s;
@@ -360,15 +347,19 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1)
   float4* s_dw1 = reinterpret_cast<float4*>(s_rows + (size_t)p.weight_rows * (kWideRows<VPT> ? V * E * 4 : rp.row_bytes));
   float4* s_comb = s_dw1 + (p.shared ? V * (E / 4) : 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) ring_init(rp, s);
+  ring_init(rp, s);
   const Tiles first(rp);
-  if (warp == consumers >> 5 && lane < rp.ranks + rp.held && first.more())
+  if (warp == kRingConsumers / 32 && lane < rp.ranks + rp.held && first.more())
     prefetch_l2(slice_source(p, lane) + first.row * (int64_t)rp.row_bytes, (uint32_t)first.count(rp) * (uint32_t)rp.row_bytes);
   __syncthreads();
   pdl_wait_and_release();
-  if (warp >= consumers >> 5) {
-    if (lane == 0) ring_produce(rp, smem, s, warp - (consumers >> 5), p.err, [&](int q) { return slice_source(p, q); });
+  if (warp >= kRingConsumers / 32) {
+    take_registers<false>();
+    const int who = warp - kRingConsumers / 32;
+    if (lane == 0 && who < rp.producers) ring_produce(rp, smem, s, who, p.err, [&](int q) { return slice_source(p, q); });
   } else {
+    take_registers<true>();
+    if (threadIdx.x >= consumers) return;
     if constexpr (kWideRows<VPT>) {
       row_to_shared<DT>(p.weight, nullptr, V, consumers, s_rows);
       if (NORM || p.factor)
@@ -382,7 +373,7 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1)
     }
     if (p.shared)
       for (int i = threadIdx.x; i < V * (E / 4); i += consumers) s_dw1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
+    consumers_barrier(rp);
     consume<DT, VPT, NORM, GATE, DROP>(p, smem, s_rows, s_comb, s_dw1, s);
   }
 }
@@ -522,8 +513,7 @@ cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, con
   p.gate_span = (uint32_t)std::max<int64_t>(br.gate_span, 1);
   const RingPlan& rp = p.ring;
   cudaError_t e = launch_pdl(pick(dtype, sh.vpt, br.norm_weight != nullptr, gate_kind(br), br.drop.active), (unsigned)sh.grid,
-                             (unsigned)(sh.teams * sh.team_threads + 32 * rp.producers),
-                             (size_t)rp.stages * rp.group * rp.teams * rp.row_bytes + beside, s, 1, p);
+                             (unsigned)kRingThreads, (size_t)rp.stages * rp.group * rp.teams * rp.row_bytes + beside, s, 1, p);
   return e == cudaSuccess ? launch_branch_sums(br, g, dtype, sh.grid, rows, cols, s) : e;
 }
 

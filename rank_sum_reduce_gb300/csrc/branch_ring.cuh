@@ -34,6 +34,20 @@ enum DropKind : int { kDropNone = 0, kDropYes = 1, kDropAny = 2 };
 enum GateFrom : int { kFromFactor = 0, kFromRing = 1, kFromRows = 2 };
 inline int gate_kind(const BranchArgs& br) { return !br.gate ? kGateNone : br.gate_span == 0 ? kGateOwn : kGateShared; }
 
+// A CTA is four warpgroups of consumers (of which the teams may leave a few warps
+// idle) and one whose first warps issue copies.  It is launched with 96 registers a
+// thread, the most that five warps on each of the SM's schedulers can have, and the
+// consumers take what the producers do without: 512 * 112 + 128 * 24 registers of
+// 640 * 96.  In 96 the backward spills 40 to 90 bytes, which costs more than
+// anything else in a row (W = 1, M = 13332, N = 1160 fp16, one gate: 66 us against
+// 43; N = 11072, W = 4, M = 2000 with norms 105 against 97).
+constexpr int kRingConsumers = 512, kRingThreads = 640;
+template <bool CONSUMER>
+__device__ __forceinline__ void take_registers() {  // every thread of a warpgroup
+  if constexpr (CONSUMER) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+}
+
 // The tiles of this CTA in order.
 struct Tiles {
   int row, end, cut, step;
@@ -64,23 +78,20 @@ struct Tiles {
 // Barriers and small arrays (static shared memory).
 struct RingShared {
   uint64_t full[kMaxRingStages], empty[kMaxRingStages];
-  uint64_t rowbar[16];      // by team
-  uint64_t done[2];         // all consumer warps
-  float warp[96];           // [teams][2][3][warps of a team]
+  float4 warp[48];          // [teams][2][3][warps of a team, in fours]: a team has 512 / teams threads at most
   int abort;
 };
 
-__device__ __forceinline__ void ring_init(const RingPlan& p, RingShared& s) {  // one thread
-  const uint32_t nwarps = (uint32_t)(p.teams * p.team_threads) >> 5;
-  for (int i = 0; i < p.stages; i++) {
-    mbar_init(&s.full[i], p.producers);
-    mbar_init(&s.empty[i], nwarps);
+__device__ __forceinline__ void ring_init(const RingPlan& p, RingShared& s) {  // all threads, before a barrier
+  if (threadIdx.x < 48) s.warp[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; i++) {
+      mbar_init(&s.full[i], p.producers);
+      mbar_init(&s.empty[i], (uint32_t)(p.teams * p.team_threads) >> 5);
+    }
+    s.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int t = 0; t < p.teams; t++) mbar_init(&s.rowbar[t], (uint32_t)(p.team_threads >> 5));
-  mbar_init(&s.done[0], nwarps);
-  mbar_init(&s.done[1], nwarps);
-  s.abort = 0;
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
 // Producer `who` of p.producers: issues every p.producers-th slice of each stage,
@@ -128,14 +139,24 @@ __device__ __forceinline__ void ring_produce(const RingPlan& p, uint8_t* ring, R
   }
 }
 
-// A consumer thread's place in the ring.
+// A consumer thread's place in the ring.  Where a wait runs out the thread carries
+// on with whatever the stage holds and stores nothing more: it reaches every one of
+// its team's barriers, which have no limit of their own, and later waits return at
+// once.
 struct RingReader {
   const RingPlan& p;
   RingShared& s;
+  unsigned int* err;
   int place = 0;
   uint32_t phase = 0;
-  __device__ __forceinline__ RingReader(const RingPlan& plan, RingShared& shared) : p(plan), s(shared) {}
-  __device__ __forceinline__ bool wait() { return wait_bounded(&s.full[place], phase, &s.abort); }
+  bool failed = false;
+  __device__ __forceinline__ RingReader(const RingPlan& plan, RingShared& shared, unsigned int* e) : p(plan), s(shared), err(e) {}
+  __device__ __forceinline__ void wait() {
+    if (failed || wait_bounded(&s.full[place], phase, &s.abort)) return;
+    failed = true;
+    atomicOr(err, 1u);
+    *static_cast<volatile int*>(&s.abort) = 1;
+  }
   __device__ __forceinline__ void release() {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&s.empty[place]);
@@ -145,43 +166,46 @@ struct RingReader {
     }
   }
   // A tile in which this team has no row.
-  __device__ __forceinline__ bool skip() {
+  __device__ __forceinline__ void skip() {
     for (int k = 0; k < p.tile_stages; k++) {
-      if (!wait()) return false;
+      wait();
       release();
     }
-    return true;
   }
 };
 
 // The rank sum of this thread's vectors of a row, from the stages that hold the
-// ranks; `mine` is its first vector in stage 0.  Leaves the reader at the stage
-// that holds the row's other slices, waited for, and returns where they begin;
-// null when a wait ran out.
-template <int DT, int VPT>
+// ranks; `mine` is the row in stage 0, at[k] this thread's vectors in it.  Leaves
+// the reader at the stage that holds the row's other slices, waited for, and
+// returns where they begin.
+//
+// Without BRANCHES a thread whose vectors lie past the row's end works on its last
+// one (at[]) and leaves its sums and stores out, here and in what follows: with no
+// branches around them the vectors' loads and arithmetic overlap.  Where many
+// values are alive that would spill.
+template <int DT, int VPT, bool BRANCHES>
 __device__ __forceinline__ const uint8_t* ring_rank_sum(const RingPlan& p, RingReader& in, const uint8_t* mine,
-                                                        const bool (&ok)[VPT], float2 (&acc)[VPT][Pack<DT>::kN / 2]) {
+                                                        const bool (&ok)[VPT], const int (&at)[VPT], float2 (&acc)[VPT][Pack<DT>::kN / 2]) {
   constexpr int E = Pack<DT>::kN;
   const uint32_t stride = (uint32_t)p.teams * (uint32_t)p.row_bytes;
   const bool whole = p.tile_stages == 1;
   int q = 0;
   while (true) {
-    if (!in.wait()) return nullptr;
-    const uint8_t* at = mine + (uint32_t)in.place * (uint32_t)p.group * stride;
-    if (q == p.ranks) return at;
+    in.wait();
+    const uint8_t* slice = mine + (uint32_t)in.place * (uint32_t)p.group * stride;
+    if (q == p.ranks) return slice;
     const int n = min(p.group, p.ranks - q);
-    for (int i = 0; i < n; i++, at += stride) {
+    for (int i = 0; i < n; i++, slice += stride) {
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
-        if (ok[k]) {
-          float2 f[E / 2];
-          widen2<DT>(lds16(at + 16 * k * p.team_threads), f);
+        if (BRANCHES && !ok[k]) continue;
+        float2 f[E / 2];
+        widen2<DT>(lds16(slice + at[k]), f);
 #pragma unroll
-          for (int e = 0; e < E / 2; e++) acc[k][e] = q + i == 0 ? f[e] : add2(acc[k][e], f[e]);
-        }
+        for (int e = 0; e < E / 2; e++) acc[k][e] = q + i == 0 ? f[e] : add2(acc[k][e], f[e]);
       }
     }
-    if (whole) return at;
+    if (whole) return slice;
     q += n;
     in.release();
   }
@@ -196,13 +220,26 @@ __device__ __forceinline__ float2 half_totals(float v) {
   return (threadIdx.x & 16) ? make_float2(other, v) : make_float2(v, other);
 }
 
-// Sums over a row: the warps of a team.  Every warp adds the warps' partials
-// itself, in the same order; they are double-buffered by the parity of the
-// team's exchange number x (what exchange x wrote is overwritten by x + 2, after
-// the barrier of x + 1, which a warp reaches only once it has read x's).
+// Barriers of the consumers: one for each team of several warps (there are at most
+// eight), one for all.
+__device__ __forceinline__ void team_barrier(const RingPlan& p, int team) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(p.team_threads) : "memory");
+}
+__device__ __forceinline__ void consumers_barrier(const RingPlan& p) {
+  __syncwarp();
+  asm volatile("bar.sync 15, %0;" ::"r"(p.teams * p.team_threads) : "memory");
+}
+
+// Sums over a row: the warps of a team.  Every thread adds the warps' partials
+// itself, in the same order; they are double-buffered by the parity of the team's
+// exchange number x (what exchange x wrote is overwritten by x + 2, after the
+// barrier of x + 1, which a warp reaches only once it has read x's).  The row waits
+// for each exchange twice, so it is kept short: a barrier in hardware and broadcast
+// loads in place of mbarriers and a second round of shuffles.
 template <int NS>
-__device__ __forceinline__ bool team_sums(const RingPlan& p, RingShared& s, int team, uint32_t x, float (&v)[NS]) {
-  const int lane = threadIdx.x & 31, nwarps = p.team_threads >> 5, warp = (threadIdx.x - team * p.team_threads) >> 5;
+__device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int team, uint32_t x, float (&v)[NS]) {
+  const int nwarps = p.team_threads >> 5, fours = (nwarps + 3) >> 2, warp = (threadIdx.x - team * p.team_threads) >> 5;
   const bool upper = threadIdx.x & 16;
   if constexpr (NS >= 2) {
     const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[1], 16);
@@ -211,27 +248,28 @@ __device__ __forceinline__ bool team_sums(const RingPlan& p, RingShared& s, int 
     v[1] = t.y;
   }
   if constexpr (NS != 2) v[NS - 1] = warp_total(v[NS - 1]);
-  if (nwarps == 1) return true;
-  float* w = s.warp + (team * 2 + (x & 1u)) * 3 * nwarps;
-  if (lane == 0) {
+  if (nwarps == 1) return;
+  const float4* w = s.warp + (team * 2 + (x & 1u)) * 3 * fours;
+  if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int i = 0; i < NS; i++) w[i * nwarps + warp] = v[i];
-    mbar_arrive(&s.rowbar[team]);
+    for (int i = 0; i < NS; i++) const_cast<float*>(reinterpret_cast<const float*>(w))[i * 4 * fours + warp] = v[i];
   }
-  if (!wait_bounded(&s.rowbar[team], x & 1u, &s.abort)) return false;
-  const int part = lane & 15;
-  if constexpr (NS >= 2) {
-    const float2 t = half_totals(part < nwarps ? w[(lane >> 4) * nwarps + part] : 0.f);
-    v[0] = t.x;
-    v[1] = t.y;
-  }
-  if constexpr (NS != 2) {
-    float t = part < nwarps ? w[(NS - 1) * nwarps + part] : 0.f;
+  team_barrier(p, team);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
-    v[NS - 1] = t;
+  for (int i = 0; i < NS; i++) {
+    const float4 t = w[i * fours];
+    v[i] = __fadd_rn(__fadd_rn(t.x, t.y), __fadd_rn(t.z, t.w));
   }
-  return true;
+#pragma unroll
+  for (int j = 1; j < 4; j++) {
+    if (j < fours) {
+#pragma unroll
+      for (int i = 0; i < NS; i++) {
+        const float4 t = w[i * fours + j];
+        v[i] = __fadd_rn(v[i], __fadd_rn(__fadd_rn(t.x, t.y), __fadd_rn(t.z, t.w)));
+      }
+    }
+  }
 }
 
 // Rows of factors in shared memory, in fp32: every vector of them is used once or

@@ -4,10 +4,8 @@
 // over both of its exchanges, and while one team of warps waits for its row's
 // sums another folds.
 //
-// Two vectors per thread: the weight and the factor norm_weight * gate (a gate of
-// all rows) lie in shared memory, in fp32.  Longer rows leave the ring no room for
-// that: both norms' weights lie there packed, or in L2, and the gate in L2, as for
-// all rows a gate row that some of them share.
+// The rows of weights, and a gate of all rows, lie in shared memory as they are, or
+// in L2 where they would leave the ring less than six slices.
 #include <algorithm>
 
 #include "branch_ring.cuh"
@@ -28,10 +26,9 @@ struct BranchTmaParams {
   DropParams drop;
   float residual_scale;
   float eps, norm_eps;
-  float cols;
+  float inv_cols;
   int gate_from;
-  bool factor;              // z is multiplied by a factor row: norm_weight, a gate of all rows or both
-  bool packed;              // rows of weights in shared memory where they are not in fp32
+  bool packed;              // the rows of weights lie in shared memory
   uint32_t gate_span;       // rows that share a gate row (kGateRows)
   RingPlan ring;
 };
@@ -41,129 +38,115 @@ __device__ __forceinline__ const uint8_t* slice_source(const BranchTmaParams& p,
                           : q == p.ring.ranks ? p.residual : reinterpret_cast<const uint8_t*>(p.gate);
 }
 
-template <int VPT>
-constexpr bool kWideRows = VPT == 2;
-
-// Weight row i (0: weight, 1: factor), vector v.
-template <int DT, int VPT>
-__device__ __forceinline__ void weight_at(const BranchTmaParams& p, const uint8_t* s_rows, int i, int v,
-                                          float2 (&f)[Pack<DT>::kN / 2]) {
-  const int V = p.ring.vec_per_row;
-  if constexpr (kWideRows<VPT>)
-    row_from_shared<DT>(s_rows + (size_t)i * V * Pack<DT>::kN * 4, V, v, f);
-  else
-    widen2<DT>(p.packed ? lds16(s_rows + (size_t)i * p.ring.row_bytes + 16 * v) : __ldg((i == 0 ? p.weight : p.norm_weight) + v), f);
+// Weight row i (0: weight, 1: norm_weight, 2: a gate of all rows), vector v.
+__device__ __forceinline__ uint4 weight_at(const BranchTmaParams& p, const uint8_t* s_rows, int i, int v) {
+  return p.packed ? lds16(s_rows + (size_t)i * p.ring.row_bytes + 16 * v)
+                  : __ldg((i == 0 ? p.weight : i == 1 ? p.norm_weight : p.gate) + v);
 }
 
 template <int DT, int VPT, bool NORM, int GATE, int DROP>
 __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t* ring, const uint8_t* s_rows, RingShared& s) {
   constexpr int E = Pack<DT>::kN;
+  constexpr bool BRANCHES = VPT > 4;
   constexpr bool SHARED = GATE == kGateShared || GATE == kGateAny, OWN = GATE == kGateOwn || GATE == kGateAny;
   const RingPlan& rp = p.ring;
   const bool own = OWN && (GATE == kGateOwn || p.gate_from == kFromRing), rows = SHARED && p.gate_from == kFromRows;
   const int T = rp.team_threads, V = rp.vec_per_row;
   const int team = threadIdx.x / T, tid = threadIdx.x - team * T;
   const uint32_t stride = (uint32_t)rp.teams * (uint32_t)rp.row_bytes;
-  const uint8_t* mine = ring + (size_t)team * rp.row_bytes + 16 * tid;  // this thread's first vector in stage 0
+  const uint8_t* mine = ring + (size_t)team * rp.row_bytes;  // the row in stage 0
   const DropState state = drop_state(p.drop);
   bool ok[VPT];
+  int col[VPT], at[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; k++) ok[k] = tid + k * T < V;
-  RingReader in(rp, s);
+  for (int k = 0; k < VPT; k++) {
+    ok[k] = tid + k * T < V;
+    col[k] = min(tid + k * T, V - 1);
+    at[k] = 16 * col[k];
+  }
+  RingReader in(rp, s, p.err);
   uint32_t x = 0;
-  bool failed = false;
-  for (Tiles t(rp); t.more() && !failed; t.next(rp)) {
+  for (Tiles t(rp); t.more(); t.next(rp)) {
     if (team >= t.count(rp)) {
-      failed = !in.skip();
+      in.skip();
       continue;
     }
     const int row = t.row + team;
-    const int64_t at = (int64_t)row * V + tid;
+    const int64_t base = (int64_t)row * V;
     float2 z[VPT][E / 2];
-    const uint8_t* held = ring_rank_sum<DT, VPT>(rp, in, mine, ok, z);
-    if (!held) {
-      failed = true;
-      break;
+    const uint8_t* held = ring_rank_sum<DT, VPT, BRANCHES>(rp, in, mine, ok, at, z);
+    if (in.failed) {
+#pragma unroll
+      for (int k = 0; k < VPT; k++) ok[k] = false;
     }
     if (p.ar_out) {
 #pragma unroll
       for (int k = 0; k < VPT; k++)
-        if (ok[k]) st16(p.ar_out + at + k * T, narrow2<DT>(z[k]));
+        if (ok[k]) st16(p.ar_out + base + col[k], narrow2<DT>(z[k]));
     }
     float2 inv = both(1.f);
     if constexpr (NORM) {
-      float2 ss = make_float2(0.f, 0.f);
+      float v[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
-        if (ok[k]) {
+        if (BRANCHES && !ok[k]) continue;
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < E / 2; e++) ss = fma2(z[k][e], z[k][e], ss);
-        }
+        for (int e = 0; e < E / 2; e++) ss = fma2(z[k][e], z[k][e], ss);
+        v[0] += ok[k] ? ss.x + ss.y : 0.f;
       }
-      float v[1] = {ss.x + ss.y};
-      if (!team_sums(rp, s, team, x++, v)) {
-        failed = true;
-        break;
-      }
-      inv = both(rsqrtf(__fdiv_rn(v[0], p.cols) + p.norm_eps));
+      team_sums(rp, s, team, x++, v);
+      inv = both(rsqrtf(fmaf(v[0], p.inv_cols, p.norm_eps)));
     }
-    const uint4* grow = rows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V + tid : nullptr;
-    float2 ss = make_float2(0.f, 0.f);
+    const uint4* grow = rows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V : nullptr;
+    float v[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
-      if (ok[k]) {
-        float2 f[E / 2];
-        if (NORM || (SHARED && p.factor)) {
-          weight_at<DT, VPT>(p, s_rows, 1, tid + k * T, f);
+      if (BRANCHES && !ok[k]) continue;
+      float2 f[E / 2];
+      if constexpr (NORM) {
+        widen2<DT>(weight_at(p, s_rows, 1, col[k]), f);
 #pragma unroll
-          for (int e = 0; e < E / 2; e++) z[k][e] = mul2(NORM ? mul2(z[k][e], inv) : z[k][e], f[e]);
-        }
-        if (own || rows) {
-          widen2<DT>(own ? lds16(held + stride + 16 * k * T) : __ldg(grow + k * T), f);
-#pragma unroll
-          for (int e = 0; e < E / 2; e++) z[k][e] = mul2(z[k][e], f[e]);
-        }
-        if (DROP == kDropYes || (DROP == kDropAny && p.drop.active)) {
-          uint32_t bits[E / 2];
-          drop_bits<E>(state, at + k * T, bits);
-#pragma unroll
-          for (int e = 0; e < E / 2; e++) z[k][e] = drop2(p.drop, bits[e], z[k][e]);
-        }
-        widen2<DT>(lds16(held + 16 * k * T), f);
-#pragma unroll
-        for (int e = 0; e < E / 2; e++) {
-          z[k][e] = fma2(both(p.residual_scale), f[e], z[k][e]);
-          ss = fma2(z[k][e], z[k][e], ss);
-        }
-        st16(p.residual_out + at + k * T, narrow2<DT>(z[k]));
+        for (int e = 0; e < E / 2; e++) z[k][e] = mul2(mul2(z[k][e], inv), f[e]);
       }
+      if (GATE && (GATE != kGateAny || p.gate)) {
+        widen2<DT>(own ? lds16(held + stride + at[k]) : rows ? __ldg(grow + col[k]) : weight_at(p, s_rows, 2, col[k]), f);
+#pragma unroll
+        for (int e = 0; e < E / 2; e++) z[k][e] = mul2(z[k][e], f[e]);
+      }
+      if (DROP == kDropYes || (DROP == kDropAny && p.drop.active)) {
+        uint32_t bits[E / 2];
+        drop_bits<E>(state, base + col[k], bits);
+#pragma unroll
+        for (int e = 0; e < E / 2; e++) z[k][e] = drop2(p.drop, bits[e], z[k][e]);
+      }
+      widen2<DT>(lds16(held + at[k]), f);
+      float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < E / 2; e++) {
+        z[k][e] = fma2(both(p.residual_scale), f[e], z[k][e]);
+        ss = fma2(z[k][e], z[k][e], ss);
+      }
+      v[0] += ok[k] ? ss.x + ss.y : 0.f;
+      if (ok[k]) st16(p.residual_out + base + col[k], narrow2<DT>(z[k]));
     }
     in.release();
-    float v[1] = {ss.x + ss.y};
-    if (!team_sums(rp, s, team, x++, v)) {
-      failed = true;
-      break;
-    }
-    const float2 r = both(rsqrtf(__fdiv_rn(v[0], p.cols) + p.eps));
+    team_sums(rp, s, team, x++, v);
+    const float2 r = both(rsqrtf(fmaf(v[0], p.inv_cols, p.eps)));
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
-      if (ok[k]) {
-        float2 f[E / 2];
-        weight_at<DT, VPT>(p, s_rows, 0, tid + k * T, f);
+      if (BRANCHES && !ok[k]) continue;
+      float2 f[E / 2];
+      widen2<DT>(weight_at(p, s_rows, 0, col[k]), f);
 #pragma unroll
-        for (int e = 0; e < E / 2; e++) f[e] = mul2(mul2(z[k][e], r), f[e]);
-        st16(p.norm_out + at + k * T, narrow2<DT>(f));
-      }
+      for (int e = 0; e < E / 2; e++) f[e] = mul2(mul2(z[k][e], r), f[e]);
+      if (ok[k]) st16(p.norm_out + base + col[k], narrow2<DT>(f));
     }
-  }
-  if (failed) {
-    atomicOr(p.err, 1u);
-    *static_cast<volatile int*>(&s.abort) = 1;
   }
 }
 
 template <int DT, int VPT, bool NORM, int GATE, int DROP>
-__global__ void __launch_bounds__(512 + 32 * kProducers, 1)
+__global__ void __launch_bounds__(kRingThreads, 1)
     reduce_branch_residual_rmsnorm_tma_kernel(const __grid_constant__ BranchTmaParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ RingShared s;
@@ -171,28 +154,27 @@ __global__ void __launch_bounds__(512 + 32 * kProducers, 1)
   uint8_t* s_rows = smem + (size_t)rp.stages * rp.group * rp.teams * rp.row_bytes;
   const int consumers = rp.teams * rp.team_threads, V = rp.vec_per_row;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) ring_init(rp, s);
+  ring_init(rp, s);
   // the first tile into L2 while the previous grid of the stream finishes
   const Tiles first(rp);
-  if (warp == consumers >> 5 && lane < rp.ranks + rp.held && first.more())
+  if (warp == kRingConsumers / 32 && lane < rp.ranks + rp.held && first.more())
     prefetch_l2(slice_source(p, lane) + first.row * (int64_t)rp.row_bytes, (uint32_t)first.count(rp) * (uint32_t)rp.row_bytes);
   __syncthreads();
   pdl_wait_and_release();
-  if (warp >= consumers >> 5) {
-    if (lane == 0) ring_produce(rp, smem, s, warp - (consumers >> 5), p.err, [&](int q) { return slice_source(p, q); });
+  if (warp >= kRingConsumers / 32) {
+    take_registers<false>();
+    const int who = warp - kRingConsumers / 32;
+    if (lane == 0 && who < rp.producers) ring_produce(rp, smem, s, who, p.err, [&](int q) { return slice_source(p, q); });
   } else {
-    if constexpr (kWideRows<VPT>) {
-      row_to_shared<DT>(p.weight, nullptr, V, consumers, s_rows);
-      if (NORM || p.factor)
-        row_to_shared<DT>(NORM ? p.norm_weight : nullptr, p.gate_from == kFromFactor ? p.gate : nullptr, V, consumers,
-                          s_rows + (size_t)V * Pack<DT>::kN * 4);
-      asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
-    } else if (p.packed) {
+    take_registers<true>();
+    if (threadIdx.x >= consumers) return;
+    if (p.packed) {
       for (int v = threadIdx.x; v < V; v += consumers) {
         reinterpret_cast<uint4*>(s_rows)[v] = __ldg(p.weight + v);
         if constexpr (NORM) reinterpret_cast<uint4*>(s_rows)[V + v] = __ldg(p.norm_weight + v);
+        if (GATE && p.gate && p.gate_from == kFromFactor) reinterpret_cast<uint4*>(s_rows)[2 * V + v] = __ldg(p.gate + v);
       }
-      asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
+      consumers_barrier(rp);
     }
     consume<DT, VPT, NORM, GATE, DROP>(p, smem, s_rows, s);
   }
@@ -202,15 +184,15 @@ using BranchTmaFn = void (*)(const BranchTmaParams);
 
 template <int DT, int VPT, bool NORM>
 BranchTmaFn pick_parts(int gate, bool drop) {
-  if constexpr (VPT == 2) {
+  if constexpr (VPT == 2 || VPT == 4) {
     if (gate == kGateNone)
-      return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, 2, NORM, kGateNone, kDropYes>
-                  : reduce_branch_residual_rmsnorm_tma_kernel<DT, 2, NORM, kGateNone, kDropNone>;
+      return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateNone, kDropYes>
+                  : reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateNone, kDropNone>;
     if (gate == kGateShared)
-      return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, 2, NORM, kGateShared, kDropYes>
-                  : reduce_branch_residual_rmsnorm_tma_kernel<DT, 2, NORM, kGateShared, kDropNone>;
-    return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, 2, NORM, kGateOwn, kDropYes>
-                : reduce_branch_residual_rmsnorm_tma_kernel<DT, 2, NORM, kGateOwn, kDropNone>;
+      return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateShared, kDropYes>
+                  : reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateShared, kDropNone>;
+    return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateOwn, kDropYes>
+                : reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateOwn, kDropNone>;
   } else {
     if (gate == kGateNone && !drop) return reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateNone, kDropNone>;
     return reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateAny, kDropAny>;
@@ -239,11 +221,9 @@ BranchTmaFn pick(int dtype, int vpt, bool norm, int gate, bool drop) {
 constexpr int kSharedBudget = 222 * 1024;  // ring and rows of weights; RingShared is static
 
 // Where a call's weights lie, and its ring; the bytes beside the ring.
-bool fit(int dtype, int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh, BranchTmaParams* p,
-         int* beside) {
-  const bool norm = br.norm_weight != nullptr, wide = sh.vpt == 2, column = br.gate && br.gate_span == rows;
-  p->gate_from = !br.gate ? kFromFactor : br.gate_span == 0 ? kFromRing : wide && column ? kFromFactor : kFromRows;
-  p->factor = norm || (wide && column);
+bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh, BranchTmaParams* p, int* beside) {
+  const bool column = br.gate && br.gate_span == rows;
+  p->gate_from = !br.gate || column ? kFromFactor : br.gate_span == 0 ? kFromRing : kFromRows;
   RingPlan& rp = p->ring;
   rp.rows = (int)rows;
   rp.row_bytes = vec_per_row * 16;
@@ -254,12 +234,9 @@ bool fit(int dtype, int W, const BranchArgs& br, int64_t rows, int vec_per_row, 
   rp.tile_rows = sh.tile_rows;
   rp.team_threads = sh.team_threads;
   rp.gate_span = 0;
-  const int weights = (p->factor ? 2 : 1) * rp.row_bytes;
-  p->packed = !wide;
-  *beside = wide && dtype != kFP32 ? 2 * weights : weights;
-  if (branch_ring_fit(kSharedBudget - *beside, &rp) && (wide || rp.stages * rp.group >= 6)) return true;
-  if (wide) return false;
-  p->packed = false;
+  *beside = (column ? 3 : br.norm_weight ? 2 : 1) * rp.row_bytes;
+  p->packed = branch_ring_fit(kSharedBudget - *beside, &rp) && rp.stages * rp.group >= 6;
+  if (p->packed) return true;
   *beside = 0;
   return branch_ring_fit(kSharedBudget, &rp);
 }
@@ -276,15 +253,21 @@ bool branch_ring_fit(int budget, RingPlan* p) {
     p->tile_stages = (p->ranks + p->group - 1) / p->group + 1;
   }
   p->stages = std::min(places / p->group, kMaxRingStages);
+  if (p->tile_stages == 1) p->stages = std::min(p->stages, std::max(3, 96 * 1024 / (p->group * p->teams * p->row_bytes)));
   p->producers = kProducers;
   return p->stages >= 2;
 }
 
-// Two vectors per thread for rows of up to 1024 vectors, three where that fits
-// clearly better or for longer ones, four only for rows that three do not hold,
-// above 2048 as few as 512 threads need (see norm_backward_tma.cu).
-bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out) {
-  const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512 : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
+// Vectors per thread: four, or as many of two to eight as leave clearly fewer of
+// the threads' places empty; the fewer warps a row has, the less of its time goes
+// into the exchanges (W = 1, M = 16389, N = 4096 bf16 with both norms and dropout:
+// two 121 us, four 97).  With four ranks and more two, three where that fits better
+// (W = 4, M = 4096, N = 2048 19.3 us, with four 20.4).  Rows of more than 2048
+// vectors take as many as 512 threads need.
+bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BranchTeams* out) {
+  const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512
+                  : W <= 3           ? team_vectors(vec_per_row, 4, 8)
+                                     : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
   if (vpt > 8) return false;
   out->vpt = vpt;
   out->use = team_use(vec_per_row, vpt);
@@ -296,10 +279,10 @@ bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* o
   return true;
 }
 
-bool branch_tma_fits(int dtype, int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh) {
+bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh) {
   BranchTmaParams p;
   int beside;
-  return fit(dtype, W, br, rows, vec_per_row, sh, &p, &beside);
+  return fit(W, br, rows, vec_per_row, sh, &p, &beside);
 }
 
 cudaError_t branch_tma_prepare(int dtype, const BranchTeams& sh) {
@@ -317,7 +300,7 @@ cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const Branch
                               cudaStream_t s) {
   BranchTmaParams p;
   int beside;
-  if (!fit(dtype, W, br, rows, vec_per_row, sh, &p, &beside)) return cudaErrorInvalidValue;
+  if (!fit(W, br, rows, vec_per_row, sh, &p, &beside)) return cudaErrorInvalidValue;
   p.in = in;
   p.residual = static_cast<const uint8_t*>(residual);
   p.weight = static_cast<const uint4*>(weight);
@@ -331,12 +314,11 @@ cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const Branch
   p.residual_scale = br.residual_scale;
   p.eps = eps;
   p.norm_eps = br.norm_eps;
-  p.cols = (float)cols;
+  p.inv_cols = 1.f / (float)cols;
   p.gate_span = (uint32_t)std::max<int64_t>(br.gate_span, 1);
   const RingPlan& rp = p.ring;
   return launch_pdl(pick(dtype, sh.vpt, br.norm_weight != nullptr, gate_kind(br), br.drop.active), (unsigned)sh.grid,
-                    (unsigned)(sh.teams * sh.team_threads + 32 * rp.producers),
-                    (size_t)rp.stages * rp.group * rp.teams * rp.row_bytes + beside, s, 1, p);
+                    (unsigned)kRingThreads, (size_t)rp.stages * rp.group * rp.teams * rp.row_bytes + beside, s, 1, p);
 }
 
 }  // namespace car
