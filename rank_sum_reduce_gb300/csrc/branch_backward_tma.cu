@@ -188,6 +188,15 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
     } else {
       const int row = tile + team;
       const int64_t base = (int64_t)row * V;
+      // a shared gate row from L2, asked for before the row's waits where registers allow
+      constexpr bool EARLY = SHARED && VPT * E <= 16;
+      const bool rows = SHARED && p.gate_from == kFromRows;
+      uint4 gv[EARLY ? VPT : 1];
+      const uint4* grow = rows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V : nullptr;
+      if (EARLY && rows) {
+#pragma unroll
+        for (int k = 0; k < VPT; k++) gv[EARLY ? k : 0] = __ldg(grow + col[k]);
+      }
       float2 g[VPT][E / 2];
       const uint8_t* held = ring_rank_sum<DT, VPT, BRANCHES>(rp, in, mine, ok, at, g);
       if (in.failed) {
@@ -224,7 +233,6 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       const float r = rsqrtf(fmaf(v[0], p.inv_cols, p.eps));
       const float2 m = both(-__fmul_rn(__fmul_rn(v[1], p.inv_cols), r));
       const float2 qn = NORM ? both(rsqrtf(fmaf(v[NORM ? 2 : 0], p.inv_cols, p.norm_eps))) : both(1.f);
-      const uint4* grow = SHARED && p.gate_from == kFromRows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V : nullptr;
       float vu = 0.f;
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
@@ -276,8 +284,8 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
 #pragma unroll
             for (int e = 0; e < E / 2; e++) ts[k][e] = fma2(g[k][e], u1[e], ts[k][e]);
           }
-          if (SHARED && p.gate_from == kFromRows) {
-            widen2<DT>(__ldg(grow + col[k]), d);
+          if (rows) {
+            widen2<DT>(EARLY ? gv[EARLY ? k : 0] : __ldg(grow + col[k]), d);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], d[e]);
           }

@@ -94,6 +94,25 @@ __device__ __forceinline__ void ring_init(const RingPlan& p, RingShared& s) {  /
   }
 }
 
+// As wait_bounded (ring.cuh), but a thread that has to wait is suspended for up to a
+// few microseconds at a time: polling warps take issue slots from the others.
+__device__ __forceinline__ bool wait_suspended(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t i = 0; i < (1u << 30); i++) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(4000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort || globaltimer() - t0 > kWaitLimitNs) return false;
+  }
+  return false;
+}
+
 // Producer `who` of p.producers: issues every p.producers-th slice of each stage,
 // then waits for the stages that were filled.  source(q): slice q of row 0.
 template <class Source>
@@ -110,7 +129,7 @@ __device__ __forceinline__ void ring_produce(const RingPlan& p, uint8_t* ring, R
     for (int q = 0; q < slices;) {
       // a stage ends with the ranks unless all of the tile is one
       const int n = slices <= p.group ? slices : q < p.ranks ? min(p.group, p.ranks - q) : slices - q;
-      if (issued >= (uint32_t)S && !wait_bounded(&s.empty[place], phase ^ 1u, &s.abort)) {
+      if (issued >= (uint32_t)S && !mbar_try_wait(&s.empty[place], phase ^ 1u) && !wait_suspended(&s.empty[place], phase ^ 1u, &s.abort)) {
         ok = false;
         break;
       }
@@ -152,7 +171,7 @@ struct RingReader {
   bool failed = false;
   __device__ __forceinline__ RingReader(const RingPlan& plan, RingShared& shared, unsigned int* e) : p(plan), s(shared), err(e) {}
   __device__ __forceinline__ void wait() {
-    if (failed || wait_bounded(&s.full[place], phase, &s.abort)) return;
+    if (mbar_try_wait(&s.full[place], phase) || failed || wait_suspended(&s.full[place], phase, &s.abort)) return;
     failed = true;
     atomicOr(err, 1u);
     *static_cast<volatile int*>(&s.abort) = 1;
@@ -211,15 +230,6 @@ __device__ __forceinline__ const uint8_t* ring_rank_sum(const RingPlan& p, RingR
   }
 }
 
-// The lower half of the warp adds one sum, the upper half another; both to all
-// lanes.
-__device__ __forceinline__ float2 half_totals(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  const float other = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
-  return (threadIdx.x & 16) ? make_float2(other, v) : make_float2(v, other);
-}
-
 // Barriers of the consumers: one for each team of several warps (there are at most
 // eight), one for all.
 __device__ __forceinline__ void team_barrier(const RingPlan& p, int team) {
@@ -237,38 +247,65 @@ __device__ __forceinline__ void consumers_barrier(const RingPlan& p) {
 // barrier of x + 1, which a warp reaches only once it has read x's).  The row waits
 // for each exchange twice, so it is kept short: a barrier in hardware and broadcast
 // loads in place of mbarriers and a second round of shuffles.
+//
+// Within a warp several sums share their shuffles: after the first step the lower
+// half of the lanes carries one, the upper half another, after the second a quarter
+// each.  Three sums: 6 shuffles, where one after the other would take 15.
 template <int NS>
 __device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int team, uint32_t x, float (&v)[NS]) {
-  const int nwarps = p.team_threads >> 5, fours = (nwarps + 3) >> 2, warp = (threadIdx.x - team * p.team_threads) >> 5;
-  const bool upper = threadIdx.x & 16;
-  if constexpr (NS >= 2) {
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[1], 16);
-    const float2 t = half_totals(__fadd_rn(upper ? v[1] : v[0], other));
-    v[0] = t.x;
-    v[1] = t.y;
+  constexpr uint32_t ALL = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31, nwarps = p.team_threads >> 5, warp = (threadIdx.x - team * p.team_threads) >> 5;
+  float t;        // of sum `which`, in the first of every eight lanes
+  int which = 0;
+  if constexpr (NS == 1) {
+    t = v[0];
+    t += __shfl_xor_sync(ALL, t, 16);
+    t += __shfl_xor_sync(ALL, t, 8);
+  } else {
+    const bool upper = lane & 16;
+    t = (upper ? v[1] : v[0]) + __shfl_xor_sync(ALL, upper ? v[0] : v[1], 16);
+    which = upper ? 1 : 0;
+    if constexpr (NS == 2) {
+      t += __shfl_xor_sync(ALL, t, 8);
+    } else {
+      const float c = v[NS - 1] + __shfl_xor_sync(ALL, v[NS - 1], 16);
+      const bool third = lane & 8;
+      t = (third ? c : t) + __shfl_xor_sync(ALL, third ? t : c, 8);
+      if (third) which = 2;
+    }
   }
-  if constexpr (NS != 2) v[NS - 1] = warp_total(v[NS - 1]);
-  if (nwarps == 1) return;
-  const float4* w = s.warp + (team * 2 + (x & 1u)) * 3 * fours;
-  if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int i = 0; i < NS; i++) const_cast<float*>(reinterpret_cast<const float*>(w))[i * 4 * fours + warp] = v[i];
+  for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(ALL, t, o);
+  if (nwarps == 1) {
+    v[0] = __shfl_sync(ALL, t, 0);
+    if constexpr (NS >= 2) v[1] = __shfl_sync(ALL, t, 16);
+    if constexpr (NS == 3) v[2] = __shfl_sync(ALL, t, 8);
+    return;
   }
+  const int fours = (nwarps + 3) >> 2;
+  float4* w = s.warp + (team * 2 + (x & 1u)) * 3 * fours;
+  // lanes 0, 16 and 8 write the sums 0, 1 and 2
+  if (NS == 1 ? lane == 0 : NS == 2 ? (lane & 15) == 0 : (lane & 7) == 0 && lane < 24)
+    reinterpret_cast<float*>(w)[which * 4 * fours + warp] = t;
   team_barrier(p, team);
 #pragma unroll
   for (int i = 0; i < NS; i++) {
-    const float4 t = w[i * fours];
-    v[i] = __fadd_rn(__fadd_rn(t.x, t.y), __fadd_rn(t.z, t.w));
-  }
+    const float4 f = w[i * fours];
+    float2 a = add2(make_float2(f.x, f.y), make_float2(f.z, f.w));
+    if (fours > 1) {
+      const float4 g = w[i * fours + 1];
+      a = add2(a, add2(make_float2(g.x, g.y), make_float2(g.z, g.w)));
+    }
+    if (fours > 2) {
 #pragma unroll
-  for (int j = 1; j < 4; j++) {
-    if (j < fours) {
-#pragma unroll
-      for (int i = 0; i < NS; i++) {
-        const float4 t = w[i * fours + j];
-        v[i] = __fadd_rn(v[i], __fadd_rn(__fadd_rn(t.x, t.y), __fadd_rn(t.z, t.w)));
+      for (int j = 2; j < 4; j++) {
+        if (j < fours) {
+          const float4 g = w[i * fours + j];
+          a = add2(a, add2(make_float2(g.x, g.y), make_float2(g.z, g.w)));
+        }
       }
     }
+    v[i] = __fadd_rn(a.x, a.y);
   }
 }
 

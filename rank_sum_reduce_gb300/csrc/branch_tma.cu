@@ -73,6 +73,14 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
     }
     const int row = t.row + team;
     const int64_t base = (int64_t)row * V;
+    // a shared gate row from L2, asked for before the row's waits where registers allow
+    constexpr bool EARLY = SHARED && VPT * E <= 16;
+    uint4 gv[EARLY ? VPT : 1];
+    const uint4* grow = rows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V : nullptr;
+    if (EARLY && rows) {
+#pragma unroll
+      for (int k = 0; k < VPT; k++) gv[EARLY ? k : 0] = __ldg(grow + col[k]);
+    }
     float2 z[VPT][E / 2];
     const uint8_t* held = ring_rank_sum<DT, VPT, BRANCHES>(rp, in, mine, ok, at, z);
     if (in.failed) {
@@ -98,7 +106,6 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
       team_sums(rp, s, team, x++, v);
       inv = both(rsqrtf(fmaf(v[0], p.inv_cols, p.norm_eps)));
     }
-    const uint4* grow = rows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * V : nullptr;
     float v[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
@@ -110,7 +117,7 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
         for (int e = 0; e < E / 2; e++) z[k][e] = mul2(mul2(z[k][e], inv), f[e]);
       }
       if (GATE && (GATE != kGateAny || p.gate)) {
-        widen2<DT>(own ? lds16(held + stride + at[k]) : rows ? __ldg(grow + col[k]) : weight_at(p, s_rows, 2, col[k]), f);
+        widen2<DT>(own ? lds16(held + stride + at[k]) : rows ? (EARLY ? gv[EARLY ? k : 0] : __ldg(grow + col[k])) : weight_at(p, s_rows, 2, col[k]), f);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) z[k][e] = mul2(z[k][e], f[e]);
       }
