@@ -65,6 +65,15 @@ __device__ __forceinline__ void drop_bits(const DropState& s, int64_t v, uint32_
   }
 }
 
+// The same, not to be put off until the bits are used: they are computed here, while
+// the row's data is on its way.
+template <int E>
+__device__ __forceinline__ void drop_bits_here(const DropState& s, int64_t v, uint32_t (&bits)[E / 2]) {
+  drop_bits<E>(s, v, bits);
+#pragma unroll
+  for (int e = 0; e < E / 2; e++) asm volatile("" : "+r"(bits[e]));
+}
+
 // Element pair of a word: kept, and scaled, where its 16 bits as the upper half of
 // a word exceed the limit; else 0 (selected, not multiplied, so that what is
 // dropped may be anything).

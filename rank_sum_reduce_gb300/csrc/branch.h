@@ -54,17 +54,14 @@ cudaError_t launch_branch(int dtype, int W, const RankPtrs& in, const BranchArgs
                           unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh,
                           const WaitHook& hook, cudaStream_t s);
 
-struct BranchTeams : TeamShape {
-  int tile_rows;  // rows of a tile, at most teams
-};
 // ---- forward, many rows (branch_tma.cu); false when a row is too long ----
-bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BranchTeams* out);
+bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, TeamShape* out);
 // Whether this call's slices and weights fit beside one another.
-bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh);
-cudaError_t branch_tma_prepare(int dtype, const BranchTeams& sh);
+bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const TeamShape& sh);
+cudaError_t branch_tma_prepare(int dtype, const TeamShape& sh);
 cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const BranchArgs& br, const void* residual,
                               const void* weight, float eps, void* residual_out, void* norm_out, void* ar_out,
-                              unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const BranchTeams& sh,
+                              unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const TeamShape& sh,
                               cudaStream_t s);
 // The ring of either pipeline (branch_ring.cuh).
 constexpr int kMaxRingStages = 32;
@@ -77,8 +74,7 @@ struct RingPlan {
   int group;            // slices that a stage has room for
   int tile_stages;      // stages of a tile
   int stages;           // of the ring
-  int teams;            // teams of consumer warps, of which each takes a row of a tile
-  int tile_rows;        // at most teams
+  int teams;            // rows of a tile, each for a team of consumer warps
   int producers;        // threads, each in a warp of its own, that issue a stage's copies
   int team_threads;     // multiple of 32
   uint32_t gate_span;   // tiles end where a gate row's rows end; 0: they need not
@@ -105,14 +101,14 @@ cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const B
                                    const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
                                    int vec_per_row, const FusedShape& sh, const WaitHook& hook, cudaStream_t s);
 // Backward, many rows (branch_backward_tma.cu); false when a row is too long.
-bool branch_backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
+bool branch_backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, TeamShape* out);
 // Whether this call's slices and sums fit beside one another.
 bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
-                              const BranchTeams& sh);
-cudaError_t branch_backward_tma_prepare(int dtype, const BranchTeams& sh);
+                              const TeamShape& sh);
+cudaError_t branch_backward_tma_prepare(int dtype, const TeamShape& sh);
 cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                        const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
-                                       int vec_per_row, const BranchTeams& sh, cudaStream_t s);
+                                       int vec_per_row, const TeamShape& sh, cudaStream_t s);
 // The sum of the groups' partials, behind either backward kernel.
 cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, int dtype, int groups, int64_t rows,
                                int64_t cols, cudaStream_t s);

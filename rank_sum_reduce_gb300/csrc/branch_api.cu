@@ -97,8 +97,8 @@ bool one_vector(int, int vpt) { return vpt == 1; }
 int branch_threads(int, int) { return kBranchThreads; }
 
 // When the pipeline is faster than the row kernel.
-bool branch_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
-bool branch_backward_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
+bool branch_pipeline_pays(const car_ctx* h, const TeamShape&) { return h->M > h->num_sms; }
+bool branch_backward_pipeline_pays(const car_ctx* h, const TeamShape&) { return h->M > h->num_sms; }
 
 car_status prepare_branch(car_ctx* h) {
   if (h->branch_ready.load(std::memory_order_acquire)) return CAR_OK;
@@ -111,7 +111,7 @@ car_status prepare_branch(car_ctx* h) {
   cudaError_t e = branch_resident_groups(h->dtype, h->W, h->branch, h->num_sms, &groups);
   if (e != cudaSuccess) return cuda_fail(e, "branch occupancy");
   h->branch.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
-  h->branch_pipeline = branch_tma_shape(h->M, h->vec_per_row, h->num_sms, h->W, &h->branch_tma) && branch_pipeline_pays(h, h->branch_tma);
+  h->branch_pipeline = branch_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_tma) && branch_pipeline_pays(h, h->branch_tma);
   if (h->branch_pipeline && (e = branch_tma_prepare(h->dtype, h->branch_tma)) != cudaSuccess)
     return cuda_fail(e, "branch pipeline smem");
   h->branch_ready.store(true, std::memory_order_release);

@@ -6,7 +6,7 @@
 // row's end.
 //
 // Two vectors per thread: the weight and the factor norm_weight * gate (a gate of
-// all rows) lie in shared memory, in fp32.  Longer rows read the weights from
+// many rows) lie in shared memory, in fp32.  Longer rows read the weights from
 // there packed, or from L2, and every gate row from L2.
 //
 // Column sums.  A thread sums g u and t (or gate t, where no gate row is shared)
@@ -45,7 +45,7 @@ struct BranchBackwardTmaParams {
   int gate_from;
   uint32_t gate_span;        // rows that share a gate row
   bool shared;               // t is summed by gate row
-  bool factor;               // dz is multiplied by a factor row: norm_weight, a gate of all rows or both
+  bool factor;               // dz is multiplied by a factor row: norm_weight, a gate of many rows or both
   int weight_rows;           // rows of weights in shared memory, in fp32 or packed
   int a_at, d_at, g_at;      // the stored sum, dres and gate behind h in their stage, in bytes
   RingPlan ring;
@@ -77,7 +77,7 @@ __device__ __forceinline__ void weight_at(const BranchBackwardTmaParams& p, cons
 
 template <int DT, int VPT, bool NORM, int GATE, int DROP>
 __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const uint8_t* ring, const uint8_t* s_rows,
-                                        float4* s_comb, float4* s_dw1, RingShared& s) {
+                                        uint8_t* s_factor, float4* s_comb, float4* s_dw1, RingShared& s) {
   constexpr int E = Pack<DT>::kN;
   constexpr bool SHARED = GATE == kGateShared || GATE == kGateAny, OWN = GATE == kGateOwn || GATE == kGateAny;
   constexpr bool BRANCHES = VPT * E > 16 || (SHARED && E == 8);
@@ -327,6 +327,13 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       flush((uint32_t)tile / p.gate_span, from, t.row);
       from = t.row;
     }
+    // the next gate row's factor, once every team is through with this one's
+    if (SHARED && rp.gate_span && p.gate_from == kFromFactor && t.row == cut && t.more()) {
+      consumers_barrier(rp);
+      row_to_shared<DT>(NORM ? p.norm_weight : nullptr, p.gate + (int64_t)((uint32_t)t.row / p.gate_span) * V, V,
+                        rp.teams * T, s_factor);
+      consumers_barrier(rp);
+    }
   }
   const int64_t plane = (int64_t)blockIdx.x * V * (E / 4);
   if (p.part_w) combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane + i] = a; });
@@ -371,8 +378,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     if constexpr (kWideRows<VPT>) {
       row_to_shared<DT>(p.weight, nullptr, V, consumers, s_rows);
       if (NORM || p.factor)
-        row_to_shared<DT>(NORM ? p.norm_weight : nullptr, p.gate_from == kFromFactor ? p.gate : nullptr, V, consumers,
-                          s_rows + (size_t)V * E * 4);
+        row_to_shared<DT>(NORM ? p.norm_weight : nullptr,
+                          p.gate && p.gate_from == kFromFactor ? p.gate + (int64_t)((uint32_t)first.row / p.gate_span) * V : nullptr,
+                          V, consumers, s_rows + (size_t)V * E * 4);
     } else if (p.weight_rows) {
       for (int v = threadIdx.x; v < V; v += consumers) {
         reinterpret_cast<uint4*>(s_rows)[v] = __ldg(p.weight + v);
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     if (p.shared)
       for (int i = threadIdx.x; i < V * (E / 4); i += consumers) s_dw1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     consumers_barrier(rp);
-    consume<DT, VPT, NORM, GATE, DROP>(p, smem, s_rows, s_comb, s_dw1, s);
+    consume<DT, VPT, NORM, GATE, DROP>(p, smem, s_rows, s_rows + (size_t)V * E * 4, s_comb, s_dw1, s);
   }
 }
 
@@ -427,12 +435,16 @@ constexpr int kSharedBudget = 222 * 1024;  // ring and what lies beside it; Ring
 
 // Where a call's weights and slices lie; the bytes beside the ring: the weights, the
 // sum of dnorm_weight behind a shared gate, the teams' sums.
-bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row, const BranchTeams& sh,
+bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row, const TeamShape& sh,
          BranchBackwardTmaParams* p, int* beside) {
   const bool norm = br.norm_weight != nullptr, wide = sh.vpt == 2, own = br.gate && br.gate_span == 0;
-  const bool column = br.gate && br.gate_span == rows;
-  p->gate_from = !br.gate ? kFromFactor : own ? kFromRing : wide && column ? kFromFactor : kFromRows;
-  p->factor = norm || (wide && column);
+  // A shared gate row is part of the factor where its rows are worth the two barriers
+  // and the L2 latency of making the next one's: W = 1, M = 16384, N = 4096 bf16 with
+  // norms, 1024 rows a gate row, 145 us against 151 with the gate read from L2 for
+  // every row; M = 13332, N = 1160 fp16, 1111 rows, 40.6 against 42.3.
+  const bool folded = wide && br.gate && !own && (br.gate_span == rows || br.gate_span * vec_per_row >= 8192);
+  p->gate_from = !br.gate || folded ? kFromFactor : own ? kFromRing : kFromRows;
+  p->factor = norm || folded;
   p->shared = br.gate && !own && (g.dgate || g.dnorm_weight);
   RingPlan& rp = p->ring;
   rp.rows = (int)rows;
@@ -440,9 +452,8 @@ bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_
   rp.vec_per_row = vec_per_row;
   rp.ranks = W;
   rp.teams = sh.teams;
-  rp.tile_rows = sh.tile_rows;
   rp.team_threads = sh.team_threads;
-  rp.gate_span = p->shared ? (uint32_t)br.gate_span : 0;
+  rp.gate_span = p->shared || (folded && br.gate_span < rows) ? (uint32_t)br.gate_span : 0;
   const int slice = sh.teams * rp.row_bytes, floats = dtype == kFP32 ? rp.row_bytes : 2 * rp.row_bytes;
   rp.held = 1;
   p->a_at = p->d_at = p->g_at = 0;
@@ -461,27 +472,27 @@ bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_
 
 }  // namespace
 
-bool branch_backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, BranchTeams* out) {
+bool branch_backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, TeamShape* out) {
   const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512 : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
   if (vpt > (dtype == kFP32 ? 6 : 4)) return false;
   out->vpt = vpt;
   out->use = team_use(vec_per_row, vpt);
   out->team_threads = team_threads(vec_per_row, vpt);
   if (out->team_threads > 512) return false;
-  out->teams = 512 / out->team_threads;
-  out->tile_rows = (int)std::min<int64_t>(out->teams, (rows + num_sms - 1) / num_sms);  // few rows: spread over the SMs
-  out->grid = (int)std::min<int64_t>((rows + out->tile_rows - 1) / out->tile_rows, num_sms);
+  // as many as a CTA has rows, so that few rows are spread over the SMs
+  out->teams = (int)std::min<int64_t>(512 / out->team_threads, (rows + num_sms - 1) / num_sms);
+  out->grid = (int)std::min<int64_t>((rows + out->teams - 1) / out->teams, num_sms);
   return true;
 }
 
 bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
-                              const BranchTeams& sh) {
+                              const TeamShape& sh) {
   BranchBackwardTmaParams p;
   int beside;
   return fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside);
 }
 
-cudaError_t branch_backward_tma_prepare(int dtype, const BranchTeams& sh) {
+cudaError_t branch_backward_tma_prepare(int dtype, const TeamShape& sh) {
   for (int parts = 0; parts < 12; parts++) {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt, parts & 1, parts >> 2, parts & 2)),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBudget);
@@ -492,7 +503,7 @@ cudaError_t branch_backward_tma_prepare(int dtype, const BranchTeams& sh) {
 
 cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                        const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
-                                       int vec_per_row, const BranchTeams& sh, cudaStream_t s) {
+                                       int vec_per_row, const TeamShape& sh, cudaStream_t s) {
   BranchBackwardTmaParams p;
   int beside;
   if (!fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside)) return cudaErrorInvalidValue;

@@ -58,13 +58,13 @@ struct Tiles {
       cut = (int)(((uint32_t)row / p.gate_span + 1) * p.gate_span);
       step = 0;
     } else {
-      row = blockIdx.x * p.tile_rows;
+      row = blockIdx.x * p.teams;
       end = cut = p.rows;
-      step = gridDim.x * p.tile_rows;
+      step = gridDim.x * p.teams;
     }
   }
   __device__ __forceinline__ bool more() const { return row < end; }
-  __device__ __forceinline__ int count(const RingPlan& p) const { return min(min(end, cut) - row, p.tile_rows); }
+  __device__ __forceinline__ int count(const RingPlan& p) const { return min(min(end, cut) - row, p.teams); }
   __device__ __forceinline__ void next(const RingPlan& p) {
     if (step) {
       row += step;
@@ -78,12 +78,12 @@ struct Tiles {
 // Barriers and small arrays (static shared memory).
 struct RingShared {
   uint64_t full[kMaxRingStages], empty[kMaxRingStages];
-  float4 warp[48];          // [teams][2][3][warps of a team, in fours]: a team has 512 / teams threads at most
+  float4 warp[64];          // [teams][2][4][warps of a team, in fours]: a team has 512 / teams threads at most
   int abort;
 };
 
 __device__ __forceinline__ void ring_init(const RingPlan& p, RingShared& s) {  // all threads, before a barrier
-  if (threadIdx.x < 48) s.warp[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (threadIdx.x < 64) s.warp[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; i++) {
       mbar_init(&s.full[i], p.producers);
@@ -268,10 +268,11 @@ __device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int 
     if constexpr (NS == 2) {
       t += __shfl_xor_sync(ALL, t, 8);
     } else {
-      const float c = v[NS - 1] + __shfl_xor_sync(ALL, v[NS - 1], 16);
+      const float c = NS == 3 ? v[NS - 1] + __shfl_xor_sync(ALL, v[NS - 1], 16)
+                              : (upper ? v[NS - 1] : v[2]) + __shfl_xor_sync(ALL, upper ? v[2] : v[NS - 1], 16);
       const bool third = lane & 8;
       t = (third ? c : t) + __shfl_xor_sync(ALL, third ? t : c, 8);
-      if (third) which = 2;
+      if (third) which = NS == 3 ? 2 : upper ? 3 : 2;
     }
   }
 #pragma unroll
@@ -279,13 +280,14 @@ __device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int 
   if (nwarps == 1) {
     v[0] = __shfl_sync(ALL, t, 0);
     if constexpr (NS >= 2) v[1] = __shfl_sync(ALL, t, 16);
-    if constexpr (NS == 3) v[2] = __shfl_sync(ALL, t, 8);
+    if constexpr (NS >= 3) v[2] = __shfl_sync(ALL, t, 8);
+    if constexpr (NS == 4) v[3] = __shfl_sync(ALL, t, 24);
     return;
   }
   const int fours = (nwarps + 3) >> 2;
-  float4* w = s.warp + (team * 2 + (x & 1u)) * 3 * fours;
-  // lanes 0, 16 and 8 write the sums 0, 1 and 2
-  if (NS == 1 ? lane == 0 : NS == 2 ? (lane & 15) == 0 : (lane & 7) == 0 && lane < 24)
+  float4* w = s.warp + (team * 2 + (x & 1u)) * 4 * fours;
+  // lanes 0, 16, 8 and 24 write the sums 0 to 3
+  if (NS == 1 ? lane == 0 : NS == 2 ? (lane & 15) == 0 : NS == 3 ? (lane & 7) == 0 && lane < 24 : (lane & 7) == 0)
     reinterpret_cast<float*>(w)[which * 4 * fours + warp] = t;
   team_barrier(p, team);
 #pragma unroll

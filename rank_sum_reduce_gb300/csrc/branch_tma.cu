@@ -66,6 +66,25 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
   }
   RingReader in(rp, s, p.err);
   uint32_t x = 0;
+  // DEFER: the second sum of the team's last row travels with the first one of the row
+  // after it, so a row passes one barrier instead of two, and its norm_out is stored
+  // then; where registers hold two rows.
+  constexpr bool DEFER = NORM && VPT * E <= 24;
+  float2 last[DEFER ? VPT : 1][E / 2];
+  float last_ss = 0.f;
+  int64_t last_base = -1;
+  auto finish = [&](const float2(&h)[VPT][E / 2], int64_t base, float sum) {
+    const float2 r = both(rsqrtf(fmaf(sum, p.inv_cols, p.eps)));
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+      if (BRANCHES && !ok[k]) continue;
+      float2 f[E / 2];
+      widen2<DT>(weight_at(p, s_rows, 0, col[k]), f);
+#pragma unroll
+      for (int e = 0; e < E / 2; e++) f[e] = mul2(mul2(h[k][e], r), f[e]);
+      if (ok[k]) st16(p.norm_out + base + col[k], narrow2<DT>(f));
+    }
+  };
   for (Tiles t(rp); t.more(); t.next(rp)) {
     if (team >= t.count(rp)) {
       in.skip();
@@ -81,6 +100,14 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
 #pragma unroll
       for (int k = 0; k < VPT; k++) gv[EARLY ? k : 0] = __ldg(grow + col[k]);
     }
+    // the mask's bits, before the row's waits where registers allow: a chain of ten
+    // dependent products that would stand between its two exchanges
+    constexpr bool BITS_FIRST = DROP != kDropNone && VPT * E <= 16;
+    uint32_t bits[BITS_FIRST ? VPT : 1][E / 2];
+    if (BITS_FIRST && (DROP == kDropYes || p.drop.active)) {
+#pragma unroll
+      for (int k = 0; k < VPT; k++) drop_bits_here<E>(state, base + col[k], bits[BITS_FIRST ? k : 0]);
+    }
     float2 z[VPT][E / 2];
     const uint8_t* held = ring_rank_sum<DT, VPT, BRANCHES>(rp, in, mine, ok, at, z);
     if (in.failed) {
@@ -94,7 +121,8 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
     }
     float2 inv = both(1.f);
     if constexpr (NORM) {
-      float v[1] = {0.f};
+      float v[DEFER ? 2 : 1] = {0.f};
+      if constexpr (DEFER) v[DEFER ? 1 : 0] = last_ss;
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
         if (BRANCHES && !ok[k]) continue;
@@ -105,8 +133,11 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
       }
       team_sums(rp, s, team, x++, v);
       inv = both(rsqrtf(fmaf(v[0], p.inv_cols, p.norm_eps)));
+      if constexpr (DEFER) {
+        if (last_base >= 0) finish(last, last_base, v[DEFER ? 1 : 0]);
+      }
     }
-    float v[1] = {0.f};
+    float hh = 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       if (BRANCHES && !ok[k]) continue;
@@ -122,10 +153,9 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
         for (int e = 0; e < E / 2; e++) z[k][e] = mul2(z[k][e], f[e]);
       }
       if (DROP == kDropYes || (DROP == kDropAny && p.drop.active)) {
-        uint32_t bits[E / 2];
-        drop_bits<E>(state, base + col[k], bits);
+        if constexpr (!BITS_FIRST) drop_bits<E>(state, base + col[k], bits[0]);
 #pragma unroll
-        for (int e = 0; e < E / 2; e++) z[k][e] = drop2(p.drop, bits[e], z[k][e]);
+        for (int e = 0; e < E / 2; e++) z[k][e] = drop2(p.drop, bits[BITS_FIRST ? k : 0][e], z[k][e]);
       }
       widen2<DT>(lds16(held + at[k]), f);
       float2 ss = make_float2(0.f, 0.f);
@@ -134,20 +164,29 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const uint8_t*
         z[k][e] = fma2(both(p.residual_scale), f[e], z[k][e]);
         ss = fma2(z[k][e], z[k][e], ss);
       }
-      v[0] += ok[k] ? ss.x + ss.y : 0.f;
+      hh += ok[k] ? ss.x + ss.y : 0.f;
       if (ok[k]) st16(p.residual_out + base + col[k], narrow2<DT>(z[k]));
     }
     in.release();
-    team_sums(rp, s, team, x++, v);
-    const float2 r = both(rsqrtf(fmaf(v[0], p.inv_cols, p.eps)));
+    if constexpr (DEFER) {
 #pragma unroll
-    for (int k = 0; k < VPT; k++) {
-      if (BRANCHES && !ok[k]) continue;
-      float2 f[E / 2];
-      widen2<DT>(weight_at(p, s_rows, 0, col[k]), f);
+      for (int k = 0; k < VPT; k++) {
 #pragma unroll
-      for (int e = 0; e < E / 2; e++) f[e] = mul2(mul2(z[k][e], r), f[e]);
-      if (ok[k]) st16(p.norm_out + base + col[k], narrow2<DT>(f));
+        for (int e = 0; e < E / 2; e++) last[k][e] = z[k][e];
+      }
+      last_base = base;
+      last_ss = hh;
+    } else {
+      float v[1] = {hh};
+      team_sums(rp, s, team, x++, v);
+      finish(z, base, v[0]);
+    }
+  }
+  if constexpr (DEFER) {
+    if (last_base >= 0) {
+      float v[1] = {last_ss};
+      team_sums(rp, s, team, x++, v);
+      finish(last, last_base, v[0]);
     }
   }
 }
@@ -191,7 +230,7 @@ using BranchTmaFn = void (*)(const BranchTmaParams);
 
 template <int DT, int VPT, bool NORM>
 BranchTmaFn pick_parts(int gate, bool drop) {
-  if constexpr (VPT == 2 || VPT == 4) {
+  if constexpr (VPT == 2) {
     if (gate == kGateNone)
       return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateNone, kDropYes>
                   : reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, NORM, kGateNone, kDropNone>;
@@ -228,7 +267,7 @@ BranchTmaFn pick(int dtype, int vpt, bool norm, int gate, bool drop) {
 constexpr int kSharedBudget = 222 * 1024;  // ring and rows of weights; RingShared is static
 
 // Where a call's weights lie, and its ring; the bytes beside the ring.
-bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh, BranchTmaParams* p, int* beside) {
+bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const TeamShape& sh, BranchTmaParams* p, int* beside) {
   const bool column = br.gate && br.gate_span == rows;
   p->gate_from = !br.gate || column ? kFromFactor : br.gate_span == 0 ? kFromRing : kFromRows;
   RingPlan& rp = p->ring;
@@ -238,7 +277,6 @@ bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const Branc
   rp.ranks = W;
   rp.held = 1 + (p->gate_from == kFromRing ? 1 : 0);
   rp.teams = sh.teams;
-  rp.tile_rows = sh.tile_rows;
   rp.team_threads = sh.team_threads;
   rp.gate_span = 0;
   *beside = (column ? 3 : br.norm_weight ? 2 : 1) * rp.row_bytes;
@@ -250,13 +288,19 @@ bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const Branc
 
 }  // namespace
 
+// A whole tile per stage where two fit, three stages or 96 KB at most: deeper rings
+// ask for more of HBM at once than helps (W = 1, M = 16389, N = 4096 bf16 without a
+// norm 83 to 85 us with 64 to 96 KB in flight per SM, 94 with 192).  Else stages of
+// two slices, as many as there is room for (W = 8, M = 512, N = 8192 with both norms
+// 20.9, 19.6 and 18.3 us with three, four and five of them; stages of one slice 20.5
+// with eight, of four 20.4 with three).
 bool branch_ring_fit(int budget, RingPlan* p) {
   const int slices = p->ranks + p->held, places = budget / (p->teams * p->row_bytes);
   if (2 * slices <= places) {
     p->group = slices;
     p->tile_stages = 1;
   } else {
-    p->group = std::max(p->held, std::min(4, places / 3));
+    p->group = std::max(p->held, 2);
     p->tile_stages = (p->ranks + p->group - 1) / p->group + 1;
   }
   p->stages = std::min(places / p->group, kMaxRingStages);
@@ -265,34 +309,32 @@ bool branch_ring_fit(int budget, RingPlan* p) {
   return p->stages >= 2;
 }
 
-// Vectors per thread: four, or as many of two to eight as leave clearly fewer of
-// the threads' places empty; the fewer warps a row has, the less of its time goes
-// into the exchanges (W = 1, M = 16389, N = 4096 bf16 with both norms and dropout:
-// two 121 us, four 97).  With four ranks and more two, three where that fits better
-// (W = 4, M = 4096, N = 2048 19.3 us, with four 20.4).  Rows of more than 2048
-// vectors take as many as 512 threads need.
-bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, int W, BranchTeams* out) {
-  const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512
-                  : W <= 3           ? team_vectors(vec_per_row, 4, 8)
-                                     : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
+// Two vectors per thread for rows of up to 1024 vectors, three where that fits
+// clearly better or for longer ones, four only for rows that three do not hold,
+// above 2048 as few as 512 threads need (see norm_backward_tma.cu).  Four vectors in
+// shorter rows halve the warps that a row's exchanges pass through, and lose to the
+// overlap of more of them: W = 1, M = 16389, N = 4096 bf16 with both norms 82.5 us
+// with two, 92.4 with four; W = 2, M = 4000, N = 8192 50.5 and 63.
+bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, TeamShape* out) {
+  const int vpt = vec_per_row > 2048 ? (vec_per_row + 511) / 512 : team_vectors(vec_per_row, 2, vec_per_row > 1536 ? 4 : 3);
   if (vpt > 8) return false;
   out->vpt = vpt;
   out->use = team_use(vec_per_row, vpt);
   out->team_threads = team_threads(vec_per_row, vpt);
   if (out->team_threads > 512) return false;
-  out->teams = 512 / out->team_threads;
-  out->tile_rows = (int)std::min<int64_t>(out->teams, (rows + num_sms - 1) / num_sms);  // few rows: spread over the SMs
-  out->grid = (int)std::min<int64_t>((rows + out->tile_rows - 1) / out->tile_rows, num_sms);
+  // as many as a CTA has rows, so that few rows are spread over the SMs
+  out->teams = (int)std::min<int64_t>(512 / out->team_threads, (rows + num_sms - 1) / num_sms);
+  out->grid = (int)std::min<int64_t>((rows + out->teams - 1) / out->teams, num_sms);
   return true;
 }
 
-bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh) {
+bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const TeamShape& sh) {
   BranchTmaParams p;
   int beside;
   return fit(W, br, rows, vec_per_row, sh, &p, &beside);
 }
 
-cudaError_t branch_tma_prepare(int dtype, const BranchTeams& sh) {
+cudaError_t branch_tma_prepare(int dtype, const TeamShape& sh) {
   for (int parts = 0; parts < 12; parts++) {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(pick(dtype, sh.vpt, parts & 1, parts >> 2, parts & 2)),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBudget);
@@ -303,7 +345,7 @@ cudaError_t branch_tma_prepare(int dtype, const BranchTeams& sh) {
 
 cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const BranchArgs& br, const void* residual,
                               const void* weight, float eps, void* residual_out, void* norm_out, void* ar_out,
-                              unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const BranchTeams& sh,
+                              unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const TeamShape& sh,
                               cudaStream_t s) {
   BranchTmaParams p;
   int beside;
