@@ -124,34 +124,32 @@ __device__ __forceinline__ void row_sums_init(RowSums& s, int cluster) {  // one
   }
 }
 
-// v becomes the sums over the row; NaN for a thread whose wait for its peers
-// runs out (it then waits until their partials have landed, bounded again, so
-// that none reaches a CTA that has exited and the phases stay in step).
+// A CTA's wait for its peers' partials; err's bits are car_sync's.
+struct ClusterWait {
+  int crank;
+  uint64_t wait_ns;
+  unsigned int* err;
+};
+
+// v, the CTA's sums in every thread, becomes the cluster's; NaN for a thread whose
+// wait for its peers runs out (it then waits until their partials have landed,
+// bounded again, so that none reaches a CTA that has exited and the phases stay in
+// step).
 template <int NS>
-__device__ __forceinline__ void row_sums(RowSums& s, float (&v)[NS], uint32_t x, int cluster, int crank, uint64_t wait_ns,
-                                         unsigned int* err) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+__device__ __forceinline__ void cluster_sums(RowSums& s, float (&v)[NS], uint32_t x, int cluster, const ClusterWait& peers) {
+  const int lane = threadIdx.x & 31;
   const uint32_t b = x & 1u, par = (x >> 1) & 1u;
-#pragma unroll
-  for (int i = 0; i < NS; i++) {
-    v[i] = warp_total(v[i]);
-    if (lane == 0) s.warp[b][i][warp] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NS; i++) v[i] = warp_total(lane < nwarps ? s.warp[b][i][lane] : 0.f);
-  if (cluster == 1) return;
-  if (warp == 0) {
+  if (threadIdx.x < 32) {
     constexpr uint32_t bytes = NS == 1 ? 4u : NS == 2 ? 8u : 16u;
     if (lane == 0) mbar_arrive_expect_tx(&s.bar[b], bytes * (uint32_t)cluster);
     if (lane < cluster) {
-      const uint32_t to = map_rank(&s.part[b][crank], (uint32_t)lane), bar = map_rank(&s.bar[b], (uint32_t)lane);
+      const uint32_t to = map_rank(&s.part[b][peers.crank], (uint32_t)lane), bar = map_rank(&s.bar[b], (uint32_t)lane);
       if constexpr (NS == 1) st_async_f32(to, v[0], bar);
       if constexpr (NS > 1) st_async_v2_b32(to, __float_as_uint(v[0]), __float_as_uint(v[1]), bar);
       if constexpr (NS > 2) st_async_v2_b32(to + 8u, __float_as_uint(v[2]), 0u, bar);
     }
   }
-  if (wait_cluster_phase(&s.bar[b], par, wait_ns)) {
+  if (wait_cluster_phase(&s.bar[b], par, peers.wait_ns)) {
 #pragma unroll
     for (int i = 0; i < NS; i++) v[i] = reinterpret_cast<const float*>(&s.part[b][0])[i];
     for (int r = 1; r < cluster; r++) {
@@ -159,11 +157,26 @@ __device__ __forceinline__ void row_sums(RowSums& s, float (&v)[NS], uint32_t x,
       for (int i = 0; i < NS; i++) v[i] += reinterpret_cast<const float*>(&s.part[b][r])[i];
     }
   } else {
-    atomicOr(err, 1u);
+    atomicOr(peers.err, 1u);
 #pragma unroll
     for (int i = 0; i < NS; i++) v[i] = __int_as_float(0x7fc00000);
-    if (!wait_cluster_phase(&s.bar[b], par)) atomicOr(err, 2u);
+    if (!wait_cluster_phase(&s.bar[b], par)) atomicOr(peers.err, 2u);
   }
+}
+
+// v becomes the sums over the row, in the row kernels.
+template <int NS>
+__device__ __forceinline__ void row_sums(RowSums& s, float (&v)[NS], uint32_t x, int cluster, const ClusterWait& peers) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+#pragma unroll
+  for (int i = 0; i < NS; i++) {
+    v[i] = warp_total(v[i]);
+    if (lane == 0) s.warp[x & 1u][i][warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NS; i++) v[i] = warp_total(lane < nwarps ? s.warp[x & 1u][i][lane] : 0.f);
+  if (cluster > 1) cluster_sums(s, v, x, cluster, peers);
 }
 
 }  // namespace

@@ -54,21 +54,27 @@ cudaError_t launch_branch(int dtype, int W, const RankPtrs& in, const BranchArgs
                           unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const FusedShape& sh,
                           const WaitHook& hook, cudaStream_t s);
 
-// ---- forward, many rows (branch_tma.cu); false when a row is too long ----
-bool branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, TeamShape* out);
+struct BranchTeams : TeamShape {  // teams: rows of a tile; grid: CTAs
+  int cluster;                    // CTAs that share a row, then with one team each
+};
+// ---- forward, many rows (branch_tma.cu) ----
+void branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
 // Whether this call's slices and weights fit beside one another.
-bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const TeamShape& sh);
-cudaError_t branch_tma_prepare(int dtype, const TeamShape& sh);
+bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh);
+// Allows the instances their shared memory, and fits the grid to the clusters that can be resident.
+cudaError_t branch_tma_prepare(int dtype, BranchTeams* sh);
 cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const BranchArgs& br, const void* residual,
                               const void* weight, float eps, void* residual_out, void* norm_out, void* ar_out,
-                              unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const TeamShape& sh,
-                              cudaStream_t s);
+                              unsigned int* err, int64_t rows, int64_t cols, int vec_per_row, const BranchTeams& sh,
+                              const WaitHook& hook, cudaStream_t s);
 // The ring of either pipeline (branch_ring.cuh).
 constexpr int kMaxRingStages = 32;
 struct RingPlan {
   int rows;
   int row_bytes;
   int vec_per_row;
+  int cluster;          // CTAs that share a row
+  int chunk;            // vectors of a row for each of them (the last one's may be fewer)
   int ranks;            // slices of a tile that are summed
   int held;             // slices that a row needs to its end
   int group;            // slices that a stage has room for
@@ -82,6 +88,10 @@ struct RingPlan {
 // Chooses group, tile_stages and stages for `budget` bytes; false when the ring
 // would be too small.
 bool branch_ring_fit(int budget, RingPlan* p);
+// Teams and grid for `cluster` CTAs a row and `vpt` vectors per thread.
+void branch_teams(int64_t rows, int vec_per_row, int num_sms, int cluster, int vpt, BranchTeams* out);
+// The clusters of `fn` that can be resident, at most *clusters.
+cudaError_t branch_clusters(const void* fn, int cluster, int smem, int* clusters);
 
 // ---- backward (branch_backward.cu) ----
 // CTAs (or clusters) take contiguous spans of rows: the g-th of n starts here.
@@ -100,15 +110,15 @@ cudaError_t branch_backward_resident_groups(int dtype, int W, const FusedShape& 
 cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                    const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
                                    int vec_per_row, const FusedShape& sh, const WaitHook& hook, cudaStream_t s);
-// Backward, many rows (branch_backward_tma.cu); false when a row is too long.
-bool branch_backward_tma_shape(int dtype, int64_t rows, int vec_per_row, int num_sms, TeamShape* out);
+// Backward, many rows (branch_backward_tma.cu).
+void branch_backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
 // Whether this call's slices and sums fit beside one another.
 bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
-                              const TeamShape& sh);
-cudaError_t branch_backward_tma_prepare(int dtype, const TeamShape& sh);
+                              const BranchTeams& sh);
+cudaError_t branch_backward_tma_prepare(int dtype, BranchTeams* sh);
 cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                        const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
-                                       int vec_per_row, const TeamShape& sh, cudaStream_t s);
+                                       int vec_per_row, const BranchTeams& sh, const WaitHook& hook, cudaStream_t s);
 // The sum of the groups' partials, behind either backward kernel.
 cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, int dtype, int groups, int64_t rows,
                                int64_t cols, cudaStream_t s);

@@ -97,8 +97,8 @@ bool one_vector(int, int vpt) { return vpt == 1; }
 int branch_threads(int, int) { return kBranchThreads; }
 
 // When the pipeline is faster than the row kernel.
-bool branch_pipeline_pays(const car_ctx* h, const TeamShape&) { return h->M > h->num_sms; }
-bool branch_backward_pipeline_pays(const car_ctx* h, const TeamShape&) { return h->M > h->num_sms; }
+bool branch_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
+bool branch_backward_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
 
 car_status prepare_branch(car_ctx* h) {
   if (h->branch_ready.load(std::memory_order_acquire)) return CAR_OK;
@@ -111,8 +111,9 @@ car_status prepare_branch(car_ctx* h) {
   cudaError_t e = branch_resident_groups(h->dtype, h->W, h->branch, h->num_sms, &groups);
   if (e != cudaSuccess) return cuda_fail(e, "branch occupancy");
   h->branch.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
-  h->branch_pipeline = branch_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_tma) && branch_pipeline_pays(h, h->branch_tma);
-  if (h->branch_pipeline && (e = branch_tma_prepare(h->dtype, h->branch_tma)) != cudaSuccess)
+  branch_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_tma);
+  h->branch_pipeline = branch_pipeline_pays(h, h->branch_tma);
+  if (h->branch_pipeline && (e = branch_tma_prepare(h->dtype, &h->branch_tma)) != cudaSuccess)
     return cuda_fail(e, "branch pipeline smem");
   h->branch_ready.store(true, std::memory_order_release);
   return CAR_OK;
@@ -129,10 +130,9 @@ car_status prepare_branch_backward(car_ctx* h) {
   cudaError_t e = branch_backward_resident_groups(h->dtype, h->W, h->branch_backward, h->num_sms, &groups);
   if (e != cudaSuccess) return cuda_fail(e, "branch backward occupancy");
   h->branch_backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
-  h->branch_backward_pipeline =
-      branch_backward_tma_shape(h->dtype, h->M, h->vec_per_row, h->num_sms, &h->branch_backward_tma) &&
-      branch_backward_pipeline_pays(h, h->branch_backward_tma);
-  if (h->branch_backward_pipeline && (e = branch_backward_tma_prepare(h->dtype, h->branch_backward_tma)) != cudaSuccess)
+  branch_backward_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_backward_tma);
+  h->branch_backward_pipeline = branch_backward_pipeline_pays(h, h->branch_backward_tma);
+  if (h->branch_backward_pipeline && (e = branch_backward_tma_prepare(h->dtype, &h->branch_backward_tma)) != cudaSuccess)
     return cuda_fail(e, "branch backward pipeline smem");
   h->branch_backward_ready.store(true, std::memory_order_release);
   return CAR_OK;
@@ -141,7 +141,7 @@ car_status prepare_branch_backward(car_ctx* h) {
 // CTAs (or clusters) of whichever kernel a call runs: which one is, where the
 // pipeline pays, found at the call (its parts decide whether a row fits).
 int workspace_groups(const car_ctx* h) {
-  return std::max(h->branch_backward.groups, h->branch_backward_pipeline ? h->branch_backward_tma.grid : 0);
+  return std::max(h->branch_backward.groups, h->branch_backward_pipeline ? h->branch_backward_tma.grid / h->branch_backward_tma.cluster : 0);
 }
 
 }  // namespace
@@ -196,7 +196,7 @@ car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inp
   cudaError_t e;
   if (h->branch_pipeline && branch_tma_fits(h->W, b, h->M, h->vec_per_row, h->branch_tma))
     e = launch_branch_tma(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M, h->N,
-                          h->vec_per_row, h->branch_tma, s);
+                          h->vec_per_row, h->branch_tma, h->hook, s);
   else
     e = launch_branch(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M, h->N,
                       h->vec_per_row, h->branch, h->hook, s);
@@ -268,7 +268,7 @@ car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* c
   cudaError_t e;
   if (h->branch_backward_pipeline && branch_backward_tma_fits(h->dtype, h->W, b, g, h->M, h->vec_per_row, h->branch_backward_tma))
     e = launch_branch_backward_tma(h->dtype, h->W, tbl, b, g, weight, eps, h->d_err, h->M, h->N, h->vec_per_row,
-                                   h->branch_backward_tma, s);
+                                   h->branch_backward_tma, h->hook, s);
   else
     e = launch_branch_backward(h->dtype, h->W, tbl, b, g, weight, eps, h->d_err, h->M, h->N, h->vec_per_row,
                                h->branch_backward, h->hook, s);

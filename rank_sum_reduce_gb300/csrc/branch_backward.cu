@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
   const int groups = gridDim.x / C, group = blockIdx.x / C;
   const int64_t first = span_start(p.rows, groups, group), end = span_start(p.rows, groups, group + 1);
   const int col0 = crank * p.chunk;
+  const ClusterWait peers{crank, p.wait_ns, p.err};
   uint32_t x = 0;
   bool peers_ready = C == 1;
   if (C > 1) {
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
     }
     // test hook: this whole CTA reaches the row's first exchange late
     if (C > 1 && crank == p.delay_cta && row == p.delay_row) spin_ns(p.delay_ns);
-    row_sums(s_sums, s, x++, C, crank, p.wait_ns, p.err);
+    row_sums(s_sums, s, x++, C, peers);
     const float r = rsqrtf(__fdiv_rn(s[0], p.cols) + p.eps);
     const float2 m = both(-__fdiv_rn(__fmul_rn(s[1], r), p.cols));
     const float2 q = NORM ? both(rsqrtf(__fdiv_rn(s[NORM ? 2 : 0], p.cols) + p.norm_eps)) : both(1.f);
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
     }
     if constexpr (NORM) {
       float t[1] = {vu.x + vu.y};
-      row_sums(s_sums, t, x++, C, crank, p.wait_ns, p.err);
+      row_sums(s_sums, t, x++, C, peers);
       const float2 mean = both(-__fdiv_rn(t[0], p.cols));
 #pragma unroll
       for (int e = 0; e < E / 2; e++) g[e] = mul2(q, fma2(u1[e], mean, g[e]));

@@ -22,13 +22,11 @@
 namespace car {
 namespace {
 
-// Instances of the pipelines: with two vectors per thread one for each kind of gate,
-// with dropout and without (what a row does not do costs it registers and
-// instructions all the same when it is found out at run time: backward, W = 1, M =
-// 16389, N = 4096 bf16 without a norm 145 us against 103), for longer rows one for
-// neither gate nor dropout and one for any.
-enum GateKind : int { kGateNone = 0, kGateShared = 1, kGateOwn = 2, kGateAny = 3 };
-enum DropKind : int { kDropNone = 0, kDropYes = 1, kDropAny = 2 };
+// The pipelines have an instance for each kind of gate, with dropout and without: what
+// a row does not do costs it registers and instructions all the same when it is found
+// out at run time (backward, W = 1, M = 16389, N = 4096 bf16 without a norm 145 us
+// against 103).
+enum GateKind : int { kGateNone = 0, kGateShared = 1, kGateOwn = 2 };
 // Where a row's gate comes from: the factor row in shared memory (also: no gate),
 // the ring, L2.
 enum GateFrom : int { kFromFactor = 0, kFromRing = 1, kFromRows = 2 };
@@ -48,19 +46,34 @@ __device__ __forceinline__ void take_registers() {  // every thread of a warpgro
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
 }
 
+// The columns of this CTA: all, or with SPLIT its part of every row.
+template <bool SPLIT>
+struct Part {
+  int crank, group, groups;  // place in the cluster; the cluster's, of how many
+  int col0, V;               // first vector of a row, and how many
+  __device__ __forceinline__ explicit Part(const RingPlan& p) {
+    crank = SPLIT ? (int)cluster_rank() : 0;
+    group = SPLIT ? (int)blockIdx.x / p.cluster : (int)blockIdx.x;
+    groups = SPLIT ? (int)gridDim.x / p.cluster : (int)gridDim.x;
+    col0 = SPLIT ? crank * p.chunk : 0;
+    V = SPLIT ? min(p.chunk, p.vec_per_row - col0) : p.vec_per_row;
+  }
+};
+
 // The tiles of this CTA in order.
 struct Tiles {
   int row, end, cut, step;
-  __device__ __forceinline__ explicit Tiles(const RingPlan& p) {
+  template <bool SPLIT>
+  __device__ __forceinline__ Tiles(const RingPlan& p, const Part<SPLIT>& part) {
     if (p.gate_span) {
-      row = (int)span_start(p.rows, gridDim.x, blockIdx.x);
-      end = (int)span_start(p.rows, gridDim.x, blockIdx.x + 1);
+      row = (int)span_start(p.rows, part.groups, part.group);
+      end = (int)span_start(p.rows, part.groups, part.group + 1);
       cut = (int)(((uint32_t)row / p.gate_span + 1) * p.gate_span);
       step = 0;
     } else {
-      row = blockIdx.x * p.teams;
+      row = part.group * p.teams;
       end = cut = p.rows;
-      step = gridDim.x * p.teams;
+      step = part.groups * p.teams;
     }
   }
   __device__ __forceinline__ bool more() const { return row < end; }
@@ -75,21 +88,26 @@ struct Tiles {
   }
 };
 
+// Bytes of a slice's place in a stage.
+__host__ __device__ inline uint32_t slice_stride(const RingPlan& p) { return (uint32_t)p.teams * (uint32_t)p.chunk * 16u; }
+
 // Barriers and small arrays (static shared memory).
 struct RingShared {
   uint64_t full[kMaxRingStages], empty[kMaxRingStages];
-  float4 warp[64];          // [teams][2][4][warps of a team, in fours]: a team has 512 / teams threads at most
+  RowSums cluster;          // its exchange, where CTAs share a row
+  float4 warp[48];          // [teams][2][3][warps of a team, in fours]: a team has 512 / teams threads at most
   int abort;
 };
 
 __device__ __forceinline__ void ring_init(const RingPlan& p, RingShared& s) {  // all threads, before a barrier
-  if (threadIdx.x < 64) s.warp[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (threadIdx.x < 48) s.warp[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; i++) {
       mbar_init(&s.full[i], p.producers);
       mbar_init(&s.empty[i], (uint32_t)(p.teams * p.team_threads) >> 5);
     }
     s.abort = 0;
+    row_sums_init(s.cluster, p.cluster);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 }
@@ -115,17 +133,17 @@ __device__ __forceinline__ bool wait_suspended(uint64_t* bar, uint32_t parity, c
 
 // Producer `who` of p.producers: issues every p.producers-th slice of each stage,
 // then waits for the stages that were filled.  source(q): slice q of row 0.
-template <class Source>
-__device__ __forceinline__ void ring_produce(const RingPlan& p, uint8_t* ring, RingShared& s, int who, unsigned int* err,
-                                             Source source) {
+template <bool SPLIT, class Source>
+__device__ __forceinline__ void ring_produce(const RingPlan& p, const Part<SPLIT>& part, uint8_t* ring, RingShared& s, int who,
+                                             unsigned int* err, Source source) {
   const int S = p.stages, slices = p.ranks + p.held;
-  const uint32_t stride = (uint32_t)p.teams * (uint32_t)p.row_bytes;
+  const uint32_t stride = slice_stride(p);
   int place = 0;
   uint32_t phase = 0, issued = 0;
   bool ok = true;
-  for (Tiles t(p); t.more() && ok; t.next(p)) {
-    const int64_t off = t.row * (int64_t)p.row_bytes;
-    const uint32_t bytes = (uint32_t)t.count(p) * (uint32_t)p.row_bytes;
+  for (Tiles t(p, part); t.more() && ok; t.next(p)) {
+    const int64_t off = t.row * (int64_t)p.row_bytes + part.col0 * 16;
+    const uint32_t bytes = (uint32_t)t.count(p) * (uint32_t)part.V * 16u;
     for (int q = 0; q < slices;) {
       // a stage ends with the ranks unless all of the tile is one
       const int n = slices <= p.group ? slices : q < p.ranks ? min(p.group, p.ranks - q) : slices - q;
@@ -206,7 +224,7 @@ template <int DT, int VPT, bool BRANCHES>
 __device__ __forceinline__ const uint8_t* ring_rank_sum(const RingPlan& p, RingReader& in, const uint8_t* mine,
                                                         const bool (&ok)[VPT], const int (&at)[VPT], float2 (&acc)[VPT][Pack<DT>::kN / 2]) {
   constexpr int E = Pack<DT>::kN;
-  const uint32_t stride = (uint32_t)p.teams * (uint32_t)p.row_bytes;
+  const uint32_t stride = slice_stride(p);
   const bool whole = p.tile_stages == 1;
   int q = 0;
   while (true) {
@@ -251,8 +269,9 @@ __device__ __forceinline__ void consumers_barrier(const RingPlan& p) {
 // Within a warp several sums share their shuffles: after the first step the lower
 // half of the lanes carries one, the upper half another, after the second a quarter
 // each.  Three sums: 6 shuffles, where one after the other would take 15.
-template <int NS>
-__device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int team, uint32_t x, float (&v)[NS]) {
+template <bool SPLIT, int NS>
+__device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int team, uint32_t x, float (&v)[NS],
+                                          const ClusterWait& peers) {
   constexpr uint32_t ALL = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31, nwarps = p.team_threads >> 5, warp = (threadIdx.x - team * p.team_threads) >> 5;
   float t;        // of sum `which`, in the first of every eight lanes
@@ -268,11 +287,10 @@ __device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int 
     if constexpr (NS == 2) {
       t += __shfl_xor_sync(ALL, t, 8);
     } else {
-      const float c = NS == 3 ? v[NS - 1] + __shfl_xor_sync(ALL, v[NS - 1], 16)
-                              : (upper ? v[NS - 1] : v[2]) + __shfl_xor_sync(ALL, upper ? v[2] : v[NS - 1], 16);
+      const float c = v[NS - 1] + __shfl_xor_sync(ALL, v[NS - 1], 16);
       const bool third = lane & 8;
       t = (third ? c : t) + __shfl_xor_sync(ALL, third ? t : c, 8);
-      if (third) which = NS == 3 ? 2 : upper ? 3 : 2;
+      if (third) which = 2;
     }
   }
 #pragma unroll
@@ -280,14 +298,14 @@ __device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int 
   if (nwarps == 1) {
     v[0] = __shfl_sync(ALL, t, 0);
     if constexpr (NS >= 2) v[1] = __shfl_sync(ALL, t, 16);
-    if constexpr (NS >= 3) v[2] = __shfl_sync(ALL, t, 8);
-    if constexpr (NS == 4) v[3] = __shfl_sync(ALL, t, 24);
+    if constexpr (NS == 3) v[2] = __shfl_sync(ALL, t, 8);
+    if constexpr (SPLIT) cluster_sums(s.cluster, v, x, p.cluster, peers);
     return;
   }
   const int fours = (nwarps + 3) >> 2;
-  float4* w = s.warp + (team * 2 + (x & 1u)) * 4 * fours;
-  // lanes 0, 16, 8 and 24 write the sums 0 to 3
-  if (NS == 1 ? lane == 0 : NS == 2 ? (lane & 15) == 0 : NS == 3 ? (lane & 7) == 0 && lane < 24 : (lane & 7) == 0)
+  float4* w = s.warp + (team * 2 + (x & 1u)) * 3 * fours;
+  // lanes 0, 16 and 8 write the sums 0, 1 and 2
+  if (NS == 1 ? lane == 0 : NS == 2 ? (lane & 15) == 0 : (lane & 7) == 0 && lane < 24)
     reinterpret_cast<float*>(w)[which * 4 * fours + warp] = t;
   team_barrier(p, team);
 #pragma unroll
@@ -309,6 +327,7 @@ __device__ __forceinline__ void team_sums(const RingPlan& p, RingShared& s, int 
     }
     v[i] = __fadd_rn(a.x, a.y);
   }
+  if constexpr (SPLIT) cluster_sums(s.cluster, v, x, p.cluster, peers);
 }
 
 // Rows of factors in shared memory, in fp32: every vector of them is used once or

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_residual_rmsnorm
   const int crank = C > 1 ? (int)cluster_rank() : 0;
   const int64_t ngroups = gridDim.x / C;
   const int col0 = crank * p.chunk;
+  const ClusterWait peers{crank, p.wait_ns, p.err};
   uint32_t x = 0;  // exchanges done
   bool peers_ready = C == 1;
   if (C > 1) {
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_residual_rmsnorm
     if (C > 1 && crank == p.delay_cta && row == p.delay_row) spin_ns(p.delay_ns);
     if constexpr (NORM) {
       float s[1] = {ss};
-      row_sums(s_sums, s, x++, C, crank, p.wait_ns, p.err);
+      row_sums(s_sums, s, x++, C, peers);
       const float2 q = both(rsqrtf(__fdiv_rn(s[0], p.cols) + p.norm_eps));
       float2 w[E / 2];
       widen2<DT>(pv, w);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_residual_rmsnorm
       st16(p.residual_out + at, narrow2<DT>(z));
     }
     float s[1] = {ss};
-    row_sums(s_sums, s, x++, C, crank, p.wait_ns, p.err);
+    row_sums(s_sums, s, x++, C, peers);
     if (ok) {
       const float2 r = both(rsqrtf(__fdiv_rn(s[0], p.cols) + p.eps));
       float2 w[E / 2];

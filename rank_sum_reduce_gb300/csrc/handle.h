@@ -45,7 +45,7 @@ struct car_ctx {
   // The branch calls and dropout, the same way (branch_api.cu).
   std::atomic<bool> branch_ready{false}, branch_backward_ready{false}, dropout_ready{false};
   car::FusedShape branch, branch_backward;   // row kernels
-  car::TeamShape branch_tma, branch_backward_tma;
+  car::BranchTeams branch_tma, branch_backward_tma;
   bool branch_pipeline, branch_backward_pipeline;
   int dropout_grid;
   int fused_kernel_auto;  // CAR_FUSED_ROWS or CAR_FUSED_PIPELINE
