@@ -82,11 +82,10 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
                                         uint8_t* s_factor, float4* s_comb, float4* s_dw1, RingShared& s) {
   constexpr int E = Pack<DT>::kN;
   constexpr bool SHARED = GATE == kGateShared;
-  constexpr bool BRANCHES = E == 8 && (SHARED || (NORM && (SPLIT || GATE == kGateOwn)));  // else they spill
+  constexpr bool BRANCHES = E == 8 && ((SHARED && !SPLIT) || (NORM && GATE == kGateOwn));  // else they spill
   const RingPlan& rp = p.ring;
   const bool shared = SHARED && p.shared;
   const int T = rp.team_threads, V = part.V, teams = SPLIT ? 1 : rp.teams;
-  const int64_t row4 = (int64_t)rp.vec_per_row * (E / 4), col4 = part.col0 * (E / 4);  // in fours of fp32
   const ClusterWait peers{part.crank, p.wait_ns, p.err};
   const int team = SPLIT ? 0 : threadIdx.x / T, tid = threadIdx.x - team * T;
   const uint8_t* mine = ring + (size_t)team * rp.row_bytes;  // the row in stage 0
@@ -159,7 +158,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
     float4* out = nullptr;
     if (p.dgate)
       out = reinterpret_cast<float4*>(whole ? p.dgate : p.part_gate) +
-            (whole ? (int64_t)b : 2 * (int64_t)part.group + (from == first ? 0 : 1)) * row4 + col4;
+            (whole ? (int64_t)b : 2 * (int64_t)part.group + (from == first ? 0 : 1)) * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
     combine(ts, [&](int i, float4 t) {
       const float4 g = four(p.gate + (int64_t)b * rp.vec_per_row + part.col0, i);
       float4 d = s_dw1[i];
@@ -185,22 +184,13 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
   RingReader in(rp, s, p.err);
   uint32_t x = 0;
   int from = first;
-  for (Tiles t(rp, part); t.more();) {
+  for (Tiles<SHARED> t(rp, part); t.more(rp);) {
     const int tile = t.row;
     if (team >= t.count(rp)) {
       in.skip();
     } else {
       const int row = tile + team;
       const int64_t base = (int64_t)row * rp.vec_per_row + part.col0;
-      // a shared gate row from L2, asked for before the row's waits where registers allow
-      constexpr bool EARLY = SHARED && VPT * E <= 16;
-      const bool rows = SHARED && p.gate_from == kFromRows;
-      uint4 gv[EARLY ? VPT : 1];
-      const uint4* grow = rows ? p.gate + (int64_t)((uint32_t)row / p.gate_span) * rp.vec_per_row + part.col0 : nullptr;
-      if (EARLY && rows) {
-#pragma unroll
-        for (int k = 0; k < VPT; k++) gv[EARLY ? k : 0] = __ldg(grow + col[k]);
-      }
       float2 g[VPT][E / 2];
       const uint8_t* held = ring_rank_sum<DT, VPT, BRANCHES>(rp, in, mine, ok, at, g);
       if (in.failed) {
@@ -246,13 +236,15 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
           float2 hf[E / 2], f[E / 2], d[E / 2];
           widen2<DT>(lds16(held + at[k]), hf);
           weight_at<DT>(p, part, s_rows, 0, col[k], f);
-          widen2<DT>(p.dres ? lds16(held + p.d_at + at[k]) : make_uint4(0u, 0u, 0u, 0u), d);
 #pragma unroll
           for (int e = 0; e < E / 2; e++) {
             const float2 u = mul2(hf[e], both(r));
             dw[k][e] = fma2(g[k][e], u, dw[k][e]);
-            g[k][e] = fma2(both(r), fma2(u, m, mul2(g[k][e], f[e])), d[e]);  // dh
+            g[k][e] = fma2(u, m, mul2(g[k][e], f[e]));
           }
+          widen2<DT>(p.dres ? lds16(held + p.d_at + at[k]) : make_uint4(0u, 0u, 0u, 0u), d);
+#pragma unroll
+          for (int e = 0; e < E / 2; e++) g[k][e] = fma2(both(r), g[k][e], d[e]);  // dh
           if (p.dresidual) {
 #pragma unroll
             for (int e = 0; e < E / 2; e++) d[e] = mul2(g[k][e], both(p.residual_scale));
@@ -290,8 +282,8 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
 #pragma unroll
             for (int e = 0; e < E / 2; e++) ts[k][e] = fma2(g[k][e], u1[e], ts[k][e]);
           }
-          if (rows) {
-            widen2<DT>(EARLY ? gv[EARLY ? k : 0] : __ldg(grow + col[k]), d);
+          if (SHARED && p.gate_from == kFromRows) {
+            widen2<DT>(__ldg(p.gate + (int64_t)((uint32_t)row / p.gate_span) * rp.vec_per_row + part.col0 + col[k]), d);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], d[e]);
           }
@@ -329,12 +321,12 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
     }
     const int cut = t.cut;
     t.next(rp);
-    if (shared && (t.row == cut || !t.more())) {
+    if (shared && (t.row == cut || !t.more(rp))) {
       flush((uint32_t)tile / p.gate_span, from, t.row);
       from = t.row;
     }
     // the next gate row's factor, once every team is through with this one's
-    if (SHARED && rp.gate_span && p.gate_from == kFromFactor && t.row == cut && t.more()) {
+    if (SHARED && rp.gate_span && p.gate_from == kFromFactor && t.row == cut && t.more(rp)) {
       consumers_barrier(rp);
       row_to_shared<DT>(NORM ? p.norm_weight + part.col0 : nullptr,
                         p.gate + (int64_t)((uint32_t)t.row / p.gate_span) * rp.vec_per_row + part.col0, V,
@@ -342,7 +334,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       consumers_barrier(rp);
     }
   }
-  const int64_t plane = part.group * row4 + col4;
+  const int64_t plane = part.group * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
   if (p.part_w) combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane + i] = a; });
   if (p.part_w1) {
     float4* to = reinterpret_cast<float4*>(p.part_w1) + plane;
@@ -370,8 +362,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   float4* s_comb = s_dw1 + (p.shared ? rp.chunk * (E / 4) : 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ring_init(rp, s);
-  const Tiles first(rp, part);
-  if (warp == kRingConsumers / 32 && lane < rp.ranks + rp.held && first.more())
+  const Tiles<GATE == kGateShared> first(rp, part);
+  if (warp == kRingConsumers / 32 && lane < rp.ranks + rp.held && first.more(rp))
     prefetch_l2(slice_source(p, lane) + first.row * (int64_t)rp.row_bytes + part.col0 * 16,
                 (uint32_t)first.count(rp) * (uint32_t)V * 16u);
   if constexpr (SPLIT) cluster_barrier();  // the peers' barriers too
@@ -380,7 +372,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   if (warp >= kRingConsumers / 32) {
     take_registers<false>();
     const int who = warp - kRingConsumers / 32;
-    if (lane == 0 && who < rp.producers) ring_produce(rp, part, smem, s, who, p.err, [&](int q) { return slice_source(p, q); });
+    if (lane == 0 && who < rp.producers) ring_produce<GATE == kGateShared>(rp, part, smem, s, who, p.err, [&](int q) { return slice_source(p, q); });
   } else {
     take_registers<true>();
     if (threadIdx.x >= consumers) return;

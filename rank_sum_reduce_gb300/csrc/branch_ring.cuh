@@ -60,12 +60,14 @@ struct Part {
   }
 };
 
-// The tiles of this CTA in order.
+// The tiles of this CTA in order: every so-many-th, or with CUTS, for a gate that rows
+// share, those of one contiguous span.
+template <bool CUTS>
 struct Tiles {
   int row, end, cut, step;
   template <bool SPLIT>
   __device__ __forceinline__ Tiles(const RingPlan& p, const Part<SPLIT>& part) {
-    if (p.gate_span) {
+    if (CUTS && p.gate_span) {
       row = (int)span_start(p.rows, part.groups, part.group);
       end = (int)span_start(p.rows, part.groups, part.group + 1);
       cut = (int)(((uint32_t)row / p.gate_span + 1) * p.gate_span);
@@ -76,10 +78,12 @@ struct Tiles {
       step = part.groups * p.teams;
     }
   }
-  __device__ __forceinline__ bool more() const { return row < end; }
-  __device__ __forceinline__ int count(const RingPlan& p) const { return min(min(end, cut) - row, p.teams); }
+  __device__ __forceinline__ bool more(const RingPlan& p) const { return row < (CUTS ? end : p.rows); }
+  __device__ __forceinline__ int count(const RingPlan& p) const {
+    return min((CUTS ? min(end, cut) : p.rows) - row, p.teams);
+  }
   __device__ __forceinline__ void next(const RingPlan& p) {
-    if (step) {
+    if (!CUTS || step) {
       row += step;
     } else {
       row += count(p);
@@ -133,7 +137,7 @@ __device__ __forceinline__ bool wait_suspended(uint64_t* bar, uint32_t parity, c
 
 // Producer `who` of p.producers: issues every p.producers-th slice of each stage,
 // then waits for the stages that were filled.  source(q): slice q of row 0.
-template <bool SPLIT, class Source>
+template <bool CUTS, bool SPLIT, class Source>
 __device__ __forceinline__ void ring_produce(const RingPlan& p, const Part<SPLIT>& part, uint8_t* ring, RingShared& s, int who,
                                              unsigned int* err, Source source) {
   const int S = p.stages, slices = p.ranks + p.held;
@@ -141,7 +145,7 @@ __device__ __forceinline__ void ring_produce(const RingPlan& p, const Part<SPLIT
   int place = 0;
   uint32_t phase = 0, issued = 0;
   bool ok = true;
-  for (Tiles t(p, part); t.more() && ok; t.next(p)) {
+  for (Tiles<CUTS> t(p, part); t.more(p) && ok; t.next(p)) {
     const int64_t off = t.row * (int64_t)p.row_bytes + part.col0 * 16;
     const uint32_t bytes = (uint32_t)t.count(p) * (uint32_t)part.V * 16u;
     for (int q = 0; q < slices;) {

@@ -97,7 +97,7 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const Part<SPL
       if (ok[k]) st16(p.norm_out + base + col[k], narrow2<DT>(f));
     }
   };
-  for (Tiles t(rp, part); t.more(); t.next(rp)) {
+  for (Tiles<false> t(rp, part); t.more(rp); t.next(rp)) {
     if (team >= t.count(rp)) {
       in.skip();
       continue;
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ring_init(rp, s);
   // the first tile into L2 while the previous grid of the stream finishes
-  const Tiles first(rp, part);
-  if (warp == kRingConsumers / 32 && lane < rp.ranks + rp.held && first.more())
+  const Tiles<false> first(rp, part);
+  if (warp == kRingConsumers / 32 && lane < rp.ranks + rp.held && first.more(rp))
     prefetch_l2(slice_source(p, lane) + first.row * (int64_t)rp.row_bytes + part.col0 * 16,
                 (uint32_t)first.count(rp) * (uint32_t)V * 16u);
   if constexpr (SPLIT) cluster_barrier();  // the peers' barriers too
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   if (warp >= kRingConsumers / 32) {
     take_registers<false>();
     const int who = warp - kRingConsumers / 32;
-    if (lane == 0 && who < rp.producers) ring_produce(rp, part, smem, s, who, p.err, [&](int q) { return slice_source(p, q); });
+    if (lane == 0 && who < rp.producers) ring_produce<false>(rp, part, smem, s, who, p.err, [&](int q) { return slice_source(p, q); });
   } else {
     take_registers<true>();
     if (threadIdx.x >= consumers) return;
