@@ -96,9 +96,39 @@ car_status prepare_dropout(car_ctx* h) {
 bool one_vector(int, int vpt) { return vpt == 1; }
 int branch_threads(int, int) { return kBranchThreads; }
 
-// When the pipeline is faster than the row kernel.
-bool branch_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
-bool branch_backward_pipeline_pays(const car_ctx* h, const BranchTeams&) { return h->M > h->num_sms; }
+// When the forward's pipeline is faster than its row kernel: from so many rows per SM
+// on.  Measured on GB300 (graph replay over cold inputs, bf16 with both norms; the row
+// kernel's time divided by the pipeline's, over M = 152, 304, 608, 1216).
+//  * Rows of more than 1024 vectors, which the row kernel has to split: N = 11072 1.30
+//    to 2.57, N = 16384 0.99 to 1.92, N = 32768 1.05 to 2.3; at M = 80 0.81 to 1.37.
+//  * Shorter ones: the more ranks and the shorter the row, the longer the row kernel,
+//    with several CTAs per SM, keeps up.  W = 1: N = 1024 0.78, 1.02, 1.20, 1.25; N =
+//    4096 0.89, 0.85, 0.94, 1.08; N = 8192 0.91, 1.00, 1.12, 1.32.  W = 4: N = 1024
+//    0.79, 0.95, 0.94, 1.10; N = 4096 0.75, 1.01, 1.20, 1.32; N = 8192 1.08, 1.18,
+//    1.41, 1.67.  W = 8: N = 1024 0.79, 0.86, 0.88, 0.96 (M = 2432 1.12); N = 2048
+//    0.83, 0.81, 0.91, 1.11; N = 4096 0.73, 0.90, 1.11, 1.16; N = 8192 0.96, 1.10,
+//    1.27, 1.39.  W = 16: N = 2048 0.67, 0.73, 0.95, 1.00; N = 4096 0.69, 0.96, 1.03,
+//    1.01; N = 8192 0.95, 1.06, 1.09, 1.12.  fp32 at the same vectors per row, and
+//    without the first norm, within 0.1 of these.
+bool branch_pipeline_pays(const car_ctx* h) {
+  const int V = h->vec_per_row, W = h->W;
+  double rows;  // per SM
+  if (V > 1024) rows = 1;
+  else if (W <= 2) rows = V <= 128 ? 3 : V <= 512 ? 5 : 3;
+  else if (W <= 4) rows = V <= 128 ? 5 : V <= 512 ? 3 : 1.5;
+  else if (W <= 8) rows = V <= 128 ? 10 : V <= 256 ? 6 : V <= 512 ? 3 : 1.5;
+  else rows = V <= 256 ? 10 : V <= 512 ? 4 : 2;
+  return (double)h->M >= rows * h->num_sms;
+}
+
+// The same for the backward (M = 152, 304, 608, 1216): W = 1: N = 1024 0.84, 1.05,
+// 1.31, 1.47; N = 4096 0.83, 1.08, 1.17, 1.34; N = 8192 1.00, 1.14, 1.37, 1.70.  W = 8:
+// N = 1024 0.77, 1.00, 1.24, 1.15; N = 4096 0.84, 0.93, 1.10, 1.12; N = 8192 0.92, 1.04,
+// 1.13, 1.29.  W = 16: N = 4096 0.90, 1.09, 1.21, 1.21.  More than 1024 vectors: N =
+// 11072 1.33 to 2.13, N = 16384 1.09 to 1.82, N = 32768 1.20 to 2.26; at M = 80 0.84 to
+// 1.24.  Rank counts that the row kernel is not compiled for: W = 3 and 6, N = 4096 0.98,
+// 1.20, 1.45, 1.65.
+bool branch_backward_pipeline_pays(const car_ctx* h) { return h->M >= (h->vec_per_row > 1024 ? 1 : 2) * (int64_t)h->num_sms; }
 
 car_status prepare_branch(car_ctx* h) {
   if (h->branch_ready.load(std::memory_order_acquire)) return CAR_OK;
@@ -112,7 +142,7 @@ car_status prepare_branch(car_ctx* h) {
   if (e != cudaSuccess) return cuda_fail(e, "branch occupancy");
   h->branch.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
   branch_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_tma);
-  h->branch_pipeline = branch_pipeline_pays(h, h->branch_tma);
+  h->branch_pipeline = branch_pipeline_pays(h);
   if (h->branch_pipeline && (e = branch_tma_prepare(h->dtype, &h->branch_tma)) != cudaSuccess)
     return cuda_fail(e, "branch pipeline smem");
   h->branch_ready.store(true, std::memory_order_release);
@@ -131,7 +161,7 @@ car_status prepare_branch_backward(car_ctx* h) {
   if (e != cudaSuccess) return cuda_fail(e, "branch backward occupancy");
   h->branch_backward.groups = (int)std::max<int64_t>(1, std::min<int64_t>(h->M, groups));
   branch_backward_tma_shape(h->M, h->vec_per_row, h->num_sms, &h->branch_backward_tma);
-  h->branch_backward_pipeline = branch_backward_pipeline_pays(h, h->branch_backward_tma);
+  h->branch_backward_pipeline = branch_backward_pipeline_pays(h);
   if (h->branch_backward_pipeline && (e = branch_backward_tma_prepare(h->dtype, &h->branch_backward_tma)) != cudaSuccess)
     return cuda_fail(e, "branch backward pipeline smem");
   h->branch_backward_ready.store(true, std::memory_order_release);

@@ -89,7 +89,6 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
   const ClusterWait peers{part.crank, p.wait_ns, p.err};
   const int team = SPLIT ? 0 : threadIdx.x / T, tid = threadIdx.x - team * T;
   const uint8_t* mine = ring + (size_t)team * rp.row_bytes;  // the row in stage 0
-  const DropState state = drop_state(p.drop);
   const int first = (int)span_start(rp.rows, part.groups, part.group);
   float2 dw[VPT][E / 2], ts[VPT][E / 2];
   bool ok[VPT];
@@ -252,7 +251,9 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
           }
           if constexpr (DROP) {
             uint32_t bits[E / 2];
-            drop_bits<E>(state, base + col[k], bits);
+            uint4 st;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(st.x), "=r"(st.y), "=r"(st.z), "=r"(st.w) : "r"(smem_addr(&s.drop)));
+            drop_bits<E>(DropState{p.drop.key0, p.drop.key1, st.x, st.y, st.z, st.w}, base + col[k], bits);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = drop2(p.drop, bits[e], g[k][e]);  // dz
           }
@@ -386,6 +387,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                         V, consumers, s_factor);
     if (p.shared)
       for (int i = threadIdx.x; i < V * (E / 4); i += consumers) s_dw1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (DROP && threadIdx.x == 0) {
+      const DropState d = drop_state(p.drop);
+      s.drop = make_uint4(d.z, d.y, d.hi, d.lo);
+    }
     consumers_barrier(rp);
     consume<DT, VPT, SPLIT, NORM, GATE, DROP>(p, part, smem, s_rows, s_factor, s_comb, s_dw1, s);
   }
