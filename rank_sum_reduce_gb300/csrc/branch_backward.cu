@@ -325,11 +325,16 @@ __global__ void __launch_bounds__(256) branch_sums_kernel(const __grid_constant_
   __syncthreads();
   if (threadIdx.x < 4 * VECS) {
     const float* c = reinterpret_cast<const float*>(&s[0][0]) + threadIdx.x;
-    float sum = 0.f;
+    float sum[PARTS];
 #pragma unroll
-    for (int k = 0; k < PARTS; k++) sum += c[k * 4 * VECS];
+    for (int k = 0; k < PARTS; k++) sum[k] = c[k * 4 * VECS];
+#pragma unroll
+    for (int n = PARTS / 2; n > 0; n /= 2) {  // in pairs: five roundings instead of 31
+#pragma unroll
+      for (int k = 0; k < n; k++) sum[k] += sum[k + n];
+    }
     const int64_t i = (int64_t)blockIdx.x * 4 * VECS + threadIdx.x;
-    if (i < 4 * (int64_t)p.vecs) reinterpret_cast<float*>(out)[i] = scale ? sum * weight_at(scale, p.dtype, i) : sum;
+    if (i < 4 * (int64_t)p.vecs) reinterpret_cast<float*>(out)[i] = scale ? sum[0] * weight_at(scale, p.dtype, i) : sum[0];
   }
 }
 
