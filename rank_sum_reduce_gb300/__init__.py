@@ -79,8 +79,7 @@ _SIGS = {
     "car_reduce_branch_residual_rmsnorm": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_branch), _vp, _vp, ctypes.c_float,
                                                           _vp, _vp, _vp, _vp]),
     "car_reduce_branch_residual_rmsnorm_backward": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_branch), _vp, _vp, _vp,
-                                                                   ctypes.c_float, _vp, ctypes.POINTER(car_branch_grads),
-                                                                   _vp, _vp]),
+                                                                   ctypes.c_float, _vp, _vp, _vp, _vp]),
     "car_branch_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.POINTER(car_branch)]),
     "car_grads_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64),
                                         ctypes.POINTER(ctypes.c_int), _pvp, _pvp, _ctx_pp]),
@@ -206,9 +205,10 @@ def car_reduce_branch_residual_rmsnorm(h, inputs, branch, residual: int, weight:
 def car_reduce_branch_residual_rmsnorm_backward(h, dnorm, branch, ar: int | None, residual_out: int, weight: int,
                                                 eps: float, dresidual_out: int | None, out, workspace: int | None,
                                                 stream: int = 0) -> int:
-    """branch: a car_branch; out: a car_branch_grads."""
+    """branch: a car_branch; out: a car_branch_grads, or its bytes."""
     return _lib.car_reduce_branch_residual_rmsnorm_backward(h, _table(dnorm) if dnorm is not None else None, _ref(branch), ar,
-                                                            residual_out, weight, eps, dresidual_out, _ref(out), workspace,
+                                                            residual_out, weight, eps, dresidual_out,
+                                                            out if isinstance(out, bytes) else _ref(out), workspace,
                                                             stream)
 
 
@@ -457,6 +457,8 @@ class Branch:
         self.struct = car_branch(norm_weight.data_ptr() if norm_weight is not None else None, norm_eps,
                                  gate.data_ptr() if gate is not None else None, gate_rows, residual_scale,
                                  ctypes.pointer(dropout.struct) if dropout is not None else None)
+        self.ref = ctypes.byref(self.struct)
+        self._checked = None   # (device, bytes of a row, rows) of the handle that it was last found right for
 
 
 class Car:
@@ -477,6 +479,7 @@ class Car:
         # bytes that the tensors of a call need, in the order of its arguments
         self._quant_sizes = [(D, Nw, D, M * N, car_quant_scale_bytes(h, k), D, D) for k in range(len(SCALE_CODE))]
         self._backward_sizes = None   # found when first asked for
+        self._branch_sizes = {}       # the same, by gate_rows
         import torch
 
         self.device = torch.cuda.current_device()
@@ -598,22 +601,24 @@ class Car:
     def _dropout(self, dropout):
         if dropout.offset_dev is not None:
             _ptr(dropout.offset_dev, 8, "offset_dev", self.device)
-        return dropout.struct
+        return ctypes.byref(dropout.struct)
 
     def _branch(self, branch):
-        """Its struct, once its tensors have been checked for this handle."""
-        row = self._row
-        if branch.norm_weight is not None:
-            _ptr(branch.norm_weight, row, "norm_weight", self.device)
-        if branch.gate is not None:
-            _ptr(branch.gate, (branch.gate_rows or self.M) * row, "gate", self.device)
-        if branch.dropout is not None:
-            self._dropout(branch.dropout)
-        return branch.struct
+        """A reference to its struct, once its tensors have been checked for this handle."""
+        key = (self.device, self._row, self.M)
+        if branch._checked != key:
+            if branch.norm_weight is not None:
+                _ptr(branch.norm_weight, self._row, "norm_weight", self.device)
+            if branch.gate is not None:
+                _ptr(branch.gate, (branch.gate_rows or self.M) * self._row, "gate", self.device)
+            if branch.dropout is not None:
+                self._dropout(branch.dropout)
+            branch._checked = key
+        return branch.ref
 
     def reduce_dropout(self, xs, dropout, ar_out, stream=None):
         """ar_out = dropout of the rank sum; its gradient is the same call on the gradient's rank contributions."""
-        check(_lib.car_reduce_dropout(self.h, _table(self._ranks(xs, self.D, "inputs")), ctypes.byref(self._dropout(dropout)),
+        check(_lib.car_reduce_dropout(self.h, _table(self._ranks(xs, self.D, "inputs")), self._dropout(dropout),
                                       self._p(ar_out, self.D, "ar_out"), _stream(stream, self.device)), "car_reduce_dropout")
 
     def reduce_branch_residual_rmsnorm(self, xs, branch, residual, weight, eps, residual_out, norm_out, ar_out=None,
@@ -624,12 +629,16 @@ class Car:
         res, w, ro, no, ar = self._ptrs((residual, weight, residual_out, norm_out, ar_out), (D, self._row, D, D, D),
                                         ("residual", "weight", "residual_out", "norm_out", "ar_out"))
         check(_lib.car_reduce_branch_residual_rmsnorm(self.h, _table(self._ranks(xs, D, "inputs")),
-                                                      ctypes.byref(self._branch(branch)), res, w, eps, ro, no, ar,
+                                                      self._branch(branch), res, w, eps, ro, no, ar,
                                                       _stream(stream, self.device)), "car_reduce_branch_residual_rmsnorm")
 
     def branch_workspace_bytes(self, branch=None) -> int:
-        """Of the backward's workspace; depends on whether rows share a row of the branch's gate, and how many."""
-        return car_branch_workspace_bytes(self.h, branch.struct if branch is not None else None)
+        """Of the backward's workspace; depends on whether rows share a row of the branch's gate."""
+        key = branch.gate_rows if branch is not None and branch.gate is not None else 0
+        need = self._branch_sizes.get(key)
+        if need is None:
+            need = self._branch_sizes[key] = car_branch_workspace_bytes(self.h, branch.struct if branch is not None else None)
+        return need
 
     def reduce_branch_residual_rmsnorm_backward(self, dnorm, branch, ar, residual_out, weight, eps, dresidual_out, dx,
                                                 dresidual=None, dweight=None, dnorm_weight=None, dgate=None,
@@ -656,8 +665,8 @@ class Car:
             (D, D, self._row, D, D, D, 4 * N, 4 * N, 4 * N * branch.gate_rows if shared else D, need),
             ("ar", "residual_out", "weight", "dresidual_out", "dx", "dresidual", "dweight", "dnorm_weight", "dgate", "workspace"))
         check(_lib.car_reduce_branch_residual_rmsnorm_backward(
-            self.h, _table(self._ranks(dnorm, D, "dnorm")), ctypes.byref(self._branch(branch)), a, h, w, eps, dro,
-            ctypes.byref(car_branch_grads(out, dr, dw, dw1, dg)), ws, _stream(stream, self.device)),
+            self.h, _table(self._ranks(dnorm, D, "dnorm")), self._branch(branch), a, h, w, eps, dro,
+            _packer(5)(out, dr or 0, dw or 0, dw1 or 0, dg or 0), ws, _stream(stream, self.device)),
             "car_reduce_branch_residual_rmsnorm_backward")
 
     def ll128_encode(self, data, flag, wire, stream=None):

@@ -39,7 +39,7 @@ bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_
   rp.ranks = W;
   rp.teams = sh.teams;
   rp.team_threads = sh.team_threads;
-  rp.gate_span = p->shared || (folded && br.gate_span < rows) ? (uint32_t)br.gate_span : 0;
+  rp.gate_span = br.gate && !own && br.gate_span < rows ? (uint32_t)br.gate_span : 0;  // whatever is asked for: the same bits
   const int part_bytes = rp.chunk * 16, slice = sh.teams * part_bytes, floats = dtype == kFP32 ? part_bytes : 2 * part_bytes;
   rp.held = 1;
   p->a_at = p->d_at = p->g_at = 0;

@@ -150,14 +150,13 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       return make_float4(f[0], f[1], f[2], f[3]);
     }
   };
-  // rows [from, to) of gate row b are in ts
-  auto flush = [&](uint32_t b, int from, int to) {
-    const int lo = (int)(b * p.gate_span);
-    const bool whole = from == lo && (uint32_t)(to - lo) == p.gate_span;
+  // ts holds all rows of gate row b (whole), or those of this span: its first gate row
+  // (slot 0) or its last (1)
+  auto flush = [&](uint32_t b, bool whole, int slot) {
     float4* out = nullptr;
     if (p.dgate)
       out = reinterpret_cast<float4*>(whole ? p.dgate : p.part_gate) +
-            (whole ? (int64_t)b : 2 * (int64_t)part.group + (from == first ? 0 : 1)) * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
+            (whole ? (int64_t)b : 2 * (int64_t)part.group + slot) * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
     combine(ts, [&](int i, float4 t) {
       const float4 g = four(p.gate + (int64_t)b * rp.vec_per_row + part.col0, i);
       float4 d = s_dw1[i];
@@ -322,9 +321,14 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
     }
     const int cut = t.cut;
     t.next(rp);
-    if (shared && (t.row == cut || !t.more(rp))) {
-      flush((uint32_t)tile / p.gate_span, from, t.row);
-      from = t.row;
+    if (shared) {
+      if (!rp.gate_span) {  // one gate row, tiles in strides
+        if (!t.more(rp)) flush(0, part.groups == 1, 0);
+      } else if (t.row == cut || !t.more(rp)) {
+        const int b = (uint32_t)tile / p.gate_span, lo = b * (int)p.gate_span;
+        flush(b, from == lo && t.row - lo == (int)p.gate_span, from == first ? 0 : 1);
+        from = t.row;
+      }
     }
     // the next gate row's factor, once every team is through with this one's
     if (SHARED && rp.gate_span && p.gate_from == kFromFactor && t.row == cut && t.more(rp)) {

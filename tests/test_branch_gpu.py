@@ -63,6 +63,11 @@ CASES = [
     (8, 333, 13000, "bf16", True, 3, 1.0, 0.0), (2, 167, 11004, "fp32", True, None, 1.0, 0.1), (4, 161, 13004, "fp32", False, 7, 1.0, 0.0),
     (3, 182, 16384, "fp32", True, 2, 1.0, 0.0), (2, 3000, 264, "fp16", True, 1000, 1.0, 0.1), (1, 3001, 512, "bf16", False, None, 0.3, 0.5),
     (1, 2800, 2048, "fp16", True, 14, 1.0, 0.0),
+    # three vectors per thread forward, clusters of two and four with each kind of gate, gate rows of few and of many rows
+    (4, 320, 5120, "bf16", True, 1, 1.0, 0.0), (2, 480, 5128, "fp16", True, 4, 1.0, 0.1), (1, 460, 6144, "fp32", True, 0, 1.0, 0.0),
+    (2, 200, 12296, "bf16", True, 0, 1.0, 0.1), (1, 156, 20488, "bf16", True, 2, 1.0, 0.0), (1, 155, 32768, "fp16", True, 155, 1.0, 0.0),
+    (3, 154, 16384, "fp32", True, 7, 1.0, 0.1), (2, 2432, 1536, "bf16", True, 1216, 1.0, 0.0), (4, 1824, 648, "fp32", False, 912, 1.0, 0.2),
+    (16, 640, 2064, "bf16", True, 5, 1.0, 0.1), (12, 310, 4104, "fp16", True, 1, 1.0, 0.0),
 ]
 
 
@@ -400,6 +405,67 @@ def test_wait_that_runs_out_is_reported(car, which):
         got = go()
         c.sync()
         assert all(t is None or torch.equal(t, got[n]) for n, t in want.items())
+
+
+@pytest.mark.parametrize("which", ["forward", "backward"])
+@pytest.mark.parametrize("W,M,N,cta", [(2, 160, 16384, 1), (1, 170, 32768, 3)])
+def test_wait_of_a_split_row_in_the_pipeline(car, which, W, M, N, cta):
+    """The same where the pipeline's CTAs share a row."""
+    k = Case(W, M, N, "bf16")
+    with car.Car(W, M, N, "bf16") as c:
+        b = k.branch(car)
+        go = (lambda: run_forward(c, k, b, empty)) if which == "forward" else (lambda: run_backward(c, k, b, k.grads(empty)))
+        want = go()
+        c.sync()
+        car.check(car.car_test_delay_partial(c.h, 20000, cta, 7, 3000000))
+        got = go()
+        with pytest.raises(car.CarError) as e:
+            c.sync()
+        assert e.value.status == car.CAR_ERR_TIMEOUT
+        row, rest = "norm_out" if which == "forward" else "dx", [m for m in range(M) if m != 7]
+        assert got[row][7].isnan().any() and torch.equal(got[row][rest], want[row][rest])
+        car.check(car.car_test_delay_partial(c.h, 0, -1, 0, 0))
+        got = go()
+        c.sync()
+        assert all(t is None or torch.equal(t, got[n]) for n, t in want.items())
+
+
+# both sides of the borders between the row kernels and the pipelines (152 SMs), and between whole and split rows
+BORDERS = [(1, 455, 1024, "bf16"), (1, 456, 1024, "bf16"), (4, 455, 2048, "fp16"), (4, 456, 2048, "fp16"), (8, 227, 8192, "bf16"),
+           (8, 228, 8192, "bf16"), (16, 303, 8192, "fp16"), (16, 304, 8192, "fp16"), (2, 151, 8200, "bf16"), (2, 152, 8200, "bf16"),
+           (2, 153, 8192, "bf16"), (1, 303, 1024, "bf16"), (1, 304, 1024, "bf16"), (3, 304, 6152, "bf16"), (1, 152, 12288, "bf16"),
+           (1, 152, 12296, "bf16"), (1, 160, 16384, "bf16"), (1, 160, 16392, "bf16"), (1, 153, 8196, "fp32"), (2, 160, 16384, "fp32")]
+
+
+@pytest.mark.parametrize("W,M,N,dtype", BORDERS)
+def test_borders_between_kernels(car, W, M, N, dtype):
+    k = Case(W, M, N, dtype, gate_rows=M % 2, p=0.1 if M % 3 else 0.0)
+    with car.Car(W, M, N, dtype) as c:
+        b = k.branch(car)
+        got, grads = run_forward(c, k, b, empty), run_backward(c, k, b, k.grads(empty))
+        c.sync()
+    k.check_forward(got)
+    k.check_backward(grads)
+
+
+@pytest.mark.parametrize("case", [(2, 37, 1032, "bf16", True, 37, 1.0, 0.2), (4, 400, 4096, "fp32", True, 4, 1.0, 0.0),
+                                  (1, 900, 2048, "fp16", False, 3, 1.0, 0.0), (1, 310, 2056, "bf16", True, 0, 1.0, 0.1),
+                                  (2, 160, 12296, "bf16", True, 1, 1.0, 0.0)], ids=lambda c: "-".join(str(v) for v in c))
+def test_every_gradient_may_be_left_out(car, case):
+    """The others keep their bits, and nothing is written in its place."""
+    k = Case(*case)
+    with car.Car(*case[:4]) as c:
+        b = k.branch(car)
+        want = run_backward(c, k, b, k.grads(empty))
+        for name in ("dresidual", "dweight", "dnorm_weight", "dgate"):
+            for alone in (False, True):
+                got = k.grads(empty)
+                for other in ("dresidual", "dweight", "dnorm_weight", "dgate"):
+                    if (other == name) != alone:
+                        got[other] = None
+                run_backward(c, k, b, got)
+                c.sync()
+                assert all(t is None or torch.equal(t, want[n]) for n, t in got.items()), (name, alone)
 
 
 def test_rows_past_32_bits_of_elements(car):
