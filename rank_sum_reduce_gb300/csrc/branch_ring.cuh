@@ -231,6 +231,11 @@ __device__ __forceinline__ const uint8_t* ring_rank_sum(const RingPlan& p, RingR
   constexpr int E = Pack<DT>::kN;
   const uint32_t stride = slice_stride(p);
   const bool whole = p.tile_stages == 1;
+#pragma unroll
+  for (int k = 0; k < VPT; k++) {
+#pragma unroll
+    for (int e = 0; e < E / 2; e++) acc[k][e] = both(-0.f);  // -0 + x is x, whatever x is
+  }
   int q = 0;
   while (true) {
     in.wait();
@@ -244,7 +249,7 @@ __device__ __forceinline__ const uint8_t* ring_rank_sum(const RingPlan& p, RingR
         float2 f[E / 2];
         widen2<DT>(lds16(slice + at[k]), f);
 #pragma unroll
-        for (int e = 0; e < E / 2; e++) acc[k][e] = q + i == 0 ? f[e] : add2(acc[k][e], f[e]);
+        for (int e = 0; e < E / 2; e++) acc[k][e] = add2(acc[k][e], f[e]);
       }
     }
     if (whole) return slice;
