@@ -17,8 +17,8 @@ BackwardTmaFn pick(int dtype, const BranchTeams& sh, bool norm, int gate, bool d
 
 constexpr int kSharedBudget = 222 * 1024;  // ring and what lies beside it; RingShared is static
 
-// Where a call's weights and slices lie; the bytes beside the ring: the weights, the
-// sum of dnorm_weight behind a shared gate, the teams' sums.
+// Where a call's weights and slices lie; the bytes beside the ring: the weights and the
+// teams' sums.
 bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row, const BranchTeams& sh,
          BranchBackwardTmaParams* p, int* beside) {
   const bool norm = br.norm_weight != nullptr, own = br.gate && br.gate_span == 0;
@@ -47,8 +47,7 @@ bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_
   if (g.dres) p->d_at = slice * rp.held++;
   if (own) p->g_at = slice * rp.held++;
   p->weight_rows = p->factor ? 2 : 1;
-  const int sums = (p->shared ? floats : 0) + (sh.teams > 1 ? sh.teams * floats : 0);
-  *beside = sums + p->weight_rows * floats;
+  *beside = ((sh.teams > 1 ? sh.teams : 0) + p->weight_rows) * floats;
   return branch_ring_fit(kSharedBudget - *beside, &rp);
 }
 

@@ -11,8 +11,10 @@
 // Column sums.  A thread sums g u and t (or gate t, where no gate row is shared)
 // over its team's rows in registers.  Where rows share a gate row, tiles end with
 // it: the teams' sums of t are then added in shared memory in team order, leave
-// as dgate or as a partial of the span (as in the row kernel), and gate * t goes
-// to dnorm_weight's sum in shared memory, where each column has one owner.
+// as dgate or as a partial of the span (as in the row kernel), and gate * t is
+// added to the span's partial of dnorm_weight, where each column has one owner.
+// (That sum in shared memory left the ring two stages in place of two tiles, W = 1,
+// M = 1216, N = 16384 bf16 with norms and one gate row PLACEHOLDER.)
 #pragma once
 
 #include "branch_ring.cuh"
@@ -43,7 +45,7 @@ struct BranchBackwardTmaParams {
   uint32_t gate_span;        // rows that share a gate row
   bool shared;               // t is summed by gate row
   bool factor;               // dz is multiplied by a factor row: norm_weight, a gate of many rows or both
-  int weight_rows;           // rows of weights in shared memory, in fp32 or packed
+  int weight_rows;           // rows of weights in shared memory, in fp32
   unsigned long long wait_ns;  // as in the row kernels, where CTAs share a row
   unsigned long long delay_ns;
   int64_t delay_row;
@@ -79,7 +81,7 @@ __device__ __forceinline__ void weight_at(const BranchBackwardTmaParams& p, cons
 
 template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP>
 __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const Part<SPLIT>& part, const uint8_t* ring, const uint8_t* s_rows,
-                                        uint8_t* s_factor, float4* s_comb, float4* s_dw1, RingShared& s) {
+                                        uint8_t* s_factor, float4* s_comb, RingShared& s) {
   constexpr int E = Pack<DT>::kN;
   constexpr bool SHARED = GATE == kGateShared;
   constexpr bool BRANCHES = E == 8 && ((SHARED && !SPLIT) || (NORM && GATE == kGateOwn));  // else they spill
@@ -150,6 +152,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       return make_float4(f[0], f[1], f[2], f[3]);
     }
   };
+  const int64_t plane = part.group * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
   // ts holds all rows of gate row b (whole), or those of this span: its first gate row
   // (slot 0) or its last (1)
   auto flush = [&](uint32_t b, bool whole, int slot) {
@@ -158,13 +161,16 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       out = reinterpret_cast<float4*>(whole ? p.dgate : p.part_gate) +
             (whole ? (int64_t)b : 2 * (int64_t)part.group + slot) * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
     combine(ts, [&](int i, float4 t) {
-      const float4 g = four(p.gate + (int64_t)b * rp.vec_per_row + part.col0, i);
-      float4 d = s_dw1[i];
-      d.x = fmaf(g.x, t.x, d.x);
-      d.y = fmaf(g.y, t.y, d.y);
-      d.z = fmaf(g.z, t.z, d.z);
-      d.w = fmaf(g.w, t.w, d.w);
-      s_dw1[i] = d;
+      if (NORM && p.part_w1) {
+        const float4 g = four(p.gate + (int64_t)b * rp.vec_per_row + part.col0, i);
+        float4* to = reinterpret_cast<float4*>(p.part_w1) + plane + i;
+        float4 d = slot == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *to;
+        d.x = fmaf(g.x, t.x, d.x);
+        d.y = fmaf(g.y, t.y, d.y);
+        d.z = fmaf(g.z, t.z, d.z);
+        d.w = fmaf(g.w, t.w, d.w);
+        *to = d;
+      }
       if (!out) return;
       if (NORM && whole) {
         const float4 w = four(p.norm_weight + part.col0, i);
@@ -339,17 +345,8 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       consumers_barrier(rp);
     }
   }
-  const int64_t plane = part.group * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
   if (p.part_w) combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane + i] = a; });
-  if (p.part_w1) {
-    float4* to = reinterpret_cast<float4*>(p.part_w1) + plane;
-    if (!shared)
-      combine(ts, [&](int i, float4 a) { to[i] = a; });
-    else if (teams > 1)
-      for (int i = threadIdx.x; i < V * (E / 4); i += teams * T) to[i] = s_dw1[i];
-    else
-      combine(ts, [&](int i, float4) { to[i] = s_dw1[i]; });
-  }
+  if (NORM && p.part_w1 && !shared) combine(ts, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w1)[plane + i] = a; });
 }
 
 template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP>
@@ -363,8 +360,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   const int consumers = rp.teams * rp.team_threads, V = part.V;
   uint8_t* s_rows = smem + (size_t)rp.stages * rp.group * slice_stride(rp);
   uint8_t* s_factor = s_rows + (size_t)rp.chunk * E * 4;
-  float4* s_dw1 = reinterpret_cast<float4*>(s_rows + (size_t)p.weight_rows * rp.chunk * E * 4);
-  float4* s_comb = s_dw1 + (p.shared ? rp.chunk * (E / 4) : 0);
+  float4* s_comb = reinterpret_cast<float4*>(s_rows + (size_t)p.weight_rows * rp.chunk * E * 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ring_init(rp, s);
   const Tiles<GATE == kGateShared> first(rp, part);
@@ -389,14 +385,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                             ? p.gate + (int64_t)((uint32_t)first.row / p.gate_span) * rp.vec_per_row + part.col0
                             : nullptr,
                         V, consumers, s_factor);
-    if (p.shared)
-      for (int i = threadIdx.x; i < V * (E / 4); i += consumers) s_dw1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (DROP && threadIdx.x == 0) {
       const DropState d = drop_state(p.drop);
       s.drop = make_uint4(d.z, d.y, d.hi, d.lo);
     }
     consumers_barrier(rp);
-    consume<DT, VPT, SPLIT, NORM, GATE, DROP>(p, part, smem, s_rows, s_factor, s_comb, s_dw1, s);
+    consume<DT, VPT, SPLIT, NORM, GATE, DROP>(p, part, smem, s_rows, s_factor, s_comb, s);
   }
 }
 
