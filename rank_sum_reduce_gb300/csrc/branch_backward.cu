@@ -250,7 +250,12 @@ __global__ void __launch_bounds__(kBranchThreads) reduce_branch_rmsnorm_backward
 // the host; the divisions took 50 us here for a gate row of 152.)  A block's threads
 // take 8 float4 columns and 32 parts of the sum, their loads in flight in
 // batches, and those are added in order: the partials were just written and
-// come from L2, so the kernel is bound by one L2 latency and its launch.
+// come from L2, so the kernel is bound by one L2 latency and its launch.  Where no
+// gate row has more than 32 partials a block takes 32 columns of one and 8 parts:
+// there are fewer blocks, which else do not fit at once (W = 1, M = 1216, N = 16384
+// bf16 with norms, 38 gate rows of 4 partials: the whole backward 90.9 us with 8
+// columns, 74.7 with 32; four of 20 partials 71.6 and 70.0; 16 of 10 at M = 16384, N =
+// 4096 149.0 and 146.0).
 struct BranchSums {
   const float4* part_w;
   const float4* part_w1;
@@ -262,6 +267,7 @@ struct BranchSums {
   int dtype;
   int groups;
   int vecs;                 // float4 in a row
+  int gate_blocks;          // blocks that sum a gate row, 0: as many as the others
   struct Cut {
     uint32_t row;         // of the gate
     uint16_t first, count;  // groups
@@ -276,10 +282,55 @@ __device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i) 
   return __half2float(static_cast<const __half*>(w)[i]);
 }
 
+// Block `block` of a job: float4 columns VECS * block .. of out.
+template <int VECS, int BATCH>
+__device__ __forceinline__ void sum_partials(float4 (&s)[256], const float4* from, const float4* head, int64_t stride, int count,
+                                             int block, int vecs, float4* out, const void* scale, int dtype) {
+  constexpr int PARTS = 256 / VECS;
+  const int col = threadIdx.x % VECS, part = threadIdx.x / VECS;
+  const int v = block * VECS + col;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (v < vecs) {
+    for (int k0 = part; k0 < count; k0 += BATCH * PARTS) {
+      float4 x[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; i++) {
+        const int k = k0 + i * PARTS;
+        x[i] = k < count ? __ldcg((k == 0 ? from : head + k * stride) + v) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; i++) {
+        a.x += x[i].x;
+        a.y += x[i].y;
+        a.z += x[i].z;
+        a.w += x[i].w;
+      }
+    }
+  }
+  s[threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.x < 4 * VECS) {
+    const float* c = reinterpret_cast<const float*>(s) + threadIdx.x;
+    float sum[PARTS];
+#pragma unroll
+    for (int k = 0; k < PARTS; k++) sum[k] = c[k * 4 * VECS];
+#pragma unroll
+    for (int n = PARTS / 2; n > 0; n /= 2) {  // in pairs: five roundings instead of 31
+#pragma unroll
+      for (int k = 0; k < n; k++) sum[k] += sum[k + n];
+    }
+    const int64_t i = (int64_t)block * 4 * VECS + threadIdx.x;
+    if (i < 4 * (int64_t)vecs) reinterpret_cast<float*>(out)[i] = scale ? sum[0] * weight_at(scale, dtype, i) : sum[0];
+  }
+}
+
 __global__ void __launch_bounds__(256) branch_sums_kernel(const __grid_constant__ BranchSums p) {
-  constexpr int VECS = 8, PARTS = 32, BATCH = 5;
-  __shared__ float4 s[PARTS][VECS];
-  const int job = blockIdx.y;
+  __shared__ float4 s[256];
+  // blocks of the two weights, then those of the gate rows
+  const int across = (p.vecs + 7) / 8, per_cut = p.gate_blocks ? p.gate_blocks : across;
+  const bool gate = blockIdx.x >= 2u * across;
+  const int rest = (int)blockIdx.x - 2 * across, cut = gate ? rest / per_cut : 0;
+  const int job = gate ? 2 + cut : (int)blockIdx.x / across, block = gate ? rest - cut * per_cut : (int)blockIdx.x - job * across;
   const float4 *from, *head;  // entry 0, entry k > 0 at head + k * stride
   float4* out;
   int count;
@@ -301,41 +352,10 @@ __global__ void __launch_bounds__(256) branch_sums_kernel(const __grid_constant_
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!out) return;
-  const int col = threadIdx.x % VECS, part = threadIdx.x / VECS;
-  const int v = blockIdx.x * VECS + col;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (v < p.vecs) {
-    for (int k0 = part; k0 < count; k0 += BATCH * PARTS) {
-      float4 x[BATCH];
-#pragma unroll
-      for (int i = 0; i < BATCH; i++) {
-        const int k = k0 + i * PARTS;
-        x[i] = k < count ? __ldcg((k == 0 ? from : head + k * stride) + v) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < BATCH; i++) {
-        a.x += x[i].x;
-        a.y += x[i].y;
-        a.z += x[i].z;
-        a.w += x[i].w;
-      }
-    }
-  }
-  s[part][col] = a;
-  __syncthreads();
-  if (threadIdx.x < 4 * VECS) {
-    const float* c = reinterpret_cast<const float*>(&s[0][0]) + threadIdx.x;
-    float sum[PARTS];
-#pragma unroll
-    for (int k = 0; k < PARTS; k++) sum[k] = c[k * 4 * VECS];
-#pragma unroll
-    for (int n = PARTS / 2; n > 0; n /= 2) {  // in pairs: five roundings instead of 31
-#pragma unroll
-      for (int k = 0; k < n; k++) sum[k] += sum[k + n];
-    }
-    const int64_t i = (int64_t)blockIdx.x * 4 * VECS + threadIdx.x;
-    if (i < 4 * (int64_t)p.vecs) reinterpret_cast<float*>(out)[i] = scale ? sum[0] * weight_at(scale, p.dtype, i) : sum[0];
-  }
+  if (gate && p.gate_blocks)
+    sum_partials<32, 2>(s, from, head, stride, count, block, p.vecs, out, scale, p.dtype);
+  else
+    sum_partials<8, 5>(s, from, head, stride, count, block, p.vecs, out, scale, p.dtype);
 }
 
 using BackwardFn = void (*)(const BranchBackwardParams);
@@ -450,7 +470,7 @@ cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, in
   p.groups = groups;
   p.vecs = (int)(cols / 4);
   // gate rows that an inner border of the spans cuts, each once
-  int cuts = 0;
+  int cuts = 0, most = 0;  // and the partials of any of them
   if (gates) {
     int64_t start = 0;  // of span c - 1
     for (int c = 1; c < groups; c++) {
@@ -464,8 +484,11 @@ cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, in
       start = at;
     }
   }
+  for (int c = 0; c < cuts; c++) most = std::max<int>(most, p.cut[c].count);
+  const int across = (p.vecs + 7) / 8;
+  p.gate_blocks = most <= 32 ? (p.vecs + 31) / 32 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.vecs + 7) / 8), (unsigned)(2 + cuts), 1);
+  cfg.gridDim = dim3((unsigned)(2 * across + cuts * (p.gate_blocks ? p.gate_blocks : across)), 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

@@ -13,8 +13,8 @@
 // it: the teams' sums of t are then added in shared memory in team order, leave
 // as dgate or as a partial of the span (as in the row kernel), and gate * t is
 // added to the span's partial of dnorm_weight, where each column has one owner.
-// (That sum in shared memory left the ring two stages in place of two tiles, W = 1,
-// M = 1216, N = 16384 bf16 with norms and one gate row PLACEHOLDER.)
+// (That sum in shared memory left the ring no room for two tiles: W = 1, M = 1216, N =
+// 16384 bf16 with norms and one gate row 87 us against 66.)
 #pragma once
 
 #include "branch_ring.cuh"
