@@ -96,6 +96,9 @@ car_status prepare_dropout(car_ctx* h) {
 bool one_vector(int, int vpt) { return vpt == 1; }
 int branch_threads(int, int) { return kBranchThreads; }
 
+// The pipelines count rows in 32 bits, a grid's step past the last one included.
+constexpr int64_t kMaxPipelineRows = 1 << 30;
+
 // When the forward's pipeline is faster than its row kernel: from so many rows per SM
 // on.  Measured on GB300 (graph replay over cold inputs, bf16 with both norms; the row
 // kernel's time divided by the pipeline's, over M = 152, 304, 608, 1216).
@@ -118,7 +121,7 @@ bool branch_pipeline_pays(const car_ctx* h) {
   else if (W <= 4) rows = V <= 128 ? 5 : V <= 512 ? 3 : 1.5;
   else if (W <= 8) rows = V <= 128 ? 10 : V <= 256 ? 6 : V <= 512 ? 3 : 1.5;
   else rows = V <= 256 ? 10 : V <= 512 ? 4 : 2;
-  return (double)h->M >= rows * h->num_sms;
+  return (double)h->M >= rows * h->num_sms && h->M <= kMaxPipelineRows;
 }
 
 // The same for the backward (M = 152, 304, 608, 1216): W = 1: N = 1024 0.84, 1.05,
@@ -128,7 +131,9 @@ bool branch_pipeline_pays(const car_ctx* h) {
 // 11072 1.33 to 2.13, N = 16384 1.09 to 1.82, N = 32768 1.20 to 2.26; at M = 80 0.84 to
 // 1.24.  Rank counts that the row kernel is not compiled for: W = 3 and 6, N = 4096 0.98,
 // 1.20, 1.45, 1.65.
-bool branch_backward_pipeline_pays(const car_ctx* h) { return h->M >= (h->vec_per_row > 1024 ? 1 : 2) * (int64_t)h->num_sms; }
+bool branch_backward_pipeline_pays(const car_ctx* h) {
+  return h->M >= (h->vec_per_row > 1024 ? 1 : 2) * (int64_t)h->num_sms && h->M <= kMaxPipelineRows;
+}
 
 car_status prepare_branch(car_ctx* h) {
   if (h->branch_ready.load(std::memory_order_acquire)) return CAR_OK;

@@ -499,6 +499,37 @@ def test_rows_past_32_bits_of_elements(car):
     small.check_backward({"dx": x[last], "dresidual": res[last]})
 
 
+def test_more_rows_than_a_pipeline_counts(car):
+    """1025 times the same 2^20 rows of one vector: the same results 1025 times, the first ones those of the formulas."""
+    P, N, W = 2**20, 8, 1
+    M = 1025 * P
+    small = Case(W, 4, N, "bf16", skip=False)
+
+    def repeated(first, seed):
+        rows = randn(gen(seed), (P, N), "bf16")
+        rows[:4] = first
+        return rows.expand(1025, P, N).contiguous().view(M, N)
+
+    def first_rows(t):
+        parts = t.view(1025, P, N)
+        assert all(torch.equal(parts[0], parts[i]) for i in range(1, 1025))
+        return parts[0][:4]
+
+    with car.Car(W, M, N, "bf16") as c:
+        b = car.Branch(small.norm_weight, small.norm_eps)
+        x, res = repeated(small.xs[0], 3), repeated(small.residual, 4)
+        no = torch.empty_like(x)
+        c.reduce_branch_residual_rmsnorm([x], b, res, small.weight, small.eps, res, no, ar_out=x)
+        c.sync()
+        a, h = first_rows(x).clone(), first_rows(res).clone()
+        small.check_forward({"ar": a, "residual_out": h, "norm_out": first_rows(no)})
+        dy = repeated(small.dys[0], 5)
+        c.reduce_branch_residual_rmsnorm_backward([dy], b, x, res, small.weight, small.eps, None, dy, no)
+        c.sync()
+        small.a, small.h = a, h
+        small.check_backward({"dx": first_rows(dy), "dresidual": first_rows(no)})
+
+
 def test_refusals(car):
     W, M, N = 2, 400, 64
     k = Case(W, M, N, "bf16", gate_rows=4)
