@@ -328,9 +328,16 @@ __global__ void __launch_bounds__(256) branch_sums_kernel(const __grid_constant_
   __shared__ float4 s[256];
   // blocks of the two weights, then those of the gate rows
   const int across = (p.vecs + 7) / 8, per_cut = p.gate_blocks ? p.gate_blocks : across;
-  const bool gate = blockIdx.x >= 2u * across;
-  const int rest = (int)blockIdx.x - 2 * across, cut = gate ? rest / per_cut : 0;
-  const int job = gate ? 2 + cut : (int)blockIdx.x / across, block = gate ? rest - cut * per_cut : (int)blockIdx.x - job * across;
+  int job = 0, block = (int)blockIdx.x;
+  if (block >= across) {
+    job = 1;
+    block -= across;
+  }
+  if (job == 1 && block >= across) {
+    block -= across;
+    job = 2 + block / per_cut;
+    block -= (job - 2) * per_cut;
+  }
   const float4 *from, *head;  // entry 0, entry k > 0 at head + k * stride
   float4* out;
   int count;
@@ -352,7 +359,7 @@ __global__ void __launch_bounds__(256) branch_sums_kernel(const __grid_constant_
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!out) return;
-  if (gate && p.gate_blocks)
+  if (job >= 2 && p.gate_blocks)
     sum_partials<32, 2>(s, from, head, stride, count, block, p.vecs, out, scale, p.dtype);
   else
     sum_partials<8, 5>(s, from, head, stride, count, block, p.vecs, out, scale, p.dtype);

@@ -152,7 +152,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       return make_float4(f[0], f[1], f[2], f[3]);
     }
   };
-  const int64_t plane = part.group * rp.vec_per_row * (E / 4) + part.col0 * (E / 4);
+  auto plane = [&] { return (int64_t)part.group * rp.vec_per_row * (E / 4) + part.col0 * (E / 4); };
   // ts holds all rows of gate row b (whole), or those of this span: its first gate row
   // (slot 0) or its last (1)
   auto flush = [&](uint32_t b, bool whole, int slot) {
@@ -163,7 +163,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
     combine(ts, [&](int i, float4 t) {
       if (NORM && p.part_w1) {
         const float4 g = four(p.gate + (int64_t)b * rp.vec_per_row + part.col0, i);
-        float4* to = reinterpret_cast<float4*>(p.part_w1) + plane + i;
+        float4* to = reinterpret_cast<float4*>(p.part_w1) + plane() + i;
         float4 d = slot == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *to;
         d.x = fmaf(g.x, t.x, d.x);
         d.y = fmaf(g.y, t.y, d.y);
@@ -345,8 +345,8 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       consumers_barrier(rp);
     }
   }
-  if (p.part_w) combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane + i] = a; });
-  if (NORM && p.part_w1 && !shared) combine(ts, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w1)[plane + i] = a; });
+  if (p.part_w) combine(dw, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w)[plane() + i] = a; });
+  if (NORM && p.part_w1 && !shared) combine(ts, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w1)[plane() + i] = a; });
 }
 
 template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP>
