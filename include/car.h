@@ -356,7 +356,9 @@ car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inp
  * same data gives the same bits (no float atomics).
  * Errors as the forward's.  Bounded waits that run out are reported by car_sync:
  * as in car_reduce_residual_rmsnorm_backward, and likewise in the forward, where
- * residual_out then holds NaN in those columns if there is a norm_weight. */
+ * residual_out then holds NaN in those columns if there is a norm_weight (and,
+ * where a split row's wait ran out in the pipeline, norm_out of the row that the
+ * CTA had before it, whose sum travels with that exchange). */
 car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const car_branch* branch,
                                                        const void* ar, const void* residual_out, const void* weight,
                                                        float eps, const void* dresidual_out,
@@ -625,12 +627,14 @@ car_status car_tune_fused(car_ctx* h, int kernel, int cluster, int threads, int 
  * then cleared).  Each wait is bounded to about one second: the pipelined
  * fused kernel's waits on its shared-memory barriers (it then stops and
  * leaves its remaining rows unwritten; the pipelines of the 8-bit output and
- * of the backward do the same), and the waits of the fused row kernel (with
- * either output), the backward's row kernel and the Lamport receive for the partials of a split row's other CTAs (each
- * thread waits for itself: the row's norm_out is then NaN in the columns of
- * every thread whose wait ran out, or those columns of the Lamport row are
- * zeroed and the row is reported stale for every rank).  None of these waits
- * runs out unless a CTA of the same launch has stopped making progress. */
+ * of the backward do the same, and those of the branch calls), and the waits of
+ * the fused row kernel (with either output), the backward's row kernel, the
+ * branch calls' kernels and the Lamport receive for the partials of a split
+ * row's other CTAs (each thread waits for itself: the row's norm_out is then
+ * NaN in the columns of every thread whose wait ran out, or those columns of
+ * the Lamport row are zeroed and the row is reported stale for every rank).
+ * None of these waits runs out unless a CTA of the same launch has stopped
+ * making progress. */
 car_status car_sync(car_ctx* h, void* stream);
 
 /* Test hook for the bounded wait of the fused row kernel (CAR_FUSED_ROWS
@@ -650,7 +654,8 @@ car_status car_sync(car_ctx* h, void* stream);
  * unaffected.  The hook acts in the same way on rows that
  * car_reduce_residual_rmsnorm_quant (NaN codes and scales) and
  * car_reduce_residual_rmsnorm_backward (NaN in dx and dweight) split over a
- * cluster.  With cta = -1 (and the other arguments 0) the default returns.
+ * cluster, and on those of the branch calls, whose pipelines split rows too
+ * (NaN as the calls say).  With cta = -1 (and the other arguments 0) the default returns.
  * Errors: CAR_ERR_ARG for values out of range, CAR_ERR_HANDLE. */
 #define CAR_TEST_MAX_DELAY_NS 100000000ull /* 100 ms */
 car_status car_test_delay_partial(car_ctx* h, uint64_t wait_limit_ns, int cta, int64_t row, uint64_t delay_ns);

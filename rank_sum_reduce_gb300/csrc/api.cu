@@ -2,7 +2,8 @@
 // launch shapes, stale-line reports.  Every operation runs in the kernels of
 // reduce.cu, fused.cu, fused_tma.cu, fused_quant.cu, quant_tma.cu,
 // norm_backward.cu, norm_backward_tma.cu, ll128.cu, ll.cu and lamport.cu;
-// nothing here computes results.  (Gradient handles: grads_api.cu.)
+// nothing here computes results.  (Gradient handles: grads_api.cu; what lies
+// between the sum and the residual add: branch_api.cu.)
 //
 // Argument rules follow the problem statement on the pages:
 //   P1 "SGLang Custom AllReduce v1 线程模型和工作原理细节", section

@@ -1,7 +1,7 @@
 // branch.cuh -- what the kernels of a block's branch share (branch_rows.cu,
-// branch_tma.cu, branch_backward.cu, branch_backward_tma.cu, dropout.cu): the
-// dropout's generator, gates, and the sums over a row that is split over warps
-// and a cluster of CTAs.
+// branch_tma.cuh, branch_backward.cu, branch_backward_tma.cuh, dropout.cu): the
+// dropout's generator, and the sums over a row that is split over warps and a
+// cluster of CTAs.
 #pragma once
 
 #include "branch.h"
@@ -17,7 +17,8 @@ namespace {
 // counter's four words are the same for all threads: one product of the first round
 // and one of the second are too.  They are taken out of the loops (DropState); the
 // other 18, at a quarter of the rate of other instructions, are what the generator
-// costs (W = 1, M = 16389, N = 4096 bf16, forward with both norms: see branch_tma.cu).
+// costs (W = 1, M = 16389, N = 4096 bf16 with both norms: forward 81 us without
+// dropout, 104 with it, backward 127 and 147).
 struct DropState {
   uint32_t k0, k1;   // the key
   uint32_t z, y, hi, lo;

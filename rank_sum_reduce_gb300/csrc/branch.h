@@ -57,7 +57,7 @@ cudaError_t launch_branch(int dtype, int W, const RankPtrs& in, const BranchArgs
 struct BranchTeams : TeamShape {  // teams: rows of a tile; grid: CTAs
   int cluster;                    // CTAs that share a row, then with one team each
 };
-// ---- forward, many rows (branch_tma.cu) ----
+// ---- forward, many rows (branch_tma.cu, branch_tma.cuh) ----
 void branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
 // Whether this call's slices and weights fit beside one another.
 bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh);
@@ -110,7 +110,7 @@ cudaError_t branch_backward_resident_groups(int dtype, int W, const FusedShape& 
 cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                    const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
                                    int vec_per_row, const FusedShape& sh, const WaitHook& hook, cudaStream_t s);
-// Backward, many rows (branch_backward_tma.cu).
+// Backward, many rows (branch_backward_tma.cu, branch_backward_tma.cuh).
 void branch_backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
 // Whether this call's slices and sums fit beside one another.
 bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,

@@ -21,15 +21,8 @@ constexpr int kSharedBudget = 222 * 1024;  // ring and what lies beside it; Ring
 // teams' sums.
 bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row, const BranchTeams& sh,
          BranchBackwardTmaParams* p, int* beside) {
-  const bool norm = br.norm_weight != nullptr, own = br.gate && br.gate_span == 0;
-  // A shared gate row is part of the factor where its rows are worth the two barriers
-  // and the L2 latency of making the next one's: W = 1, M = 16384, N = 4096 bf16 with
-  // norms, 1024 rows a gate row, 145 us against 151 with the gate read from L2 for
-  // every row; M = 13332, N = 1160 fp16, 1111 rows, 40.6 against 42.3.
-  const bool folded = br.gate && !own && (br.gate_span == rows || br.gate_span * vec_per_row >= 8192);
-  p->gate_from = !br.gate || folded ? kFromFactor : own ? kFromRing : kFromRows;
-  p->factor = norm || folded;
-  p->shared = br.gate && !own && (g.dgate || g.dnorm_weight);
+  const bool norm = br.norm_weight != nullptr, own = br.gate && br.gate_span == 0, shared = br.gate && !own;
+  p->shared = shared && (g.dgate || g.dnorm_weight);
   RingPlan& rp = p->ring;
   rp.rows = (int)rows;
   rp.row_bytes = vec_per_row * 16;
@@ -39,14 +32,14 @@ bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_
   rp.ranks = W;
   rp.teams = sh.teams;
   rp.team_threads = sh.team_threads;
-  rp.gate_span = br.gate && !own && br.gate_span < rows ? (uint32_t)br.gate_span : 0;  // whatever is asked for: the same bits
+  rp.gate_span = shared && br.gate_span < rows ? (uint32_t)br.gate_span : 0;  // whatever is asked for: the same bits
   const int part_bytes = rp.chunk * 16, slice = sh.teams * part_bytes, floats = dtype == kFP32 ? part_bytes : 2 * part_bytes;
   rp.held = 1;
   p->a_at = p->d_at = p->g_at = 0;
   if (g.ar) p->a_at = slice * rp.held++;
   if (g.dres) p->d_at = slice * rp.held++;
   if (own) p->g_at = slice * rp.held++;
-  p->weight_rows = p->factor ? 2 : 1;
+  p->weight_rows = norm || shared ? 2 : 1;
   *beside = ((sh.teams > 1 ? sh.teams : 0) + p->weight_rows) * floats;
   return branch_ring_fit(kSharedBudget - *beside, &rp);
 }

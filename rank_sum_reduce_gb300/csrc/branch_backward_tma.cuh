@@ -5,8 +5,12 @@
 // and v in turn; the others are read again from their stage, which is held to the
 // row's end.
 //
-// The weight and the factor norm_weight * gate (a gate of many rows) lie in shared
-// memory, in fp32; a gate of few rows comes from L2.
+// The weight and the factor norm_weight * gate row lie in shared memory, in fp32.  The
+// factor is made anew for each gate row: two barriers and an L2 latency, which cost
+// less than the gate read from L2 and another product for every row even where four
+// rows share one (bf16 with norms, W = 1, M = 16384, N = 4096: 16 gate rows 146 us
+// against 166, 4096 of them 238 against 255; W = 4, M = 2048, N = 2048 fp32, a gate
+// row for each row, 59 against 64).
 //
 // Column sums.  A thread sums g u and t (or gate t, where no gate row is shared)
 // over its team's rows in registers.  Where rows share a gate row, tiles end with
@@ -41,10 +45,8 @@ struct BranchBackwardTmaParams {
   float residual_scale;
   float eps, norm_eps;
   float inv_cols;
-  int gate_from;
   uint32_t gate_span;        // rows that share a gate row
   bool shared;               // t is summed by gate row
-  bool factor;               // dz is multiplied by a factor row: norm_weight, a gate of many rows or both
   int weight_rows;           // rows of weights in shared memory, in fp32
   unsigned long long wait_ns;  // as in the row kernels, where CTAs share a row
   unsigned long long delay_ns;
@@ -60,7 +62,6 @@ BackwardTmaFn branch_backward_tma_fp16(int vpt, bool split, bool norm, int gate,
 BackwardTmaFn branch_backward_tma_fp32(int vpt, bool split, bool norm, int gate, bool drop);
 
 namespace {
-
 
 // Slices of a tile: the ranks, h, then those of ar, dres and the gate that there are.
 __device__ __forceinline__ const uint8_t* slice_source(const BranchBackwardTmaParams& p, int q) {
@@ -84,14 +85,14 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
                                         uint8_t* s_factor, float4* s_comb, RingShared& s) {
   constexpr int E = Pack<DT>::kN;
   constexpr bool SHARED = GATE == kGateShared;
-  constexpr bool BRANCHES = E == 8 && ((SHARED && !SPLIT) || (NORM && GATE == kGateOwn));  // else they spill
+  constexpr bool FACTOR = NORM || SHARED;  // dz is multiplied by a factor row: norm_weight, the gate row or both
+  constexpr bool BRANCHES = E == 8 && (SHARED || (NORM && GATE == kGateOwn));  // else they spill
   const RingPlan& rp = p.ring;
   const bool shared = SHARED && p.shared;
   const int T = rp.team_threads, V = part.V, teams = SPLIT ? 1 : rp.teams;
   const ClusterWait peers{part.crank, p.wait_ns, p.err};
   const int team = SPLIT ? 0 : threadIdx.x / T, tid = threadIdx.x - team * T;
   const uint8_t* mine = ring + (size_t)team * rp.row_bytes;  // the row in stage 0
-  const int first = (int)span_start(rp.rows, part.groups, part.group);
   float2 dw[VPT][E / 2], ts[VPT][E / 2];
   bool ok[VPT];
   int col[VPT], at[VPT];
@@ -187,7 +188,6 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
 
   RingReader in(rp, s, p.err);
   uint32_t x = 0;
-  int from = first;
   for (Tiles<SHARED> t(rp, part); t.more(rp);) {
     const int tile = t.row;
     if (team >= t.count(rp)) {
@@ -270,7 +270,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
               for (int e = 0; e < E / 2; e++) u1[e] = mul2(u1[e], qn);
             }
           }
-          if (NORM || (SHARED && p.factor)) weight_at<DT>(p, part, s_rows, 1, col[k], f);
+          if constexpr (FACTOR) weight_at<DT>(p, part, s_rows, 1, col[k], f);
           if constexpr (GATE == kGateOwn) {
             widen2<DT>(lds16(held + p.g_at + at[k]), d);
             if (p.dgate_own) {
@@ -288,12 +288,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
 #pragma unroll
             for (int e = 0; e < E / 2; e++) ts[k][e] = fma2(g[k][e], u1[e], ts[k][e]);
           }
-          if (SHARED && p.gate_from == kFromRows) {
-            widen2<DT>(__ldg(p.gate + (int64_t)((uint32_t)row / p.gate_span) * rp.vec_per_row + part.col0 + col[k]), d);
-#pragma unroll
-            for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], d[e]);
-          }
-          if (NORM || (SHARED && p.factor)) {
+          if constexpr (FACTOR) {
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = mul2(g[k][e], f[e]);  // v
           }
@@ -331,14 +326,15 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
       if (!rp.gate_span) {  // one gate row, tiles in strides
         if (!t.more(rp)) flush(0, part.groups == 1, 0);
       } else if (t.row == cut || !t.more(rp)) {
+        // the span's rows of it are those from `lo` on, or from the span's first row
         const int b = (uint32_t)tile / p.gate_span, lo = b * (int)p.gate_span;
-        flush(b, from == lo && t.row - lo == (int)p.gate_span, from == first ? 0 : 1);
-        from = t.row;
+        const int first = (int)span_start(rp.rows, part.groups, part.group);
+        flush(b, first <= lo && t.row - lo == (int)p.gate_span, first >= lo ? 0 : 1);
       }
     }
     // the next gate row's factor, once every team is through with this one's
-    if (SHARED && rp.gate_span && p.gate_from == kFromFactor && t.row == cut && t.more(rp)) {
-      consumers_barrier(rp);
+    if (SHARED && rp.gate_span && t.row == cut && t.more(rp)) {
+      if (!shared || teams == 1) consumers_barrier(rp);  // else flush() ended with one
       row_to_shared<DT>(NORM ? p.norm_weight + part.col0 : nullptr,
                         p.gate + (int64_t)((uint32_t)t.row / p.gate_span) * rp.vec_per_row + part.col0, V,
                         rp.teams * T, s_factor);
@@ -379,11 +375,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     if (threadIdx.x >= consumers) return;
     const uint4 *weight = p.weight + part.col0, *norm_weight = NORM ? p.norm_weight + part.col0 : nullptr;
     row_to_shared<DT>(weight, nullptr, V, consumers, s_rows);
-    if (NORM || p.factor)
+    if (NORM || GATE == kGateShared)
       row_to_shared<DT>(norm_weight,
-                        p.gate && p.gate_from == kFromFactor
-                            ? p.gate + (int64_t)((uint32_t)first.row / p.gate_span) * rp.vec_per_row + part.col0
-                            : nullptr,
+                        GATE == kGateShared ? p.gate + (int64_t)((uint32_t)first.row / p.gate_span) * rp.vec_per_row + part.col0
+                                            : nullptr,
                         V, consumers, s_factor);
     if (DROP && threadIdx.x == 0) {
       const DropState d = drop_state(p.drop);

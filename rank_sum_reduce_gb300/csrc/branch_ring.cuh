@@ -1,13 +1,14 @@
 // branch_ring.cuh -- what the two pipelines of a block's branch share
-// (branch_tma.cu, branch_backward_tma.cu): tiles of rows streamed through a ring
+// (branch_tma.cuh, branch_backward_tma.cuh): tiles of rows streamed through a ring
 // of shared-memory stages by TMA bulk copies.
 //
-// A CTA takes one contiguous span of rows, in tiles of `teams` consecutive rows
-// (the last one shorter; with a gate that rows share also the last one before a
-// gate row's end).  One bulk copy brings the same slice (a rank, the residual
-// ...) of all rows of a tile; each team of consumer warps owns one of them.
-// Spans and not every so-many-th tile: with fewer rows than a CTA has teams for,
-// the rows are spread over all SMs, and a gate row is cut by few CTAs.
+// A tile is `teams` consecutive rows (the last one fewer).  One bulk copy brings the
+// same slice (a rank, the residual ...) of all rows of a tile; each team of consumer
+// warps owns one of them.  A CTA takes every so-many-th tile; in the backward of a
+// gate whose rows fewer than all rows share, one contiguous span of rows, whose tiles
+// end where a gate row's rows do, so that a gate row is cut by few CTAs.  A row that
+// is split over a cluster is the tile of its CTAs, each with one team and its part of
+// every slice.
 //
 // Slices travel in stages of up to `group`, with one full and one empty barrier
 // each: the ranks' in order, then those that a row needs to its end, which share
@@ -27,8 +28,8 @@ namespace {
 // out at run time (backward, W = 1, M = 16389, N = 4096 bf16 without a norm 145 us
 // against 103).
 enum GateKind : int { kGateNone = 0, kGateShared = 1, kGateOwn = 2 };
-// Where a row's gate comes from: the factor row in shared memory (also: no gate),
-// the ring, L2.
+// Where a row's gate comes from in the forward: a row in shared memory (also: no
+// gate), the ring, L2.
 enum GateFrom : int { kFromFactor = 0, kFromRing = 1, kFromRows = 2 };
 inline int gate_kind(const BranchArgs& br) { return !br.gate ? kGateNone : br.gate_span == 0 ? kGateOwn : kGateShared; }
 

@@ -6,6 +6,13 @@
 //
 // The rows of weights, and a gate of all rows, lie in shared memory as they are, or
 // in L2 where they would leave the ring less than six slices.
+//
+// What bounds it: HBM with two and more ranks and enough rows (W = 4, M = 8191, N =
+// 8192 bf16 with both norms 133 us, 1.04 of a copy's rate; W = 8, M = 3040 81, 0.99;
+// W = 1, M = 16389, N = 4096 81, 0.98); with few rows per SM whole rows (W = 8, M =
+// 512, N = 8192 18.5, 0.80: 3.4 rows per SM); with one rank and dropout instructions
+// (104, 0.76); without a norm W = 1, M = 16389 takes 91 us, longer than with one: the
+// CTAs then ask for more of HBM at once (fewer and smaller stages did not mend it).
 #pragma once
 
 #include "branch_ring.cuh"
@@ -28,7 +35,7 @@ struct BranchTmaParams {
   float inv_cols;
   int gate_from;
   bool packed;              // the rows of weights lie in shared memory
-  uint32_t gate_span;       // rows that share a gate row (kGateRows)
+  uint32_t gate_span;       // rows that share a gate row
   unsigned long long wait_ns;  // as in the row kernels, where CTAs share a row
   unsigned long long delay_ns;
   int64_t delay_row;
@@ -81,7 +88,9 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const Part<SPL
   uint32_t x = 0;
   // With a norm behind the block the second sum of the team's last row travels with the
   // first one of the row after it, so a row passes one barrier instead of two, and its
-  // norm_out is stored then.
+  // norm_out is stored then: bf16 W = 1, M = 1216, N = 16384 (two CTAs a row) 41.3 ->
+  // 35.6 us, M = 1000, N = 32768 (four) 69.9 -> 59.1, M = 8192, N = 1024 16.2 -> 15.2;
+  // with many ranks it costs a little (W = 16, M = 1000, N = 4096 26.8 -> 27.6).
   constexpr bool DEFER = NORM;
   float2 last[DEFER ? VPT : 1][E / 2];
   float last_ss = 0.f;
@@ -139,7 +148,7 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const Part<SPL
       if constexpr (DEFER) v[DEFER ? 1 : 0] = last_ss;
 #pragma unroll
       for (int k = 0; k < VPT; k++) {
-          float2 ss = make_float2(0.f, 0.f);
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) ss = fma2(z[k][e], z[k][e], ss);
         v[0] += ok[k] ? ss.x + ss.y : 0.f;
