@@ -15,7 +15,7 @@ BranchTmaFn pick(int dtype, const BranchTeams& sh, bool norm, int gate, bool dro
   }
 }
 
-constexpr int kSharedBudget = 222 * 1024;  // ring and rows of weights; RingShared is static
+constexpr int kSharedBudget = 224 * 1024;  // ring and rows of weights; RingShared is static
 
 // Where a call's weights lie, and its ring; the bytes beside the ring.
 bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh, BranchTmaParams* p, int* beside) {

@@ -215,7 +215,7 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const Part<SPL
 template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP>
 __global__ void __launch_bounds__(kRingThreads, 1)
     reduce_branch_residual_rmsnorm_tma_kernel(const __grid_constant__ BranchTmaParams p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RingShared s;
   const RingPlan& rp = p.ring;
   const Part<SPLIT> part(rp);
