@@ -21,8 +21,9 @@ LIB_PATH = os.path.join(PKG, "libcar.so")
 SOURCES = ["api.cu", "reduce.cu", "fused.cu", "fused_quant.cu", "fused_tma.cu", "quant_tma.cu", "norm_backward.cu",
            "norm_backward_tma.cu", "branch_rows.cu", "branch_tma.cu", "branch_tma_bf16.cu", "branch_tma_fp16.cu",
            "branch_tma_fp32.cu", "branch_backward.cu", "branch_backward_tma.cu", "branch_backward_tma_bf16.cu",
-           "branch_backward_tma_fp16.cu", "branch_backward_tma_fp32.cu", "dropout.cu", "branch_api.cu", "grads.cu",
-           "grads_api.cu", "ll128.cu", "ll.cu", "ll128_noalloc.cu", "lamport.cu"]
+           "branch_backward_tma_fp16.cu", "branch_backward_tma_fp32.cu", "branch_backward_tma_packed_bf16.cu",
+           "branch_backward_tma_packed_fp16.cu", "dropout.cu", "branch_api.cu", "grads.cu", "grads_api.cu", "ll128.cu",
+           "ll.cu", "ll128_noalloc.cu", "lamport.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                      "-I", INCLUDE, "-I", CSRC]

@@ -6,12 +6,11 @@
 namespace car {
 namespace {
 
-BackwardTmaFn pick(int dtype, const BranchTeams& sh, bool norm, int gate, bool drop) {
-  const bool split = sh.cluster > 1;
+BackwardTmaFn pick(int dtype, bool split, bool norm, int gate, bool drop, bool packed) {
   switch (dtype) {
-    case kBF16: return branch_backward_tma_bf16(sh.vpt, split, norm, gate, drop);
-    case kFP16: return branch_backward_tma_fp16(sh.vpt, split, norm, gate, drop);
-    default: return branch_backward_tma_fp32(sh.vpt, split, norm, gate, drop);
+    case kBF16: return packed ? branch_backward_tma_packed_bf16(split, gate, drop) : branch_backward_tma_bf16(split, norm, gate, drop);
+    case kFP16: return packed ? branch_backward_tma_packed_fp16(split, gate, drop) : branch_backward_tma_fp16(split, norm, gate, drop);
+    default: return branch_backward_tma_fp32(split, norm, gate, drop);
   }
 }
 
@@ -24,7 +23,7 @@ constexpr int kSharedBudget = 224 * 1024;
 // Where a call's weights and slices lie; the bytes beside the ring: the weights and the
 // teams' sums.
 bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row, const BranchTeams& sh,
-         BranchBackwardTmaParams* p, int* beside) {
+         BranchBackwardTmaParams* p, int* beside, bool* packed) {
   const bool norm = br.norm_weight != nullptr, own = br.gate && br.gate_span == 0, shared = br.gate && !own;
   p->shared = shared && (g.dgate || g.dnorm_weight);
   RingPlan& rp = p->ring;
@@ -43,9 +42,19 @@ bool fit(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_
   if (g.ar) p->a_at = slice * rp.held++;
   if (g.dres) p->d_at = slice * rp.held++;
   if (own) p->g_at = slice * rp.held++;
-  p->weight_rows = norm || shared ? 2 : 1;
-  *beside = ((sh.teams > 1 ? sh.teams : 0) + p->weight_rows) * floats;
-  return branch_ring_fit(kSharedBudget - *beside, &rp);
+  // The weights in fp32 where two tiles fit beside them, else packed where that gains a stage (branch_backward_tma.cuh).
+  const bool factor = norm || shared;
+  auto place = [&](bool pack) {
+    *packed = pack;
+    p->factor_at = pack ? part_bytes : floats;
+    p->sums_at = p->factor_at + (!factor ? 0 : pack && !shared ? part_bytes : floats);
+    *beside = p->sums_at + (sh.teams > 1 ? sh.teams : 0) * floats;
+    return branch_ring_fit(kSharedBudget - *beside, &rp);
+  };
+  const bool wide = place(false);
+  if (dtype == kFP32 || !norm || (wide && rp.tile_stages == 1)) return wide;
+  const int stages = wide ? rp.stages : 0;
+  return (place(true) && (rp.tile_stages == 1 || rp.stages > stages)) || place(false);
 }
 
 }  // namespace
@@ -62,13 +71,16 @@ bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const Bran
                               const BranchTeams& sh) {
   BranchBackwardTmaParams p;
   int beside;
-  return fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside);
+  bool packed;
+  return fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside, &packed);
 }
 
 cudaError_t branch_backward_tma_prepare(int dtype, BranchTeams* sh) {
   int clusters = sh->grid / sh->cluster;
-  for (int parts = 0; parts < 12; parts++) {
-    const void* fn = reinterpret_cast<const void*>(pick(dtype, *sh, parts & 1, parts >> 2, parts & 2));
+  for (int parts = 0; parts < 24; parts++) {
+    const bool packed = parts >= 12;  // instances with a norm of the 16-bit types
+    if (packed && (dtype == kFP32 || !(parts & 1))) continue;
+    const void* fn = reinterpret_cast<const void*>(pick(dtype, sh->cluster > 1, parts & 1, parts % 12 >> 2, parts & 2, packed));
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBudget);
     if (e == cudaSuccess && sh->cluster > 1) e = branch_clusters(fn, sh->cluster, kSharedBudget, &clusters);
     if (e != cudaSuccess) return e;
@@ -82,7 +94,8 @@ cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, con
                                        int vec_per_row, const BranchTeams& sh, const WaitHook& hook, cudaStream_t s) {
   BranchBackwardTmaParams p;
   int beside;
-  if (!fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside)) return cudaErrorInvalidValue;
+  bool packed;
+  if (!fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside, &packed)) return cudaErrorInvalidValue;
   const int groups = sh.grid / sh.cluster;
   const bool one = groups == 1, own = br.gate && br.gate_span == 0;
   p.dy = dy;
@@ -112,7 +125,7 @@ cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, con
   p.delay_row = hook.delay_row;
   p.delay_cta = hook.delay_cta;
   const RingPlan& rp = p.ring;
-  cudaError_t e = launch_pdl(pick(dtype, sh, br.norm_weight != nullptr, gate_kind(br), br.drop.active), (unsigned)sh.grid,
+  cudaError_t e = launch_pdl(pick(dtype, sh.cluster > 1, br.norm_weight != nullptr, gate_kind(br), br.drop.active, packed), (unsigned)sh.grid,
                              (unsigned)kRingThreads, (size_t)rp.stages * rp.group * slice_stride(rp) + beside, s, (unsigned)sh.cluster, p);
   return e == cudaSuccess ? launch_branch_sums(br, g, dtype, groups, rows, cols, s) : e;
 }

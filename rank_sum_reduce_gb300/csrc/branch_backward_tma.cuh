@@ -5,8 +5,15 @@
 // and v in turn; the others are read again from their stage, which is held to the
 // row's end.
 //
-// The weight and the factor norm_weight * gate row lie in shared memory, in fp32.  The
-// factor is made anew for each gate row: two barriers and an L2 latency, which cost
+// The weight and the factor norm_weight * gate row lie in shared memory, in fp32, or
+// packed (PACK; not the product) where two tiles do not fit and the ring gets deeper:
+// bf16 with both norms, W = 4, M = 1216, N = 16384 81.5 us in fp32, 67.0 packed; M =
+// 2000, N = 8192 62.2 and 53.4; W = 8, M = 512 29.0 and 27.5.  Where two tiles fit it
+// changes little (W = 1, M = 1216, N = 16384 58.7 and 58.4, with dropout 65.4 and 67.0).
+// In an instance of its own: chosen at run time it spills (W = 1, M = 16389, N = 4096
+// with dropout 147 us against 169).
+//
+// The factor is made anew for each gate row: two barriers and an L2 latency, which cost
 // less than the gate read from L2 and another product for every row even where four
 // rows share one (bf16 with norms, W = 1, M = 16384, N = 4096: 16 gate rows 146 us
 // against 166, 4096 of them 238 against 255; W = 4, M = 2048, N = 2048 fp32, a gate
@@ -47,7 +54,7 @@ struct BranchBackwardTmaParams {
   float inv_cols;
   uint32_t gate_span;        // rows that share a gate row
   bool shared;               // t is summed by gate row
-  int weight_rows;           // rows of weights in shared memory, in fp32
+  int factor_at, sums_at;    // the factor and the teams' sums behind the weight, in bytes
   unsigned long long wait_ns;  // as in the row kernels, where CTAs share a row
   unsigned long long delay_ns;
   int64_t delay_row;
@@ -57,9 +64,12 @@ struct BranchBackwardTmaParams {
 };
 
 using BackwardTmaFn = void (*)(const BranchBackwardTmaParams);
-BackwardTmaFn branch_backward_tma_bf16(int vpt, bool split, bool norm, int gate, bool drop);
-BackwardTmaFn branch_backward_tma_fp16(int vpt, bool split, bool norm, int gate, bool drop);
-BackwardTmaFn branch_backward_tma_fp32(int vpt, bool split, bool norm, int gate, bool drop);
+BackwardTmaFn branch_backward_tma_bf16(bool split, bool norm, int gate, bool drop);
+BackwardTmaFn branch_backward_tma_fp16(bool split, bool norm, int gate, bool drop);
+BackwardTmaFn branch_backward_tma_fp32(bool split, bool norm, int gate, bool drop);
+// With a norm, weights packed.
+BackwardTmaFn branch_backward_tma_packed_bf16(bool split, int gate, bool drop);
+BackwardTmaFn branch_backward_tma_packed_fp16(bool split, int gate, bool drop);
 
 namespace {
 
@@ -73,14 +83,21 @@ __device__ __forceinline__ const uint8_t* slice_source(const BranchBackwardTmaPa
   return reinterpret_cast<const uint8_t*>(p.gate);
 }
 
-// Weight row i (0: weight, 1: factor), vector v of this CTA's.
-template <int DT, bool SPLIT>
-__device__ __forceinline__ void weight_at(const BranchBackwardTmaParams& p, const Part<SPLIT>& part, const uint8_t* s_rows, int i,
-                                          int v, float2 (&f)[Pack<DT>::kN / 2]) {
-  row_from_shared<DT>(s_rows + (size_t)i * p.ring.chunk * Pack<DT>::kN * 4, part.V, v, f);
+// A row of weights in shared memory, and vector v of it.
+template <int DT, bool PACK>
+__device__ __forceinline__ void weights_to_shared(const uint4* __restrict__ row, int vecs, int threads, uint8_t* to) {
+  if constexpr (PACK)
+    for (int v = threadIdx.x; v < vecs; v += threads) reinterpret_cast<uint4*>(to)[v] = __ldg(row + v);
+  else
+    row_to_shared<DT>(row, nullptr, vecs, threads, to);
+}
+template <int DT, bool PACK>
+__device__ __forceinline__ void weight_at(const uint8_t* row, int vecs, int v, float2 (&f)[Pack<DT>::kN / 2]) {
+  if constexpr (PACK) widen2<DT>(lds16(row + 16 * v), f);
+  else row_from_shared<DT>(row, vecs, v, f);
 }
 
-template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP>
+template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP, bool PACK>
 __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const Part<SPLIT>& part, const uint8_t* ring, const uint8_t* s_rows,
                                         uint8_t* s_factor, float4* s_comb, RingShared& s) {
   constexpr int E = Pack<DT>::kN;
@@ -212,7 +229,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
         if (!BRANCHES || ok[k]) {
           float2 hf[E / 2], wf[E / 2], sh = make_float2(0.f, 0.f), sg = sh, sa = sh;
           widen2<DT>(lds16(held + at[k]), hf);
-          weight_at<DT>(p, part, s_rows, 0, col[k], wf);
+          weight_at<DT, PACK>(s_rows, V, col[k], wf);
 #pragma unroll
           for (int e = 0; e < E / 2; e++) {
             sh = fma2(hf[e], hf[e], sh);
@@ -242,7 +259,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
         if (!BRANCHES || ok[k]) {
           float2 hf[E / 2], f[E / 2], d[E / 2];
           widen2<DT>(lds16(held + at[k]), hf);
-          weight_at<DT>(p, part, s_rows, 0, col[k], f);
+          weight_at<DT, PACK>(s_rows, V, col[k], f);
 #pragma unroll
           for (int e = 0; e < E / 2; e++) {
             const float2 u = mul2(hf[e], both(r));
@@ -273,7 +290,7 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
               for (int e = 0; e < E / 2; e++) u1[e] = mul2(u1[e], qn);
             }
           }
-          if constexpr (FACTOR) weight_at<DT>(p, part, s_rows, 1, col[k], f);
+          if constexpr (FACTOR) weight_at<DT, PACK && !SHARED>(s_factor, V, col[k], f);
           if constexpr (GATE == kGateOwn) {
             widen2<DT>(lds16(held + p.g_at + at[k]), d);
             if (p.dgate_own) {
@@ -348,18 +365,17 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
   if (NORM && p.part_w1 && !shared) combine(ts, [&](int i, float4 a) { reinterpret_cast<float4*>(p.part_w1)[plane() + i] = a; });
 }
 
-template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP>
+template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP, bool PACK>
 __global__ void __launch_bounds__(kRingThreads, 1)
     reduce_branch_rmsnorm_backward_tma_kernel(const __grid_constant__ BranchBackwardTmaParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RingShared s;
   const RingPlan& rp = p.ring;
-  constexpr int E = Pack<DT>::kN;
   const Part<SPLIT> part(rp);
   const int consumers = rp.teams * rp.team_threads, V = part.V;
   uint8_t* s_rows = smem + (size_t)rp.stages * rp.group * slice_stride(rp);
-  uint8_t* s_factor = s_rows + (size_t)rp.chunk * E * 4;
-  float4* s_comb = reinterpret_cast<float4*>(s_rows + (size_t)p.weight_rows * rp.chunk * E * 4);
+  uint8_t* s_factor = s_rows + p.factor_at;
+  float4* s_comb = reinterpret_cast<float4*>(s_rows + p.sums_at);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ring_init(rp, s);
   const Tiles<GATE == kGateShared> first(rp, part);
@@ -377,40 +393,40 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     take_registers<true>();
     if (threadIdx.x >= consumers) return;
     const uint4 *weight = p.weight + part.col0, *norm_weight = NORM ? p.norm_weight + part.col0 : nullptr;
-    row_to_shared<DT>(weight, nullptr, V, consumers, s_rows);
-    if (NORM || GATE == kGateShared)
-      row_to_shared<DT>(norm_weight,
-                        GATE == kGateShared ? p.gate + (int64_t)((uint32_t)first.row / p.gate_span) * rp.vec_per_row + part.col0
-                                            : nullptr,
-                        V, consumers, s_factor);
+    weights_to_shared<DT, PACK>(weight, V, consumers, s_rows);
+    if constexpr (GATE == kGateShared)
+      row_to_shared<DT>(norm_weight, p.gate + (int64_t)((uint32_t)first.row / p.gate_span) * rp.vec_per_row + part.col0, V,
+                        consumers, s_factor);
+    else if constexpr (NORM)
+      weights_to_shared<DT, PACK>(norm_weight, V, consumers, s_factor);
     if (DROP && threadIdx.x == 0) {
       const DropState d = drop_state(p.drop);
       s.drop = make_uint4(d.z, d.y, d.hi, d.lo);
     }
     consumers_barrier(rp);
-    consume<DT, VPT, SPLIT, NORM, GATE, DROP>(p, part, smem, s_rows, s_factor, s_comb, s);
+    consume<DT, VPT, SPLIT, NORM, GATE, DROP, PACK>(p, part, smem, s_rows, s_factor, s_comb, s);
   }
 }
 
-template <int DT, int VPT, bool SPLIT, bool NORM, int GATE>
+template <int DT, bool SPLIT, bool NORM, int GATE, bool PACK>
 BackwardTmaFn pick_drop(bool drop) {
-  return drop ? reduce_branch_rmsnorm_backward_tma_kernel<DT, VPT, SPLIT, NORM, GATE, true> : reduce_branch_rmsnorm_backward_tma_kernel<DT, VPT, SPLIT, NORM, GATE, false>;
+  return drop ? reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, SPLIT, NORM, GATE, true, PACK>
+              : reduce_branch_rmsnorm_backward_tma_kernel<DT, 2, SPLIT, NORM, GATE, false, PACK>;
 }
-template <int DT, int VPT, bool SPLIT, bool NORM>
+template <int DT, bool SPLIT, bool NORM, bool PACK>
 BackwardTmaFn pick_gate(int gate, bool drop) {
-  return gate == kGateNone     ? pick_drop<DT, VPT, SPLIT, NORM, kGateNone>(drop)
-         : gate == kGateShared ? pick_drop<DT, VPT, SPLIT, NORM, kGateShared>(drop)
-                               : pick_drop<DT, VPT, SPLIT, NORM, kGateOwn>(drop);
+  return gate == kGateNone     ? pick_drop<DT, SPLIT, NORM, kGateNone, PACK>(drop)
+         : gate == kGateShared ? pick_drop<DT, SPLIT, NORM, kGateShared, PACK>(drop)
+                               : pick_drop<DT, SPLIT, NORM, kGateOwn, PACK>(drop);
 }
-template <int DT, int VPT, bool SPLIT>
-BackwardTmaFn pick_norm(bool norm, int gate, bool drop) {
-  return norm ? pick_gate<DT, VPT, SPLIT, true>(gate, drop) : pick_gate<DT, VPT, SPLIT, false>(gate, drop);
+// The instances of a type, in files of their own: they compile side by side.
+template <int DT, bool NORM, bool PACK>
+BackwardTmaFn pick_split(bool split, int gate, bool drop) {
+  return split ? pick_gate<DT, true, NORM, PACK>(gate, drop) : pick_gate<DT, false, NORM, PACK>(gate, drop);
 }
-// The instance of a type, in a file of its own: they compile side by side.
 template <int DT>
-BackwardTmaFn pick_instance([[maybe_unused]] int vpt, bool split, bool norm, int gate, bool drop) {
-  if (split) return pick_norm<DT, 2, true>(norm, gate, drop);
-  return pick_norm<DT, 2, false>(norm, gate, drop);
+BackwardTmaFn pick_norm(bool split, bool norm, int gate, bool drop) {
+  return norm ? pick_split<DT, true, false>(split, gate, drop) : pick_split<DT, false, false>(split, gate, drop);
 }
 
 }  // namespace

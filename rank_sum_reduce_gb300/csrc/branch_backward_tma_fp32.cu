@@ -1,8 +1,8 @@
-// branch_backward_tma_fp32.cu -- the fp32 instances of branch_backward_tma.cuh.
+// branch_backward_tma_fp32.cu -- instances of the backward pipeline of a block's branch: fp32.
 #include "branch_backward_tma.cuh"
 
 namespace car {
-BackwardTmaFn branch_backward_tma_fp32(int vpt, bool split, bool norm, int gate, bool drop) {
-  return pick_instance<kFP32>(vpt, split, norm, gate, drop);
-}
+
+BackwardTmaFn branch_backward_tma_fp32(bool split, bool norm, int gate, bool drop) { return pick_norm<kFP32>(split, norm, gate, drop); }
+
 }  // namespace car

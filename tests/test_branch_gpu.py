@@ -68,6 +68,10 @@ CASES = [
     (2, 200, 12296, "bf16", True, 0, 1.0, 0.1), (1, 156, 20488, "bf16", True, 2, 1.0, 0.0), (1, 155, 32768, "fp16", True, 155, 1.0, 0.0),
     (3, 154, 16384, "fp32", True, 7, 1.0, 0.1), (2, 2432, 1536, "bf16", True, 1216, 1.0, 0.0), (4, 1824, 648, "fp32", False, 912, 1.0, 0.2),
     (16, 640, 2064, "bf16", True, 5, 1.0, 0.1), (12, 310, 4104, "fp16", True, 1, 1.0, 0.0),
+    # slices that leave the backward's ring room for less than two tiles
+    (4, 400, 8192, "bf16", True, 4, 1.0, 0.1), (8, 320, 8192, "fp16", True, 0, 1.0, 0.1), (6, 200, 16384, "bf16", True, 0, 1.0, 0.1),
+    (4, 200, 16384, "fp16", True, 2, 1.0, 0.1), (4, 170, 16384, "bf16", True, None, 1.0, 0.1), (16, 180, 16384, "fp16", True, 0, 1.0, 0.0),
+    (5, 330, 7000, "bf16", True, 11, 1.0, 0.0), (16, 156, 32768, "bf16", True, 1, 1.0, 0.1),
 ]
 
 
