@@ -277,7 +277,10 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
           if constexpr (DROP) {
             uint32_t bits[E / 2];
             uint4 st;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(st.x), "=r"(st.y), "=r"(st.z), "=r"(st.w) : "r"(smem_addr(&s.drop)));
+            // read here each time, so that it takes no registers between rows
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(st.x), "=r"(st.y), "=r"(st.z), "=r"(st.w)
+                         : "r"(smem_addr(&s.drop)));
             drop_bits<E>(DropState{p.drop.key0, p.drop.key1, st.x, st.y, st.z, st.w}, base + col[k], bits);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = drop2(p.drop, bits[e], g[k][e]);  // dz

@@ -169,7 +169,10 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const Part<SPL
         for (int e = 0; e < E / 2; e++) z[k][e] = mul2(mul2(z[k][e], inv), f[e]);
       }
       if constexpr (GATE != kGateNone) {
-        widen2<DT>(GATE == kGateOwn ? lds16(held + stride + at[k]) : rows ? (EARLY ? gv[EARLY ? k : 0] : __ldg(grow + col[k])) : weight_at(p, part, s_rows, 2, col[k]), f);
+        widen2<DT>(GATE == kGateOwn ? lds16(held + stride + at[k])
+                   : rows           ? (EARLY ? gv[EARLY ? k : 0] : __ldg(grow + col[k]))
+                                    : weight_at(p, part, s_rows, 2, col[k]),
+                   f);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) z[k][e] = mul2(z[k][e], f[e]);
       }
@@ -253,7 +256,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 
 template <int DT, int VPT, bool SPLIT, bool NORM, int GATE>
 BranchTmaFn pick_drop(bool drop) {
-  return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, SPLIT, NORM, GATE, true> : reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, SPLIT, NORM, GATE, false>;
+  return drop ? reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, SPLIT, NORM, GATE, true>
+              : reduce_branch_residual_rmsnorm_tma_kernel<DT, VPT, SPLIT, NORM, GATE, false>;
 }
 template <int DT, int VPT, bool SPLIT, bool NORM>
 BranchTmaFn pick_gate(int gate, bool drop) {
@@ -267,7 +271,7 @@ BranchTmaFn pick_norm(bool norm, int gate, bool drop) {
 }
 // The instance of a type, in a file of its own: they compile side by side.
 template <int DT>
-BranchTmaFn pick_instance([[maybe_unused]] int vpt, bool split, bool norm, int gate, bool drop) {
+BranchTmaFn pick_instance(int vpt, bool split, bool norm, int gate, bool drop) {
   if (split) return pick_norm<DT, 2, true>(norm, gate, drop);
   if (vpt == 3) return pick_norm<DT, 3, false>(norm, gate, drop);
   return pick_norm<DT, 2, false>(norm, gate, drop);
