@@ -410,21 +410,24 @@ def _ptr(t, nbytes: int, what: str, device=None) -> int:
 
 class Dropout:
     """Dropout with probability p (rounded to a multiple of 2^-16) whose mask is a function of seed, offset and the
-    element's place alone (see car_dropout): a backward with the same object sees the forward's mask.  offset_dev, if
+    element's place alone (see car_dropout): a backward with the same values sees the forward's mask.  offset_dev, if
     given, is a CUDA tensor of one 64-bit integer that is added to offset when a kernel runs, so that a captured call can
-    be given another mask at every replay.  seed and offset are any integers, taken mod 2^64, and may be set anew between
-    calls; p and offset_dev are fixed."""
+    be given another mask at every replay.  seed and offset are any integers, taken mod 2^64.  Every field may be set
+    anew between calls, which take what it holds then; the object keeps offset_dev, whose address each call takes."""
 
     def __init__(self, p, seed, offset=0, offset_dev=None):
-        if not 0.0 <= p <= 1.0:
-            raise ValueError(f"p: {p} is not in [0, 1]")
-        if offset_dev is not None:
-            import torch
+        self.struct = car_dropout()
+        self.p, self.seed, self.offset, self.offset_dev = p, seed, offset, offset_dev
 
-            _check_type(offset_dev, (torch.int64, torch.uint64), "offset_dev")
-            _ptr(offset_dev, 8, "offset_dev")
-        self.p, self.offset_dev = p, offset_dev
-        self.struct = car_dropout(p, seed % 2**64, offset % 2**64, offset_dev.data_ptr() if offset_dev is not None else None)
+    @property
+    def p(self) -> float:
+        return self._p
+
+    @p.setter
+    def p(self, value: float):
+        if not 0.0 <= value <= 1.0:
+            raise ValueError(f"p: {value} is not in [0, 1]")
+        self._p = self.struct.p = value
 
     @property
     def seed(self) -> int:
@@ -442,23 +445,69 @@ class Dropout:
     def offset(self, value: int):
         self.struct.offset = value % 2**64
 
+    @property
+    def offset_dev(self):
+        return self._offset_dev
+
+    @offset_dev.setter
+    def offset_dev(self, t):
+        if t is not None:
+            import torch
+
+            _check_type(t, (torch.int64, torch.uint64), "offset_dev")
+            _ptr(t, 8, "offset_dev")
+        self._offset_dev = t
+        self.struct.offset_dev = t.data_ptr() if t is not None else None
+
 
 class Branch:
     """What a block adds to the residual stream (see car_branch): the rank sum, normalised if there is a norm_weight
     [N], times the gate, dropped out; residual_scale multiplies the residual.  gate_rows: 1 for a gate [N] (or [1, N]) of
     all rows, G for one row [G, N] for each of G samples of M / G consecutive rows, 0 for [M, N], a row of its own for
-    every row.  norm_weight and gate are contiguous CUDA tensors of the handle's type (taken as bytes); the object keeps
-    them."""
+    every row.  norm_weight and gate are contiguous CUDA tensors of the handle's type (taken as bytes).  Every field may
+    be set anew between calls, which take what it holds then; the object keeps its tensors, whose addresses each call
+    takes (a parameter's data may be another tensor's by then)."""
 
     def __init__(self, norm_weight=None, norm_eps=1e-6, gate=None, gate_rows=1, residual_scale=1.0, dropout=None):
-        if gate_rows < 0:
-            raise ValueError(f"gate_rows: {gate_rows} is negative")
-        self.norm_weight, self.gate, self.gate_rows, self.dropout = norm_weight, gate, gate_rows, dropout
-        self.struct = car_branch(norm_weight.data_ptr() if norm_weight is not None else None, norm_eps,
-                                 gate.data_ptr() if gate is not None else None, gate_rows, residual_scale,
-                                 ctypes.pointer(dropout.struct) if dropout is not None else None)
+        self.struct = car_branch()
         self.ref = ctypes.byref(self.struct)
-        self._checked = None   # (device, bytes of a row, rows) of the handle that it was last found right for
+        self.norm_weight, self.gate = norm_weight, gate   # their addresses: written into the struct by every call
+        self.norm_eps, self.gate_rows, self.residual_scale, self.dropout = norm_eps, gate_rows, residual_scale, dropout
+
+    @property
+    def norm_eps(self) -> float:
+        return self._norm_eps
+
+    @norm_eps.setter
+    def norm_eps(self, value: float):
+        self._norm_eps = self.struct.norm_eps = value
+
+    @property
+    def gate_rows(self) -> int:
+        return self._gate_rows
+
+    @gate_rows.setter
+    def gate_rows(self, value: int):
+        if value < 0:
+            raise ValueError(f"gate_rows: {value} is negative")
+        self._gate_rows = self.struct.gate_rows = value
+
+    @property
+    def residual_scale(self) -> float:
+        return self._residual_scale
+
+    @residual_scale.setter
+    def residual_scale(self, value: float):
+        self._residual_scale = self.struct.residual_scale = value
+
+    @property
+    def dropout(self):
+        return self._dropout
+
+    @dropout.setter
+    def dropout(self, value):
+        self.struct.dropout = ctypes.pointer(value.struct) if value is not None else None
+        self._dropout = value
 
 
 class Car:
@@ -599,21 +648,19 @@ class Car:
               "car_reduce_residual_rmsnorm_backward")
 
     def _dropout(self, dropout):
-        if dropout.offset_dev is not None:
-            _ptr(dropout.offset_dev, 8, "offset_dev", self.device)
+        """A reference to its struct, with what its tensor is now."""
+        t = dropout._offset_dev
+        if t is not None:
+            dropout.struct.offset_dev = self._p(t, 8, "offset_dev")
         return ctypes.byref(dropout.struct)
 
     def _branch(self, branch):
-        """A reference to its struct, once its tensors have been checked for this handle."""
-        key = (self.device, self._row, self.M)
-        if branch._checked != key:
-            if branch.norm_weight is not None:
-                _ptr(branch.norm_weight, self._row, "norm_weight", self.device)
-            if branch.gate is not None:
-                _ptr(branch.gate, (branch.gate_rows or self.M) * self._row, "gate", self.device)
-            if branch.dropout is not None:
-                self._dropout(branch.dropout)
-            branch._checked = key
+        """A reference to its struct, with what its tensors are now."""
+        w, g, d, s = branch.norm_weight, branch.gate, branch._dropout, branch.struct
+        s.norm_weight = self._p(w, self._row, "norm_weight") if w is not None else None
+        s.gate = self._p(g, (branch._gate_rows or self.M) * self._row, "gate") if g is not None else None
+        if d is not None and d._offset_dev is not None:
+            self._dropout(d)
         return branch.ref
 
     def reduce_dropout(self, xs, dropout, ar_out, stream=None):
@@ -634,10 +681,11 @@ class Car:
 
     def branch_workspace_bytes(self, branch=None) -> int:
         """Of the backward's workspace; depends on whether rows share a row of the branch's gate."""
-        key = branch.gate_rows if branch is not None and branch.gate is not None else 0
+        key = branch._gate_rows if branch is not None and branch.gate is not None else 0
         need = self._branch_sizes.get(key)
         if need is None:
-            need = self._branch_sizes[key] = car_branch_workspace_bytes(self.h, branch.struct if branch is not None else None)
+            gate = 16 if key else None   # any: a shared gate, or none
+            need = self._branch_sizes[key] = car_branch_workspace_bytes(self.h, car_branch(gate=gate, gate_rows=key))
         return need
 
     def reduce_branch_residual_rmsnorm_backward(self, dnorm, branch, ar, residual_out, weight, eps, dresidual_out, dx,
@@ -647,7 +695,8 @@ class Car:
         every gradient but dx may be None.  dweight and dnorm_weight are fp32 [N]; dgate is fp32 like the gate, or with
         gate_rows 0 [M, N] of the handle's type.  workspace (branch_workspace_bytes(branch) bytes) is taken from torch's
         allocator on the current stream when one is needed and none is given."""
-        f32, D, N, shared = _types()[2], self.D, self.N, branch.gate_rows > 0
+        f32, D, N, rows = _types()[2], self.D, self.N, branch._gate_rows
+        shared = rows > 0
         for t, what in ((dweight, "dweight"), (dnorm_weight, "dnorm_weight"), (dgate if shared else None, "dgate")):
             if t is not None:
                 _check_type(t, f32, what)
@@ -662,7 +711,7 @@ class Car:
             workspace = torch.empty(need, dtype=torch.uint8, device=dx.device)
         a, h, w, dro, out, dr, dw, dw1, dg, ws = self._ptrs(
             (ar, residual_out, weight, dresidual_out, dx, dresidual, dweight, dnorm_weight, dgate, workspace if need else None),
-            (D, D, self._row, D, D, D, 4 * N, 4 * N, 4 * N * branch.gate_rows if shared else D, need),
+            (D, D, self._row, D, D, D, 4 * N, 4 * N, 4 * N * rows if shared else D, need),
             ("ar", "residual_out", "weight", "dresidual_out", "dx", "dresidual", "dweight", "dnorm_weight", "dgate", "workspace"))
         check(_lib.car_reduce_branch_residual_rmsnorm_backward(
             self.h, _table(self._ranks(dnorm, D, "dnorm")), self._branch(branch), a, h, w, eps, dro,
