@@ -75,11 +75,10 @@ _SIGS = {
     "car_reduce_residual_rmsnorm_backward": (ctypes.c_int, [_vp, _pvp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp,
                                                             _vp]),
     "car_backward_workspace_bytes": (ctypes.c_size_t, [_vp]),
-    "car_reduce_dropout": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_dropout), _vp, _vp]),
-    "car_reduce_branch_residual_rmsnorm": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_branch), _vp, _vp, ctypes.c_float,
-                                                          _vp, _vp, _vp, _vp]),
-    "car_reduce_branch_residual_rmsnorm_backward": (ctypes.c_int, [_vp, _pvp, ctypes.POINTER(car_branch), _vp, _vp, _vp,
-                                                                   ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "car_reduce_dropout": (ctypes.c_int, [_vp, _pvp, _vp, _vp, _vp]),
+    "car_reduce_branch_residual_rmsnorm": (ctypes.c_int, [_vp, _pvp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "car_reduce_branch_residual_rmsnorm_backward": (ctypes.c_int, [_vp, _pvp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp,
+                                                                   _vp, _vp]),
     "car_branch_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.POINTER(car_branch)]),
     "car_grads_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64),
                                         ctypes.POINTER(ctypes.c_int), _pvp, _pvp, _ctx_pp]),
@@ -393,6 +392,20 @@ def _check_type(t, allowed, what: str) -> None:
         raise ValueError(f"{what}: {t.dtype}, the call needs {' or '.join(str(d) for d in allowed)}")
 
 
+@functools.lru_cache(maxsize=1)
+def _own_types():
+    """The handles' types, by name."""
+    import torch
+
+    return {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def _check_own_type(t, own, what: str) -> None:
+    """A tensor of a handle's type: that, or raw bytes in one of whole numbers."""
+    if t.dtype is not own and (t.is_floating_point() or t.is_complex()):
+        raise ValueError(f"{what}: {t.dtype}, the handle's type is {own}")
+
+
 def _ptr(t, nbytes: int, what: str, device=None) -> int:
     """Device pointer of a tensor the library will read or write `nbytes` of:
     it must be a contiguous CUDA tensor at least that large, on `device` when
@@ -417,6 +430,7 @@ class Dropout:
 
     def __init__(self, p, seed, offset=0, offset_dev=None):
         self.struct = car_dropout()
+        self.address = ctypes.addressof(self.struct)   # quicker to pass than a reference
         self.p, self.seed, self.offset, self.offset_dev = p, seed, offset, offset_dev
 
     @property
@@ -464,13 +478,14 @@ class Branch:
     """What a block adds to the residual stream (see car_branch): the rank sum, normalised if there is a norm_weight
     [N], times the gate, dropped out; residual_scale multiplies the residual.  gate_rows: 1 for a gate [N] (or [1, N]) of
     all rows, G for one row [G, N] for each of G samples of M / G consecutive rows, 0 for [M, N], a row of its own for
-    every row.  norm_weight and gate are contiguous CUDA tensors of the handle's type (taken as bytes).  Every field may
-    be set anew between calls, which take what it holds then; the object keeps its tensors, whose addresses each call
-    takes (a parameter's data may be another tensor's by then)."""
+    every row.  norm_weight and gate are contiguous CUDA tensors of the handle's type (or its bytes in a type of whole
+    numbers) with just so many values: a gate of more rows than gate_rows is refused.  Every field may be set anew
+    between calls, which take what it holds then; the object keeps its tensors, whose addresses each call takes (a
+    parameter's data may be another tensor's by then)."""
 
     def __init__(self, norm_weight=None, norm_eps=1e-6, gate=None, gate_rows=1, residual_scale=1.0, dropout=None):
         self.struct = car_branch()
-        self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
         self.norm_weight, self.gate = norm_weight, gate   # their addresses: written into the struct by every call
         self.norm_eps, self.gate_rows, self.residual_scale, self.dropout = norm_eps, gate_rows, residual_scale, dropout
 
@@ -529,6 +544,7 @@ class Car:
         self._quant_sizes = [(D, Nw, D, M * N, car_quant_scale_bytes(h, k), D, D) for k in range(len(SCALE_CODE))]
         self._backward_sizes = None   # found when first asked for
         self._branch_sizes = {}       # the same, by gate_rows
+        self._type = _own_types()[dtype]
         import torch
 
         self.device = torch.cuda.current_device()
@@ -648,20 +664,40 @@ class Car:
               "car_reduce_residual_rmsnorm_backward")
 
     def _dropout(self, dropout):
-        """A reference to its struct, with what its tensor is now."""
+        """Address of its struct, with what its tensor is now."""
         t = dropout._offset_dev
         if t is not None:
             dropout.struct.offset_dev = self._p(t, 8, "offset_dev")
-        return ctypes.byref(dropout.struct)
+        return dropout.address
 
     def _branch(self, branch):
-        """A reference to its struct, with what its tensors are now."""
-        w, g, d, s = branch.norm_weight, branch.gate, branch._dropout, branch.struct
-        s.norm_weight = self._p(w, self._row, "norm_weight") if w is not None else None
-        s.gate = self._p(g, (branch._gate_rows or self.M) * self._row, "gate") if g is not None else None
+        """Address of its struct, with what its tensors are now."""
+        w, g, d, s, own, dev = branch.norm_weight, branch.gate, branch._dropout, branch.struct, self._type, self.device
+        if w is None:
+            s.norm_weight = None
+        elif w.dtype is own and w.nbytes == self._row and w.get_device() == dev and w.is_contiguous():
+            s.norm_weight = w.data_ptr()
+        else:
+            s.norm_weight = self._values(w, self._row, "norm_weight")
+        if g is None:
+            s.gate = None
+        else:
+            n = (branch._gate_rows or self.M) * self._row
+            if g.dtype is own and g.nbytes == n and g.get_device() == dev and g.is_contiguous():
+                s.gate = g.data_ptr()
+            else:
+                s.gate = self._values(g, n, "gate")
         if d is not None and d._offset_dev is not None:
             self._dropout(d)
-        return branch.ref
+        return branch.address
+
+    def _values(self, t, nbytes: int, what: str) -> int:
+        """Address of a tensor of the handle's type that holds just that much."""
+        _check_own_type(t, self._type, what)
+        at = self._p(t, nbytes, what)
+        if t.nbytes != nbytes:
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, the call takes {nbytes // t.element_size()} values")
+        return at
 
     def reduce_dropout(self, xs, dropout, ar_out, stream=None):
         """ar_out = dropout of the rank sum; its gradient is the same call on the gradient's rank contributions."""
@@ -673,6 +709,8 @@ class Car:
         """reduce_residual_rmsnorm with a Branch between the rank sum and the residual add.  ar_out: the rank sum, which
         the backward needs behind a norm and for the gate's gradient."""
         D = self.D
+        if weight.dtype is not self._type:
+            _check_own_type(weight, self._type, "weight")
         res, w, ro, no, ar = self._ptrs((residual, weight, residual_out, norm_out, ar_out), (D, self._row, D, D, D),
                                         ("residual", "weight", "residual_out", "norm_out", "ar_out"))
         check(_lib.car_reduce_branch_residual_rmsnorm(self.h, _table(self._ranks(xs, D, "inputs")),
@@ -698,8 +736,13 @@ class Car:
         f32, D, N, rows = _types()[2], self.D, self.N, branch._gate_rows
         shared = rows > 0
         for t, what in ((dweight, "dweight"), (dnorm_weight, "dnorm_weight"), (dgate if shared else None, "dgate")):
-            if t is not None:
+            if t is not None and t.dtype not in f32:
                 _check_type(t, f32, what)
+        own = self._type
+        if weight.dtype is not own:
+            _check_own_type(weight, own, "weight")
+        if not shared and dgate is not None and dgate.dtype is not own:
+            _check_own_type(dgate, own, "dgate")
         need = 0
         if dweight is not None or dnorm_weight is not None or (dgate is not None and shared):
             need = self.branch_workspace_bytes(branch)

@@ -49,6 +49,9 @@ class Tensor:
     def is_floating_point(self):
         return self.dtype.is_floating_point
 
+    def is_complex(self):
+        return self.dtype.is_complex
+
 
 @pytest.fixture
 def calls(car, monkeypatch):
@@ -57,14 +60,14 @@ def calls(car, monkeypatch):
 
     def record(name, at):
         def call(*args):
-            b = car.car_branch.from_buffer_copy(args[at]._obj)
+            b = car.car_branch.from_buffer_copy(car.car_branch.from_address(args[at]))
             d = car.car_dropout.from_buffer_copy(b.dropout.contents) if b.dropout else None
             seen.append(types.SimpleNamespace(name=name, branch=b, dropout=d, args=args))
             return car.CAR_OK
         return call
 
     def dropout(*args):
-        seen.append(types.SimpleNamespace(name="dropout", dropout=car.car_dropout.from_buffer_copy(args[2]._obj)))
+        seen.append(types.SimpleNamespace(name="dropout", dropout=car.car_dropout.from_buffer_copy(car.car_dropout.from_address(args[2]))))
         return car.CAR_OK
 
     monkeypatch.setattr(car, "_lib", types.SimpleNamespace(
@@ -76,19 +79,20 @@ def calls(car, monkeypatch):
 def handle(car):
     c = object.__new__(car.Car)
     c.h, c.W, c.M, c.N, c.dtype, c.device = None, W, M, N, "bf16", 0
-    c.D, c._row, c._branch_sizes = M * N * 2, N * 2, {}
+    c.D, c._row, c._branch_sizes, c._type = M * N * 2, N * 2, {}, torch.bfloat16
     return c
 
 
-def forward(c, b):
+def forward(c, b, weight=None):
     t = [Tensor(0x1000 * (i + 1), (M, N)) for i in range(W + 3)]
-    c.reduce_branch_residual_rmsnorm(t[:W], b, t[W], Tensor(0x100, (N,)), 1e-6, t[W + 1], t[W + 2], stream=0)
+    weight = weight or Tensor(0x100, (N,))
+    c.reduce_branch_residual_rmsnorm(t[:W], b, t[W], weight, 1e-6, t[W + 1], t[W + 2], stream=0)
 
 
-def backward(c, b, dgate=None, dnorm_weight=None):
+def backward(c, b, weight=None, dgate=None):
     t = [Tensor(0x1000 * (i + 1), (M, N)) for i in range(W + 3)]
-    c.reduce_branch_residual_rmsnorm_backward(t[:W], b, t[W], t[W + 1], Tensor(0x100, (N,)), 1e-6, None, t[W + 2],
-                                              dgate=dgate, dnorm_weight=dnorm_weight, stream=0)
+    weight = weight or Tensor(0x100, (N,))
+    c.reduce_branch_residual_rmsnorm_backward(t[:W], b, t[W], t[W + 1], weight, 1e-6, None, t[W + 2], dgate=dgate, stream=0)
 
 
 def test_the_struct_is_the_c_one(car):
@@ -188,3 +192,45 @@ def test_two_branches_share_a_dropout(car, calls):
     for b in bs:
         forward(c, b)
     assert [(k.dropout.seed, k.dropout.offset) for k in calls] == [(9, 10)] * 2
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+@pytest.mark.parametrize("name", ["norm_weight", "gate", "weight"])
+@pytest.mark.parametrize("bad", [torch.float32, torch.float64, torch.float16, torch.float8_e4m3fn, torch.complex64])
+def test_weights_and_gates_of_another_type_are_refused(car, calls, call, name, bad):
+    """Large enough all the same: an fp32 weight holds a bf16 one's bytes twice."""
+    t = Tensor(0x300, (4 * N,) if bad.itemsize == 1 else (N,), bad)
+    with pytest.raises(ValueError, match=f"{name}: {bad}"):
+        call(handle(car), car.Branch(**({name: t} if name != "weight" else {})), **({} if name != "weight" else {name: t}))
+    assert not calls
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+@pytest.mark.parametrize("name,gate_rows,shape", [("gate", 1, (M, N)), ("gate", 1, (2, N)), ("gate", 4, (M, N)), ("gate", 2, (1, N)),
+                                                  ("gate", 0, (M + 1, N)), ("norm_weight", 1, (M, N)), ("norm_weight", 1, (N + 8,)),
+                                                  ("norm_weight", 1, (0,))])
+def test_weights_and_gates_of_another_size_are_refused(car, calls, call, name, gate_rows, shape):
+    """A gate of a row for every row is not a gate of all rows, whatever its first row holds."""
+    with pytest.raises(ValueError, match=name):
+        call(handle(car), car.Branch(gate_rows=gate_rows, **{name: Tensor(0x300, shape)}))
+    assert not calls
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+@pytest.mark.parametrize("gate_rows,shape", [(1, (N,)), (1, (1, N)), (4, (4, N)), (4, (4, 1, N)), (4, (4 * N,)), (0, (M, N)),
+                                             (0, (2, M // 2, N)), (M, (M, N))])
+def test_every_shape_of_as_many_values_is_taken(car, calls, call, gate_rows, shape):
+    call(handle(car), car.Branch(gate=Tensor(0x300, shape), gate_rows=gate_rows))
+    raw = Tensor(0x300, (torch.Size(shape).numel() * 2,), torch.uint8)     # the same as bytes
+    call(handle(car), car.Branch(gate=raw, gate_rows=gate_rows, norm_weight=Tensor(0x200, (N,), torch.int16)))
+    assert [k.branch.gate for k in calls] == [0x300] * 2
+
+
+@pytest.mark.parametrize("bad", [torch.float32, torch.float16, torch.float64])
+def test_a_gradient_of_another_type_for_a_gate_of_each_rows_own_is_refused(car, calls, bad):
+    c, b = handle(car), car.Branch(gate=Tensor(0x300, (M, N)), gate_rows=0)
+    with pytest.raises(ValueError, match=f"dgate: {bad}"):
+        backward(c, b, dgate=Tensor(0x800, (M, N), bad))
+    assert not calls
+    backward(c, b, dgate=Tensor(0x800, (M, N)))
+    assert len(calls) == 1
