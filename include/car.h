@@ -353,7 +353,9 @@ car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inp
  * dx and dresidual may each equal one of dnorm[k], ar, residual_out and
  * dresidual_out; every other overlap of an output with an output, an input or
  * the workspace is refused.  All outputs are overwritten.  The same call on the
- * same data gives the same bits (no float atomics).
+ * same data gives the same bits (no float atomics).  Sums over very many rows
+ * take several launches, of at most 512 rows for each thread, so that an fp32 sum's
+ * error does not grow with the rows.
  * Errors as the forward's.  Bounded waits that run out are reported by car_sync:
  * as in car_reduce_residual_rmsnorm_backward, and likewise in the forward, where
  * residual_out then holds NaN in those columns if there is a norm_weight (and,

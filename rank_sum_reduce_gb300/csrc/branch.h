@@ -110,7 +110,8 @@ cudaError_t branch_backward_resident_groups(int dtype, int W, const FusedShape& 
 cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                    const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
                                    int vec_per_row, const FusedShape& sh, const WaitHook& hook, cudaStream_t s);
-// Backward, many rows (branch_backward_tma.cu, branch_backward_tma.cuh).
+// Backward, many rows (branch_backward_tma.cu, branch_backward_tma.cuh): a launch, or
+// several of a part of the rows each.
 void branch_backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
 // Whether this call's slices and sums fit beside one another.
 bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
@@ -119,8 +120,9 @@ cudaError_t branch_backward_tma_prepare(int dtype, BranchTeams* sh);
 cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                        const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
                                        int vec_per_row, const BranchTeams& sh, const WaitHook& hook, cudaStream_t s);
-// The sum of the groups' partials, behind either backward kernel.
+// The sum of the groups' partials, behind either backward kernel; add, add_gate: to what
+// dweight and dnorm_weight, or dgate, hold.
 cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, int dtype, int groups, int64_t rows,
-                               int64_t cols, cudaStream_t s);
+                               int64_t cols, bool add, bool add_gate, cudaStream_t s);
 
 }  // namespace car

@@ -96,7 +96,7 @@ car_status prepare_dropout(car_ctx* h) {
 bool one_vector(int, int vpt) { return vpt == 1; }
 int branch_threads(int, int) { return kBranchThreads; }
 
-// The pipelines count rows in 32 bits, a grid's step past the last one included.
+// The forward's pipeline counts rows in 32 bits, a grid's step past the last one included.
 constexpr int64_t kMaxPipelineRows = 1 << 30;
 
 // When the forward's pipeline is faster than its row kernel: from so many rows per SM
@@ -132,7 +132,7 @@ bool branch_pipeline_pays(const car_ctx* h) {
 // 1.24.  Rank counts that the row kernel is not compiled for: W = 3 and 6, N = 4096 0.98,
 // 1.20, 1.45, 1.65.
 bool branch_backward_pipeline_pays(const car_ctx* h) {
-  return h->M >= (h->vec_per_row > 1024 ? 1 : 2) * (int64_t)h->num_sms && h->M <= kMaxPipelineRows;
+  return h->M >= (h->vec_per_row > 1024 ? 1 : 2) * (int64_t)h->num_sms;
 }
 
 car_status prepare_branch(car_ctx* h) {

@@ -267,6 +267,7 @@ struct BranchSums {
   int dtype;
   int groups;
   int vecs;                 // float4 in a row
+  bool add, add_gate;       // to what the launch before this one left
   int gate_blocks;          // blocks that sum a gate row, 0: as many as the others
   struct Cut {
     uint32_t row;         // of the gate
@@ -285,7 +286,7 @@ __device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i) 
 // Block `block` of a job: float4 columns VECS * block .. of out.
 template <int VECS, int BATCH>
 __device__ __forceinline__ void sum_partials(float4 (&s)[256], const float4* from, const float4* head, int64_t stride, int count,
-                                             int block, int vecs, float4* out, const void* scale, int dtype) {
+                                             int block, int vecs, float4* out, bool add, const void* scale, int dtype) {
   constexpr int PARTS = 256 / VECS;
   const int col = threadIdx.x % VECS, part = threadIdx.x / VECS;
   const int v = block * VECS + col;
@@ -320,7 +321,11 @@ __device__ __forceinline__ void sum_partials(float4 (&s)[256], const float4* fro
       for (int k = 0; k < n; k++) sum[k] += sum[k + n];
     }
     const int64_t i = (int64_t)block * 4 * VECS + threadIdx.x;
-    if (i < 4 * (int64_t)vecs) reinterpret_cast<float*>(out)[i] = scale ? sum[0] * weight_at(scale, dtype, i) : sum[0];
+    if (i < 4 * (int64_t)vecs) {
+      float* to = reinterpret_cast<float*>(out) + i;
+      const float v = scale ? sum[0] * weight_at(scale, dtype, i) : sum[0];
+      *to = add ? *to + v : v;
+    }
   }
 }
 
@@ -360,9 +365,9 @@ __global__ void __launch_bounds__(256) branch_sums_kernel(const __grid_constant_
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!out) return;
   if (job >= 2 && p.gate_blocks)
-    sum_partials<32, 2>(s, from, head, stride, count, block, p.vecs, out, scale, p.dtype);
+    sum_partials<32, 2>(s, from, head, stride, count, block, p.vecs, out, p.add_gate, scale, p.dtype);
   else
-    sum_partials<8, 5>(s, from, head, stride, count, block, p.vecs, out, scale, p.dtype);
+    sum_partials<8, 5>(s, from, head, stride, count, block, p.vecs, out, job < 2 ? p.add : p.add_gate, scale, p.dtype);
 }
 
 using BackwardFn = void (*)(const BranchBackwardParams);
@@ -457,11 +462,11 @@ cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const B
   p.delay_cta = hook.delay_cta;
   cudaError_t e = launch_pdl(pick(dtype, W, br.norm_weight != nullptr), (unsigned)(sh.groups * sh.cluster), (unsigned)sh.threads,
                              0, s, (unsigned)sh.cluster, p);
-  return e == cudaSuccess ? launch_branch_sums(br, g, dtype, sh.groups, rows, cols, s) : e;
+  return e == cudaSuccess ? launch_branch_sums(br, g, dtype, sh.groups, rows, cols, false, false, s) : e;
 }
 
 cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, int dtype, int groups, int64_t rows,
-                               int64_t cols, cudaStream_t s) {
+                               int64_t cols, bool add, bool add_gate, cudaStream_t s) {
   const bool gates = br.gate && br.gate_span > 0 && g.dgate;
   if (groups == 1 || (!g.dweight && !g.dnorm_weight && !gates)) return cudaSuccess;
   BranchSums p;
@@ -475,6 +480,8 @@ cudaError_t launch_branch_sums(const BranchArgs& br, const BranchGradArgs& g, in
   p.norm_weight = br.norm_weight;
   p.dtype = dtype;
   p.groups = groups;
+  p.add = add;
+  p.add_gate = add_gate;
   p.vecs = (int)(cols / 4);
   // gate rows that an inner border of the spans cuts, each once
   int cuts = 0, most = 0;  // and the partials of any of them

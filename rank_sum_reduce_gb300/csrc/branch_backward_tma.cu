@@ -89,9 +89,12 @@ cudaError_t branch_backward_tma_prepare(int dtype, BranchTeams* sh) {
   return cudaSuccess;
 }
 
-cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
-                                       const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
-                                       int vec_per_row, const BranchTeams& sh, const WaitHook& hook, cudaStream_t s) {
+namespace {
+
+// One launch, of `rows` rows from row `row0` of the problem on, and the sum of its partials.
+cudaError_t launch_part(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g, const void* weight,
+                        float eps, unsigned int* err, int64_t row0, int64_t rows, int64_t cols, int vec_per_row,
+                        const BranchTeams& sh, const WaitHook& hook, bool add, bool add_gate, cudaStream_t s) {
   BranchBackwardTmaParams p;
   int beside;
   bool packed;
@@ -119,15 +122,70 @@ cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, con
   p.eps = eps;
   p.norm_eps = br.norm_eps;
   p.inv_cols = 1.f / (float)cols;
+  p.first_vec = (uint32_t)(row0 * vec_per_row);
   p.gate_span = (uint32_t)std::max<int64_t>(br.gate_span, 1);
   p.wait_ns = hook.wait_ns;
   p.delay_ns = hook.delay_ns;
-  p.delay_row = hook.delay_row;
+  p.delay_row = hook.delay_row - row0;
   p.delay_cta = hook.delay_cta;
   const RingPlan& rp = p.ring;
   cudaError_t e = launch_pdl(pick(dtype, sh.cluster > 1, br.norm_weight != nullptr, gate_kind(br), br.drop.active, packed), (unsigned)sh.grid,
                              (unsigned)kRingThreads, (size_t)rp.stages * rp.group * slice_stride(rp) + beside, s, (unsigned)sh.cluster, p);
-  return e == cudaSuccess ? launch_branch_sums(br, g, dtype, groups, rows, cols, s) : e;
+  return e == cudaSuccess ? launch_branch_sums(br, g, dtype, groups, rows, cols, add, add_gate, s) : e;
+}
+
+// Rows that a thread adds to its column sums one after the other.  Each addition rounds to
+// fp32, and where the terms are alike all of them the same way: off by up to 2^-13 for 2^12
+// rows, and 1.6 % were measured for 3.5 million (N = 8, 1025 * 2^20 rows).  So
+// a launch has at most this many for each thread, and the next one adds to what it left: N =
+// 8192 has two from 77,825 rows on, N = 4096 from twice as many.  Fewer of them would mean
+// more launches where rows are short (N = 8: 1.2 million rows a launch).
+constexpr int64_t kSumRows = 512;
+// The pipelines count rows in 32 bits, a grid's step past the last one included.
+constexpr int64_t kMaxRows = 1 << 30;
+
+}  // namespace
+
+cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
+                                       const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,
+                                       int vec_per_row, const BranchTeams& sh, const WaitHook& hook, cudaStream_t s) {
+  const bool own = br.gate && br.gate_span == 0, shared = br.gate && !own;
+  const bool sums = g.dweight || g.dnorm_weight || (shared && g.dgate);
+  const int64_t groups = sh.grid / sh.cluster;
+  const int64_t most = sums && groups > 1 ? kSumRows * sh.teams * groups : kMaxRows;
+  // Parts of whole gate rows, with which tiles end (gate rows of fewer rows than there are
+  // teams leave teams out), or where one has more rows than a launch, of that one's; of nearly
+  // the same size, so that each has rows for every CTA.
+  const bool cut = shared && br.gate_span > most;
+  const int64_t unit = shared && !cut ? br.gate_span : 1, outer = cut ? rows / br.gate_span : 1, units = rows / outer / unit;
+  const int64_t tiles = sums && shared && !cut ? (unit + sh.teams - 1) / sh.teams : 0;  // of a gate row
+  const int64_t per = std::max<int64_t>(tiles ? most / sh.teams / tiles : most / unit, 1);
+  const int parts = (int)((units + per - 1) / per);
+  const size_t row_bytes = (size_t)vec_per_row * 16;
+  auto at = [](auto* p, size_t bytes) { return p ? reinterpret_cast<decltype(p)>(reinterpret_cast<uintptr_t>(p) + bytes) : p; };
+  for (int64_t o = 0; o < outer; o++) {
+    for (int i = 0; i < parts; i++) {
+      const int64_t row0 = o * (rows / outer) + unit * span_start(units, parts, i);
+      const int64_t n = unit * (span_start(units, parts, i + 1) - span_start(units, parts, i));
+      const size_t off = (size_t)row0 * row_bytes, gate_row = shared ? (size_t)(row0 / br.gate_span) : 0;
+      RankPtrs d = dy;
+      for (int r = 0; r < W; r++) d.p[r] = at(dy.p[r], off);
+      BranchArgs b = br;
+      b.gate = at(br.gate, own ? off : gate_row * row_bytes);
+      if (cut) b.gate_span = n;
+      BranchGradArgs to = g;
+      to.ar = at(g.ar, off);
+      to.h = at(g.h, off);
+      to.dres = at(g.dres, off);
+      to.dx = at(g.dx, off);
+      to.dresidual = at(g.dresidual, off);
+      to.dgate = at(g.dgate, own ? off : gate_row * (size_t)cols * sizeof(float));
+      const cudaError_t e = launch_part(dtype, W, d, b, to, weight, eps, err, row0, n, cols, vec_per_row, sh, hook, row0 > 0,
+                                        cut && i > 0, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
 }
 
 }  // namespace car

@@ -53,6 +53,7 @@ struct BranchBackwardTmaParams {
   float eps, norm_eps;
   float inv_cols;
   uint32_t gate_span;        // rows that share a gate row
+  uint32_t first_vec;        // of the [M, N] problem's vectors: this launch's first
   bool shared;               // t is summed by gate row
   int factor_at, sums_at;    // the factor and the teams' sums behind the weight, in bytes
   unsigned long long wait_ns;  // as in the row kernels, where CTAs share a row
@@ -277,11 +278,13 @@ __device__ __forceinline__ void consume(const BranchBackwardTmaParams& p, const 
           if constexpr (DROP) {
             uint32_t bits[E / 2];
             uint4 st;
+            uint32_t first;
             // read here each time, so that it takes no registers between rows
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(st.x), "=r"(st.y), "=r"(st.z), "=r"(st.w)
                          : "r"(smem_addr(&s.drop)));
-            drop_bits<E>(DropState{p.drop.key0, p.drop.key1, st.x, st.y, st.z, st.w}, base + col[k], bits);
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(first) : "r"(smem_addr(&s.first_vec)));
+            drop_bits<E>(DropState{p.drop.key0, p.drop.key1, st.x, st.y, st.z, st.w}, first + (uint32_t)base + (uint32_t)col[k], bits);
 #pragma unroll
             for (int e = 0; e < E / 2; e++) g[k][e] = drop2(p.drop, bits[e], g[k][e]);  // dz
           }
@@ -405,6 +408,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     if (DROP && threadIdx.x == 0) {
       const DropState d = drop_state(p.drop);
       s.drop = make_uint4(d.z, d.y, d.hi, d.lo);
+      s.first_vec = p.first_vec;
     }
     consumers_barrier(rp);
     consume<DT, VPT, SPLIT, NORM, GATE, DROP, PACK>(p, part, smem, s_rows, s_factor, s_comb, s);

@@ -100,7 +100,8 @@ __host__ __device__ inline uint32_t slice_stride(const RingPlan& p) { return (ui
 struct RingShared {
   uint64_t full[kMaxRingStages], empty[kMaxRingStages];
   RowSums cluster;          // its exchange, where CTAs share a row
-  uint4 drop;               // the generator's state, where registers are short
+  uint4 drop;               // the generator's state, where registers are short,
+  uint32_t first_vec;       // and the launch's first vector of the [M, N] problem
   float4 warp[48];          // [teams][2][3][warps of a team, in fours]: a team has 512 / teams threads at most
   int abort;
 };
