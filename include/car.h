@@ -356,11 +356,19 @@ car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inp
  * same data gives the same bits (no float atomics).  Sums over very many rows
  * take several launches, of at most 512 rows for each thread, so that an fp32 sum's
  * error does not grow with the rows.
- * Errors as the forward's.  Bounded waits that run out are reported by car_sync:
- * as in car_reduce_residual_rmsnorm_backward, and likewise in the forward, where
- * residual_out then holds NaN in those columns if there is a norm_weight (and,
- * where a split row's wait ran out in the pipeline, norm_out of the row that the
- * CTA had before it, whose sum travels with that exchange). */
+ * Errors as the forward's.  Bounded waits that run out are reported by car_sync.
+ * Where a row's statistic did not arrive it is NaN, in the columns of the threads
+ * that gave up, and so is what is computed from it:
+ *   forward: residual_out there if there is a norm_weight, but for dropped
+ *     elements, which are residual_scale * residual as ever; norm_out there, or in
+ *     the whole row where residual_out has a NaN.  (Where the pipeline splits rows,
+ *     a row's second statistic travels with the first one of the row that the CTA
+ *     has next, and norm_out of both is NaN.)
+ *   backward: dresidual there; dx there, or in the whole row with a norm_weight,
+ *     but for dropped elements without one, which are 0 as ever; the sums over
+ *     rows that such values enter.
+ * The pipelines leave rows unwritten instead where what runs out is the wait for
+ * a row's data, and the sums over rows are of no use. */
 car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* const* dnorm, const car_branch* branch,
                                                        const void* ar, const void* residual_out, const void* weight,
                                                        float eps, const void* dresidual_out,
