@@ -59,8 +59,6 @@ struct BranchTeams : TeamShape {  // teams: rows of a tile; grid: CTAs
 };
 // ---- forward, many rows (branch_tma.cu, branch_tma.cuh) ----
 void branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
-// Whether this call's slices and weights fit beside one another.
-bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh);
 // Allows the instances their shared memory, and fits the grid to the clusters that can be resident.
 cudaError_t branch_tma_prepare(int dtype, BranchTeams* sh);
 cudaError_t launch_branch_tma(int dtype, int W, const RankPtrs& in, const BranchArgs& br, const void* residual,
@@ -113,9 +111,6 @@ cudaError_t launch_branch_backward(int dtype, int W, const RankPtrs& dy, const B
 // Backward, many rows (branch_backward_tma.cu, branch_backward_tma.cuh): a launch, or
 // several of a part of the rows each.
 void branch_backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out);
-// Whether this call's slices and sums fit beside one another.
-bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
-                              const BranchTeams& sh);
 cudaError_t branch_backward_tma_prepare(int dtype, BranchTeams* sh);
 cudaError_t launch_branch_backward_tma(int dtype, int W, const RankPtrs& dy, const BranchArgs& br, const BranchGradArgs& g,
                                        const void* weight, float eps, unsigned int* err, int64_t rows, int64_t cols,

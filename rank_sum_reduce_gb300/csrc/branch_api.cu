@@ -173,10 +173,9 @@ car_status prepare_branch_backward(car_ctx* h) {
   return CAR_OK;
 }
 
-// CTAs (or clusters) of whichever kernel a call runs: which one is, where the
-// pipeline pays, found at the call (its parts decide whether a row fits).
+// CTAs (or clusters) of the backward's kernel.
 int workspace_groups(const car_ctx* h) {
-  return std::max(h->branch_backward.groups, h->branch_backward_pipeline ? h->branch_backward_tma.grid / h->branch_backward_tma.cluster : 0);
+  return h->branch_backward_pipeline ? h->branch_backward_tma.grid / h->branch_backward_tma.cluster : h->branch_backward.groups;
 }
 
 }  // namespace
@@ -229,7 +228,7 @@ car_status car_reduce_branch_residual_rmsnorm(car_ctx* h, const void* const* inp
   if ((st = prepare_branch(h)) != CAR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (h->branch_pipeline && branch_tma_fits(h->W, b, h->M, h->vec_per_row, h->branch_tma))
+  if (h->branch_pipeline)
     e = launch_branch_tma(h->dtype, h->W, tbl, b, residual, weight, eps, residual_out, norm_out, ar_out, h->d_err, h->M, h->N,
                           h->vec_per_row, h->branch_tma, h->hook, s);
   else
@@ -301,7 +300,7 @@ car_status car_reduce_branch_residual_rmsnorm_backward(car_ctx* h, const void* c
   g.workspace = static_cast<float*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (h->branch_backward_pipeline && branch_backward_tma_fits(h->dtype, h->W, b, g, h->M, h->vec_per_row, h->branch_backward_tma))
+  if (h->branch_backward_pipeline)
     e = launch_branch_backward_tma(h->dtype, h->W, tbl, b, g, weight, eps, h->d_err, h->M, h->N, h->vec_per_row,
                                    h->branch_backward_tma, h->hook, s);
   else

@@ -67,14 +67,6 @@ void branch_backward_tma_shape(int64_t rows, int vec_per_row, int num_sms, Branc
   branch_teams(rows, vec_per_row, num_sms, vec_per_row > 2048 ? 4 : vec_per_row > 1024 ? 2 : 1, 2, out);
 }
 
-bool branch_backward_tma_fits(int dtype, int W, const BranchArgs& br, const BranchGradArgs& g, int64_t rows, int vec_per_row,
-                              const BranchTeams& sh) {
-  BranchBackwardTmaParams p;
-  int beside;
-  bool packed;
-  return fit(dtype, W, br, g, rows, vec_per_row, sh, &p, &beside, &packed);
-}
-
 cudaError_t branch_backward_tma_prepare(int dtype, BranchTeams* sh) {
   int clusters = sh->grid / sh->cluster;
   for (int parts = 0; parts < 24; parts++) {

@@ -153,7 +153,7 @@ __device__ __forceinline__ void ring_produce(const RingPlan& p, const Part<SPLIT
     const uint32_t bytes = (uint32_t)t.count(p) * (uint32_t)part.V * 16u;
     for (int q = 0; q < slices;) {
       // a stage ends with the ranks unless all of the tile is one
-      const int n = slices <= p.group ? slices : q < p.ranks ? min(p.group, p.ranks - q) : slices - q;
+      const int n = p.tile_stages == 1 ? slices : q < p.ranks ? min(p.group, p.ranks - q) : slices - q;
       if (issued >= (uint32_t)S && !mbar_try_wait(&s.empty[place], phase ^ 1u) && !wait_suspended(&s.empty[place], phase ^ 1u, &s.abort)) {
         ok = false;
         break;

@@ -17,7 +17,8 @@ BranchTmaFn pick(int dtype, const BranchTeams& sh, bool norm, int gate, bool dro
 
 constexpr int kSharedBudget = 224 * 1024;  // ring and rows of weights; RingShared is static
 
-// Where a call's weights lie, and its ring; the bytes beside the ring.
+// A call's ring, and the bytes beside it: the weight, norm_weight, and a gate of all rows
+// behind both.  At least six slices fit beside them, whatever the call's parts.
 bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh, BranchTmaParams* p, int* beside) {
   const bool column = br.gate && br.gate_span == rows;
   p->gate_from = !br.gate || column ? kFromFactor : br.gate_span == 0 ? kFromRing : kFromRows;
@@ -33,10 +34,7 @@ bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const Branc
   rp.team_threads = sh.team_threads;
   rp.gate_span = 0;
   *beside = (column ? 3 : br.norm_weight ? 2 : 1) * rp.chunk * 16;
-  p->packed = branch_ring_fit(kSharedBudget - *beside, &rp) && rp.stages * rp.group >= 6;
-  if (p->packed) return true;
-  *beside = 0;
-  return branch_ring_fit(kSharedBudget, &rp);
+  return branch_ring_fit(kSharedBudget - *beside, &rp);
 }
 
 }  // namespace
@@ -100,12 +98,6 @@ cudaError_t branch_clusters(const void* fn, int cluster, int smem, int* clusters
 void branch_tma_shape(int64_t rows, int vec_per_row, int num_sms, BranchTeams* out) {
   const int cluster = vec_per_row > 2048 ? 4 : vec_per_row > 1536 ? 2 : 1;
   branch_teams(rows, vec_per_row, num_sms, cluster, cluster > 1 ? 2 : team_vectors(vec_per_row, 2, 3), out);
-}
-
-bool branch_tma_fits(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const BranchTeams& sh) {
-  BranchTmaParams p;
-  int beside;
-  return fit(W, br, rows, vec_per_row, sh, &p, &beside);
 }
 
 cudaError_t branch_tma_prepare(int dtype, BranchTeams* sh) {

@@ -4,8 +4,7 @@
 // over both of its exchanges, and while one team of warps waits for its row's
 // sums another folds.
 //
-// The rows of weights, and a gate of all rows, lie in shared memory as they are, or
-// in L2 where they would leave the ring less than six slices.
+// The rows of weights, and a gate of all rows, lie in shared memory as they are.
 //
 // What bounds it: HBM with two and more ranks and enough rows (W = 4, M = 8191, N =
 // 8192 bf16 with both norms 133 us, 1.04 of a copy's rate; W = 8, M = 3040 81, 0.99;
@@ -34,7 +33,6 @@ struct BranchTmaParams {
   float eps, norm_eps;
   float inv_cols;
   int gate_from;
-  bool packed;              // the rows of weights lie in shared memory
   uint32_t gate_span;       // rows that share a gate row
   unsigned long long wait_ns;  // as in the row kernels, where CTAs share a row
   unsigned long long delay_ns;
@@ -57,10 +55,8 @@ __device__ __forceinline__ const uint8_t* slice_source(const BranchTmaParams& p,
 
 // Weight row i (0: weight, 1: norm_weight, 2: a gate of all rows), vector v of this
 // CTA's.
-template <bool SPLIT>
-__device__ __forceinline__ uint4 weight_at(const BranchTmaParams& p, const Part<SPLIT>& part, const uint8_t* s_rows, int i, int v) {
-  return p.packed ? lds16(s_rows + 16 * (i * p.ring.chunk + v))
-                  : __ldg((i == 0 ? p.weight : i == 1 ? p.norm_weight : p.gate) + part.col0 + v);
+__device__ __forceinline__ uint4 weight_at(const BranchTmaParams& p, const uint8_t* s_rows, int i, int v) {
+  return lds16(s_rows + 16 * (i * p.ring.chunk + v));
 }
 
 template <int DT, int VPT, bool SPLIT, bool NORM, int GATE, bool DROP>
@@ -100,7 +96,7 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const Part<SPL
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       float2 f[E / 2];
-      widen2<DT>(weight_at(p, part, s_rows, 0, col[k]), f);
+      widen2<DT>(weight_at(p, s_rows, 0, col[k]), f);
 #pragma unroll
       for (int e = 0; e < E / 2; e++) f[e] = mul2(mul2(h[k][e], r), f[e]);
       if (ok[k]) st16(p.norm_out + base + col[k], narrow2<DT>(f));
@@ -164,14 +160,18 @@ __device__ __forceinline__ void consume(const BranchTmaParams& p, const Part<SPL
     for (int k = 0; k < VPT; k++) {
       float2 f[E / 2];
       if constexpr (NORM) {
-        widen2<DT>(weight_at(p, part, s_rows, 1, col[k]), f);
+        // keeps the vectors' arithmetic apart: all at once the CTAs' stores come in
+        // bursts where HBM is the limit (W = 1, M = 16389, N = 4096 84.4 us, with this
+        // 82.0; N = 5120, W = 2 with one gate row and dropout 76.7 and 72.2)
+        __syncwarp();
+        widen2<DT>(weight_at(p, s_rows, 1, col[k]), f);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) z[k][e] = mul2(mul2(z[k][e], inv), f[e]);
       }
       if constexpr (GATE != kGateNone) {
         widen2<DT>(GATE == kGateOwn ? lds16(held + stride + at[k])
                    : rows           ? (EARLY ? gv[EARLY ? k : 0] : __ldg(grow + col[k]))
-                                    : weight_at(p, part, s_rows, 2, col[k]),
+                                    : weight_at(p, s_rows, 2, col[k]),
                    f);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) z[k][e] = mul2(z[k][e], f[e]);
@@ -241,15 +241,13 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   } else {
     take_registers<true>();
     if (threadIdx.x >= consumers) return;
-    if (p.packed) {
-      uint4* to = reinterpret_cast<uint4*>(s_rows);
-      for (int v = threadIdx.x; v < V; v += consumers) {
-        to[v] = __ldg(p.weight + part.col0 + v);
-        if constexpr (NORM) to[rp.chunk + v] = __ldg(p.norm_weight + part.col0 + v);
-        if (GATE && p.gate && p.gate_from == kFromFactor) to[2 * rp.chunk + v] = __ldg(p.gate + part.col0 + v);
-      }
-      consumers_barrier(rp);
+    uint4* to = reinterpret_cast<uint4*>(s_rows);
+    for (int v = threadIdx.x; v < V; v += consumers) {
+      to[v] = __ldg(p.weight + part.col0 + v);
+      if constexpr (NORM) to[rp.chunk + v] = __ldg(p.norm_weight + part.col0 + v);
+      if (GATE && p.gate && p.gate_from == kFromFactor) to[2 * rp.chunk + v] = __ldg(p.gate + part.col0 + v);
     }
+    consumers_barrier(rp);
     consume<DT, VPT, SPLIT, NORM, GATE, DROP>(p, part, smem, s_rows, s);
   }
 }
