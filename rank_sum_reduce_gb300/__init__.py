@@ -433,6 +433,9 @@ class Dropout:
         self.address = ctypes.addressof(self.struct)   # quicker to pass than a reference
         self.p, self.seed, self.offset, self.offset_dev = p, seed, offset, offset_dev
 
+    def __copy__(self):   # with a struct of its own
+        return Dropout(self.p, self.seed, self.offset, self.offset_dev)
+
     @property
     def p(self) -> float:
         return self._p
@@ -488,6 +491,9 @@ class Branch:
         self.address = ctypes.addressof(self.struct)
         self.norm_weight, self.gate = norm_weight, gate   # their addresses: written into the struct by every call
         self.norm_eps, self.gate_rows, self.residual_scale, self.dropout = norm_eps, gate_rows, residual_scale, dropout
+
+    def __copy__(self):   # with a struct of its own; its tensors and dropout are the same objects
+        return Branch(self.norm_weight, self.norm_eps, self.gate, self.gate_rows, self.residual_scale, self.dropout)
 
     @property
     def norm_eps(self) -> float:

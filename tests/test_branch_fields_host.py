@@ -1,6 +1,7 @@
 """What a call makes of a Branch's and a Dropout's fields, which may change between calls: it takes their tensors' addresses,
 their sizes and the gate's rows as they are then.  The library is replaced by a recorder and tensors by stand-ins, so nothing
 here needs a device or launches a kernel."""
+import copy
 import ctypes
 import types
 
@@ -234,3 +235,23 @@ def test_a_gradient_of_another_type_for_a_gate_of_each_rows_own_is_refused(car, 
     assert not calls
     backward(c, b, dgate=Tensor(0x800, (M, N)))
     assert len(calls) == 1
+
+
+def test_copies_have_fields_of_their_own(car, calls):
+    """What is set on a copy does not reach the first one's calls: not its number of gate rows either, by which its gradient
+    is sized."""
+    c, d = handle(car), car.Dropout(0.5, 1, 2)
+    b = car.Branch(Tensor(0x200, (N,)), 1e-5, Tensor(0x300, (N,)), residual_scale=0.5, dropout=d)
+    other, e = copy.copy(b), copy.copy(d)
+    other.gate, other.gate_rows, other.residual_scale, other.norm_eps = Tensor(0x500, (4, N)), 4, 2.0, 0.25
+    other.dropout, e.seed, e.p = None, 9, 0.25
+    backward(c, b, dgate=Tensor(0x800, (N,), torch.float32))
+    s = calls[-1].branch
+    assert (s.norm_weight, s.gate, s.gate_rows, s.residual_scale, calls[-1].dropout.seed) == (0x200, 0x300, 1, 0.5, 1)
+    assert abs(s.norm_eps - 1e-5) < 1e-11 and (d.seed, d.p) == (1, 0.5) and (e.seed, e.offset, e.p) == (9, 2, 0.25)
+    backward(c, other, dgate=Tensor(0x800, (4, N), torch.float32))
+    s = calls[-1].branch
+    assert (s.norm_weight, s.gate, s.gate_rows, s.residual_scale, calls[-1].dropout) == (0x200, 0x500, 4, 2.0, None)
+    for x in (b, d):
+        with pytest.raises(ValueError):   # addresses are this process's
+            copy.deepcopy(x)
