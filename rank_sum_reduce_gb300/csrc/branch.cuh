@@ -17,8 +17,8 @@ namespace {
 // counter's four words are the same for all threads: one product of the first round
 // and one of the second are too.  They are taken out of the loops (DropState); the
 // other 18, at a quarter of the rate of other instructions, are what the generator
-// costs (W = 1, M = 16389, N = 4096 bf16 with both norms: forward 81 us without
-// dropout, 104 with it, backward 127 and 147).
+// costs (W = 1, M = 16389, N = 4096 bf16 with both norms: forward 82 us without
+// dropout, 97 with it, backward 126 and 148).
 struct DropState {
   uint32_t k0, k1;   // the key
   uint32_t z, y, hi, lo;

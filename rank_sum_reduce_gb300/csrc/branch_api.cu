@@ -102,17 +102,23 @@ constexpr int64_t kMaxPipelineRows = 1 << 30;
 // When the forward's pipeline is faster than its row kernel: from so many rows per SM
 // on.  Measured on GB300 (graph replay over cold inputs, bf16 with both norms; the row
 // kernel's time divided by the pipeline's, over M = 152, 304, 608, 1216).
-//  * Rows of more than 1024 vectors, which the row kernel has to split: N = 11072 1.30
-//    to 2.57, N = 16384 0.99 to 1.92, N = 32768 1.05 to 2.3; at M = 80 0.81 to 1.37.
+//  * Rows of more than 1024 vectors, which the row kernel has to split: N = 11072 1.40
+//    to 2.60, N = 16384 1.07 to 1.91, N = 32768 1.14 to 2.32; at M = 80 0.92 to 1.42.
 //  * Shorter ones: the more ranks and the shorter the row, the longer the row kernel,
-//    with several CTAs per SM, keeps up.  W = 1: N = 1024 0.78, 1.02, 1.20, 1.25; N =
-//    4096 0.89, 0.85, 0.94, 1.08; N = 8192 0.91, 1.00, 1.12, 1.32.  W = 4: N = 1024
-//    0.79, 0.95, 0.94, 1.10; N = 4096 0.75, 1.01, 1.20, 1.32; N = 8192 1.08, 1.18,
-//    1.41, 1.67.  W = 8: N = 1024 0.79, 0.86, 0.88, 0.96 (M = 2432 1.12); N = 2048
-//    0.83, 0.81, 0.91, 1.11; N = 4096 0.73, 0.90, 1.11, 1.16; N = 8192 0.96, 1.10,
-//    1.27, 1.39.  W = 16: N = 2048 0.67, 0.73, 0.95, 1.00; N = 4096 0.69, 0.96, 1.03,
-//    1.01; N = 8192 0.95, 1.06, 1.09, 1.12.  fp32 at the same vectors per row, and
+//    with several CTAs per SM, keeps up.  W = 1: N = 1024 0.77, 1.02, 1.21, 1.30; N =
+//    4096 0.88, 0.88, 0.97, 1.11; N = 8192 0.93, 1.04, 1.16, 1.38.  W = 4: N = 1024
+//    0.77, 0.97, 0.96, 1.10; N = 4096 0.76, 1.03, 1.22, 1.33; N = 8192 1.10, 1.19,
+//    1.42, 1.70.  W = 8: N = 1024 0.81, 0.86, 0.90, 0.98 (M = 2432 1.14); N = 2048
+//    0.86, 0.81, 0.92, 1.11; N = 4096 0.72, 0.92, 1.14, 1.16; N = 8192 0.97, 1.16,
+//    1.32, 1.42.  W = 16: N = 2048 0.68, 0.74, 0.96, 1.03; N = 4096 0.70, 0.98, 1.04,
+//    1.04; N = 8192 0.97, 1.08, 1.09, 1.10.  fp32 at the same vectors per row, and
 //    without the first norm, within 0.1 of these.
+//  * Rank counts that the row kernel is not compiled for keep to the rule of those
+//    beside them, though its instance for 16 ranks falls behind earlier: W = 3: N =
+//    4096 0.82, 1.11, 1.38, 1.58 (M = 228 5.2 us against 4.4), N = 8192 1.20, 1.40,
+//    1.65, 2.13 (M = 80 5.9 against 4.4); W = 6: N = 4096 0.76, 0.99, 1.21, 1.43; N =
+//    8192 1.05, 1.23, 1.57, 1.72.  At M = 228 the rule also leaves a little with W = 4:
+//    N = 4096 5.1 us against 4.7.
 bool branch_pipeline_pays(const car_ctx* h) {
   const int V = h->vec_per_row, W = h->W;
   double rows;  // per SM
@@ -124,13 +130,17 @@ bool branch_pipeline_pays(const car_ctx* h) {
   return (double)h->M >= rows * h->num_sms && h->M <= kMaxPipelineRows;
 }
 
-// The same for the backward (M = 152, 304, 608, 1216): W = 1: N = 1024 0.84, 1.05,
-// 1.31, 1.47; N = 4096 0.83, 1.08, 1.17, 1.34; N = 8192 1.00, 1.14, 1.37, 1.70.  W = 8:
-// N = 1024 0.77, 1.00, 1.24, 1.15; N = 4096 0.84, 0.93, 1.10, 1.12; N = 8192 0.92, 1.04,
-// 1.13, 1.29.  W = 16: N = 4096 0.90, 1.09, 1.21, 1.21.  More than 1024 vectors: N =
-// 11072 1.33 to 2.13, N = 16384 1.09 to 1.82, N = 32768 1.20 to 2.26; at M = 80 0.84 to
-// 1.24.  Rank counts that the row kernel is not compiled for: W = 3 and 6, N = 4096 0.98,
-// 1.20, 1.45, 1.65.
+// The same for the backward (M = 152, 228, 304, 608, 1216): W = 1: N = 1024 0.89, 1.10,
+// 1.16, 1.41, 1.55; N = 4096 0.84, 1.11, 1.11, 1.18, 1.39; N = 8192 1.01, 0.99, 1.16, 1.40,
+// 1.72.  W = 4: N = 2048 0.92, 1.18, 1.12, 1.07, 1.18; N = 8192 0.98, 0.98, 1.15, 1.41,
+// 1.60.  W = 8: N = 1024 0.77, 1.06, 1.08, 1.35, 1.20; N = 4096 0.86, 0.97, 0.95, 1.11,
+// 1.12; N = 8192 0.97, 0.93, 1.10, 1.19, 1.33.  W = 16: N = 4096 0.96, 1.11, 1.10, 1.21,
+// 1.25.  More than 1024 vectors (M = 152, 304, 1216): N = 11072 1.30 to 2.10, N = 16384
+// 1.15 to 1.81, N = 32768 1.32 to 2.25; at M = 80 0.89 to 1.23.  Rank counts that the row
+// kernel is not compiled for (M = 152, 228, 304, 608): W = 3, N = 4096 1.01, 1.29, 1.25,
+// 1.51; W = 6, N = 2048 1.07, 1.35, 1.33, 1.33.  So rows of up to 512 vectors would gain
+// from one and a half rows per SM on already (W = 1, N = 2048, M = 228 7.4 us against 6.3;
+// W = 3, N = 4096 12.0 against 9.2).
 bool branch_backward_pipeline_pays(const car_ctx* h) {
   return h->M >= (h->vec_per_row > 1024 ? 1 : 2) * (int64_t)h->num_sms;
 }

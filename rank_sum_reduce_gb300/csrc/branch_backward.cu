@@ -22,7 +22,13 @@
 // partials go to the caller's workspace and branch_sums_kernel adds them in a
 // fixed order (no float atomics: the same call gives the same bits).
 // Roofline: HBM, (W + 5) * 16 bytes per vector with norm and skip gradient, 2
-// more for a gate of each row's own, and the partials (L2).
+// more for a gate of each row's own, and the partials (L2).  With a row for each CTA
+// the partials are more than the data: 16 bytes per element in fp32, written and
+// read again, where one rank in bf16 moves 12 (W = 1, M = 152, N = 8192 with norms:
+// 11.9 us, floor 2.2, of which the second kernel is 5.8 by itself; W = 4 12.7, floor
+// 3.3).  512 threads leave a thread 128 registers: the instances of the 16-bit types
+// with a norm spill 36 to 60 bytes for two and four ranks (bf16 one, too), 180 to 240
+// for sixteen and for rank counts without an instance of their own.
 #include <algorithm>
 
 #include "branch.cuh"

@@ -96,7 +96,8 @@ struct Tiles {
 // Bytes of a slice's place in a stage.
 __host__ __device__ inline uint32_t slice_stride(const RingPlan& p) { return (uint32_t)p.teams * (uint32_t)p.chunk * 16u; }
 
-// Barriers and small arrays (static shared memory).
+// Barriers and small arrays (static shared memory).  Row statistics are sums times a
+// rounded 1 / N here, where the row kernels divide: a rounding more.
 struct RingShared {
   uint64_t full[kMaxRingStages], empty[kMaxRingStages];
   RowSums cluster;          // its exchange, where CTAs share a row

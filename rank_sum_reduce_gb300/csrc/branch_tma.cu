@@ -40,8 +40,9 @@ bool fit(int W, const BranchArgs& br, int64_t rows, int vec_per_row, const Branc
 }  // namespace
 
 // A whole tile per stage where two fit, three stages or 96 KB at most: deeper rings
-// ask for more of HBM at once than helps (W = 1, M = 16389, N = 4096 bf16 without a
-// norm 83 to 85 us with 64 to 96 KB in flight per SM, 94 with 192).  Else stages of
+// ask for more of HBM at once than helps (W = 1, M = 16389, N = 4096 bf16 with both
+// norms, 64, 96 and 128 KB in flight per SM: 88, 84 and 92 us; without 83, 91 and 93; own
+// gates, M = 8192, 51, 54 and 57; N = 8192, M = 4000 46, 41 and 41).  Else stages of
 // two slices, as many as there is room for (W = 8, M = 512, N = 8192 with both norms
 // 20.9, 19.6 and 18.3 us with three, four and five of them; stages of one slice 20.5
 // with eight, of four 20.4 with three).

@@ -7,11 +7,13 @@
 // The rows of weights, and a gate of all rows, lie in shared memory as they are.
 //
 // What bounds it: HBM with two and more ranks and enough rows (W = 4, M = 8191, N =
-// 8192 bf16 with both norms 133 us, 1.04 of a copy's rate; W = 8, M = 3040 81, 0.99;
-// W = 1, M = 16389, N = 4096 81, 0.98); with few rows per SM whole rows (W = 8, M =
-// 512, N = 8192 18.5, 0.80: 3.4 rows per SM); with one rank and dropout instructions
-// (104, 0.76); without a norm W = 1, M = 16389 takes 91 us, longer than with one: the
-// CTAs then ask for more of HBM at once (fewer and smaller stages did not mend it).
+// 8192 bf16 with both norms 133 us, 1.04 of a copy's rate; W = 8, M = 3040 83, 0.97; own
+// gates W = 2, M = 8192, N = 4096 64, 0.92; W = 1, M = 16389, N = 4096 82, 0.97); with
+// few rows per SM whole rows (W = 8, M = 512, N = 8192 17.4, 0.85: 3.4 rows per SM); rows
+// that CTAs share, with one rank, their exchanges (N = 16384, M = 1216 32-33, 0.72): a
+// CTA has one team then, so nothing folds while the row waits; with one rank and dropout
+// instructions (97, 0.82); without a norm W = 1, M = 16389 takes 91 us, longer than with
+// one: the CTAs then ask for more of HBM at once (see branch_ring_fit).
 #pragma once
 
 #include "branch_ring.cuh"
