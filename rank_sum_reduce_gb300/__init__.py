@@ -488,12 +488,30 @@ class Branch:
 
     def __init__(self, norm_weight=None, norm_eps=1e-6, gate=None, gate_rows=1, residual_scale=1.0, dropout=None):
         self.struct = car_branch()
-        self.address = ctypes.addressof(self.struct)
-        self.norm_weight, self.gate = norm_weight, gate   # their addresses: written into the struct by every call
+        self.ref, self.address = ctypes.byref(self.struct), ctypes.addressof(self.struct)
+        self.norm_weight, self.gate = norm_weight, gate   # their addresses: written into the struct here and by every call
         self.norm_eps, self.gate_rows, self.residual_scale, self.dropout = norm_eps, gate_rows, residual_scale, dropout
 
     def __copy__(self):   # with a struct of its own; its tensors and dropout are the same objects
         return Branch(self.norm_weight, self.norm_eps, self.gate, self.gate_rows, self.residual_scale, self.dropout)
+
+    @property
+    def norm_weight(self):
+        return self._norm_weight
+
+    @norm_weight.setter
+    def norm_weight(self, t):
+        self.struct.norm_weight = t.data_ptr() if t is not None else None
+        self._norm_weight = t
+
+    @property
+    def gate(self):
+        return self._gate
+
+    @gate.setter
+    def gate(self, t):
+        self.struct.gate = t.data_ptr() if t is not None else None
+        self._gate = t
 
     @property
     def norm_eps(self) -> float:
@@ -678,7 +696,7 @@ class Car:
 
     def _branch(self, branch):
         """Address of its struct, with what its tensors are now."""
-        w, g, d, s, own, dev = branch.norm_weight, branch.gate, branch._dropout, branch.struct, self._type, self.device
+        w, g, d, s, own, dev = branch._norm_weight, branch._gate, branch._dropout, branch.struct, self._type, self.device
         if w is None:
             s.norm_weight = None
         elif w.dtype is own and w.nbytes == self._row and w.get_device() == dev and w.is_contiguous():
@@ -725,7 +743,7 @@ class Car:
 
     def branch_workspace_bytes(self, branch=None) -> int:
         """Of the backward's workspace; depends on whether rows share a row of the branch's gate."""
-        key = branch._gate_rows if branch is not None and branch.gate is not None else 0
+        key = branch._gate_rows if branch is not None and branch._gate is not None else 0
         need = self._branch_sizes.get(key)
         if need is None:
             gate = 16 if key else None   # any: a shared gate, or none

@@ -255,3 +255,14 @@ def test_copies_have_fields_of_their_own(car, calls):
     for x in (b, d):
         with pytest.raises(ValueError):   # addresses are this process's
             copy.deepcopy(x)
+
+
+def test_the_struct_is_ready_for_the_c_calls(car):
+    """Without a call through a handle: what was given and what was set."""
+    d = car.Dropout(0.5, 1, 2, offset_dev=Tensor(0x40, (1,), torch.int64))
+    b = car.Branch(Tensor(0x200, (N,)), 1e-5, Tensor(0x300, (4, N)), 4, 0.5, d)
+    s = car.car_branch.from_address(b.address)
+    assert (s.norm_weight, s.gate, s.gate_rows, s.residual_scale) == (0x200, 0x300, 4, 0.5)
+    assert s.dropout.contents.offset_dev == 0x40 and ctypes.addressof(b.ref._obj) == b.address
+    b.norm_weight, b.gate = None, Tensor(0x500, (4, N))
+    assert (s.norm_weight, s.gate) == (None, 0x500)
